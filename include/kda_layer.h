@@ -1,0 +1,143 @@
+/*
+ * kda_layer.h -- C ABI of the operators around the chunk solve: the gated delta
+ * rule over prompts and for single tokens, and the norms of the layer that holds
+ * it.  Part of the same library as kda_solve_tril.h, whose rules on ownership,
+ * streams, stream capture and errors hold here too.
+ *
+ * The gated delta rule.  Every head keeps a state S [K, V] in FP32.  For each
+ * token of a sequence, with its query q, key k (K values each), value v (V
+ * values), log decays g and beta:
+ *
+ *     S <- diag(exp(g)) S
+ *     u  = beta (v - S^T k)
+ *     S <- S + k u^T
+ *     o  = scale S^T q
+ *
+ * g is the token's own log decay (not a cumulative one), one for each channel
+ * (KDA_GATE_CHANNEL) or one for a whole head (KDA_GATE_HEAD), and not positive.
+ *
+ * Tensors are contiguous and row-major:
+ *   q, k    [.., Hk, K] of dtype; head h of the H heads uses key head h / (H / Hk)
+ *   v, o    [.., H, V] of dtype
+ *   g       [.., H, K] (channel) or [.., H] (head), float32
+ *   beta    [.., H] of dtype
+ *   states  [entries, H, K, V], float32
+ * with K and V each 32, 64, 96 or 128.
+ */
+#ifndef KDA_LAYER_H
+#define KDA_LAYER_H
+
+#include "kda_solve_tril.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum {
+    KDA_GATE_CHANNEL = 0,         /* g [.., H, K] */
+    KDA_GATE_HEAD = 1             /* g [.., H] */
+} kda_gate_t;
+
+typedef enum {
+    KDA_ACT_SIGMOID = 0,
+    KDA_ACT_SILU = 1
+} kda_act_t;
+
+/* Largest row width of kda_add_norm and kda_gated_norm. */
+#define KDA_NORM_MAX_DIM 16384
+
+/*
+ * Workspace bytes kda_delta_prefill needs for this shape (0 for an empty or
+ * invalid one).  Pure host arithmetic.
+ */
+KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K,
+                                                int32_t V);
+
+/*
+ * The gated delta rule over whole sequences.
+ *
+ *   q, k, v, g, beta, o   as above with leading dimensions [B, T] (dense: every
+ *               batch row is a sequence) or [1, T] with cu_seqlens (packed).
+ *               16-byte aligned (beta: to its element size).  o must not overlap
+ *               an input.
+ *   cu_seqlens, num_seqs, B, T   as for kda_solve_tril.  Sequences may be empty.
+ *   state_in    states to start from, or NULL: all zero.
+ *   state_out   states after the last token, or NULL: not wanted.  May be
+ *               state_in itself; otherwise the two must not overlap.
+ *   slots       device int32 [sequences], or NULL.  Sequence n uses entry
+ *               slots[n] of state_in and state_out, which then have num_slots
+ *               entries; a slot outside [0, num_slots) means that the sequence
+ *               starts from zero and its state is not stored.  Two sequences must
+ *               not share a slot.  NULL: sequence n uses entry n (num_slots is
+ *               ignored).
+ *   Hk, H       key heads and heads; H is a multiple of Hk.  H * K and H * V are
+ *               below 2^24, B*T < 2^31 and chunks * H < 2^30 with chunks of 64
+ *               tokens, as for kda_solve_tril; larger sizes give
+ *               KDA_ERR_UNSUPPORTED.
+ *   gate        kda_gate_t.
+ *   scale       factor on the output, usually K^-0.5.
+ *   workspace   device, 16-byte aligned, kda_delta_prefill_workspace_size()
+ *               bytes; its contents are scratch (KDA_ERR_WORKSPACE if missing or
+ *               too small).
+ *
+ * Sequences of no tokens copy their state (zeros without state_in).  With T == 0
+ * or B == 0 there is nothing to read but the states.
+ */
+KDA_API kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                                       void *o, const float *state_in, float *state_out, const int32_t *slots,
+                                       int32_t num_slots, const int32_t *cu_seqlens, int32_t num_seqs, int64_t B,
+                                       int64_t T, int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dtype,
+                                       int32_t gate, float scale, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/*
+ * One token of each of N running requests; the states are updated in place.
+ *
+ *   q, k, v, g, beta, o   as above with the leading dimension [N].
+ *   state       [num_slots, H, K, V].
+ *   slots       device int32 [N], or NULL: request n uses entry n, and num_slots
+ *               is at least N.  A slot outside [0, num_slots) (-1 for the padding
+ *               rows of a captured batch) reads a state of zeros and stores
+ *               nothing.  Two requests must not share a slot.
+ *   N           N == 0 is a no-op.  N * H < 2^31 - 1 over 4.
+ */
+KDA_API kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                                    void *o, float *state, const int32_t *slots, int32_t num_slots, int32_t N,
+                                    int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dtype, int32_t gate,
+                                    float scale, void *stream);
+
+/*
+ * The norm before a block, with the residual sum that precedes it:
+ *
+ *     r = residual + alpha x;   residual_out = r;   y = r / sqrt(mean(r^2) + eps) * weight
+ *
+ *   x, residual, residual_out, y   [rows, dim] of dtype; weight [dim] of dtype.
+ *               residual may be NULL (r = alpha x); residual_out may be NULL (not
+ *               wanted) or residual itself.  y may be x.  No other overlap.
+ *               Aligned to the element size.
+ *   dim         1 .. KDA_NORM_MAX_DIM, else KDA_ERR_UNSUPPORTED.
+ *   rows        rows == 0 is a no-op.
+ * r and the norm are FP32; y comes from r before it is rounded to residual_out.
+ */
+KDA_API kda_status_t kda_add_norm(const void *x, const void *residual, const void *weight, void *y,
+                                  void *residual_out, int64_t rows, int32_t dim, float alpha, float eps,
+                                  int32_t dtype, void *stream);
+
+/*
+ * The norm after a block, times its gate:
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate)
+ *
+ *   x, gate, y  [rows, dim] of dtype (one row for each token and head); weight
+ *               [dim] of dtype.  y may be x or gate.  Aligned to the element size.
+ *   act         kda_act_t: sigmoid(z) or z sigmoid(z).
+ *   dim, rows   as for kda_add_norm.
+ */
+KDA_API kda_status_t kda_gated_norm(const void *x, const void *gate, const void *weight, void *y, int64_t rows,
+                                    int32_t dim, float eps, int32_t act, int32_t dtype, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KDA_LAYER_H */

@@ -4,7 +4,9 @@
 the chunk's strictly lower-triangular matrix ``A`` (LightLLM PR #1703,
 "perf(kda): parallelize diagonal solves in Prefill"); chunks of 16 and 32
 tokens (the solver's shorter branches) are taken from A's last dimension.
-Every step runs in the
+``delta_prefill``,
+``delta_step``, ``add_norm`` and ``gated_norm`` are the operators of the layer that
+holds the solve.  Every step runs in the
 CUDA kernels of ``libkda_solve_tril.so``; this module only checks and
 marshals arguments (torch provides device memory and streams).
 """
@@ -16,6 +18,8 @@ from typing import Optional
 import torch
 
 from ._lib import lib, LIB_PATH  # noqa: F401
+from .layer import (add_norm, delta_prefill, delta_prefill_workspace_size, delta_step,  # noqa: F401
+                    gated_norm)
 
 BT = 64
 CHUNK_LENGTHS = (16, 32, 64)

@@ -1,4 +1,5 @@
-"""ctypes loader for libkda_solve_tril.so (the C ABI in include/kda_solve_tril.h).
+"""ctypes loader for libkda_solve_tril.so (the C ABI in include/kda_solve_tril.h
+and include/kda_layer.h).
 
 There is no fallback: if the library is missing this raises, so nothing can
 silently run anywhere but the CUDA kernels.
@@ -33,6 +34,15 @@ SIGNATURES = [
     ("kda_solve_tril_kgb", _c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32,
                                       _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32,
                                       _c.c_void_p]),
+    ("kda_delta_prefill_workspace_size", _c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32,
+                                                       _c.c_int32]),
+    ("kda_delta_prefill", _c.c_int, [_c.c_void_p] * 9 + [_c.c_int32, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int64]
+     + [_c.c_int32] * 6 + [_c.c_float, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    ("kda_delta_step", _c.c_int, [_c.c_void_p] * 8 + [_c.c_int32] * 8 + [_c.c_float, _c.c_void_p]),
+    ("kda_add_norm", _c.c_int, [_c.c_void_p] * 5 + [_c.c_int64, _c.c_int32, _c.c_float, _c.c_float, _c.c_int32,
+                                                    _c.c_void_p]),
+    ("kda_gated_norm", _c.c_int, [_c.c_void_p] * 4 + [_c.c_int64, _c.c_int32, _c.c_float, _c.c_int32, _c.c_int32,
+                                                      _c.c_void_p]),
     ("kda_selftest_wait", _c.c_int, [_c.c_int32, _c.c_uint32, _c.c_void_p]),
     ("kda_status_string", _c.c_char_p, [_c.c_int32]),
     ("kda_device_error", _c.c_int, [_c.c_int32, _c.POINTER(_c.c_uint32)]),

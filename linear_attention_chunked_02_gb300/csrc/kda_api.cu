@@ -39,21 +39,16 @@ __global__ void kda_wait_selftest_kernel(unsigned *err, int complete, unsigned l
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1 - 2 * kda::BT;
 
-int elt_size(int32_t dt) { return dt == KDA_F32 ? 4 : 2; }
-bool dtype_ok(int32_t dt) { return dt == KDA_F32 || dt == KDA_BF16 || dt == KDA_F16; }
+}  // namespace
 
-// Upper bound on the number of chunks of length bt that needs no look at cu_seqlens.
-int64_t max_chunks(int64_t B, int64_t T, int32_t num_seqs, int bt = kda::BT) {
+namespace kda {
+
+int64_t max_chunks(int64_t B, int64_t T, int32_t num_seqs, int bt) {
     if (B <= 0 || T <= 0) return 0;
     if (num_seqs <= 0) return B * ((T + bt - 1) / bt);
     const int64_t bound = (T + int64_t(bt - 1) * num_seqs) / bt;
     return bound < T ? bound : T;
 }
-
-struct DeviceInfo {
-    int num_sms = 0;
-    unsigned *err = nullptr;
-};
 
 cudaError_t device_info(int device, DeviceInfo &out) {
     static std::mutex mu;
@@ -72,6 +67,21 @@ cudaError_t device_info(int device, DeviceInfo &out) {
     }
     out = cache[device];
     return cudaSuccess;
+}
+
+}  // namespace kda
+
+namespace {
+
+using kda::aligned16;
+using kda::device_info;
+using kda::DeviceInfo;
+using kda::dtype_ok;
+using kda::elt_size;
+using kda::overlaps;
+
+int64_t max_chunks(int64_t B, int64_t T, int32_t num_seqs, int bt = kda::BT) {
+    return kda::max_chunks(B, T, num_seqs, bt);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -176,13 +186,6 @@ bool encode_kg_maps(const void *k, int32_t in_dt, const float *g, int32_t H, int
     }
     return true;
 }
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 cudaError_t dispatch(int mode, int32_t in_dt, int32_t out_dt, const kda::Maps &maps, const kda::Params &p,
                      int device, int sms, cudaStream_t s) {

@@ -1,0 +1,138 @@
+// kda_delta.cu -- C ABI of the gated delta rule: argument checks and dispatch of
+// kda_delta_prefill and kda_delta_step.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kda_delta_rec.cuh"
+#include "kda_internal.h"
+#include "kda_launch.cuh"
+#include "kda_layer.h"
+
+namespace {
+
+using namespace kda;
+
+bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }
+
+template <typename T>
+cudaError_t launch_rec(const DeltaParams &p, int sms, cudaStream_t s) {
+    // whole heads to a block once they fill the GPU, else 32 columns each
+    const int64_t heads = int64_t(p.nseq) * p.H;
+    if (p.V == 128 && heads >= 2 * sms)
+        return launch_pdl(true, kda_delta_rec_kernel<T, 32>, unsigned(heads), REC_THREADS, 0, s, p);
+    return launch_pdl(true, kda_delta_rec_kernel<T, 8>, unsigned(heads * (p.V / 32)), REC_THREADS, 0, s, p);
+}
+
+kda_status_t run_rec(const DeltaParams &p, int32_t dtype, cudaStream_t s) {
+    int device = 0;
+    DeviceInfo info;
+    if (cudaGetDevice(&device) != cudaSuccess || device_info(device, info) != cudaSuccess) return KDA_ERR_CUDA;
+    cudaError_t e;
+    switch (dtype) {
+        case KDA_F32: e = launch_rec<float>(p, info.num_sms, s); break;
+        case KDA_BF16: e = launch_rec<__nv_bfloat16>(p, info.num_sms, s); break;
+        default: e = launch_rec<__half>(p, info.num_sms, s); break;
+    }
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// Heads, widths, types and the gate form.
+kda_status_t check_heads(int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dtype, int32_t gate) {
+    if (!dtype_ok(dtype) || !width_ok(K) || !width_ok(V)) return KDA_ERR_UNSUPPORTED;
+    if (Hk < 1 || H < 1 || H % Hk != 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (gate != KDA_GATE_CHANNEL && gate != KDA_GATE_HEAD) return KDA_ERR_INVALID_ARGUMENT;
+    if (int64_t(H) * 128 >= (int64_t(1) << 24)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// Pointers of the token tensors: present, aligned, o clear of the inputs.
+kda_status_t check_tokens(const void *q, const void *k, const void *v, const float *g, const void *beta,
+                          const void *o, size_t rows, int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dtype,
+                          int32_t gate) {
+    const size_t es = size_t(elt_size(dtype));
+    if (q == nullptr || k == nullptr || v == nullptr || g == nullptr || beta == nullptr || o == nullptr)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(o) ||
+        reinterpret_cast<uintptr_t>(beta) % es != 0)
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t qb = rows * size_t(Hk) * size_t(K) * es, vb = rows * size_t(H) * size_t(V) * es;
+    const size_t gb = rows * size_t(H) * (gate == KDA_GATE_CHANNEL ? size_t(K) : 1) * 4, bb = rows * size_t(H) * es;
+    if (overlaps(o, vb, q, qb) || overlaps(o, vb, k, qb) || overlaps(o, vb, v, vb) || overlaps(o, vb, g, gb) ||
+        overlaps(o, vb, beta, bb))
+        return KDA_ERR_INVALID_ARGUMENT;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K, int32_t V) {
+    if (H < 1 || num_seqs < 0 || !width_ok(K) || !width_ok(V)) return 0;
+    if (num_seqs > 0 && B != 1) return 0;
+    return 0;
+}
+
+kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
+                               const float *state_in, float *state_out, const int32_t *slots, int32_t num_slots,
+                               const int32_t *cu_seqlens, int32_t num_seqs, int64_t B, int64_t T, int32_t Hk,
+                               int32_t H, int32_t K, int32_t V, int32_t dtype, int32_t gate, float scale,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    kda_status_t st = check_heads(Hk, H, K, V, dtype, gate);
+    if (st != KDA_OK) return st;
+    if (B < 0 || T < 0 || num_seqs < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if ((cu_seqlens != nullptr) != (num_seqs > 0)) return KDA_ERR_INVALID_ARGUMENT;
+    if (cu_seqlens != nullptr && B != 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (slots != nullptr && num_slots < 0) return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t seqs = cu_seqlens != nullptr ? num_seqs : B;
+    const int64_t max_rows = (int64_t(1) << 31) - 1 - 2 * BT;
+    if (T > 0 && B > max_rows / T) return KDA_ERR_UNSUPPORTED;
+    if (max_chunks(B, T, num_seqs, BT) * H >= (int64_t(1) << 30) || seqs * H >= (int64_t(1) << 28))
+        return KDA_ERR_UNSUPPORTED;
+    if (seqs == 0) return KDA_OK;
+    const size_t rows = size_t(B) * size_t(T);
+    if (rows > 0) {
+        st = check_tokens(q, k, v, g, beta, o, rows, Hk, H, K, V, dtype, gate);
+        if (st != KDA_OK) return st;
+    }
+    if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_INVALID_ARGUMENT;
+    const size_t sb = size_t(slots != nullptr ? num_slots : seqs) * size_t(H) * size_t(K) * size_t(V) * 4;
+    if (state_in != nullptr && state_out != nullptr && state_in != state_out && overlaps(state_in, sb, state_out, sb))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && overlaps(o, rows * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state_in, state_in != nullptr ? sb : 0))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && overlaps(o, rows * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state_out, state_out != nullptr ? sb : 0))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t need = kda_delta_prefill_workspace_size(B, T, H, num_seqs, K, V);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return KDA_ERR_INVALID_ARGUMENT;
+    }
+    if (rows == 0 && state_out == nullptr) return KDA_OK;
+    const DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
+                        Hk, H, K, V, gate, scale, nullptr};
+    return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
+                            float *state, const int32_t *slots, int32_t num_slots, int32_t N, int32_t Hk, int32_t H,
+                            int32_t K, int32_t V, int32_t dtype, int32_t gate, float scale, void *stream) {
+    kda_status_t st = check_heads(Hk, H, K, V, dtype, gate);
+    if (st != KDA_OK) return st;
+    if (N < 0 || num_slots < 0 || (slots == nullptr && num_slots < N)) return KDA_ERR_INVALID_ARGUMENT;
+    if (int64_t(N) * H >= (int64_t(1) << 28)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    st = check_tokens(q, k, v, g, beta, o, size_t(N), Hk, H, K, V, dtype, gate);
+    if (st != KDA_OK) return st;
+    if (state == nullptr || !aligned16(state)) return KDA_ERR_INVALID_ARGUMENT;
+    if (overlaps(o, size_t(N) * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state,
+                 size_t(num_slots) * size_t(H) * size_t(K) * size_t(V) * 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const DeltaParams p{q, k, v, g, beta, o, state, state, slots, num_slots, nullptr, N, 1, Hk, H, K, V, gate, scale,
+                        nullptr};
+    return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -2,11 +2,31 @@
 // (not exported).
 #pragma once
 
+#include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "kda_solve_tril.h"
 
 namespace kda {
+
+inline int elt_size(int32_t dt) { return dt == KDA_F32 ? 4 : 2; }
+inline bool dtype_ok(int32_t dt) { return dt == KDA_F32 || dt == KDA_BF16 || dt == KDA_F16; }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Number of SMs and the address of the error word of a device, looked up once.
+struct DeviceInfo {
+    int num_sms = 0;
+    unsigned *err = nullptr;
+};
+cudaError_t device_info(int device, DeviceInfo &out);
+
+// Upper bound on the number of chunks of length bt that needs no look at cu_seqlens.
+int64_t max_chunks(int64_t B, int64_t T, int32_t num_seqs, int bt);
 
 // The host-side argument checks of kda_solve_tril that do not involve the
 // workspace: dtypes, shape limits, the packed/dense layout rules, null

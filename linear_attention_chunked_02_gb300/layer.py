@@ -1,0 +1,254 @@
+"""The gated delta rule and the norms around it: binding of include/kda_layer.h.
+
+A layer's operators between its projections, as a server runs them: ``add_norm``
+before the block, ``delta_prefill`` over prompts or ``delta_step`` for one token of
+each running request, ``gated_norm`` on the heads' outputs.  Inference only: no
+operator records gradients.
+
+With ``stream``, everything a call does (copies of tensors whose layout does not fit
+and new outputs among it) happens on that stream; ordering it after the work that
+produced the inputs, and the outputs' use on other streams, is the caller's.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional
+
+import torch
+
+from ._lib import lib
+
+WIDTHS = (32, 64, 96, 128)
+ACT_CODE = {"sigmoid": 0, "silu": 1}
+
+
+def _bind():
+    # the package's helpers; imported late because the package imports this module
+    from . import DTYPE_CODE, _check
+    return DTYPE_CODE, _check
+
+
+def _launch_on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """Context in which `device` is current and, if given, `stream` is its current stream."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _current_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on_gpu(**tensors) -> torch.device:
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+        device = t.device
+    return device
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t itself, or a contiguous copy where its layout or address does not fit the kernels' vectors."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _rule_shapes(q, k, v, g, beta, lead: int):
+    """Checks of the token tensors, which have `lead` leading dimensions; (Hk, H, K, V, gate code)."""
+    codes = _bind()[0]
+    if q.dim() != lead + 2 or v.dim() != lead + 2 or k.shape != q.shape or q.shape[:lead] != v.shape[:lead]:
+        raise ValueError(f"shapes q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
+    Hk, K = q.shape[lead:]
+    H, V = v.shape[lead:]
+    if K not in WIDTHS or V not in WIDTHS:
+        raise ValueError(f"K and V must be among {WIDTHS}, got {K} and {V}")
+    if Hk < 1 or H < 1 or H % Hk != 0:
+        raise ValueError(f"{H} heads cannot share {Hk} key heads")
+    if beta.shape != v.shape[:-1]:
+        raise ValueError(f"beta must be {tuple(v.shape[:-1])}, got {tuple(beta.shape)}")
+    if g.shape == v.shape[:-1] + (K,):
+        gate = 0
+    elif g.shape == v.shape[:-1]:
+        gate = 1
+    else:
+        raise ValueError(f"g must be {tuple(v.shape[:-1])} or that with {K} channels, got {tuple(g.shape)}")
+    if q.dtype not in codes or any(t.dtype != q.dtype for t in (k, v, beta)) or g.dtype != torch.float32:
+        raise ValueError(f"unsupported dtypes q {q.dtype}, k {k.dtype}, v {v.dtype}, beta {beta.dtype}, g {g.dtype}")
+    return Hk, H, K, V, gate
+
+
+def _int32(name: str, t: Optional[torch.Tensor], numel: Optional[int] = None) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a 1-D int32 CUDA tensor" + (f" of {numel}" if numel is not None else ""))
+    return t
+
+
+def _state(name: str, t: torch.Tensor, entries: Optional[int], H: int, K: int, V: int) -> None:
+    if t.dtype != torch.float32 or t.dim() != 4 or tuple(t.shape[1:]) != (H, K, V) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [entries, {H}, {K}, {V}], got {t.dtype} {tuple(t.shape)}")
+    if entries is not None and t.shape[0] != entries:
+        raise ValueError(f"{name} must have {entries} entries, got {t.shape[0]}")
+
+
+def _output(name: str, out: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
+    return out
+
+
+def delta_prefill_workspace_size(B: int, T: int, H: int, num_seqs: int = 0, K: int = 128, V: int = 128) -> int:
+    """Bytes of workspace delta_prefill needs for this shape."""
+    return int(lib().kda_delta_prefill_workspace_size(B, T, H, num_seqs, K, V))
+
+
+def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                  slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The gated delta rule over whole sequences; returns (o, final states).
+
+    q, k: [B, T, Hk, K]; v: [B, T, H, V], H a multiple of Hk; beta: [B, T, H], all of one
+    dtype (float32 / bfloat16 / float16).  g: the tokens' log decays, float32, [B, T, H, K]
+    or [B, T, H], none positive.  cu_seqlens: int32 CUDA tensor [N+1] for the packed layout
+    (then B == 1).  scale: factor on the output, K ** -0.5 if not given.
+    initial_state, final_state: float32 [N, H, K, V] (N = B for the dense layout); zeros and
+    a new tensor if not given.  With slots (int32 [N]) both are pools of which sequence n
+    uses entry slots[n], final_state is written in place and defaults to initial_state.
+    workspace: optional CUDA buffer of delta_prefill_workspace_size() bytes.
+    """
+    codes, check = _bind()
+    device = _on_gpu(q=q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                     final_state=final_state, slots=slots, out=out, workspace=workspace)
+    Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 2)
+    B, T = q.shape[:2]
+    cu_seqlens = _int32("cu_seqlens", cu_seqlens)
+    if cu_seqlens is not None and (B != 1 or cu_seqlens.numel() < 2):
+        raise ValueError("cu_seqlens needs B == 1 and at least one sequence")
+    nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    N = nseq if cu_seqlens is not None else B
+    slots = _int32("slots", slots, N)
+    if slots is not None and initial_state is None and final_state is None:
+        raise ValueError("slots need a state pool")
+    if final_state is None and slots is not None:
+        final_state = initial_state
+    entries = N if slots is None else final_state.shape[0]
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _state(name, t, entries, H, K, V)
+    with _launch_on(device, stream):
+        q, k, v, g, beta = (_aligned(t) for t in (q, k, v, g, beta))
+        slots = slots.contiguous() if slots is not None else None
+        out = _output("out", out, v)
+        cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
+        if final_state is None:
+            final_state = torch.empty((N, H, K, V), dtype=torch.float32, device=device)
+        need = delta_prefill_workspace_size(B, T, H, nseq, K, V)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        st = lib().kda_delta_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
+            _ptr(initial_state), final_state.data_ptr(), _ptr(slots), entries, _ptr(cu_seqlens), nseq, B, T,
+            Hk, H, K, V, codes[q.dtype], gate, float(K ** -0.5 if scale is None else scale), _ptr(workspace), ws_bytes,
+            _current_stream(device))
+    check(st, "kda_delta_prefill")
+    return out, final_state
+
+
+def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+               state: torch.Tensor, slots: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One token of each of N running requests; updates the states in place and returns o.
+
+    q, k: [N, Hk, K]; v: [N, H, V]; beta: [N, H], of one dtype; g: float32 [N, H, K] or [N, H].
+    state: float32 pool [entries, H, K, V]; request n uses entry slots[n] (int32 [N]), or n
+    without slots.  A slot outside the pool (-1 for padding) reads zeros and stores nothing.
+    """
+    codes, check = _bind()
+    device = _on_gpu(q=q, k=k, v=v, g=g, beta=beta, state=state, slots=slots, out=out)
+    Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 1)
+    N = q.shape[0]
+    slots = _int32("slots", slots, N)
+    _state("state", state, None, H, K, V)
+    if slots is None and state.shape[0] < N:
+        raise ValueError(f"{N} requests and a pool of {state.shape[0]} states")
+    with _launch_on(device, stream):
+        q, k, v, g, beta = (_aligned(t) for t in (q, k, v, g, beta))
+        slots = slots.contiguous() if slots is not None else None
+        out = _output("out", out, v)
+        st = lib().kda_delta_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), state.data_ptr(),
+            _ptr(slots), state.shape[0], N, Hk, H, K, V, codes[q.dtype], gate,
+            float(K ** -0.5 if scale is None else scale), _current_stream(device))
+    check(st, "kda_delta_step")
+    return out
+
+
+def _norm_shapes(x: torch.Tensor, weight: torch.Tensor, **others) -> None:
+    codes = _bind()[0]
+    if x.dim() < 1 or x.dtype not in codes:
+        raise ValueError(f"unsupported x {x.dtype} {tuple(x.shape)}")
+    if tuple(weight.shape) != (x.shape[-1],) or weight.dtype != x.dtype:
+        raise ValueError(f"weight must be a {x.dtype} [{x.shape[-1]}], got {weight.dtype} {tuple(weight.shape)}")
+    for name, t in others.items():
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError(f"{name} must match x, a {x.dtype} {tuple(x.shape)}; got {t.dtype} {tuple(t.shape)}")
+
+
+def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float = 1e-6,
+             alpha: float = 1.0, out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """r = residual + alpha x, y = r / sqrt(mean(r^2) + eps) * weight over the last dimension; returns (y, r).
+
+    residual may be None (r = alpha x); residual_out may be residual and out may be x.
+    """
+    codes, check = _bind()
+    device = _on_gpu(x=x, residual=residual, weight=weight, out=out, residual_out=residual_out)
+    _norm_shapes(x, weight, residual=residual)
+    dim = x.shape[-1]
+    with _launch_on(device, stream):
+        x, weight = x.contiguous(), weight.contiguous()
+        residual = residual.contiguous() if residual is not None else None
+        out, residual_out = _output("out", out, x), _output("residual_out", residual_out, x)
+        st = lib().kda_add_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(),
+                                residual_out.data_ptr(), x.numel() // dim if dim else 0, dim, alpha, eps,
+                                codes[x.dtype], _current_stream(device))
+    check(st, "kda_add_norm")
+    return out, residual_out
+
+
+def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+               activation: str = "sigmoid", out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """x / sqrt(mean(x^2) + eps) * weight * act(gate) over the last dimension; act is "sigmoid" or "silu".
+
+    out may be x or gate.
+    """
+    codes, check = _bind()
+    if activation not in ACT_CODE:
+        raise ValueError(f"unknown activation {activation!r}")
+    device = _on_gpu(x=x, gate=gate, weight=weight, out=out)
+    _norm_shapes(x, weight, gate=gate)
+    dim = x.shape[-1]
+    with _launch_on(device, stream):
+        x, gate, weight = x.contiguous(), gate.contiguous(), weight.contiguous()
+        out = _output("out", out, x)
+        st = lib().kda_gated_norm(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), out.data_ptr(),
+                                  x.numel() // dim if dim else 0, dim, eps, ACT_CODE[activation], codes[x.dtype],
+                                  _current_stream(device))
+    check(st, "kda_gated_norm")
+    return out
