@@ -4,8 +4,10 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "kda_delta_rec.cuh"
+#include "kda_delta_scan.cuh"
 #include "kda_internal.h"
 #include "kda_launch.cuh"
 #include "kda_layer.h"
@@ -13,6 +15,13 @@
 namespace {
 
 using namespace kda;
+
+// Whether prompts of this shape go chunk by chunk rather than token by token: from
+// an average length on.
+bool chunked_form(int64_t B, int64_t T, int32_t num_seqs) {
+    const int64_t seqs = num_seqs > 0 ? num_seqs : B;
+    return B > 0 && T > 0 && B * T >= 16 * seqs;
+}
 
 bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }
 
@@ -34,6 +43,48 @@ kda_status_t run_rec(const DeltaParams &p, int32_t dtype, cudaStream_t s) {
         case KDA_F32: e = launch_rec<float>(p, info.num_sms, s); break;
         case KDA_BF16: e = launch_rec<__nv_bfloat16>(p, info.num_sms, s); break;
         default: e = launch_rec<__half>(p, info.num_sms, s); break;
+    }
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// Opt-in shared memory of the chunked form's kernels, set once per device.
+template <typename T, bool PLO>
+cudaError_t chunked_ready(int device) {
+    static std::mutex mu;
+    static bool done[64] = {false};
+    std::lock_guard<std::mutex> lock(mu);
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    if (done[device]) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PREP_BYTES);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 scan_bytes<PLO>());
+    done[device] = e == cudaSuccess;
+    return e;
+}
+
+template <typename T, bool PLO>
+cudaError_t launch_chunked(const DeltaParams &p, int device, int sms, cudaStream_t s) {
+    cudaError_t e = chunked_ready<T, PLO>(device);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms);
+    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(PREP_BYTES), s, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(true, kda_delta_scan_kernel<T, PLO>, unsigned(p.nseq) * unsigned(p.H), SCAN_THREADS,
+                      size_t(scan_bytes<PLO>()), s, p);
+}
+
+kda_status_t run_chunked(DeltaParams p, int32_t dtype, cudaStream_t s) {
+    int device = 0;
+    DeviceInfo info;
+    if (cudaGetDevice(&device) != cudaSuccess || device_info(device, info) != cudaSuccess) return KDA_ERR_CUDA;
+    p.err = info.err;
+    cudaError_t e;
+    switch (dtype) {
+        case KDA_F32: e = launch_chunked<float, true>(p, device, info.num_sms, s); break;
+        case KDA_BF16: e = launch_chunked<__nv_bfloat16, false>(p, device, info.num_sms, s); break;
+        default: e = launch_chunked<__half, true>(p, device, info.num_sms, s); break;
     }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -72,7 +123,8 @@ extern "C" {
 size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K, int32_t V) {
     if (H < 1 || num_seqs < 0 || !width_ok(K) || !width_ok(V)) return 0;
     if (num_seqs > 0 && B != 1) return 0;
-    return 0;
+    if (!chunked_form(B, T, num_seqs)) return 0;
+    return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * img_bytes<true>();
 }
 
 kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
@@ -111,9 +163,13 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
         if (!aligned16(workspace)) return KDA_ERR_INVALID_ARGUMENT;
     }
     if (rows == 0 && state_out == nullptr) return KDA_OK;
-    const DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
-                        Hk, H, K, V, gate, scale, nullptr};
-    return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
+    DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
+                  Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr};
+    if (!chunked_form(B, T, num_seqs)) return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
+    p.cpr = int32_t((T + BT - 1) / BT);
+    p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
+    p.ws = static_cast<unsigned char *>(workspace);
+    return run_chunked(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
 kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
@@ -131,7 +187,7 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
                  size_t(num_slots) * size_t(H) * size_t(K) * size_t(V) * 4))
         return KDA_ERR_INVALID_ARGUMENT;
     const DeltaParams p{q, k, v, g, beta, o, state, state, slots, num_slots, nullptr, N, 1, Hk, H, K, V, gate, scale,
-                        nullptr};
+                        nullptr, 0, 0, nullptr};
     return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
 }
 

@@ -1,0 +1,476 @@
+// kda_delta_prep.cuh -- what the chunked gated delta rule needs of a chunk before
+// its state is known: for every 64-token chunk and head, from q, k, g and beta,
+//
+//   A_ij = beta_i sum_d k_id k_jd e^{G_id - G_jd}  (j < i),   M = (I + A)^-1 diag(beta),
+//   P_ij = scale sum_d q_id k_jd e^{G_id - G_jd}   (j <= i),
+//
+// with G the cumulative log decay inside the chunk.  All chunk-heads are
+// independent.  M and P go to the workspace as the operand images that
+// kda_delta_scan.cuh multiplies with.
+//
+// One product for both.  With E = G - G_31 (the reference in the chunk's middle),
+//   [A; P] = [K e^E; Q e^E] (K e^{-E})^T,
+// a 128 x 64 product over the channels on tcgen05, FP32 accuracy from TF32 as in the
+// fused construction kernel (hi hi + hi lo + lo hi).  E is summed outward from the
+// middle, so that it is exact to FP32 of its own size where it matters.  A channel
+// whose decay over either half of the chunk exceeds PREP_SAFE nats is left out of
+// the product and its terms are added one by one, with running products of e^g.
+//
+// One persistent CTA of five warpgroups per SM; every role walks the same chunk-heads:
+//   * warp 0, lane 0: MMA issue;
+//   * warps 8-15 (transform): slices of 32 channels from global memory
+//     (prefetched into registers one slice ahead) into TF32 operands; lane =
+//     channel, warp = eight rows, so that the sums along the rows run in registers and
+//     one exchange of eight totals to a channel;
+//   * warps 4, 5 (A) and 6, 7 (P): the accumulator's rows out of tensor memory; A
+//     with beta and the mask into the solve's tile, P straight into its image;
+//   * warps 16-19: two pairs, each the 64-token solve of every second chunk-head,
+//     and M's image.
+// The warpgroups' registers are moved to where the row of 64 values needs them.
+#pragma once
+
+#include "kda_delta_rec.cuh"
+#include "kda_kgb.cuh"
+
+namespace kda {
+
+// Image of one chunk-head in the workspace.  M and P are FP16 pairs hi + lo (22
+// bits) scaled by a power of two for each half of 32 rows, 64 rows of 128
+// bytes with the 128-byte swizzle: the B operands of the scan's products.
+constexpr int IMG_MHI = 0, IMG_MLO = 8192, IMG_PHI = 16384, IMG_PLO = 24576;
+template <bool PLO>
+constexpr int img_hdr() { return PLO ? 32768 : 24576; }   // 16-bit outputs in bf16 need no low part of P
+constexpr int IMG_HDR_BYTES = 128;
+template <bool PLO>
+constexpr int img_bytes() { return img_hdr<PLO>() + IMG_HDR_BYTES; }
+// header (floats): 1 / scale of M rows 0-31, 32-63; largest row sum of |M| in the halves;
+// 1 / scale of P in the halves; largest |k|, |q|
+constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7;
+
+constexpr int PREP_THREADS = 20 * 32;
+constexpr int PREP_TW = 8;                         // transform warps 8-15
+constexpr float PREP_SAFE = 48.0f;
+constexpr int PREP_NOPS = 3;
+constexpr int PREP_OPS_BYTES = 48 * 1024;          // A hi, A lo (128 rows), B hi, B lo (64 rows), 128-byte rows
+constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NOPS, PB_D_EMPTY = PB_D_FULL + 2,
+              PB_AT_FULL = PB_D_EMPTY + 2, PB_AT_EMPTY = PB_AT_FULL + 2, PREP_NBARS = PB_AT_EMPTY + 2;
+constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
+constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
+constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][8 warps] largest |k|, |q|
+constexpr int PREP_OFF_TOT = 1024;                 // [2][8 warps][32 channels] sums of g
+constexpr int PREP_OFF_SC = PREP_OFF_TOT + 2 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
+constexpr int PREP_OFF_BETA = PREP_OFF_SC + 2 * 64 * 8;        // [pairs][64]
+constexpr int PREP_OFF_CU = PREP_OFF_BETA + 2 * 64 * 4;
+constexpr int PREP_OFF_OPS = 6 * 1024;
+constexpr int PREP_OFF_AT = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
+constexpr int PREP_OFF_X = PREP_OFF_AT + 2 * 10 * 256 * 4;
+constexpr int PREP_XP = 68;                        // pitch of the solved tile (floats)
+constexpr int PREP_OFF_XS = PREP_OFF_X + 2 * KGB_X_FLOATS * 4;
+constexpr int PREP_BYTES = PREP_OFF_XS + 2 * 64 * PREP_XP * 4 + 1024;
+static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 8 * 8 <= PREP_OFF_TOT, "header fits");
+static_assert(PREP_OFF_CU + CU_CAP * 4 <= PREP_OFF_OPS, "cu_seqlens fits");
+static_assert(PREP_BYTES <= 227 * 1024, "fits the shared memory of one CTA");
+
+// Power-of-two scale that brings values of at most `bound` below 2^15, within FP16;
+// the exponent is kept in [lo, hi] so that products of two scales and their
+// inverses stay normal.  `inv` is its exact inverse.
+__device__ __forceinline__ float pow2_scale(float bound, int lo, int hi, float &inv) {
+    int e = 14 - (int((__float_as_uint(bound) >> 23) & 255u) - 127);
+    e = e < lo ? lo : e > hi ? hi : e;
+    inv = __uint_as_float(uint32_t(127 - e) << 23);
+    return __uint_as_float(uint32_t(127 + e) << 23);
+}
+constexpr int KQ_LO = -26, KQ_HI = 40;             // exponents for keys, queries, M and P
+constexpr int VS_LO = -100, VS_HI = 80;            // for states and values
+
+// Two values as FP16 hi and lo parts, x ~ hi + lo to 2^-22.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ float warp_max(float v) {   // v >= 0
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// Row i of an image tile from 64 floats (already scaled): hi and, if `lo` is not null, lo.
+__device__ __forceinline__ void image_row(unsigned char *hi, unsigned char *lo, int i, const float (&x)[64], float s) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint4 h, l;
+        split_f16(x[8 * c] * s, x[8 * c + 1] * s, h.x, l.x);
+        split_f16(x[8 * c + 2] * s, x[8 * c + 3] * s, h.y, l.y);
+        split_f16(x[8 * c + 4] * s, x[8 * c + 5] * s, h.z, l.z);
+        split_f16(x[8 * c + 6] * s, x[8 * c + 7] * s, h.w, l.w);
+        const int at = i * 128 + 16 * (c ^ (i & 7));
+        *reinterpret_cast<uint4 *>(hi + at) = h;
+        if (lo != nullptr) *reinterpret_cast<uint4 *>(lo + at) = l;
+    }
+}
+
+// A wait that gives up once, after WAIT_LIMIT_NS: the thread then records it and waits no
+// more, but keeps arriving, so that no other thread is stranded.  The timer is read
+// only every 65536 tries: reading it takes longer than most of these waits.
+__device__ __forceinline__ void prep_wait(bool &ok, uint64_t *bar, uint32_t parity, unsigned *err) {
+    if (!ok || mbar_try_wait(bar, parity)) return;
+    unsigned long long t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return;
+        if ((it & 0xffffu) == 0u) {
+            const unsigned long long t = globaltimer();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > WAIT_LIMIT_NS) break;
+        }
+    }
+    ok = false;
+    atomicOr(err, ERR_WAIT_TIMEOUT);
+}
+
+template <typename T, bool PLO>
+__global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const DeltaParams p) {
+    extern __shared__ __align__(1024) unsigned char smraw[];
+    unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PREP_OFF_TMEM);
+    uint32_t *steep_m = reinterpret_cast<uint32_t *>(sm + PREP_OFF_STEEP);
+    float2 *kq_m = reinterpret_cast<float2 *>(sm + PREP_OFF_KQ);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nsl = p.K / 32;
+    const int32_t G = gridDim.x;
+    const int group = p.H / p.Hk;
+    pdl_launch_dependents();
+
+    if (tid == 0) {
+        for (int b = 0; b < PREP_NOPS; ++b) {
+            mbar_init(&bars[PB_OPS_FULL + b], PREP_TW);
+            mbar_init(&bars[PB_OPS_EMPTY + b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars[PB_D_FULL + b], 2);
+            mbar_init(&bars[PB_D_EMPTY + b], 4);
+            mbar_init(&bars[PB_AT_FULL + b], 2);
+            mbar_init(&bars[PB_AT_EMPTY + b], 2);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    DeltaParams ps = p;
+    if (p.cu != nullptr && p.nseq < CU_CAP) {
+        int32_t *cs = reinterpret_cast<int32_t *>(sm + PREP_OFF_CU);
+        for (int i = tid; i <= p.nseq; i += PREP_THREADS) cs[i] = __ldg(p.cu + i);
+        ps.cu = cs;
+    }
+    if (warp == 4) {
+        tc::tmem_alloc(smem_u32(tmem_slot), 128);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    // registers: 640 threads of 96 at launch; 32 + 120 + 2 * 88 + 136 <= 5 * 96
+    if (warp < 4) {
+        tc::fewer_registers<32>();
+        // ---------------------------------------------------- MMA issue (one lane)
+        if (warp == 0 && lane == 0) {
+            TaskWalk w(ps, blockIdx.x, G);
+            uint32_t u = 0;
+            for (uint32_t c = 0; w.next(ps).valid; ++c) {
+                const int db = c & 1;
+                prep_wait(ok, &bars[PB_D_EMPTY + db], ((c >> 1) & 1) ^ 1, p.err);
+                for (int s = 0; s < nsl; ++s, ++u) {
+                    const int ob = u % PREP_NOPS;
+                    prep_wait(ok, &bars[PB_OPS_FULL + ob], (u / PREP_NOPS) & 1, p.err);
+                    tc::fence_after_sync();
+                    const uint32_t ah = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES), al = ah + 16384;
+                    const uint32_t bh = al + 16384, bl = bh + 8192;
+                    const uint32_t d = tmem + db * 64;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        tc::mma_tf32(d, tc::sw128_desc(ah + 32 * kk), tc::sw128_desc(bh + 32 * kk), KGB_IDESC,
+                                     s > 0 || kk > 0);
+                        tc::mma_tf32(d, tc::sw128_desc(ah + 32 * kk), tc::sw128_desc(bl + 32 * kk), KGB_IDESC, true);
+                        tc::mma_tf32(d, tc::sw128_desc(al + 32 * kk), tc::sw128_desc(bh + 32 * kk), KGB_IDESC, true);
+                    }
+                    tc::commit(smem_u32(&bars[PB_OPS_EMPTY + ob]));
+                }
+                tc::commit(smem_u32(&bars[PB_D_FULL + db]));
+                mbar_arrive(&bars[PB_D_FULL + db]);        // releases the steep masks and maxima
+            }
+        }
+    } else if (warp >= 8 && warp < 16) {
+        tc::fewer_registers<88>();
+        // -------------------------------------------------------------- transform
+        const int tw = warp - 8;                           // rows 8 tw .. + 7
+        const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k);
+        float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT);
+        TaskWalk walk(ps, blockIdx.x, G);
+        T rk[8], rq[8];
+        float rg[8];
+        auto fetch = [&](const Meta &m, int s) {
+            const int d = 32 * s + lane;
+            const int64_t row = int64_t(m.row0) + 8 * tw;
+            const T *kp = k + (row * p.Hk + m.h / group) * p.K + d, *qp = q + (row * p.Hk + m.h / group) * p.K + d;
+            const int gs = p.gate == 0 ? p.H * p.K : p.H;
+            const float *gp = p.gate == 0 ? p.g + (row * p.H + m.h) * p.K + d : p.g + row * p.H + m.h;
+            const int ks = p.Hk * p.K;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = 8 * tw + i < m.n;
+                rk[i] = in ? kp[i * ks] : T(0.f);
+                rq[i] = in ? qp[i * ks] : T(0.f);
+                rg[i] = in ? gp[i * gs] : 0.f;
+            }
+        };
+        Meta m = walk.next(ps);
+        if (m.valid) fetch(m, 0);
+        uint32_t u = 0;
+        for (uint32_t c = 0; m.valid; ++c) {
+            const Meta mn = walk.next(ps);
+            float kmax = 0.f, qmax = 0.f;
+            for (int s = 0; s < nsl; ++s, ++u) {
+                const int ob = u % PREP_NOPS;
+                float kv[8], qv[8], gv[8], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    kv[i] = widen1(rk[i]);
+                    qv[i] = widen1(rq[i]);
+                    gv[i] = rg[i];
+                    sum += gv[i];
+                    kmax = fmaxf(kmax, fabsf(kv[i]));
+                    qmax = fmaxf(qmax, fabsf(qv[i]));
+                }
+                if (s + 1 < nsl) fetch(m, s + 1);
+                else if (mn.valid) fetch(mn, 0);
+                float *tb = tot + (u & 1) * 256;
+                tb[tw * 32 + lane] = sum;
+                named_sync<1, 256>();
+                // decay from the middle of the chunk (between rows 31 and 32) outward
+                float lo = 0.f, hi = 0.f, off = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const float t = tb[w * 32 + lane];
+                    if (w < 4) lo += t;
+                    else hi += t;
+                    if (tw < 4 ? (w > tw && w < 4) : (w >= 4 && w < tw)) off += t;
+                }
+                const bool keep = lo >= -PREP_SAFE && hi >= -PREP_SAFE;     // false for NaN too
+                float E[8];
+                if (tw < 4) {
+#pragma unroll
+                    for (int i = 7; i >= 0; --i) {
+                        E[i] = -off;
+                        off += gv[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        off += gv[i];
+                        E[i] = off;
+                    }
+                }
+                const uint32_t steep = __ballot_sync(0xffffffffu, !keep);
+                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
+                unsigned char *ops = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    constexpr float L2E = 1.4426950408889634f;
+                    const float e = keep ? E[i] * L2E : 0.f;
+                    const float kk = keep ? kv[i] : 0.f, qq = keep ? qv[i] : 0.f;
+                    const float up = ex2(e), dn = ex2(-e);
+                    const float a = kk * up, b = qq * up, x = kk * dn;
+                    const uint32_t ah = __float_as_uint(a) & 0xffffe000u, bh = __float_as_uint(b) & 0xffffe000u,
+                                   xh = __float_as_uint(x) & 0xffffe000u;
+                    // row 8 tw + i of the tile, its 16-byte chunk lane / 4 at position (lane / 4) ^ i
+                    unsigned char *at = ops + tw * 1024 + i * 128 + 16 * ((lane >> 2) ^ i) + 4 * (lane & 3);
+                    *reinterpret_cast<uint32_t *>(at) = ah;
+                    *reinterpret_cast<uint32_t *>(at + 8192) = bh;
+                    *reinterpret_cast<float *>(at + 16384) = a - __uint_as_float(ah);
+                    *reinterpret_cast<float *>(at + 24576) = b - __uint_as_float(bh);
+                    *reinterpret_cast<uint32_t *>(at + 32768) = xh;
+                    *reinterpret_cast<float *>(at + 40960) = x - __uint_as_float(xh);
+                }
+                if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
+                if (s == nsl - 1) {
+                    kmax = warp_max(kmax);
+                    qmax = warp_max(qmax);
+                    if (lane == 0) kq_m[(c & 7) * 8 + tw] = make_float2(kmax, qmax);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[PB_OPS_FULL + ob]);
+            }
+            m = mn;
+        }
+    } else if (warp < 8) {
+        tc::more_registers<120>();
+        // --------------------------------------------------------------- epilogue
+        const bool isP = warp >= 6;
+        const int i = 32 * (warp & 1) + lane;              // chunk row
+        float2 *sc = reinterpret_cast<float2 *>(sm + PREP_OFF_SC) + (isP ? 64 : 0);
+        TaskWalk walk(ps, blockIdx.x, G);
+        int32_t qi;
+        Meta m = walk.next(ps, &qi);
+        for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps, &qi)) {
+            const int db = c & 1;
+            float *Ab = reinterpret_cast<float *>(sm + PREP_OFF_AT) + db * 2560;
+            float f = p.scale;
+            if (!isP)
+                f = i < m.n ? widen1(static_cast<const T *>(p.beta)[(int64_t(m.row0) + i) * p.H + m.h]) : 0.f;
+            if (!isP) prep_wait(ok, &bars[PB_AT_EMPTY + db], ((c >> 1) & 1) ^ 1, p.err);
+            prep_wait(ok, &bars[PB_D_FULL + db], (c >> 1) & 1, p.err);
+            __syncwarp();
+            tc::fence_after_sync();
+            const uint32_t td = tmem + db * 64 + (uint32_t(32 * (warp - 4)) << 16);
+            float x[64];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float v[16];
+                tc::ld16(td + 16 * b, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[16 * b + e] = v[e];
+            }
+            tc::wait_ld();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[PB_D_EMPTY + db]);
+            const int last = isP ? i : i - 1;              // largest column of this row
+            // select: rows past the end and masked columns may hold anything
+#pragma unroll
+            for (int j = 0; j < 64; ++j) x[j] = j <= last && i < m.n ? x[j] : 0.f;
+            const uint32_t sb = (c & 7) * 4;
+            uint32_t any = 0u;
+            for (int s = 0; s < nsl; ++s) any |= steep_m[sb + s];
+            if (any != 0u) {
+                // steep channels: k_j q_i (or k_i) prod_{j < t <= i} e^{g_t}, from the diagonal left
+                const int64_t row = int64_t(m.row0) + i;
+                const int64_t kb = (row * p.Hk + m.h / group) * p.K;
+                for (int s = 0; s < nsl; ++s) {
+                    uint32_t mask = steep_m[sb + s];
+                    while (mask != 0u) {
+                        const int d = 32 * s + __ffs(mask) - 1;
+                        mask &= mask - 1u;
+                        if (isP) named_sync<2, 64>();
+                        else named_sync<3, 64>();
+                        const bool live = i < m.n;
+                        const float kd = live ? widen1(static_cast<const T *>(p.k)[kb + d]) : 0.f;
+                        const float own = isP ? (live ? widen1(static_cast<const T *>(p.q)[kb + d]) : 0.f) : kd;
+                        const float gd = live ? p.g[p.gate == 0 ? (row * p.H + m.h) * p.K + d : row * p.H + m.h] : 0.f;
+                        sc[i] = make_float2(expf(gd), kd);
+                        if (isP) named_sync<2, 64>();
+                        else named_sync<3, 64>();
+                        if (live) {
+                            float run = own;
+                            if (!isP) run *= sc[i].x;      // A starts one token before the row's own
+#pragma unroll
+                            for (int j = 63; j >= 0; --j) {
+                                const float2 t = sc[j];
+                                if (j <= last) {
+                                    x[j] = fmaf(run, t.y, x[j]);
+                                    run *= t.x;
+                                }
+                            }
+                        }
+                    }
+                }
+                if (isP) named_sync<2, 64>();
+                else named_sync<3, 64>();
+            }
+#pragma unroll
+            for (int j = 0; j < 64; ++j) x[j] *= f;
+            if (!isP) {
+#pragma unroll
+                for (int j0 = 0; j0 < 4; ++j0)
+                    if (16 * j0 <= i) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(at_elem(Ab, i, 16 * j0 + e)) =
+                                make_float4(x[16 * j0 + e], x[16 * j0 + e + 1], x[16 * j0 + e + 2], x[16 * j0 + e + 3]);
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[PB_AT_FULL + db]);
+            } else {
+                float mx = 0.f;
+#pragma unroll
+                for (int j = 0; j < 64; ++j) mx = fmaxf(mx, fabsf(x[j]));
+                float inv;
+                const float s = pow2_scale(warp_max(mx), KQ_LO, KQ_HI, inv);
+                unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>();
+                image_row(img + IMG_PHI, PLO ? img + IMG_PLO : nullptr, i, x, s);
+                float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
+                if (lane == 0) hdr[HDR_PINV + (warp & 1)] = inv;
+                if (warp == 6 && lane < 8) {
+                    float2 t = kq_m[(c & 7) * 8 + lane];
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) {
+                        t.x = fmaxf(t.x, __shfl_xor_sync(0xffu, t.x, o));
+                        t.y = fmaxf(t.y, __shfl_xor_sync(0xffu, t.y, o));
+                    }
+                    if (lane == 0) {
+                        hdr[HDR_KMAX] = t.x;
+                        hdr[HDR_QMAX] = t.y;
+                    }
+                }
+            }
+        }
+    } else {
+        tc::more_registers<136>();
+        // ------------------------------------------------------------ solve pairs
+        const int pr = (warp - 16) >> 1, pt = tid - 16 * 32 - 64 * pr, bar = 4 + pr;
+        float *Ab = reinterpret_cast<float *>(sm + PREP_OFF_AT) + pr * 2560;
+        float *X = reinterpret_cast<float *>(sm + PREP_OFF_X) + pr * KGB_X_FLOATS;
+        float *xs = reinterpret_cast<float *>(sm + PREP_OFF_XS) + pr * 64 * PREP_XP;
+        float *sbeta = reinterpret_cast<float *>(sm + PREP_OFF_BETA) + pr * 64;
+        TaskWalk walk(ps, int32_t(blockIdx.x) + pr * G, 2 * G);
+        int32_t qi;
+        Meta m = walk.next(ps, &qi);
+        for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps, &qi)) {
+            const float b = pt < m.n ? widen1(static_cast<const T *>(p.beta)[(int64_t(m.row0) + pt) * p.H + m.h]) : 0.f;
+            prep_wait(ok, &bars[PB_AT_FULL + pr], c & 1, p.err);
+            bar64(bar);                                    // the previous tile and betas are consumed
+            sbeta[pt] = b;
+            kgb_solve<float>(Ab, X, X + 4 * XTS, xs, PREP_XP, m.n, pt, bar);
+            bar64(bar);
+            if ((pt & 31) == 0) mbar_arrive(&bars[PB_AT_EMPTY + pr]);
+            float x[64], mx = 0.f, sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(xs + pt * PREP_XP + j);
+                const float4 bt = *reinterpret_cast<const float4 *>(sbeta + j);
+                const bool live = pt < m.n;
+                x[j] = live ? t.x * bt.x : 0.f;
+                x[j + 1] = live ? t.y * bt.y : 0.f;
+                x[j + 2] = live ? t.z * bt.z : 0.f;
+                x[j + 3] = live ? t.w * bt.w : 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mx = fmaxf(mx, fabsf(x[j + e]));
+                    sum += fabsf(x[j + e]);
+                }
+            }
+            float inv;
+            const float s = pow2_scale(warp_max(mx), KQ_LO, KQ_HI, inv);
+            sum = warp_max(sum);
+            unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>();
+            image_row(img + IMG_MHI, img + IMG_MLO, pt, x, s);
+            if ((pt & 31) == 0) {
+                float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
+                hdr[HDR_MINV + (pt >> 5)] = inv;
+                hdr[HDR_MSUM + (pt >> 5)] = sum;
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 4) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 128);
+    }
+}
+
+}  // namespace kda

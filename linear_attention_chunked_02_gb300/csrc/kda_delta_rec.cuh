@@ -35,6 +35,10 @@ struct DeltaParams {
     int32_t gate;               // kda_gate_t
     float scale;
     unsigned *err;              // device error word
+    // the chunked form
+    int32_t cpr;                // dense: chunks per batch row
+    int32_t n_tasks;            // bound on chunk-heads
+    unsigned char *ws;          // workspace: one image to a chunk-head
 };
 
 // State entry of sequence n, or -1 for none.
