@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "kda_delta_rec.cuh"
@@ -47,6 +48,33 @@ kda_status_t run_rec(const DeltaParams &p, int32_t dtype, cudaStream_t s) {
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+// [rows, heads, width] as {width, heads, rows} with boxes of box x 1 x 64.
+bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, int32_t heads, int32_t width, int box) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const CUtensorMapDataType ty = dt == KDA_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dt == KDA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t es = cuuint64_t(elt_size(dt));
+    const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(width) * es, cuuint64_t(heads) * cuuint64_t(width) * es};
+    const cuuint32_t boxes[3] = {cuuint32_t(box), 1, 64}, estr[3] = {1, 1, 1};
+    return fn(map, ty, 3, const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps of both kernels; g has none where a head has one decay.
+bool encode_delta(const DeltaParams &p, int32_t dt, int64_t rows, DeltaMaps &prep, DeltaMaps &scan) {
+    std::memset(&prep, 0, sizeof(prep));
+    std::memset(&scan, 0, sizeof(scan));
+    return encode_rows(&prep.q, p.q, dt, rows, p.Hk, p.K, 32) && encode_rows(&prep.k, p.k, dt, rows, p.Hk, p.K, 32) &&
+           encode_rows(&scan.v, p.v, dt, rows, p.H, p.V, p.V) && encode_rows(&scan.q, p.q, dt, rows, p.Hk, p.K, p.K) &&
+           encode_rows(&scan.k, p.k, dt, rows, p.Hk, p.K, p.K) &&
+           (p.gate != KDA_GATE_CHANNEL || (encode_rows(&prep.g, p.g, KDA_F32, rows, p.H, p.K, 32) &&
+                                           encode_rows(&scan.g, p.g, KDA_F32, rows, p.H, p.K, p.K)));
+}
+
 // Opt-in shared memory of the chunked form's kernels, set once per device.
 template <typename T, bool PLO>
 cudaError_t chunked_ready(int device) {
@@ -56,35 +84,38 @@ cudaError_t chunked_ready(int device) {
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (done[device]) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PREP_BYTES);
+                                         prep_bytes<T>());
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 scan_bytes<PLO>());
+                                 scan_bytes<T, PLO>());
     done[device] = e == cudaSuccess;
     return e;
 }
 
 template <typename T, bool PLO>
-cudaError_t launch_chunked(const DeltaParams &p, int device, int sms, cudaStream_t s) {
+cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms, cudaStream_t s) {
     cudaError_t e = chunked_ready<T, PLO>(device);
     if (e != cudaSuccess) return e;
     const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms);
-    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(PREP_BYTES), s, p);
+    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(prep_bytes<T>()), s, prep,
+                   p);
     if (e != cudaSuccess) return e;
     return launch_pdl(true, kda_delta_scan_kernel<T, PLO>, unsigned(p.nseq) * unsigned(p.H), SCAN_THREADS,
-                      size_t(scan_bytes<PLO>()), s, p);
+                      size_t(scan_bytes<T, PLO>()), s, scan, p);
 }
 
-kda_status_t run_chunked(DeltaParams p, int32_t dtype, cudaStream_t s) {
+kda_status_t run_chunked(DeltaParams p, int32_t dtype, int64_t rows, cudaStream_t s) {
     int device = 0;
     DeviceInfo info;
     if (cudaGetDevice(&device) != cudaSuccess || device_info(device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;
+    DeltaMaps prep, scan;
+    if (!encode_delta(p, dtype, rows, prep, scan)) return KDA_ERR_CUDA;
     cudaError_t e;
     switch (dtype) {
-        case KDA_F32: e = launch_chunked<float, true>(p, device, info.num_sms, s); break;
-        case KDA_BF16: e = launch_chunked<__nv_bfloat16, false>(p, device, info.num_sms, s); break;
-        default: e = launch_chunked<__half, true>(p, device, info.num_sms, s); break;
+        case KDA_F32: e = launch_chunked<float, true>(p, prep, scan, device, info.num_sms, s); break;
+        case KDA_BF16: e = launch_chunked<__nv_bfloat16, false>(p, prep, scan, device, info.num_sms, s); break;
+        default: e = launch_chunked<__half, true>(p, prep, scan, device, info.num_sms, s); break;
     }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -169,7 +200,7 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     p.cpr = int32_t((T + BT - 1) / BT);
     p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
     p.ws = static_cast<unsigned char *>(workspace);
-    return run_chunked(p, dtype, static_cast<cudaStream_t>(stream));
+    return run_chunked(p, dtype, int64_t(rows), static_cast<cudaStream_t>(stream));
 }
 
 kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,

@@ -17,10 +17,10 @@
 // the product and its terms are added one by one, with running products of e^g.
 //
 // One persistent CTA of five warpgroups per SM; every role walks the same chunk-heads:
-//   * warp 0, lane 0: MMA issue;
-//   * warps 8-15 (transform): slices of 32 channels from global memory
-//     (prefetched into registers one slice ahead) into TF32 operands; lane =
-//     channel, warp = eight rows, so that the sums along the rows run in registers and
+//   * warp 0: MMA issue; warp 1: TMA loads of q, k and g in slices of 32 channels into a
+//     ring (plain loads stall here: what the CTA leaves of the L1 holds too little in
+//     flight);
+//   * warps 8-15 (transform): slices into TF32 operands; lane = channel, warp = eight rows, so that the sums along the rows run in registers and
 //     one exchange of eight totals to a channel;
 //   * warps 4, 5 (A) and 6, 7 (P): the accumulator's rows out of tensor memory; A
 //     with beta and the mask into the solve's tile, P straight into its image;
@@ -50,10 +50,16 @@ constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX =
 constexpr int PREP_THREADS = 20 * 32;
 constexpr int PREP_TW = 8;                         // transform warps 8-15
 constexpr float PREP_SAFE = 48.0f;
-constexpr int PREP_NOPS = 3;
+constexpr int PREP_NOPS = 2;
 constexpr int PREP_OPS_BYTES = 48 * 1024;          // A hi, A lo (128 rows), B hi, B lo (64 rows), 128-byte rows
+// staging ring: a slice of 64 rows x 32 channels of k, q (at most 8 KiB each) and g
+template <typename T>
+constexpr int prep_stage_bytes() { return 2 * 64 * 32 * int(sizeof(T)) + 8192; }
+template <typename T>
+constexpr int prep_stages() { return sizeof(T) == 2 ? 3 : 2; }
 constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NOPS, PB_D_EMPTY = PB_D_FULL + 2,
-              PB_AT_FULL = PB_D_EMPTY + 2, PB_AT_EMPTY = PB_AT_FULL + 2, PREP_NBARS = PB_AT_EMPTY + 2;
+              PB_AT_FULL = PB_D_EMPTY + 2, PB_AT_EMPTY = PB_AT_FULL + 2, PB_ST_FULL = PB_AT_EMPTY + 2,
+              PB_ST_EMPTY = PB_ST_FULL + 3, PREP_NBARS = PB_ST_EMPTY + 3;
 constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
 constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
 constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][8 warps] largest |k|, |q|
@@ -66,10 +72,19 @@ constexpr int PREP_OFF_AT = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
 constexpr int PREP_OFF_X = PREP_OFF_AT + 2 * 10 * 256 * 4;
 constexpr int PREP_XP = 68;                        // pitch of the solved tile (floats)
 constexpr int PREP_OFF_XS = PREP_OFF_X + 2 * KGB_X_FLOATS * 4;
-constexpr int PREP_BYTES = PREP_OFF_XS + 2 * 64 * PREP_XP * 4 + 1024;
+constexpr int PREP_OFF_ST = PREP_OFF_XS + 2 * 64 * PREP_XP * 4;
+template <typename T>
+constexpr int prep_bytes() { return PREP_OFF_ST + prep_stages<T>() * prep_stage_bytes<T>() + 1024; }
 static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 8 * 8 <= PREP_OFF_TOT, "header fits");
 static_assert(PREP_OFF_CU + CU_CAP * 4 <= PREP_OFF_OPS, "cu_seqlens fits");
-static_assert(PREP_BYTES <= 227 * 1024, "fits the shared memory of one CTA");
+static_assert(PREP_OFF_ST % 128 == 0 && prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
+              "fits the shared memory of one CTA");
+
+// Tensor maps of q, k [rows, Hk, K] and g [rows, H, K] as {channels, heads, rows}: boxes of 32
+// channels x 64 rows here, of all channels (and of v's values) in the scan.
+struct DeltaMaps {
+    CUtensorMap q, k, g, v;
+};
 
 // Power-of-two scale that brings values of at most `bound` below 2^15, within FP16;
 // the exponent is kept in [lo, hi] so that products of two scales and their
@@ -83,13 +98,24 @@ __device__ __forceinline__ float pow2_scale(float bound, int lo, int hi, float &
 constexpr int KQ_LO = -26, KQ_HI = 40;             // exponents for keys, queries, M and P
 constexpr int VS_LO = -100, VS_HI = 80;            // for states and values
 
-// Two values as FP16 hi and lo parts, x ~ hi + lo to 2^-22.
+// Two values as FP16 hi and lo parts, x ~ hi + lo to 2^-22 (x - hi is exact).
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
+    asm("{\n\t.reg .b16 h0, h1, m;\n\t.reg .f32 x, y;\n\t"
+        "cvt.rn.f16x2.f32 %0, %3, %2;\n\t"
+        "mov.b32 {h0, h1}, %0;\n\t"
+        "mov.b16 m, 0xBC00;\n\t"                    // -1
+        "fma.rn.f32.f16 x, h0, m, %2;\n\t"
+        "fma.rn.f32.f16 y, h1, m, %3;\n\t"
+        "cvt.rn.f16x2.f32 %1, y, x;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(a), "f"(b));
+}
+
+// Largest of m and |a|, |b|.
+__device__ __forceinline__ float max3(float m, float a, float b) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
 }
 
 __device__ __forceinline__ float warp_max(float v) {   // v >= 0
@@ -130,20 +156,25 @@ __device__ __forceinline__ void prep_wait(bool &ok, uint64_t *bar, uint32_t pari
 }
 
 template <typename T, bool PLO>
-__global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PREP_OFF_TMEM);
     uint32_t *steep_m = reinterpret_cast<uint32_t *>(sm + PREP_OFF_STEEP);
     float2 *kq_m = reinterpret_cast<float2 *>(sm + PREP_OFF_KQ);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    constexpr int NST = prep_stages<T>(), STB = prep_stage_bytes<T>(), ST_Q = 64 * 32 * int(sizeof(T)), ST_G = 2 * ST_Q;
     const int nsl = p.K / 32;
     const int32_t G = gridDim.x;
     const int group = p.H / p.Hk;
     pdl_launch_dependents();
 
     if (tid == 0) {
+        for (int b = 0; b < NST; ++b) {
+            mbar_init(&bars[PB_ST_FULL + b], 1);
+            mbar_init(&bars[PB_ST_EMPTY + b], PREP_TW);
+        }
         for (int b = 0; b < PREP_NOPS; ++b) {
             mbar_init(&bars[PB_OPS_FULL + b], PREP_TW);
             mbar_init(&bars[PB_OPS_EMPTY + b], 1);
@@ -176,8 +207,8 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const D
     // registers: 640 threads of 96 at launch; 32 + 120 + 2 * 88 + 136 <= 5 * 96
     if (warp < 4) {
         tc::fewer_registers<32>();
-        // ---------------------------------------------------- MMA issue (one lane)
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
+            // ------------------------------------------------------------- MMA issue
             TaskWalk w(ps, blockIdx.x, G);
             uint32_t u = 0;
             for (uint32_t c = 0; w.next(ps).valid; ++c) {
@@ -186,67 +217,91 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const D
                 for (int s = 0; s < nsl; ++s, ++u) {
                     const int ob = u % PREP_NOPS;
                     prep_wait(ok, &bars[PB_OPS_FULL + ob], (u / PREP_NOPS) & 1, p.err);
+                    __syncwarp();
                     tc::fence_after_sync();
-                    const uint32_t ah = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES), al = ah + 16384;
-                    const uint32_t bh = al + 16384, bl = bh + 8192;
+                    const uint32_t ah = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES);
                     const uint32_t d = tmem + db * 64;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        tc::mma_tf32(d, tc::sw128_desc(ah + 32 * kk), tc::sw128_desc(bh + 32 * kk), KGB_IDESC,
-                                     s > 0 || kk > 0);
-                        tc::mma_tf32(d, tc::sw128_desc(ah + 32 * kk), tc::sw128_desc(bl + 32 * kk), KGB_IDESC, true);
-                        tc::mma_tf32(d, tc::sw128_desc(al + 32 * kk), tc::sw128_desc(bh + 32 * kk), KGB_IDESC, true);
+                    if (tc::elect_one()) {
+                        // K = 8 channels: 32 bytes along the rows
+                        uint64_t dah = tc::sw128_desc(ah), dal = tc::sw128_desc(ah + 16384),
+                                 dbh = tc::sw128_desc(ah + 32768), dbl = tc::sw128_desc(ah + 40960);
+#pragma unroll 1
+                        for (int kk = 0; kk < 4; ++kk) {
+                            tc::mma_tf32(d, dah, dbh, KGB_IDESC, s > 0 || kk > 0);
+                            tc::mma_tf32(d, dah, dbl, KGB_IDESC, true);
+                            tc::mma_tf32(d, dal, dbh, KGB_IDESC, true);
+                            dah += 2;
+                            dal += 2;
+                            dbh += 2;
+                            dbl += 2;
+                        }
+                        tc::commit(smem_u32(&bars[PB_OPS_EMPTY + ob]));
+                        if (s == nsl - 1) {
+                            tc::commit(smem_u32(&bars[PB_D_FULL + db]));
+                            mbar_arrive(&bars[PB_D_FULL + db]);    // releases the steep masks and maxima
+                        }
                     }
-                    tc::commit(smem_u32(&bars[PB_OPS_EMPTY + ob]));
+                    __syncwarp();
                 }
-                tc::commit(smem_u32(&bars[PB_D_FULL + db]));
-                mbar_arrive(&bars[PB_D_FULL + db]);        // releases the steep masks and maxima
             }
+        } else if (warp == 1) {
+            // ----------------------------------------------------------------- loads
+            TaskWalk w(ps, blockIdx.x, G);
+            uint32_t u = 0;
+            for (Meta m = w.next(ps); m.valid; m = w.next(ps))
+                for (int s = 0; s < nsl; ++s, ++u) {
+                    const int st = u % NST;
+                    prep_wait(ok, &bars[PB_ST_EMPTY + st], ((u / NST) & 1) ^ 1, p.err);
+                    __syncwarp();
+                    if (tc::elect_one()) {
+                        unsigned char *to = sm + PREP_OFF_ST + st * STB;
+                        uint64_t *full = &bars[PB_ST_FULL + st];
+                        mbar_arrive_expect_tx(full, 2 * ST_Q + (p.gate == 0 ? 8192 : 0));
+                        tma_load_3d(to, &maps.k, 32 * s, m.h / group, m.row0, full);
+                        tma_load_3d(to + ST_Q, &maps.q, 32 * s, m.h / group, m.row0, full);
+                        if (p.gate == 0) tma_load_3d(to + ST_G, &maps.g, 32 * s, m.h, m.row0, full);
+                    }
+                    __syncwarp();
+                }
+            // no copy may be in flight when the CTA ends
+            for (uint32_t i = u > NST ? u - NST : 0; i < u; ++i)
+                prep_wait(ok, &bars[PB_ST_FULL + i % NST], (i / NST) & 1, p.err);
         }
     } else if (warp >= 8 && warp < 16) {
         tc::fewer_registers<88>();
         // -------------------------------------------------------------- transform
         const int tw = warp - 8;                           // rows 8 tw .. + 7
-        const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k);
         float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT);
         TaskWalk walk(ps, blockIdx.x, G);
-        T rk[8], rq[8];
-        float rg[8];
-        auto fetch = [&](const Meta &m, int s) {
-            const int d = 32 * s + lane;
-            const int64_t row = int64_t(m.row0) + 8 * tw;
-            const T *kp = k + (row * p.Hk + m.h / group) * p.K + d, *qp = q + (row * p.Hk + m.h / group) * p.K + d;
-            const int gs = p.gate == 0 ? p.H * p.K : p.H;
-            const float *gp = p.gate == 0 ? p.g + (row * p.H + m.h) * p.K + d : p.g + row * p.H + m.h;
-            const int ks = p.Hk * p.K;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = 8 * tw + i < m.n;
-                rk[i] = in ? kp[i * ks] : T(0.f);
-                rq[i] = in ? qp[i * ks] : T(0.f);
-                rg[i] = in ? gp[i * gs] : 0.f;
-            }
-        };
         Meta m = walk.next(ps);
-        if (m.valid) fetch(m, 0);
         uint32_t u = 0;
-        for (uint32_t c = 0; m.valid; ++c) {
-            const Meta mn = walk.next(ps);
-            float kmax = 0.f, qmax = 0.f;
+        for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps)) {
+            float kmax = 0.f, qmax = 0.f, gh[8];
+            if (p.gate != 0) {                             // one decay to a row, from global memory
+                const float *gp = p.g + (int64_t(m.row0) + 8 * tw) * p.H + m.h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gh[i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
+            }
             for (int s = 0; s < nsl; ++s, ++u) {
-                const int ob = u % PREP_NOPS;
+                const int ob = u % PREP_NOPS, st = u % NST;
+                const unsigned char *stage = sm + PREP_OFF_ST + st * STB;
+                const T *kt = reinterpret_cast<const T *>(stage) + tw * 256 + lane;
+                const T *qt = reinterpret_cast<const T *>(stage + ST_Q) + tw * 256 + lane;
+                const float *gt = reinterpret_cast<const float *>(stage + ST_G) + tw * 256 + lane;
+                prep_wait(ok, &bars[PB_ST_FULL + st], (u / NST) & 1, p.err);
                 float kv[8], qv[8], gv[8], sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    kv[i] = widen1(rk[i]);
-                    qv[i] = widen1(rq[i]);
-                    gv[i] = rg[i];
+                    const bool in = 8 * tw + i < m.n;      // select: rows past the end hold the next request's
+                    kv[i] = in ? widen1(kt[32 * i]) : 0.f;
+                    qv[i] = in ? widen1(qt[32 * i]) : 0.f;
+                    gv[i] = p.gate != 0 ? gh[i] : in ? gt[32 * i] : 0.f;
                     sum += gv[i];
                     kmax = fmaxf(kmax, fabsf(kv[i]));
                     qmax = fmaxf(qmax, fabsf(qv[i]));
                 }
-                if (s + 1 < nsl) fetch(m, s + 1);
-                else if (mn.valid) fetch(mn, 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[PB_ST_EMPTY + st]);
                 float *tb = tot + (u & 1) * 256;
                 tb[tw * 32 + lane] = sum;
                 named_sync<1, 256>();
@@ -305,7 +360,6 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const D
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[PB_OPS_FULL + ob]);
             }
-            m = mn;
         }
     } else if (warp < 8) {
         tc::more_registers<120>();

@@ -30,9 +30,13 @@
 // One CTA of five warpgroups per sequence-head (registers moved to the chain):
 //   * warps 0-7 (chain): two warps to each lane quarter, half the columns each; S in
 //     registers;
-//   * warps 8-15 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, from global memory
-//     prefetched into registers; a thread has two channels of 16 rows;
-//   * warp 16, one lane: MMA issue.  M and P arrive by bulk copy, double-buffered.
+//   * warps 8-15 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
+//     time; a thread has two channels of eight rows, so that sums along the rows run in
+//     registers and eight tokens of a channel make one 16-byte store;
+//   * warp 16: MMA issue; warps 17, 18 and 19: the loads (TMA) of q, k and g, of v, and of the
+//     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
+//     little in flight), so 16-bit q, k and g are staged in shared memory; 32-bit ones
+//     find no room there and are read directly.
 #pragma once
 
 #include "kda_delta_prep.cuh"
@@ -42,56 +46,78 @@ namespace kda {
 constexpr int SCAN_THREADS = 20 * 32;
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
-              SCAN_NBARS = 16;
+              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SCAN_NBARS = 20;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_RED = 192;                  // a word to a warp: chunks before the sequence
 constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [2 halves][128 lanes] largest |S|
 constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [2 halves][128 lanes] largest |v|
-constexpr int SCAN_OFF_TOT = SCAN_OFF_VMAX + 2 * 128 * 4;      // [2][4 row groups][128] sums of g
-constexpr int SCAN_OFF_SUM = 7680;                 // [2 halves][3][128], sums of a chunk taken token by token
+constexpr int SCAN_OFF_TOT = SCAN_OFF_VMAX + 2 * 128 * 4;      // [8 row groups][128] sums of g
+constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [2 halves][3][128], sums of a chunk taken token by token
 constexpr int SCAN_OFF_KQ = 11 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
-constexpr int SCAN_OFF_KH = SCAN_OFF_KQ + 4 * 16384;           // K e^{G_C-G} transposed, hi and lo: [128 channels][128 B]
-constexpr int SCAN_OFF_IMG = SCAN_OFF_KH + 2 * 16384;
+template <bool PLO>
+constexpr int scan_off_kh() { return SCAN_OFF_KQ + (PLO ? 4 : 3) * 16384; }    // K e^{G_C-G} transposed, hi and lo:
+                                                                               // [128 channels][128 B]
+template <bool PLO>
+constexpr int scan_off_img() { return scan_off_kh<PLO>() + 2 * 16384; }
+// images held at once: two, one beside a low part of P
+template <bool PLO>
+constexpr int scan_nimg() { return PLO ? 1 : 2; }
 template <bool PLO>
 constexpr int scan_img_pitch() { return (img_bytes<PLO>() + 1023) / 1024 * 1024; }
 template <bool PLO>
-constexpr int scan_bytes() { return SCAN_OFF_IMG + 2 * scan_img_pitch<PLO>() + 1024; }
-static_assert(SCAN_OFF_TOT + 2 * 4 * 128 * 4 <= SCAN_OFF_SUM && SCAN_OFF_SUM + 2 * 3 * 128 * 4 <= SCAN_OFF_KQ,
-              "small buffers fit");
+constexpr int scan_off_v() { return scan_off_img<PLO>() + scan_nimg<PLO>() * scan_img_pitch<PLO>(); }  // [64 tokens][V]
+template <typename T, bool PLO>
+constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
+template <typename T, bool PLO>
+constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
+static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 20 * 4 <= SCAN_OFF_GAM, "header fits");
+static_assert(SCAN_OFF_SUM + 2 * 3 * 128 * 4 <= SCAN_OFF_KQ, "small buffers fit");
+static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
+                  scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
 // A chunk is taken token by token where its values are below 2^-16 of what the state can add to R
 // and no channel keeps more than 2^-12 of the state: what comes out is then
 // possibly below 2^-20 of what goes in.
 constexpr float SCAN_WEAK_V = 65536.f, SCAN_WEAK_G = 1.f / 4096.f;
-static_assert(scan_bytes<true>() <= 227 * 1024, "fits the shared memory of one CTA");
 
 // TMEM columns.  U's accumulator takes the place of (K e^G) S's, which R has consumed.
 constexpr uint32_t TM_SHI = 0, TM_SLO = 64, TM_RHI = 128, TM_RLO = 160, TM_D1 = 192, TM_O1 = 256, TM_O2 = 320,
                    TM_D3 = 384;
 constexpr uint32_t SCAN_ID64 = tc::idesc_f16<128, 64>(), SCAN_ID128 = tc::idesc_f16<128, 128>();
 
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // 16 values, scaled, to the hi and lo operand columns at ch, cl (8 columns each).
 __device__ __forceinline__ void put_operand(uint32_t ch, uint32_t cl, const float (&x)[16], float s) {
     uint32_t h[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_f16(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
+    for (int i = 0; i < 8; ++i) {
+        const float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), both(s));
+        split_f16(y.x, y.y, h[i], l[i]);
+    }
     tc::st8(ch, h);
     tc::st8(cl, l);
 }
 
-// D (+)= A B over KS steps of 16: A at TMEM columns ah, al; B at shared addresses bh, bl
+// D (+)= A B over `steps` steps of 16: A at TMEM columns ah, al; B at shared addresses bh, bl
 // (128-byte rows of 64 values; the second 64 values of a row at + bstep).  HI: hi hi only.
-template <int KS, bool HI>
-__device__ __forceinline__ void mma_split(uint32_t d, uint32_t ah, uint32_t al, uint32_t bh, uint32_t bl,
+// Not unrolled: the issuing warp has few registers.
+template <bool HI>
+__device__ __forceinline__ void mma_split(int steps, uint32_t d, uint32_t ah, uint32_t al, uint32_t bh, uint32_t bl,
                                           uint32_t bstep, uint32_t idesc) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        const uint32_t b = (ks >> 2) * bstep + (ks & 3) * 32;
-        tc::mma_f16_ts(d, ah + 8 * ks, tc::sw128_desc(bh + b), idesc, ks > 0);
+    uint64_t dh = tc::sw128_desc(bh), dl = tc::sw128_desc(bl);
+#pragma unroll 1
+    for (int ks = 0; ks < steps; ++ks) {
+        tc::mma_f16_ts(d, ah, dh, idesc, ks > 0);
         if (!HI) {
-            tc::mma_f16_ts(d, ah + 8 * ks, tc::sw128_desc(bl + b), idesc, true);
-            tc::mma_f16_ts(d, al + 8 * ks, tc::sw128_desc(bh + b), idesc, true);
+            tc::mma_f16_ts(d, ah, dl, idesc, true);
+            tc::mma_f16_ts(d, al, dh, idesc, true);
         }
+        ah += 8;
+        al += 8;
+        const uint32_t step = (ks == 3 ? bstep - 96 : 32) >> 4;    // the address field counts 16 bytes
+        dh += step;
+        dl += step;
     }
 }
 
@@ -152,19 +178,21 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[64]
 }
 
 template <typename T, bool PLO>
-__global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SCAN_OFF_TMEM);
     int32_t *red = reinterpret_cast<int32_t *>(sm + SCAN_OFF_RED);
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int NI = scan_nimg<PLO>();
+    constexpr bool STAGED = sizeof(T) == 2;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int n = int(blockIdx.x) / p.H, h = int(blockIdx.x) - n * p.H;
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {8, 8, 1, 1, 8, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1};
+        const int count[SCAN_NBARS] = {8, 8, 1, 1, 8, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -199,15 +227,28 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
     if (before < 0 || (int64_t(before) + nc) * p.H > p.n_tasks) nc = 0;
     const unsigned char *img0 = p.ws + (int64_t(before) * p.H + h) * img_bytes<PLO>();
     const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
+    const int nh = p.K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
 
-    // registers: 640 threads of 96 at launch; 2 * 128 + 2 * 96 + 24 <= 5 * 96
+    // registers: 640 threads of 96 at launch; 2 * 128 + 2 * 96 + 32 <= 5 * 96
     if (warp < 8) {
         tc::more_registers<128>();
         // ------------------------------------------------------------------ chain
         const int quarter = warp & 3, half = warp >> 2, v = 32 * quarter + lane;
         const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
         float *smax = reinterpret_cast<float *>(sm + SCAN_OFF_MAX), *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX);
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory"); };
+        auto release = [&](int b) {                        // operand columns written, accumulators read
+            tc::wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[b]);
+        };
+        auto accumulator = [&](int b, uint32_t ph) {
+            prep_wait(ok, &bars[b], ph, p.err);
+            __syncwarp();
+            tc::fence_after_sync();
+        };
         const int32_t e = state_entry(p, n);
         const bool mine = v < p.V;
         float S[64];                                       // S[64 half + i][v]
@@ -218,15 +259,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
                 S[i] = p.state_in != nullptr && e >= 0 && mine && 64 * half + i < p.K ? sp[int64_t(i) * p.V] : 0.f;
         }
         const int vs = p.H * p.V;
-        const T *vp = static_cast<const T *>(p.v) + (ra * p.H + h) * p.V + v;
         T *op = static_cast<T *>(p.o) + (ra * p.H + h) * p.V + v;
-        float bS = 0.f;
+        const int t0 = 32 * half;                          // this thread's tokens of a chunk: t0 .. t0 + 31
+        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * p.V + (mine ? v : 0);
+        float bS = 0.f, invS = 1.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) bS = fmaxf(bS, fabsf(S[i]));
-        float invS;
         if (nc > 0) {
             smax[half * 128 + v] = bS;
-            asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
+            pair_sync();
             bS = fmaxf(smax[v], smax[128 + v]);
             const float s = pow2_scale(bS, VS_LO, VS_HI, invS);
 #pragma unroll
@@ -236,27 +277,25 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
                 for (int i = 0; i < 16; ++i) x[i] = S[16 * b + i];
                 put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, s);
             }
-            tc::wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_S]);
+            release(SB_S);
         }
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
-            const int left = rows - 64 * c, t0 = 32 * half;        // this thread's tokens t0 .. t0 + 31
-            const int64_t at = int64_t(64 * c + t0) * vs;
-            T vr[32];
+            const int left = rows - 64 * c;
+            prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
+            // rows past the end hold the next request's; columns past V stay in their lanes
+            for (int i = left > t0 ? left - t0 : 0; i < 32; ++i)
+                if (mine) sv[i * p.V] = T(0.f);
             float bv = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) vr[i] = mine && t0 + i < left ? vp[at + i * vs] : T(0.f);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) bv = fmaxf(bv, fabsf(widen1(vr[i])));
+            for (int i = 0; i < 32; i += 2) bv = max3(bv, widen1(sv[i * p.V]), widen1(sv[(i + 1) * p.V]));
             svmax[half * 128 + v] = bv;
-            prep_wait(ok, &bars[SB_IMG_FULL + ph], (c >> 1) & 1, p.err);
-            const float *hdr = reinterpret_cast<const float *>(sm + SCAN_OFF_IMG + ph * scan_img_pitch<PLO>() + img_hdr<PLO>());
+            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
+            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
+                                                               img_hdr<PLO>());
             const float minv = hdr[HDR_MINV + half], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
             const float pinv = hdr[HDR_PINV + half], kmax = hdr[HDR_KMAX], qmax = hdr[HDR_QMAX];
-            asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
+            pair_sync();
             bv = fmaxf(svmax[v], svmax[128 + v]);
             float invk, invq, invR, invU, invS1;
             pow2_scale(kmax, KQ_LO, KQ_HI, invk);
@@ -267,7 +306,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
             const float sU = pow2_scale(bU, VS_LO, VS_HI, invU);
             float sS = pow2_scale(bS + 64.f * kmax * bU, VS_LO, VS_HI, invS1);
             bool weak = __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
-            if (weak) {                                            // the same in both warps of the quarter
+            if (weak) {                                    // the same in both warps of the quarter
                 prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
                 float gmax = 0.f;
                 for (int i = 0; i < p.K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
@@ -275,103 +314,110 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
                 if (weak) {
                     scan_tokens<T>(p, S, ra + 64 * c, left < 64 ? left : 64, h, half, v, quarter,
                                    reinterpret_cast<float *>(sm + SCAN_OFF_SUM));
-                    float mx = 0.f;                                // the new state's own bound
+                    float mx = 0.f;                        // the new state's own bound
 #pragma unroll
                     for (int i = 0; i < 64; ++i) mx = fmaxf(mx, fabsf(S[i]));
                     smax[half * 128 + v] = mx;
-                    asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
+                    pair_sync();
                     sS = pow2_scale(fmaxf(smax[v], smax[128 + v]), VS_LO, VS_HI, invS1);
                 }
             }
-            // R = V - (K e^G) S
-            prep_wait(ok, &bars[SB_D1], ph, p.err);
-            __syncwarp();
-            tc::fence_after_sync();
-            const float f1 = invS * invk;
+            // R = V - (K e^G) S, scaled
+            accumulator(SB_D1, ph);
+            {
+                const float2 f = both(-invS * invk * sR), s2 = both(sR);
+                float x[2][16];
+                tc::ld16(tq + TM_D1 + t0, x[0]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[16];
-                tc::ld16(tq + TM_D1 + t0 + 16 * b, x);
-                tc::wait_ld();
+                for (int b = 0; b < 2; ++b) {
+                    float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = fmaf(-f1, x[i], widen1(vr[16 * b + i]));
-                put_operand(tq + TM_RHI + 16 * half + 8 * b, tq + TM_RLO + 16 * half + 8 * b, x, sR);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 w = __fmul2_rn(make_float2(widen1(sv[(16 * b + i) * p.V]),
+                                                                widen1(sv[(16 * b + i + 1) * p.V])), s2);
+                        y[i] = w.x;
+                        y[i + 1] = w.y;
+                    }
+                    tc::wait_ld();
+                    if (b == 0) tc::ld16(tq + TM_D1 + t0 + 16, x[1]);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 w = __ffma2_rn(f, make_float2(x[b][2 * i], x[b][2 * i + 1]),
+                                                    make_float2(y[2 * i], y[2 * i + 1]));
+                        split_f16(w.x, w.y, hi[i], lo[i]);
+                    }
+                    tc::st8(tq + TM_RHI + 16 * half + 8 * b, hi);
+                    tc::st8(tq + TM_RLO + 16 * half + 8 * b, lo);
+                }
             }
-            tc::wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_R]);
+            release(SB_R);
+            if (lane == 0) mbar_arrive(&bars[SB_V_EMPTY]);
             // U = M R
-            prep_wait(ok, &bars[SB_D2], ph, p.err);
-            __syncwarp();
-            tc::fence_after_sync();
-            const float f2 = invR * minv * sU;
+            accumulator(SB_D2, ph);
+            {
+                const float f = invR * minv * sU;
+                float x[2][16];
+                tc::ld16(tq + TM_D1 + t0, x[0]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[16];
-                tc::ld16(tq + TM_D1 + t0 + 16 * b, x);
-                tc::wait_ld();
-                put_operand(tq + TM_RHI + 16 * half + 8 * b, tq + TM_RLO + 16 * half + 8 * b, x, f2);
+                for (int b = 0; b < 2; ++b) {
+                    tc::wait_ld();
+                    if (b == 0) tc::ld16(tq + TM_D1 + t0 + 16, x[1]);
+                    put_operand(tq + TM_RHI + 16 * half + 8 * b, tq + TM_RLO + 16 * half + 8 * b, x[b], f);
+                }
             }
-            tc::wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_U]);
+            release(SB_U);
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
             prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
-            prep_wait(ok, &bars[SB_D3], ph, p.err);
-            __syncwarp();
-            tc::fence_after_sync();
-            const float f3 = invU * invk;
-            float mx = 0.f;
+            accumulator(SB_D3, ph);
+            {
+                const float2 f = both(invU * invk);
+                float mx = 0.f, x[2][16];
+                tc::ld16(tq + TM_D3 + 64 * half, x[0]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float x[16];
-                tc::ld16(tq + TM_D3 + 64 * half + 16 * b, x);
-                tc::wait_ld();
+                for (int b = 0; b < 4; ++b) {
+                    tc::wait_ld();
+                    if (b < 3) tc::ld16(tq + TM_D3 + 64 * half + 16 * (b + 1), x[(b + 1) & 1]);
+                    float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 gm = *reinterpret_cast<const float4 *>(gam + ph * 128 + 64 * half + 16 * b + i);
-                    x[i] = fmaf(gm.x, S[16 * b + i], f3 * x[i]);
-                    x[i + 1] = fmaf(gm.y, S[16 * b + i + 1], f3 * x[i + 1]);
-                    x[i + 2] = fmaf(gm.z, S[16 * b + i + 2], f3 * x[i + 2]);
-                    x[i + 3] = fmaf(gm.w, S[16 * b + i + 3], f3 * x[i + 3]);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 gm = *reinterpret_cast<const float2 *>(gam + ph * 128 + 64 * half + 16 * b + i);
+                        float2 w = __ffma2_rn(gm, make_float2(S[16 * b + i], S[16 * b + i + 1]),
+                                              __fmul2_rn(f, make_float2(x[b & 1][i], x[b & 1][i + 1])));
+                        if (weak) w = make_float2(S[16 * b + i], S[16 * b + i + 1]);
+                        mx = max3(mx, w.x, w.y);
+                        S[16 * b + i] = y[i] = w.x;
+                        S[16 * b + i + 1] = y[i + 1] = w.y;
+                    }
+                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, y, sS);
                 }
-                if (weak) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = S[16 * b + i];
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    S[16 * b + i] = x[i];
-                    mx = fmaxf(mx, fabsf(x[i]));
-                }
-                put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, sS);
+                smax[half * 128 + v] = mx;
             }
-            smax[half * 128 + v] = mx;
-            tc::wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_S]);
+            release(SB_S);
             // O = (scale Q e^G) S0 + P U
-            prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
-            __syncwarp();
-            tc::fence_after_sync();
-            const float f4 = invS * invq, f5 = invU * pinv;
+            accumulator(SB_O_FULL, ph);
+            {
+                const float2 f = both(invS * invq), f2 = both(invU * pinv);
+                T *o = op + int64_t(64 * c + t0) * vs;
+                const int live = mine && !weak ? left - t0 : 0;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[16], y[16];
-                tc::ld16(tq + TM_O1 + t0 + 16 * b, x);
-                tc::ld16(tq + TM_O2 + t0 + 16 * b, y);
-                tc::wait_ld();
+                for (int b = 0; b < 2; ++b) {
+                    float x[16], y[16];
+                    tc::ld16(tq + TM_O1 + t0 + 16 * b, x);
+                    tc::ld16(tq + TM_O2 + t0 + 16 * b, y);
+                    tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (mine && !weak && t0 + 16 * b + i < left) put1(op + at + (16 * b + i) * vs, fmaf(f4, x[i], f5 * y[i]));
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 w = __ffma2_rn(f, make_float2(x[i], x[i + 1]), __fmul2_rn(f2, make_float2(y[i], y[i + 1])));
+                        if (16 * b + i < live) put1(o + (16 * b + i) * vs, w.x);
+                        if (16 * b + i + 1 < live) put1(o + (16 * b + i + 1) * vs, w.y);
+                    }
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[SB_O_EMPTY]);
-            asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
+            pair_sync();
             bS = fmaxf(smax[v], smax[128 + v]);
             invS = invS1;
         }
@@ -386,154 +432,219 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const D
         // --------------------------------------------------------------- operands
         constexpr float L2E = 1.4426950408889634f;
         using W2 = Two<T>;
-        const int pw = warp - 8, ch = pw & 1, rg = pw >> 1;         // channel half, row group of 16
-        const int d = 64 * ch + 2 * lane;                           // channels d, d + 1
-        const bool chan = d < p.K;
+        using raw = typename W2::raw;
+        const int rg = warp - 8;                           // rows 8 rg .. + 7
         const int hk = h / (p.H / p.Hk);
-        const int ks = p.Hk * p.K, gs = p.gate == 0 ? p.H * p.K : p.H;
-        const T *qp = static_cast<const T *>(p.q) + ((ra + 16 * rg) * p.Hk + hk) * p.K + d;
-        const T *kp = static_cast<const T *>(p.k) + ((ra + 16 * rg) * p.Hk + hk) * p.K + d;
-        const float *gp = p.gate == 0 ? p.g + ((ra + 16 * rg) * p.H + h) * p.K + d : p.g + (ra + 16 * rg) * p.H + h;
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
-        typename W2::raw rk[16], rq[16];
-        float2 rgd[16];
-        float2 kqmax = make_float2(0.f, 0.f);
-        auto fetch = [&](int c) {
-            const int left = rows - 64 * c - 16 * rg;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool in = chan && i < left;
-                const int64_t r = int64_t(64) * c + i;
-                rgd[i] = make_float2(0.f, 0.f);
-                if (in) {
-                    if (p.gate == 0) rgd[i] = *reinterpret_cast<const float2 *>(gp + r * gs);
-                    else rgd[i].x = rgd[i].y = gp[r * gs];
-                }
-                rk[i] = in ? *reinterpret_cast<const typename W2::raw *>(kp + r * ks) : typename W2::raw{};
-                rq[i] = in ? *reinterpret_cast<const typename W2::raw *>(qp + r * ks) : typename W2::raw{};
-            }
-            kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + img_hdr<PLO>() + 4 * HDR_KMAX);
-        };
-        if (nc > 0) fetch(0);
+        // this thread's first row, channels 2 lane, 2 lane + 1 (+ 64 x), in the staging buffer or in memory
+        const int ks = STAGED ? p.K : p.Hk * p.K, gs = p.gate != 0 ? p.H : STAGED ? p.K : p.H * p.K;
+        unsigned char *st = sm + scan_off_st<T, PLO>();
+        T *kst = reinterpret_cast<T *>(st) + 8 * rg * p.K + 2 * lane;
+        float *gst = reinterpret_cast<float *>(st + 32768) + 8 * rg * p.K + 2 * lane;
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
-            if (pw == 0 && lane == 0) {                             // M and P of this chunk
-                prep_wait(ok, &bars[SB_IMG_EMPTY + ph], ((c >> 1) & 1) ^ 1, p.err);
-                mbar_arrive_expect_tx(&bars[SB_IMG_FULL + ph], img_bytes<PLO>());
-                bulk_load(sm + SCAN_OFF_IMG + ph * scan_img_pitch<PLO>(), img0 + c * img_step, img_bytes<PLO>(),
-                          &bars[SB_IMG_FULL + ph]);
+            const int left = rows - 64 * c - 8 * rg;       // live rows from this thread's first on
+            const int64_t row = ra + 64 * c + 8 * rg;
+            const T *kp, *qp;
+            const float *gp;
+            if (STAGED) {
+                kp = kst;
+                qp = kst + 64 * 128;
+                gp = gst;
+            } else {
+                kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * p.K + 2 * lane;
+                qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * p.K + 2 * lane;
+                gp = p.g + (row * p.H + h) * p.K + 2 * lane;
             }
-            __syncwarp();
-            float2 sum = make_float2(0.f, 0.f);
+            const float *gh = p.g + row * p.H + h;         // one decay to a head
+            const float2 kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + img_hdr<PLO>() + 4 * HDR_KMAX);
+            if (STAGED) {
+                prep_wait(ok, &bars[SB_ST_FULL], ph, p.err);
+                for (int i = left > 0 ? left : 0; i < 8; ++i)      // rows past the end hold the next request's
+                    for (int x = 0; x < nh; ++x)
+                        if (64 * x + 2 * lane < p.K) {
+                            *reinterpret_cast<raw *>(kst + i * p.K + 64 * x) = raw{};
+                            *reinterpret_cast<raw *>(kst + 64 * 128 + i * p.K + 64 * x) = raw{};
+                            if (p.gate == 0) *reinterpret_cast<float2 *>(gst + i * p.K + 64 * x) = both(0.f);
+                        }
+            }
+            // row i of channel half x; channels past K count as zeros
+            auto two = [&](const T *at, int i, int x) {
+                const bool in = 64 * x + 2 * lane < p.K && (STAGED || i < left);
+                return W2::wide(in ? *reinterpret_cast<const raw *>(at + i * ks + 64 * x) : raw{});
+            };
+            auto decay = [&](int i, int x) {
+                if (p.gate != 0) return __fmul2_rn(both(i < left ? gh[i * gs] : 0.f), both(L2E));
+                const bool in = 64 * x + 2 * lane < p.K && (STAGED || i < left);
+                return __fmul2_rn(in ? *reinterpret_cast<const float2 *>(gp + i * gs + 64 * x) : both(0.f), both(L2E));
+            };
+            for (int x = 0; x < nh; ++x) {
+                float2 sum = both(0.f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sum.x += rgd[i].x;
-                sum.y += rgd[i].y;
+                for (int i = 0; i < 8; ++i) sum = __fadd2_rn(sum, decay(i, x));
+                *reinterpret_cast<float2 *>(tot + rg * 128 + 64 * x + 2 * lane) = sum;
             }
-            float *tb = tot + ph * 512;
-            *reinterpret_cast<float2 *>(tb + rg * 128 + d) = sum;
+            float inv, unused;
+            const float2 sk = both(pow2_scale(kqmax.x, KQ_LO, KQ_HI, inv));
+            const float2 cq = both(p.scale * pow2_scale(kqmax.y * fabsf(p.scale), KQ_LO, KQ_HI, unused) * inv);
             named_sync<1, 256>();
-            float2 pre = make_float2(0.f, 0.f), post = pre, all = pre;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float2 t = *reinterpret_cast<const float2 *>(tb + w * 128 + d);
-                if (w < rg) { pre.x += t.x; pre.y += t.y; }
-                if (w > rg) { post.x += t.x; post.y += t.y; }
-                all.x += t.x;
-                all.y += t.y;
-            }
-            float unused;
-            const float sk = pow2_scale(kqmax.x, KQ_LO, KQ_HI, unused);
-            const float sq = p.scale * pow2_scale(kqmax.y * fabsf(p.scale), KQ_LO, KQ_HI, unused);
             // K e^G and scale Q e^G: row r of a tile is 128 bytes, its 16-byte chunk lane / 4 at (lane / 4) ^ (r & 7)
             prep_wait(ok, &bars[SB_KQ_EMPTY], ph ^ 1, p.err);
-            unsigned char *kq = sm + SCAN_OFF_KQ + ch * 8192 + rg * 2048 + 4 * (lane & 3);
+            for (int x = 0; x < nh; ++x) {
+                const float *tb = tot + 64 * x + 2 * lane;
+                float2 G = both(0.f);
+                for (int w = 0; w < rg; ++w) G = __fadd2_rn(G, *reinterpret_cast<const float2 *>(tb + w * 128));
+                unsigned char *kq = sm + SCAN_OFF_KQ + x * 8192 + rg * 1024 + 4 * (lane & 3);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                pre.x += rgd[i].x;
-                pre.y += rgd[i].y;
-                const float2 kv = W2::wide(rk[i]), qv = W2::wide(rq[i]);
-                const float e0 = ex2(pre.x * L2E), e1 = ex2(pre.y * L2E);
-                uint32_t kh, kl, qh, ql;
-                split_f16(kv.x * e0 * sk, kv.y * e1 * sk, kh, kl);
-                split_f16(qv.x * e0 * sq, qv.y * e1 * sq, qh, ql);
-                unsigned char *at = kq + i * 128 + 16 * ((lane >> 2) ^ (i & 7));
-                *reinterpret_cast<uint32_t *>(at) = kh;
-                *reinterpret_cast<uint32_t *>(at + 16384) = kl;
-                *reinterpret_cast<uint32_t *>(at + 32768) = qh;
-                if (PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+                for (int i = 0; i < 8; ++i) {
+                    G = __fadd2_rn(G, decay(i, x));
+                    const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
+                    const float2 kv = __fmul2_rn(two(kp, i, x), e);
+                    const float2 qv = __fmul2_rn(two(qp, i, x), __fmul2_rn(e, cq));
+                    uint32_t kh, kl, qh, ql;
+                    split_f16(kv.x, kv.y, kh, kl);
+                    split_f16(qv.x, qv.y, qh, ql);
+                    unsigned char *at = kq + i * 128 + 16 * ((lane >> 2) ^ i);
+                    *reinterpret_cast<uint32_t *>(at) = kh;
+                    *reinterpret_cast<uint32_t *>(at + 16384) = kl;
+                    *reinterpret_cast<uint32_t *>(at + 32768) = qh;
+                    if (PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+                }
+                if (rg == 7)                               // here G is the whole chunk's sum
+                    *reinterpret_cast<float2 *>(gam + ph * 128 + 64 * x + 2 * lane) = make_float2(ex2(G.x), ex2(G.y));
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[SB_KQ_FULL]);
             // K e^{G_C-G} transposed: channel d's row holds the 64 tokens, eight to a 16-byte chunk
             prep_wait(ok, &bars[SB_KH_EMPTY], ph ^ 1, p.err);
-            if (rg == 0) *reinterpret_cast<float2 *>(gam + ph * 128 + d) = make_float2(ex2(all.x * L2E), ex2(all.y * L2E));
-#pragma unroll
-            for (int o = 1; o >= 0; --o) {                          // tokens 8 o .. 8 o + 7 of the group, from the end
-                float x[8], y[8];
+            for (int x = 0; x < nh; ++x) {
+                const float *tb = tot + 64 * x + 2 * lane;
+                float2 after = both(0.f), y[8];
+                for (int w = 7; w > rg; --w) after = __fadd2_rn(after, *reinterpret_cast<const float2 *>(tb + w * 128));
 #pragma unroll
                 for (int i = 7; i >= 0; --i) {
-                    const float2 kv = W2::wide(rk[8 * o + i]);
-                    x[i] = kv.x * ex2(post.x * L2E) * sk;
-                    y[i] = kv.y * ex2(post.y * L2E) * sk;
-                    post.x += rgd[8 * o + i].x;
-                    post.y += rgd[8 * o + i].y;
+                    y[i] = __fmul2_rn(two(kp, i, x), __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
+                    after = __fadd2_rn(after, decay(i, x));
                 }
-                uint4 xh, xl, yh, yl;
-                split_f16(x[0], x[1], xh.x, xl.x); split_f16(x[2], x[3], xh.y, xl.y);
-                split_f16(x[4], x[5], xh.z, xl.z); split_f16(x[6], x[7], xh.w, xl.w);
-                split_f16(y[0], y[1], yh.x, yl.x); split_f16(y[2], y[3], yh.y, yl.y);
-                split_f16(y[4], y[5], yh.z, yl.z); split_f16(y[6], y[7], yh.w, yl.w);
-                const int cc = 2 * rg + o;                          // chunk of the row
-                unsigned char *a0 = sm + SCAN_OFF_KH + d * 128 + 16 * (cc ^ (d & 7));
-                unsigned char *a1 = sm + SCAN_OFF_KH + (d + 1) * 128 + 16 * (cc ^ ((d + 1) & 7));
-                *reinterpret_cast<uint4 *>(a0) = xh;
-                *reinterpret_cast<uint4 *>(a0 + 16384) = xl;
-                *reinterpret_cast<uint4 *>(a1) = yh;
-                *reinterpret_cast<uint4 *>(a1 + 16384) = yl;
+                uint4 ah, al, bh, bl;
+                split_f16(y[0].x, y[1].x, ah.x, al.x); split_f16(y[2].x, y[3].x, ah.y, al.y);
+                split_f16(y[4].x, y[5].x, ah.z, al.z); split_f16(y[6].x, y[7].x, ah.w, al.w);
+                split_f16(y[0].y, y[1].y, bh.x, bl.x); split_f16(y[2].y, y[3].y, bh.y, bl.y);
+                split_f16(y[4].y, y[5].y, bh.z, bl.z); split_f16(y[6].y, y[7].y, bh.w, bl.w);
+                const int d = 64 * x + 2 * lane;
+                unsigned char *a0 = sm + scan_off_kh<PLO>() + d * 128 + 16 * (rg ^ (d & 7));
+                unsigned char *a1 = sm + scan_off_kh<PLO>() + (d + 1) * 128 + 16 * (rg ^ ((d + 1) & 7));
+                *reinterpret_cast<uint4 *>(a0) = ah;
+                *reinterpret_cast<uint4 *>(a0 + 16384) = al;
+                *reinterpret_cast<uint4 *>(a1) = bh;
+                *reinterpret_cast<uint4 *>(a1 + 16384) = bl;
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_KH_FULL]);
-            if (c + 1 < nc) fetch(c + 1);
+            if (lane == 0) {
+                mbar_arrive(&bars[SB_KH_FULL]);
+                mbar_arrive(&bars[SB_ST_EMPTY]);
+            }
+            named_sync<1, 256>();                          // the sums are consumed
         }
-        // no copy may be in flight when the CTA ends
-        if (pw == 0 && lane == 0)
-            for (int c = nc > 2 ? nc - 2 : 0; c < nc; ++c) prep_wait(ok, &bars[SB_IMG_FULL + (c & 1)], (c >> 1) & 1, p.err);
     } else {
-        tc::fewer_registers<24>();
-        // ------------------------------------------------------------- MMA issue
-        if (warp == 16 && lane == 0) {
-        const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + SCAN_OFF_KH);
-        auto commit = [&](int b) { tc::commit(smem_u32(&bars[b])); };
-        for (int c = 0; c < nc; ++c) {
-            const uint32_t ph = c & 1;
-            const uint32_t img = smem_u32(sm + SCAN_OFF_IMG + ph * scan_img_pitch<PLO>());
-            prep_wait(ok, &bars[SB_KQ_FULL], ph, p.err);
-            prep_wait(ok, &bars[SB_S], ph, p.err);
-            tc::fence_after_sync();
-            mma_split<8, false>(tmem + TM_D1, tmem + TM_SHI, tmem + TM_SLO, kq, kq + 16384, 8192, SCAN_ID64);
-            commit(SB_D1);
-            prep_wait(ok, &bars[SB_O_EMPTY], ph ^ 1, p.err);
-            tc::fence_after_sync();
-            mma_split<8, !PLO>(tmem + TM_O1, tmem + TM_SHI, tmem + TM_SLO, kq + 32768, kq + 49152, 8192, SCAN_ID64);
-            commit(SB_KQ_EMPTY);
-            prep_wait(ok, &bars[SB_IMG_FULL + ph], (c >> 1) & 1, p.err);
-            prep_wait(ok, &bars[SB_R], ph, p.err);
-            tc::fence_after_sync();
-            mma_split<4, false>(tmem + TM_D1, tmem + TM_RHI, tmem + TM_RLO, img + IMG_MHI, img + IMG_MLO, 0, SCAN_ID64);
-            commit(SB_D2);
-            prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
-            prep_wait(ok, &bars[SB_U], ph, p.err);
-            tc::fence_after_sync();
-            mma_split<4, false>(tmem + TM_D3, tmem + TM_RHI, tmem + TM_RLO, kh, kh + 16384, 0, SCAN_ID128);
-            commit(SB_D3);
-            commit(SB_KH_EMPTY);
-            mma_split<4, !PLO>(tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0, SCAN_ID64);
-            commit(SB_O_FULL);
-            commit(SB_IMG_EMPTY + ph);
-        }
+        tc::fewer_registers<32>();
+        if (warp == 16) {
+            // --------------------------------------------------------- MMA issue
+            const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + scan_off_kh<PLO>());
+            const int steps = 4 * nh;                      // of 16 channels
+            const uint32_t id3 = nh == 2 ? SCAN_ID128 : SCAN_ID64;
+            auto commit = [&](int b) { tc::commit(smem_u32(&bars[b])); };
+            auto wait = [&](int b, uint32_t parity) { prep_wait(ok, &bars[b], parity, p.err); };
+            for (int c = 0; c < nc; ++c) {
+                const uint32_t ph = c & 1;
+                const uint32_t img = smem_u32(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>());
+                wait(SB_KQ_FULL, ph);
+                wait(SB_S, ph);
+                __syncwarp();
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    mma_split<false>(steps, tmem + TM_D1, tmem + TM_SHI, tmem + TM_SLO, kq, kq + 16384, 8192, SCAN_ID64);
+                    commit(SB_D1);
+                }
+                wait(SB_O_EMPTY, ph ^ 1);
+                __syncwarp();
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    mma_split<!PLO>(steps, tmem + TM_O1, tmem + TM_SHI, tmem + TM_SLO, kq + 32768, kq + 49152, 8192,
+                                    SCAN_ID64);
+                    commit(SB_KQ_EMPTY);
+                }
+                wait(SB_IMG_FULL + c % NI, (c / NI) & 1);
+                wait(SB_R, ph);
+                __syncwarp();
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    mma_split<false>(4, tmem + TM_D1, tmem + TM_RHI, tmem + TM_RLO, img + IMG_MHI, img + IMG_MLO, 0,
+                                     SCAN_ID64);
+                    commit(SB_D2);
+                }
+                wait(SB_KH_FULL, ph);
+                wait(SB_U, ph);
+                __syncwarp();
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    mma_split<false>(4, tmem + TM_D3, tmem + TM_RHI, tmem + TM_RLO, kh, kh + 16384, 0, id3);
+                    commit(SB_D3);
+                    commit(SB_KH_EMPTY);
+                    mma_split<!PLO>(4, tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0,
+                                    SCAN_ID64);
+                    commit(SB_O_FULL);
+                    commit(SB_IMG_EMPTY + c % NI);
+                }
+                __syncwarp();
+            }
+        } else if (warp == 17) {
+            // -------------------------------------------- loads of q, k and g (16-bit)
+            if (STAGED) {
+                unsigned char *st = sm + scan_off_st<T, PLO>();
+                const uint32_t bytes = 2 * 64 * p.K * sizeof(T) + (p.gate == 0 ? 64 * p.K * 4 : 0);
+                const int hk = h / (p.H / p.Hk);
+                for (int c = 0; c < nc; ++c) {
+                    prep_wait(ok, &bars[SB_ST_EMPTY], (c & 1) ^ 1, p.err);
+                    __syncwarp();
+                    if (tc::elect_one()) {
+                        mbar_arrive_expect_tx(&bars[SB_ST_FULL], bytes);
+                        tma_load_3d(st, &maps.k, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
+                        tma_load_3d(st + 16384, &maps.q, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
+                        if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, h, int(ra) + 64 * c, &bars[SB_ST_FULL]);
+                    }
+                    __syncwarp();
+                }
+                if (nc > 0) prep_wait(ok, &bars[SB_ST_FULL], (nc - 1) & 1, p.err);
+            }
+        } else if (warp == 18) {
+            // --------------------------------------------------------- loads of v
+            for (int c = 0; c < nc; ++c) {
+                prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
+                __syncwarp();
+                if (tc::elect_one()) {
+                    mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * p.V * sizeof(T));
+                    tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, h, int(ra) + 64 * c, &bars[SB_V_FULL]);
+                }
+                __syncwarp();
+            }
+            if (nc > 0) prep_wait(ok, &bars[SB_V_FULL], (nc - 1) & 1, p.err);
+        } else {
+            // ------------------------------------------------- loads of M and P
+            for (int c = 0; c < nc; ++c) {
+                prep_wait(ok, &bars[SB_IMG_EMPTY + c % NI], ((c / NI) & 1) ^ 1, p.err);
+                __syncwarp();
+                if (tc::elect_one()) {
+                    mbar_arrive_expect_tx(&bars[SB_IMG_FULL + c % NI], img_bytes<PLO>());
+                    bulk_load(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>(), img0 + c * img_step,
+                              img_bytes<PLO>(), &bars[SB_IMG_FULL + c % NI]);
+                }
+                __syncwarp();
+            }
+            for (int c = nc > NI ? nc - NI : 0; c < nc; ++c)
+                prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
         }
     }
     tc::fence_before_sync();

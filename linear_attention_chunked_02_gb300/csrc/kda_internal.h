@@ -2,6 +2,8 @@
 // (not exported).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -24,6 +26,9 @@ struct DeviceInfo {
     unsigned *err = nullptr;
 };
 cudaError_t device_info(int device, DeviceInfo &out);
+
+// cuTensorMapEncodeTiled, looked up once; nullptr if the driver has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Upper bound on the number of chunks of length bt that needs no look at cu_seqlens.
 int64_t max_chunks(int64_t B, int64_t T, int32_t num_seqs, int bt);

@@ -68,6 +68,19 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// One lane of a converged warp.  Issuing tensor-core instructions under it, in control
+// flow that is uniform for the warp, takes 32 cycles for an N = 64 step on
+// GB300 (its arithmetic time); under a test of the thread index it took 50 to 100.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------- MMA
 // D[tmem] (+)= A[smem] * B[smem]^T, one K step (8 TF32 values).
 __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
