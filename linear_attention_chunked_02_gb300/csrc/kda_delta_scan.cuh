@@ -27,13 +27,15 @@
 // the four lane quarters each look out for such a chunk and take it token by token in
 // FP32 (scan_tokens).
 //
-// One CTA of five warpgroups per sequence-head (registers moved to the chain):
+// One CTA of six warpgroups per sequence-head (registers moved to the chain):
 //   * warps 0-7 (chain): two warps to each lane quarter, half the columns each; S in
-//     registers;
+//     registers.  What bounds the walk is their path from state to state, so all
+//     else is on other warps;
 //   * warps 8-15 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
 //     time; a thread has two channels of eight rows, so that sums along the rows run in
 //     registers and eight tokens of a channel make one 16-byte store;
-//   * warp 16: MMA issue; warps 17, 18 and 19: the loads (TMA) of q, k and g, of v, and of the
+//   * warps 16-19 (output): a lane quarter each, |v| of the next chunk and O;
+//   * warp 20: MMA issue; warps 21, 22 and 23: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
 //     little in flight), so 16-bit q, k and g are staged in shared memory; 32-bit ones
 //     find no room there and are read directly.
@@ -43,18 +45,20 @@
 
 namespace kda {
 
-constexpr int SCAN_THREADS = 20 * 32;
+constexpr int SCAN_THREADS = 24 * 32;
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
-              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SCAN_NBARS = 20;
+              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_VMAX = 20, SB_IMG_READ = 21,
+              SCAN_NBARS = 23;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_RED = 192;                  // a word to a warp: chunks before the sequence
 constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [2 halves][128 lanes] largest |S|
-constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [2 halves][128 lanes] largest |v|
-constexpr int SCAN_OFF_TOT = SCAN_OFF_VMAX + 2 * 128 * 4;      // [8 row groups][128] sums of g
+constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [128 lanes] largest |v|
+constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
+constexpr int SCAN_OFF_TOT = SCAN_OFF_OUT + 2 * 128 * 8;       // [8 row groups][128] sums of g
 constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [2 halves][3][128], sums of a chunk taken token by token
-constexpr int SCAN_OFF_KQ = 11 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
+constexpr int SCAN_OFF_KQ = 12 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
 template <bool PLO>
 constexpr int scan_off_kh() { return SCAN_OFF_KQ + (PLO ? 4 : 3) * 16384; }    // K e^{G_C-G} transposed, hi and lo:
                                                                                // [128 channels][128 B]
@@ -71,7 +75,7 @@ template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
 template <typename T, bool PLO>
 constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
-static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 20 * 4 <= SCAN_OFF_GAM, "header fits");
+static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 24 * 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_SUM + 2 * 3 * 128 * 4 <= SCAN_OFF_KQ, "small buffers fit");
 static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {8, 8, 1, 1, 8, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8};
+        const int count[SCAN_NBARS] = {8, 8, 1, 1, 4, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8, 4, 4, 4};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -230,13 +234,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     const int nh = p.K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
 
-    // registers: 640 threads of 96 at launch; 2 * 128 + 2 * 96 + 32 <= 5 * 96
+    // registers: 768 threads of 80 at launch; 2 * 120 + 2 * 80 + 48 + 32 <= 6 * 80
     if (warp < 8) {
-        tc::more_registers<128>();
+        tc::more_registers<120>();
         // ------------------------------------------------------------------ chain
         const int quarter = warp & 3, half = warp >> 2, v = 32 * quarter + lane;
         const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
         float *smax = reinterpret_cast<float *>(sm + SCAN_OFF_MAX), *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX);
+        float2 *sout = reinterpret_cast<float2 *>(sm + SCAN_OFF_OUT);
         auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory"); };
         auto release = [&](int b) {                        // operand columns written, accumulators read
             tc::wait_st();
@@ -258,10 +263,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             for (int i = 0; i < 64; ++i)
                 S[i] = p.state_in != nullptr && e >= 0 && mine && 64 * half + i < p.K ? sp[int64_t(i) * p.V] : 0.f;
         }
-        const int vs = p.H * p.V;
-        T *op = static_cast<T *>(p.o) + (ra * p.H + h) * p.V + v;
         const int t0 = 32 * half;                          // this thread's tokens of a chunk: t0 .. t0 + 31
-        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * p.V + (mine ? v : 0);
+        const T *sv = reinterpret_cast<const T *>(sm + scan_off_v<PLO>()) + t0 * p.V + (mine ? v : 0);
         float bS = 0.f, invS = 1.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) bS = fmaxf(bS, fabsf(S[i]));
@@ -282,24 +285,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             const int left = rows - 64 * c;
-            prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
-            // rows past the end hold the next request's; columns past V stay in their lanes
-            for (int i = left > t0 ? left - t0 : 0; i < 32; ++i)
-                if (mine) sv[i * p.V] = T(0.f);
-            float bv = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) bv = max3(bv, widen1(sv[i * p.V]), widen1(sv[(i + 1) * p.V]));
-            svmax[half * 128 + v] = bv;
             prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
             const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
                                                                img_hdr<PLO>());
             const float minv = hdr[HDR_MINV + half], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
-            const float pinv = hdr[HDR_PINV + half], kmax = hdr[HDR_KMAX], qmax = hdr[HDR_QMAX];
-            pair_sync();
-            bv = fmaxf(svmax[v], svmax[128 + v]);
-            float invk, invq, invR, invU, invS1;
+            const float kmax = hdr[HDR_KMAX];
+            prep_wait(ok, &bars[SB_VMAX], ph, p.err);
+            const float bv = svmax[v];
+            struct { T a, b; } vr[sizeof(T) == 2 ? 16 : 1];                // 16-bit values, two tokens to a word
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) vr[i] = {sv[2 * i * p.V], sv[(2 * i + 1) * p.V]};
+            }
+            float invk, invR, invU, invS1;
             pow2_scale(kmax, KQ_LO, KQ_HI, invk);
-            pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
             const float bR = bv + float(p.K) * kmax * bS;
             const float sR = pow2_scale(bR, VS_LO, VS_HI, invR);
             const float bU = msum * bR;
@@ -322,6 +321,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     sS = pow2_scale(fmaxf(smax[v], smax[128 + v]), VS_LO, VS_HI, invS1);
                 }
             }
+            if (half == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
             // R = V - (K e^G) S, scaled
             accumulator(SB_D1, ph);
             {
@@ -330,21 +330,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 tc::ld16(tq + TM_D1 + t0, x[0]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float y[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 w = __fmul2_rn(make_float2(widen1(sv[(16 * b + i) * p.V]),
-                                                                widen1(sv[(16 * b + i + 1) * p.V])), s2);
-                        y[i] = w.x;
-                        y[i + 1] = w.y;
-                    }
                     tc::wait_ld();
                     if (b == 0) tc::ld16(tq + TM_D1 + t0 + 16, x[1]);
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float2 w = __ffma2_rn(f, make_float2(x[b][2 * i], x[b][2 * i + 1]),
-                                                    make_float2(y[2 * i], y[2 * i + 1]));
+                        float2 w;
+                        if constexpr (sizeof(T) == 2) w = make_float2(widen1(vr[8 * b + i].a), widen1(vr[8 * b + i].b));
+                        else w = make_float2(widen1(sv[(16 * b + 2 * i) * p.V]), widen1(sv[(16 * b + 2 * i + 1) * p.V]));
+                        w = __ffma2_rn(f, make_float2(x[b][2 * i], x[b][2 * i + 1]), __fmul2_rn(w, s2));
                         split_f16(w.x, w.y, hi[i], lo[i]);
                     }
                     tc::st8(tq + TM_RHI + 16 * half + 8 * b, hi);
@@ -372,51 +366,30 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             accumulator(SB_D3, ph);
             {
                 const float2 f = both(invU * invk);
-                float mx = 0.f, x[2][16];
-                tc::ld16(tq + TM_D3 + 64 * half, x[0]);
+                float mx = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
+                    float x[16];
+                    tc::ld16(tq + TM_D3 + 64 * half + 16 * b, x);
+                    float2 gm[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        gm[i] = *reinterpret_cast<const float2 *>(gam + ph * 128 + 64 * half + 16 * b + 2 * i);
                     tc::wait_ld();
-                    if (b < 3) tc::ld16(tq + TM_D3 + 64 * half + 16 * (b + 1), x[(b + 1) & 1]);
-                    float y[16];
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const float2 gm = *reinterpret_cast<const float2 *>(gam + ph * 128 + 64 * half + 16 * b + i);
-                        float2 w = __ffma2_rn(gm, make_float2(S[16 * b + i], S[16 * b + i + 1]),
-                                              __fmul2_rn(f, make_float2(x[b & 1][i], x[b & 1][i + 1])));
+                        float2 w = __ffma2_rn(gm[i / 2], make_float2(S[16 * b + i], S[16 * b + i + 1]),
+                                              __fmul2_rn(f, make_float2(x[i], x[i + 1])));
                         if (weak) w = make_float2(S[16 * b + i], S[16 * b + i + 1]);
                         mx = max3(mx, w.x, w.y);
-                        S[16 * b + i] = y[i] = w.x;
-                        S[16 * b + i + 1] = y[i + 1] = w.y;
+                        S[16 * b + i] = x[i] = w.x;
+                        S[16 * b + i + 1] = x[i + 1] = w.y;
                     }
-                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, y, sS);
+                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, sS);
                 }
                 smax[half * 128 + v] = mx;
             }
             release(SB_S);
-            // O = (scale Q e^G) S0 + P U
-            accumulator(SB_O_FULL, ph);
-            {
-                const float2 f = both(invS * invq), f2 = both(invU * pinv);
-                T *o = op + int64_t(64 * c + t0) * vs;
-                const int live = mine && !weak ? left - t0 : 0;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float x[16], y[16];
-                    tc::ld16(tq + TM_O1 + t0 + 16 * b, x);
-                    tc::ld16(tq + TM_O2 + t0 + 16 * b, y);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 w = __ffma2_rn(f, make_float2(x[i], x[i + 1]), __fmul2_rn(f2, make_float2(y[i], y[i + 1])));
-                        if (16 * b + i < live) put1(o + (16 * b + i) * vs, w.x);
-                        if (16 * b + i + 1 < live) put1(o + (16 * b + i + 1) * vs, w.y);
-                    }
-                }
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_O_EMPTY]);
             pair_sync();
             bS = fmaxf(smax[v], smax[128 + v]);
             invS = invS1;
@@ -428,7 +401,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (64 * half + i < p.K) sp[int64_t(i) * p.V] = S[i];
         }
     } else if (warp < 16) {
-        tc::fewer_registers<96>();
+        // (80 registers, as at launch)
         // --------------------------------------------------------------- operands
         constexpr float L2E = 1.4426950408889634f;
         using W2 = Two<T>;
@@ -471,7 +444,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // row i of channel half x; channels past K count as zeros
             auto two = [&](const T *at, int i, int x) {
                 const bool in = 64 * x + 2 * lane < p.K && (STAGED || i < left);
-                return W2::wide(in ? *reinterpret_cast<const raw *>(at + i * ks + 64 * x) : raw{});
+                return in ? *reinterpret_cast<const raw *>(at + i * ks + 64 * x) : raw{};
             };
             auto decay = [&](int i, int x) {
                 if (p.gate != 0) return __fmul2_rn(both(i < left ? gh[i * gs] : 0.f), both(L2E));
@@ -495,12 +468,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 float2 G = both(0.f);
                 for (int w = 0; w < rg; ++w) G = __fadd2_rn(G, *reinterpret_cast<const float2 *>(tb + w * 128));
                 unsigned char *kq = sm + SCAN_OFF_KQ + x * 8192 + rg * 1024 + 4 * (lane & 3);
+                raw rk[8], rq[8];                          // all loads before the first store
+                float2 g[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    G = __fadd2_rn(G, decay(i, x));
+                    rk[i] = two(kp, i, x);
+                    rq[i] = two(qp, i, x);
+                    g[i] = decay(i, x);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    G = __fadd2_rn(G, g[i]);
                     const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
-                    const float2 kv = __fmul2_rn(two(kp, i, x), e);
-                    const float2 qv = __fmul2_rn(two(qp, i, x), __fmul2_rn(e, cq));
+                    const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
+                    const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
                     uint32_t kh, kl, qh, ql;
                     split_f16(kv.x, kv.y, kh, kl);
                     split_f16(qv.x, qv.y, qh, ql);
@@ -524,7 +505,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int w = 7; w > rg; --w) after = __fadd2_rn(after, *reinterpret_cast<const float2 *>(tb + w * 128));
 #pragma unroll
                 for (int i = 7; i >= 0; --i) {
-                    y[i] = __fmul2_rn(two(kp, i, x), __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
+                    y[i] = __fmul2_rn(W2::wide(two(kp, i, x)), __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
                     after = __fadd2_rn(after, decay(i, x));
                 }
                 uint4 ah, al, bh, bl;
@@ -548,9 +529,78 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             named_sync<1, 256>();                          // the sums are consumed
         }
+    } else if (warp < 20) {
+        tc::fewer_registers<48>();
+        // ----------------------------------------------------------------- output
+        const int quarter = warp & 3, v = 32 * quarter + lane;
+        const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
+        const bool mine = v < p.V;
+        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + (mine ? v : 0);
+        float *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX);
+        const float2 *sout = reinterpret_cast<const float2 *>(sm + SCAN_OFF_OUT);
+        const int vs = p.H * p.V;
+        T *op = static_cast<T *>(p.o) + (ra * p.H + h) * p.V + v;
+        auto values = [&](int c) {                         // the largest |v| of chunk c
+            const int left = rows - 64 * c;
+            prep_wait(ok, &bars[SB_V_FULL], c & 1, p.err);
+            // rows past the end hold the next request's; columns past V stay in their lanes
+            for (int i = left; i < 64; ++i)
+                if (mine) sv[i * p.V] = T(0.f);
+            float b = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < 64; i += 2) b = max3(b, widen1(sv[i * p.V]), widen1(sv[(i + 1) * p.V]));
+            svmax[v] = b;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SB_VMAX]);
+        };
+        if (nc > 0) values(0);
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = c & 1;
+            // O = (scale Q e^G) S0 + P U
+            prep_wait(ok, &bars[SB_U], ph, p.err);         // the chain's scales
+            const float2 inv = sout[ph * 128 + v];
+            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
+                                                               img_hdr<PLO>());
+            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
+            const float p0 = hdr[HDR_PINV], p1 = hdr[HDR_PINV + 1], qmax = hdr[HDR_QMAX];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ + c % NI]);
+            float invq;
+            pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
+            if (c + 1 < nc) values(c + 1);
+            prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
+            __syncwarp();
+            tc::fence_after_sync();
+            const bool weak = inv.x < 0.f;
+            const int left = mine && !weak ? rows - 64 * c : 0;
+            T *o = op + int64_t(64 * c) * vs;
+            const float2 f = both(inv.x * invq);
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                const float2 f2 = both(inv.y * (b < 4 ? p0 : p1));
+                float x[8], y[8];
+                tc::ld8(tq + TM_O1 + 8 * b, x);
+                tc::ld8(tq + TM_O2 + 8 * b, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 w = __ffma2_rn(f, make_float2(x[i], x[i + 1]), __fmul2_rn(f2, make_float2(y[i], y[i + 1])));
+                    x[i] = w.x;
+                    x[i + 1] = w.y;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (8 * b + i < left) put1(o, x[i]);
+                    o += vs;
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SB_O_EMPTY]);
+        }
     } else {
         tc::fewer_registers<32>();
-        if (warp == 16) {
+        if (warp == 20) {
             // --------------------------------------------------------- MMA issue
             const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + scan_off_kh<PLO>());
             const int steps = 4 * nh;                      // of 16 channels
@@ -600,7 +650,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 __syncwarp();
             }
-        } else if (warp == 17) {
+        } else if (warp == 21) {
             // -------------------------------------------- loads of q, k and g (16-bit)
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
@@ -619,7 +669,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 if (nc > 0) prep_wait(ok, &bars[SB_ST_FULL], (nc - 1) & 1, p.err);
             }
-        } else if (warp == 18) {
+        } else if (warp == 22) {
             // --------------------------------------------------------- loads of v
             for (int c = 0; c < nc; ++c) {
                 prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
@@ -635,6 +685,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // ------------------------------------------------- loads of M and P
             for (int c = 0; c < nc; ++c) {
                 prep_wait(ok, &bars[SB_IMG_EMPTY + c % NI], ((c / NI) & 1) ^ 1, p.err);
+                prep_wait(ok, &bars[SB_IMG_READ + c % NI], ((c / NI) & 1) ^ 1, p.err);
                 __syncwarp();
                 if (tc::elect_one()) {
                     mbar_arrive_expect_tx(&bars[SB_IMG_FULL + c % NI], img_bytes<PLO>());
