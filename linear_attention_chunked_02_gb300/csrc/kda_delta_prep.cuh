@@ -16,15 +16,15 @@
 // whose decay over either half of the chunk exceeds PREP_SAFE nats is left out of
 // the product and its terms are added one by one, with running products of e^g.
 //
-// One persistent CTA of five warpgroups per SM; every role walks the same chunk-heads:
+// One persistent CTA of seven warpgroups per SM; every role walks the same chunk-heads:
 //   * warp 0: MMA issue; warp 1: TMA loads of q, k and g in slices of 32 channels into a
 //     ring (plain loads stall here: what the CTA leaves of the L1 holds too little in
 //     flight);
-//   * warps 8-15 (transform): slices into TF32 operands; lane = channel, warp = eight rows, so that the sums along the rows run in registers and
+//   * warps 8-15 and 16-23 (transform): every second slice each into TF32 operands; lane = channel, warp = eight rows, so that the sums along the rows run in registers and
 //     one exchange of eight totals to a channel;
 //   * warps 4, 5 (A) and 6, 7 (P): the accumulator's rows out of tensor memory; A
 //     with beta and the mask into the solve's tile, P straight into its image;
-//   * warps 16-19: two pairs, each the 64-token solve of every second chunk-head,
+//   * warps 24-27: two pairs, each the 64-token solve of every second chunk-head,
 //     and M's image.
 // The warpgroups' registers are moved to where the row of 64 values needs them.
 #pragma once
@@ -47,8 +47,8 @@ constexpr int img_bytes() { return img_hdr<PLO>() + IMG_HDR_BYTES; }
 // 1 / scale of P in the halves; largest |k|, |q|
 constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7;
 
-constexpr int PREP_THREADS = 20 * 32;
-constexpr int PREP_TW = 8;                         // transform warps 8-15
+constexpr int PREP_THREADS = 28 * 32;
+constexpr int PREP_TW = 8;                         // transform warps of a group
 constexpr float PREP_SAFE = 48.0f;
 constexpr int PREP_NOPS = 2;
 constexpr int PREP_OPS_BYTES = 48 * 1024;          // A hi, A lo (128 rows), B hi, B lo (64 rows), 128-byte rows
@@ -62,12 +62,12 @@ constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NO
               PB_ST_EMPTY = PB_ST_FULL + 3, PREP_NBARS = PB_ST_EMPTY + 3;
 constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
 constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
-constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][8 warps] largest |k|, |q|
-constexpr int PREP_OFF_TOT = 1024;                 // [2][8 warps][32 channels] sums of g
-constexpr int PREP_OFF_SC = PREP_OFF_TOT + 2 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
+constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][16 warps] largest |k|, |q|
+constexpr int PREP_OFF_TOT = 1536;                 // [2 groups][2][8 warps][32 channels] sums of g
+constexpr int PREP_OFF_SC = PREP_OFF_TOT + 4 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
 constexpr int PREP_OFF_BETA = PREP_OFF_SC + 2 * 64 * 8;        // [pairs][64]
 constexpr int PREP_OFF_CU = PREP_OFF_BETA + 2 * 64 * 4;
-constexpr int PREP_OFF_OPS = 6 * 1024;
+constexpr int PREP_OFF_OPS = 8 * 1024;
 constexpr int PREP_OFF_AT = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
 constexpr int PREP_OFF_X = PREP_OFF_AT + 2 * 10 * 256 * 4;
 constexpr int PREP_XP = 68;                        // pitch of the solved tile (floats)
@@ -75,7 +75,7 @@ constexpr int PREP_OFF_XS = PREP_OFF_X + 2 * KGB_X_FLOATS * 4;
 constexpr int PREP_OFF_ST = PREP_OFF_XS + 2 * 64 * PREP_XP * 4;
 template <typename T>
 constexpr int prep_bytes() { return PREP_OFF_ST + prep_stages<T>() * prep_stage_bytes<T>() + 1024; }
-static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 8 * 8 <= PREP_OFF_TOT, "header fits");
+static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 16 * 8 <= PREP_OFF_TOT, "header fits");
 static_assert(PREP_OFF_CU + CU_CAP * 4 <= PREP_OFF_OPS, "cu_seqlens fits");
 static_assert(PREP_OFF_ST % 128 == 0 && prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
               "fits the shared memory of one CTA");
@@ -111,6 +111,12 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32
         : "f"(a), "f"(b));
 }
 
+// The hi part alone.
+__device__ __forceinline__ uint32_t round_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // Largest of m and |a|, |b|.
 __device__ __forceinline__ float max3(float m, float a, float b) {
     float r;
@@ -138,14 +144,15 @@ __device__ __forceinline__ void image_row(unsigned char *hi, unsigned char *lo, 
 }
 
 // A wait that gives up once, after WAIT_LIMIT_NS: the thread then records it and waits no
-// more, but keeps arriving, so that no other thread is stranded.  The timer is read
-// only every 65536 tries: reading it takes longer than most of these waits.
+// more, but keeps arriving, so that no other thread is stranded.  The tries suspend
+// the warp (polling takes issue slots from those at work), and the timer is read only
+// every 64 of them: reading it takes longer than most of these waits.
 __device__ __forceinline__ void prep_wait(bool &ok, uint64_t *bar, uint32_t parity, unsigned *err) {
     if (!ok || mbar_try_wait(bar, parity)) return;
     unsigned long long t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return;
-        if ((it & 0xffffu) == 0u) {
+        if (mbar_try_wait_suspend(bar, parity, 100000u)) return;
+        if ((it & 63u) == 0u) {
             const unsigned long long t = globaltimer();
             if (t0 == 0) t0 = t;
             if (t - t0 > WAIT_LIMIT_NS) break;
@@ -204,9 +211,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    // registers: 640 threads of 96 at launch; 32 + 120 + 2 * 88 + 136 <= 5 * 96
+    // registers: 896 threads of 72 at launch; 24 + 112 + 4 * 64 + 112 <= 7 * 72
     if (warp < 4) {
-        tc::fewer_registers<32>();
+        tc::fewer_registers<24>();
         if (warp == 0) {
             // ------------------------------------------------------------- MMA issue
             TaskWalk w(ps, blockIdx.x, G);
@@ -267,44 +274,57 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             for (uint32_t i = u > NST ? u - NST : 0; i < u; ++i)
                 prep_wait(ok, &bars[PB_ST_FULL + i % NST], (i / NST) & 1, p.err);
         }
-    } else if (warp >= 8 && warp < 16) {
-        tc::fewer_registers<88>();
+    } else if (warp >= 8 && warp < 24) {
+        tc::fewer_registers<64>();
         // -------------------------------------------------------------- transform
-        const int tw = warp - 8;                           // rows 8 tw .. + 7
-        float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT);
+        constexpr float L2E = 1.4426950408889634f;
+        const int tw = warp & 7, tg = (warp >> 3) - 1;     // rows 8 tw .. + 7 of slices tg, tg + 2
+        float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT) + tg * 512;
         TaskWalk walk(ps, blockIdx.x, G);
         Meta m = walk.next(ps);
-        uint32_t u = 0;
+        uint32_t turn = 0;
         for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps)) {
-            float kmax = 0.f, qmax = 0.f, gh[8];
-            if (p.gate != 0) {                             // one decay to a row, from global memory
-                const float *gp = p.g + (int64_t(m.row0) + 8 * tw) * p.H + m.h;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) gh[i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
-            }
-            for (int s = 0; s < nsl; ++s, ++u) {
+            float kmax = 0.f, qmax = 0.f;
+            for (int s = tg; s < nsl; s += 2, ++turn) {
+                const uint32_t u = c * nsl + s;
                 const int ob = u % PREP_NOPS, st = u % NST;
-                const unsigned char *stage = sm + PREP_OFF_ST + st * STB;
-                const T *kt = reinterpret_cast<const T *>(stage) + tw * 256 + lane;
-                const T *qt = reinterpret_cast<const T *>(stage + ST_Q) + tw * 256 + lane;
-                const float *gt = reinterpret_cast<const float *>(stage + ST_G) + tw * 256 + lane;
+                unsigned char *stage = sm + PREP_OFF_ST + st * STB;
+                T *kt = reinterpret_cast<T *>(stage) + tw * 256 + lane;
+                T *qt = reinterpret_cast<T *>(stage + ST_Q) + tw * 256 + lane;
+                float *gt = reinterpret_cast<float *>(stage + ST_G) + tw * 256 + lane;
                 prep_wait(ok, &bars[PB_ST_FULL + st], (u / NST) & 1, p.err);
+                if (p.gate != 0) {                         // one decay to a row, from global memory
+                    const float *gp = p.g + (int64_t(m.row0) + 8 * tw) * p.H + m.h;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) gt[32 * i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
+                }
+                for (int i = m.n > 8 * tw ? m.n - 8 * tw : 0; i < 8; ++i) {    // rows past the end hold the next request's
+                    kt[32 * i] = T(0.f);
+                    qt[32 * i] = T(0.f);
+                    gt[32 * i] = 0.f;
+                }
                 float kv[8], qv[8], gv[8], sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const bool in = 8 * tw + i < m.n;      // select: rows past the end hold the next request's
-                    kv[i] = in ? widen1(kt[32 * i]) : 0.f;
-                    qv[i] = in ? widen1(qt[32 * i]) : 0.f;
-                    gv[i] = p.gate != 0 ? gh[i] : in ? gt[32 * i] : 0.f;
+                    kv[i] = widen1(kt[32 * i]);
+                    qv[i] = widen1(qt[32 * i]);
+                    gv[i] = gt[32 * i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    gv[i] *= L2E;
                     sum += gv[i];
-                    kmax = fmaxf(kmax, fabsf(kv[i]));
-                    qmax = fmaxf(qmax, fabsf(qv[i]));
+                    if (i & 1) {
+                        kmax = max3(kmax, kv[i - 1], kv[i]);
+                        qmax = max3(qmax, qv[i - 1], qv[i]);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[PB_ST_EMPTY + st]);
-                float *tb = tot + (u & 1) * 256;
+                float *tb = tot + (turn & 1) * 256;
                 tb[tw * 32 + lane] = sum;
-                named_sync<1, 256>();
+                if (tg == 0) named_sync<1, 256>();
+                else named_sync<6, 256>();
                 // decay from the middle of the chunk (between rows 31 and 32) outward
                 float lo = 0.f, hi = 0.f, off = 0.f;
 #pragma unroll
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     else hi += t;
                     if (tw < 4 ? (w > tw && w < 4) : (w >= 4 && w < tw)) off += t;
                 }
-                const bool keep = lo >= -PREP_SAFE && hi >= -PREP_SAFE;     // false for NaN too
+                const bool keep = lo >= -PREP_SAFE * L2E && hi >= -PREP_SAFE * L2E;     // false for NaN too
                 float E[8];
                 if (tw < 4) {
 #pragma unroll
@@ -330,31 +350,37 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     }
                 }
                 const uint32_t steep = __ballot_sync(0xffffffffu, !keep);
-                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
-                unsigned char *ops = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES;
+                if (steep != 0u && !keep) {                // a steep channel enters the product as zeros
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    constexpr float L2E = 1.4426950408889634f;
-                    const float e = keep ? E[i] * L2E : 0.f;
-                    const float kk = keep ? kv[i] : 0.f, qq = keep ? qv[i] : 0.f;
-                    const float up = ex2(e), dn = ex2(-e);
-                    const float a = kk * up, b = qq * up, x = kk * dn;
-                    const uint32_t ah = __float_as_uint(a) & 0xffffe000u, bh = __float_as_uint(b) & 0xffffe000u,
-                                   xh = __float_as_uint(x) & 0xffffe000u;
-                    // row 8 tw + i of the tile, its 16-byte chunk lane / 4 at position (lane / 4) ^ i
-                    unsigned char *at = ops + tw * 1024 + i * 128 + 16 * ((lane >> 2) ^ i) + 4 * (lane & 3);
-                    *reinterpret_cast<uint32_t *>(at) = ah;
-                    *reinterpret_cast<uint32_t *>(at + 8192) = bh;
-                    *reinterpret_cast<float *>(at + 16384) = a - __uint_as_float(ah);
-                    *reinterpret_cast<float *>(at + 24576) = b - __uint_as_float(bh);
-                    *reinterpret_cast<uint32_t *>(at + 32768) = xh;
-                    *reinterpret_cast<float *>(at + 40960) = x - __uint_as_float(xh);
+                    for (int i = 0; i < 8; ++i) kv[i] = qv[i] = E[i] = 0.f;
+                }
+                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
+                unsigned char *ops = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES + tw * 1024 + 4 * (lane & 3);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {           // two rows at a time, in paired instructions
+                    const float2 k2 = make_float2(kv[i], kv[i + 1]);
+                    const float2 up = make_float2(ex2(E[i]), ex2(E[i + 1])), dn = make_float2(ex2(-E[i]), ex2(-E[i + 1]));
+                    uint32_t h[3][2], l[3][2];
+                    split2(__fmul2_rn(k2, up), h[0][0], h[0][1], l[0][0], l[0][1]);
+                    split2(__fmul2_rn(make_float2(qv[i], qv[i + 1]), up), h[1][0], h[1][1], l[1][0], l[1][1]);
+                    split2(__fmul2_rn(k2, dn), h[2][0], h[2][1], l[2][0], l[2][1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // row 8 tw + i + e of the tile, its 16-byte chunk lane / 4 at position (lane / 4) ^ (i + e)
+                        unsigned char *at = ops + (i + e) * 128 + 16 * ((lane >> 2) ^ (i + e));
+                        *reinterpret_cast<uint32_t *>(at) = h[0][e];
+                        *reinterpret_cast<uint32_t *>(at + 8192) = h[1][e];
+                        *reinterpret_cast<uint32_t *>(at + 16384) = l[0][e];
+                        *reinterpret_cast<uint32_t *>(at + 24576) = l[1][e];
+                        *reinterpret_cast<uint32_t *>(at + 32768) = h[2][e];
+                        *reinterpret_cast<uint32_t *>(at + 40960) = l[2][e];
+                    }
                 }
                 if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
-                if (s == nsl - 1) {
+                if (s + 2 >= nsl) {
                     kmax = warp_max(kmax);
                     qmax = warp_max(qmax);
-                    if (lane == 0) kq_m[(c & 7) * 8 + tw] = make_float2(kmax, qmax);
+                    if (lane == 0) kq_m[(c & 7) * 16 + 8 * tg + tw] = make_float2(kmax, qmax);
                 }
                 fence_proxy_async();
                 __syncwarp();
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             }
         }
     } else if (warp < 8) {
-        tc::more_registers<120>();
+        tc::more_registers<112>();
         // --------------------------------------------------------------- epilogue
         const bool isP = warp >= 6;
         const int i = 32 * (warp & 1) + lane;              // chunk row
@@ -458,24 +484,20 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                 image_row(img + IMG_PHI, PLO ? img + IMG_PLO : nullptr, i, x, s);
                 float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
                 if (lane == 0) hdr[HDR_PINV + (warp & 1)] = inv;
-                if (warp == 6 && lane < 8) {
-                    float2 t = kq_m[(c & 7) * 8 + lane];
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) {
-                        t.x = fmaxf(t.x, __shfl_xor_sync(0xffu, t.x, o));
-                        t.y = fmaxf(t.y, __shfl_xor_sync(0xffu, t.y, o));
-                    }
+                if (warp == 6) {                           // 8 transform warps to a group, the second idle at K = 32
+                    const float2 t = lane < 8 * (nsl > 1 ? 2 : 1) ? kq_m[(c & 7) * 16 + lane] : make_float2(0.f, 0.f);
+                    const float km = warp_max(t.x), qm = warp_max(t.y);
                     if (lane == 0) {
-                        hdr[HDR_KMAX] = t.x;
-                        hdr[HDR_QMAX] = t.y;
+                        hdr[HDR_KMAX] = km;
+                        hdr[HDR_QMAX] = qm;
                     }
                 }
             }
         }
     } else {
-        tc::more_registers<136>();
+        tc::more_registers<112>();
         // ------------------------------------------------------------ solve pairs
-        const int pr = (warp - 16) >> 1, pt = tid - 16 * 32 - 64 * pr, bar = 4 + pr;
+        const int pr = (warp - 24) >> 1, pt = tid - 24 * 32 - 64 * pr, bar = 4 + pr;
         float *Ab = reinterpret_cast<float *>(sm + PREP_OFF_AT) + pr * 2560;
         float *X = reinterpret_cast<float *>(sm + PREP_OFF_X) + pr * KGB_X_FLOATS;
         float *xs = reinterpret_cast<float *>(sm + PREP_OFF_XS) + pr * 64 * PREP_XP;

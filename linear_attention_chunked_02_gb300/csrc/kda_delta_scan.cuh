@@ -58,7 +58,8 @@ constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [128 lanes] la
 constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
 constexpr int SCAN_OFF_TOT = SCAN_OFF_OUT + 2 * 128 * 8;       // [8 row groups][128] sums of g
 constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [2 halves][3][128], sums of a chunk taken token by token
-constexpr int SCAN_OFF_KQ = 12 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
+constexpr int SCAN_OFF_GH = SCAN_OFF_SUM + 2 * 3 * 128 * 4;     // [64] decays of the rows, where a head has one
+constexpr int SCAN_OFF_KQ = 13 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
 template <bool PLO>
 constexpr int scan_off_kh() { return SCAN_OFF_KQ + (PLO ? 4 : 3) * 16384; }    // K e^{G_C-G} transposed, hi and lo:
                                                                                // [128 channels][128 B]
@@ -76,7 +77,7 @@ constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T
 template <typename T, bool PLO>
 constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
 static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 24 * 4 <= SCAN_OFF_GAM, "header fits");
-static_assert(SCAN_OFF_SUM + 2 * 3 * 128 * 4 <= SCAN_OFF_KQ, "small buffers fit");
+static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
 static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
 // A chunk is taken token by token where its values are below 2^-16 of what the state can add to R
@@ -364,7 +365,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
             prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
             accumulator(SB_D3, ph);
-            {
+            if (weak) {                                    // S and its bound are there
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = S[16 * b + i];
+                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, sS);
+                }
+            } else {
                 const float2 f = both(invU * invk);
                 float mx = 0.f;
 #pragma unroll
@@ -380,7 +389,6 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     for (int i = 0; i < 16; i += 2) {
                         float2 w = __ffma2_rn(gm[i / 2], make_float2(S[16 * b + i], S[16 * b + i + 1]),
                                               __fmul2_rn(f, make_float2(x[i], x[i + 1])));
-                        if (weak) w = make_float2(S[16 * b + i], S[16 * b + i + 1]);
                         mx = max3(mx, w.x, w.y);
                         S[16 * b + i] = x[i] = w.x;
                         S[16 * b + i + 1] = x[i + 1] = w.y;
@@ -409,11 +417,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         const int rg = warp - 8;                           // rows 8 rg .. + 7
         const int hk = h / (p.H / p.Hk);
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
-        // this thread's first row, channels 2 lane, 2 lane + 1 (+ 64 x), in the staging buffer or in memory
-        const int ks = STAGED ? p.K : p.Hk * p.K, gs = p.gate != 0 ? p.H : STAGED ? p.K : p.H * p.K;
+        // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
+        // the next one.  Channels past K take another's values under a scale of zero.
+        const int ks = STAGED ? p.K : p.Hk * p.K, gs = p.gate != 0 ? 0 : STAGED ? p.K : p.H * p.K;
         unsigned char *st = sm + scan_off_st<T, PLO>();
-        T *kst = reinterpret_cast<T *>(st) + 8 * rg * p.K + 2 * lane;
-        float *gst = reinterpret_cast<float *>(st + 32768) + 8 * rg * p.K + 2 * lane;
+        float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             const int left = rows - 64 * c - 8 * rg;       // live rows from this thread's first on
@@ -421,44 +429,51 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const T *kp, *qp;
             const float *gp;
             if (STAGED) {
-                kp = kst;
-                qp = kst + 64 * 128;
-                gp = gst;
+                kp = reinterpret_cast<T *>(st) + 8 * rg * p.K;
+                qp = kp + 64 * 128;
+                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * p.K;
             } else {
-                kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * p.K + 2 * lane;
-                qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * p.K + 2 * lane;
-                gp = p.g + (row * p.H + h) * p.K + 2 * lane;
+                kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * p.K;
+                qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * p.K;
+                gp = p.g + (row * p.H + h) * p.K;
             }
-            const float *gh = p.g + row * p.H + h;         // one decay to a head
+            if (p.gate != 0) {                             // one decay to a row
+                if (lane < 8) sg[8 * rg + lane] = lane < left ? p.g[(row + lane) * p.H + h] : 0.f;
+                __syncwarp();
+                gp = sg + 8 * rg;
+            }
             const float2 kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + img_hdr<PLO>() + 4 * HDR_KMAX);
             if (STAGED) {
                 prep_wait(ok, &bars[SB_ST_FULL], ph, p.err);
                 for (int i = left > 0 ? left : 0; i < 8; ++i)      // rows past the end hold the next request's
-                    for (int x = 0; x < nh; ++x)
-                        if (64 * x + 2 * lane < p.K) {
-                            *reinterpret_cast<raw *>(kst + i * p.K + 64 * x) = raw{};
-                            *reinterpret_cast<raw *>(kst + 64 * 128 + i * p.K + 64 * x) = raw{};
-                            if (p.gate == 0) *reinterpret_cast<float2 *>(gst + i * p.K + 64 * x) = both(0.f);
-                        }
+                    for (int x = lane; x < p.K; x += 32) {
+                        const_cast<T *>(kp)[i * ks + x] = T(0.f);
+                        const_cast<T *>(qp)[i * ks + x] = T(0.f);
+                        if (p.gate == 0) const_cast<float *>(gp)[i * gs + x] = 0.f;
+                    }
+                __syncwarp();
             }
-            // row i of channel half x; channels past K count as zeros
-            auto two = [&](const T *at, int i, int x) {
-                const bool in = 64 * x + 2 * lane < p.K && (STAGED || i < left);
-                return in ? *reinterpret_cast<const raw *>(at + i * ks + 64 * x) : raw{};
+            auto chan = [&](int x) { const int d = 64 * x + 2 * lane; return d < p.K ? d : 2 * lane % p.K; };
+            auto two = [&](const T *at, int i, int d) {
+                const bool in = STAGED || i < left;
+                return in ? *reinterpret_cast<const raw *>(at + i * ks + d) : raw{};
             };
-            auto decay = [&](int i, int x) {
-                if (p.gate != 0) return __fmul2_rn(both(i < left ? gh[i * gs] : 0.f), both(L2E));
-                const bool in = 64 * x + 2 * lane < p.K && (STAGED || i < left);
-                return __fmul2_rn(in ? *reinterpret_cast<const float2 *>(gp + i * gs + 64 * x) : both(0.f), both(L2E));
+            auto decay = [&](int i, int d) {               // in powers of two
+                float2 g;
+                if (p.gate != 0) g = both(gp[i]);
+                else if (STAGED || i < left) g = *reinterpret_cast<const float2 *>(gp + i * gs + d);
+                else g = both(0.f);
+                return __fmul2_rn(g, both(L2E));
             };
             for (int x = 0; x < nh; ++x) {
                 float2 sum = both(0.f);
+                const int d = chan(x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = __fadd2_rn(sum, decay(i, x));
+                for (int i = 0; i < 8; ++i) sum = __fadd2_rn(sum, decay(i, d));
                 *reinterpret_cast<float2 *>(tot + rg * 128 + 64 * x + 2 * lane) = sum;
             }
             float inv, unused;
-            const float2 sk = both(pow2_scale(kqmax.x, KQ_LO, KQ_HI, inv));
+            const float sk1 = pow2_scale(kqmax.x, KQ_LO, KQ_HI, inv);
             const float2 cq = both(p.scale * pow2_scale(kqmax.y * fabsf(p.scale), KQ_LO, KQ_HI, unused) * inv);
             named_sync<1, 256>();
             // K e^G and scale Q e^G: row r of a tile is 128 bytes, its 16-byte chunk lane / 4 at (lane / 4) ^ (r & 7)
@@ -470,11 +485,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 unsigned char *kq = sm + SCAN_OFF_KQ + x * 8192 + rg * 1024 + 4 * (lane & 3);
                 raw rk[8], rq[8];                          // all loads before the first store
                 float2 g[8];
+                const int d = chan(x);
+                const float2 sk = both(64 * x + 2 * lane < p.K ? sk1 : 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    rk[i] = two(kp, i, x);
-                    rq[i] = two(qp, i, x);
-                    g[i] = decay(i, x);
+                    rk[i] = two(kp, i, d);
+                    rq[i] = two(qp, i, d);
+                    g[i] = decay(i, d);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -482,9 +499,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
                     const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
                     const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
-                    uint32_t kh, kl, qh, ql;
+                    uint32_t kh, kl, qh, ql = 0u;
                     split_f16(kv.x, kv.y, kh, kl);
-                    split_f16(qv.x, qv.y, qh, ql);
+                    if (PLO) split_f16(qv.x, qv.y, qh, ql);
+                    else qh = round_f16(qv.x, qv.y);
                     unsigned char *at = kq + i * 128 + 16 * ((lane >> 2) ^ i);
                     *reinterpret_cast<uint32_t *>(at) = kh;
                     *reinterpret_cast<uint32_t *>(at + 16384) = kl;
@@ -501,12 +519,19 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             prep_wait(ok, &bars[SB_KH_EMPTY], ph ^ 1, p.err);
             for (int x = 0; x < nh; ++x) {
                 const float *tb = tot + 64 * x + 2 * lane;
-                float2 after = both(0.f), y[8];
+                float2 after = both(0.f), y[8], g[8];
+                const int dc = chan(x);
+                const float2 sk = both(64 * x + 2 * lane < p.K ? sk1 : 0.f);
                 for (int w = 7; w > rg; --w) after = __fadd2_rn(after, *reinterpret_cast<const float2 *>(tb + w * 128));
 #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = W2::wide(two(kp, i, dc));
+                    g[i] = decay(i, dc);
+                }
+#pragma unroll
                 for (int i = 7; i >= 0; --i) {
-                    y[i] = __fmul2_rn(W2::wide(two(kp, i, x)), __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
-                    after = __fadd2_rn(after, decay(i, x));
+                    y[i] = __fmul2_rn(y[i], __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
+                    after = __fadd2_rn(after, g[i]);
                 }
                 uint4 ah, al, bh, bl;
                 split_f16(y[0].x, y[1].x, ah.x, al.x); split_f16(y[2].x, y[3].x, ah.y, al.y);
