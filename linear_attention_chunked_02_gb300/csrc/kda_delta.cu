@@ -76,7 +76,7 @@ bool encode_delta(const DeltaParams &p, int32_t dt, int64_t rows, DeltaMaps &pre
 }
 
 // Opt-in shared memory of the chunked form's kernels, set once per device.
-template <typename T, bool PLO>
+template <typename T, bool PLO, bool W128>
 cudaError_t chunked_ready(int device) {
     static std::mutex mu;
     static bool done[64] = {false};
@@ -86,22 +86,29 @@ cudaError_t chunked_ready(int device) {
     cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          prep_bytes<T>());
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  scan_bytes<T, PLO>());
     done[device] = e == cudaSuccess;
     return e;
 }
 
-template <typename T, bool PLO>
-cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms, cudaStream_t s) {
-    cudaError_t e = chunked_ready<T, PLO>(device);
+template <typename T, bool PLO, bool W128>
+cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms, cudaStream_t s) {
+    cudaError_t e = chunked_ready<T, PLO, W128>(device);
     if (e != cudaSuccess) return e;
     const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms);
     e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(prep_bytes<T>()), s, prep,
                    p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(true, kda_delta_scan_kernel<T, PLO>, unsigned(p.nseq) * unsigned(p.H), SCAN_THREADS,
+    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128>, unsigned(p.nseq) * unsigned(p.H), SCAN_THREADS,
                       size_t(scan_bytes<T, PLO>()), s, scan, p);
+}
+
+template <typename T, bool PLO>
+cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
+                           cudaStream_t s) {
+    return p.K == 128 && p.V == 128 ? launch_widths<T, PLO, true>(p, prep, scan, device, sms, s)
+                                    : launch_widths<T, PLO, false>(p, prep, scan, device, sms, s);
 }
 
 kda_status_t run_chunked(DeltaParams p, int32_t dtype, int64_t rows, cudaStream_t s) {

@@ -34,7 +34,7 @@
 //   * warps 8-15 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
 //     time; a thread has two channels of eight rows, so that sums along the rows run in
 //     registers and eight tokens of a channel make one 16-byte store;
-//   * warps 16-19 (output): a lane quarter each, |v| of the next chunk and O;
+//   * warps 16-19 (output): O, a lane quarter each;
 //   * warp 20: MMA issue; warps 21, 22 and 23: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
 //     little in flight), so 16-bit q, k and g are staged in shared memory; 32-bit ones
@@ -48,14 +48,14 @@ namespace kda {
 constexpr int SCAN_THREADS = 24 * 32;
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
-              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_VMAX = 20, SB_IMG_READ = 21,
-              SCAN_NBARS = 23;
+              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_IMG_READ = 20,
+              SCAN_NBARS = 22;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_RED = 192;                  // a word to a warp: chunks before the sequence
 constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [2 halves][128 lanes] largest |S|
-constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [128 lanes] largest |v|
-constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
+constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [2 halves][128 lanes] largest |v|
+constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 2 * 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
 constexpr int SCAN_OFF_TOT = SCAN_OFF_OUT + 2 * 128 * 8;       // [8 row groups][128] sums of g
 constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [2 halves][3][128], sums of a chunk taken token by token
 constexpr int SCAN_OFF_GH = SCAN_OFF_SUM + 2 * 3 * 128 * 4;     // [64] decays of the rows, where a head has one
@@ -126,6 +126,33 @@ __device__ __forceinline__ void mma_split(int steps, uint32_t d, uint32_t ah, ui
     }
 }
 
+// Two 16-bit values in a register.
+template <typename T> struct Pair {
+    uint32_t r;
+    __device__ Pair() : r(0u) {}
+    __device__ Pair(T a, T b) : r(uint32_t(reinterpret_cast<const uint16_t &>(a)) | uint32_t(reinterpret_cast<const uint16_t &>(b)) << 16) {}
+    __device__ Pair abs() const { Pair x; x.r = r & 0x7fff7fffu; return x; }
+    __device__ Pair max(Pair o) const;                     // of values without NaN; a NaN counts as nothing
+    __device__ float2 wide() const;
+};
+template <> __device__ __forceinline__ Pair<__nv_bfloat16> Pair<__nv_bfloat16>::max(Pair o) const {
+    Pair x;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(x.r) : "r"(r), "r"(o.r));
+    return x;
+}
+template <> __device__ __forceinline__ Pair<__half> Pair<__half>::max(Pair o) const {
+    Pair x;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(x.r) : "r"(r), "r"(o.r));
+    return x;
+}
+template <> __device__ __forceinline__ float2 Pair<__nv_bfloat16>::wide() const {
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 Pair<__half>::wide() const {
+    return __half22float2(reinterpret_cast<const __half2 &>(r));
+}
+template <> struct Pair<float> {};
+
 // Two consecutive channels of q or k as they lie in memory, and widened.
 template <typename T> struct Two;
 template <> struct Two<float> { using raw = float2; static __device__ float2 wide(raw r) { return r; } };
@@ -182,7 +209,8 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[64]
     }
 }
 
-template <typename T, bool PLO>
+// W128: K and V are 128, which makes every row pitch on chip an immediate.
+template <typename T, bool PLO, bool W128>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -194,10 +222,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     constexpr bool STAGED = sizeof(T) == 2;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int n = int(blockIdx.x) / p.H, h = int(blockIdx.x) - n * p.H;
+    const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {8, 8, 1, 1, 4, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8, 4, 4, 4};
+        const int count[SCAN_NBARS] = {8, 8, 1, 1, 4, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8, 4, 4};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -232,7 +261,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     if (before < 0 || (int64_t(before) + nc) * p.H > p.n_tasks) nc = 0;
     const unsigned char *img0 = p.ws + (int64_t(before) * p.H + h) * img_bytes<PLO>();
     const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
-    const int nh = p.K > 64 ? 2 : 1;                       // halves of 64 channels
+    const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
 
     // registers: 768 threads of 80 at launch; 2 * 120 + 2 * 80 + 48 + 32 <= 6 * 80
@@ -256,16 +285,16 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             tc::fence_after_sync();
         };
         const int32_t e = state_entry(p, n);
-        const bool mine = v < p.V;
+        const bool mine = v < V;
         float S[64];                                       // S[64 half + i][v]
         {
-            const float *sp = p.state_in + ((int64_t(e < 0 ? 0 : e) * p.H + h) * p.K + 64 * half) * p.V + v;
+            const float *sp = p.state_in + ((int64_t(e < 0 ? 0 : e) * p.H + h) * K + 64 * half) * V + v;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-                S[i] = p.state_in != nullptr && e >= 0 && mine && 64 * half + i < p.K ? sp[int64_t(i) * p.V] : 0.f;
+                S[i] = p.state_in != nullptr && e >= 0 && mine && 64 * half + i < K ? sp[int64_t(i) * V] : 0.f;
         }
         const int t0 = 32 * half;                          // this thread's tokens of a chunk: t0 .. t0 + 31
-        const T *sv = reinterpret_cast<const T *>(sm + scan_off_v<PLO>()) + t0 * p.V + (mine ? v : 0);
+        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (mine ? v : 0);
         float bS = 0.f, invS = 1.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) bS = fmaxf(bS, fabsf(S[i]));
@@ -291,16 +320,30 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                                                                img_hdr<PLO>());
             const float minv = hdr[HDR_MINV + half], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
             const float kmax = hdr[HDR_KMAX];
-            prep_wait(ok, &bars[SB_VMAX], ph, p.err);
-            const float bv = svmax[v];
-            struct { T a, b; } vr[sizeof(T) == 2 ? 16 : 1];                // 16-bit values, two tokens to a word
+            prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
+            // rows past the end hold the next request's; columns past V stay in their lanes
+            for (int i = left > t0 ? left - t0 : 0; i < 32; ++i)
+                if (mine) sv[i * V] = T(0.f);
+            Pair<T> vr[sizeof(T) == 2 ? 16 : 1];           // 16-bit values, two tokens to a word
+            float bv = 0.f;
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) vr[i] = {sv[2 * i * p.V], sv[(2 * i + 1) * p.V]};
+                for (int i = 0; i < 16; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
+                Pair<T> m = vr[0].abs();
+#pragma unroll
+                for (int i = 1; i < 16; ++i) m = m.max(vr[i].abs());
+                const float2 f = m.wide();
+                bv = fmaxf(f.x, f.y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
             }
+            svmax[half * 128 + v] = bv;
+            pair_sync();
+            bv = fmaxf(svmax[v], svmax[128 + v]);
             float invk, invR, invU, invS1;
             pow2_scale(kmax, KQ_LO, KQ_HI, invk);
-            const float bR = bv + float(p.K) * kmax * bS;
+            const float bR = bv + float(K) * kmax * bS;
             const float sR = pow2_scale(bR, VS_LO, VS_HI, invR);
             const float bU = msum * bR;
             const float sU = pow2_scale(bU, VS_LO, VS_HI, invU);
@@ -309,7 +352,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             if (weak) {                                    // the same in both warps of the quarter
                 prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
                 float gmax = 0.f;
-                for (int i = 0; i < p.K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
+                for (int i = 0; i < K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
                 weak = __all_sync(0xffffffffu, gmax < SCAN_WEAK_G);
                 if (weak) {
                     scan_tokens<T>(p, S, ra + 64 * c, left < 64 ? left : 64, h, half, v, quarter,
@@ -337,8 +380,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float2 w;
-                        if constexpr (sizeof(T) == 2) w = make_float2(widen1(vr[8 * b + i].a), widen1(vr[8 * b + i].b));
-                        else w = make_float2(widen1(sv[(16 * b + 2 * i) * p.V]), widen1(sv[(16 * b + 2 * i + 1) * p.V]));
+                        if constexpr (sizeof(T) == 2) w = vr[8 * b + i].wide();
+                        else w = make_float2(widen1(sv[(16 * b + 2 * i) * V]), widen1(sv[(16 * b + 2 * i + 1) * V]));
                         w = __ffma2_rn(f, make_float2(x[b][2 * i], x[b][2 * i + 1]), __fmul2_rn(w, s2));
                         split_f16(w.x, w.y, hi[i], lo[i]);
                     }
@@ -403,10 +446,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             invS = invS1;
         }
         if (p.state_out != nullptr && e >= 0 && mine) {
-            float *sp = p.state_out + ((int64_t(e) * p.H + h) * p.K + 64 * half) * p.V + v;
+            float *sp = p.state_out + ((int64_t(e) * p.H + h) * K + 64 * half) * V + v;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-                if (64 * half + i < p.K) sp[int64_t(i) * p.V] = S[i];
+                if (64 * half + i < K) sp[int64_t(i) * V] = S[i];
         }
     } else if (warp < 16) {
         // (80 registers, as at launch)
@@ -419,7 +462,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
         // the next one.  Channels past K take another's values under a scale of zero.
-        const int ks = STAGED ? p.K : p.Hk * p.K, gs = p.gate != 0 ? 0 : STAGED ? p.K : p.H * p.K;
+        const int ks = STAGED ? K : p.Hk * K, gs = STAGED ? K : p.H * K;
         unsigned char *st = sm + scan_off_st<T, PLO>();
         float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
         for (int c = 0; c < nc; ++c) {
@@ -429,13 +472,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const T *kp, *qp;
             const float *gp;
             if (STAGED) {
-                kp = reinterpret_cast<T *>(st) + 8 * rg * p.K;
+                kp = reinterpret_cast<T *>(st) + 8 * rg * K;
                 qp = kp + 64 * 128;
-                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * p.K;
+                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * K;
             } else {
-                kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * p.K;
-                qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * p.K;
-                gp = p.g + (row * p.H + h) * p.K;
+                kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * K;
+                qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * K;
+                gp = p.g + (row * p.H + h) * K;
             }
             if (p.gate != 0) {                             // one decay to a row
                 if (lane < 8) sg[8 * rg + lane] = lane < left ? p.g[(row + lane) * p.H + h] : 0.f;
@@ -446,30 +489,27 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             if (STAGED) {
                 prep_wait(ok, &bars[SB_ST_FULL], ph, p.err);
                 for (int i = left > 0 ? left : 0; i < 8; ++i)      // rows past the end hold the next request's
-                    for (int x = lane; x < p.K; x += 32) {
+                    for (int x = lane; x < K; x += 32) {
                         const_cast<T *>(kp)[i * ks + x] = T(0.f);
                         const_cast<T *>(qp)[i * ks + x] = T(0.f);
                         if (p.gate == 0) const_cast<float *>(gp)[i * gs + x] = 0.f;
                     }
                 __syncwarp();
             }
-            auto chan = [&](int x) { const int d = 64 * x + 2 * lane; return d < p.K ? d : 2 * lane % p.K; };
+            auto chan = [&](int x) { const int d = 64 * x + 2 * lane; return W128 || d < K ? d : 2 * lane % K; };
             auto two = [&](const T *at, int i, int d) {
                 const bool in = STAGED || i < left;
                 return in ? *reinterpret_cast<const raw *>(at + i * ks + d) : raw{};
             };
-            auto decay = [&](int i, int d) {               // in powers of two
-                float2 g;
-                if (p.gate != 0) g = both(gp[i]);
-                else if (STAGED || i < left) g = *reinterpret_cast<const float2 *>(gp + i * gs + d);
-                else g = both(0.f);
-                return __fmul2_rn(g, both(L2E));
+            auto decay = [&](int i, int d) {
+                if (p.gate != 0) return both(gp[i]);
+                return STAGED || i < left ? *reinterpret_cast<const float2 *>(gp + i * gs + d) : both(0.f);
             };
             for (int x = 0; x < nh; ++x) {
                 float2 sum = both(0.f);
                 const int d = chan(x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = __fadd2_rn(sum, decay(i, d));
+                for (int i = 0; i < 8; ++i) sum = __ffma2_rn(decay(i, d), both(L2E), sum);   // in powers of two
                 *reinterpret_cast<float2 *>(tot + rg * 128 + 64 * x + 2 * lane) = sum;
             }
             float inv, unused;
@@ -486,7 +526,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 raw rk[8], rq[8];                          // all loads before the first store
                 float2 g[8];
                 const int d = chan(x);
-                const float2 sk = both(64 * x + 2 * lane < p.K ? sk1 : 0.f);
+                const float2 sk = both(W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     rk[i] = two(kp, i, d);
@@ -495,7 +535,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    G = __fadd2_rn(G, g[i]);
+                    G = __ffma2_rn(g[i], both(L2E), G);
                     const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
                     const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
                     const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
@@ -521,7 +561,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 const float *tb = tot + 64 * x + 2 * lane;
                 float2 after = both(0.f), y[8], g[8];
                 const int dc = chan(x);
-                const float2 sk = both(64 * x + 2 * lane < p.K ? sk1 : 0.f);
+                const float2 sk = both(W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
                 for (int w = 7; w > rg; --w) after = __fadd2_rn(after, *reinterpret_cast<const float2 *>(tb + w * 128));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -531,7 +571,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 #pragma unroll
                 for (int i = 7; i >= 0; --i) {
                     y[i] = __fmul2_rn(y[i], __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
-                    after = __fadd2_rn(after, g[i]);
+                    after = __ffma2_rn(g[i], both(L2E), after);
                 }
                 uint4 ah, al, bh, bl;
                 split_f16(y[0].x, y[1].x, ah.x, al.x); split_f16(y[2].x, y[3].x, ah.y, al.y);
@@ -559,26 +599,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         // ----------------------------------------------------------------- output
         const int quarter = warp & 3, v = 32 * quarter + lane;
         const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
-        const bool mine = v < p.V;
-        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + (mine ? v : 0);
-        float *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX);
+        const bool mine = v < V;
         const float2 *sout = reinterpret_cast<const float2 *>(sm + SCAN_OFF_OUT);
-        const int vs = p.H * p.V;
-        T *op = static_cast<T *>(p.o) + (ra * p.H + h) * p.V + v;
-        auto values = [&](int c) {                         // the largest |v| of chunk c
-            const int left = rows - 64 * c;
-            prep_wait(ok, &bars[SB_V_FULL], c & 1, p.err);
-            // rows past the end hold the next request's; columns past V stay in their lanes
-            for (int i = left; i < 64; ++i)
-                if (mine) sv[i * p.V] = T(0.f);
-            float b = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < 64; i += 2) b = max3(b, widen1(sv[i * p.V]), widen1(sv[(i + 1) * p.V]));
-            svmax[v] = b;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_VMAX]);
-        };
-        if (nc > 0) values(0);
+        // token 8 b + i of a chunk: a base that is the same for the warp, and this lane's offset of row i
+        const uint32_t step = uint32_t(p.H) * V * sizeof(T);
+        uint32_t off[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) off[i] = v * sizeof(T) + i * step;
+        unsigned char *const ob = static_cast<unsigned char *>(p.o) + (ra * p.H + h) * V * int64_t(sizeof(T));
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             // O = (scale Q e^G) S0 + P U
@@ -592,13 +620,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             if (lane == 0) mbar_arrive(&bars[SB_IMG_READ + c % NI]);
             float invq;
             pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
-            if (c + 1 < nc) values(c + 1);
             prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
             __syncwarp();
             tc::fence_after_sync();
             const bool weak = inv.x < 0.f;
             const int left = mine && !weak ? rows - 64 * c : 0;
-            T *o = op + int64_t(64 * c) * vs;
+            const bool whole = __all_sync(0xffffffffu, left >= 64);
             const float2 f = both(inv.x * invq);
 #pragma unroll 1
             for (int b = 0; b < 8; ++b) {
@@ -613,10 +640,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     x[i] = w.x;
                     x[i + 1] = w.y;
                 }
+                unsigned char *o = ob + int64_t(64 * c + 8 * b) * step;
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (8 * b + i < left) put1(o, x[i]);
-                    o += vs;
+                    for (int i = 0; i < 8; ++i) put1(reinterpret_cast<T *>(o + off[i]), x[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (8 * b + i < left) put1(reinterpret_cast<T *>(o + off[i]), x[i]);
                 }
             }
             tc::fence_before_sync();
@@ -679,7 +710,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // -------------------------------------------- loads of q, k and g (16-bit)
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
-                const uint32_t bytes = 2 * 64 * p.K * sizeof(T) + (p.gate == 0 ? 64 * p.K * 4 : 0);
+                const uint32_t bytes = 2 * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);
                 const int hk = h / (p.H / p.Hk);
                 for (int c = 0; c < nc; ++c) {
                     prep_wait(ok, &bars[SB_ST_EMPTY], (c & 1) ^ 1, p.err);
@@ -700,7 +731,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
                 __syncwarp();
                 if (tc::elect_one()) {
-                    mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * p.V * sizeof(T));
+                    mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * V * sizeof(T));
                     tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, h, int(ra) + 64 * c, &bars[SB_V_FULL]);
                 }
                 __syncwarp();
