@@ -720,6 +720,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         tma_load_3d(st, &maps.k, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
                         tma_load_3d(st + 16384, &maps.q, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
                         if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, h, int(ra) + 64 * c, &bars[SB_ST_FULL]);
+                        if (c + 1 < nc) {                  // the next chunk's on their way to L2 meanwhile
+                            tc::prefetch_3d(&maps.k, 0, hk, int(ra) + 64 * c + 64);
+                            tc::prefetch_3d(&maps.q, 0, hk, int(ra) + 64 * c + 64);
+                            if (p.gate == 0) tc::prefetch_3d(&maps.g, 0, h, int(ra) + 64 * c + 64);
+                        }
                     }
                     __syncwarp();
                 }
@@ -733,6 +738,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (tc::elect_one()) {
                     mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * V * sizeof(T));
                     tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, h, int(ra) + 64 * c, &bars[SB_V_FULL]);
+                    if (c + 1 < nc) tc::prefetch_3d(&maps.v, 0, h, int(ra) + 64 * c + 64);
                 }
                 __syncwarp();
             }
@@ -747,6 +753,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     mbar_arrive_expect_tx(&bars[SB_IMG_FULL + c % NI], img_bytes<PLO>());
                     bulk_load(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>(), img0 + c * img_step,
                               img_bytes<PLO>(), &bars[SB_IMG_FULL + c % NI]);
+                    if (c + 1 < nc) tc::prefetch_bulk(img0 + (c + 1) * img_step, img_bytes<PLO>());
                 }
                 __syncwarp();
             }

@@ -12,6 +12,7 @@
 // 1024-byte swizzle atom, and atoms follow each other along M (or N).
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 namespace kda {
@@ -149,6 +150,15 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A tile, or consecutive bytes (a multiple of 16), on their way to L2 only.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 
 // Registers of a warpgroup (four aligned warps, all of which execute it) moved to or
 // from the pool that the CTA was launched with.
