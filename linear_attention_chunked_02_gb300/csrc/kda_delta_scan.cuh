@@ -27,15 +27,15 @@
 // the four lane quarters each look out for such a chunk and take it token by token in
 // FP32 (scan_tokens).
 //
-// One CTA of six warpgroups per sequence-head (registers moved to the chain):
-//   * warps 0-7 (chain): two warps to each lane quarter, half the columns each; S in
+// One CTA of eight warpgroups per sequence-head (registers moved to the chain):
+//   * warps 0-15 (chain): four warps to each lane quarter, a quarter of the columns each; S in
 //     registers.  What bounds the walk is their path from state to state, so all
 //     else is on other warps;
-//   * warps 8-15 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
+//   * warps 16-23 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
 //     time; a thread has two channels of eight rows, so that sums along the rows run in
 //     registers and eight tokens of a channel make one 16-byte store;
-//   * warps 16-19 (output): O, a lane quarter each;
-//   * warp 20: MMA issue; warps 21, 22 and 23: the loads (TMA) of q, k and g, of v, and of the
+//   * warps 24-27 (output): O, a lane quarter each;
+//   * warp 28: MMA issue; warps 29, 30 and 31: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
 //     little in flight), so 16-bit q, k and g are staged in shared memory; 32-bit ones
 //     find no room there and are read directly.
@@ -45,7 +45,8 @@
 
 namespace kda {
 
-constexpr int SCAN_THREADS = 24 * 32;
+constexpr int SCAN_THREADS = 32 * 32;
+constexpr int SCAN_PARTS = 4;                      // chain threads to a lane
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
               SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_IMG_READ = 20,
@@ -53,13 +54,13 @@ constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY =
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_RED = 192;                  // a word to a warp: chunks before the sequence
 constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
-constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [2 halves][128 lanes] largest |S|
-constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 2 * 128 * 4;      // [2 halves][128 lanes] largest |v|
-constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 2 * 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
+constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [4 parts][128 lanes] largest |S|
+constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 4 * 128 * 4;      // [4 parts][128 lanes] largest |v|
+constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 4 * 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
 constexpr int SCAN_OFF_TOT = SCAN_OFF_OUT + 2 * 128 * 8;       // [8 row groups][128] sums of g
-constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [2 halves][3][128], sums of a chunk taken token by token
-constexpr int SCAN_OFF_GH = SCAN_OFF_SUM + 2 * 3 * 128 * 4;     // [64] decays of the rows, where a head has one
-constexpr int SCAN_OFF_KQ = 13 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
+constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [4 parts][128], sums of a chunk taken token by token
+constexpr int SCAN_OFF_GH = SCAN_OFF_SUM + 4 * 128 * 4;     // [64] decays of the rows, where a head has one
+constexpr int SCAN_OFF_KQ = 14 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
 template <bool PLO>
 constexpr int scan_off_kh() { return SCAN_OFF_KQ + (PLO ? 4 : 3) * 16384; }    // K e^{G_C-G} transposed, hi and lo:
                                                                                // [128 channels][128 B]
@@ -76,7 +77,7 @@ template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
 template <typename T, bool PLO>
 constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
-static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 24 * 4 <= SCAN_OFF_GAM, "header fits");
+static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 32 * 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
 static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
@@ -167,45 +168,49 @@ template <> struct Two<__half> {
     static __device__ float2 wide(raw r) { return __half22float2(*reinterpret_cast<const __half2 *>(&r)); }
 };
 
-// A chunk token by token, for the two warps of one lane quarter: thread (half, v) has
-// S[64 half + i][v].  `row` is the chunk's first row, `n` its tokens; `sum` [2][3][128]
-// of shared memory takes the halves' partial sums.
+// A chunk token by token, for the four warps of one lane quarter: thread (part, v) has
+// S[32 part + i][v].  `row` is the chunk's first row, `n` its tokens; `sum` [4][128]
+// of shared memory takes the parts' sums.
 template <typename T>
-__device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[64], int64_t row, int n, int h, int half,
+__device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32], int64_t row, int n, int h, int part,
                                             int v, int quarter, float *sum) {
-    const int hk = h / (p.H / p.Hk);
+    const int hk = h / (p.H / p.Hk), d0 = 32 * part;
+    auto sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(8 + quarter) : "memory"); };
+    auto total = [&](float x) {
+        sum[part * 128 + v] = x;
+        sync();
+        x = (sum[v] + sum[128 + v]) + (sum[256 + v] + sum[384 + v]);
+        sync();
+        return x;
+    };
     for (int t = 0; t < n; ++t) {
         const int64_t r = row + t;
-        const T *kp = static_cast<const T *>(p.k) + (r * p.Hk + hk) * p.K + 64 * half;
-        const T *qp = static_cast<const T *>(p.q) + (r * p.Hk + hk) * p.K + 64 * half;
-        const float *gp = p.g + (p.gate == 0 ? (r * p.H + h) * p.K + 64 * half : r * p.H + h);
+        const T *kp = static_cast<const T *>(p.k) + (r * p.Hk + hk) * p.K + d0;
+        const T *qp = static_cast<const T *>(p.q) + (r * p.Hk + hk) * p.K + d0;
+        const float *gp = p.g + (p.gate == 0 ? (r * p.H + h) * p.K + d0 : r * p.H + h);
         float a = 0.f, b = 0.f, qk = 0.f;
+        if (d0 < p.K) {                                    // K is a multiple of 32
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (64 * half + i < p.K) {
+            for (int i = 0; i < 32; ++i) {
                 const float kd = widen1(kp[i]), qd = widen1(qp[i]);
                 S[i] *= expf(gp[p.gate == 0 ? i : 0]);
                 a = fmaf(kd, S[i], a);
                 b = fmaf(qd, S[i], b);
                 qk = fmaf(qd, kd, qk);
             }
-        float *mine = sum + half * 384 + v;
-        mine[0] = a;
-        mine[128] = b;
-        mine[256] = qk;
-        asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
-        a = sum[v] + sum[384 + v];
-        b = sum[128 + v] + sum[512 + v];
-        qk = sum[256 + v] + sum[640 + v];
+        }
+        a = total(a);
+        b = total(b);
+        qk = total(qk);
         const bool in = v < p.V;
         const int64_t at = (r * p.H + h) * p.V + v;
         const float val = in ? widen1(static_cast<const T *>(p.v)[at]) : 0.f;
         const float u = widen1(static_cast<const T *>(p.beta)[r * p.H + h]) * (val - a);
-        if (in && half == 0) put1(static_cast<T *>(p.o) + at, p.scale * fmaf(qk, u, b));
+        if (in && part == 0) put1(static_cast<T *>(p.o) + at, p.scale * fmaf(qk, u, b));
+        if (d0 < p.K) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (64 * half + i < p.K) S[i] = fmaf(widen1(kp[i]), u, S[i]);
-        asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory");
+            for (int i = 0; i < 32; ++i) S[i] = fmaf(widen1(kp[i]), u, S[i]);
+        }
     }
 }
 
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {8, 8, 1, 1, 4, 1, 1, 1, 1, 8, 1, 8, 1, 8, 1, 1, 1, 8, 1, 8, 4, 4};
+        const int count[SCAN_NBARS] = {16, 8, 1, 1, 4, 1, 1, 1, 1, 16, 1, 8, 1, 16, 1, 1, 1, 16, 1, 8, 4, 4};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -264,15 +269,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
 
-    // registers: 768 threads of 80 at launch; 2 * 120 + 2 * 80 + 48 + 32 <= 6 * 80
-    if (warp < 8) {
-        tc::more_registers<120>();
+    // registers: 1024 threads of 64 at launch; 4 * 80 + 2 * 64 + 40 + 24 <= 8 * 64
+    if (warp < 16) {
+        tc::more_registers<80>();
         // ------------------------------------------------------------------ chain
-        const int quarter = warp & 3, half = warp >> 2, v = 32 * quarter + lane;
+        const int quarter = warp & 3, part = warp >> 2, v = 32 * quarter + lane;
         const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
-        float *smax = reinterpret_cast<float *>(sm + SCAN_OFF_MAX), *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX);
+        float *smax = reinterpret_cast<float *>(sm + SCAN_OFF_MAX) + v, *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX) + v;
         float2 *sout = reinterpret_cast<float2 *>(sm + SCAN_OFF_OUT);
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(8 + quarter) : "memory"); };
+        // the four threads of a lane
+        auto lane_max = [&](float *at, float x) {
+            at[part * 128] = x;
+            asm volatile("bar.sync %0, 128;" ::"r"(8 + quarter) : "memory");
+            return fmaxf(max3(at[0], at[128], at[256]), at[384]);
+        };
         auto release = [&](int b) {                        // operand columns written, accumulators read
             tc::wait_st();
             tc::fence_before_sync();
@@ -286,61 +296,65 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         };
         const int32_t e = state_entry(p, n);
         const bool mine = v < V;
-        float S[64];                                       // S[64 half + i][v]
+        float S[32];                                       // S[32 part + i][v]
+        const bool held = 32 * part < K;                   // K is a multiple of 32
         {
-            const float *sp = p.state_in + ((int64_t(e < 0 ? 0 : e) * p.H + h) * K + 64 * half) * V + v;
+            const float *sp = p.state_in + ((int64_t(e < 0 ? 0 : e) * p.H + h) * K + 32 * part) * V + v;
+            const bool read = p.state_in != nullptr && e >= 0 && mine && held;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                S[i] = p.state_in != nullptr && e >= 0 && mine && 64 * half + i < K ? sp[int64_t(i) * V] : 0.f;
+            for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * V] : 0.f;
         }
-        const int t0 = 32 * half;                          // this thread's tokens of a chunk: t0 .. t0 + 31
+        const int t0 = 16 * part;                          // this thread's tokens of a chunk: t0 .. t0 + 15
         T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (mine ? v : 0);
-        float bS = 0.f, invS = 1.f;
+        const uint32_t sop = tq + TM_SHI + 16 * part, rop = tq + TM_RHI + 8 * part;      // operand columns, hi parts
+        auto put_state = [&](float s) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) bS = fmaxf(bS, fabsf(S[i]));
-        if (nc > 0) {
-            smax[half * 128 + v] = bS;
-            pair_sync();
-            bS = fmaxf(smax[v], smax[128 + v]);
-            const float s = pow2_scale(bS, VS_LO, VS_HI, invS);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = S[16 * b + i];
-                put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, s);
+                put_operand(sop + 8 * b, sop + TM_SLO - TM_SHI + 8 * b, x, s);
             }
+        };
+        auto state_max = [&] {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) m = max3(m, S[i], S[i + 1]);
+            return m;
+        };
+        float bS = 0.f, invS = 1.f;
+        if (nc > 0) {
+            bS = lane_max(smax, state_max());
+            put_state(pow2_scale(bS, VS_LO, VS_HI, invS));
             release(SB_S);
         }
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             const int left = rows - 64 * c;
-            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
-            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
-                                                               img_hdr<PLO>());
-            const float minv = hdr[HDR_MINV + half], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
-            const float kmax = hdr[HDR_KMAX];
             prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
             // rows past the end hold the next request's; columns past V stay in their lanes
-            for (int i = left > t0 ? left - t0 : 0; i < 32; ++i)
+            for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
                 if (mine) sv[i * V] = T(0.f);
-            Pair<T> vr[sizeof(T) == 2 ? 16 : 1];           // 16-bit values, two tokens to a word
+            Pair<T> vr[sizeof(T) == 2 ? 8 : 1];            // 16-bit values, two tokens to a word
             float bv = 0.f;
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
+                for (int i = 0; i < 8; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
                 Pair<T> m = vr[0].abs();
 #pragma unroll
-                for (int i = 1; i < 16; ++i) m = m.max(vr[i].abs());
+                for (int i = 1; i < 8; ++i) m = m.max(vr[i].abs());
                 const float2 f = m.wide();
                 bv = fmaxf(f.x, f.y);
             } else {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
+                for (int i = 0; i < 16; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
             }
-            svmax[half * 128 + v] = bv;
-            pair_sync();
-            bv = fmaxf(svmax[v], svmax[128 + v]);
+            bv = lane_max(svmax, bv);
+            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
+            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
+                                                               img_hdr<PLO>());
+            const float minv = hdr[HDR_MINV + (part >> 1)], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
+            const float kmax = hdr[HDR_KMAX];
             float invk, invR, invU, invS1;
             pow2_scale(kmax, KQ_LO, KQ_HI, invk);
             const float bR = bv + float(K) * kmax * bS;
@@ -349,115 +363,90 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float sU = pow2_scale(bU, VS_LO, VS_HI, invU);
             float sS = pow2_scale(bS + 64.f * kmax * bU, VS_LO, VS_HI, invS1);
             bool weak = __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
-            if (weak) {                                    // the same in both warps of the quarter
+            if (weak) {                                    // the same in the four warps of the quarter
                 prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
                 float gmax = 0.f;
                 for (int i = 0; i < K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
                 weak = __all_sync(0xffffffffu, gmax < SCAN_WEAK_G);
                 if (weak) {
-                    scan_tokens<T>(p, S, ra + 64 * c, left < 64 ? left : 64, h, half, v, quarter,
+                    scan_tokens<T>(p, S, ra + 64 * c, left < 64 ? left : 64, h, part, v, quarter,
                                    reinterpret_cast<float *>(sm + SCAN_OFF_SUM));
-                    float mx = 0.f;                        // the new state's own bound
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) mx = fmaxf(mx, fabsf(S[i]));
-                    smax[half * 128 + v] = mx;
-                    pair_sync();
-                    sS = pow2_scale(fmaxf(smax[v], smax[128 + v]), VS_LO, VS_HI, invS1);
+                    sS = pow2_scale(lane_max(smax, state_max()), VS_LO, VS_HI, invS1);     // the new state's own bound
                 }
             }
-            if (half == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
+            if (part == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
             // R = V - (K e^G) S, scaled
             accumulator(SB_D1, ph);
             {
                 const float2 f = both(-invS * invk * sR), s2 = both(sR);
-                float x[2][16];
-                tc::ld16(tq + TM_D1 + t0, x[0]);
+                float x[16];
+                uint32_t hi[8], lo[8];
+                tc::ld16(tq + TM_D1 + t0, x);
+                tc::wait_ld();
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tc::wait_ld();
-                    if (b == 0) tc::ld16(tq + TM_D1 + t0 + 16, x[1]);
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 w;
-                        if constexpr (sizeof(T) == 2) w = vr[8 * b + i].wide();
-                        else w = make_float2(widen1(sv[(16 * b + 2 * i) * V]), widen1(sv[(16 * b + 2 * i + 1) * V]));
-                        w = __ffma2_rn(f, make_float2(x[b][2 * i], x[b][2 * i + 1]), __fmul2_rn(w, s2));
-                        split_f16(w.x, w.y, hi[i], lo[i]);
-                    }
-                    tc::st8(tq + TM_RHI + 16 * half + 8 * b, hi);
-                    tc::st8(tq + TM_RLO + 16 * half + 8 * b, lo);
+                for (int i = 0; i < 8; ++i) {
+                    float2 w;
+                    if constexpr (sizeof(T) == 2) w = vr[i].wide();
+                    else w = make_float2(widen1(sv[2 * i * V]), widen1(sv[(2 * i + 1) * V]));
+                    w = __ffma2_rn(f, make_float2(x[2 * i], x[2 * i + 1]), __fmul2_rn(w, s2));
+                    split_f16(w.x, w.y, hi[i], lo[i]);
                 }
+                tc::st8(rop, hi);
+                tc::st8(rop + TM_RLO - TM_RHI, lo);
             }
             release(SB_R);
             if (lane == 0) mbar_arrive(&bars[SB_V_EMPTY]);
             // U = M R
             accumulator(SB_D2, ph);
             {
-                const float f = invR * minv * sU;
-                float x[2][16];
-                tc::ld16(tq + TM_D1 + t0, x[0]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tc::wait_ld();
-                    if (b == 0) tc::ld16(tq + TM_D1 + t0 + 16, x[1]);
-                    put_operand(tq + TM_RHI + 16 * half + 8 * b, tq + TM_RLO + 16 * half + 8 * b, x[b], f);
-                }
+                float x[16];
+                tc::ld16(tq + TM_D1 + t0, x);
+                tc::wait_ld();
+                put_operand(rop, rop + TM_RLO - TM_RHI, x, invR * minv * sU);
             }
             release(SB_U);
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
             prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
             accumulator(SB_D3, ph);
-            if (weak) {                                    // S and its bound are there
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = S[16 * b + i];
-                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, sS);
-                }
-            } else {
+            float mx = 0.f;
+            if (weak) {                                    // S is there
+                put_state(sS);
+                mx = state_max();
+            } else if (held) {                             // channels past K stay zero
                 const float2 f = both(invU * invk);
-                float mx = 0.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     float x[16];
-                    tc::ld16(tq + TM_D3 + 64 * half + 16 * b, x);
-                    float2 gm[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        gm[i] = *reinterpret_cast<const float2 *>(gam + ph * 128 + 64 * half + 16 * b + 2 * i);
+                    tc::ld16(tq + TM_D3 + 32 * part + 16 * b, x);
                     tc::wait_ld();
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        float2 w = __ffma2_rn(gm[i / 2], make_float2(S[16 * b + i], S[16 * b + i + 1]),
-                                              __fmul2_rn(f, make_float2(x[i], x[i + 1])));
+                        const float2 gm = *reinterpret_cast<const float2 *>(gam + ph * 128 + 32 * part + 16 * b + i);
+                        const float2 w = __ffma2_rn(gm, make_float2(S[16 * b + i], S[16 * b + i + 1]),
+                                                    __fmul2_rn(f, make_float2(x[i], x[i + 1])));
                         mx = max3(mx, w.x, w.y);
                         S[16 * b + i] = x[i] = w.x;
                         S[16 * b + i + 1] = x[i + 1] = w.y;
                     }
-                    put_operand(tq + TM_SHI + 32 * half + 8 * b, tq + TM_SLO + 32 * half + 8 * b, x, sS);
+                    put_operand(sop + 8 * b, sop + TM_SLO - TM_SHI + 8 * b, x, sS);
                 }
-                smax[half * 128 + v] = mx;
             }
             release(SB_S);
-            pair_sync();
-            bS = fmaxf(smax[v], smax[128 + v]);
+            bS = lane_max(smax, mx);
             invS = invS1;
         }
-        if (p.state_out != nullptr && e >= 0 && mine) {
-            float *sp = p.state_out + ((int64_t(e) * p.H + h) * K + 64 * half) * V + v;
+        if (p.state_out != nullptr && e >= 0 && mine && held) {
+            float *sp = p.state_out + ((int64_t(e) * p.H + h) * K + 32 * part) * V + v;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (64 * half + i < K) sp[int64_t(i) * V] = S[i];
+            for (int i = 0; i < 32; ++i) sp[int64_t(i) * V] = S[i];
         }
-    } else if (warp < 16) {
-        // (80 registers, as at launch)
+    } else if (warp < 24) {
+        // (64 registers, as at launch)
         // --------------------------------------------------------------- operands
         constexpr float L2E = 1.4426950408889634f;
         using W2 = Two<T>;
         using raw = typename W2::raw;
-        const int rg = warp - 8;                           // rows 8 rg .. + 7
+        const int rg = warp - 16;                          // rows 8 rg .. + 7
         const int hk = h / (p.H / p.Hk);
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
@@ -594,8 +583,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             named_sync<1, 256>();                          // the sums are consumed
         }
-    } else if (warp < 20) {
-        tc::fewer_registers<48>();
+    } else if (warp < 28) {
+        tc::fewer_registers<40>();
         // ----------------------------------------------------------------- output
         const int quarter = warp & 3, v = 32 * quarter + lane;
         const uint32_t tq = tmem + (uint32_t(32 * quarter) << 16);
@@ -655,8 +644,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             if (lane == 0) mbar_arrive(&bars[SB_O_EMPTY]);
         }
     } else {
-        tc::fewer_registers<32>();
-        if (warp == 20) {
+        tc::fewer_registers<24>();
+        if (warp == 28) {
             // --------------------------------------------------------- MMA issue
             const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + scan_off_kh<PLO>());
             const int steps = 4 * nh;                      // of 16 channels
@@ -706,7 +695,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 __syncwarp();
             }
-        } else if (warp == 21) {
+        } else if (warp == 29) {
             // -------------------------------------------- loads of q, k and g (16-bit)
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
@@ -730,7 +719,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 if (nc > 0) prep_wait(ok, &bars[SB_ST_FULL], (nc - 1) & 1, p.err);
             }
-        } else if (warp == 22) {
+        } else if (warp == 30) {
             // --------------------------------------------------------- loads of v
             for (int c = 0; c < nc; ++c) {
                 prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
