@@ -48,8 +48,10 @@ kda_status_t run_rec(const DeltaParams &p, int32_t dtype, cudaStream_t s) {
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-// [rows, heads, width] as {width, heads, rows} with boxes of box x 1 x 64.
-bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, int32_t heads, int32_t width, int box) {
+// [rows, heads, width] as {width, heads, rows} with boxes of box x 1 x 64; swizzled: over the
+// box's row of 64 or 128 bytes.
+bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, int32_t heads, int32_t width, int box,
+                 bool swizzle = false) {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return false;
     const CUtensorMapDataType ty = dt == KDA_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -60,7 +62,10 @@ bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, i
     const cuuint64_t strides[2] = {cuuint64_t(width) * es, cuuint64_t(heads) * cuuint64_t(width) * es};
     const cuuint32_t boxes[3] = {cuuint32_t(box), 1, 64}, estr[3] = {1, 1, 1};
     return fn(map, ty, 3, const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              !swizzle             ? CU_TENSOR_MAP_SWIZZLE_NONE
+              : box * es == 64     ? CU_TENSOR_MAP_SWIZZLE_64B
+                                   : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -68,10 +73,10 @@ bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, i
 bool encode_delta(const DeltaParams &p, int32_t dt, int64_t rows, DeltaMaps &prep, DeltaMaps &scan) {
     std::memset(&prep, 0, sizeof(prep));
     std::memset(&scan, 0, sizeof(scan));
-    return encode_rows(&prep.q, p.q, dt, rows, p.Hk, p.K, 32) && encode_rows(&prep.k, p.k, dt, rows, p.Hk, p.K, 32) &&
+    return encode_rows(&prep.q, p.q, dt, rows, p.Hk, p.K, 32, true) && encode_rows(&prep.k, p.k, dt, rows, p.Hk, p.K, 32, true) &&
            encode_rows(&scan.v, p.v, dt, rows, p.H, p.V, p.V) && encode_rows(&scan.q, p.q, dt, rows, p.Hk, p.K, p.K) &&
            encode_rows(&scan.k, p.k, dt, rows, p.Hk, p.K, p.K) &&
-           (p.gate != KDA_GATE_CHANNEL || (encode_rows(&prep.g, p.g, KDA_F32, rows, p.H, p.K, 32) &&
+           (p.gate != KDA_GATE_CHANNEL || (encode_rows(&prep.g, p.g, KDA_F32, rows, p.H, p.K, 32, true) &&
                                            encode_rows(&scan.g, p.g, KDA_F32, rows, p.H, p.K, p.K)));
 }
 

@@ -16,17 +16,26 @@
 // whose decay over either half of the chunk exceeds PREP_SAFE nats is left out of
 // the product and its terms are added one by one, with running products of e^g.
 //
+// Shared memory is what bounds this: a version with both operands there moved 7000
+// 128-byte wavefronts for a chunk-head, a third of them the tensor core's reads of the
+// 128-row side.  So that side goes to tensor memory, written by threads that own its
+// rows, and the images leave by bulk copies from shared memory (stores of 16 bytes
+// a lane had taken 50 of 320 us at 16 x 512 tokens x 64 heads).
+//
 // One persistent CTA of seven warpgroups per SM; every role walks the same chunk-heads:
-//   * warp 0: MMA issue; warp 1: TMA loads of q, k and g in slices of 32 channels into a
-//     ring (plain loads stall here: what the CTA leaves of the L1 holds too little in
-//     flight);
-//   * warps 8-15 and 16-23 (transform): every second slice each into TF32 operands; lane = channel, warp = eight rows, so that the sums along the rows run in registers and
-//     one exchange of eight totals to a channel;
+//   * warp 0: MMA issue; warp 1: TMA loads of k, q and g in slices of 32 channels into a
+//     ring, swizzled so that both passes of the transform read them without conflicts;
+//   * warps 8-15 and 16-23 (transform): every second slice each.  First lane = channel, warp = eight
+//     rows: E, summed in registers with one exchange of eight totals to a channel, takes
+//     g's place.  Then lane = row: K e^E and Q e^E to tensor memory, K e^{-E} to shared;
 //   * warps 4, 5 (A) and 6, 7 (P): the accumulator's rows out of tensor memory; A
-//     with beta and the mask into the solve's tile, P straight into its image;
+//     with beta and the mask into the solve's tile, P into its image;
 //   * warps 24-27: two pairs, each the 64-token solve of every second chunk-head,
 //     and M's image.
-// The warpgroups' registers are moved to where the row of 64 values needs them.
+// Five kinds of code run at once on an SM whose instruction cache holds about 32 KB of
+// them: with everything unrolled (100 KB) half the cache's requests missed and
+// that, not any pipe, set the time (424 us under the profiler, 16 x 512 tokens x 64
+// heads).  So the loops here are kept rolled wherever registers allow it.
 #pragma once
 
 #include "kda_delta_rec.cuh"
@@ -50,38 +59,50 @@ constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX =
 constexpr int PREP_THREADS = 28 * 32;
 constexpr int PREP_TW = 8;                         // transform warps of a group
 constexpr float PREP_SAFE = 48.0f;
-constexpr int PREP_NOPS = 2;
-constexpr int PREP_OPS_BYTES = 48 * 1024;          // A hi, A lo (128 rows), B hi, B lo (64 rows), 128-byte rows
-// staging ring: a slice of 64 rows x 32 channels of k, q (at most 8 KiB each) and g
+constexpr int PREP_NOPS = 2;                       // slices' operands: 64 TMEM columns and, in shared memory,
+constexpr int PREP_OPS_BYTES = 16 * 1024;          // K e^{-E} hi and lo, 64 rows of 128 bytes each
+// staging ring: a slice of 64 rows x 32 channels of k, q and g
 template <typename T>
 constexpr int prep_stage_bytes() { return 2 * 64 * 32 * int(sizeof(T)) + 8192; }
 template <typename T>
 constexpr int prep_stages() { return sizeof(T) == 2 ? 3 : 2; }
 constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NOPS, PB_D_EMPTY = PB_D_FULL + 2,
               PB_AT_FULL = PB_D_EMPTY + 2, PB_AT_EMPTY = PB_AT_FULL + 2, PB_ST_FULL = PB_AT_EMPTY + 2,
-              PB_ST_EMPTY = PB_ST_FULL + 3, PREP_NBARS = PB_ST_EMPTY + 3;
+              PB_ST_EMPTY = PB_ST_FULL + 4, PREP_NBARS = PB_ST_EMPTY + 4;
 constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
 constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
-constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][16 warps] largest |k|, |q|
-constexpr int PREP_OFF_TOT = 1536;                 // [2 groups][2][8 warps][32 channels] sums of g
+constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][16 warps] largest |k| or |q|
+constexpr int PREP_OFF_TOT = 1024;                 // [2 groups][2][8 warps][32 channels] sums of g
 constexpr int PREP_OFF_SC = PREP_OFF_TOT + 4 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
 constexpr int PREP_OFF_BETA = PREP_OFF_SC + 2 * 64 * 8;        // [pairs][64]
 constexpr int PREP_OFF_CU = PREP_OFF_BETA + 2 * 64 * 4;
 constexpr int PREP_OFF_OPS = 8 * 1024;
-constexpr int PREP_OFF_AT = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
-constexpr int PREP_OFF_X = PREP_OFF_AT + 2 * 10 * 256 * 4;
+constexpr int PREP_OFF_ST = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
 constexpr int PREP_XP = 68;                        // pitch of the solved tile (floats)
-constexpr int PREP_OFF_XS = PREP_OFF_X + 2 * KGB_X_FLOATS * 4;
-constexpr int PREP_OFF_ST = PREP_OFF_XS + 2 * 64 * PREP_XP * 4;
+constexpr int PREP_X_FLOATS = 6 * XTS + 3 * XRS;   // transposed inverse blocks, negated diagonal ones
+// after the staging ring: the solve's tiles, its inverse tiles, the solved tiles, M's images, P's image
 template <typename T>
-constexpr int prep_bytes() { return PREP_OFF_ST + prep_stages<T>() * prep_stage_bytes<T>() + 1024; }
-static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 16 * 8 <= PREP_OFF_TOT, "header fits");
+constexpr int prep_off_at() { return PREP_OFF_ST + prep_stages<T>() * prep_stage_bytes<T>(); }
+template <typename T>
+constexpr int prep_off_x() { return prep_off_at<T>() + 2 * 10 * 256 * 4; }
+template <typename T>
+constexpr int prep_off_xs() { return prep_off_x<T>() + 2 * PREP_X_FLOATS * 4; }
+template <typename T>
+constexpr int prep_off_m() { return prep_off_xs<T>() + 2 * 64 * PREP_XP * 4; }
+template <typename T>
+constexpr int prep_off_p() { return prep_off_m<T>() + 2 * 16384; }
+template <typename T>
+constexpr int prep_bytes() { return prep_off_p<T>() + 16384 + 1024; }
+static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 16 * 4 <= PREP_OFF_TOT, "header fits");
 static_assert(PREP_OFF_CU + CU_CAP * 4 <= PREP_OFF_OPS, "cu_seqlens fits");
-static_assert(PREP_OFF_ST % 128 == 0 && prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
+static_assert(prep_stage_bytes<float>() % 1024 == 0 && prep_stage_bytes<__half>() % 1024 == 0 &&
+                  prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
               "fits the shared memory of one CTA");
+constexpr uint32_t PREP_TM_D = 0, PREP_TM_A = 128; // accumulators [2][64], operands [PREP_NOPS]{hi 32, lo 32}
 
 // Tensor maps of q, k [rows, Hk, K] and g [rows, H, K] as {channels, heads, rows}: boxes of 32
-// channels x 64 rows here, of all channels (and of v's values) in the scan.
+// channels x 64 rows here, swizzled over their row's bytes; of all channels (and of v's
+// values) in the scan.
 struct DeltaMaps {
     CUtensorMap q, k, g, v;
 };
@@ -124,22 +145,86 @@ __device__ __forceinline__ float max3(float m, float a, float b) {
     return r;
 }
 
+// Eight channels d .. d + 7 (a multiple of 8) of row r of a staged slice, as the tensor map's
+// swizzle over the row's bytes (64 or 128) left them.
+template <typename T>
+__device__ __forceinline__ void load_row(const unsigned char *tile, int r, int d, float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 t = *reinterpret_cast<const uint4 *>(tile + r * 64 + 16 * ((d >> 3) ^ ((r >> 1) & 3)));
+        Elt<T>::widen(t, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 t = *reinterpret_cast<const float4 *>(tile + r * 128 + 16 * (((d >> 2) + j) ^ (r & 7)));
+            x[4 * j] = t.x; x[4 * j + 1] = t.y; x[4 * j + 2] = t.z; x[4 * j + 3] = t.w;
+        }
+    }
+}
+
 __device__ __forceinline__ float warp_max(float v) {   // v >= 0
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// Row i of an image tile from 64 floats (already scaled): hi and, if `lo` is not null, lo.
-__device__ __forceinline__ void image_row(unsigned char *hi, unsigned char *lo, int i, const float (&x)[64], float s) {
+// Columns 8 c .. + 7 of row i of an image tile, times s: hi and, if `lo` is not null, lo.
+__device__ __forceinline__ void image_put(unsigned char *hi, unsigned char *lo, int i, int c, const float (&x)[8], float s) {
+    uint4 h, l;
+    split_f16(x[0] * s, x[1] * s, h.x, l.x);
+    split_f16(x[2] * s, x[3] * s, h.y, l.y);
+    split_f16(x[4] * s, x[5] * s, h.z, l.z);
+    split_f16(x[6] * s, x[7] * s, h.w, l.w);
+    const int at = i * 128 + 16 * (c ^ (i & 7));
+    *reinterpret_cast<uint4 *>(hi + at) = h;
+    if (lo != nullptr) *reinterpret_cast<uint4 *>(lo + at) = l;
+}
+
+// The 64-token solve of the A tile (blocks (i, j) at Ab + 256 blk(i, j)) by two warps: the row-major
+// inverse into xs (its blocks above the diagonal are not written).  Block by block along
+// the diagonals, X_rc = -X_rr sum_k A_rk X_kc, transposed and in split TF32 as in the chunk
+// solver; one loop body does every product, where the chunk solver unrolls its two levels.
+__device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs, int pt, int bar) {
+    const int warp = pt >> 5, lane = pt & 31, g = lane >> 2, t = lane & 3;
+    float *Xn = X + 6 * XTS;
+    {
+        const int b = pt >> 4, l = pt & 15;
+        float x[16];
+        diag_invert<true>(Ab + blk(b, b) * 256, 16, l, x);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint4 h, l;
-        split_f16(x[8 * c] * s, x[8 * c + 1] * s, h.x, l.x);
-        split_f16(x[8 * c + 2] * s, x[8 * c + 3] * s, h.y, l.y);
-        split_f16(x[8 * c + 4] * s, x[8 * c + 5] * s, h.z, l.z);
-        split_f16(x[8 * c + 6] * s, x[8 * c + 7] * s, h.w, l.w);
-        const int at = i * 128 + 16 * (c ^ (i & 7));
-        *reinterpret_cast<uint4 *>(hi + at) = h;
-        if (lo != nullptr) *reinterpret_cast<uint4 *>(lo + at) = l;
+        for (int i = 0; i < 16; ++i) xs[(16 * b + i) * PREP_XP + 16 * b + l] = x[i];
+        if (b != 3) {                                      // X_bb^T row-major (row = lane)
+            float4 *d = reinterpret_cast<float4 *>(X + blk(b, b) * XTS + l * XTP);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i ^ xt_swz(l)] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+        if (b != 0) {                                      // -X_bb row-major (column = lane)
+            float *d = Xn + (b - 1) * XRS + l;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d[i * XRP] = -x[i];
+        }
+    }
+    bar64(bar);
+#pragma unroll 1
+    for (int d = 1; d < 4; ++d) {
+#pragma unroll 1
+        for (int r = d + warp; r < 4; r += 2) {
+            const int c = r - d;
+            TileA la;
+            TileB rb;
+            TileC acc, out;
+            zero(acc);
+            zero(out);
+#pragma unroll 1
+            for (int k = c; k < r; ++k) {
+                left_smem<true>(la, X + blk(k, c) * XTS, XTP, g, t);
+                right4<false>(rb, Ab + blk(r, k) * 256, 16, g, t);
+                mma_tile<false>(acc, la, rb);
+            }
+            left_regs(la, acc);
+            right2(rb, Xn + (r - 1) * XRS, XRP, g, t);
+            mma_tile<false>(out, la, rb);
+            if (r < 3) smem_tile_t<true>(X + blk(r, c) * XTS, out, g, t);
+            out_tile_t(xs, PREP_XP, BT, r, c, out, g, t);
+        }
+        bar64(bar);
     }
 }
 
@@ -169,7 +254,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PREP_OFF_TMEM);
     uint32_t *steep_m = reinterpret_cast<uint32_t *>(sm + PREP_OFF_STEEP);
-    float2 *kq_m = reinterpret_cast<float2 *>(sm + PREP_OFF_KQ);
+    float *kq_m = reinterpret_cast<float *>(sm + PREP_OFF_KQ);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int NST = prep_stages<T>(), STB = prep_stage_bytes<T>(), ST_Q = 64 * 32 * int(sizeof(T)), ST_G = 2 * ST_Q;
     const int nsl = p.K / 32;
@@ -202,7 +287,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         ps.cu = cs;
     }
     if (warp == 4) {
-        tc::tmem_alloc(smem_u32(tmem_slot), 128);
+        tc::tmem_alloc(smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
     tc::fence_before_sync();
@@ -226,19 +311,18 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     prep_wait(ok, &bars[PB_OPS_FULL + ob], (u / PREP_NOPS) & 1, p.err);
                     __syncwarp();
                     tc::fence_after_sync();
-                    const uint32_t ah = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES);
-                    const uint32_t d = tmem + db * 64;
+                    const uint32_t bh = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES);
+                    const uint32_t d = tmem + PREP_TM_D + db * 64;
                     if (tc::elect_one()) {
-                        // K = 8 channels: 32 bytes along the rows
-                        uint64_t dah = tc::sw128_desc(ah), dal = tc::sw128_desc(ah + 16384),
-                                 dbh = tc::sw128_desc(ah + 32768), dbl = tc::sw128_desc(ah + 40960);
+                        // K = 8 channels: 8 columns of A, 32 bytes along B's rows
+                        uint32_t ta = tmem + PREP_TM_A + ob * 64;
+                        uint64_t dbh = tc::sw128_desc(bh), dbl = tc::sw128_desc(bh + 8192);
 #pragma unroll 1
                         for (int kk = 0; kk < 4; ++kk) {
-                            tc::mma_tf32(d, dah, dbh, KGB_IDESC, s > 0 || kk > 0);
-                            tc::mma_tf32(d, dah, dbl, KGB_IDESC, true);
-                            tc::mma_tf32(d, dal, dbh, KGB_IDESC, true);
-                            dah += 2;
-                            dal += 2;
+                            tc::mma_tf32_ts(d, ta, dbh, KGB_IDESC, s > 0 || kk > 0);
+                            tc::mma_tf32_ts(d, ta, dbl, KGB_IDESC, true);
+                            tc::mma_tf32_ts(d, ta + 32, dbh, KGB_IDESC, true);
+                            ta += 8;
                             dbh += 2;
                             dbl += 2;
                         }
@@ -278,53 +362,48 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         tc::fewer_registers<64>();
         // -------------------------------------------------------------- transform
         constexpr float L2E = 1.4426950408889634f;
-        const int tw = warp & 7, tg = (warp >> 3) - 1;     // rows 8 tw .. + 7 of slices tg, tg + 2
+        const int tw = warp & 7, tg = (warp >> 3) - 1;     // slices tg, tg + 2
+        // second pass: this thread's row of K (quarters 0, 1) or Q (2, 3), sixteen channels of it
+        const int quarter = warp & 3, row = 32 * (quarter & 1) + lane, half = tw >> 2;
+        const bool isQ = quarter >= 2;
+        const uint32_t ta = tmem + PREP_TM_A + (uint32_t(32 * quarter) << 16) + 16 * half;
         float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT) + tg * 512;
+        auto group_sync = [&] {
+            if (tg == 0) named_sync<1, 256>();
+            else named_sync<6, 256>();
+        };
         TaskWalk walk(ps, blockIdx.x, G);
         Meta m = walk.next(ps);
         uint32_t turn = 0;
         for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps)) {
-            float kmax = 0.f, qmax = 0.f;
+            float big = 0.f;                               // largest |k| or |q| seen
             for (int s = tg; s < nsl; s += 2, ++turn) {
                 const uint32_t u = c * nsl + s;
                 const int ob = u % PREP_NOPS, st = u % NST;
                 unsigned char *stage = sm + PREP_OFF_ST + st * STB;
-                T *kt = reinterpret_cast<T *>(stage) + tw * 256 + lane;
-                T *qt = reinterpret_cast<T *>(stage + ST_Q) + tw * 256 + lane;
-                float *gt = reinterpret_cast<float *>(stage + ST_G) + tw * 256 + lane;
                 prep_wait(ok, &bars[PB_ST_FULL + st], (u / NST) & 1, p.err);
+                // ---- E in g's place: rows 8 tw .. + 7 of channel `lane`; the 16-byte chunk j of row r lies at j ^ (r & 7)
+                float *ge = reinterpret_cast<float *>(stage + ST_G + tw * 1024 + 4 * (lane & 3));
+                float gv[8], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gv[i] = ge[32 * i + 4 * ((lane >> 2) ^ i)];
                 if (p.gate != 0) {                         // one decay to a row, from global memory
                     const float *gp = p.g + (int64_t(m.row0) + 8 * tw) * p.H + m.h;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) gt[32 * i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
+                    for (int i = 0; i < 8; ++i) gv[i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
                 }
-                for (int i = m.n > 8 * tw ? m.n - 8 * tw : 0; i < 8; ++i) {    // rows past the end hold the next request's
-                    kt[32 * i] = T(0.f);
-                    qt[32 * i] = T(0.f);
-                    gt[32 * i] = 0.f;
-                }
-                float kv[8], qv[8], gv[8], sum = 0.f;
+                if (m.n < 8 * tw + 8) {                    // rows past the end hold the next request's
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    kv[i] = widen1(kt[32 * i]);
-                    qv[i] = widen1(qt[32 * i]);
-                    gv[i] = gt[32 * i];
+                    for (int i = 0; i < 8; ++i) gv[i] = 8 * tw + i < m.n ? gv[i] : 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     gv[i] *= L2E;
                     sum += gv[i];
-                    if (i & 1) {
-                        kmax = max3(kmax, kv[i - 1], kv[i]);
-                        qmax = max3(qmax, qv[i - 1], qv[i]);
-                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[PB_ST_EMPTY + st]);
                 float *tb = tot + (turn & 1) * 256;
                 tb[tw * 32 + lane] = sum;
-                if (tg == 0) named_sync<1, 256>();
-                else named_sync<6, 256>();
+                group_sync();
                 // decay from the middle of the chunk (between rows 31 and 32) outward
                 float lo = 0.f, hi = 0.f, off = 0.f;
 #pragma unroll
@@ -335,56 +414,79 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     if (tw < 4 ? (w > tw && w < 4) : (w >= 4 && w < tw)) off += t;
                 }
                 const bool keep = lo >= -PREP_SAFE * L2E && hi >= -PREP_SAFE * L2E;     // false for NaN too
-                float E[8];
+                const uint32_t steep = __ballot_sync(0xffffffffu, !keep);
                 if (tw < 4) {
 #pragma unroll
                     for (int i = 7; i >= 0; --i) {
-                        E[i] = -off;
+                        ge[32 * i + 4 * ((lane >> 2) ^ i)] = -off;
                         off += gv[i];
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         off += gv[i];
-                        E[i] = off;
-                    }
-                }
-                const uint32_t steep = __ballot_sync(0xffffffffu, !keep);
-                if (steep != 0u && !keep) {                // a steep channel enters the product as zeros
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) kv[i] = qv[i] = E[i] = 0.f;
-                }
-                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
-                unsigned char *ops = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES + tw * 1024 + 4 * (lane & 3);
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {           // two rows at a time, in paired instructions
-                    const float2 k2 = make_float2(kv[i], kv[i + 1]);
-                    const float2 up = make_float2(ex2(E[i]), ex2(E[i + 1])), dn = make_float2(ex2(-E[i]), ex2(-E[i + 1]));
-                    uint32_t h[3][2], l[3][2];
-                    split2(__fmul2_rn(k2, up), h[0][0], h[0][1], l[0][0], l[0][1]);
-                    split2(__fmul2_rn(make_float2(qv[i], qv[i + 1]), up), h[1][0], h[1][1], l[1][0], l[1][1]);
-                    split2(__fmul2_rn(k2, dn), h[2][0], h[2][1], l[2][0], l[2][1]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // row 8 tw + i + e of the tile, its 16-byte chunk lane / 4 at position (lane / 4) ^ (i + e)
-                        unsigned char *at = ops + (i + e) * 128 + 16 * ((lane >> 2) ^ (i + e));
-                        *reinterpret_cast<uint32_t *>(at) = h[0][e];
-                        *reinterpret_cast<uint32_t *>(at + 8192) = h[1][e];
-                        *reinterpret_cast<uint32_t *>(at + 16384) = l[0][e];
-                        *reinterpret_cast<uint32_t *>(at + 24576) = l[1][e];
-                        *reinterpret_cast<uint32_t *>(at + 32768) = h[2][e];
-                        *reinterpret_cast<uint32_t *>(at + 40960) = l[2][e];
+                        ge[32 * i + 4 * ((lane >> 2) ^ i)] = off;
                     }
                 }
                 if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
-                if (s + 2 >= nsl) {
-                    kmax = warp_max(kmax);
-                    qmax = warp_max(qmax);
-                    if (lane == 0) kq_m[(c & 7) * 16 + 8 * tg + tw] = make_float2(kmax, qmax);
+                group_sync();
+                // ---- operands: this thread's row
+                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
+                tc::fence_after_sync();
+                const unsigned char *er = stage + ST_G + row * 128, *xr = stage + (isQ ? ST_Q : 0);
+                unsigned char *br = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES + row * 128;
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b) {              // eight channels, chunks 4 half + 2 b and the next
+                    float x[8], E[8];
+                    load_row<T>(xr, row, 16 * half + 8 * b, x);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 t = *reinterpret_cast<const float4 *>(er + 16 * ((4 * half + 2 * b + j) ^ (row & 7)));
+                        E[4 * j] = t.x; E[4 * j + 1] = t.y; E[4 * j + 2] = t.z; E[4 * j + 3] = t.w;
+                    }
+                    if (m.n < 64) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = row < m.n ? x[i] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) big = max3(big, x[i], x[i + 1]);
+                    if (steep != 0u) {                     // a steep channel enters the product as zeros
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if ((steep >> (16 * half + 8 * b + i)) & 1u) x[i] = E[i] = 0.f;
+                    }
+                    uint32_t h[8], l[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2)
+                        split2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(E[i]), ex2(E[i + 1]))), h[i], h[i + 1],
+                               l[i], l[i + 1]);
+                    tc::st8(ta + ob * 64 + 8 * b, h);
+                    tc::st8(ta + ob * 64 + 32 + 8 * b, l);
+                    if (!isQ) {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            split2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(-E[i]), ex2(-E[i + 1]))), h[i],
+                                   h[i + 1], l[i], l[i + 1]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            unsigned char *at = br + 16 * ((4 * half + 2 * b + j) ^ (row & 7));
+                            *reinterpret_cast<uint4 *>(at) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                            *reinterpret_cast<uint4 *>(at + 8192) = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+                        }
+                    }
                 }
+                if (s + 2 >= nsl) {
+                    big = warp_max(big);
+                    if (lane == 0) kq_m[(c & 7) * 16 + 8 * tg + tw] = big;
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[PB_OPS_FULL + ob]);
+                if (lane == 0) {
+                    mbar_arrive(&bars[PB_OPS_FULL + ob]);
+                    mbar_arrive(&bars[PB_ST_EMPTY + st]);
+                }
             }
         }
     } else if (warp < 8) {
@@ -398,7 +500,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         Meta m = walk.next(ps, &qi);
         for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps, &qi)) {
             const int db = c & 1;
-            float *Ab = reinterpret_cast<float *>(sm + PREP_OFF_AT) + db * 2560;
+            float *Ab = reinterpret_cast<float *>(sm + prep_off_at<T>()) + db * 2560;
             float f = p.scale;
             if (!isP)
                 f = i < m.n ? widen1(static_cast<const T *>(p.beta)[(int64_t(m.row0) + i) * p.H + m.h]) : 0.f;
@@ -406,87 +508,128 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             prep_wait(ok, &bars[PB_D_FULL + db], (c >> 1) & 1, p.err);
             __syncwarp();
             tc::fence_after_sync();
-            const uint32_t td = tmem + db * 64 + (uint32_t(32 * (warp - 4)) << 16);
-            float x[64];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float v[16];
-                tc::ld16(td + 16 * b, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[16 * b + e] = v[e];
-            }
-            tc::wait_ld();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[PB_D_EMPTY + db]);
+            const uint32_t td = tmem + PREP_TM_D + db * 64 + (uint32_t(32 * (warp - 4)) << 16);
             const int last = isP ? i : i - 1;              // largest column of this row
-            // select: rows past the end and masked columns may hold anything
-#pragma unroll
-            for (int j = 0; j < 64; ++j) x[j] = j <= last && i < m.n ? x[j] : 0.f;
+            const int nb = 2 * (warp & 1) + 2;             // blocks of 16 columns with any of this warp's rows
             const uint32_t sb = (c & 7) * 4;
             uint32_t any = 0u;
             for (int s = 0; s < nsl; ++s) any |= steep_m[sb + s];
             if (any != 0u) {
-                // steep channels: k_j q_i (or k_i) prod_{j < t <= i} e^{g_t}, from the diagonal left
+                // steep channels: k_j q_i (or k_i) prod_{j < t <= i} e^{g_t}, from the diagonal left, added to
+                // the accumulator
                 const int64_t row = int64_t(m.row0) + i;
                 const int64_t kb = (row * p.Hk + m.h / group) * p.K;
-                for (int s = 0; s < nsl; ++s) {
-                    uint32_t mask = steep_m[sb + s];
-                    while (mask != 0u) {
-                        const int d = 32 * s + __ffs(mask) - 1;
-                        mask &= mask - 1u;
-                        if (isP) named_sync<2, 64>();
-                        else named_sync<3, 64>();
-                        const bool live = i < m.n;
-                        const float kd = live ? widen1(static_cast<const T *>(p.k)[kb + d]) : 0.f;
-                        const float own = isP ? (live ? widen1(static_cast<const T *>(p.q)[kb + d]) : 0.f) : kd;
-                        const float gd = live ? p.g[p.gate == 0 ? (row * p.H + m.h) * p.K + d : row * p.H + m.h] : 0.f;
-                        sc[i] = make_float2(expf(gd), kd);
-                        if (isP) named_sync<2, 64>();
-                        else named_sync<3, 64>();
-                        if (live) {
+                const bool live = i < m.n;
+                auto sync = [&] {
+                    if (isP) named_sync<2, 64>();
+                    else named_sync<3, 64>();
+                };
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float x[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+#pragma unroll 1
+                    for (int s = 0; s < nsl; ++s) {
+                        uint32_t mask = steep_m[sb + s];
+                        while (mask != 0u) {
+                            const int d = 32 * s + __ffs(mask) - 1;
+                            mask &= mask - 1u;
+                            sync();                        // the previous channel is consumed
+                            const float kd = live ? widen1(static_cast<const T *>(p.k)[kb + d]) : 0.f;
+                            const float own = isP ? (live ? widen1(static_cast<const T *>(p.q)[kb + d]) : 0.f) : kd;
+                            const float gd = live ? p.g[p.gate == 0 ? (row * p.H + m.h) * p.K + d : row * p.H + m.h] : 0.f;
+                            sc[i] = make_float2(expf(gd), kd);
+                            sync();
                             float run = own;
                             if (!isP) run *= sc[i].x;      // A starts one token before the row's own
+                            for (int j = last; j >= 16 * b + 16; --j) run *= sc[j].x;
 #pragma unroll
-                            for (int j = 63; j >= 0; --j) {
-                                const float2 t = sc[j];
-                                if (j <= last) {
-                                    x[j] = fmaf(run, t.y, x[j]);
+                            for (int e = 15; e >= 0; --e) {
+                                const float2 t = sc[16 * b + e];
+                                if (16 * b + e <= last) {
+                                    x[e] = fmaf(run, t.y, x[e]);
                                     run *= t.x;
                                 }
                             }
                         }
                     }
-                }
-                if (isP) named_sync<2, 64>();
-                else named_sync<3, 64>();
-            }
+                    if (b < nb) {
+                        float v[16];
+                        uint32_t w[2][8];
+                        tc::ld16(td + 16 * b, v);
+                        tc::wait_ld();
 #pragma unroll
-            for (int j = 0; j < 64; ++j) x[j] *= f;
-            if (!isP) {
-#pragma unroll
-                for (int j0 = 0; j0 < 4; ++j0)
-                    if (16 * j0 <= i) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4 *>(at_elem(Ab, i, 16 * j0 + e)) =
-                                make_float4(x[16 * j0 + e], x[16 * j0 + e + 1], x[16 * j0 + e + 2], x[16 * j0 + e + 3]);
+                        for (int e = 0; e < 16; ++e) w[e >> 3][e & 7] = __float_as_uint(v[e] + x[e]);
+                        tc::st8(td + 16 * b, w[0]);
+                        tc::st8(td + 16 * b + 8, w[1]);
+                        tc::wait_st();
                     }
+                }
+            }
+            // columns 8 b .. of this row, masked by selects: what they drop may hold anything
+            auto columns = [&](int b, float (&x)[8]) {
+                tc::ld8(td + 8 * b, x);
+                tc::wait_ld();
+                const int end = i < m.n ? last - 8 * b : -1;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = e <= end ? x[e] * f : 0.f;
+            };
+            auto done = [&] {                              // the accumulator is read
+                tc::fence_before_sync();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[PB_D_EMPTY + db]);
+            };
+            if (!isP) {
+#pragma unroll 1
+                for (int b = 0; b < 2 * nb; ++b) {
+                    float x[8];
+                    columns(b, x);
+                    if (16 * (b >> 1) <= i) {
+                        float4 *to = reinterpret_cast<float4 *>(at_elem(Ab, i, 8 * b));
+                        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+                        to[1] = make_float4(x[4], x[5], x[6], x[7]);
+                    }
+                }
+                done();
                 if (lane == 0) mbar_arrive(&bars[PB_AT_FULL + db]);
             } else {
-                float mx = 0.f;
+                float mx = 0.f, inv;
+#pragma unroll 1
+                for (int b = 0; b < 2 * nb; ++b) {
+                    float x[8];
+                    columns(b, x);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) mx = fmaxf(mx, fabsf(x[j]));
-                float inv;
+                    for (int e = 0; e < 8; e += 2) mx = max3(mx, x[e], x[e + 1]);
+                }
                 const float s = pow2_scale(warp_max(mx), KQ_LO, KQ_HI, inv);
-                unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>();
-                image_row(img + IMG_PHI, PLO ? img + IMG_PLO : nullptr, i, x, s);
+                unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>(), *pi = sm + prep_off_p<T>();
+                if (warp == 6 && lane == 0) tc::bulk_wait_read();      // the previous image has left
+                named_sync<2, 64>();
+#pragma unroll 1
+                for (int b = 0; b < 8; ++b) {
+                    float x[8];
+                    if (b < 2 * nb) {
+                        columns(b, x);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                    }
+                    image_put(pi, PLO ? pi + 8192 : nullptr, i, b, x, s);
+                }
+                done();
+                fence_proxy_async();
+                named_sync<2, 64>();
                 float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
                 if (lane == 0) hdr[HDR_PINV + (warp & 1)] = inv;
-                if (warp == 6) {                           // 8 transform warps to a group, the second idle at K = 32
-                    const float2 t = lane < 8 * (nsl > 1 ? 2 : 1) ? kq_m[(c & 7) * 16 + lane] : make_float2(0.f, 0.f);
-                    const float km = warp_max(t.x), qm = warp_max(t.y);
+                if (warp == 6) {
+                    if (lane == 0) {
+                        tc::bulk_store(img + IMG_PHI, smem_u32(pi), PLO ? 16384 : 8192);
+                        tc::bulk_commit();
+                    }
+                    // warps 0, 1, 4, 5 of a group of eight saw k, the others q; the second group is idle at K = 32
+                    const float t = lane < 8 * (nsl > 1 ? 2 : 1) ? kq_m[(c & 7) * 16 + lane] : 0.f;
+                    const float km = warp_max((lane & 3) < 2 ? t : 0.f), qm = warp_max((lane & 3) < 2 ? 0.f : t);
                     if (lane == 0) {
                         hdr[HDR_KMAX] = km;
                         hdr[HDR_QMAX] = qm;
@@ -494,58 +637,85 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                 }
             }
         }
+        if (warp == 6 && lane == 0) tc::bulk_wait();
     } else {
         tc::more_registers<112>();
         // ------------------------------------------------------------ solve pairs
         const int pr = (warp - 24) >> 1, pt = tid - 24 * 32 - 64 * pr, bar = 4 + pr;
-        float *Ab = reinterpret_cast<float *>(sm + PREP_OFF_AT) + pr * 2560;
-        float *X = reinterpret_cast<float *>(sm + PREP_OFF_X) + pr * KGB_X_FLOATS;
-        float *xs = reinterpret_cast<float *>(sm + PREP_OFF_XS) + pr * 64 * PREP_XP;
+        float *Ab = reinterpret_cast<float *>(sm + prep_off_at<T>()) + pr * 2560;
+        float *X = reinterpret_cast<float *>(sm + prep_off_x<T>()) + pr * PREP_X_FLOATS;
+        float *xs = reinterpret_cast<float *>(sm + prep_off_xs<T>()) + pr * 64 * PREP_XP;
         float *sbeta = reinterpret_cast<float *>(sm + PREP_OFF_BETA) + pr * 64;
+        unsigned char *mi = sm + prep_off_m<T>() + pr * 16384;
         TaskWalk walk(ps, int32_t(blockIdx.x) + pr * G, 2 * G);
         int32_t qi;
         Meta m = walk.next(ps, &qi);
         for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps, &qi)) {
             const float b = pt < m.n ? widen1(static_cast<const T *>(p.beta)[(int64_t(m.row0) + pt) * p.H + m.h]) : 0.f;
             prep_wait(ok, &bars[PB_AT_FULL + pr], c & 1, p.err);
-            bar64(bar);                                    // the previous tile and betas are consumed
+            if (pt == 0) tc::bulk_wait_read();             // the previous image has left
+            bar64(bar);                                    // and the betas are consumed
             sbeta[pt] = b;
-            kgb_solve<float>(Ab, X, X + 4 * XTS, xs, PREP_XP, m.n, pt, bar);
-            bar64(bar);
+            prep_solve(Ab, X, xs, pt, bar);
             if ((pt & 31) == 0) mbar_arrive(&bars[PB_AT_EMPTY + pr]);
-            float x[64], mx = 0.f, sum = 0.f;
+            // columns 8 j .. of row pt of M; zeros past the chunk's end and past the row's block
+            auto columns = [&](int j, float (&x)[8]) {
+                const bool in = pt < m.n && 8 * j <= pt;
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(xs + pt * PREP_XP + j);
-                const float4 bt = *reinterpret_cast<const float4 *>(sbeta + j);
-                const bool live = pt < m.n;
-                x[j] = live ? t.x * bt.x : 0.f;
-                x[j + 1] = live ? t.y * bt.y : 0.f;
-                x[j + 2] = live ? t.z * bt.z : 0.f;
-                x[j + 3] = live ? t.w * bt.w : 0.f;
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(xs + pt * PREP_XP + 8 * j + e);
+                    const float4 bt = *reinterpret_cast<const float4 *>(sbeta + 8 * j + e);
+                    x[e] = in ? t.x * bt.x : 0.f;
+                    x[e + 1] = in ? t.y * bt.y : 0.f;
+                    x[e + 2] = in ? t.z * bt.z : 0.f;
+                    x[e + 3] = in ? t.w * bt.w : 0.f;
+                }
+            };
+            const int nj = 4 * (pt >> 5) + 4;              // blocks of 8 columns with any of this warp's rows
+            float mx = 0.f, sum = 0.f, inv;
+#pragma unroll 1
+            for (int j = 0; j < nj; ++j) {
+                float x[8];
+                columns(j, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mx = fmaxf(mx, fabsf(x[j + e]));
-                    sum += fabsf(x[j + e]);
+                for (int e = 0; e < 8; e += 2) {
+                    mx = max3(mx, x[e], x[e + 1]);
+                    sum += fabsf(x[e]) + fabsf(x[e + 1]);
                 }
             }
-            float inv;
             const float s = pow2_scale(warp_max(mx), KQ_LO, KQ_HI, inv);
             sum = warp_max(sum);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                float x[8];
+                if (j < nj) {
+                    columns(j, x);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                }
+                image_put(mi, mi + 8192, pt, j, x, s);
+            }
+            fence_proxy_async();
+            bar64(bar);
             unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>();
-            image_row(img + IMG_MHI, img + IMG_MLO, pt, x, s);
             if ((pt & 31) == 0) {
                 float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
                 hdr[HDR_MINV + (pt >> 5)] = inv;
                 hdr[HDR_MSUM + (pt >> 5)] = sum;
             }
+            if (pt == 0) {
+                tc::bulk_store(img + IMG_MHI, smem_u32(mi), 16384);
+                tc::bulk_commit();
+            }
         }
+        if (pt == 0) tc::bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 4) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 128);
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
