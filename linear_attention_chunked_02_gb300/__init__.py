@@ -17,28 +17,16 @@ from typing import Optional
 
 import torch
 
-from ._lib import lib, LIB_PATH  # noqa: F401
+from ._lib import DTYPE_CODE, KdaError, LIB_PATH, check as _check, lib  # noqa: F401
 from .layer import (add_norm, delta_prefill, delta_prefill_workspace_size, delta_step,  # noqa: F401
                     gated_norm)
 
 BT = 64
 CHUNK_LENGTHS = (16, 32, 64)
 WS_TILE_BYTES = 4096
-DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 PATH_CODE = {"auto": 0, "split": 1, "single": 2}
 PATH_NAME = {v: k for k, v in PATH_CODE.items()}
 PRECISION_CODE = {"ieee": 0, "tf32": 1}
-
-
-class KdaError(RuntimeError):
-    def __init__(self, status: int, where: str):
-        self.status = status
-        super().__init__(f"{where}: {lib().kda_status_string(status).decode()} (status {status})")
-
-
-def _check(status: int, where: str) -> None:
-    if status != 0:
-        raise KdaError(status, where)
 
 
 def _shape(A: torch.Tensor, cu_seqlens: Optional[torch.Tensor], lengths=(BT,)):

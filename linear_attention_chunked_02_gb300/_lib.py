@@ -9,6 +9,10 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
+DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkda_solve_tril.so")
 
@@ -66,3 +70,14 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _LIB = handle
     return _LIB
+
+
+class KdaError(RuntimeError):
+    def __init__(self, status: int, where: str):
+        self.status = status
+        super().__init__(f"{where}: {lib().kda_status_string(status).decode()} (status {status})")
+
+
+def check(status: int, where: str) -> None:
+    if status != 0:
+        raise KdaError(status, where)

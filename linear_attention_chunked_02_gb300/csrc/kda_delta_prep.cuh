@@ -59,30 +59,33 @@ constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX =
 constexpr int PREP_THREADS = 28 * 32;
 constexpr int PREP_TW = 8;                         // transform warps of a group
 constexpr float PREP_SAFE = 48.0f;
-constexpr int PREP_NOPS = 2;                       // slices' operands: 64 TMEM columns and, in shared memory,
+// The slices of a chunk go to the two transform groups in turn.  Each group has buffers of
+// its own, so that all who wait on a buffer's barrier take part in every one of its phases
+// (a group that skipped two phases would take the barrier's parity for its turn).
+constexpr int PREP_NOPS = 2;                       // slices' operands, a group's: 64 TMEM columns and, in shared memory,
 constexpr int PREP_OPS_BYTES = 16 * 1024;          // K e^{-E} hi and lo, 64 rows of 128 bytes each
 // staging ring: a slice of 64 rows x 32 channels of k, q and g
 template <typename T>
 constexpr int prep_stage_bytes() { return 2 * 64 * 32 * int(sizeof(T)) + 8192; }
 template <typename T>
-constexpr int prep_stages() { return sizeof(T) == 2 ? 3 : 2; }
+constexpr int prep_stages() { return sizeof(T) == 2 ? 2 : 1; }     // of a group
 constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NOPS, PB_D_EMPTY = PB_D_FULL + 2,
               PB_AT_FULL = PB_D_EMPTY + 2, PB_AT_EMPTY = PB_AT_FULL + 2, PB_ST_FULL = PB_AT_EMPTY + 2,
               PB_ST_EMPTY = PB_ST_FULL + 4, PREP_NBARS = PB_ST_EMPTY + 4;
 constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
 constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
 constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][16 warps] largest |k| or |q|
-constexpr int PREP_OFF_TOT = 1024;                 // [2 groups][2][8 warps][32 channels] sums of g
-constexpr int PREP_OFF_SC = PREP_OFF_TOT + 4 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
+constexpr int PREP_OFF_TOT = 1024;                 // [2 groups][8 warps][32 channels] sums of g
+constexpr int PREP_OFF_SC = PREP_OFF_TOT + 2 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
 constexpr int PREP_OFF_BETA = PREP_OFF_SC + 2 * 64 * 8;        // [pairs][64]
 constexpr int PREP_OFF_CU = PREP_OFF_BETA + 2 * 64 * 4;
-constexpr int PREP_OFF_OPS = 8 * 1024;
+constexpr int PREP_OFF_OPS = 6 * 1024;
 constexpr int PREP_OFF_ST = PREP_OFF_OPS + PREP_NOPS * PREP_OPS_BYTES;
 constexpr int PREP_XP = 68;                        // pitch of the solved tile (floats)
 constexpr int PREP_X_FLOATS = 6 * XTS + 3 * XRS;   // transposed inverse blocks, negated diagonal ones
 // after the staging ring: the solve's tiles, its inverse tiles, the solved tiles, M's images, P's image
 template <typename T>
-constexpr int prep_off_at() { return PREP_OFF_ST + prep_stages<T>() * prep_stage_bytes<T>(); }
+constexpr int prep_off_at() { return PREP_OFF_ST + 2 * prep_stages<T>() * prep_stage_bytes<T>(); }
 template <typename T>
 constexpr int prep_off_x() { return prep_off_at<T>() + 2 * 10 * 256 * 4; }
 template <typename T>
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
     pdl_launch_dependents();
 
     if (tid == 0) {
-        for (int b = 0; b < NST; ++b) {
+        for (int b = 0; b < 2 * NST; ++b) {
             mbar_init(&bars[PB_ST_FULL + b], 1);
             mbar_init(&bars[PB_ST_EMPTY + b], PREP_TW);
         }
@@ -302,13 +305,13 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         if (warp == 0) {
             // ------------------------------------------------------------- MMA issue
             TaskWalk w(ps, blockIdx.x, G);
-            uint32_t u = 0;
+            uint32_t turn[2] = {0u, 0u};                   // slices of each group so far
             for (uint32_t c = 0; w.next(ps).valid; ++c) {
                 const int db = c & 1;
                 prep_wait(ok, &bars[PB_D_EMPTY + db], ((c >> 1) & 1) ^ 1, p.err);
-                for (int s = 0; s < nsl; ++s, ++u) {
-                    const int ob = u % PREP_NOPS;
-                    prep_wait(ok, &bars[PB_OPS_FULL + ob], (u / PREP_NOPS) & 1, p.err);
+                for (int s = 0; s < nsl; ++s) {
+                    const int ob = s & 1;
+                    prep_wait(ok, &bars[PB_OPS_FULL + ob], (ob ? turn[1]++ : turn[0]++) & 1, p.err);
                     __syncwarp();
                     tc::fence_after_sync();
                     const uint32_t bh = smem_u32(sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES);
@@ -338,10 +341,11 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         } else if (warp == 1) {
             // ----------------------------------------------------------------- loads
             TaskWalk w(ps, blockIdx.x, G);
-            uint32_t u = 0;
+            uint32_t turn[2] = {0u, 0u};
             for (Meta m = w.next(ps); m.valid; m = w.next(ps))
-                for (int s = 0; s < nsl; ++s, ++u) {
-                    const int st = u % NST;
+                for (int s = 0; s < nsl; ++s) {
+                    const uint32_t u = s & 1 ? turn[1]++ : turn[0]++;
+                    const int st = (s & 1) * NST + u % NST;
                     prep_wait(ok, &bars[PB_ST_EMPTY + st], ((u / NST) & 1) ^ 1, p.err);
                     __syncwarp();
                     if (tc::elect_one()) {
@@ -355,8 +359,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     __syncwarp();
                 }
             // no copy may be in flight when the CTA ends
-            for (uint32_t i = u > NST ? u - NST : 0; i < u; ++i)
-                prep_wait(ok, &bars[PB_ST_FULL + i % NST], (i / NST) & 1, p.err);
+            for (int tg = 0; tg < 2; ++tg)
+                for (uint32_t i = turn[tg] > NST ? turn[tg] - NST : 0; i < turn[tg]; ++i)
+                    prep_wait(ok, &bars[PB_ST_FULL + tg * NST + i % NST], (i / NST) & 1, p.err);
         }
     } else if (warp >= 8 && warp < 24) {
         tc::fewer_registers<64>();
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         const int quarter = warp & 3, row = 32 * (quarter & 1) + lane, half = tw >> 2;
         const bool isQ = quarter >= 2;
         const uint32_t ta = tmem + PREP_TM_A + (uint32_t(32 * quarter) << 16) + 16 * half;
-        float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT) + tg * 512;
+        float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT) + tg * 256;
         auto group_sync = [&] {
             if (tg == 0) named_sync<1, 256>();
             else named_sync<6, 256>();
@@ -378,10 +383,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps)) {
             float big = 0.f;                               // largest |k| or |q| seen
             for (int s = tg; s < nsl; s += 2, ++turn) {
-                const uint32_t u = c * nsl + s;
-                const int ob = u % PREP_NOPS, st = u % NST;
+                const int ob = tg, st = tg * NST + turn % NST;
                 unsigned char *stage = sm + PREP_OFF_ST + st * STB;
-                prep_wait(ok, &bars[PB_ST_FULL + st], (u / NST) & 1, p.err);
+                prep_wait(ok, &bars[PB_ST_FULL + st], (turn / NST) & 1, p.err);
                 // ---- E in g's place: rows 8 tw .. + 7 of channel `lane`; the 16-byte chunk j of row r lies at j ^ (r & 7)
                 float *ge = reinterpret_cast<float *>(stage + ST_G + tw * 1024 + 4 * (lane & 3));
                 float gv[8], sum = 0.f;
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     gv[i] *= L2E;
                     sum += gv[i];
                 }
-                float *tb = tot + (turn & 1) * 256;
+                float *tb = tot;                           // free since the second synchronisation of the last slice
                 tb[tw * 32 + lane] = sum;
                 group_sync();
                 // decay from the middle of the chunk (between rows 31 and 32) outward
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                 if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
                 group_sync();
                 // ---- operands: this thread's row
-                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], ((u / PREP_NOPS) & 1) ^ 1, p.err);
+                prep_wait(ok, &bars[PB_OPS_EMPTY + ob], (turn & 1) ^ 1, p.err);
                 tc::fence_after_sync();
                 const unsigned char *er = stage + ST_G + row * 128, *xr = stage + (isQ ? ST_Q : 0);
                 unsigned char *br = sm + PREP_OFF_OPS + ob * PREP_OPS_BYTES + row * 128;

@@ -50,9 +50,9 @@ constexpr int SCAN_PARTS = 4;                      // chain threads to a lane
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
               SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_IMG_READ = 20,
-              SCAN_NBARS = 22;
+              SB_GAM = 22, SCAN_NBARS = 24;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
-constexpr int SCAN_OFF_RED = 192;                  // a word to a warp: chunks before the sequence
+constexpr int SCAN_OFF_RED = 256;                  // a word to a warp: chunks before the sequence
 constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [4 parts][128 lanes] largest |S|
 constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 4 * 128 * 4;      // [4 parts][128 lanes] largest |v|
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {16, 8, 1, 1, 4, 1, 1, 1, 1, 16, 1, 8, 1, 16, 1, 1, 1, 16, 1, 8, 4, 4};
+        const int count[SCAN_NBARS] = {16, 8, 1, 1, 4, 1, 1, 1, 1, 16, 1, 8, 1, 16, 1, 1, 1, 16, 1, 8, 4, 4, 1, 1};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             float sS = pow2_scale(bS + 64.f * kmax * bU, VS_LO, VS_HI, invS1);
             bool weak = __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
             if (weak) {                                    // the same in the four warps of the quarter
-                prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
+                prep_wait(ok, &bars[SB_GAM + ph], (c >> 1) & 1, p.err);
                 float gmax = 0.f;
                 for (int i = 0; i < K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
                 weak = __all_sync(0xffffffffu, gmax < SCAN_WEAK_G);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             release(SB_U);
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
-            prep_wait(ok, &bars[SB_KH_FULL], ph, p.err);
+            prep_wait(ok, &bars[SB_GAM + ph], (c >> 1) & 1, p.err);
             accumulator(SB_D3, ph);
             float mx = 0.f;
             if (weak) {                                    // S is there
@@ -543,7 +543,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_KQ_FULL]);
+            if (lane == 0) {
+                mbar_arrive(&bars[SB_KQ_FULL]);
+                // e^{G_C} for the chain, on barriers for even and odd chunks: the next chunk's may come
+                // before a slow warp of the chain has seen this one's, but not the one's after
+                if (rg == 7) mbar_arrive(&bars[SB_GAM + ph]);
+            }
             // K e^{G_C-G} transposed: channel d's row holds the 64 tokens, eight to a 16-byte chunk
             prep_wait(ok, &bars[SB_KH_EMPTY], ph ^ 1, p.err);
             for (int x = 0; x < nh; ++x) {

@@ -44,85 +44,138 @@ struct alignas(VEC * sizeof(T)) Raw {
     T v[VEC];
 };
 
-// One row for each group of TPR threads (a power of two up to 32: several rows to a
-// warp; else TPR is the block: one row to a block), NV vectors of VEC elements
-// to a thread, vector i of thread t at element (i TPR + t) VEC.
-template <typename T, int KIND, int VEC, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 256) kda_norm_kernel(const NormParams p, const int lanes) {
-    const int tpr = BLOCK ? int(blockDim.x) : lanes;
-    const int t = BLOCK ? int(threadIdx.x) : int(threadIdx.x) & (lanes - 1);
-    const int64_t row = BLOCK ? int64_t(blockIdx.x)
-                              : int64_t(blockIdx.x) * (blockDim.x / lanes) + int(threadIdx.x) / lanes;
+// A row's elements on its group of threads: NV vectors of VEC elements to a thread, vector i
+// of thread t at element (i tpr + t) VEC.
+template <typename T, int KIND, int VEC, int NV>
+struct NormRow {
     using R = Raw<T, VEC>;
-    pdl_launch_dependents();
-    pdl_wait();
-    const bool live = row < p.rows;
-    const int nvec = p.dim / VEC;              // VEC > 1 only where it divides dim
-    const int64_t base = row * p.dim;
-    R xr[NV], zr[NV];
-    const bool second = KIND != NORM_ADD || p.other != nullptr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = i * tpr + t;
-        if (live && j < nvec) {
-            xr[i] = *reinterpret_cast<const R *>(static_cast<const T *>(p.x) + base + int64_t(j) * VEC);
-            if (second) zr[i] = *reinterpret_cast<const R *>(static_cast<const T *>(p.other) + base + int64_t(j) * VEC);
-        }
-    }
+    R x[NV], z[NV];
     float r[NV][VEC];
-    float ss = 0.f;
+
+    __device__ __forceinline__ void load(const NormParams &p, int64_t row, int t, int tpr, int nvec) {
+        const bool second = KIND != NORM_ADD || p.other != nullptr;
+        const int64_t base = row * p.dim;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = live && i * tpr + t < nvec;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float a = in ? to_f32(xr[i].v[e]) : 0.f;
-            if (KIND == NORM_ADD) {
-                a *= p.alpha;
-                if (second && in) a += to_f32(zr[i].v[e]);
+        for (int i = 0; i < NV; ++i) {
+            const int j = i * tpr + t;
+            if (row < p.rows && j < nvec) {
+                x[i] = *reinterpret_cast<const R *>(static_cast<const T *>(p.x) + base + int64_t(j) * VEC);
+                if (second) z[i] = *reinterpret_cast<const R *>(static_cast<const T *>(p.other) + base + int64_t(j) * VEC);
             }
-            r[i][e] = a;
-            ss = fmaf(a, a, ss);
         }
     }
-    if (BLOCK) {
-        __shared__ float part[32];
+    // the row to be normed, in FP32; this thread's sum of its squares
+    __device__ __forceinline__ float squares(const NormParams &p, int64_t row, int t, int tpr, int nvec) {
+        const bool second = KIND != NORM_ADD || p.other != nullptr;
+        float ss = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        ss = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+        for (int i = 0; i < NV; ++i) {
+            const bool in = row < p.rows && i * tpr + t < nvec;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    } else {
-        for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int e = 0; e < VEC; ++e) {
+                float a = in ? to_f32(x[i].v[e]) : 0.f;
+                if (KIND == NORM_ADD) {
+                    a *= p.alpha;
+                    if (second && in) a += to_f32(z[i].v[e]);
+                }
+                r[i][e] = a;
+                ss = fmaf(a, a, ss);
+            }
+        }
+        return ss;
     }
-    if (!live) return;
-    const float inv = rsqrtf(ss / float(p.dim) + p.eps);
+    __device__ __forceinline__ void store(const NormParams &p, const R (&w)[NV], float inv, int64_t row, int t, int tpr,
+                                          int nvec) {
+        const int64_t base = row * p.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = i * tpr + t;
+            if (row >= p.rows || j >= nvec) continue;
+            R y, s;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float a = r[i][e] * inv * to_f32(w[i].v[e]);
+                if (KIND != NORM_ADD) {
+                    const float g = to_f32(z[i].v[e]);
+                    const float sg = 1.f / (1.f + __expf(-g));
+                    a *= KIND == NORM_GATED_SILU ? g * sg : sg;
+                }
+                put1(&y.v[e], a);
+                if (KIND == NORM_ADD) put1(&s.v[e], r[i][e]);
+            }
+            if (KIND == NORM_ADD && p.out != nullptr)
+                *reinterpret_cast<R *>(static_cast<T *>(p.out) + base + int64_t(j) * VEC) = s;
+            *reinterpret_cast<R *>(static_cast<T *>(p.y) + base + int64_t(j) * VEC) = y;
+        }
+    }
+};
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_weight(const NormParams &p, Raw<T, VEC> (&w)[NV], int t, int tpr, int nvec) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = i * tpr + t;
-        if (j >= nvec) break;
-        const R w = *reinterpret_cast<const R *>(static_cast<const T *>(p.weight) + int64_t(j) * VEC);
-        R y, s;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float a = r[i][e] * inv * to_f32(w.v[e]);
-            if (KIND != NORM_ADD) {
-                const float z = to_f32(zr[i].v[e]);
-                const float g = 1.f / (1.f + __expf(-z));
-                a *= KIND == NORM_GATED_SILU ? z * g : g;
-            }
-            put1(&y.v[e], a);
-            if (KIND == NORM_ADD) put1(&s.v[e], r[i][e]);
-        }
-        if (KIND == NORM_ADD && p.out != nullptr)
-            *reinterpret_cast<R *>(static_cast<T *>(p.out) + base + int64_t(j) * VEC) = s;
-        *reinterpret_cast<R *>(static_cast<T *>(p.y) + base + int64_t(j) * VEC) = y;
+        if (j < nvec) w[i] = *reinterpret_cast<const Raw<T, VEC> *>(static_cast<const T *>(p.weight) + int64_t(j) * VEC);
     }
 }
 
-constexpr int NORM_THREADS = 256;              // block of the several-rows form
+constexpr int NORM_THREADS = 256;              // block of the narrow form
+
+// Narrow rows: `lanes` threads (a power of two up to 32) to a row, ROWS rows to a thread.  One row of
+// 128 bf16 values alone keeps 32 bytes of a thread in flight; with four, 8192 x 64 rows of a
+// gated norm took 92 -> 71 us (bound: 59 us of copies).
+template <typename T, int KIND, int VEC, int NV, int ROWS>
+__global__ void __launch_bounds__(NORM_THREADS) kda_norm_narrow_kernel(const NormParams p, const int lanes) {
+    const int t = int(threadIdx.x) & (lanes - 1), groups = NORM_THREADS / lanes;
+    const int64_t row0 = int64_t(blockIdx.x) * groups * ROWS + int(threadIdx.x) / lanes;
+    const int nvec = p.dim / VEC;              // VEC > 1 only where it divides dim
+    pdl_launch_dependents();
+    pdl_wait();
+    NormRow<T, KIND, VEC, NV> row[ROWS];
+    Raw<T, VEC> w[NV];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) row[i].load(p, row0 + i * groups, t, lanes, nvec);
+    load_weight<T, VEC, NV>(p, w, t, lanes, nvec);
+    float ss[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) ss[i] = row[i].squares(p, row0 + i * groups, t, lanes, nvec);
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        row[i].store(p, w, rsqrtf(ss[i] / float(p.dim) + p.eps), row0 + i * groups, t, lanes, nvec);
+}
+
+// Wide rows: one to a block.
+template <typename T, int KIND, int VEC, int NV>
+__global__ void __launch_bounds__(1024) kda_norm_wide_kernel(const NormParams p) {
+    __shared__ float part[32];
+    const int t = threadIdx.x, tpr = blockDim.x, nvec = p.dim / VEC;
+    pdl_launch_dependents();
+    pdl_wait();
+    NormRow<T, KIND, VEC, NV> row;
+    Raw<T, VEC> w[NV];
+    row.load(p, blockIdx.x, t, tpr, nvec);
+    load_weight<T, VEC, NV>(p, w, t, tpr, nvec);
+    float ss = row.squares(p, blockIdx.x, t, tpr, nvec);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if ((t & 31) == 0) part[t >> 5] = ss;
+    __syncthreads();
+    ss = (t & 31) < (tpr >> 5) ? part[t & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    row.store(p, w, rsqrtf(ss / float(p.dim) + p.eps), blockIdx.x, t, tpr, nvec);
+}
+
+template <typename T, int KIND, int VEC, int NV, int ROWS>
+cudaError_t launch_narrow(const NormParams &p, int lanes, cudaStream_t s) {
+    const int64_t per = int64_t(NORM_THREADS / lanes) * ROWS;
+    return launch_pdl(true, kda_norm_narrow_kernel<T, KIND, VEC, NV, ROWS>, unsigned((p.rows + per - 1) / per), NORM_THREADS,
+                      0, s, p, lanes);
+}
 
 template <typename T, int KIND, int VEC>
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
@@ -131,11 +184,11 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
     if (nvec <= 64) {
         int lanes = 1;
         while (lanes < 32 && lanes < nvec) lanes *= 2;
-        const int64_t per = NORM_THREADS / lanes;
-        const int64_t grid = (p.rows + per - 1) / per;
-        if (nvec <= 32)
-            return launch_pdl(true, kda_norm_kernel<T, KIND, VEC, 1, false>, unsigned(grid), NORM_THREADS, 0, s, p, lanes);
-        return launch_pdl(true, kda_norm_kernel<T, KIND, VEC, 2, false>, unsigned(grid), NORM_THREADS, 0, s, p, lanes);
+        // several rows to a thread once there are enough to fill the GPU with them
+        const bool many = p.rows * lanes >= int64_t(1) << 20;
+        if (nvec > 32)
+            return many ? launch_narrow<T, KIND, VEC, 2, 2>(p, lanes, s) : launch_narrow<T, KIND, VEC, 2, 1>(p, lanes, s);
+        return many ? launch_narrow<T, KIND, VEC, 1, 4>(p, lanes, s) : launch_narrow<T, KIND, VEC, 1, 1>(p, lanes, s);
     }
     // wider rows: one to a block, as few vectors to a thread as 1024 threads allow
     // (two from 256 vectors on: fewer, busier warps to sum over)
@@ -143,13 +196,15 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
     while ((nv < 2 && nvec > 256) || nvec > nv * 1024) nv *= 2;
     const unsigned threads = unsigned((nvec + nv - 1) / nv + 31) / 32 * 32;
     const unsigned grid = unsigned(p.rows);
-    switch (nv) {
-        case 1: return launch_pdl(true, kda_norm_kernel<T, KIND, VEC, 1, true>, grid, threads, 0, s, p, 0);
-        case 2: return launch_pdl(true, kda_norm_kernel<T, KIND, VEC, 2, true>, grid, threads, 0, s, p, 0);
-        case 4: return launch_pdl(true, kda_norm_kernel<T, KIND, VEC, 4, true>, grid, threads, 0, s, p, 0);
-        case 8: if (VEC == 1) return launch_pdl(true, kda_norm_kernel<T, KIND, 1, 8, true>, grid, threads, 0, s, p, 0);
-        default: return launch_pdl(true, kda_norm_kernel<T, KIND, 1, 16, true>, grid, threads, 0, s, p, 0);
+    if (nv == 1) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 1>, grid, threads, 0, s, p);
+    if (nv == 2) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 2>, grid, threads, 0, s, p);
+    if (nv == 4) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 4>, grid, threads, 0, s, p);
+    // only rows read one element at a time are this wide
+    if constexpr (VEC == 1) {
+        if (nv == 8) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, 1, 8>, grid, threads, 0, s, p);
+        return launch_pdl(true, kda_norm_wide_kernel<T, KIND, 1, 16>, grid, threads, 0, s, p);
     }
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>

@@ -16,39 +16,36 @@ from typing import Optional
 
 import torch
 
-from ._lib import lib
+from ._lib import DTYPE_CODE, check, lib
 
 WIDTHS = (32, 64, 96, 128)
 ACT_CODE = {"sigmoid": 0, "silu": 1}
 
 
-def _bind():
-    # the package's helpers; imported late because the package imports this module
-    from . import DTYPE_CODE, _check
-    return DTYPE_CODE, _check
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _launch_on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     """Context in which `device` is current and, if given, `stream` is its current stream."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+    return _NO_CONTEXT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _current_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _on_gpu(**tensors) -> torch.device:
-    device = None
-    for name, t in tensors.items():
+def _on_gpu(names: str, *tensors) -> torch.device:
+    """The device of the tensors (named in `names`; None ones are skipped), which must be one GPU."""
+    device = tensors[0].device
+    for i, t in enumerate(tensors):
         if t is None:
             continue
         if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-        device = t.device
+            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{names.split()[i]} is on {t.device}, {names.split()[0]} on {device}")
     return device
 
 
@@ -58,13 +55,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """t itself, or a contiguous copy where its layout or address does not fit the kernels' vectors."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 def _rule_shapes(q, k, v, g, beta, lead: int):
     """Checks of the token tensors, which have `lead` leading dimensions; (Hk, H, K, V, gate code)."""
-    codes = _bind()[0]
     if q.dim() != lead + 2 or v.dim() != lead + 2 or k.shape != q.shape or q.shape[:lead] != v.shape[:lead]:
         raise ValueError(f"shapes q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
     Hk, K = q.shape[lead:]
@@ -81,7 +78,8 @@ def _rule_shapes(q, k, v, g, beta, lead: int):
         gate = 1
     else:
         raise ValueError(f"g must be {tuple(v.shape[:-1])} or that with {K} channels, got {tuple(g.shape)}")
-    if q.dtype not in codes or any(t.dtype != q.dtype for t in (k, v, beta)) or g.dtype != torch.float32:
+    dt = q.dtype
+    if dt not in DTYPE_CODE or k.dtype != dt or v.dtype != dt or beta.dtype != dt or g.dtype != torch.float32:
         raise ValueError(f"unsupported dtypes q {q.dtype}, k {k.dtype}, v {v.dtype}, beta {beta.dtype}, g {g.dtype}")
     return Hk, H, K, V, gate
 
@@ -103,7 +101,7 @@ def _state(name: str, t: torch.Tensor, entries: Optional[int], H: int, K: int, V
 
 def _output(name: str, out: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like)
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
     return out
@@ -130,9 +128,8 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     uses entry slots[n], final_state is written in place and defaults to initial_state.
     workspace: optional CUDA buffer of delta_prefill_workspace_size() bytes.
     """
-    codes, check = _bind()
-    device = _on_gpu(q=q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
-                     final_state=final_state, slots=slots, out=out, workspace=workspace)
+    device = _on_gpu("q k v g beta cu_seqlens initial_state final_state slots out workspace", q, k, v, g, beta,
+                     cu_seqlens, initial_state, final_state, slots, out, workspace)
     Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 2)
     B, T = q.shape[:2]
     cu_seqlens = _int32("cu_seqlens", cu_seqlens)
@@ -150,7 +147,7 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         if t is not None:
             _state(name, t, entries, H, K, V)
     with _launch_on(device, stream):
-        q, k, v, g, beta = (_aligned(t) for t in (q, k, v, g, beta))
+        q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
         slots = slots.contiguous() if slots is not None else None
         out = _output("out", out, v)
         cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
@@ -163,7 +160,7 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         st = lib().kda_delta_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
             _ptr(initial_state), final_state.data_ptr(), _ptr(slots), entries, _ptr(cu_seqlens), nseq, B, T,
-            Hk, H, K, V, codes[q.dtype], gate, float(K ** -0.5 if scale is None else scale), _ptr(workspace), ws_bytes,
+            Hk, H, K, V, DTYPE_CODE[q.dtype], gate, float(K ** -0.5 if scale is None else scale), _ptr(workspace), ws_bytes,
             _current_stream(device))
     check(st, "kda_delta_prefill")
     return out, final_state
@@ -178,8 +175,7 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     state: float32 pool [entries, H, K, V]; request n uses entry slots[n] (int32 [N]), or n
     without slots.  A slot outside the pool (-1 for padding) reads zeros and stores nothing.
     """
-    codes, check = _bind()
-    device = _on_gpu(q=q, k=k, v=v, g=g, beta=beta, state=state, slots=slots, out=out)
+    device = _on_gpu("q k v g beta state slots out", q, k, v, g, beta, state, slots, out)
     Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 1)
     N = q.shape[0]
     slots = _int32("slots", slots, N)
@@ -187,26 +183,24 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     if slots is None and state.shape[0] < N:
         raise ValueError(f"{N} requests and a pool of {state.shape[0]} states")
     with _launch_on(device, stream):
-        q, k, v, g, beta = (_aligned(t) for t in (q, k, v, g, beta))
+        q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
         slots = slots.contiguous() if slots is not None else None
         out = _output("out", out, v)
         st = lib().kda_delta_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), state.data_ptr(),
-            _ptr(slots), state.shape[0], N, Hk, H, K, V, codes[q.dtype], gate,
+            _ptr(slots), state.shape[0], N, Hk, H, K, V, DTYPE_CODE[q.dtype], gate,
             float(K ** -0.5 if scale is None else scale), _current_stream(device))
     check(st, "kda_delta_step")
     return out
 
 
-def _norm_shapes(x: torch.Tensor, weight: torch.Tensor, **others) -> None:
-    codes = _bind()[0]
-    if x.dim() < 1 or x.dtype not in codes:
+def _norm_shapes(x: torch.Tensor, weight: torch.Tensor, other: Optional[torch.Tensor], name: str) -> None:
+    if x.dim() < 1 or x.dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported x {x.dtype} {tuple(x.shape)}")
-    if tuple(weight.shape) != (x.shape[-1],) or weight.dtype != x.dtype:
+    if weight.dim() != 1 or weight.shape[0] != x.shape[-1] or weight.dtype != x.dtype:
         raise ValueError(f"weight must be a {x.dtype} [{x.shape[-1]}], got {weight.dtype} {tuple(weight.shape)}")
-    for name, t in others.items():
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
-            raise ValueError(f"{name} must match x, a {x.dtype} {tuple(x.shape)}; got {t.dtype} {tuple(t.shape)}")
+    if other is not None and (other.shape != x.shape or other.dtype != x.dtype):
+        raise ValueError(f"{name} must match x, a {x.dtype} {tuple(x.shape)}; got {other.dtype} {tuple(other.shape)}")
 
 
 def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float = 1e-6,
@@ -216,9 +210,8 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Te
 
     residual may be None (r = alpha x); residual_out may be residual and out may be x.
     """
-    codes, check = _bind()
-    device = _on_gpu(x=x, residual=residual, weight=weight, out=out, residual_out=residual_out)
-    _norm_shapes(x, weight, residual=residual)
+    device = _on_gpu("x residual weight out residual_out", x, residual, weight, out, residual_out)
+    _norm_shapes(x, weight, residual, "residual")
     dim = x.shape[-1]
     with _launch_on(device, stream):
         x, weight = x.contiguous(), weight.contiguous()
@@ -226,7 +219,7 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Te
         out, residual_out = _output("out", out, x), _output("residual_out", residual_out, x)
         st = lib().kda_add_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(),
                                 residual_out.data_ptr(), x.numel() // dim if dim else 0, dim, alpha, eps,
-                                codes[x.dtype], _current_stream(device))
+                                DTYPE_CODE[x.dtype], _current_stream(device))
     check(st, "kda_add_norm")
     return out, residual_out
 
@@ -238,17 +231,16 @@ def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: f
 
     out may be x or gate.
     """
-    codes, check = _bind()
     if activation not in ACT_CODE:
         raise ValueError(f"unknown activation {activation!r}")
-    device = _on_gpu(x=x, gate=gate, weight=weight, out=out)
-    _norm_shapes(x, weight, gate=gate)
+    device = _on_gpu("x gate weight out", x, gate, weight, out)
+    _norm_shapes(x, weight, gate, "gate")
     dim = x.shape[-1]
     with _launch_on(device, stream):
         x, gate, weight = x.contiguous(), gate.contiguous(), weight.contiguous()
         out = _output("out", out, x)
         st = lib().kda_gated_norm(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), out.data_ptr(),
-                                  x.numel() // dim if dim else 0, dim, eps, ACT_CODE[activation], codes[x.dtype],
+                                  x.numel() // dim if dim else 0, dim, eps, ACT_CODE[activation], DTYPE_CODE[x.dtype],
                                   _current_stream(device))
     check(st, "kda_gated_norm")
     return out

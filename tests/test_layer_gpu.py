@@ -151,6 +151,14 @@ def test_prefill_widths(kda, K, V):
     Rule([70, 5, 64, 129], K=K, V=V, seed=K + V, dtype=F16, initial=True).check(kda)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("K,V", [(32, 64), (64, 32), (96, 32), (96, 128), (128, 96)])
+def test_prefill_widths_many_chunks(kda, dtype, K, V):
+    """Enough chunk-heads that every buffer of a persistent block goes round several times, with one to four
+    slices of channels to a chunk."""
+    Rule([170, 126, 276, 64], Hk=49, H=49, K=K, V=V, seed=K + V + 1, dtype=dtype).check(kda)
+
+
 @pytest.mark.parametrize("Hk,H", [(1, 1), (1, 4), (2, 6), (5, 5), (3, 12)])
 @pytest.mark.parametrize("gate", ["channel", "head"])
 def test_prefill_shared_key_heads(kda, Hk, H, gate):
