@@ -9,6 +9,7 @@
 
 #include "kda_delta_rec.cuh"
 #include "kda_delta_scan.cuh"
+#include "kda_delta_launch.h"
 #include "kda_internal.h"
 #include "kda_launch.cuh"
 #include "kda_layer.h"
@@ -22,6 +23,34 @@ using namespace kda;
 bool chunked_form(int64_t B, int64_t T, int32_t num_seqs) {
     const int64_t seqs = num_seqs > 0 ? num_seqs : B;
     return B > 0 && T > 0 && B * T >= 16 * seqs;
+}
+
+// Chunks to a segment for this shape, 0 where sequences are not split, and a bound on the segments.
+// The model: a chunk of the walk takes 4 us, 3 without outputs; the first run has two walks to a
+// segment but the first's one and the last's none; the join takes 2 us a segment and the two more
+// launches 10.  Sized for the 152 SMs of a GB300.
+int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_t &units) {
+    const int64_t seqs = num_seqs > 0 ? num_seqs : B, heads = seqs * H, sms = 152;
+    const int64_t total = max_chunks(B, T, num_seqs, BT);
+    const double c = double(total) / double(seqs);
+    auto waves = [&](int64_t n) { return double((n + sms - 1) / sms); };
+    double best = waves(heads) * c * 4.0;
+    int32_t seg = 0;
+    for (int P = 2; P <= 32 && heads < sms; ++P) {
+        const int32_t s = int32_t(c / P + 0.999);
+        if (s < 4) break;
+        const double t = waves((2 * P - 3) * heads) * s * 3.0 + waves(P * heads) * s * 4.0 + 2.0 * P + 10.0;
+        if (t < 0.95 * best) {
+            best = t;
+            seg = s;
+        }
+    }
+    units = seg == 0 ? seqs : num_seqs > 0 ? total / seg + seqs : B * ((((T + BT - 1) / BT) + seg - 1) / seg);
+    return seg;
+}
+
+size_t image_bytes(int64_t B, int64_t T, int32_t H, int32_t num_seqs) {
+    return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * img_bytes<true>();
 }
 
 bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }
@@ -80,42 +109,6 @@ bool encode_delta(const DeltaParams &p, int32_t dt, int64_t rows, DeltaMaps &pre
                                            encode_rows(&scan.g, p.g, KDA_F32, rows, p.H, p.K, p.K)));
 }
 
-// Opt-in shared memory of the chunked form's kernels, set once per device.
-template <typename T, bool PLO, bool W128>
-cudaError_t chunked_ready(int device) {
-    static std::mutex mu;
-    static bool done[64] = {false};
-    std::lock_guard<std::mutex> lock(mu);
-    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    if (done[device]) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         prep_bytes<T>());
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 scan_bytes<T, PLO>());
-    done[device] = e == cudaSuccess;
-    return e;
-}
-
-template <typename T, bool PLO, bool W128>
-cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms, cudaStream_t s) {
-    cudaError_t e = chunked_ready<T, PLO, W128>(device);
-    if (e != cudaSuccess) return e;
-    const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms);
-    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(prep_bytes<T>()), s, prep,
-                   p);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128>, unsigned(p.nseq) * unsigned(p.H), SCAN_THREADS,
-                      size_t(scan_bytes<T, PLO>()), s, scan, p);
-}
-
-template <typename T, bool PLO>
-cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
-                           cudaStream_t s) {
-    return p.K == 128 && p.V == 128 ? launch_widths<T, PLO, true>(p, prep, scan, device, sms, s)
-                                    : launch_widths<T, PLO, false>(p, prep, scan, device, sms, s);
-}
-
 kda_status_t run_chunked(DeltaParams p, int32_t dtype, int64_t rows, cudaStream_t s) {
     int device = 0;
     DeviceInfo info;
@@ -125,9 +118,9 @@ kda_status_t run_chunked(DeltaParams p, int32_t dtype, int64_t rows, cudaStream_
     if (!encode_delta(p, dtype, rows, prep, scan)) return KDA_ERR_CUDA;
     cudaError_t e;
     switch (dtype) {
-        case KDA_F32: e = launch_chunked<float, true>(p, prep, scan, device, info.num_sms, s); break;
-        case KDA_BF16: e = launch_chunked<__nv_bfloat16, false>(p, prep, scan, device, info.num_sms, s); break;
-        default: e = launch_chunked<__half, true>(p, prep, scan, device, info.num_sms, s); break;
+        case KDA_F32: e = launch_chunked_f32(p, prep, scan, device, info.num_sms, s); break;
+        case KDA_BF16: e = launch_chunked_bf16(p, prep, scan, device, info.num_sms, s); break;
+        default: e = launch_chunked_f16(p, prep, scan, device, info.num_sms, s); break;
     }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -167,7 +160,10 @@ size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t
     if (H < 1 || num_seqs < 0 || !width_ok(K) || !width_ok(V)) return 0;
     if (num_seqs > 0 && B != 1) return 0;
     if (!chunked_form(B, T, num_seqs)) return 0;
-    return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * img_bytes<true>();
+    int64_t units = 0;
+    const int32_t seg = segment_chunks(B, T, H, num_seqs, units);
+    return image_bytes(B, T, H, num_seqs) +
+           (seg > 0 ? size_t(units) * size_t(H) * size_t(K) * size_t(K + V) * sizeof(float) : 0);
 }
 
 kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
@@ -207,11 +203,15 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     }
     if (rows == 0 && state_out == nullptr) return KDA_OK;
     DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
-                  Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr};
+                  Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr, 0, 0, nullptr};
     if (!chunked_form(B, T, num_seqs)) return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
     p.cpr = int32_t((T + BT - 1) / BT);
     p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
     p.ws = static_cast<unsigned char *>(workspace);
+    int64_t units = 0;
+    p.seg = segment_chunks(B, T, H, num_seqs, units);
+    p.n_units = int32_t(units);
+    p.trans = reinterpret_cast<float *>(p.ws + image_bytes(B, T, H, num_seqs));
     return run_chunked(p, dtype, int64_t(rows), static_cast<cudaStream_t>(stream));
 }
 
@@ -230,7 +230,7 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
                  size_t(num_slots) * size_t(H) * size_t(K) * size_t(V) * 4))
         return KDA_ERR_INVALID_ARGUMENT;
     const DeltaParams p{q, k, v, g, beta, o, state, state, slots, num_slots, nullptr, N, 1, Hk, H, K, V, gate, scale,
-                        nullptr, 0, 0, nullptr};
+                        nullptr, 0, 0, nullptr, 0, 0, nullptr};
     return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
 }
 

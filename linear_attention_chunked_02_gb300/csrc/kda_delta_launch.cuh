@@ -1,0 +1,55 @@
+// kda_delta_launch.cuh -- host-side launches of the chunked gated delta rule for one type.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "kda_delta_launch.h"
+#include "kda_launch.cuh"
+
+namespace kda {
+
+// Opt-in shared memory of the kernels, set once per device.
+template <typename T, bool PLO, bool W128>
+cudaError_t chunked_ready(int device) {
+    static std::mutex mu;
+    static bool done[64] = {false};
+    std::lock_guard<std::mutex> lock(mu);
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    if (done[device]) return cudaSuccess;
+    constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, attr, prep_bytes<T>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, false>, attr, scan_bytes<T, PLO>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, true>, attr, scan_bytes<T, PLO>());
+    done[device] = e == cudaSuccess;
+    return e;
+}
+
+template <typename T, bool PLO, bool W128>
+cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
+                          cudaStream_t s) {
+    cudaError_t e = chunked_ready<T, PLO, W128>(device);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms), walks = unsigned(p.n_units) * unsigned(p.H);
+    const size_t bytes = size_t(scan_bytes<T, PLO>());
+    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
+    if (e == cudaSuccess && p.seg > 0) {
+        e = launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, true>, 2 * walks, SCAN_THREADS, bytes, s, scan, p);
+        if (e == cudaSuccess)
+            e = launch_pdl(true, kda_delta_join_kernel, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / 8), JOIN_THREADS, 0,
+                           s, p);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, false>, walks, SCAN_THREADS, bytes, s, scan, p);
+}
+
+// PLO: P and Q keep a low part (all types but bf16, whose rounding is above what it adds).
+template <typename T, bool PLO>
+cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
+                           cudaStream_t s) {
+    return p.K == 128 && p.V == 128 ? launch_widths<T, PLO, true>(p, prep, scan, device, sms, s)
+                                    : launch_widths<T, PLO, false>(p, prep, scan, device, sms, s);
+}
+
+}  // namespace kda

@@ -39,6 +39,9 @@ struct DeltaParams {
     int32_t cpr;                // dense: chunks per batch row
     int32_t n_tasks;            // bound on chunk-heads
     unsigned char *ws;          // workspace: one image to a chunk-head
+    int32_t seg;                // chunks to a segment of a sequence; 0: sequences are not split
+    int32_t n_units;            // bound on segments (seg == 0: sequences)
+    float *trans;               // [n_units][H]{N [K, V], M [K, K]}: what a segment does to the state
 };
 
 // State entry of sequence n, or -1 for none.

@@ -27,6 +27,13 @@
 // the four lane quarters each look out for such a chunk and take it token by token in
 // FP32 (scan_tokens).
 //
+// Few heads and long sequences leave most of the GPU idle in that walk, so sequences can be split
+// into segments.  A segment maps the state by S -> M S + N, M [K, K], N [K, V]: a first run of
+// this kernel (TRANS) takes N from the walk without outputs, from zero states (the sequence's
+// own in its first segment), and M from the walk of the identity with v = 0;
+// kda_delta_join_kernel chains them into every segment's initial state; then all
+// segments are walked at once.
+//
 // One CTA of eight warpgroups per sequence-head (registers moved to the chain):
 //   * warps 0-15 (chain): four warps to each lane quarter, a quarter of the columns each; S in
 //     registers.  What bounds the walk is their path from state to state, so all
@@ -53,7 +60,7 @@ constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY =
               SB_GAM = 22, SCAN_NBARS = 24;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_RED = 256;                  // a word to a warp: chunks before the sequence
-constexpr int SCAN_OFF_GAM = 512;                  // [2][128] e^{G_C}
+constexpr int SCAN_OFF_GAM = 640;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [4 parts][128 lanes] largest |S|
 constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 4 * 128 * 4;      // [4 parts][128 lanes] largest |v|
 constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 4 * 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
@@ -77,7 +84,7 @@ template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
 template <typename T, bool PLO>
 constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
-static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 32 * 4 <= SCAN_OFF_GAM, "header fits");
+static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 68 * 4 <= SCAN_OFF_GAM && 2 * 128 >= 256, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
 static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
@@ -214,8 +221,81 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
     }
 }
 
+// Which segment of which sequence the CTA has, and the chunks before that sequence.
+struct Unit {
+    int32_t n, part, before, parts;        // parts == 0: none
+};
+constexpr int SCAN_SORT = 256;             // packed batches of up to this many sequences go longest first
+
+// Unit u, by all threads of the CTA; `red` and `len` are shared memory of 68 and SCAN_SORT words.
+__device__ __forceinline__ Unit scan_unit(const DeltaParams &p, int32_t u, int32_t *red, int32_t *len) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.cu == nullptr) {
+        const int32_t parts = p.seg > 0 ? max(1, (p.cpr + p.seg - 1) / p.seg) : 1, n = u / parts;
+        return {n, u - n * parts, n * p.cpr, n < p.nseq ? parts : 0};
+    }
+    if (p.seg == 0 && p.nseq <= SCAN_SORT) {
+        // the u-th longest sequence (equal ones in their order): the long walks start first
+        if (tid < p.nseq) len[tid] = max(0, __ldg(p.cu + tid + 1) - __ldg(p.cu + tid));
+        __syncthreads();
+        if (tid < p.nseq) {
+            int rank = 0;
+            const int mine = len[tid];
+            for (int j = 0; j < p.nseq; ++j) rank += len[j] > mine || (len[j] == mine && j < tid);
+            if (rank == u) red[0] = tid;
+        }
+        __syncthreads();
+        const int32_t n = red[0];
+        int32_t before = 0;
+        for (int j = 0; j < n; ++j) before += (len[j] + BT - 1) / BT;
+        return {n, 0, before, 1};
+    }
+    int32_t units = 0, chunks = 0;          // of the sequences before this tile of 1024
+    for (int32_t base = 0; base < p.nseq; base += SCAN_THREADS) {
+        const int32_t i = base + tid;
+        const int32_t nc = i < p.nseq ? nchunks<BT>(__ldg(p.cu + i), __ldg(p.cu + i + 1)) : 0;
+        const int32_t nu = i < p.nseq ? (p.seg > 0 ? max(1, (nc + p.seg - 1) / p.seg) : 1) : 0;
+        int32_t su = nu, sc = nc;           // inclusive sums over the warp, then over the warps
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t a = __shfl_up_sync(0xffffffffu, su, o), b = __shfl_up_sync(0xffffffffu, sc, o);
+            if (lane >= o) {
+                su += a;
+                sc += b;
+            }
+        }
+        if (lane == 31) {
+            red[warp] = su;
+            red[32 + warp] = sc;
+        }
+        if (tid == 0) red[64] = -1;
+        __syncthreads();
+        int32_t all_u = 0, all_c = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) {
+                su += red[w];
+                sc += red[32 + w];
+            }
+            all_u += red[w];
+            all_c += red[32 + w];
+        }
+        if (nu > 0 && u >= units + su - nu && u < units + su) {
+            red[64] = i;
+            red[65] = u - (units + su - nu);
+            red[66] = chunks + sc - nc;
+            red[67] = nu;
+        }
+        __syncthreads();
+        if (red[64] >= 0) return {red[64], red[65], red[66], red[67]};
+        __syncthreads();
+        units += all_u;
+        chunks += all_c;
+    }
+    return {0, 0, 0, 0};
+}
+
 // W128: K and V are 128, which makes every row pitch on chip an immediate.
-template <typename T, bool PLO, bool W128>
+template <typename T, bool PLO, bool W128, bool TRANS>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -226,7 +306,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     constexpr int NI = scan_nimg<PLO>();
     constexpr bool STAGED = sizeof(T) == 2;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int n = int(blockIdx.x) / p.H, h = int(blockIdx.x) - n * p.H;
+    // TRANS: even CTAs take N, odd ones M
+    const int run = TRANS ? int(blockIdx.x) & 1 : 0, index = TRANS ? int(blockIdx.x) >> 1 : int(blockIdx.x);
+    const int u = index / p.H, h = index - u * p.H;
     const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
 
@@ -241,29 +323,42 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         tc::tmem_alloc(smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
-    // the sequence's rows, and the number of chunks before its first
-    int64_t ra, rb;
-    sequence_rows(p, n, ra, rb);
-    int32_t before = 0;
-    if (p.cu != nullptr) {
-        for (int i = tid; i < n; i += SCAN_THREADS) before += nchunks<BT>(__ldg(p.cu + i), __ldg(p.cu + i + 1));
-        before = __reduce_add_sync(0xffffffffu, before);
-        if (lane == 0) red[warp] = before;
-    }
+    const Unit unit = scan_unit(p, u, red, reinterpret_cast<int32_t *>(gam));
+    const int n = unit.n;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    if (p.cu != nullptr) {
-        before = 0;
-        for (int i = 0; i < SCAN_THREADS / 32; ++i) before += red[i];
-    } else {
-        before = n * p.cpr;
-    }
-    const int rows = int(rb - ra);
+    // rows of this unit, and its chunks from `before` on
+    int64_t ra = 0, rb = 0;
+    if (unit.parts > 0) sequence_rows(p, n, ra, rb);
+    const int32_t first = unit.part * p.seg, before = unit.before + first;
+    const bool last = unit.part == unit.parts - 1;
+    ra += int64_t(64) * first;
+    if (p.seg > 0 && rb - ra > int64_t(64) * p.seg) rb = ra + int64_t(64) * p.seg;
+    const int rows = rb > ra ? int(rb - ra) : 0;
     int nc = (rows + BT - 1) / BT;
-    // malformed cu_seqlens must not lead past the workspace
+    // malformed cu_seqlens must not lead past the workspace; the last segment's map is not needed,
+    // nor what the first makes of another state than its own
     if (before < 0 || (int64_t(before) + nc) * p.H > p.n_tasks) nc = 0;
+    const bool idle = unit.parts == 0 || (TRANS && (last || (run == 1 && unit.part == 0)));
+    if (idle) nc = 0;
+    // states: where the walk starts from and where it ends
+    const float *from = nullptr;
+    float *to = nullptr;
+    if (!idle) {
+        const int32_t e = state_entry(p, n);
+        const int64_t sz = int64_t(K) * V, tz = sz + int64_t(K) * K;
+        float *mine = p.trans + (int64_t(u) * p.H + h) * tz;
+        if (unit.part == 0) {
+            if (p.state_in != nullptr && e >= 0) from = p.state_in + (int64_t(e) * p.H + h) * sz;
+        } else if (!TRANS) {
+            from = mine - int64_t(p.H) * tz;               // chained into the segment before
+        }
+        if (TRANS) to = mine + (run == 1 ? sz : 0);
+        else if (last && p.state_out != nullptr && e >= 0) to = p.state_out + (int64_t(e) * p.H + h) * sz;
+    }
+    const int W = run == 1 ? K : V;                        // columns of the state that is walked
     const unsigned char *img0 = p.ws + (int64_t(before) * p.H + h) * img_bytes<PLO>();
     const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
     const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
@@ -294,18 +389,21 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             __syncwarp();
             tc::fence_after_sync();
         };
-        const int32_t e = state_entry(p, n);
-        const bool mine = v < V;
+        const bool mine = v < W;
         float S[32];                                       // S[32 part + i][v]
         const bool held = 32 * part < K;                   // K is a multiple of 32
         {
-            const float *sp = p.state_in + ((int64_t(e < 0 ? 0 : e) * p.H + h) * K + 32 * part) * V + v;
-            const bool read = p.state_in != nullptr && e >= 0 && mine && held;
+            const float *sp = from + int64_t(32 * part) * W + v;
+            const bool read = from != nullptr && mine && held;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * V] : 0.f;
+            for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * W] : 0.f;
+            if (run == 1) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i] = 32 * part + i == v && held ? 1.f : 0.f;
+            }
         }
         const int t0 = 16 * part;                          // this thread's tokens of a chunk: t0 .. t0 + 15
-        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (mine ? v : 0);
+        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (v < V ? v : 0);
         const uint32_t sop = tq + TM_SHI + 16 * part, rop = tq + TM_RHI + 8 * part;      // operand columns, hi parts
         auto put_state = [&](float s) {
 #pragma unroll
@@ -331,13 +429,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             const int left = rows - 64 * c;
-            prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
-            // rows past the end hold the next request's; columns past V stay in their lanes
-            for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
-                if (mine) sv[i * V] = T(0.f);
+            if (run == 0) {
+                prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
+                // rows past the end hold the next request's; columns past V stay in their lanes
+                for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
+                    if (v < V) sv[i * V] = T(0.f);
+            }
             Pair<T> vr[sizeof(T) == 2 ? 8 : 1];            // 16-bit values, two tokens to a word
             float bv = 0.f;
-            if constexpr (sizeof(T) == 2) {
+            if (run == 1) {
+                // values of zero
+            } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
                 Pair<T> m = vr[0].abs();
@@ -362,7 +464,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float bU = msum * bR;
             const float sU = pow2_scale(bU, VS_LO, VS_HI, invU);
             float sS = pow2_scale(bS + 64.f * kmax * bU, VS_LO, VS_HI, invS1);
-            bool weak = __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
+            // (M and N come without outputs, and are as good as the state that goes in)
+            bool weak = !TRANS && __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
             if (weak) {                                    // the same in the four warps of the quarter
                 prep_wait(ok, &bars[SB_GAM + ph], (c >> 1) & 1, p.err);
                 float gmax = 0.f;
@@ -374,7 +477,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     sS = pow2_scale(lane_max(smax, state_max()), VS_LO, VS_HI, invS1);     // the new state's own bound
                 }
             }
-            if (part == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
+            if (!TRANS && part == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
             // R = V - (K e^G) S, scaled
             accumulator(SB_D1, ph);
             {
@@ -387,7 +490,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < 8; ++i) {
                     float2 w;
                     if constexpr (sizeof(T) == 2) w = vr[i].wide();
-                    else w = make_float2(widen1(sv[2 * i * V]), widen1(sv[(2 * i + 1) * V]));
+                    else w = run == 1 ? both(0.f) : make_float2(widen1(sv[2 * i * V]), widen1(sv[(2 * i + 1) * V]));
                     w = __ffma2_rn(f, make_float2(x[2 * i], x[2 * i + 1]), __fmul2_rn(w, s2));
                     split_f16(w.x, w.y, hi[i], lo[i]);
                 }
@@ -435,10 +538,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             bS = lane_max(smax, mx);
             invS = invS1;
         }
-        if (p.state_out != nullptr && e >= 0 && mine && held) {
-            float *sp = p.state_out + ((int64_t(e) * p.H + h) * K + 32 * part) * V + v;
+        if (to != nullptr && mine && held) {
+            float *sp = to + int64_t(32 * part) * W + v;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sp[int64_t(i) * V] = S[i];
+            for (int i = 0; i < 32; ++i) sp[int64_t(i) * W] = S[i];
         }
     } else if (warp < 24) {
         // (64 registers, as at launch)
@@ -519,7 +622,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     rk[i] = two(kp, i, d);
-                    rq[i] = two(qp, i, d);
+                    if (!TRANS) rq[i] = two(qp, i, d);
                     g[i] = decay(i, d);
                 }
 #pragma unroll
@@ -527,16 +630,18 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     G = __ffma2_rn(g[i], both(L2E), G);
                     const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
                     const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
-                    const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
-                    uint32_t kh, kl, qh, ql = 0u;
+                    uint32_t kh, kl, qh = 0u, ql = 0u;
                     split_f16(kv.x, kv.y, kh, kl);
-                    if (PLO) split_f16(qv.x, qv.y, qh, ql);
-                    else qh = round_f16(qv.x, qv.y);
+                    if (!TRANS) {
+                        const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
+                        if (PLO) split_f16(qv.x, qv.y, qh, ql);
+                        else qh = round_f16(qv.x, qv.y);
+                    }
                     unsigned char *at = kq + i * 128 + 16 * ((lane >> 2) ^ i);
                     *reinterpret_cast<uint32_t *>(at) = kh;
                     *reinterpret_cast<uint32_t *>(at + 16384) = kl;
-                    *reinterpret_cast<uint32_t *>(at + 32768) = qh;
-                    if (PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+                    if (!TRANS) *reinterpret_cast<uint32_t *>(at + 32768) = qh;
+                    if (!TRANS && PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
                 }
                 if (rg == 7)                               // here G is the whole chunk's sum
                     *reinterpret_cast<float2 *>(gam + ph * 128 + 64 * x + 2 * lane) = make_float2(ex2(G.x), ex2(G.y));
@@ -601,7 +706,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 #pragma unroll
         for (int i = 0; i < 8; ++i) off[i] = v * sizeof(T) + i * step;
         unsigned char *const ob = static_cast<unsigned char *>(p.o) + (ra * p.H + h) * V * int64_t(sizeof(T));
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; !TRANS && c < nc; ++c) {
             const uint32_t ph = c & 1;
             // O = (scale Q e^G) S0 + P U
             prep_wait(ok, &bars[SB_U], ph, p.err);         // the chain's scales
@@ -667,11 +772,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (tc::elect_one()) {
                     mma_split<false>(steps, tmem + TM_D1, tmem + TM_SHI, tmem + TM_SLO, kq, kq + 16384, 8192, SCAN_ID64);
                     commit(SB_D1);
+                    if (TRANS) commit(SB_KQ_EMPTY);
                 }
-                wait(SB_O_EMPTY, ph ^ 1);
+                if (!TRANS) wait(SB_O_EMPTY, ph ^ 1);
                 __syncwarp();
                 tc::fence_after_sync();
-                if (tc::elect_one()) {
+                if (!TRANS && tc::elect_one()) {
                     mma_split<!PLO>(steps, tmem + TM_O1, tmem + TM_SHI, tmem + TM_SLO, kq + 32768, kq + 49152, 8192,
                                     SCAN_ID64);
                     commit(SB_KQ_EMPTY);
@@ -693,9 +799,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     mma_split<false>(4, tmem + TM_D3, tmem + TM_RHI, tmem + TM_RLO, kh, kh + 16384, 0, id3);
                     commit(SB_D3);
                     commit(SB_KH_EMPTY);
-                    mma_split<!PLO>(4, tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0,
-                                    SCAN_ID64);
-                    commit(SB_O_FULL);
+                    if (!TRANS) {
+                        mma_split<!PLO>(4, tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0,
+                                        SCAN_ID64);
+                        commit(SB_O_FULL);
+                    }
                     commit(SB_IMG_EMPTY + c % NI);
                 }
                 __syncwarp();
@@ -704,7 +812,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // -------------------------------------------- loads of q, k and g (16-bit)
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
-                const uint32_t bytes = 2 * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);
+                const uint32_t bytes = (TRANS ? 1 : 2) * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);
                 const int hk = h / (p.H / p.Hk);
                 for (int c = 0; c < nc; ++c) {
                     prep_wait(ok, &bars[SB_ST_EMPTY], (c & 1) ^ 1, p.err);
@@ -712,11 +820,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     if (tc::elect_one()) {
                         mbar_arrive_expect_tx(&bars[SB_ST_FULL], bytes);
                         tma_load_3d(st, &maps.k, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
-                        tma_load_3d(st + 16384, &maps.q, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
+                        if (!TRANS) tma_load_3d(st + 16384, &maps.q, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
                         if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, h, int(ra) + 64 * c, &bars[SB_ST_FULL]);
                         if (c + 1 < nc) {                  // the next chunk's on their way to L2 meanwhile
                             tc::prefetch_3d(&maps.k, 0, hk, int(ra) + 64 * c + 64);
-                            tc::prefetch_3d(&maps.q, 0, hk, int(ra) + 64 * c + 64);
+                            if (!TRANS) tc::prefetch_3d(&maps.q, 0, hk, int(ra) + 64 * c + 64);
                             if (p.gate == 0) tc::prefetch_3d(&maps.g, 0, h, int(ra) + 64 * c + 64);
                         }
                     }
@@ -726,7 +834,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
         } else if (warp == 30) {
             // --------------------------------------------------------- loads of v
-            for (int c = 0; c < nc; ++c) {
+            for (int c = 0; run == 0 && c < nc; ++c) {
                 prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
                 __syncwarp();
                 if (tc::elect_one()) {
@@ -736,18 +844,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 __syncwarp();
             }
-            if (nc > 0) prep_wait(ok, &bars[SB_V_FULL], (nc - 1) & 1, p.err);
+            if (run == 0 && nc > 0) prep_wait(ok, &bars[SB_V_FULL], (nc - 1) & 1, p.err);
         } else {
             // ------------------------------------------------- loads of M and P
             for (int c = 0; c < nc; ++c) {
                 prep_wait(ok, &bars[SB_IMG_EMPTY + c % NI], ((c / NI) & 1) ^ 1, p.err);
-                prep_wait(ok, &bars[SB_IMG_READ + c % NI], ((c / NI) & 1) ^ 1, p.err);
+                if (!TRANS) prep_wait(ok, &bars[SB_IMG_READ + c % NI], ((c / NI) & 1) ^ 1, p.err);
                 __syncwarp();
                 if (tc::elect_one()) {
-                    mbar_arrive_expect_tx(&bars[SB_IMG_FULL + c % NI], img_bytes<PLO>());
-                    bulk_load(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>(), img0 + c * img_step,
-                              img_bytes<PLO>(), &bars[SB_IMG_FULL + c % NI]);
-                    if (c + 1 < nc) tc::prefetch_bulk(img0 + (c + 1) * img_step, img_bytes<PLO>());
+                    unsigned char *img = sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>();
+                    const unsigned char *src = img0 + c * img_step;
+                    uint64_t *full = &bars[SB_IMG_FULL + c % NI];
+                    if (TRANS) {                           // M and the header
+                        mbar_arrive_expect_tx(full, IMG_PHI + IMG_HDR_BYTES);
+                        bulk_load(img, src, IMG_PHI, full);
+                        bulk_load(img + img_hdr<PLO>(), src + img_hdr<PLO>(), IMG_HDR_BYTES, full);
+                    } else {
+                        mbar_arrive_expect_tx(full, img_bytes<PLO>());
+                        bulk_load(img, src, img_bytes<PLO>(), full);
+                    }
+                    if (c + 1 < nc) tc::prefetch_bulk(src + img_step, TRANS ? IMG_PHI : img_bytes<PLO>());
                 }
                 __syncwarp();
             }
@@ -760,6 +876,61 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     if (warp == 0) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The segments' maps chained: the state that segment i + 1 of a sequence starts from replaces N of
+// segment i.  A block has eight columns of one sequence-head; thread (r, half) row r and
+// four of them.  FP32; the sequence's first segment gave its state itself.
+constexpr int JOIN_THREADS = 256;
+static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const DeltaParams p) {
+    __shared__ int32_t red[68];
+    __shared__ __align__(16) float S[128][8];
+    const int tid = threadIdx.x, r = tid >> 1, c4 = 4 * (tid & 1);
+    const int slices = p.V / 8, slice = int(blockIdx.x) % slices, nh = int(blockIdx.x) / slices;
+    const int n = nh / p.H, h = nh - n * p.H;
+    pdl_launch_dependents();
+    pdl_wait();
+    // the sequence's first unit, and its units
+    int32_t u0 = 0, parts;
+    if (p.cu == nullptr) {
+        parts = max(1, (p.cpr + p.seg - 1) / p.seg);
+        u0 = n * parts;
+    } else {
+        for (int i = tid; i < n; i += JOIN_THREADS)
+            u0 += max(1, (nchunks<BT>(__ldg(p.cu + i), __ldg(p.cu + i + 1)) + p.seg - 1) / p.seg);
+        u0 = __reduce_add_sync(0xffffffffu, u0);
+        if ((tid & 31) == 0) red[tid >> 5] = u0;
+        __syncthreads();
+        u0 = 0;
+        for (int w = 0; w < JOIN_THREADS / 32; ++w) u0 += red[w];
+        parts = max(1, (nchunks<BT>(__ldg(p.cu + n), __ldg(p.cu + n + 1)) + p.seg - 1) / p.seg);
+    }
+    if (u0 < 0 || int64_t(u0) + parts > p.n_units) return;  // malformed cu_seqlens
+    const int64_t sz = int64_t(p.K) * p.V, tz = sz + int64_t(p.K) * p.K;
+    for (int i = 1; i < parts - 1; ++i) {
+        float *at = p.trans + (int64_t(u0 + i) * p.H + h) * tz, *prev = at - int64_t(p.H) * tz;
+        if (r < p.K)
+            *reinterpret_cast<float4 *>(&S[r][c4]) = *reinterpret_cast<const float4 *>(prev + int64_t(r) * p.V + 8 * slice + c4);
+        __syncthreads();
+        if (r < p.K) {
+            float4 *out = reinterpret_cast<float4 *>(at + int64_t(r) * p.V + 8 * slice + c4);
+            const float *m = at + sz + int64_t(r) * p.K;
+            float4 a = *out;
+#pragma unroll 4
+            for (int k = 0; k < p.K; k += 4) {
+                const float4 mk = *reinterpret_cast<const float4 *>(m + k);
+                const float mv[4] = {mk.x, mk.y, mk.z, mk.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 sk = *reinterpret_cast<const float4 *>(&S[k + j][c4]);
+                    a.x = fmaf(mv[j], sk.x, a.x); a.y = fmaf(mv[j], sk.y, a.y);
+                    a.z = fmaf(mv[j], sk.z, a.z); a.w = fmaf(mv[j], sk.w, a.w);
+                }
+            }
+            *out = a;
+        }
+        __syncthreads();
     }
 }
 

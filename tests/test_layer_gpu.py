@@ -244,6 +244,39 @@ def test_prefill_long_sequence_few_heads(kda):
     Rule([3000, 20], Hk=1, H=2, dtype=BF16, seed=17, rate=0.3).check(kda)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("K,V,gate", [(128, 128, "channel"), (64, 128, "head"), (128, 32, "channel"), (32, 96, "channel")])
+def test_prefill_split_sequences(kda, dtype, K, V, gate):
+    """Few heads and long sequences, which are walked in segments; short and empty ones among them."""
+    Rule([1500, 0, 700, 1, 64, 2111], Hk=1, H=2, K=K, V=V, gate=gate, dtype=dtype, seed=41, rate=0.03,
+         initial=True).check(kda, "packed")
+    Rule([1300, 1300], packed=False, Hk=1, H=1, K=K, V=V, gate=gate, dtype=dtype, seed=42, rate=0.5).check(kda, "dense")
+
+
+def test_prefill_split_sequences_with_slots(kda):
+    x = Rule([1200, 900, 0, 1000], dtype=F32, seed=43, rate=0.05)
+    pool = torch.randn(5, 2, 128, 128, device=DEV)
+    before = pool.clone()
+    slots = [3, -1, 1, 0]
+    x.state = torch.stack([before[s].cpu() if s >= 0 else torch.zeros(2, 128, 128) for s in slots])
+    wo, wS = x.want()
+    o, _ = kda.delta_prefill(*x.args(), cu_seqlens=x.cu.to(DEV), initial_state=pool,
+                             slots=torch.tensor(slots, dtype=torch.int32, device=DEV))
+    for n, (a, b) in enumerate(x.rows()):
+        close(o[0, a:b], wo[n], F32, f"o {n}")
+        if slots[n] >= 0:
+            close(pool[slots[n]], wS[n], F32, f"state {n}")
+    assert torch.equal(pool[2], before[2]) and torch.equal(pool[4], before[4])
+
+
+def test_prefill_many_sequences_of_any_order(kda):
+    """More sequences than are sorted by length, and fewer; long, short and empty ones mixed."""
+    rng = np.random.default_rng(5)
+    for n in (300, 90):
+        lens = rng.integers(0, 3, n) * rng.integers(0, 90, n)
+        Rule(lens, Hk=1, H=1, K=64, V=64, dtype=BF16, seed=44, initial=True).check(kda, f"{n} sequences")
+
+
 def test_prefill_continues(kda):
     """A prompt given in two calls, its state passed on, is the prompt given at once."""
     x = Rule([200], dtype=F32, seed=18)
