@@ -27,7 +27,7 @@ bool chunked_form(int64_t B, int64_t T, int32_t num_seqs) {
 
 // Chunks to a segment for this shape, 0 where sequences are not split, and a bound on the segments.
 // The model: a chunk of the walk takes 4 us, 3 without outputs; the first run has two walks to a
-// segment but the first's one and the last's none; the join takes 2 us a segment and the two more
+// segment but the first's one and the last's none; the join takes 3 us a segment and the two more
 // launches 10.  Sized for the 152 SMs of a GB300.
 int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_t &units) {
     const int64_t seqs = num_seqs > 0 ? num_seqs : B, heads = seqs * H, sms = 152;
@@ -39,7 +39,7 @@ int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_
     for (int P = 2; P <= 32 && heads < sms; ++P) {
         const int32_t s = int32_t(c / P + 0.999);
         if (s < 4) break;
-        const double t = waves((2 * P - 3) * heads) * s * 3.0 + waves(P * heads) * s * 4.0 + 2.0 * P + 10.0;
+        const double t = waves((2 * P - 3) * heads) * s * 3.0 + waves(P * heads) * s * 4.0 + 3.0 * P + 10.0;
         if (t < 0.95 * best) {
             best = t;
             seg = s;
@@ -162,7 +162,7 @@ size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t
     if (!chunked_form(B, T, num_seqs)) return 0;
     int64_t units = 0;
     const int32_t seg = segment_chunks(B, T, H, num_seqs, units);
-    return image_bytes(B, T, H, num_seqs) +
+    return image_bytes(B, T, H, num_seqs) + (num_seqs > 0 ? size_t(units) * sizeof(int4) : 0) +
            (seg > 0 ? size_t(units) * size_t(H) * size_t(K) * size_t(K + V) * sizeof(float) : 0);
 }
 
@@ -203,7 +203,7 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     }
     if (rows == 0 && state_out == nullptr) return KDA_OK;
     DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
-                  Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr, 0, 0, nullptr};
+                  Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr};
     if (!chunked_form(B, T, num_seqs)) return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
     p.cpr = int32_t((T + BT - 1) / BT);
     p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
@@ -211,7 +211,12 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     int64_t units = 0;
     p.seg = segment_chunks(B, T, H, num_seqs, units);
     p.n_units = int32_t(units);
-    p.trans = reinterpret_cast<float *>(p.ws + image_bytes(B, T, H, num_seqs));
+    unsigned char *after = p.ws + image_bytes(B, T, H, num_seqs);
+    if (num_seqs > 0) {
+        p.units = reinterpret_cast<int4 *>(after);
+        after += size_t(units) * sizeof(int4);
+    }
+    p.trans = reinterpret_cast<float *>(after);
     return run_chunked(p, dtype, int64_t(rows), static_cast<cudaStream_t>(stream));
 }
 
@@ -230,7 +235,7 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
                  size_t(num_slots) * size_t(H) * size_t(K) * size_t(V) * 4))
         return KDA_ERR_INVALID_ARGUMENT;
     const DeltaParams p{q, k, v, g, beta, o, state, state, slots, num_slots, nullptr, N, 1, Hk, H, K, V, gate, scale,
-                        nullptr, 0, 0, nullptr, 0, 0, nullptr};
+                        nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr};
     return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
 }
 

@@ -22,6 +22,7 @@ cudaError_t chunked_ready(int device) {
     cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, attr, prep_bytes<T>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, false>, attr, scan_bytes<T, PLO>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, true>, attr, scan_bytes<T, PLO>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_join_kernel, attr, JOIN_BYTES);
     done[device] = e == cudaSuccess;
     return e;
 }
@@ -31,17 +32,18 @@ cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const Del
                           cudaStream_t s) {
     cudaError_t e = chunked_ready<T, PLO, W128>(device);
     if (e != cudaSuccess) return e;
-    const unsigned grid = unsigned(p.n_tasks < sms ? p.n_tasks : sms), walks = unsigned(p.n_units) * unsigned(p.H);
+    auto blocks = [&](int64_t n) { return unsigned(n < sms ? n : sms); };     // persistent, one to an SM
+    const int64_t walks = int64_t(p.n_units) * p.H;
     const size_t bytes = size_t(scan_bytes<T, PLO>());
-    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, grid, PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
+    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, blocks(p.n_tasks), PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
     if (e == cudaSuccess && p.seg > 0) {
-        e = launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, true>, 2 * walks, SCAN_THREADS, bytes, s, scan, p);
+        e = launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, true>, blocks(2 * walks), SCAN_THREADS, bytes, s, scan, p);
         if (e == cudaSuccess)
-            e = launch_pdl(true, kda_delta_join_kernel, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / 8), JOIN_THREADS, 0,
-                           s, p);
+            e = launch_pdl(true, kda_delta_join_kernel, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / JOIN_COLS),
+                           JOIN_THREADS, size_t(JOIN_BYTES), s, p);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, false>, walks, SCAN_THREADS, bytes, s, scan, p);
+    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, false>, blocks(walks), SCAN_THREADS, bytes, s, scan, p);
 }
 
 // PLO: P and Q keep a low part (all types but bf16, whose rounding is above what it adds).

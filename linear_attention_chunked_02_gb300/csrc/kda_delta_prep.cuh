@@ -23,6 +23,7 @@
 // a lane had taken 50 of 320 us at 16 x 512 tokens x 64 heads).
 //
 // One persistent CTA of seven warpgroups per SM; every role walks the same chunk-heads:
+//   * warps 2 and 3 of the first CTA: the scan's list of segments, from cu_seqlens;
 //   * warp 0: MMA issue; warp 1: TMA loads of k, q and g in slices of 32 channels into a
 //     ring, swizzled so that both passes of the transform read them without conflicts;
 //   * warps 8-15 and 16-23 (transform): every second slice each.  First lane = channel, warp = eight
@@ -250,6 +251,63 @@ __device__ __forceinline__ void prep_wait(bool &ok, uint64_t *bar, uint32_t pari
     atomicOr(err, ERR_WAIT_TIMEOUT);
 }
 
+// The segments that the scan walks, {sequence, segment of it, chunks before the sequence, its
+// segments} each (the last is 0 past the end), from cu_seqlens by threads t = 0 .. 63.  Whole
+// sequences go longest first where there are at most SORTED of them, so that a
+// long one does not start last; segments stay in order.
+constexpr int PREP_SORTED = 128;
+__device__ __forceinline__ void list_units(const DeltaParams &p, int t) {
+    const int lane = t & 31;
+    if (p.seg == 0 && p.nseq <= PREP_SORTED) {
+#pragma unroll 1
+        for (int i = t; i < p.nseq; i += 64) {
+            const int32_t mine = max(0, p.cu[i + 1] - p.cu[i]);
+            int32_t rank = 0, before = 0, a = p.cu[0];
+#pragma unroll 1
+            for (int j = 0; j < p.nseq; ++j) {
+                const int32_t b = p.cu[j + 1], len = max(0, b - a);
+                rank += len > mine || (len == mine && j < i);
+                before += j < i ? (len + BT - 1) / BT : 0;
+                a = b;
+            }
+            p.units[rank] = make_int4(i, 0, before, 1);
+        }
+        return;
+    }
+    if (t >= 32) return;
+    // a lane has consecutive sequences; first their totals, then the entries
+    const int per = (p.nseq + 31) / 32, i0 = min(p.nseq, lane * per), i1 = min(p.nseq, i0 + per);
+    int32_t units = 0, chunks = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            const int32_t nc = nchunks<BT>(p.cu[i], p.cu[i + 1]), nu = p.seg > 0 ? max(1, (nc + p.seg - 1) / p.seg) : 1;
+            if (pass == 1)
+                for (int j = 0; j < nu; ++j)
+                    if (units + j < p.n_units) p.units[units + j] = make_int4(i, j, chunks, nu);
+            units += nu;
+            chunks += nc;
+        }
+        if (pass == 0) {
+            int32_t su = units, sc = chunks;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t a = __shfl_up_sync(0xffffffffu, su, o), b = __shfl_up_sync(0xffffffffu, sc, o);
+                if (lane >= o) {
+                    su += a;
+                    sc += b;
+                }
+            }
+            const int32_t all = __shfl_sync(0xffffffffu, su, 31);
+            for (int32_t i = max(0, all) + lane; i < p.n_units; i += 32) p.units[i] = make_int4(0, 0, 0, 0);
+            units = su - units;
+            chunks = sc - chunks;
+            if (units < 0) return;                         // malformed cu_seqlens
+        }
+    }
+}
+
 template <typename T, bool PLO>
 __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
@@ -299,9 +357,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    // registers: 896 threads of 72 at launch; 24 + 112 + 4 * 64 + 112 <= 7 * 72
+    // registers: 896 threads of 72 at launch; 32 + 104 + 4 * 64 + 112 <= 7 * 72
     if (warp < 4) {
-        tc::fewer_registers<24>();
+        tc::fewer_registers<32>();
         if (warp == 0) {
             // ------------------------------------------------------------- MMA issue
             TaskWalk w(ps, blockIdx.x, G);
@@ -362,6 +420,8 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             for (int tg = 0; tg < 2; ++tg)
                 for (uint32_t i = turn[tg] > NST ? turn[tg] - NST : 0; i < turn[tg]; ++i)
                     prep_wait(ok, &bars[PB_ST_FULL + tg * NST + i % NST], (i / NST) & 1, p.err);
+        } else if (blockIdx.x == 0 && p.cu != nullptr) {
+            list_units(ps, tid - 64);
         }
     } else if (warp >= 8 && warp < 24) {
         tc::fewer_registers<64>();
@@ -494,7 +554,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             }
         }
     } else if (warp < 8) {
-        tc::more_registers<112>();
+        tc::more_registers<104>();
         // --------------------------------------------------------------- epilogue
         const bool isP = warp >= 6;
         const int i = 32 * (warp & 1) + lane;              // chunk row

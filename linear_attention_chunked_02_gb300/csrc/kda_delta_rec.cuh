@@ -42,6 +42,7 @@ struct DeltaParams {
     int32_t seg;                // chunks to a segment of a sequence; 0: sequences are not split
     int32_t n_units;            // bound on segments (seg == 0: sequences)
     float *trans;               // [n_units][H]{N [K, V], M [K, K]}: what a segment does to the state
+    int4 *units;                // packed: [n_units] segments (kda_delta_prep.cuh writes them)
 };
 
 // State entry of sequence n, or -1 for none.

@@ -34,7 +34,9 @@
 // kda_delta_join_kernel chains them into every segment's initial state; then all
 // segments are walked at once.
 //
-// One CTA of eight warpgroups per sequence-head (registers moved to the chain):
+// One persistent CTA of eight warpgroups per SM, whose roles go through its walks (sequence-heads, or
+// their segments) as one stream of chunks: the loads and operands of the next walk
+// are under way while the chain ends one.  Registers are moved to the chain.
 //   * warps 0-15 (chain): four warps to each lane quarter, a quarter of the columns each; S in
 //     registers.  What bounds the walk is their path from state to state, so all
 //     else is on other warps;
@@ -59,8 +61,7 @@ constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY =
               SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_IMG_READ = 20,
               SB_GAM = 22, SCAN_NBARS = 24;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
-constexpr int SCAN_OFF_RED = 256;                  // a word to a warp: chunks before the sequence
-constexpr int SCAN_OFF_GAM = 640;                  // [2][128] e^{G_C}
+constexpr int SCAN_OFF_GAM = 256;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [4 parts][128 lanes] largest |S|
 constexpr int SCAN_OFF_VMAX = SCAN_OFF_MAX + 4 * 128 * 4;      // [4 parts][128 lanes] largest |v|
 constexpr int SCAN_OFF_OUT = SCAN_OFF_VMAX + 4 * 128 * 4;          // [2][128 lanes] inverse scales of S and U for O
@@ -84,7 +85,7 @@ template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
 template <typename T, bool PLO>
 constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
-static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_RED && SCAN_OFF_RED + 68 * 4 <= SCAN_OFF_GAM && 2 * 128 >= 256, "header fits");
+static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
 static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
@@ -221,79 +222,6 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
     }
 }
 
-// Which segment of which sequence the CTA has, and the chunks before that sequence.
-struct Unit {
-    int32_t n, part, before, parts;        // parts == 0: none
-};
-constexpr int SCAN_SORT = 256;             // packed batches of up to this many sequences go longest first
-
-// Unit u, by all threads of the CTA; `red` and `len` are shared memory of 68 and SCAN_SORT words.
-__device__ __forceinline__ Unit scan_unit(const DeltaParams &p, int32_t u, int32_t *red, int32_t *len) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (p.cu == nullptr) {
-        const int32_t parts = p.seg > 0 ? max(1, (p.cpr + p.seg - 1) / p.seg) : 1, n = u / parts;
-        return {n, u - n * parts, n * p.cpr, n < p.nseq ? parts : 0};
-    }
-    if (p.seg == 0 && p.nseq <= SCAN_SORT) {
-        // the u-th longest sequence (equal ones in their order): the long walks start first
-        if (tid < p.nseq) len[tid] = max(0, __ldg(p.cu + tid + 1) - __ldg(p.cu + tid));
-        __syncthreads();
-        if (tid < p.nseq) {
-            int rank = 0;
-            const int mine = len[tid];
-            for (int j = 0; j < p.nseq; ++j) rank += len[j] > mine || (len[j] == mine && j < tid);
-            if (rank == u) red[0] = tid;
-        }
-        __syncthreads();
-        const int32_t n = red[0];
-        int32_t before = 0;
-        for (int j = 0; j < n; ++j) before += (len[j] + BT - 1) / BT;
-        return {n, 0, before, 1};
-    }
-    int32_t units = 0, chunks = 0;          // of the sequences before this tile of 1024
-    for (int32_t base = 0; base < p.nseq; base += SCAN_THREADS) {
-        const int32_t i = base + tid;
-        const int32_t nc = i < p.nseq ? nchunks<BT>(__ldg(p.cu + i), __ldg(p.cu + i + 1)) : 0;
-        const int32_t nu = i < p.nseq ? (p.seg > 0 ? max(1, (nc + p.seg - 1) / p.seg) : 1) : 0;
-        int32_t su = nu, sc = nc;           // inclusive sums over the warp, then over the warps
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t a = __shfl_up_sync(0xffffffffu, su, o), b = __shfl_up_sync(0xffffffffu, sc, o);
-            if (lane >= o) {
-                su += a;
-                sc += b;
-            }
-        }
-        if (lane == 31) {
-            red[warp] = su;
-            red[32 + warp] = sc;
-        }
-        if (tid == 0) red[64] = -1;
-        __syncthreads();
-        int32_t all_u = 0, all_c = 0;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) {
-                su += red[w];
-                sc += red[32 + w];
-            }
-            all_u += red[w];
-            all_c += red[32 + w];
-        }
-        if (nu > 0 && u >= units + su - nu && u < units + su) {
-            red[64] = i;
-            red[65] = u - (units + su - nu);
-            red[66] = chunks + sc - nc;
-            red[67] = nu;
-        }
-        __syncthreads();
-        if (red[64] >= 0) return {red[64], red[65], red[66], red[67]};
-        __syncthreads();
-        units += all_u;
-        chunks += all_c;
-    }
-    return {0, 0, 0, 0};
-}
-
 // W128: K and V are 128, which makes every row pitch on chip an immediate.
 template <typename T, bool PLO, bool W128, bool TRANS>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
@@ -301,14 +229,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SCAN_OFF_TMEM);
-    int32_t *red = reinterpret_cast<int32_t *>(sm + SCAN_OFF_RED);
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
     constexpr int NI = scan_nimg<PLO>();
     constexpr bool STAGED = sizeof(T) == 2;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    // TRANS: even CTAs take N, odd ones M
-    const int run = TRANS ? int(blockIdx.x) & 1 : 0, index = TRANS ? int(blockIdx.x) >> 1 : int(blockIdx.x);
-    const int u = index / p.H, h = index - u * p.H;
     const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
 
@@ -323,43 +247,50 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         tc::tmem_alloc(smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
-    const Unit unit = scan_unit(p, u, red, reinterpret_cast<int32_t *>(gam));
-    const int n = unit.n;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // rows of this unit, and its chunks from `before` on
-    int64_t ra = 0, rb = 0;
-    if (unit.parts > 0) sequence_rows(p, n, ra, rb);
-    const int32_t first = unit.part * p.seg, before = unit.before + first;
-    const bool last = unit.part == unit.parts - 1;
-    ra += int64_t(64) * first;
-    if (p.seg > 0 && rb - ra > int64_t(64) * p.seg) rb = ra + int64_t(64) * p.seg;
-    const int rows = rb > ra ? int(rb - ra) : 0;
-    int nc = (rows + BT - 1) / BT;
-    // malformed cu_seqlens must not lead past the workspace; the last segment's map is not needed,
-    // nor what the first makes of another state than its own
-    if (before < 0 || (int64_t(before) + nc) * p.H > p.n_tasks) nc = 0;
-    const bool idle = unit.parts == 0 || (TRANS && (last || (run == 1 && unit.part == 0)));
-    if (idle) nc = 0;
-    // states: where the walk starts from and where it ends
-    const float *from = nullptr;
-    float *to = nullptr;
-    if (!idle) {
-        const int32_t e = state_entry(p, n);
-        const int64_t sz = int64_t(K) * V, tz = sz + int64_t(K) * K;
-        float *mine = p.trans + (int64_t(u) * p.H + h) * tz;
-        if (unit.part == 0) {
-            if (p.state_in != nullptr && e >= 0) from = p.state_in + (int64_t(e) * p.H + h) * sz;
-        } else if (!TRANS) {
-            from = mine - int64_t(p.H) * tz;               // chained into the segment before
-        }
-        if (TRANS) to = mine + (run == 1 ? sz : 0);
-        else if (last && p.state_out != nullptr && e >= 0) to = p.state_out + (int64_t(e) * p.H + h) * sz;
-    }
-    const int W = run == 1 ? K : V;                        // columns of the state that is walked
-    const unsigned char *img0 = p.ws + (int64_t(before) * p.H + h) * img_bytes<PLO>();
+    // walk w: unit w / H (TRANS: w / 2 / H, for N where w is even and for M where it is odd)
+    const int32_t walks = p.n_units * p.H * (TRANS ? 2 : 1);
+    auto entry = [&](int32_t w) {
+        if (w >= walks) return make_int4(0, 0, 0, 0);
+        const int32_t u = (TRANS ? w >> 1 : w) / p.H;
+        if (p.cu != nullptr) return __ldg(p.units + u);
+        const int32_t parts = p.seg > 0 ? (p.cpr + p.seg - 1) / p.seg : 1, n = u / parts;
+        return make_int4(n, u - n * parts, n * p.cpr, parts);
+    };
+    struct Walk1 {
+        int32_t w, h, run, rows, nc, row;  // run 1: M; first row
+        int4 e;
+        int32_t before;                    // chunks before the first
+        bool idle, last;
+    };
+    auto walk_at = [&](int32_t w, const int4 &e) {
+        Walk1 x;
+        x.w = w;
+        x.e = e;
+        const int32_t i = TRANS ? w >> 1 : w, u = i / p.H;
+        x.h = i - u * p.H;
+        x.run = TRANS ? w & 1 : 0;
+        int64_t a = 0, b = 0;
+        if (e.w > 0) sequence_rows(p, e.x, a, b);
+        x.last = e.y == e.w - 1;
+        a += int64_t(64) * e.y * p.seg;
+        if (p.seg > 0 && b - a > int64_t(64) * p.seg) b = a + int64_t(64) * p.seg;
+        x.rows = b > a ? int(b - a) : 0;
+        x.row = int(a);
+        x.nc = (x.rows + BT - 1) / BT;
+        x.before = e.z + e.y * p.seg;
+        // malformed cu_seqlens must not lead past the workspace; the last segment's map is not
+        // needed, nor what the first makes of another state than its own
+        if (x.before < 0 || (int64_t(x.before) + x.nc) * p.H > p.n_tasks) x.nc = 0;
+        x.idle = w >= walks || e.w <= 0 || (TRANS && (x.last || (x.run == 1 && e.y == 0)));
+        if (x.idle) x.nc = 0;
+        return x;
+    };
+    auto image_at = [&](const Walk1 &x) { return p.ws + (int64_t(x.before) * p.H + x.h) * img_bytes<PLO>(); };
+    const int32_t w0 = blockIdx.x, wstep = gridDim.x;
     const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
     const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
@@ -389,19 +320,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             __syncwarp();
             tc::fence_after_sync();
         };
-        const bool mine = v < W;
         float S[32];                                       // S[32 part + i][v]
         const bool held = 32 * part < K;                   // K is a multiple of 32
-        {
-            const float *sp = from + int64_t(32 * part) * W + v;
-            const bool read = from != nullptr && mine && held;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * W] : 0.f;
-            if (run == 1) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[i] = 32 * part + i == v && held ? 1.f : 0.f;
-            }
-        }
         const int t0 = 16 * part;                          // this thread's tokens of a chunk: t0 .. t0 + 15
         T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (v < V ? v : 0);
         const uint32_t sop = tq + TM_SHI + 16 * part, rop = tq + TM_RHI + 8 * part;      // operand columns, hi parts
@@ -420,17 +340,49 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             for (int i = 0; i < 32; i += 2) m = max3(m, S[i], S[i + 1]);
             return m;
         };
+        const int64_t sz = int64_t(K) * V, tz = sz + int64_t(K) * K;
+        uint32_t cc = 0, vc = 0;                           // chunks so far, and those with values
+        int4 next = entry(w0);
+        for (int32_t w = w0; w < walks; w += wstep) {
+        const Walk1 x = walk_at(w, next);
+        next = entry(w + wstep);
+        const int run = x.run, W = run == 1 ? K : V;       // columns of the state that is walked
+        const bool mine = v < W && held;
+        // the state that it starts from, and where it ends
+        float *to = nullptr;
+        {
+            const float *from = nullptr;
+            if (!x.idle) {
+                const int32_t e = state_entry(p, x.e.x);
+                float *map = p.trans + (int64_t((TRANS ? w >> 1 : w) / p.H) * p.H + x.h) * tz;
+                if (x.e.y > 0) {
+                    if (!TRANS) from = map - int64_t(p.H) * tz;        // chained into the segment before
+                } else if (p.state_in != nullptr && e >= 0) {
+                    from = p.state_in + (int64_t(e) * p.H + x.h) * sz;
+                }
+                if (TRANS) to = map + (run == 1 ? sz : 0);
+                else if (x.last && p.state_out != nullptr && e >= 0) to = p.state_out + (int64_t(e) * p.H + x.h) * sz;
+            }
+            const float *sp = from + int64_t(32 * part) * W + v;
+            const bool read = from != nullptr && mine;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * W] : 0.f;
+            if (run == 1) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i] = 32 * part + i == v && held ? 1.f : 0.f;
+            }
+        }
         float bS = 0.f, invS = 1.f;
-        if (nc > 0) {
+        if (x.nc > 0) {
             bS = lane_max(smax, state_max());
             put_state(pow2_scale(bS, VS_LO, VS_HI, invS));
             release(SB_S);
         }
-        for (int c = 0; c < nc; ++c) {
-            const uint32_t ph = c & 1;
-            const int left = rows - 64 * c;
+        for (int c = 0; c < x.nc; ++c, ++cc) {
+            const uint32_t ph = cc & 1;
+            const int left = x.rows - 64 * c;
             if (run == 0) {
-                prep_wait(ok, &bars[SB_V_FULL], ph, p.err);
+                prep_wait(ok, &bars[SB_V_FULL], vc++ & 1, p.err);
                 // rows past the end hold the next request's; columns past V stay in their lanes
                 for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
                     if (v < V) sv[i * V] = T(0.f);
@@ -452,8 +404,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < 16; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
             }
             bv = lane_max(svmax, bv);
-            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
-            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
+            prep_wait(ok, &bars[SB_IMG_FULL + cc % NI], (cc / NI) & 1, p.err);
+            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>() +
                                                                img_hdr<PLO>());
             const float minv = hdr[HDR_MINV + (part >> 1)], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
             const float kmax = hdr[HDR_KMAX];
@@ -467,12 +419,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // (M and N come without outputs, and are as good as the state that goes in)
             bool weak = !TRANS && __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
             if (weak) {                                    // the same in the four warps of the quarter
-                prep_wait(ok, &bars[SB_GAM + ph], (c >> 1) & 1, p.err);
+                prep_wait(ok, &bars[SB_GAM + ph], (cc >> 1) & 1, p.err);
                 float gmax = 0.f;
                 for (int i = 0; i < K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
                 weak = __all_sync(0xffffffffu, gmax < SCAN_WEAK_G);
                 if (weak) {
-                    scan_tokens<T>(p, S, ra + 64 * c, left < 64 ? left : 64, h, part, v, quarter,
+                    scan_tokens<T>(p, S, x.row + 64 * c, left < 64 ? left : 64, x.h, part, v, quarter,
                                    reinterpret_cast<float *>(sm + SCAN_OFF_SUM));
                     sS = pow2_scale(lane_max(smax, state_max()), VS_LO, VS_HI, invS1);     // the new state's own bound
                 }
@@ -497,8 +449,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 tc::st8(rop, hi);
                 tc::st8(rop + TM_RLO - TM_RHI, lo);
             }
+            if (left < 64) fence_proxy_async();            // zeros written into v's tile, before the next copy there
             release(SB_R);
-            if (lane == 0) mbar_arrive(&bars[SB_V_EMPTY]);
+            if (run == 0 && lane == 0) mbar_arrive(&bars[SB_V_EMPTY]);
             // U = M R
             accumulator(SB_D2, ph);
             {
@@ -509,11 +462,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             release(SB_U);
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
-            prep_wait(ok, &bars[SB_GAM + ph], (c >> 1) & 1, p.err);
+            prep_wait(ok, &bars[SB_GAM + ph], (cc >> 1) & 1, p.err);
             accumulator(SB_D3, ph);
+            const bool more = c + 1 < x.nc;                // the next walk puts its own state
             float mx = 0.f;
             if (weak) {                                    // S is there
-                put_state(sS);
+                if (more) put_state(sS);
                 mx = state_max();
             } else if (held) {                             // channels past K stay zero
                 const float2 f = both(invU * invk);
@@ -531,17 +485,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         S[16 * b + i] = x[i] = w.x;
                         S[16 * b + i + 1] = x[i + 1] = w.y;
                     }
-                    put_operand(sop + 8 * b, sop + TM_SLO - TM_SHI + 8 * b, x, sS);
+                    if (more) put_operand(sop + 8 * b, sop + TM_SLO - TM_SHI + 8 * b, x, sS);
                 }
             }
-            release(SB_S);
-            bS = lane_max(smax, mx);
-            invS = invS1;
+            if (more) {
+                release(SB_S);
+                bS = lane_max(smax, mx);
+                invS = invS1;
+            }
         }
-        if (to != nullptr && mine && held) {
+        if (to != nullptr && mine) {
             float *sp = to + int64_t(32 * part) * W + v;
 #pragma unroll
             for (int i = 0; i < 32; ++i) sp[int64_t(i) * W] = S[i];
+        }
         }
     } else if (warp < 24) {
         // (64 registers, as at launch)
@@ -550,17 +507,23 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         using W2 = Two<T>;
         using raw = typename W2::raw;
         const int rg = warp - 16;                          // rows 8 rg .. + 7
-        const int hk = h / (p.H / p.Hk);
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
         // the next one.  Channels past K take another's values under a scale of zero.
         const int ks = STAGED ? K : p.Hk * K, gs = STAGED ? K : p.H * K;
         unsigned char *st = sm + scan_off_st<T, PLO>();
         float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
-        for (int c = 0; c < nc; ++c) {
-            const uint32_t ph = c & 1;
-            const int left = rows - 64 * c - 8 * rg;       // live rows from this thread's first on
-            const int64_t row = ra + 64 * c + 8 * rg;
+        uint32_t cc = 0;
+        int4 next = entry(w0);
+        for (int32_t w = w0; w < walks; w += wstep) {
+        const Walk1 wk = walk_at(w, next);
+        next = entry(w + wstep);
+        const int h = wk.h, hk = h / (p.H / p.Hk);
+        const unsigned char *img0 = image_at(wk);
+        for (int c = 0; c < wk.nc; ++c, ++cc) {
+            const uint32_t ph = cc & 1;
+            const int left = wk.rows - 64 * c - 8 * rg;    // live rows from this thread's first on
+            const int64_t row = wk.row + 64 * c + 8 * rg;
             const T *kp, *qp;
             const float *gp;
             if (STAGED) {
@@ -693,6 +656,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             named_sync<1, 256>();                          // the sums are consumed
         }
+        }
     } else if (warp < 28) {
         tc::fewer_registers<40>();
         // ----------------------------------------------------------------- output
@@ -705,25 +669,30 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         uint32_t off[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) off[i] = v * sizeof(T) + i * step;
-        unsigned char *const ob = static_cast<unsigned char *>(p.o) + (ra * p.H + h) * V * int64_t(sizeof(T));
-        for (int c = 0; !TRANS && c < nc; ++c) {
-            const uint32_t ph = c & 1;
+        uint32_t cc = 0;
+        int4 next = entry(w0);
+        for (int32_t w = w0; !TRANS && w < walks; w += wstep) {
+        const Walk1 wk = walk_at(w, next);
+        next = entry(w + wstep);
+        unsigned char *const ob = static_cast<unsigned char *>(p.o) + (int64_t(wk.row) * p.H + wk.h) * V * int64_t(sizeof(T));
+        for (int c = 0; c < wk.nc; ++c, ++cc) {
+            const uint32_t ph = cc & 1;
             // O = (scale Q e^G) S0 + P U
             prep_wait(ok, &bars[SB_U], ph, p.err);         // the chain's scales
             const float2 inv = sout[ph * 128 + v];
-            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>() +
+            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>() +
                                                                img_hdr<PLO>());
-            prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
+            prep_wait(ok, &bars[SB_IMG_FULL + cc % NI], (cc / NI) & 1, p.err);
             const float p0 = hdr[HDR_PINV], p1 = hdr[HDR_PINV + 1], qmax = hdr[HDR_QMAX];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ + c % NI]);
+            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ + cc % NI]);
             float invq;
             pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
             prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
             __syncwarp();
             tc::fence_after_sync();
             const bool weak = inv.x < 0.f;
-            const int left = mine && !weak ? rows - 64 * c : 0;
+            const int left = mine && !weak ? wk.rows - 64 * c : 0;
             const bool whole = __all_sync(0xffffffffu, left >= 64);
             const float2 f = both(inv.x * invq);
 #pragma unroll 1
@@ -753,6 +722,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[SB_O_EMPTY]);
         }
+        }
     } else {
         tc::fewer_registers<24>();
         if (warp == 28) {
@@ -762,7 +732,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const uint32_t id3 = nh == 2 ? SCAN_ID128 : SCAN_ID64;
             auto commit = [&](int b) { tc::commit(smem_u32(&bars[b])); };
             auto wait = [&](int b, uint32_t parity) { prep_wait(ok, &bars[b], parity, p.err); };
-            for (int c = 0; c < nc; ++c) {
+            uint32_t c = 0, end = 0;                       // chunks so far, and at the end of this walk
+            int4 next = entry(w0);
+            for (int32_t w = w0; w < walks; w += wstep) {
+            end += walk_at(w, next).nc;
+            next = entry(w + wstep);
+            for (; c < end; ++c) {
                 const uint32_t ph = c & 1;
                 const uint32_t img = smem_u32(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>());
                 wait(SB_KQ_FULL, ph);
@@ -808,67 +783,90 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 }
                 __syncwarp();
             }
+            }
         } else if (warp == 29) {
             // -------------------------------------------- loads of q, k and g (16-bit)
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
                 const uint32_t bytes = (TRANS ? 1 : 2) * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);
-                const int hk = h / (p.H / p.Hk);
-                for (int c = 0; c < nc; ++c) {
-                    prep_wait(ok, &bars[SB_ST_EMPTY], (c & 1) ^ 1, p.err);
-                    __syncwarp();
-                    if (tc::elect_one()) {
-                        mbar_arrive_expect_tx(&bars[SB_ST_FULL], bytes);
-                        tma_load_3d(st, &maps.k, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
-                        if (!TRANS) tma_load_3d(st + 16384, &maps.q, 0, hk, int(ra) + 64 * c, &bars[SB_ST_FULL]);
-                        if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, h, int(ra) + 64 * c, &bars[SB_ST_FULL]);
-                        if (c + 1 < nc) {                  // the next chunk's on their way to L2 meanwhile
-                            tc::prefetch_3d(&maps.k, 0, hk, int(ra) + 64 * c + 64);
-                            if (!TRANS) tc::prefetch_3d(&maps.q, 0, hk, int(ra) + 64 * c + 64);
-                            if (p.gate == 0) tc::prefetch_3d(&maps.g, 0, h, int(ra) + 64 * c + 64);
+                uint32_t cc = 0;
+                Walk1 wk = walk_at(w0, entry(w0));
+                for (int32_t w = w0; w < walks; w += wstep) {
+                    const Walk1 nx = walk_at(w + wstep, entry(w + wstep));
+                    const int hk = wk.h / (p.H / p.Hk);
+                    for (int c = 0; c < wk.nc; ++c, ++cc) {
+                        prep_wait(ok, &bars[SB_ST_EMPTY], (cc & 1) ^ 1, p.err);
+                        __syncwarp();
+                        if (tc::elect_one()) {
+                            const int r = wk.row + 64 * c;
+                            mbar_arrive_expect_tx(&bars[SB_ST_FULL], bytes);
+                            tma_load_3d(st, &maps.k, 0, hk, r, &bars[SB_ST_FULL]);
+                            if (!TRANS) tma_load_3d(st + 16384, &maps.q, 0, hk, r, &bars[SB_ST_FULL]);
+                            if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, wk.h, r, &bars[SB_ST_FULL]);
+                            // the next chunk's on their way to L2 meanwhile
+                            const bool more = c + 1 < wk.nc;
+                            if (more || nx.nc > 0) {
+                                const int pr = more ? r + 64 : nx.row, ph = more ? wk.h : nx.h, pk = ph / (p.H / p.Hk);
+                                tc::prefetch_3d(&maps.k, 0, pk, pr);
+                                if (!TRANS) tc::prefetch_3d(&maps.q, 0, pk, pr);
+                                if (p.gate == 0) tc::prefetch_3d(&maps.g, 0, ph, pr);
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    wk = nx;
                 }
-                if (nc > 0) prep_wait(ok, &bars[SB_ST_FULL], (nc - 1) & 1, p.err);
+                if (cc > 0) prep_wait(ok, &bars[SB_ST_FULL], (cc - 1) & 1, p.err);
             }
         } else if (warp == 30) {
             // --------------------------------------------------------- loads of v
-            for (int c = 0; run == 0 && c < nc; ++c) {
-                prep_wait(ok, &bars[SB_V_EMPTY], (c & 1) ^ 1, p.err);
-                __syncwarp();
-                if (tc::elect_one()) {
-                    mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * V * sizeof(T));
-                    tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, h, int(ra) + 64 * c, &bars[SB_V_FULL]);
-                    if (c + 1 < nc) tc::prefetch_3d(&maps.v, 0, h, int(ra) + 64 * c + 64);
+            uint32_t cc = 0;                               // chunks that have values
+            int4 next = entry(w0);
+            for (int32_t w = w0; w < walks; w += wstep) {
+                const Walk1 wk = walk_at(w, next);
+                next = entry(w + wstep);
+                for (int c = 0; wk.run == 0 && c < wk.nc; ++c, ++cc) {
+                    prep_wait(ok, &bars[SB_V_EMPTY], (cc & 1) ^ 1, p.err);
+                    __syncwarp();
+                    if (tc::elect_one()) {
+                        mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * V * sizeof(T));
+                        tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, wk.h, wk.row + 64 * c, &bars[SB_V_FULL]);
+                        if (c + 1 < wk.nc) tc::prefetch_3d(&maps.v, 0, wk.h, wk.row + 64 * c + 64);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-            if (run == 0 && nc > 0) prep_wait(ok, &bars[SB_V_FULL], (nc - 1) & 1, p.err);
+            if (cc > 0) prep_wait(ok, &bars[SB_V_FULL], (cc - 1) & 1, p.err);
         } else {
             // ------------------------------------------------- loads of M and P
-            for (int c = 0; c < nc; ++c) {
-                prep_wait(ok, &bars[SB_IMG_EMPTY + c % NI], ((c / NI) & 1) ^ 1, p.err);
-                if (!TRANS) prep_wait(ok, &bars[SB_IMG_READ + c % NI], ((c / NI) & 1) ^ 1, p.err);
-                __syncwarp();
-                if (tc::elect_one()) {
-                    unsigned char *img = sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>();
-                    const unsigned char *src = img0 + c * img_step;
-                    uint64_t *full = &bars[SB_IMG_FULL + c % NI];
-                    if (TRANS) {                           // M and the header
-                        mbar_arrive_expect_tx(full, IMG_PHI + IMG_HDR_BYTES);
-                        bulk_load(img, src, IMG_PHI, full);
-                        bulk_load(img + img_hdr<PLO>(), src + img_hdr<PLO>(), IMG_HDR_BYTES, full);
-                    } else {
-                        mbar_arrive_expect_tx(full, img_bytes<PLO>());
-                        bulk_load(img, src, img_bytes<PLO>(), full);
+            uint32_t cc = 0;
+            int4 next = entry(w0);
+            for (int32_t w = w0; w < walks; w += wstep) {
+                const Walk1 wk = walk_at(w, next);
+                next = entry(w + wstep);
+                const unsigned char *src = image_at(wk);
+                for (int c = 0; c < wk.nc; ++c, ++cc, src += img_step) {
+                    prep_wait(ok, &bars[SB_IMG_EMPTY + cc % NI], ((cc / NI) & 1) ^ 1, p.err);
+                    if (!TRANS) prep_wait(ok, &bars[SB_IMG_READ + cc % NI], ((cc / NI) & 1) ^ 1, p.err);
+                    __syncwarp();
+                    if (tc::elect_one()) {
+                        unsigned char *img = sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>();
+                        uint64_t *full = &bars[SB_IMG_FULL + cc % NI];
+                        if (TRANS) {                       // M and the header
+                            mbar_arrive_expect_tx(full, IMG_PHI + IMG_HDR_BYTES);
+                            bulk_load(img, src, IMG_PHI, full);
+                            bulk_load(img + img_hdr<PLO>(), src + img_hdr<PLO>(), IMG_HDR_BYTES, full);
+                        } else {
+                            mbar_arrive_expect_tx(full, img_bytes<PLO>());
+                            bulk_load(img, src, img_bytes<PLO>(), full);
+                        }
+                        if (c + 1 < wk.nc) tc::prefetch_bulk(src + img_step, TRANS ? IMG_PHI : img_bytes<PLO>());
                     }
-                    if (c + 1 < nc) tc::prefetch_bulk(src + img_step, TRANS ? IMG_PHI : img_bytes<PLO>());
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-            for (int c = nc > NI ? nc - NI : 0; c < nc; ++c)
-                prep_wait(ok, &bars[SB_IMG_FULL + c % NI], (c / NI) & 1, p.err);
+            for (uint32_t i = cc > NI ? cc - NI : 0; i < cc; ++i)
+                prep_wait(ok, &bars[SB_IMG_FULL + i % NI], (i / NI) & 1, p.err);
         }
     }
     tc::fence_before_sync();
@@ -880,14 +878,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 }
 
 // The segments' maps chained: the state that segment i + 1 of a sequence starts from replaces N of
-// segment i.  A block has eight columns of one sequence-head; thread (r, half) row r and
-// four of them.  FP32; the sequence's first segment gave its state itself.
-constexpr int JOIN_THREADS = 256;
+// segment i.  A block has 16 columns of one sequence-head; thread (r, half) row r and eight of
+// them.  FP32; the sequence's first segment gave its state itself.  M comes through shared memory, the
+// next one's copy under way during a product.
+constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 132;
+constexpr int JOIN_BYTES = 2 * 128 * JOIN_PITCH * 4;
 static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const DeltaParams p) {
-    __shared__ int32_t red[68];
-    __shared__ __align__(16) float S[128][8];
-    const int tid = threadIdx.x, r = tid >> 1, c4 = 4 * (tid & 1);
-    const int slices = p.V / 8, slice = int(blockIdx.x) % slices, nh = int(blockIdx.x) / slices;
+    extern __shared__ __align__(16) float join_m[];
+    __shared__ int32_t red[8];
+    __shared__ __align__(16) float S[128][JOIN_COLS];
+    const int tid = threadIdx.x, r = tid >> 1, c8 = 8 * (tid & 1);
+    const int slices = p.V / JOIN_COLS, slice = int(blockIdx.x) % slices, nh = int(blockIdx.x) / slices;
     const int n = nh / p.H, h = nh - n * p.H;
     pdl_launch_dependents();
     pdl_wait();
@@ -908,30 +909,56 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
     }
     if (u0 < 0 || int64_t(u0) + parts > p.n_units) return;  // malformed cu_seqlens
     const int64_t sz = int64_t(p.K) * p.V, tz = sz + int64_t(p.K) * p.K;
-    for (int i = 1; i < parts - 1; ++i) {
-        float *at = p.trans + (int64_t(u0 + i) * p.H + h) * tz, *prev = at - int64_t(p.H) * tz;
-        if (r < p.K)
-            *reinterpret_cast<float4 *>(&S[r][c4]) = *reinterpret_cast<const float4 *>(prev + int64_t(r) * p.V + 8 * slice + c4);
-        __syncthreads();
-        if (r < p.K) {
-            float4 *out = reinterpret_cast<float4 *>(at + int64_t(r) * p.V + 8 * slice + c4);
-            const float *m = at + sz + int64_t(r) * p.K;
-            float4 a = *out;
-#pragma unroll 4
-            for (int k = 0; k < p.K; k += 4) {
-                const float4 mk = *reinterpret_cast<const float4 *>(m + k);
-                const float mv[4] = {mk.x, mk.y, mk.z, mk.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 sk = *reinterpret_cast<const float4 *>(&S[k + j][c4]);
-                    a.x = fmaf(mv[j], sk.x, a.x); a.y = fmaf(mv[j], sk.y, a.y);
-                    a.z = fmaf(mv[j], sk.z, a.z); a.w = fmaf(mv[j], sk.w, a.w);
-                }
+    float *map0 = p.trans + (int64_t(u0) * p.H + h) * tz;
+    const int k4 = p.K / 4;                                 // 16-byte pieces of a row of M
+    auto fetch = [&](int i) {
+        if (i < parts - 1) {
+            const float *m = map0 + int64_t(i) * p.H * tz + sz;
+            float *to = join_m + (i & 1) * 128 * JOIN_PITCH;
+            for (int j = tid; j < p.K * k4; j += JOIN_THREADS) {
+                const int row = j / k4, x = 4 * (j - row * k4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + row * JOIN_PITCH + x)),
+                             "l"(m + int64_t(row) * p.K + x) : "memory");
             }
-            *out = a;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (parts > 2 && r < p.K) {                             // the state after the first segment
+        const float4 *from = reinterpret_cast<const float4 *>(map0 + int64_t(r) * p.V + JOIN_COLS * slice + c8);
+        *reinterpret_cast<float4 *>(&S[r][c8]) = from[0];
+        *reinterpret_cast<float4 *>(&S[r][c8 + 4]) = from[1];
+    }
+    fetch(1);
+    for (int i = 1; i < parts - 1; ++i) {
+        fetch(i + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
+        float4 *out = reinterpret_cast<float4 *>(map0 + int64_t(i) * p.H * tz + int64_t(r) * p.V + JOIN_COLS * slice + c8);
+        if (r < p.K) {
+            a0 = out[0];
+            a1 = out[1];
+            const float *m = join_m + (i & 1) * 128 * JOIN_PITCH + r * JOIN_PITCH;
+#pragma unroll 4
+            for (int k = 0; k < p.K; ++k) {
+                const float mk = m[k];
+                const float4 s0 = *reinterpret_cast<const float4 *>(&S[k][c8]);
+                const float4 s1 = *reinterpret_cast<const float4 *>(&S[k][c8 + 4]);
+                a0.x = fmaf(mk, s0.x, a0.x); a0.y = fmaf(mk, s0.y, a0.y);
+                a0.z = fmaf(mk, s0.z, a0.z); a0.w = fmaf(mk, s0.w, a0.w);
+                a1.x = fmaf(mk, s1.x, a1.x); a1.y = fmaf(mk, s1.y, a1.y);
+                a1.z = fmaf(mk, s1.z, a1.z); a1.w = fmaf(mk, s1.w, a1.w);
+            }
         }
         __syncthreads();
+        if (r < p.K) {
+            out[0] = a0;
+            out[1] = a1;
+            *reinterpret_cast<float4 *>(&S[r][c8]) = a0;
+            *reinterpret_cast<float4 *>(&S[r][c8 + 4]) = a1;
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 }  // namespace kda
