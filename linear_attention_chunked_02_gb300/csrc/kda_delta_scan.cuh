@@ -878,8 +878,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 }
 
 // The segments' maps chained: the state that segment i + 1 of a sequence starts from replaces N of
-// segment i.  A block has 16 columns of one sequence-head; thread (r, half) row r and eight of
-// them.  FP32; the sequence's first segment gave its state itself.  M comes through shared memory, the
+// segment i.  A block has 16 columns of one sequence-head, a thread four of them in two rows.  FP32; the sequence's first segment gave its state itself.  M comes through shared memory, the
 // next one's copy under way during a product.
 constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 132;
 constexpr int JOIN_BYTES = 2 * 128 * JOIN_PITCH * 4;
@@ -887,7 +886,7 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
     extern __shared__ __align__(16) float join_m[];
     __shared__ int32_t red[8];
     __shared__ __align__(16) float S[128][JOIN_COLS];
-    const int tid = threadIdx.x, r = tid >> 1, c8 = 8 * (tid & 1);
+    const int tid = threadIdx.x, r = 2 * (tid >> 2), c = 4 * (tid & 3);
     const int slices = p.V / JOIN_COLS, slice = int(blockIdx.x) % slices, nh = int(blockIdx.x) / slices;
     const int n = nh / p.H, h = nh - n * p.H;
     pdl_launch_dependents();
@@ -923,39 +922,41 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    const int64_t at = int64_t(r) * p.V + JOIN_COLS * slice + c;
+    auto row = [&](int i, int j) { return reinterpret_cast<float4 *>(map0 + int64_t(i) * p.H * tz + at + int64_t(j) * p.V); };
     if (parts > 2 && r < p.K) {                             // the state after the first segment
-        const float4 *from = reinterpret_cast<const float4 *>(map0 + int64_t(r) * p.V + JOIN_COLS * slice + c8);
-        *reinterpret_cast<float4 *>(&S[r][c8]) = from[0];
-        *reinterpret_cast<float4 *>(&S[r][c8 + 4]) = from[1];
+        *reinterpret_cast<float4 *>(&S[r][c]) = *row(0, 0);
+        *reinterpret_cast<float4 *>(&S[r + 1][c]) = *row(0, 1);
     }
     fetch(1);
     for (int i = 1; i < parts - 1; ++i) {
         fetch(i + 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
-        float4 *out = reinterpret_cast<float4 *>(map0 + int64_t(i) * p.H * tz + int64_t(r) * p.V + JOIN_COLS * slice + c8);
+        float4 a[2];
         if (r < p.K) {
-            a0 = out[0];
-            a1 = out[1];
+            a[0] = *row(i, 0);
+            a[1] = *row(i, 1);
             const float *m = join_m + (i & 1) * 128 * JOIN_PITCH + r * JOIN_PITCH;
-#pragma unroll 4
-            for (int k = 0; k < p.K; ++k) {
-                const float mk = m[k];
-                const float4 s0 = *reinterpret_cast<const float4 *>(&S[k][c8]);
-                const float4 s1 = *reinterpret_cast<const float4 *>(&S[k][c8 + 4]);
-                a0.x = fmaf(mk, s0.x, a0.x); a0.y = fmaf(mk, s0.y, a0.y);
-                a0.z = fmaf(mk, s0.z, a0.z); a0.w = fmaf(mk, s0.w, a0.w);
-                a1.x = fmaf(mk, s1.x, a1.x); a1.y = fmaf(mk, s1.y, a1.y);
-                a1.z = fmaf(mk, s1.z, a1.z); a1.w = fmaf(mk, s1.w, a1.w);
+#pragma unroll 2
+            for (int k = 0; k < p.K; k += 4) {
+                const float4 m0 = *reinterpret_cast<const float4 *>(m + k), m1 = *reinterpret_cast<const float4 *>(m + JOIN_PITCH + k);
+                const float mk[2][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 s = *reinterpret_cast<const float4 *>(&S[k + j][c]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[e].x = fmaf(mk[e][j], s.x, a[e].x); a[e].y = fmaf(mk[e][j], s.y, a[e].y);
+                        a[e].z = fmaf(mk[e][j], s.z, a[e].z); a[e].w = fmaf(mk[e][j], s.w, a[e].w);
+                    }
+                }
             }
         }
         __syncthreads();
         if (r < p.K) {
-            out[0] = a0;
-            out[1] = a1;
-            *reinterpret_cast<float4 *>(&S[r][c8]) = a0;
-            *reinterpret_cast<float4 *>(&S[r][c8 + 4]) = a1;
+            *row(i, 0) = *reinterpret_cast<float4 *>(&S[r][c]) = a[0];
+            *row(i, 1) = *reinterpret_cast<float4 *>(&S[r + 1][c]) = a[1];
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
