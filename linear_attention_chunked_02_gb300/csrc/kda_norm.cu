@@ -29,7 +29,7 @@ struct NormParams {
     void *out;             // add: residual_out or nullptr
     int64_t rows;
     int32_t dim;
-    float alpha, eps;
+    float alpha, eps, inv_dim;
 };
 
 enum { NORM_ADD = 0, NORM_GATED_SIGMOID = 1, NORM_GATED_SILU = 2 };
@@ -43,6 +43,19 @@ template <typename T, int VEC>
 struct alignas(VEC * sizeof(T)) Raw {
     T v[VEC];
 };
+
+// VEC values rounded to the type, two at a time where there are two.
+template <typename T, int VEC>
+__device__ __forceinline__ void pack(Raw<T, VEC> &to, const float (&a)[VEC]) {
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+        uint32_t *u = reinterpret_cast<uint32_t *>(&to);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) u[e / 2] = pack2(a[e], a[e + 1], (T *)nullptr);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) put1(&to.v[e], a[e]);
+    }
+}
 
 // A row's elements on its group of threads: NV vectors of VEC elements to a thread, vector i
 // of thread t at element (i tpr + t) VEC.
@@ -92,17 +105,20 @@ struct NormRow {
             const int j = i * tpr + t;
             if (row >= p.rows || j >= nvec) continue;
             R y, s;
+            float a[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float a = r[i][e] * inv * to_f32(w[i].v[e]);
+                a[e] = r[i][e] * inv * to_f32(w[i].v[e]);
                 if (KIND != NORM_ADD) {
+                    // the fast quotient and exponential: a few units in the last place, and 0 for a gate
+                    // far below zero, where the divisor passes 2^126
                     const float g = to_f32(z[i].v[e]);
-                    const float sg = 1.f / (1.f + __expf(-g));
-                    a *= KIND == NORM_GATED_SILU ? g * sg : sg;
+                    const float sg = __fdividef(1.f, 1.f + __expf(-g));
+                    a[e] *= KIND == NORM_GATED_SILU ? g * sg : sg;
                 }
-                put1(&y.v[e], a);
-                if (KIND == NORM_ADD) put1(&s.v[e], r[i][e]);
             }
+            pack(y, a);
+            if (KIND == NORM_ADD) pack(s, r[i]);
             if (KIND == NORM_ADD && p.out != nullptr)
                 *reinterpret_cast<R *>(static_cast<T *>(p.out) + base + int64_t(j) * VEC) = s;
             *reinterpret_cast<R *>(static_cast<T *>(p.y) + base + int64_t(j) * VEC) = y;
@@ -119,12 +135,13 @@ __device__ __forceinline__ void load_weight(const NormParams &p, Raw<T, VEC> (&w
     }
 }
 
-constexpr int NORM_THREADS = 256;              // block of the narrow form
-
-// Narrow rows: `lanes` threads (a power of two up to 32) to a row, ROWS rows to a thread.  One row of
-// 128 bf16 values alone keeps 32 bytes of a thread in flight; with four, 8192 x 64 rows of a
-// gated norm took 92 -> 71 us (bound: 59 us of copies).
-template <typename T, int KIND, int VEC, int NV, int ROWS>
+// Narrow rows: `lanes` threads (a power of two up to 32) to a row, ROWS rows to a thread: one row of
+// 128 bf16 values alone keeps 32 bytes of a thread in flight.  Gated norm of 8192 x 64 rows of 128
+// (bound: 59 us of copies) with one, two, three and four rows to a thread: 73, 65, 63 and 64 us in
+// blocks of 128 threads, 72, 78, 67 and 72 us in blocks of 256; in FP32, half as many rows: 68, 58, 58
+// and 58 us in blocks of 128.
+constexpr int NORM_THREADS = 128, ROWS = 3;
+template <typename T, int KIND, int VEC, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) kda_norm_narrow_kernel(const NormParams p, const int lanes) {
     const int t = int(threadIdx.x) & (lanes - 1), groups = NORM_THREADS / lanes;
     const int64_t row0 = int64_t(blockIdx.x) * groups * ROWS + int(threadIdx.x) / lanes;
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(NORM_THREADS) kda_norm_narrow_kernel(const Nor
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
-        row[i].store(p, w, rsqrtf(ss[i] / float(p.dim) + p.eps), row0 + i * groups, t, lanes, nvec);
+        row[i].store(p, w, rsqrtf(ss[i] * p.inv_dim + p.eps), row0 + i * groups, t, lanes, nvec);
 }
 
 // Wide rows: one to a block.
@@ -167,13 +184,13 @@ __global__ void __launch_bounds__(1024) kda_norm_wide_kernel(const NormParams p)
     ss = (t & 31) < (tpr >> 5) ? part[t & 31] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    row.store(p, w, rsqrtf(ss / float(p.dim) + p.eps), blockIdx.x, t, tpr, nvec);
+    row.store(p, w, rsqrtf(ss * p.inv_dim + p.eps), blockIdx.x, t, tpr, nvec);
 }
 
-template <typename T, int KIND, int VEC, int NV, int ROWS>
+template <typename T, int KIND, int VEC, int NV>
 cudaError_t launch_narrow(const NormParams &p, int lanes, cudaStream_t s) {
     const int64_t per = int64_t(NORM_THREADS / lanes) * ROWS;
-    return launch_pdl(true, kda_norm_narrow_kernel<T, KIND, VEC, NV, ROWS>, unsigned((p.rows + per - 1) / per), NORM_THREADS,
+    return launch_pdl(true, kda_norm_narrow_kernel<T, KIND, VEC, NV>, unsigned((p.rows + per - 1) / per), NORM_THREADS,
                       0, s, p, lanes);
 }
 
@@ -184,11 +201,7 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
     if (nvec <= 64) {
         int lanes = 1;
         while (lanes < 32 && lanes < nvec) lanes *= 2;
-        // several rows to a thread once there are enough to fill the GPU with them
-        const bool many = p.rows * lanes >= int64_t(1) << 20;
-        if (nvec > 32)
-            return many ? launch_narrow<T, KIND, VEC, 2, 2>(p, lanes, s) : launch_narrow<T, KIND, VEC, 2, 1>(p, lanes, s);
-        return many ? launch_narrow<T, KIND, VEC, 1, 4>(p, lanes, s) : launch_narrow<T, KIND, VEC, 1, 1>(p, lanes, s);
+        return nvec > 32 ? launch_narrow<T, KIND, VEC, 2>(p, lanes, s) : launch_narrow<T, KIND, VEC, 1>(p, lanes, s);
     }
     // wider rows: one to a block, as few vectors to a thread as 1024 threads allow
     // (two from 256 vectors on: fewer, busier warps to sum over)
@@ -263,7 +276,7 @@ kda_status_t kda_add_norm(const void *x, const void *residual, const void *weigh
         (overlaps(residual_out, n, x, n) || overlaps(residual_out, n, y, n) || overlaps(residual_out, n, weight, wn) ||
          (residual != nullptr && residual_out != residual && overlaps(residual_out, n, residual, n))))
         return KDA_ERR_INVALID_ARGUMENT;
-    const NormParams p{x, residual, weight, y, residual_out, rows, dim, alpha, eps};
+    const NormParams p{x, residual, weight, y, residual_out, rows, dim, alpha, eps, 1.f / float(dim)};
     return run_norm(NORM_ADD, dtype, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -279,7 +292,7 @@ kda_status_t kda_gated_norm(const void *x, const void *gate, const void *weight,
         if (reinterpret_cast<uintptr_t>(q) % es != 0) return KDA_ERR_INVALID_ARGUMENT;
     if ((y != x && overlaps(y, n, x, n)) || (y != gate && overlaps(y, n, gate, n)) || overlaps(y, n, weight, wn))
         return KDA_ERR_INVALID_ARGUMENT;
-    const NormParams p{x, gate, weight, y, nullptr, rows, dim, 1.f, eps};
+    const NormParams p{x, gate, weight, y, nullptr, rows, dim, 1.f, eps, 1.f / float(dim)};
     return run_norm(act == KDA_ACT_SILU ? NORM_GATED_SILU : NORM_GATED_SIGMOID, dtype, p,
                     static_cast<cudaStream_t>(stream));
 }
