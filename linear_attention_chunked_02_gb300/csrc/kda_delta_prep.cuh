@@ -103,6 +103,7 @@ static_assert(prep_stage_bytes<float>() % 1024 == 0 && prep_stage_bytes<__half>(
                   prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
               "fits the shared memory of one CTA");
 constexpr uint32_t PREP_TM_D = 0, PREP_TM_A = 128; // accumulators [2][64], operands [PREP_NOPS]{hi 32, lo 32}
+constexpr uint32_t PREP_TM_FINE = 256;             // from an accumulator to its own for the small products
 
 // Tensor maps of q, k [rows, Hk, K] and g [rows, H, K] as {channels, heads, rows}: boxes of 32
 // channels x 64 rows here, swizzled over their row's bytes; of all channels (and of v's
@@ -308,6 +309,23 @@ __device__ __forceinline__ void list_units(const DeltaParams &p, int t) {
     }
 }
 
+// FP32 inputs need more of the TF32 products than 16-bit ones, whose own rounding is far above this:
+// the instruction cuts the operands that it reads and cuts its sums as it adds to them, so that all
+// parts err toward zero.  FINE rounds high and low parts to nearest, and gives the small products an
+// accumulator of their own (16 sums at the accumulator's full size for K = 128, not 48).  P, 64 tokens
+// of K = 128, against 64 bits: 1.5e-6 plain, 1.0e-6 with rounded parts, 3.6e-07 with both.
+template <typename T>
+constexpr bool prep_fine() { return sizeof(T) == 4; }
+template <bool FINE>
+__device__ __forceinline__ void prep_split(float2 v, uint32_t &h0, uint32_t &h1, uint32_t &l0, uint32_t &l1) {
+    if (!FINE) return split2(v, h0, h1, l0, l1);
+    h0 = (__float_as_uint(v.x) + 0x1000u) & 0xffffe000u;
+    h1 = (__float_as_uint(v.y) + 0x1000u) & 0xffffe000u;
+    const float2 lo = __fadd2_rn(v, make_float2(-__uint_as_float(h0), -__uint_as_float(h1)));
+    l0 = __float_as_uint(lo.x) + 0x1000u;
+    l1 = __float_as_uint(lo.y) + 0x1000u;
+}
+
 template <typename T, bool PLO>
 __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
@@ -381,8 +399,13 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
 #pragma unroll 1
                         for (int kk = 0; kk < 4; ++kk) {
                             tc::mma_tf32_ts(d, ta, dbh, KGB_IDESC, s > 0 || kk > 0);
-                            tc::mma_tf32_ts(d, ta, dbl, KGB_IDESC, true);
-                            tc::mma_tf32_ts(d, ta + 32, dbh, KGB_IDESC, true);
+                            if (prep_fine<T>()) {
+                                tc::mma_tf32_ts(d + PREP_TM_FINE, ta, dbl, KGB_IDESC, s > 0 || kk > 0);
+                                tc::mma_tf32_ts(d + PREP_TM_FINE, ta + 32, dbh, KGB_IDESC, true);
+                            } else {
+                                tc::mma_tf32_ts(d, ta, dbl, KGB_IDESC, true);
+                                tc::mma_tf32_ts(d, ta + 32, dbh, KGB_IDESC, true);
+                            }
                             ta += 8;
                             dbh += 2;
                             dbl += 2;
@@ -522,15 +545,15 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     uint32_t h[8], l[8];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2)
-                        split2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(E[i]), ex2(E[i + 1]))), h[i], h[i + 1],
-                               l[i], l[i + 1]);
+                        prep_split<prep_fine<T>()>(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(E[i]), ex2(E[i + 1]))), h[i],
+                                        h[i + 1], l[i], l[i + 1]);
                     tc::st8(ta + ob * 64 + 8 * b, h);
                     tc::st8(ta + ob * 64 + 32 + 8 * b, l);
                     if (!isQ) {
 #pragma unroll
                         for (int i = 0; i < 8; i += 2)
-                            split2(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(-E[i]), ex2(-E[i + 1]))), h[i],
-                                   h[i + 1], l[i], l[i + 1]);
+                            prep_split<prep_fine<T>()>(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ex2(-E[i]), ex2(-E[i + 1]))),
+                                            h[i], h[i + 1], l[i], l[i + 1]);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             unsigned char *at = br + 16 * ((4 * half + 2 * b + j) ^ (row & 7));
@@ -634,7 +657,15 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             // columns 8 b .. of this row, masked by selects: what they drop may hold anything
             auto columns = [&](int b, float (&x)[8]) {
                 tc::ld8(td + 8 * b, x);
-                tc::wait_ld();
+                if (prep_fine<T>()) {
+                    float y[8];
+                    tc::ld8(td + PREP_TM_FINE + 8 * b, y);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] += y[e];
+                } else {
+                    tc::wait_ld();
+                }
                 const int end = i < m.n ? last - 8 * b : -1;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = e <= end ? x[e] * f : 0.f;
