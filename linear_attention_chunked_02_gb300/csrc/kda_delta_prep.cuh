@@ -313,7 +313,7 @@ __device__ __forceinline__ void list_units(const DeltaParams &p, int t) {
 // the instruction cuts the operands that it reads and cuts its sums as it adds to them, so that all
 // parts err toward zero.  FINE rounds high and low parts to nearest, and gives the small products an
 // accumulator of their own (16 sums at the accumulator's full size for K = 128, not 48).  P, 64 tokens
-// of K = 128, against 64 bits: 1.5e-6 plain, 1.0e-6 with rounded parts, 3.6e-07 with both.
+// of K = 128, against 64 bits: 1.0e-6 with rounded parts alone, 3.6e-7 with both.
 template <typename T>
 constexpr bool prep_fine() { return sizeof(T) == 4; }
 template <bool FINE>

@@ -25,28 +25,33 @@ ACT_CODE = {"sigmoid": 0, "silu": 1}
 _NO_CONTEXT = contextlib.nullcontext()
 
 
-def _launch_on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+def _launch_on(device: int, stream: Optional[torch.cuda.Stream]):
     """Context in which `device` is current and, if given, `stream` is its current stream."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return _NO_CONTEXT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NO_CONTEXT if device == torch.cuda.current_device() else torch.cuda.device(device)
 
 
-def _current_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _current_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _on_gpu(names: str, *tensors) -> torch.device:
-    """The device of the tensors (named in `names`; None ones are skipped), which must be one GPU."""
-    device = tensors[0].device
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{names.split()[i]} is on {t.device}, {names.split()[0]} on {device}")
+def _on_gpu(names: str, *tensors) -> int:
+    """The device index of the tensors (named in `names`; None ones are skipped), which must be on one GPU."""
+    device = tensors[0].get_device()                       # one integer a tensor; -1 on the CPU
+    for t in tensors:
+        if t is not None and (t.get_device() != device or not t.is_cuda):
+            _refuse_devices(names, tensors)
     return device
+
+
+def _refuse_devices(names: str, tensors) -> None:
+    for name, t in zip(names.split(), tensors):
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    for name, t in zip(names.split(), tensors):
+        if t is not None and t.device != tensors[0].device:
+            raise ValueError(f"{name} is on {t.device}, {names.split()[0]} on {tensors[0].device}")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -62,22 +67,24 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 
 def _rule_shapes(q, k, v, g, beta, lead: int):
     """Checks of the token tensors, which have `lead` leading dimensions; (Hk, H, K, V, gate code)."""
-    if q.dim() != lead + 2 or v.dim() != lead + 2 or k.shape != q.shape or q.shape[:lead] != v.shape[:lead]:
-        raise ValueError(f"shapes q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
-    Hk, K = q.shape[lead:]
-    H, V = v.shape[lead:]
+    qs, vs, gs = q.shape, v.shape, g.shape
+    if len(qs) != lead + 2 or len(vs) != lead + 2 or k.shape != qs or qs[:lead] != vs[:lead]:
+        raise ValueError(f"shapes q {tuple(qs)}, k {tuple(k.shape)}, v {tuple(vs)} do not match")
+    Hk, K = qs[-2:]
+    H, V = vs[-2:]
     if K not in WIDTHS or V not in WIDTHS:
         raise ValueError(f"K and V must be among {WIDTHS}, got {K} and {V}")
     if Hk < 1 or H < 1 or H % Hk != 0:
         raise ValueError(f"{H} heads cannot share {Hk} key heads")
-    if beta.shape != v.shape[:-1]:
-        raise ValueError(f"beta must be {tuple(v.shape[:-1])}, got {tuple(beta.shape)}")
-    if g.shape == v.shape[:-1] + (K,):
+    heads = vs[:-1]
+    if beta.shape != heads:
+        raise ValueError(f"beta must be {tuple(heads)}, got {tuple(beta.shape)}")
+    if len(gs) == lead + 2 and gs[:-1] == heads and gs[-1] == K:
         gate = 0
-    elif g.shape == v.shape[:-1]:
+    elif gs == heads:
         gate = 1
     else:
-        raise ValueError(f"g must be {tuple(v.shape[:-1])} or that with {K} channels, got {tuple(g.shape)}")
+        raise ValueError(f"g must be {tuple(heads)} or that with {K} channels, got {tuple(gs)}")
     dt = q.dtype
     if dt not in DTYPE_CODE or k.dtype != dt or v.dtype != dt or beta.dtype != dt or g.dtype != torch.float32:
         raise ValueError(f"unsupported dtypes q {q.dtype}, k {k.dtype}, v {v.dtype}, beta {beta.dtype}, g {g.dtype}")
@@ -93,7 +100,7 @@ def _int32(name: str, t: Optional[torch.Tensor], numel: Optional[int] = None) ->
 
 
 def _state(name: str, t: torch.Tensor, entries: Optional[int], H: int, K: int, V: int) -> None:
-    if t.dtype != torch.float32 or t.dim() != 4 or tuple(t.shape[1:]) != (H, K, V) or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape[1:] != (H, K, V) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [entries, {H}, {K}, {V}], got {t.dtype} {tuple(t.shape)}")
     if entries is not None and t.shape[0] != entries:
         raise ValueError(f"{name} must have {entries} entries, got {t.shape[0]}")
@@ -102,7 +109,7 @@ def _state(name: str, t: torch.Tensor, entries: Optional[int], H: int, K: int, V
 def _output(name: str, out: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
     if out is None:
         return torch.empty_like(like)
-    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
+    if out.shape != like.shape or out.dtype != like.dtype or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
     return out
 
@@ -152,10 +159,10 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         out = _output("out", out, v)
         cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
         if final_state is None:
-            final_state = torch.empty((N, H, K, V), dtype=torch.float32, device=device)
+            final_state = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
         need = delta_prefill_workspace_size(B, T, H, nseq, K, V)
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
         st = lib().kda_delta_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
