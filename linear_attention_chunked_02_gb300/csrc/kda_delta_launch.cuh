@@ -10,7 +10,17 @@
 
 namespace kda {
 
-// Opt-in shared memory of the kernels, set once per device.
+// Opt-in shared memory, and a check that the kernel launches with the registers that its warp
+// groups' shares add up to: with fewer, the groups that take more would wait for ever.
+template <typename F>
+cudaError_t kernel_ready(F *fn, int bytes, int registers) {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, fn);
+    if (e == cudaSuccess && a.numRegs < registers) e = cudaErrorInvalidConfiguration;
+    return e == cudaSuccess ? cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : e;
+}
+
+// Once per device.
 template <typename T, bool PLO, bool W128>
 cudaError_t chunked_ready(int device) {
     static std::mutex mu;
@@ -18,11 +28,12 @@ cudaError_t chunked_ready(int device) {
     std::lock_guard<std::mutex> lock(mu);
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (done[device]) return cudaSuccess;
-    constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(kda_delta_prep_kernel<T, PLO>, attr, prep_bytes<T>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, false>, attr, scan_bytes<T, PLO>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_scan_kernel<T, PLO, W128, true>, attr, scan_bytes<T, PLO>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_delta_join_kernel, attr, JOIN_BYTES);
+    cudaError_t e = kernel_ready(kda_delta_prep_kernel<T, PLO>, prep_bytes<T>(), PREP_REGISTERS);
+    if (e == cudaSuccess)
+        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, false>, scan_bytes<T, PLO>(), SCAN_REGISTERS);
+    if (e == cudaSuccess)
+        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, true>, scan_bytes<T, PLO>(), SCAN_REGISTERS);
+    if (e == cudaSuccess) e = kernel_ready(kda_delta_join_kernel, JOIN_BYTES, 0);
     done[device] = e == cudaSuccess;
     return e;
 }

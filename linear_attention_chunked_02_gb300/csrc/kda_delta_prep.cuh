@@ -57,7 +57,7 @@ constexpr int img_bytes() { return img_hdr<PLO>() + IMG_HDR_BYTES; }
 // 1 / scale of P in the halves; largest |k|, |q|
 constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7;
 
-constexpr int PREP_THREADS = 28 * 32;
+constexpr int PREP_THREADS = 28 * 32, PREP_REGISTERS = 72;     // per thread at launch
 constexpr int PREP_TW = 8;                         // transform warps of a group
 constexpr float PREP_SAFE = 48.0f;
 // The slices of a chunk go to the two transform groups in turn.  Each group has buffers of
@@ -76,6 +76,8 @@ constexpr int PB_OPS_FULL = 0, PB_OPS_EMPTY = PREP_NOPS, PB_D_FULL = 2 * PREP_NO
 constexpr int PREP_OFF_TMEM = PREP_NBARS * 8;
 constexpr int PREP_OFF_STEEP = 256;                // [8 chunk-heads][4 slices]
 constexpr int PREP_OFF_KQ = PREP_OFF_STEEP + 8 * 4 * 4;        // [8 chunk-heads][16 warps] largest |k| or |q|
+constexpr int PREP_OFF_HALF = PREP_OFF_KQ + 8 * 16 * 4;        // [2 groups][2] steep channels by half
+constexpr int PREP_OFF_META = PREP_OFF_HALF + 2 * 2 * 4;       // [4 stages] rows, first row, head
 constexpr int PREP_OFF_TOT = 1024;                 // [2 groups][8 warps][32 channels] sums of g
 constexpr int PREP_OFF_SC = PREP_OFF_TOT + 2 * 8 * 32 * 4;     // slow path: e^g, k of a channel, for A and for P
 constexpr int PREP_OFF_BETA = PREP_OFF_SC + 2 * 64 * 8;        // [pairs][64]
@@ -97,7 +99,7 @@ template <typename T>
 constexpr int prep_off_p() { return prep_off_m<T>() + 2 * 16384; }
 template <typename T>
 constexpr int prep_bytes() { return prep_off_p<T>() + 16384 + 1024; }
-static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_KQ + 8 * 16 * 4 <= PREP_OFF_TOT, "header fits");
+static_assert(PREP_OFF_TMEM + 4 <= PREP_OFF_STEEP && PREP_OFF_META + 4 * 16 <= PREP_OFF_TOT, "header fits");
 static_assert(PREP_OFF_CU + CU_CAP * 4 <= PREP_OFF_OPS, "cu_seqlens fits");
 static_assert(prep_stage_bytes<float>() % 1024 == 0 && prep_stage_bytes<__half>() % 1024 == 0 &&
                   prep_bytes<float>() <= 227 * 1024 && prep_bytes<__half>() <= 227 * 1024,
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    // registers: 896 threads of 72 at launch; 32 + 104 + 4 * 64 + 112 <= 7 * 72
+    static_assert(32 + 104 + 4 * 64 + 112 <= PREP_THREADS / 128 * PREP_REGISTERS, "the groups' shares");
     if (warp < 4) {
         tc::fewer_registers<32>();
         if (warp == 0) {
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     if (tc::elect_one()) {
                         unsigned char *to = sm + PREP_OFF_ST + st * STB;
                         uint64_t *full = &bars[PB_ST_FULL + st];
+                        *reinterpret_cast<int4 *>(sm + PREP_OFF_META + 16 * st) = make_int4(m.n, m.row0, m.h, 0);
                         mbar_arrive_expect_tx(full, 2 * ST_Q + (p.gate == 0 ? 8192 : 0));
                         tma_load_3d(to, &maps.k, 32 * s, m.h / group, m.row0, full);
                         tma_load_3d(to + ST_Q, &maps.q, 32 * s, m.h / group, m.row0, full);
@@ -456,67 +459,95 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         const bool isQ = quarter >= 2;
         const uint32_t ta = tmem + PREP_TM_A + (uint32_t(32 * quarter) << 16) + 16 * half;
         float *tot = reinterpret_cast<float *>(sm + PREP_OFF_TOT) + tg * 256;
+        uint32_t *half_steep = reinterpret_cast<uint32_t *>(sm + PREP_OFF_HALF) + tg * 2;
+        // first pass: four rows of two channels
+        const int cp = lane & 15, rh = lane >> 4, row_e = 8 * tw + 4 * rh;
+        const bool low = tw < 4;
+        const float dir = low ? -L2E : L2E;
         auto group_sync = [&] {
             if (tg == 0) named_sync<1, 256>();
             else named_sync<6, 256>();
         };
-        TaskWalk walk(ps, blockIdx.x, G);
-        Meta m = walk.next(ps);
+        // chunk-heads of this CTA; which they are comes with the stages (a walk takes twelve registers)
+        int32_t chunks = p.n_tasks / p.H;
+        if (p.cu != nullptr) {
+            int32_t sum = 0;
+            for (int i = lane; i < p.nseq; i += 32) sum += nchunks<BT>(ps.cu[i], ps.cu[i + 1]);
+            chunks = min(chunks, __reduce_add_sync(0xffffffffu, sum));
+        }
+        const uint32_t own = tg < nsl ? uint32_t(max(0, (chunks * p.H - int32_t(blockIdx.x) + G - 1) / G)) : 0u;
         uint32_t turn = 0;
-        for (uint32_t c = 0; m.valid; ++c, m = walk.next(ps)) {
+        for (uint32_t c = 0; c < own; ++c) {
             float big = 0.f;                               // largest |k| or |q| seen
             for (int s = tg; s < nsl; s += 2, ++turn) {
                 const int ob = tg, st = tg * NST + turn % NST;
                 unsigned char *stage = sm + PREP_OFF_ST + st * STB;
                 prep_wait(ok, &bars[PB_ST_FULL + st], (turn / NST) & 1, p.err);
-                // ---- E in g's place: rows 8 tw .. + 7 of channel `lane`; the 16-byte chunk j of row r lies at j ^ (r & 7)
-                float *ge = reinterpret_cast<float *>(stage + ST_G + tw * 1024 + 4 * (lane & 3));
-                float gv[8], sum = 0.f;
+                const int4 *meta = reinterpret_cast<const int4 *>(sm + PREP_OFF_META + 16 * st);
+                const int n = ok ? meta->x : 0;
+                // ---- E in g's place: rows 8 tw + 4 rh .. + 3 of channels 2 cp, 2 cp + 1; the 16-byte chunk j of row r
+                // lies at j ^ (r & 7).  Decays in powers of two, of the lower rows negated: E runs outward from
+                // between rows 31 and 32
+                float *ge = reinterpret_cast<float *>(stage + ST_G + tw * 1024 + rh * 512 + 8 * (cp & 1));
+                auto at = [&](int i) { return reinterpret_cast<float2 *>(ge + 32 * i + 4 * ((cp >> 1) ^ (4 * rh) ^ i)); };
+                float2 gv[4], sum = make_float2(0.f, 0.f);
+                if (p.gate == 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) gv[i] = ge[32 * i + 4 * ((lane >> 2) ^ i)];
-                if (p.gate != 0) {                         // one decay to a row, from global memory
-                    const float *gp = p.g + (int64_t(m.row0) + 8 * tw) * p.H + m.h;
+                    for (int i = 0; i < 4; ++i) gv[i] = *at(i);
+                } else {                                   // one decay to a row, from global memory
+                    const float *gp = p.g + (int64_t(meta->y) + row_e) * p.H + meta->z;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) gv[i] = 8 * tw + i < m.n ? gp[i * p.H] : 0.f;
+                    for (int i = 0; i < 4; ++i) gv[i].x = gv[i].y = row_e + i < n ? gp[i * p.H] : 0.f;
                 }
-                if (m.n < 8 * tw + 8) {                    // rows past the end hold the next request's
+                if (n < row_e + 4) {                     // rows past the end hold the next request's
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) gv[i] = 8 * tw + i < m.n ? gv[i] : 0.f;
+                    for (int i = 0; i < 4; ++i)
+                        if (row_e + i >= n) gv[i] = make_float2(0.f, 0.f);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    gv[i] *= L2E;
-                    sum += gv[i];
+                for (int i = 0; i < 4; ++i) {
+                    gv[i] = __fmul2_rn(gv[i], make_float2(dir, dir));
+                    sum = __fadd2_rn(sum, gv[i]);
                 }
-                float *tb = tot;                           // free since the second synchronisation of the last slice
-                tb[tw * 32 + lane] = sum;
+                const float2 next = make_float2(__shfl_xor_sync(0xffffffffu, sum.x, 16),
+                                                __shfl_xor_sync(0xffffffffu, sum.y, 16));
+                const float2 eight = __fadd2_rn(sum, next);
+                float2 *tb = reinterpret_cast<float2 *>(tot);      // free since the second synchronisation of the last slice
+                if (rh == 0) tb[tw * 16 + cp] = eight;
                 group_sync();
-                // decay from the middle of the chunk (between rows 31 and 32) outward
-                float lo = 0.f, hi = 0.f, off = 0.f;
+                float2 off = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const float t = tb[w * 32 + lane];
-                    if (w < 4) lo += t;
-                    else hi += t;
-                    if (tw < 4 ? (w > tw && w < 4) : (w >= 4 && w < tw)) off += t;
+                for (int w = 0; w < 3; ++w)
+                    if (w < (low ? 3 - tw : tw - 4)) off = __fadd2_rn(off, tb[(low ? 3 - w : 4 + w) * 16 + cp]);
+                if (tw == 0 || tw == 7) {                  // the half's decay: steep channels
+                    const float2 t = __fadd2_rn(off, eight);
+                    const float lim = PREP_SAFE * L2E;
+                    const uint32_t ex = __ballot_sync(0xffffffffu, !(low ? t.x <= lim : t.x >= -lim)) & 0xffffu,
+                                   ey = __ballot_sync(0xffffffffu, !(low ? t.y <= lim : t.y >= -lim)) & 0xffffu;
+                    if (lane == 0) {                       // (true for NaN too)
+                        uint32_t mask = 0u;
+                        if ((ex | ey) != 0u)
+                            for (int i = 0; i < 16; ++i) mask |= (((ex >> i) & 1u) | ((ey >> i) & 1u) << 1) << (2 * i);
+                        half_steep[low ? 0 : 1] = mask;
+                    }
                 }
-                const bool keep = lo >= -PREP_SAFE * L2E && hi >= -PREP_SAFE * L2E;     // false for NaN too
-                const uint32_t steep = __ballot_sync(0xffffffffu, !keep);
-                if (tw < 4) {
+                if (low != (rh == 1)) off = __fadd2_rn(off, next);
+                if (low) {
 #pragma unroll
-                    for (int i = 7; i >= 0; --i) {
-                        ge[32 * i + 4 * ((lane >> 2) ^ i)] = -off;
-                        off += gv[i];
+                    for (int i = 3; i >= 0; --i) {
+                        *at(i) = off;
+                        off = __fadd2_rn(off, gv[i]);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        off += gv[i];
-                        ge[32 * i + 4 * ((lane >> 2) ^ i)] = off;
+                    for (int i = 0; i < 4; ++i) {
+                        off = __fadd2_rn(off, gv[i]);
+                        *at(i) = off;
                     }
                 }
-                if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
                 group_sync();
+                const uint32_t steep = half_steep[0] | half_steep[1];
+                if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
                 // ---- operands: this thread's row
                 prep_wait(ok, &bars[PB_OPS_EMPTY + ob], (turn & 1) ^ 1, p.err);
                 tc::fence_after_sync();
@@ -531,9 +562,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                         const float4 t = *reinterpret_cast<const float4 *>(er + 16 * ((4 * half + 2 * b + j) ^ (row & 7)));
                         E[4 * j] = t.x; E[4 * j + 1] = t.y; E[4 * j + 2] = t.z; E[4 * j + 3] = t.w;
                     }
-                    if (m.n < 64) {
+                    if (n < 64) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = row < m.n ? x[i] : 0.f;
+                        for (int i = 0; i < 8; ++i) x[i] = row < n ? x[i] : 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) big = max3(big, x[i], x[i + 1]);

@@ -54,7 +54,7 @@
 
 namespace kda {
 
-constexpr int SCAN_THREADS = 32 * 32;
+constexpr int SCAN_THREADS = 32 * 32, SCAN_REGISTERS = 64;     // per thread at launch
 constexpr int SCAN_PARTS = 4;                      // chain threads to a lane
 constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
               SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
     bool ok = true;
 
-    // registers: 1024 threads of 64 at launch; 4 * 80 + 2 * 64 + 40 + 24 <= 8 * 64
+    static_assert(4 * 80 + 2 * 64 + 40 + 24 <= SCAN_THREADS / 128 * SCAN_REGISTERS, "the groups' shares");
     if (warp < 16) {
         tc::more_registers<80>();
         // ------------------------------------------------------------------ chain
