@@ -185,10 +185,12 @@ __device__ __forceinline__ void image_put(unsigned char *hi, unsigned char *lo, 
 }
 
 // The 64-token solve of the A tile (blocks (i, j) at Ab + 256 blk(i, j)) by two warps: the row-major
-// inverse into xs (its blocks above the diagonal are not written).  Block by block along
+// M = (I + A)^-1 diag(beta) into xs (its blocks above the diagonal are not written); `beta` is row pt's,
+// sbeta all of them from the first barrier on.  Block by block along
 // the diagonals, X_rc = -X_rr sum_k A_rk X_kc, transposed and in split TF32 as in the chunk
 // solver; one loop body does every product, where the chunk solver unrolls its two levels.
-__device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs, int pt, int bar) {
+__device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs, float beta, const float *sbeta, int pt,
+                                           int bar) {
     const int warp = pt >> 5, lane = pt & 31, g = lane >> 2, t = lane & 3;
     float *Xn = X + 6 * XTS;
     {
@@ -196,7 +198,7 @@ __device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs,
         float x[16];
         diag_invert<true>(Ab + blk(b, b) * 256, 16, l, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xs[(16 * b + i) * PREP_XP + 16 * b + l] = x[i];
+        for (int i = 0; i < 16; ++i) xs[(16 * b + i) * PREP_XP + 16 * b + l] = x[i] * beta;
         if (b != 3) {                                      // X_bb^T row-major (row = lane)
             float4 *d = reinterpret_cast<float4 *>(X + blk(b, b) * XTS + l * XTP);
 #pragma unroll
@@ -210,10 +212,9 @@ __device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs,
     }
     bar64(bar);
 #pragma unroll 1
-    for (int d = 1; d < 4; ++d) {
+    for (int c = warp; c < 3; c += warp == 0 ? 3 : 1) {    // 9 tile products against 7
 #pragma unroll 1
-        for (int r = d + warp; r < 4; r += 2) {
-            const int c = r - d;
+        for (int r = c + 1; r < 4; ++r) {
             TileA la;
             TileB rb;
             TileC acc, out;
@@ -229,10 +230,16 @@ __device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs,
             right2(rb, Xn + (r - 1) * XRS, XRP, g, t);
             mma_tile<false>(out, la, rb);
             if (r < 3) smem_tile_t<true>(X + blk(r, c) * XTS, out, g, t);
+            const float b0 = sbeta[16 * c + g], b1 = sbeta[16 * c + g + 8];    // the tile is transposed
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out.c[nt][e] *= e < 2 ? b0 : b1;
             out_tile_t(xs, PREP_XP, BT, r, c, out, g, t);
+            __syncwarp();
         }
-        bar64(bar);
     }
+    bar64(bar);
 }
 
 // A wait that gives up once, after WAIT_LIMIT_NS: the thread then records it and waits no
@@ -548,6 +555,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                 group_sync();
                 const uint32_t steep = half_steep[0] | half_steep[1];
                 if (tw == 0 && lane == 0) steep_m[(c & 7) * 4 + s] = steep;
+                const bool rare = n < 64 || steep != 0u;
                 // ---- operands: this thread's row
                 prep_wait(ok, &bars[PB_OPS_EMPTY + ob], (turn & 1) ^ 1, p.err);
                 tc::fence_after_sync();
@@ -562,17 +570,16 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                         const float4 t = *reinterpret_cast<const float4 *>(er + 16 * ((4 * half + 2 * b + j) ^ (row & 7)));
                         E[4 * j] = t.x; E[4 * j + 1] = t.y; E[4 * j + 2] = t.z; E[4 * j + 3] = t.w;
                     }
-                    if (n < 64) {
+                    if (rare) {                            // rows past the end; a steep channel enters the product as zeros
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = row < n ? x[i] : 0.f;
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] = row < n ? x[i] : 0.f;
+                            big = max3(big, x[i], x[i]);
+                            if ((steep >> (16 * half + 8 * b + i)) & 1u) x[i] = E[i] = 0.f;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) big = max3(big, x[i], x[i + 1]);
-                    if (steep != 0u) {                     // a steep channel enters the product as zeros
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if ((steep >> (16 * half + 8 * b + i)) & 1u) x[i] = E[i] = 0.f;
-                    }
                     uint32_t h[8], l[8];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2)
@@ -773,6 +780,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
         float *xs = reinterpret_cast<float *>(sm + prep_off_xs<T>()) + pr * 64 * PREP_XP;
         float *sbeta = reinterpret_cast<float *>(sm + PREP_OFF_BETA) + pr * 64;
         unsigned char *mi = sm + prep_off_m<T>() + pr * 16384;
+        // what the solve leaves out
+#pragma unroll 1
+        for (int j = 0; j < 64; ++j) xs[pt * PREP_XP + j] = 0.f;
         TaskWalk walk(ps, int32_t(blockIdx.x) + pr * G, 2 * G);
         int32_t qi;
         Meta m = walk.next(ps, &qi);
@@ -782,19 +792,17 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             if (pt == 0) tc::bulk_wait_read();             // the previous image has left
             bar64(bar);                                    // and the betas are consumed
             sbeta[pt] = b;
-            prep_solve(Ab, X, xs, pt, bar);
+            prep_solve(Ab, X, xs, b, sbeta, pt, bar);
             if ((pt & 31) == 0) mbar_arrive(&bars[PB_AT_EMPTY + pr]);
-            // columns 8 j .. of row pt of M; zeros past the chunk's end and past the row's block
-            auto columns = [&](int j, float (&x)[8]) {
-                const bool in = pt < m.n && 8 * j <= pt;
+            if (pt >= m.n) {                               // rows past the end: zeros whatever is in the others
+#pragma unroll 1
+                for (int j = 0; j < 64; ++j) xs[pt * PREP_XP + j] = 0.f;
+            }
+            auto columns = [&](int j, float (&x)[8]) {     // columns 8 j .. of row pt of M
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
                     const float4 t = *reinterpret_cast<const float4 *>(xs + pt * PREP_XP + 8 * j + e);
-                    const float4 bt = *reinterpret_cast<const float4 *>(sbeta + 8 * j + e);
-                    x[e] = in ? t.x * bt.x : 0.f;
-                    x[e + 1] = in ? t.y * bt.y : 0.f;
-                    x[e + 2] = in ? t.z * bt.z : 0.f;
-                    x[e + 3] = in ? t.w * bt.w : 0.f;
+                    x[e] = t.x; x[e + 1] = t.y; x[e + 2] = t.z; x[e + 3] = t.w;
                 }
             };
             const int nj = 4 * (pt >> 5) + 4;              // blocks of 8 columns with any of this warp's rows
