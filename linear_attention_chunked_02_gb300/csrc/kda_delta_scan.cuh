@@ -304,10 +304,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         float *smax = reinterpret_cast<float *>(sm + SCAN_OFF_MAX) + v, *svmax = reinterpret_cast<float *>(sm + SCAN_OFF_VMAX) + v;
         float2 *sout = reinterpret_cast<float2 *>(sm + SCAN_OFF_OUT);
         // the four threads of a lane
-        auto lane_max = [&](float *at, float x) {
-            at[part * 128] = x;
+        auto lane_max = [&](float &x, float &y) {          // of the state and of the values
+            smax[part * 128] = x;
+            svmax[part * 128] = y;
             asm volatile("bar.sync %0, 128;" ::"r"(8 + quarter) : "memory");
-            return fmaxf(max3(at[0], at[128], at[256]), at[384]);
+            x = fmaxf(max3(smax[0], smax[128], smax[256]), smax[384]);
+            y = fmaxf(max3(svmax[0], svmax[128], svmax[256]), svmax[384]);
         };
         auto release = [&](int b) {                        // operand columns written, accumulators read
             tc::wait_st();
@@ -372,26 +374,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < 32; ++i) S[i] = 32 * part + i == v && held ? 1.f : 0.f;
             }
         }
-        float bS = 0.f, invS = 1.f;
-        if (x.nc > 0) {
-            bS = lane_max(smax, state_max());
-            put_state(pow2_scale(bS, VS_LO, VS_HI, invS));
-            release(SB_S);
-        }
-        for (int c = 0; c < x.nc; ++c, ++cc) {
-            const uint32_t ph = cc & 1;
-            const int left = x.rows - 64 * c;
-            if (run == 0) {
-                prep_wait(ok, &bars[SB_V_FULL], vc++ & 1, p.err);
-                // rows past the end hold the next request's; columns past V stay in their lanes
-                for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
-                    if (v < V) sv[i * V] = T(0.f);
-            }
-            Pair<T> vr[sizeof(T) == 2 ? 8 : 1];            // 16-bit values, two tokens to a word
+        // a chunk's values: this thread's part of the largest, and 16-bit ones themselves.  The next chunk's
+        // come while the products of this one run
+        Pair<T> vr[sizeof(T) == 2 ? 8 : 1];                // two tokens to a word
+        auto values = [&](int left) {
             float bv = 0.f;
-            if (run == 1) {
-                // values of zero
-            } else if constexpr (sizeof(T) == 2) {
+            if (run == 1) return bv;                       // values of zero
+            prep_wait(ok, &bars[SB_V_FULL], vc++ & 1, p.err);
+            // rows past the end hold the next request's; columns past V stay in their lanes
+            for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
+                if (v < V) sv[i * V] = T(0.f);
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
                 Pair<T> m = vr[0].abs();
@@ -403,7 +396,19 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
             }
-            bv = lane_max(svmax, bv);
+            return bv;
+        };
+        float bS = 0.f, bv = 0.f, invS = 1.f;
+        if (x.nc > 0) {
+            bS = state_max();
+            bv = values(x.rows);
+            lane_max(bS, bv);
+            put_state(pow2_scale(bS, VS_LO, VS_HI, invS));
+            release(SB_S);
+        }
+        for (int c = 0; c < x.nc; ++c, ++cc) {
+            const uint32_t ph = cc & 1;
+            const int left = x.rows - 64 * c;
             prep_wait(ok, &bars[SB_IMG_FULL + cc % NI], (cc / NI) & 1, p.err);
             const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>() +
                                                                img_hdr<PLO>());
@@ -426,7 +431,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (weak) {
                     scan_tokens<T>(p, S, x.row + 64 * c, left < 64 ? left : 64, x.h, part, v, quarter,
                                    reinterpret_cast<float *>(sm + SCAN_OFF_SUM));
-                    sS = pow2_scale(lane_max(smax, state_max()), VS_LO, VS_HI, invS1);     // the new state's own bound
+                    float m = state_max(), unused = 0.f;
+                    lane_max(m, unused);
+                    sS = pow2_scale(m, VS_LO, VS_HI, invS1);           // the new state's own bound
                 }
             }
             if (!TRANS && part == 0) sout[ph * 128 + v] = weak ? both(-1.f) : make_float2(invS, invU);
@@ -461,10 +468,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 put_operand(rop, rop + TM_RLO - TM_RHI, x, invR * minv * sU);
             }
             release(SB_U);
+            const bool more = c + 1 < x.nc;                // the next walk puts its own state
+            float bvn = more ? values(left - 64) : 0.f;
             // S1 = diag(e^{G_C}) S + (K e^{G_C-G})^T U
             prep_wait(ok, &bars[SB_GAM + ph], (cc >> 1) & 1, p.err);
             accumulator(SB_D3, ph);
-            const bool more = c + 1 < x.nc;                // the next walk puts its own state
             float mx = 0.f;
             if (weak) {                                    // S is there
                 if (more) put_state(sS);
@@ -490,7 +498,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             if (more) {
                 release(SB_S);
-                bS = lane_max(smax, mx);
+                lane_max(mx, bvn);
+                bS = mx;
+                bv = bvn;
                 invS = invS1;
             }
         }
@@ -630,6 +640,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     y[i] = W2::wide(two(kp, i, dc));
                     g[i] = decay(i, dc);
                 }
+                if (x == nh - 1) {                         // the staged chunk is read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[SB_ST_EMPTY]);
+                }
 #pragma unroll
                 for (int i = 7; i >= 0; --i) {
                     y[i] = __fmul2_rn(y[i], __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
@@ -650,10 +664,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars[SB_KH_FULL]);
-                mbar_arrive(&bars[SB_ST_EMPTY]);
-            }
+            if (lane == 0) mbar_arrive(&bars[SB_KH_FULL]);
             named_sync<1, 256>();                          // the sums are consumed
         }
         }
