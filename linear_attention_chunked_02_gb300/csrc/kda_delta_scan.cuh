@@ -570,7 +570,28 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (p.gate != 0) return both(gp[i]);
                 return STAGED || i < left ? *reinterpret_cast<const float2 *>(gp + i * gs + d) : both(0.f);
             };
-            for (int x = 0; x < nh; ++x) {
+            // at K = 128 a lane has four channels in a row for the first two passes: half the loads and stores
+            // of two (the whole scan of 16 x 512 tokens, 64 heads: XXX)
+            struct alignas(2 * sizeof(raw)) raw4 { raw r[2]; };
+            auto four = [&](const T *at, int i) {
+                const bool in = STAGED || i < left;
+                return in ? *reinterpret_cast<const raw4 *>(at + i * ks + 4 * lane) : raw4{};
+            };
+            auto decay4 = [&](int i) {
+                if (p.gate != 0) return make_float4(gp[i], gp[i], gp[i], gp[i]);
+                return STAGED || i < left ? *reinterpret_cast<const float4 *>(gp + i * gs + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            if (W128) {
+                float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 t = decay4(i);
+                    s0 = __ffma2_rn(make_float2(t.x, t.y), both(L2E), s0);      // in powers of two
+                    s1 = __ffma2_rn(make_float2(t.z, t.w), both(L2E), s1);
+                }
+                *reinterpret_cast<float4 *>(tot + rg * 128 + 4 * lane) = make_float4(s0.x, s0.y, s1.x, s1.y);
+            }
+            for (int x = 0; !W128 && x < nh; ++x) {
                 float2 sum = both(0.f);
                 const int d = chan(x);
 #pragma unroll
@@ -583,7 +604,51 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             named_sync<1, 256>();
             // K e^G and scale Q e^G: row r of a tile is 128 bytes, its 16-byte chunk lane / 4 at (lane / 4) ^ (r & 7)
             prep_wait(ok, &bars[SB_KQ_EMPTY], ph ^ 1, p.err);
-            for (int x = 0; x < nh; ++x) {
+            if (W128) {
+                float2 G[2] = {both(0.f), both(0.f)};
+                for (int w = 0; w < rg; ++w) {
+                    const float4 t = *reinterpret_cast<const float4 *>(tot + w * 128 + 4 * lane);
+                    G[0] = __fadd2_rn(G[0], make_float2(t.x, t.y));
+                    G[1] = __fadd2_rn(G[1], make_float2(t.z, t.w));
+                }
+                unsigned char *kq = sm + SCAN_OFF_KQ + (lane >> 4) * 8192 + rg * 1024 + 8 * (lane & 1);
+#pragma unroll 1
+                for (int b = 0; b < 8; b += 4) {
+                    raw4 rk[4], rq[4];                     // all loads before the first store
+                    float4 g[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        rk[i] = four(kp, b + i);
+                        if (!TRANS) rq[i] = four(qp, b + i);
+                        g[i] = decay4(b + i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t kh[2], kl[2], qh[2], ql[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            G[j] = __ffma2_rn(j == 0 ? make_float2(g[i].x, g[i].y) : make_float2(g[i].z, g[i].w), both(L2E), G[j]);
+                            const float2 e = __fmul2_rn(make_float2(ex2(G[j].x), ex2(G[j].y)), both(sk1));
+                            const float2 kv = __fmul2_rn(W2::wide(rk[i].r[j]), e);
+                            split_f16(kv.x, kv.y, kh[j], kl[j]);
+                            if (!TRANS) {
+                                const float2 qv = __fmul2_rn(W2::wide(rq[i].r[j]), __fmul2_rn(e, cq));
+                                if (PLO) split_f16(qv.x, qv.y, qh[j], ql[j]);
+                                else qh[j] = round_f16(qv.x, qv.y);
+                            }
+                        }
+                        unsigned char *at = kq + (b + i) * 128 + 16 * (((lane & 15) >> 1) ^ (b + i));
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(kh[0], kh[1]);
+                        *reinterpret_cast<uint2 *>(at + 16384) = make_uint2(kl[0], kl[1]);
+                        if (!TRANS) *reinterpret_cast<uint2 *>(at + 32768) = make_uint2(qh[0], qh[1]);
+                        if (!TRANS && PLO) *reinterpret_cast<uint2 *>(at + 49152) = make_uint2(ql[0], ql[1]);
+                    }
+                }
+                if (rg == 7)                               // here G is the whole chunk's sum
+                    *reinterpret_cast<float4 *>(gam + ph * 128 + 4 * lane) =
+                        make_float4(ex2(G[0].x), ex2(G[0].y), ex2(G[1].x), ex2(G[1].y));
+            }
+            for (int x = 0; !W128 && x < nh; ++x) {
                 const float *tb = tot + 64 * x + 2 * lane;
                 float2 G = both(0.f);
                 for (int w = 0; w < rg; ++w) G = __fadd2_rn(G, *reinterpret_cast<const float2 *>(tb + w * 128));
