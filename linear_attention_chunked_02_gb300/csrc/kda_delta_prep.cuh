@@ -242,23 +242,24 @@ __device__ __forceinline__ void prep_solve(const float *Ab, float *X, float *xs,
     bar64(bar);
 }
 
-// A wait that gives up once, after WAIT_LIMIT_NS: the thread then records it and waits no
-// more, but keeps arriving, so that no other thread is stranded.  The tries suspend
-// the warp (polling takes issue slots from those at work), and the timer is read only
-// every 64 of them: reading it takes longer than most of these waits.
+// A wait that gives up once, after WAIT_TRIES tries: the thread then records it and waits no more, but
+// keeps arriving, so that no other thread is stranded.  A try suspends the warp until the phase ends
+// or some 4 us have passed (polling takes issue slots from the warps at work), so that the tries make
+// about a second; each of these waits ends within microseconds, or some hundred where a chunk goes the
+// slow way.  No clock is read: a wait is a few instructions, which matters here (the kernels' loops
+// fill the instruction cache; with a clock in every wait the two
+// kernels of 16 x 512 x 64 heads took 221 and 265 us, without 204 and 257).
+constexpr uint32_t WAIT_TRIES = 1u << 18;
 __device__ __forceinline__ void prep_wait(bool &ok, uint64_t *bar, uint32_t parity, unsigned *err) {
-    if (!ok || mbar_try_wait(bar, parity)) return;
-    unsigned long long t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_suspend(bar, parity, 100000u)) return;
-        if ((it & 63u) == 0u) {
-            const unsigned long long t = globaltimer();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > WAIT_LIMIT_NS) break;
+    if (!ok) return;
+    uint32_t left = WAIT_TRIES;
+#pragma unroll 1
+    while (!mbar_try_wait_suspend(bar, parity, 100000u))
+        if (--left == 0u) {
+            ok = false;
+            atomicOr(err, ERR_WAIT_TIMEOUT);
+            return;
         }
-    }
-    ok = false;
-    atomicOr(err, ERR_WAIT_TIMEOUT);
 }
 
 // The segments that the scan walks, {sequence, segment of it, chunks before the sequence, its
