@@ -18,28 +18,36 @@ namespace {
 
 using namespace kda;
 
-// Whether prompts of this shape go chunk by chunk rather than token by token: from
-// an average length on.
+// Whether prompts of this shape go chunk by chunk rather than token by token: from an average length
+// of 16 on.  Measured for 32 heads of K = V = 128 in BF16, us token by token and by chunks:
+//   1 sequence of 16 / 24 / 32 tokens:     20 / 31 / 41     25 / 25 / 25
+//   32 sequences of 8 / 16 / 24 tokens:    57 / 115 / 176   106 / 107 / 107
+//   128 sequences of 8 / 16 / 24 tokens:   240 / 439 / 637  335 / 336 / 338
 bool chunked_form(int64_t B, int64_t T, int32_t num_seqs) {
     const int64_t seqs = num_seqs > 0 ? num_seqs : B;
     return B > 0 && T > 0 && B * T >= 16 * seqs;
 }
 
 // Chunks to a segment for this shape, 0 where sequences are not split, and a bound on the segments.
-// The model: a chunk of the walk takes 4 us, 3 without outputs; the first run has two walks to a
-// segment but the first's one and the last's none; the join takes 3 us a segment and the two more
-// launches 10.  Sized for the 152 SMs of a GB300.
+// The model: a chunk of the walk takes 4.7 us, 2.9 without outputs; the first run has two walks to a
+// segment but the first's one and the last's none; the join takes 6 us a segment and the two more
+// launches 10.  Sized for the 152 SMs of a GB300.  K = V = 128 in BF16, us for the whole operator with
+// sequences whole and in 3, 4, 6 and 9 segments (the model's choice is at most 3 % from the best):
+//   1 x 16384 tokens, 32 heads:  1192   855  916  889  913   (3)
+//   1 x 65536, 16 heads:         4302  2853 2251 1659 1650   (9)
+//   1 x 2048, 32 heads:           176   155  171  193  201   (3)
+//   1 x 8192, 64 heads:           707   872  841  866  959   (whole)
 int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_t &units) {
     const int64_t seqs = num_seqs > 0 ? num_seqs : B, heads = seqs * H, sms = 152;
     const int64_t total = max_chunks(B, T, num_seqs, BT);
     const double c = double(total) / double(seqs);
     auto waves = [&](int64_t n) { return double((n + sms - 1) / sms); };
-    double best = waves(heads) * c * 4.0;
+    double best = waves(heads) * c * 4.7;
     int32_t seg = 0;
     for (int P = 2; P <= 32 && heads < sms; ++P) {
         const int32_t s = int32_t(c / P + 0.999);
         if (s < 4) break;
-        const double t = waves((2 * P - 3) * heads) * s * 3.0 + waves(P * heads) * s * 4.0 + 3.0 * P + 10.0;
+        const double t = waves((2 * P - 3) * heads) * s * 2.9 + waves(P * heads) * s * 4.7 + 6.0 * P + 10.0;
         if (t < 0.95 * best) {
             best = t;
             seg = s;

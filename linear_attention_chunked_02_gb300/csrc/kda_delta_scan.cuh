@@ -251,17 +251,35 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // walk w: unit w / H (TRANS: w / 2 / H, for N where w is even and for M where it is odd)
-    const int32_t walks = p.n_units * p.H * (TRANS ? 2 : 1);
+    // walk w: unit w / H.  TRANS: N, then M of every unit in turn; dense, only what the join needs: N of a
+    // sequence's first segment, N and M of the others but the last (a CTA goes through walks gridDim.x
+    // apart, and those with nothing to do would leave some CTAs twice the work of others)
+    const int32_t parts = p.cu == nullptr && p.seg > 0 ? (p.cpr + p.seg - 1) / p.seg : 1;     // dense: segments
+    const int32_t maps1 = max(1, 2 * parts - 3);           // dense, TRANS: walks to a sequence-head
+    const int32_t walks = !TRANS ? p.n_units * p.H : p.cu != nullptr ? 2 * p.n_units * p.H
+                                                                     : parts > 1 ? p.nseq * maps1 * p.H : 0;
+    auto unit_at = [&](int32_t w, int &run) {              // run 1: M
+        run = 0;
+        if (!TRANS) return w / p.H;
+        if (p.cu != nullptr) {
+            run = w & 1;
+            return (w >> 1) / p.H;
+        }
+        const int32_t g = w / p.H, n = g / maps1, r = g - n * maps1;
+        if (r == 0) return n * parts;
+        run = (r - 1) & 1;
+        return n * parts + 1 + ((r - 1) >> 1);
+    };
     auto entry = [&](int32_t w) {
         if (w >= walks) return make_int4(0, 0, 0, 0);
-        const int32_t u = (TRANS ? w >> 1 : w) / p.H;
+        int run;
+        const int32_t u = unit_at(w, run);
         if (p.cu != nullptr) return __ldg(p.units + u);
-        const int32_t parts = p.seg > 0 ? (p.cpr + p.seg - 1) / p.seg : 1, n = u / parts;
+        const int32_t n = u / parts;
         return make_int4(n, u - n * parts, n * p.cpr, parts);
     };
     struct Walk1 {
-        int32_t w, h, run, rows, nc, row;  // run 1: M; first row
+        int32_t w, unit, h, run, rows, nc, row;    // run 1: M; first row
         int4 e;
         int32_t before;                    // chunks before the first
         bool idle, last;
@@ -270,9 +288,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         Walk1 x;
         x.w = w;
         x.e = e;
-        const int32_t i = TRANS ? w >> 1 : w, u = i / p.H;
-        x.h = i - u * p.H;
-        x.run = TRANS ? w & 1 : 0;
+        x.unit = unit_at(w, x.run);
+        x.h = TRANS && p.cu != nullptr ? (w >> 1) - x.unit * p.H : w - w / p.H * p.H;
         int64_t a = 0, b = 0;
         if (e.w > 0) sequence_rows(p, e.x, a, b);
         x.last = e.y == e.w - 1;
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float *from = nullptr;
             if (!x.idle) {
                 const int32_t e = state_entry(p, x.e.x);
-                float *map = p.trans + (int64_t((TRANS ? w >> 1 : w) / p.H) * p.H + x.h) * tz;
+                float *map = p.trans + (int64_t(x.unit) * p.H + x.h) * tz;
                 if (x.e.y > 0) {
                     if (!TRANS) from = map - int64_t(p.H) * tz;        // chained into the segment before
                 } else if (p.state_in != nullptr && e >= 0) {
