@@ -30,9 +30,9 @@ cudaError_t chunked_ready(int device) {
     if (done[device]) return cudaSuccess;
     cudaError_t e = kernel_ready(kda_delta_prep_kernel<T, PLO>, prep_bytes<T>(), PREP_REGISTERS);
     if (e == cudaSuccess)
-        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, false>, scan_bytes<T, PLO>(), SCAN_REGISTERS);
+        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, false>, scan_bytes<T, PLO>(W128 ? 128 : 64), SCAN_REGISTERS);
     if (e == cudaSuccess)
-        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, true>, scan_bytes<T, PLO>(), SCAN_REGISTERS);
+        e = kernel_ready(kda_delta_scan_kernel<T, PLO, W128, true>, scan_bytes<T, PLO>(W128 ? 128 : 64), SCAN_REGISTERS);
     if (e == cudaSuccess) e = kernel_ready(kda_delta_join_kernel, JOIN_BYTES, 0);
     done[device] = e == cudaSuccess;
     return e;
@@ -45,7 +45,7 @@ cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const Del
     if (e != cudaSuccess) return e;
     auto blocks = [&](int64_t n) { return unsigned(n < sms ? n : sms); };     // persistent, one to an SM
     const int64_t walks = int64_t(p.n_units) * p.H;
-    const size_t bytes = size_t(scan_bytes<T, PLO>());
+    const size_t bytes = size_t(scan_bytes<T, PLO>(p.K));
     e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, blocks(p.n_tasks), PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
     if (e == cudaSuccess && p.seg > 0) {
         e = launch_pdl(true, kda_delta_scan_kernel<T, PLO, W128, true>, blocks(2 * walks), SCAN_THREADS, bytes, s, scan, p);

@@ -46,8 +46,9 @@
 //   * warps 24-27 (output): O, a lane quarter each;
 //   * warp 28: MMA issue; warps 29, 30 and 31: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
-//     little in flight), so 16-bit q, k and g are staged in shared memory; 32-bit ones
-//     find no room there and are read directly.
+//     little in flight), so 16-bit q, k and g are staged in shared memory, 32-bit ones of up to 64
+//     channels too (the scan of 2 x 1000 tokens, 16 heads, K = 64: 73 us, not 77); of more channels they find no room
+//     there and are read directly.
 #pragma once
 
 #include "kda_delta_prep.cuh"
@@ -83,12 +84,16 @@ template <bool PLO>
 constexpr int scan_off_v() { return scan_off_img<PLO>() + scan_nimg<PLO>() * scan_img_pitch<PLO>(); }  // [64 tokens][V]
 template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
+template <typename T>
+constexpr int scan_stage() { return sizeof(T) == 2 ? 65536 : 49152; }      // 32-bit: of 64 channels
+template <typename T>
+constexpr bool scan_staged(int K) { return sizeof(T) == 2 || K <= 64; }
 template <typename T, bool PLO>
-constexpr int scan_bytes() { return scan_off_st<T, PLO>() + (sizeof(T) == 2 ? 65536 : 0) + 1024; }
+constexpr int scan_bytes(int K) { return scan_off_st<T, PLO>() + (scan_staged<T>(K) ? scan_stage<T>() : 0) + 1024; }
 static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
-static_assert(scan_bytes<float, true>() <= 227 * 1024 && scan_bytes<__half, true>() <= 227 * 1024 &&
-                  scan_bytes<__nv_bfloat16, false>() <= 227 * 1024, "fits the shared memory of one CTA");
+static_assert(scan_bytes<float, true>(64) <= 227 * 1024 && scan_bytes<__half, true>(128) <= 227 * 1024 &&
+                  scan_bytes<__nv_bfloat16, false>(128) <= 227 * 1024, "fits the shared memory of one CTA");
 // A chunk is taken token by token where its values are below 2^-16 of what the state can add to R
 // and no channel keeps more than 2^-12 of the state: what comes out is then
 // possibly below 2^-20 of what goes in.
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SCAN_OFF_TMEM);
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
     constexpr int NI = scan_nimg<PLO>();
-    constexpr bool STAGED = sizeof(T) == 2;
+    const bool STAGED = W128 ? scan_staged<T>(128) : scan_staged<T>(p.K);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float *gp;
             if (STAGED) {
                 kp = reinterpret_cast<T *>(st) + 8 * rg * K;
-                qp = kp + 64 * 128;
+                qp = reinterpret_cast<T *>(st + 16384) + 8 * rg * K;
                 gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * K;
             } else {
                 kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * K;
@@ -885,7 +890,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
             }
         } else if (warp == 29) {
-            // -------------------------------------------- loads of q, k and g (16-bit)
+            // ------------------------------------------------- loads of q, k and g
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
                 const uint32_t bytes = (TRANS ? 1 : 2) * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);

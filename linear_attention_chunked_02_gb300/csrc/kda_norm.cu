@@ -203,13 +203,13 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
         while (lanes < 32 && lanes < nvec) lanes *= 2;
         return nvec > 32 ? launch_narrow<T, KIND, VEC, 2>(p, lanes, s) : launch_narrow<T, KIND, VEC, 1>(p, lanes, s);
     }
-    // wider rows: one to a block, as few vectors to a thread as 1024 threads allow
-    // (two from 256 vectors on: fewer, busier warps to sum over)
-    int nv = 1;
-    while ((nv < 2 && nvec > 256) || nvec > nv * 1024) nv *= 2;
+    // wider rows: one to a block, two vectors to a thread or as many more as 1024 threads need.  add_norm
+    // of 8192 BF16 rows of 2048 / 4096 / 8192 with one vector to a thread: 19.7, 41.5 and 92.4 us, with
+    // two 19.1, 40.6 and 85.3 us, with four (rows of 4096 and 8192) 53.2 and 107.7 us
+    int nv = 2;
+    while (nvec > nv * 1024) nv *= 2;
     const unsigned threads = unsigned((nvec + nv - 1) / nv + 31) / 32 * 32;
     const unsigned grid = unsigned(p.rows);
-    if (nv == 1) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 1>, grid, threads, 0, s, p);
     if (nv == 2) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 2>, grid, threads, 0, s, p);
     if (nv == 4) return launch_pdl(true, kda_norm_wide_kernel<T, KIND, VEC, 4>, grid, threads, 0, s, p);
     // only rows read one element at a time are this wide
