@@ -32,11 +32,11 @@ bool chunked_form(int64_t B, int64_t T, int32_t num_seqs) {
 // The model: a chunk of the walk takes 4.7 us, 2.9 without outputs; the first run has two walks to a
 // segment but the first's one and the last's none; the join takes 6 us a segment and the two more
 // launches 10.  Sized for the 152 SMs of a GB300.  K = V = 128 in BF16, us for the whole operator with
-// sequences whole and in 3, 4, 6 and 9 segments (the model's choice is at most 3 % from the best):
-//   1 x 16384 tokens, 32 heads:  1192   855  916  889  913   (3)
-//   1 x 65536, 16 heads:         4302  2853 2251 1659 1650   (9)
-//   1 x 2048, 32 heads:           176   155  171  193  201   (3)
-//   1 x 8192, 64 heads:           707   872  841  866  959   (whole)
+// sequences whole, in 3, 4, 6 and 9 segments, and in as many as the model takes:
+//   1 x 16384 tokens, 32 heads:  1192   855  916  889  913    861 (8)
+//   1 x 65536, 16 heads:         4302  2853 2251 1659 1650   1650 (9)
+//   1 x 2048, 32 heads:           176   155  171  193  201    155 (3)
+//   1 x 8192, 64 heads:           707   872  841  866  959    699 (2)
 int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_t &units) {
     const int64_t seqs = num_seqs > 0 ? num_seqs : B, heads = seqs * H, sms = 152;
     const int64_t total = max_chunks(B, T, num_seqs, BT);

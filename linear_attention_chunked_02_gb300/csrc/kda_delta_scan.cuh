@@ -983,9 +983,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 }
 
 // The segments' maps chained: the state that segment i + 1 of a sequence starts from replaces N of
-// segment i.  A block has 16 columns of one sequence-head, a thread four of them in two rows.  FP32; the sequence's first segment gave its state itself.  M comes through shared memory, the
-// next one's copy under way during a product.
-constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 132;
+// segment i.  A block has 16 columns of one sequence-head, a thread four of them in two rows.  FP32;
+// the sequence's first segment gave its state itself.  M comes through shared memory 64 columns
+// at a time, the next ones' copy under way during a product: at that size two blocks share an SM,
+// and the 256 blocks of 32 heads are one wave (8 segments: 45 us, 57 with all of M staged).
+constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 68;
 constexpr int JOIN_BYTES = 2 * 128 * JOIN_PITCH * 4;
 static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const DeltaParams p) {
     extern __shared__ __align__(16) float join_m[];
@@ -1014,13 +1016,15 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
     if (u0 < 0 || int64_t(u0) + parts > p.n_units) return;  // malformed cu_seqlens
     const int64_t sz = int64_t(p.K) * p.V, tz = sz + int64_t(p.K) * p.K;
     float *map0 = p.trans + (int64_t(u0) * p.H + h) * tz;
-    const int k4 = p.K / 4;                                 // 16-byte pieces of a row of M
-    auto fetch = [&](int i) {
+    const int halves = p.K > 64 ? 2 : 1;
+    auto fetch = [&](int j) {                               // columns 64 (j % halves) .. of segment j / halves's M
+        const int i = halves == 2 ? j >> 1 : j, k0 = halves == 2 ? 64 * (j & 1) : 0;
         if (i < parts - 1) {
-            const float *m = map0 + int64_t(i) * p.H * tz + sz;
-            float *to = join_m + (i & 1) * 128 * JOIN_PITCH;
-            for (int j = tid; j < p.K * k4; j += JOIN_THREADS) {
-                const int row = j / k4, x = 4 * (j - row * k4);
+            const int k4 = min(64, p.K - k0) / 4;           // 16-byte pieces of a row
+            const float *m = map0 + int64_t(i) * p.H * tz + sz + k0;
+            float *to = join_m + (j & 1) * 128 * JOIN_PITCH;
+            for (int x4 = tid; x4 < p.K * k4; x4 += JOIN_THREADS) {
+                const int row = x4 / k4, x = 4 * (x4 - row * k4);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + row * JOIN_PITCH + x)),
                              "l"(m + int64_t(row) * p.K + x) : "memory");
             }
@@ -1033,32 +1037,37 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
         *reinterpret_cast<float4 *>(&S[r][c]) = *row(0, 0);
         *reinterpret_cast<float4 *>(&S[r + 1][c]) = *row(0, 1);
     }
-    fetch(1);
+    fetch(halves);
     for (int i = 1; i < parts - 1; ++i) {
-        fetch(i + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
         float4 a[2];
         if (r < p.K) {
             a[0] = *row(i, 0);
             a[1] = *row(i, 1);
-            const float *m = join_m + (i & 1) * 128 * JOIN_PITCH + r * JOIN_PITCH;
+        }
+        for (int j = halves * i; j < halves * (i + 1); ++j) {
+            fetch(j + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            if (r < p.K) {
+                const int k0 = 64 * (j - halves * i), kn = min(64, p.K - k0);
+                const float *m = join_m + (j & 1) * 128 * JOIN_PITCH + r * JOIN_PITCH;
 #pragma unroll 2
-            for (int k = 0; k < p.K; k += 4) {
-                const float4 m0 = *reinterpret_cast<const float4 *>(m + k), m1 = *reinterpret_cast<const float4 *>(m + JOIN_PITCH + k);
-                const float mk[2][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}};
+                for (int k = 0; k < kn; k += 4) {
+                    const float4 m0 = *reinterpret_cast<const float4 *>(m + k), m1 = *reinterpret_cast<const float4 *>(m + JOIN_PITCH + k);
+                    const float mk[2][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 s = *reinterpret_cast<const float4 *>(&S[k + j][c]);
+                    for (int e4 = 0; e4 < 4; ++e4) {
+                        const float4 s = *reinterpret_cast<const float4 *>(&S[k0 + k + e4][c]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        a[e].x = fmaf(mk[e][j], s.x, a[e].x); a[e].y = fmaf(mk[e][j], s.y, a[e].y);
-                        a[e].z = fmaf(mk[e][j], s.z, a[e].z); a[e].w = fmaf(mk[e][j], s.w, a[e].w);
+                        for (int e = 0; e < 2; ++e) {
+                            a[e].x = fmaf(mk[e][e4], s.x, a[e].x); a[e].y = fmaf(mk[e][e4], s.y, a[e].y);
+                            a[e].z = fmaf(mk[e][e4], s.z, a[e].z); a[e].w = fmaf(mk[e][e4], s.w, a[e].w);
+                        }
                     }
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
         if (r < p.K) {
             *row(i, 0) = *reinterpret_cast<float4 *>(&S[r][c]) = a[0];
             *row(i, 1) = *reinterpret_cast<float4 *>(&S[r + 1][c]) = a[1];
