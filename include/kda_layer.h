@@ -47,8 +47,12 @@ typedef enum {
 #define KDA_NORM_MAX_DIM 16384
 
 /*
- * Workspace bytes kda_delta_prefill needs for this shape (0 for an empty or
- * invalid one).  Pure host arithmetic.
+ * Workspace bytes kda_delta_prefill needs for this shape: 0 for an empty or
+ * invalid one, and for sequences of fewer than 16 tokens on average, which run
+ * token by token; else 32,896 for each chunk of 64 tokens and head, and where
+ * sequences are split (few heads, many chunks) K (K + V) 4 for each segment and
+ * head.  It grows with T and depends on nothing but the arguments.  Pure host
+ * arithmetic.
  */
 KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K,
                                                 int32_t V);
@@ -81,7 +85,21 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  *               too small).
  *
  * Sequences of no tokens copy their state (zeros without state_in).  With T == 0
- * or B == 0 there is nothing to read but the states.
+ * or B == 0 there is nothing to read but the states.  Rows of T past the last
+ * sequence of cu_seqlens are not written.
+ *
+ * Accuracy.  Products keep FP32's 22 to 24 bits of their operands, the states and
+ * all sums are FP32: outputs and states are within about 1e-6 of the 64-bit
+ * result's norm (FP32), or within the output type's rounding.  For BF16 outputs the
+ * queries' and the chunk's own products are rounded to 11 bits first.  Any decay is
+ * allowed: channels that fall by more than e^-48 over half a chunk, and chunks that
+ * clear the state, take slower ways of the same accuracy.  The result does not
+ * depend on the values in other heads and sequences, nor on what the workspace
+ * held; repeated calls give the same bits.
+ *
+ * The call launches two to four kernels and allocates nothing; it may be captured
+ * into a graph after one call of the same type and widths (K = V = 128 or not) on
+ * the device, which sets the kernels' shared memory sizes.
  */
 KDA_API kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta,
                                        void *o, const float *state_in, float *state_out, const int32_t *slots,

@@ -26,13 +26,16 @@
 //   * warps 2 and 3 of the first CTA: the scan's list of segments, from cu_seqlens;
 //   * warp 0: MMA issue; warp 1: TMA loads of k, q and g in slices of 32 channels into a
 //     ring, swizzled so that both passes of the transform read them without conflicts;
-//   * warps 8-15 and 16-23 (transform): every second slice each.  First lane = channel, warp = eight
-//     rows: E, summed in registers with one exchange of eight totals to a channel, takes
+//   * warps 8-15 and 16-23 (transform): every second slice each.  First a thread has four rows of two
+//     channels: E, summed in registers with one exchange of eight totals to a channel, takes
 //     g's place.  Then lane = row: K e^E and Q e^E to tensor memory, K e^{-E} to shared;
 //   * warps 4, 5 (A) and 6, 7 (P): the accumulator's rows out of tensor memory; A
 //     with beta and the mask into the solve's tile, P into its image;
 //   * warps 24-27: two pairs, each the 64-token solve of every second chunk-head,
 //     and M's image.
+// 16 x 512 tokens x 64 heads of BF16, K = 128: 203 us and 710 MB, 3.5 TB/s.  What bounds it is issue: 160
+// million warp instructions, 69 % of the slots; the transform groups and the solve pairs
+// are both busy nearly all the time (7400 and 6500 cycles to a chunk-head).
 // Five kinds of code run at once on an SM whose instruction cache holds about 32 KB of
 // them: with everything unrolled (100 KB) half the cache's requests missed and
 // that, not any pipe, set the time (424 us under the profiler, 16 x 512 tokens x 64

@@ -40,15 +40,19 @@
 //   * warps 0-15 (chain): four warps to each lane quarter, a quarter of the columns each; S in
 //     registers.  What bounds the walk is their path from state to state, so all
 //     else is on other warps;
-//   * warps 16-23 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk, 64 channels at a
-//     time; a thread has two channels of eight rows, so that sums along the rows run in
-//     registers and eight tokens of a channel make one 16-byte store;
+//   * warps 16-23 (operands): K e^G, scale Q e^G, K e^{G_C-G} of the next chunk; a thread has two or
+//     four channels of eight rows, so that sums along the rows run in registers and eight tokens
+//     of a channel make one 16-byte store;
 //   * warps 24-27 (output): O, a lane quarter each;
 //   * warp 28: MMA issue; warps 29, 30 and 31: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
 //     little in flight), so 16-bit q, k and g are staged in shared memory, 32-bit ones of up to 64
 //     channels too (the scan of 2 x 1000 tokens, 16 heads, K = 64: 73 us, not 77); of more channels they find no room
 //     there and are read directly.
+// 16 x 512 tokens x 64 heads of BF16, K = V = 128: 250 us and 1055 MB, 4.2 TB/s; 4.7 us a chunk and
+// CTA.  179 million warp instructions take 65 % of the issue slots, and the chain and the operand
+// warps each need about the whole of a chunk's 9000 cycles.  With segments (1 x 16384 x 32 heads):
+// N and M 333 us (2.9 us a chunk), the join 45, the walk 267.
 #pragma once
 
 #include "kda_delta_prep.cuh"
