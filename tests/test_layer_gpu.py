@@ -671,3 +671,24 @@ def test_refusals(kda):
     wide = torch.zeros(1, 16385, device=DEV)
     with pytest.raises(kda.KdaError):
         kda.add_norm(wide, None, wide[0])
+
+
+@pytest.mark.parametrize("dtype, K", [(F32, 64), (F32, 128), (F16, 128), (BF16, 96)], ids=str)
+def test_prefill_batch_rows_do_not_mix(kda, dtype, K):
+    """A dense batch whose middle row is NaN: its neighbours' last chunks are partial."""
+    x = Rule([70, 70, 70], K=K, dtype=dtype, packed=False, seed=41)
+    wo, wS = x.want()
+    for t in (x.q, x.k, x.v, x.g, x.beta):
+        t[1] = float("nan")
+    o, S = x.run(kda)
+    for n, (a, b) in enumerate(x.rows()):
+        if n != 1:
+            close(o[a:b], wo[n], dtype, f"o {n}")
+            close(S[n], wS[n], F32, f"state {n}")
+
+
+@pytest.mark.parametrize("batch, tokens", [(1, 1500), (2, 1500), (3, 1030), (5, 2048)])
+def test_prefill_split_batches(kda, batch, tokens):
+    """Dense batches of few heads, whose rows are split into segments."""
+    x = Rule([tokens] * batch, H=1, Hk=1, dtype=F32, packed=False, seed=42, rate=0.02, initial=True)
+    x.check(kda)
