@@ -65,12 +65,12 @@ bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }
 
 template <typename T>
 cudaError_t launch_rec(const DeltaParams &p, int sms, cudaStream_t s) {
-    // whole heads to a block once they fill the GPU, else 32 columns each.  A step of BF16, K = V = 128,
-    // in us, whole and split: 3.9 and 3.0 at 32 heads, 7.4 and 5.7 at 128, 9.2 and 10.0 at 288, 12.1 and
-    // 10.9 at 320, 15.7 and 15.8 at 512, 51 and 59 at 2048, 355 and 444 at 16384
+    // 64 columns of a head to a block, or 32 where there are few heads.  A step of BF16, K = V = 128, in us, by
+    // 64 and by 32: 3.2 and 3.3 at 32 heads, 6.6 and 5.5 at 128, 8.4 and 9.3 at 256, 14.6 and 16.0 at 512,
+    // 44 and 53 at 2048, 313 and 426 at 16384
     const int64_t heads = int64_t(p.nseq) * p.H;
-    if (p.V == 128 && heads >= 2 * sms)
-        return launch_pdl(true, kda_delta_rec_kernel<T, 32>, unsigned(heads), REC_THREADS, 0, s, p);
+    if (p.V % 64 == 0 && heads >= sms)
+        return launch_pdl(true, kda_delta_rec_kernel<T, 16>, unsigned(heads * (p.V / 64)), REC_THREADS, 0, s, p);
     return launch_pdl(true, kda_delta_rec_kernel<T, 8>, unsigned(heads * (p.V / 32)), REC_THREADS, 0, s, p);
 }
 
