@@ -231,8 +231,10 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
     }
 }
 
-// W128: K and V are 128, which makes every row pitch on chip an immediate.
-template <typename T, bool PLO, bool W128, bool TRANS>
+// KW 128: K and V are 128, which makes every row pitch on chip an immediate; 64: K is at most 64; 0: other
+// widths.  (One kernel for the last two, which reads FP32 both staged and not, took 592 us for 64 x 512
+// tokens, 32 heads of K = 64, V = 128; its own takes 434.)
+template <typename T, bool PLO, int KW, bool TRANS>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SCAN_OFF_TMEM);
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
     constexpr int NI = scan_nimg<PLO>();
-    const bool STAGED = W128 ? scan_staged<T>(128) : scan_staged<T>(p.K);
+    constexpr bool W128 = KW == 128, STAGED = scan_staged<T>(KW == 64 ? 64 : 128);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     auto image_at = [&](const Walk1 &x) { return p.ws + (int64_t(x.before) * p.H + x.h) * img_bytes<PLO>(); };
     const int32_t w0 = blockIdx.x, wstep = gridDim.x;
     const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
-    const int nh = W128 || K > 64 ? 2 : 1;                       // halves of 64 channels
+    constexpr int nh = KW == 64 ? 1 : 2;                         // halves of 64 channels
     bool ok = true;
 
     static_assert(4 * 80 + 2 * 64 + 40 + 24 <= SCAN_THREADS / 128 * SCAN_REGISTERS, "the groups' shares");
@@ -685,33 +687,36 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 float2 G = both(0.f);
                 for (int w = 0; w < rg; ++w) G = __fadd2_rn(G, *reinterpret_cast<const float2 *>(tb + w * 128));
                 unsigned char *kq = sm + SCAN_OFF_KQ + x * 8192 + rg * 1024 + 4 * (lane & 3);
-                raw rk[8], rq[8];                          // all loads before the first store
-                float2 g[8];
                 const int d = chan(x);
                 const float2 sk = both(W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
+#pragma unroll 1
+                for (int b = 0; b < 8; b += 4) {
+                    raw rk[4], rq[4];                      // all loads before the first store
+                    float2 g[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    rk[i] = two(kp, i, d);
-                    if (!TRANS) rq[i] = two(qp, i, d);
-                    g[i] = decay(i, d);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    G = __ffma2_rn(g[i], both(L2E), G);
-                    const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
-                    const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
-                    uint32_t kh, kl, qh = 0u, ql = 0u;
-                    split_f16(kv.x, kv.y, kh, kl);
-                    if (!TRANS) {
-                        const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
-                        if (PLO) split_f16(qv.x, qv.y, qh, ql);
-                        else qh = round_f16(qv.x, qv.y);
+                    for (int i = 0; i < 4; ++i) {
+                        rk[i] = two(kp, b + i, d);
+                        if (!TRANS) rq[i] = two(qp, b + i, d);
+                        g[i] = decay(b + i, d);
                     }
-                    unsigned char *at = kq + i * 128 + 16 * ((lane >> 2) ^ i);
-                    *reinterpret_cast<uint32_t *>(at) = kh;
-                    *reinterpret_cast<uint32_t *>(at + 16384) = kl;
-                    if (!TRANS) *reinterpret_cast<uint32_t *>(at + 32768) = qh;
-                    if (!TRANS && PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        G = __ffma2_rn(g[i], both(L2E), G);
+                        const float2 e = __fmul2_rn(make_float2(ex2(G.x), ex2(G.y)), sk);
+                        const float2 kv = __fmul2_rn(W2::wide(rk[i]), e);
+                        uint32_t kh, kl, qh = 0u, ql = 0u;
+                        split_f16(kv.x, kv.y, kh, kl);
+                        if (!TRANS) {
+                            const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
+                            if (PLO) split_f16(qv.x, qv.y, qh, ql);
+                            else qh = round_f16(qv.x, qv.y);
+                        }
+                        unsigned char *at = kq + (b + i) * 128 + 16 * ((lane >> 2) ^ (b + i));
+                        *reinterpret_cast<uint32_t *>(at) = kh;
+                        *reinterpret_cast<uint32_t *>(at + 16384) = kl;
+                        if (!TRANS) *reinterpret_cast<uint32_t *>(at + 32768) = qh;
+                        if (!TRANS && PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+                    }
                 }
                 if (rg == 7)                               // here G is the whole chunk's sum
                     *reinterpret_cast<float2 *>(gam + ph * 128 + 64 * x + 2 * lane) = make_float2(ex2(G.x), ex2(G.y));
