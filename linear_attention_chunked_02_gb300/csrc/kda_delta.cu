@@ -112,11 +112,12 @@ bool encode_rows(CUtensorMap *map, const void *base, int32_t dt, int64_t rows, i
 bool encode_delta(const DeltaParams &p, int32_t dt, int64_t rows, DeltaMaps &prep, DeltaMaps &scan) {
     std::memset(&prep, 0, sizeof(prep));
     std::memset(&scan, 0, sizeof(scan));
+    const int box = p.K <= 64 ? 64 : 128;                  // the scan's rows, whatever K
     return encode_rows(&prep.q, p.q, dt, rows, p.Hk, p.K, 32, true) && encode_rows(&prep.k, p.k, dt, rows, p.Hk, p.K, 32, true) &&
-           encode_rows(&scan.v, p.v, dt, rows, p.H, p.V, p.V) && encode_rows(&scan.q, p.q, dt, rows, p.Hk, p.K, p.K) &&
-           encode_rows(&scan.k, p.k, dt, rows, p.Hk, p.K, p.K) &&
+           encode_rows(&scan.v, p.v, dt, rows, p.H, p.V, 128) && encode_rows(&scan.q, p.q, dt, rows, p.Hk, p.K, box) &&
+           encode_rows(&scan.k, p.k, dt, rows, p.Hk, p.K, box) &&
            (p.gate != KDA_GATE_CHANNEL || (encode_rows(&prep.g, p.g, KDA_F32, rows, p.H, p.K, 32, true) &&
-                                           encode_rows(&scan.g, p.g, KDA_F32, rows, p.H, p.K, p.K)));
+                                           encode_rows(&scan.g, p.g, KDA_F32, rows, p.H, p.K, box)));
 }
 
 kda_status_t run_chunked(DeltaParams p, int32_t dtype, int64_t rows, cudaStream_t s) {

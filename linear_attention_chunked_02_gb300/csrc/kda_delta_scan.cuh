@@ -231,8 +231,8 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
     }
 }
 
-// KW 128: K and V are 128, which makes every row pitch on chip an immediate; 64: K is at most 64; 0: other
-// widths.  (One kernel for the last two, which reads FP32 both staged and not, took 592 us for 64 x 512
+// KW 128: K and V are 128, which makes every row pitch an immediate; 64: K is at most 64; 0: other
+// widths.  Staged rows are KP channels and 128 values long for all, zeros past K and V from the copy.  (One kernel for the last two, which reads FP32 both staged and not, took 592 us for 64 x 512
 // tokens, 32 heads of K = 64, V = 128; its own takes 434.)
 template <typename T, bool PLO, int KW, bool TRANS>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
     constexpr int NI = scan_nimg<PLO>();
     constexpr bool W128 = KW == 128, STAGED = scan_staged<T>(KW == 64 ? 64 : 128);
+    constexpr bool FOUR = W128 || (KW == 0 && STAGED);     // operands: four channels to a lane
+    constexpr int KP = KW == 64 ? 64 : 128;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int K = W128 ? 128 : p.K, V = W128 ? 128 : p.V;
     pdl_launch_dependents();
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         float S[32];                                       // S[32 part + i][v]
         const bool held = 32 * part < K;                   // K is a multiple of 32
         const int t0 = 16 * part;                          // this thread's tokens of a chunk: t0 .. t0 + 15
-        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * V + (v < V ? v : 0);
+        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * 128 + v;
         const uint32_t sop = tq + TM_SHI + 16 * part, rop = tq + TM_RHI + 8 * part;      // operand columns, hi parts
         auto put_state = [&](float s) {
 #pragma unroll
@@ -412,10 +414,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // rows past the end hold the next request's; columns past V stay in their lanes
 #pragma unroll 1
             for (int i = left > t0 ? left - t0 : 0; i < 16; ++i)
-                if (v < V) sv[i * V] = T(0.f);
+                sv[i * 128] = T(0.f);
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) vr[i] = Pair<T>(sv[2 * i * V], sv[(2 * i + 1) * V]);
+                for (int i = 0; i < 8; ++i) vr[i] = Pair<T>(sv[2 * i * 128], sv[(2 * i + 1) * 128]);
                 Pair<T> m = vr[0].abs();
 #pragma unroll
                 for (int i = 1; i < 8; ++i) m = m.max(vr[i].abs());
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 bv = fmaxf(f.x, f.y);
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) bv = max3(bv, widen1(sv[i * V]), widen1(sv[(i + 1) * V]));
+                for (int i = 0; i < 16; i += 2) bv = max3(bv, widen1(sv[i * 128]), widen1(sv[(i + 1) * 128]));
             }
             return bv;
         };
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < 8; ++i) {
                     float2 w;
                     if constexpr (sizeof(T) == 2) w = vr[i].wide();
-                    else w = run == 1 ? both(0.f) : make_float2(widen1(sv[2 * i * V]), widen1(sv[(2 * i + 1) * V]));
+                    else w = run == 1 ? both(0.f) : make_float2(widen1(sv[2 * i * 128]), widen1(sv[(2 * i + 1) * 128]));
                     w = __ffma2_rn(f, make_float2(x[2 * i], x[2 * i + 1]), __fmul2_rn(w, s2));
                     split_f16(w.x, w.y, hi[i], lo[i]);
                 }
@@ -549,8 +551,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         const int rg = warp - 16;                          // rows 8 rg .. + 7
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
-        // the next one.  Channels past K take another's values under a scale of zero.
-        const int ks = STAGED ? K : p.Hk * K, gs = STAGED ? K : p.H * K;
+        // the next one.  Channels past K are zeros where staged, else another's values under a scale of zero.
+        const int ks = STAGED ? KP : p.Hk * K, gs = STAGED ? KP : p.H * K;
         unsigned char *st = sm + scan_off_st<T, PLO>();
         float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
         uint32_t cc = 0;
@@ -567,9 +569,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const T *kp, *qp;
             const float *gp;
             if (STAGED) {
-                kp = reinterpret_cast<T *>(st) + 8 * rg * K;
-                qp = reinterpret_cast<T *>(st + 16384) + 8 * rg * K;
-                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * K;
+                kp = reinterpret_cast<T *>(st) + 8 * rg * KP;
+                qp = reinterpret_cast<T *>(st + 16384) + 8 * rg * KP;
+                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * KP;
             } else {
                 kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * K;
                 qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * K;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     }
                 __syncwarp();
             }
-            auto chan = [&](int x) { const int d = 64 * x + 2 * lane; return W128 || d < K ? d : 2 * lane % K; };
+            auto chan = [&](int x) { const int d = 64 * x + 2 * lane; return STAGED || W128 || d < K ? d : 2 * lane % K; };
             auto two = [&](const T *at, int i, int d) {
                 const bool in = STAGED || i < left;
                 return in ? *reinterpret_cast<const raw *>(at + i * ks + d) : raw{};
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (p.gate != 0) return both(gp[i]);
                 return STAGED || i < left ? *reinterpret_cast<const float2 *>(gp + i * gs + d) : both(0.f);
             };
-            // at K = 128 a lane has four channels in a row for the first two passes: half the loads and stores
+            // above 64 channels a lane has four in a row for the first two passes: half the loads and stores
             // of two (the scan of 16 x 512 tokens, 64 heads: 263 us, not 267)
             struct alignas(2 * sizeof(raw)) raw4 { raw r[2]; };
             auto four = [&](const T *at, int i) {
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 if (p.gate != 0) return make_float4(gp[i], gp[i], gp[i], gp[i]);
                 return STAGED || i < left ? *reinterpret_cast<const float4 *>(gp + i * gs + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
             };
-            if (W128) {
+            if (FOUR) {
                 float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 *reinterpret_cast<float4 *>(tot + rg * 128 + 4 * lane) = make_float4(s0.x, s0.y, s1.x, s1.y);
             }
 #pragma unroll 1
-            for (int x = 0; !W128 && x < nh; ++x) {
+            for (int x = 0; !FOUR && x < nh; ++x) {
                 float2 sum = both(0.f);
                 const int d = chan(x);
 #pragma unroll
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             named_sync<1, 256>();
             // K e^G and scale Q e^G: row r of a tile is 128 bytes, its 16-byte chunk lane / 4 at (lane / 4) ^ (r & 7)
             prep_wait(ok, &bars[SB_KQ_EMPTY], ph ^ 1, p.err);
-            if (W128) {
+            if (FOUR) {
                 float2 G[2] = {both(0.f), both(0.f)};
                 for (int w = 0; w < rg; ++w) {
                     const float4 t = *reinterpret_cast<const float4 *>(tot + w * 128 + 4 * lane);
@@ -682,13 +684,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         make_float4(ex2(G[0].x), ex2(G[0].y), ex2(G[1].x), ex2(G[1].y));
             }
 #pragma unroll 1
-            for (int x = 0; !W128 && x < nh; ++x) {
+            for (int x = 0; !FOUR && x < nh; ++x) {
                 const float *tb = tot + 64 * x + 2 * lane;
                 float2 G = both(0.f);
                 for (int w = 0; w < rg; ++w) G = __fadd2_rn(G, *reinterpret_cast<const float2 *>(tb + w * 128));
                 unsigned char *kq = sm + SCAN_OFF_KQ + x * 8192 + rg * 1024 + 4 * (lane & 3);
                 const int d = chan(x);
-                const float2 sk = both(W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
+                const float2 sk = both(STAGED || W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
 #pragma unroll 1
                 for (int b = 0; b < 8; b += 4) {
                     raw rk[4], rq[4];                      // all loads before the first store
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 const float *tb = tot + 64 * x + 2 * lane;
                 float2 after = both(0.f), y[8], g[8];
                 const int dc = chan(x);
-                const float2 sk = both(W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
+                const float2 sk = both(STAGED || W128 || 64 * x + 2 * lane < K ? sk1 : 0.f);
                 for (int w = 7; w > rg; --w) after = __fadd2_rn(after, *reinterpret_cast<const float2 *>(tb + w * 128));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -902,7 +904,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // ------------------------------------------------- loads of q, k and g
             if (STAGED) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
-                const uint32_t bytes = (TRANS ? 1 : 2) * 64 * K * sizeof(T) + (p.gate == 0 ? 64 * K * 4 : 0);
+                const uint32_t bytes = (TRANS ? 1 : 2) * 64 * KP * sizeof(T) + (p.gate == 0 ? 64 * KP * 4 : 0);
                 uint32_t cc = 0;
                 Walk1 wk = walk_at(w0, entry(w0));
                 for (int32_t w = w0; w < walks; w += wstep) {
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     prep_wait(ok, &bars[SB_V_EMPTY], (cc & 1) ^ 1, p.err);
                     __syncwarp();
                     if (tc::elect_one()) {
-                        mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * V * sizeof(T));
+                        mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * 128 * sizeof(T));
                         tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, wk.h, wk.row + 64 * c, &bars[SB_V_FULL]);
                         if (c + 1 < wk.nc) tc::prefetch_3d(&maps.v, 0, wk.h, wk.row + 64 * c + 64);
                     }
