@@ -46,9 +46,10 @@
 //   * warps 24-27 (output): O, a lane quarter each;
 //   * warp 28: MMA issue; warps 29, 30 and 31: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
-//     little in flight), so 16-bit q, k and g are staged in shared memory, 32-bit ones of up to 64
-//     channels too (the scan of 2 x 1000 tokens, 16 heads, K = 64: 73 us, not 77); of more channels they find no room
-//     there and are read directly.
+//     little in flight), so g is staged in shared memory, and q and k where they find room: of 16
+//     bits, or of 32 bits and up to 64 channels (2 x 1000 tokens, 16 heads, K = 64: 73 us, not 77).
+//     32-bit ones of more channels are read directly (64 x 512 tokens, 32 heads of
+//     K = V = 128, the whole operator: 1250 us, 1397 with g read directly too).
 // 16 x 512 tokens x 64 heads of BF16, K = V = 128: 250 us and 1055 MB, 4.2 TB/s; 4.7 us a chunk and
 // CTA.  179 million warp instructions take 65 % of the issue slots, and the chain and the operand
 // warps each need about the whole of a chunk's 9000 cycles.  With segments (1 x 16384 x 32 heads):
@@ -89,14 +90,16 @@ constexpr int scan_off_v() { return scan_off_img<PLO>() + scan_nimg<PLO>() * sca
 template <typename T, bool PLO>
 constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
 template <typename T>
-constexpr int scan_stage() { return sizeof(T) == 2 ? 65536 : 49152; }      // 32-bit: of 64 channels
+constexpr bool scan_staged(int K) { return sizeof(T) == 2 || K <= 64; }    // q and k too, not g alone
 template <typename T>
-constexpr bool scan_staged(int K) { return sizeof(T) == 2 || K <= 64; }
+constexpr int scan_off_g(int K) { return !scan_staged<T>(K) ? 0 : 32768; } // g, in the staging buffer
+template <typename T>
+constexpr int scan_stage(int K) { return scan_off_g<T>(K) + 64 * (K <= 64 ? 64 : 128) * 4; }
 template <typename T, bool PLO>
-constexpr int scan_bytes(int K) { return scan_off_st<T, PLO>() + (scan_staged<T>(K) ? scan_stage<T>() : 0) + 1024; }
+constexpr int scan_bytes(int K) { return scan_off_st<T, PLO>() + scan_stage<T>(K) + 1024; }
 static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
-static_assert(scan_bytes<float, true>(64) <= 227 * 1024 && scan_bytes<__half, true>(128) <= 227 * 1024 &&
+static_assert(scan_bytes<float, true>(64) <= 227 * 1024 && scan_bytes<float, true>(128) <= 227 * 1024 && scan_bytes<__half, true>(128) <= 227 * 1024 &&
                   scan_bytes<__nv_bfloat16, false>(128) <= 227 * 1024, "fits the shared memory of one CTA");
 // A chunk is taken token by token where its values are below 2^-16 of what the state can add to R
 // and no channel keeps more than 2^-12 of the state: what comes out is then
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         float *tot = reinterpret_cast<float *>(sm + SCAN_OFF_TOT);
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
         // the next one.  Channels past K are zeros where staged, else another's values under a scale of zero.
-        const int ks = STAGED ? KP : p.Hk * K, gs = STAGED ? KP : p.H * K;
+        const int ks = STAGED ? KP : p.Hk * K;
         unsigned char *st = sm + scan_off_st<T, PLO>();
         float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
         uint32_t cc = 0;
@@ -567,15 +570,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const int left = wk.rows - 64 * c - 8 * rg;    // live rows from this thread's first on
             const int64_t row = wk.row + 64 * c + 8 * rg;
             const T *kp, *qp;
-            const float *gp;
+            const float *gp = reinterpret_cast<float *>(st + scan_off_g<T>(KP)) + 8 * rg * KP;
             if (STAGED) {
                 kp = reinterpret_cast<T *>(st) + 8 * rg * KP;
                 qp = reinterpret_cast<T *>(st + 16384) + 8 * rg * KP;
-                gp = reinterpret_cast<float *>(st + 32768) + 8 * rg * KP;
             } else {
                 kp = static_cast<const T *>(p.k) + (row * p.Hk + hk) * K;
                 qp = static_cast<const T *>(p.q) + (row * p.Hk + hk) * K;
-                gp = p.g + (row * p.H + h) * K;
             }
             if (p.gate != 0) {                             // one decay to a row
                 if (lane < 8) sg[8 * rg + lane] = lane < left ? p.g[(row + lane) * p.H + h] : 0.f;
@@ -583,15 +584,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 gp = sg + 8 * rg;
             }
             const float2 kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + img_hdr<PLO>() + 4 * HDR_KMAX);
-            if (STAGED) {
+            if (STAGED || p.gate == 0) {
                 prep_wait(ok, &bars[SB_ST_FULL], ph, p.err);
 #pragma unroll 1
                 for (int i = left > 0 ? left : 0; i < 8; ++i)      // rows past the end hold the next request's
 #pragma unroll 1
                     for (int x = lane; x < K; x += 32) {
-                        const_cast<T *>(kp)[i * ks + x] = T(0.f);
-                        const_cast<T *>(qp)[i * ks + x] = T(0.f);
-                        if (p.gate == 0) const_cast<float *>(gp)[i * gs + x] = 0.f;
+                        if (STAGED) {
+                            const_cast<T *>(kp)[i * ks + x] = T(0.f);
+                            const_cast<T *>(qp)[i * ks + x] = T(0.f);
+                        }
+                        if (p.gate == 0) const_cast<float *>(gp)[i * KP + x] = 0.f;
                     }
                 __syncwarp();
             }
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             };
             auto decay = [&](int i, int d) {
                 if (p.gate != 0) return both(gp[i]);
-                return STAGED || i < left ? *reinterpret_cast<const float2 *>(gp + i * gs + d) : both(0.f);
+                return *reinterpret_cast<const float2 *>(gp + i * KP + d);
             };
             // above 64 channels a lane has four in a row for the first two passes: half the loads and stores
             // of two (the scan of 16 x 512 tokens, 64 heads: 263 us, not 267)
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             };
             auto decay4 = [&](int i) {
                 if (p.gate != 0) return make_float4(gp[i], gp[i], gp[i], gp[i]);
-                return STAGED || i < left ? *reinterpret_cast<const float4 *>(gp + i * gs + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                return *reinterpret_cast<const float4 *>(gp + i * KP + 4 * lane);
             };
             if (FOUR) {
                 float2 s0 = both(0.f), s1 = both(0.f);
@@ -902,9 +905,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             }
         } else if (warp == 29) {
             // ------------------------------------------------- loads of q, k and g
-            if (STAGED) {
+            if (STAGED || p.gate == 0) {
                 unsigned char *st = sm + scan_off_st<T, PLO>();
-                const uint32_t bytes = (TRANS ? 1 : 2) * 64 * KP * sizeof(T) + (p.gate == 0 ? 64 * KP * 4 : 0);
+                const uint32_t bytes = (STAGED ? (TRANS ? 1 : 2) * 64 * KP * sizeof(T) : 0) + (p.gate == 0 ? 64 * KP * 4 : 0);
                 uint32_t cc = 0;
                 Walk1 wk = walk_at(w0, entry(w0));
                 for (int32_t w = w0; w < walks; w += wstep) {
@@ -916,9 +919,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         if (tc::elect_one()) {
                             const int r = wk.row + 64 * c;
                             mbar_arrive_expect_tx(&bars[SB_ST_FULL], bytes);
-                            tma_load_3d(st, &maps.k, 0, hk, r, &bars[SB_ST_FULL]);
-                            if (!TRANS) tma_load_3d(st + 16384, &maps.q, 0, hk, r, &bars[SB_ST_FULL]);
-                            if (p.gate == 0) tma_load_3d(st + 32768, &maps.g, 0, wk.h, r, &bars[SB_ST_FULL]);
+                            if (STAGED) tma_load_3d(st, &maps.k, 0, hk, r, &bars[SB_ST_FULL]);
+                            if (STAGED && !TRANS) tma_load_3d(st + 16384, &maps.q, 0, hk, r, &bars[SB_ST_FULL]);
+                            if (p.gate == 0) tma_load_3d(st + scan_off_g<T>(KP), &maps.g, 0, wk.h, r, &bars[SB_ST_FULL]);
                             // the next chunk's on their way to L2 meanwhile
                             const bool more = c + 1 < wk.nc;
                             if (more || nx.nc > 0) {
