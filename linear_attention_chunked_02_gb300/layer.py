@@ -11,7 +11,6 @@ produced the inputs, and the outputs' use on other streams, is the caller's.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -22,14 +21,11 @@ WIDTHS = (32, 64, 96, 128)
 ACT_CODE = {"sigmoid": 0, "silu": 1}
 
 
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def _launch_on(device: int, stream: Optional[torch.cuda.Stream]):
-    """Context in which `device` is current and, if given, `stream` is its current stream."""
+def _elsewhere(device: int, stream: Optional[torch.cuda.Stream]):
+    """None where the call can run as it is; else the context in which it can: `stream`, or `device` made current."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return _NO_CONTEXT if device == torch.cuda.current_device() else torch.cuda.device(device)
+    return None if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _current_stream(device: int) -> int:
@@ -137,6 +133,10 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     """
     device = _on_gpu("q k v g beta cu_seqlens initial_state final_state slots out workspace", q, k, v, g, beta,
                      cu_seqlens, initial_state, final_state, slots, out, workspace)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return delta_prefill(q, k, v, g, beta, cu_seqlens, scale, initial_state, final_state, slots, out, workspace)
     Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 2)
     B, T = q.shape[:2]
     cu_seqlens = _int32("cu_seqlens", cu_seqlens)
@@ -153,22 +153,21 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
             _state(name, t, entries, H, K, V)
-    with _launch_on(device, stream):
-        q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
-        slots = slots.contiguous() if slots is not None else None
-        out = _output("out", out, v)
-        cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
-        if final_state is None:
-            final_state = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
-        need = delta_prefill_workspace_size(B, T, H, nseq, K, V)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        st = lib().kda_delta_prefill(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
-            _ptr(initial_state), final_state.data_ptr(), _ptr(slots), entries, _ptr(cu_seqlens), nseq, B, T,
-            Hk, H, K, V, DTYPE_CODE[q.dtype], gate, float(K ** -0.5 if scale is None else scale), _ptr(workspace), ws_bytes,
-            _current_stream(device))
+    q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
+    slots = slots.contiguous() if slots is not None else None
+    out = _output("out", out, v)
+    cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
+    if final_state is None:
+        final_state = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
+    need = delta_prefill_workspace_size(B, T, H, nseq, K, V)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib().kda_delta_prefill(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
+        _ptr(initial_state), final_state.data_ptr(), _ptr(slots), entries, _ptr(cu_seqlens), nseq, B, T,
+        Hk, H, K, V, DTYPE_CODE[q.dtype], gate, float(K ** -0.5 if scale is None else scale), _ptr(workspace), ws_bytes,
+        _current_stream(device))
     check(st, "kda_delta_prefill")
     return out, final_state
 
@@ -183,20 +182,23 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     without slots.  A slot outside the pool (-1 for padding) reads zeros and stores nothing.
     """
     device = _on_gpu("q k v g beta state slots out", q, k, v, g, beta, state, slots, out)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return delta_step(q, k, v, g, beta, state, slots, scale, out)
     Hk, H, K, V, gate = _rule_shapes(q, k, v, g, beta, 1)
     N = q.shape[0]
     slots = _int32("slots", slots, N)
     _state("state", state, None, H, K, V)
     if slots is None and state.shape[0] < N:
         raise ValueError(f"{N} requests and a pool of {state.shape[0]} states")
-    with _launch_on(device, stream):
-        q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
-        slots = slots.contiguous() if slots is not None else None
-        out = _output("out", out, v)
-        st = lib().kda_delta_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), state.data_ptr(),
-            _ptr(slots), state.shape[0], N, Hk, H, K, V, DTYPE_CODE[q.dtype], gate,
-            float(K ** -0.5 if scale is None else scale), _current_stream(device))
+    q, k, v, g, beta = _aligned(q), _aligned(k), _aligned(v), _aligned(g), _aligned(beta)
+    slots = slots.contiguous() if slots is not None else None
+    out = _output("out", out, v)
+    st = lib().kda_delta_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), state.data_ptr(),
+        _ptr(slots), state.shape[0], N, Hk, H, K, V, DTYPE_CODE[q.dtype], gate,
+        float(K ** -0.5 if scale is None else scale), _current_stream(device))
     check(st, "kda_delta_step")
     return out
 
@@ -218,15 +220,18 @@ def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Te
     residual may be None (r = alpha x); residual_out may be residual and out may be x.
     """
     device = _on_gpu("x residual weight out residual_out", x, residual, weight, out, residual_out)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return add_norm(x, residual, weight, eps, alpha, out, residual_out)
     _norm_shapes(x, weight, residual, "residual")
     dim = x.shape[-1]
-    with _launch_on(device, stream):
-        x, weight = x.contiguous(), weight.contiguous()
-        residual = residual.contiguous() if residual is not None else None
-        out, residual_out = _output("out", out, x), _output("residual_out", residual_out, x)
-        st = lib().kda_add_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(),
-                                residual_out.data_ptr(), x.numel() // dim if dim else 0, dim, alpha, eps,
-                                DTYPE_CODE[x.dtype], _current_stream(device))
+    x, weight = x.contiguous(), weight.contiguous()
+    residual = residual.contiguous() if residual is not None else None
+    out, residual_out = _output("out", out, x), _output("residual_out", residual_out, x)
+    st = lib().kda_add_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), out.data_ptr(),
+                            residual_out.data_ptr(), x.numel() // dim if dim else 0, dim, alpha, eps,
+                            DTYPE_CODE[x.dtype], _current_stream(device))
     check(st, "kda_add_norm")
     return out, residual_out
 
@@ -241,13 +246,16 @@ def gated_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: f
     if activation not in ACT_CODE:
         raise ValueError(f"unknown activation {activation!r}")
     device = _on_gpu("x gate weight out", x, gate, weight, out)
+    other = _elsewhere(device, stream)
+    if other is not None:
+        with other:
+            return gated_norm(x, gate, weight, eps, activation, out)
     _norm_shapes(x, weight, gate, "gate")
     dim = x.shape[-1]
-    with _launch_on(device, stream):
-        x, gate, weight = x.contiguous(), gate.contiguous(), weight.contiguous()
-        out = _output("out", out, x)
-        st = lib().kda_gated_norm(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), out.data_ptr(),
-                                  x.numel() // dim if dim else 0, dim, eps, ACT_CODE[activation], DTYPE_CODE[x.dtype],
-                                  _current_stream(device))
+    x, gate, weight = x.contiguous(), gate.contiguous(), weight.contiguous()
+    out = _output("out", out, x)
+    st = lib().kda_gated_norm(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), out.data_ptr(),
+                              x.numel() // dim if dim else 0, dim, eps, ACT_CODE[activation], DTYPE_CODE[x.dtype],
+                              _current_stream(device))
     check(st, "kda_gated_norm")
     return out
