@@ -97,9 +97,9 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  * depend on the values in other heads and sequences, nor on what the workspace
  * held; repeated calls give the same bits.
  *
- * The call launches two to four kernels and allocates nothing; it may be captured
- * into a graph after one call of the same type and widths (K = V = 128 or not) on
- * the device, which sets the kernels' shared memory sizes.
+ * The call launches one to four kernels and allocates nothing; it may be captured
+ * into a graph after one call of the same type and widths on the device, which sets
+ * the kernels' shared memory sizes.
  */
 KDA_API kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta,
                                        void *o, const float *state_in, float *state_out, const int32_t *slots,

@@ -692,3 +692,20 @@ def test_prefill_split_batches(kda, batch, tokens):
     """Dense batches of few heads, whose rows are split into segments."""
     x = Rule([tokens] * batch, H=1, Hk=1, dtype=F32, packed=False, seed=42, rate=0.02, initial=True)
     x.check(kda)
+
+
+@pytest.mark.parametrize("lens", [(70, 33), (5, 3)], ids=["chunks", "tokens"])
+def test_prefill_rows_past_the_last_sequence(kda, lens):
+    """Rows of the packed tensors that belong to no sequence are neither read nor written."""
+    x = Rule([*lens, 20], dtype=BF16, seed=44)
+    used = sum(lens)
+    wo, wS = x.want()
+    for t in (x.q, x.k, x.v, x.g, x.beta):
+        t[0, used:] = float("nan")
+    out = torch.full((1, used + 20, 2, 128), 3.0, dtype=BF16, device=DEV)
+    o, S = kda.delta_prefill(*x.args(), cu_seqlens=x.cu[:-1].to(DEV), out=out)
+    torch.cuda.synchronize()
+    assert torch.all(out[0, used:] == 3)
+    for n, (a, b) in enumerate(list(x.rows())[:-1]):
+        close(o[0, a:b], wo[n], BF16, f"o {n}")
+        close(S[n], wS[n], F32, f"state {n}")
