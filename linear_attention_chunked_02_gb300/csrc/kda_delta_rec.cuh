@@ -44,7 +44,8 @@ struct DeltaParams {
     unsigned char *ws;          // workspace: one image to a chunk-head
     int32_t seg;                // chunks to a segment of a sequence; 0: sequences are not split
     int32_t n_units;            // bound on segments (seg == 0: sequences)
-    float *trans;               // [n_units][H]{N [K, V], M [K, K]}: what a segment does to the state
+    float *trans;               // [n_units][H]{N [K, V], M [K, K]}: what a segment does to the state; in N's place
+                                // of a sequence's last segment, the state that the sequence starts from
     int4 *units;                // packed: [n_units] segments (kda_delta_prep.cuh writes them)
 };
 

@@ -32,7 +32,8 @@
 // this kernel (TRANS) takes N from the walk without outputs, from zero states (the sequence's
 // own in its first segment), and M from the walk of the identity with v = 0;
 // kda_delta_join_kernel chains them into every segment's initial state; then all
-// segments are walked at once.
+// segments are walked at once.  That last run reads no state that it may write: what the first segments
+// start from was copied by the first run, since a state pool is usually updated in place.
 //
 // One persistent CTA of eight warpgroups per SM, whose roles go through its walks (sequence-heads, or
 // their segments) as one stream of chunks: the loads and operands of the next walk
@@ -318,7 +319,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         // malformed cu_seqlens must not lead past the workspace; the last segment's map is not
         // needed, nor what the first makes of another state than its own
         if (x.before < 0 || (int64_t(x.before) + x.nc) * p.H > p.n_tasks) x.nc = 0;
-        x.idle = w >= walks || e.w <= 0 || (TRANS && (x.last || (x.run == 1 && e.y == 0)));
+        // (nor past the maps: with them, all units of a sequence are listed)
+        x.idle = w >= walks || e.w <= 0 || (p.seg > 0 && int64_t(x.unit) - e.y + e.w > p.n_units) ||
+                 (TRANS && (x.last || (x.run == 1 && e.y == 0)));
         if (x.idle) x.nc = 0;
         return x;
     };
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         const int run = x.run, W = run == 1 ? K : V;       // columns of the state that is walked
         const bool mine = v < W && held;
         // the state that it starts from, and where it ends
-        float *to = nullptr;
+        float *to = nullptr, *keep = nullptr;
         {
             const float *from = nullptr;
             if (!x.idle) {
@@ -394,6 +397,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     if (!TRANS) from = map - int64_t(p.H) * tz;        // chained into the segment before
                 } else if (p.state_in != nullptr && e >= 0) {
                     from = p.state_in + (int64_t(e) * p.H + x.h) * sz;
+                    // The last segment's walk may store over that entry (state_out may be state_in) before the
+                    // last run gets to this one: walks go to CTAs in turn, and nothing orders two of them.  So
+                    // the first run copies the state to the last segment's place, whose own map nobody makes or
+                    // reads, and the last run starts from the copy.
+                    if (x.e.w > 1) {
+                        float *copy = map + int64_t(x.e.w - 1) * p.H * tz;
+                        if (TRANS) keep = copy;
+                        else from = copy;
+                    }
                 }
                 if (TRANS) to = map + (run == 1 ? sz : 0);
                 else if (x.last && p.state_out != nullptr && e >= 0) to = p.state_out + (int64_t(e) * p.H + x.h) * sz;
@@ -402,6 +414,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const bool read = from != nullptr && mine;
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = read ? sp[int64_t(i) * W] : 0.f;
+            if (TRANS && keep != nullptr && mine) {
+                float *kp = keep + int64_t(32 * part) * W + v;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) kp[int64_t(i) * W] = S[i];
+            }
             if (run == 1) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) S[i] = 32 * part + i == v && held ? 1.f : 0.f;
