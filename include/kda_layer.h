@@ -89,9 +89,8 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  * sequence of cu_seqlens are not written.
  *
  * Accuracy.  Products keep FP32's 22 to 24 bits of their operands, the states and
- * all sums are FP32: outputs and states are within about 1e-6 of the 64-bit
- * result's norm (FP32), or within the output type's rounding.  For BF16 outputs the
- * queries' and the chunk's own products are rounded to 11 bits first.  Any decay is
+ * all sums are FP32, whatever the type: outputs and states are within about 1e-6 of
+ * the 64-bit result's norm, before a 16-bit output's one rounding.  Any decay is
  * allowed: channels that fall by more than e^-48 over half a chunk, and chunks that
  * clear the state, take slower ways of the same accuracy.  The result does not
  * depend on the values in other heads and sequences, nor on what the workspace

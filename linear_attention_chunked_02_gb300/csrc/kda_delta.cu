@@ -58,7 +58,7 @@ int32_t segment_chunks(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int64_
 }
 
 size_t image_bytes(int64_t B, int64_t T, int32_t H, int32_t num_seqs) {
-    return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * img_bytes<true>();
+    return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * IMG_BYTES;
 }
 
 bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }

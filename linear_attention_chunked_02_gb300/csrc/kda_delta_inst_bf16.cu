@@ -4,6 +4,6 @@
 namespace kda {
 cudaError_t launch_chunked_bf16(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
                                cudaStream_t s) {
-    return launch_chunked<__nv_bfloat16, false>(p, prep, scan, device, sms, s);
+    return launch_chunked<__nv_bfloat16>(p, prep, scan, device, sms, s);
 }
 }  // namespace kda

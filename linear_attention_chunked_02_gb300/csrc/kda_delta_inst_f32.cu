@@ -4,6 +4,6 @@
 namespace kda {
 cudaError_t launch_chunked_f32(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
                                cudaStream_t s) {
-    return launch_chunked<float, true>(p, prep, scan, device, sms, s);
+    return launch_chunked<float>(p, prep, scan, device, sms, s);
 }
 }  // namespace kda

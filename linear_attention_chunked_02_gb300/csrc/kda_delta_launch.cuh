@@ -21,49 +21,48 @@ cudaError_t kernel_ready(F *fn, int bytes, int registers) {
 }
 
 // Once per device.
-template <typename T, bool PLO, int KW>
+template <typename T, int KW>
 cudaError_t chunked_ready(int device) {
     static std::mutex mu;
     static bool done[64] = {false};
     std::lock_guard<std::mutex> lock(mu);
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (done[device]) return cudaSuccess;
-    cudaError_t e = kernel_ready(kda_delta_prep_kernel<T, PLO>, prep_bytes<T>(), PREP_REGISTERS);
+    cudaError_t e = kernel_ready(kda_delta_prep_kernel<T>, prep_bytes<T>(), PREP_REGISTERS);
     if (e == cudaSuccess)
-        e = kernel_ready(kda_delta_scan_kernel<T, PLO, KW, false>, scan_bytes<T, PLO>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
+        e = kernel_ready(kda_delta_scan_kernel<T, KW, false>, scan_bytes<T>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
     if (e == cudaSuccess)
-        e = kernel_ready(kda_delta_scan_kernel<T, PLO, KW, true>, scan_bytes<T, PLO>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
+        e = kernel_ready(kda_delta_scan_kernel<T, KW, true>, scan_bytes<T>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
     if (e == cudaSuccess) e = kernel_ready(kda_delta_join_kernel, JOIN_BYTES, 0);
     done[device] = e == cudaSuccess;
     return e;
 }
 
-template <typename T, bool PLO, int KW>
+template <typename T, int KW>
 cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
                           cudaStream_t s) {
-    cudaError_t e = chunked_ready<T, PLO, KW>(device);
+    cudaError_t e = chunked_ready<T, KW>(device);
     if (e != cudaSuccess) return e;
     auto blocks = [&](int64_t n) { return unsigned(n < sms ? n : sms); };     // persistent, one to an SM
     const int64_t walks = int64_t(p.n_units) * p.H;
-    const size_t bytes = size_t(scan_bytes<T, PLO>(p.K));
-    e = launch_pdl(true, kda_delta_prep_kernel<T, PLO>, blocks(p.n_tasks), PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
+    const size_t bytes = size_t(scan_bytes<T>(p.K));
+    e = launch_pdl(true, kda_delta_prep_kernel<T>, blocks(p.n_tasks), PREP_THREADS, size_t(prep_bytes<T>()), s, prep, p);
     if (e == cudaSuccess && p.seg > 0) {
-        e = launch_pdl(true, kda_delta_scan_kernel<T, PLO, KW, true>, blocks(2 * walks), SCAN_THREADS, bytes, s, scan, p);
+        e = launch_pdl(true, kda_delta_scan_kernel<T, KW, true>, blocks(2 * walks), SCAN_THREADS, bytes, s, scan, p);
         if (e == cudaSuccess)
             e = launch_pdl(true, kda_delta_join_kernel, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / JOIN_COLS),
                            JOIN_THREADS, size_t(JOIN_BYTES), s, p);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(true, kda_delta_scan_kernel<T, PLO, KW, false>, blocks(walks), SCAN_THREADS, bytes, s, scan, p);
+    return launch_pdl(true, kda_delta_scan_kernel<T, KW, false>, blocks(walks), SCAN_THREADS, bytes, s, scan, p);
 }
 
-// PLO: P and Q keep a low part (all types but bf16, whose rounding is above what it adds).
-template <typename T, bool PLO>
+template <typename T>
 cudaError_t launch_chunked(const DeltaParams &p, const DeltaMaps &prep, const DeltaMaps &scan, int device, int sms,
                            cudaStream_t s) {
-    return p.K == 128 && p.V == 128 ? launch_widths<T, PLO, 128>(p, prep, scan, device, sms, s)
-           : p.K <= 64              ? launch_widths<T, PLO, 64>(p, prep, scan, device, sms, s)
-                                    : launch_widths<T, PLO, 0>(p, prep, scan, device, sms, s);
+    return p.K == 128 && p.V == 128 ? launch_widths<T, 128>(p, prep, scan, device, sms, s)
+           : p.K <= 64              ? launch_widths<T, 64>(p, prep, scan, device, sms, s)
+                                    : launch_widths<T, 0>(p, prep, scan, device, sms, s);
 }
 
 }  // namespace kda

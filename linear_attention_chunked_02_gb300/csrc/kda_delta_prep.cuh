@@ -50,12 +50,8 @@ namespace kda {
 // Image of one chunk-head in the workspace.  M and P are FP16 pairs hi + lo (22
 // bits) scaled by a power of two for each half of 32 rows, 64 rows of 128
 // bytes with the 128-byte swizzle: the B operands of the scan's products.
-constexpr int IMG_MHI = 0, IMG_MLO = 8192, IMG_PHI = 16384, IMG_PLO = 24576;
-template <bool PLO>
-constexpr int img_hdr() { return PLO ? 32768 : 24576; }   // 16-bit outputs in bf16 need no low part of P
-constexpr int IMG_HDR_BYTES = 128;
-template <bool PLO>
-constexpr int img_bytes() { return img_hdr<PLO>() + IMG_HDR_BYTES; }
+constexpr int IMG_MHI = 0, IMG_MLO = 8192, IMG_PHI = 16384, IMG_PLO = 24576, IMG_HDR = 32768;
+constexpr int IMG_HDR_BYTES = 128, IMG_BYTES = IMG_HDR + IMG_HDR_BYTES;
 // header (floats): 1 / scale of M rows 0-31, 32-63; largest row sum of |M| in the halves;
 // 1 / scale of P in the halves; largest |k|, |q|
 constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7;
@@ -142,12 +138,6 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32
         : "f"(a), "f"(b));
 }
 
-// The hi part alone.
-__device__ __forceinline__ uint32_t round_f16(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Largest of m and |a|, |b|.
 __device__ __forceinline__ float max3(float m, float a, float b) {
     float r;
@@ -175,7 +165,7 @@ __device__ __forceinline__ float warp_max(float v) {   // v >= 0
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// Columns 8 c .. + 7 of row i of an image tile, times s: hi and, if `lo` is not null, lo.
+// Columns 8 c .. + 7 of row i of an image tile, times s: hi and lo.
 __device__ __forceinline__ void image_put(unsigned char *hi, unsigned char *lo, int i, int c, const float (&x)[8], float s) {
     uint4 h, l;
     split_f16(x[0] * s, x[1] * s, h.x, l.x);
@@ -184,7 +174,7 @@ __device__ __forceinline__ void image_put(unsigned char *hi, unsigned char *lo, 
     split_f16(x[6] * s, x[7] * s, h.w, l.w);
     const int at = i * 128 + 16 * (c ^ (i & 7));
     *reinterpret_cast<uint4 *>(hi + at) = h;
-    if (lo != nullptr) *reinterpret_cast<uint4 *>(lo + at) = l;
+    *reinterpret_cast<uint4 *>(lo + at) = l;
 }
 
 // The 64-token solve of the A tile (blocks (i, j) at Ab + 256 blk(i, j)) by two warps: the row-major
@@ -339,7 +329,7 @@ __device__ __forceinline__ void prep_split(float2 v, uint32_t &h0, uint32_t &h1,
     l1 = __float_as_uint(lo.y) + 0x1000u;
 }
 
-template <typename T, bool PLO>
+template <typename T>
 __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -751,7 +741,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
                     for (int e = 0; e < 8; e += 2) mx = max3(mx, x[e], x[e + 1]);
                 }
                 const float s = pow2_scale(warp_max(mx), KQ_LO, KQ_HI, inv);
-                unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>(), *pi = sm + prep_off_p<T>();
+                unsigned char *img = p.ws + int64_t(qi) * IMG_BYTES, *pi = sm + prep_off_p<T>();
                 if (warp == 6 && lane == 0) tc::bulk_wait_read();      // the previous image has left
                 named_sync<2, 64>();
 #pragma unroll 1
@@ -763,16 +753,16 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = 0.f;
                     }
-                    image_put(pi, PLO ? pi + 8192 : nullptr, i, b, x, s);
+                    image_put(pi, pi + 8192, i, b, x, s);
                 }
                 done();
                 fence_proxy_async();
                 named_sync<2, 64>();
-                float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
+                float *hdr = reinterpret_cast<float *>(img + IMG_HDR);
                 if (lane == 0) hdr[HDR_PINV + (warp & 1)] = inv;
                 if (warp == 6) {
                     if (lane == 0) {
-                        tc::bulk_store(img + IMG_PHI, smem_u32(pi), PLO ? 16384 : 8192);
+                        tc::bulk_store(img + IMG_PHI, smem_u32(pi), 16384);
                         tc::bulk_commit();
                     }
                     // warps 0, 1, 4, 5 of a group of eight saw k, the others q; the second group is idle at K = 32
@@ -847,9 +837,9 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) kda_delta_prep_kernel(const _
             }
             fence_proxy_async();
             bar64(bar);
-            unsigned char *img = p.ws + int64_t(qi) * img_bytes<PLO>();
+            unsigned char *img = p.ws + int64_t(qi) * IMG_BYTES;
             if ((pt & 31) == 0) {
-                float *hdr = reinterpret_cast<float *>(img + img_hdr<PLO>());
+                float *hdr = reinterpret_cast<float *>(img + IMG_HDR);
                 hdr[HDR_MINV + (pt >> 5)] = inv;
                 hdr[HDR_MSUM + (pt >> 5)] = sum;
             }

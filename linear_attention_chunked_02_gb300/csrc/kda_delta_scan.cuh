@@ -16,8 +16,9 @@
 // step, and lanes (value columns) never mix: a lane has scales of its own.
 //
 // FP32 accuracy from FP16: every operand is hi + lo (22 bits) and a product hi hi + hi lo +
-// lo hi; what only reaches a bf16 output (Q, P) takes hi hi alone, 2^-11 against
-// the output's 2^-9.  FP16 has range for that only under scales.  They are powers of two from
+// lo hi, for all types: Q and P of BF16 calls with their high parts alone would save 2 to 4 %
+// (16 x 512 x 64 heads: 462 us, not 476) and take their outputs 1.1e-3 of the norm away from the rounded
+// 64-bit result, which they now meet to 1e-4.  FP16 has range for that only under scales.  They are powers of two from
 // rigorous bounds: the images carry the largest |k|, |q| and M's row sums; a lane
 // measures |S| after each chunk and knows |v|; then |R| <= |v| + K |k| |S|,
 // |U| <= |M|_1 |R|, |S1| <= |S| + 64 |k| |U|.  The bounds overshoot by up to 2^13
@@ -63,10 +64,10 @@ namespace kda {
 
 constexpr int SCAN_THREADS = 32 * 32, SCAN_REGISTERS = 64;     // per thread at launch
 constexpr int SCAN_PARTS = 4;                      // chain threads to a lane
-constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 7,
-              SB_R = 9, SB_D2 = 10, SB_KH_FULL = 11, SB_KH_EMPTY = 12, SB_U = 13, SB_D3 = 14, SB_O_FULL = 15,
-              SB_V_FULL = 16, SB_V_EMPTY = 17, SB_ST_FULL = 18, SB_ST_EMPTY = 19, SB_IMG_READ = 20,
-              SB_GAM = 22, SCAN_NBARS = 24;
+constexpr int SB_S = 0, SB_KQ_FULL = 1, SB_KQ_EMPTY = 2, SB_D1 = 3, SB_O_EMPTY = 4, SB_IMG_FULL = 5, SB_IMG_EMPTY = 6,
+              SB_R = 7, SB_D2 = 8, SB_KH_FULL = 9, SB_KH_EMPTY = 10, SB_U = 11, SB_D3 = 12, SB_O_FULL = 13,
+              SB_V_FULL = 14, SB_V_EMPTY = 15, SB_ST_FULL = 16, SB_ST_EMPTY = 17, SB_IMG_READ = 18,
+              SB_GAM = 19, SCAN_NBARS = 21;
 constexpr int SCAN_OFF_TMEM = SCAN_NBARS * 8;
 constexpr int SCAN_OFF_GAM = 256;                  // [2][128] e^{G_C}
 constexpr int SCAN_OFF_MAX = SCAN_OFF_GAM + 2 * 128 * 4;       // [4 parts][128 lanes] largest |S|
@@ -76,32 +77,23 @@ constexpr int SCAN_OFF_TOT = SCAN_OFF_OUT + 2 * 128 * 8;       // [8 row groups]
 constexpr int SCAN_OFF_SUM = SCAN_OFF_TOT + 8 * 128 * 4;       // [4 parts][128], sums of a chunk taken token by token
 constexpr int SCAN_OFF_GH = SCAN_OFF_SUM + 4 * 128 * 4;     // [64] decays of the rows, where a head has one
 constexpr int SCAN_OFF_KQ = 14 * 1024;             // K hi, K lo, Q hi, Q lo: [2 channel halves][64 rows][128 B] each
-template <bool PLO>
-constexpr int scan_off_kh() { return SCAN_OFF_KQ + (PLO ? 4 : 3) * 16384; }    // K e^{G_C-G} transposed, hi and lo:
-                                                                               // [128 channels][128 B]
-template <bool PLO>
-constexpr int scan_off_img() { return scan_off_kh<PLO>() + 2 * 16384; }
-// images held at once: two, one beside a low part of P
-template <bool PLO>
-constexpr int scan_nimg() { return PLO ? 1 : 2; }
-template <bool PLO>
-constexpr int scan_img_pitch() { return (img_bytes<PLO>() + 1023) / 1024 * 1024; }
-template <bool PLO>
-constexpr int scan_off_v() { return scan_off_img<PLO>() + scan_nimg<PLO>() * scan_img_pitch<PLO>(); }  // [64 tokens][V]
-template <typename T, bool PLO>
-constexpr int scan_off_st() { return scan_off_v<PLO>() + 64 * 128 * int(sizeof(T)); }   // k, q, g: [64 rows][K] each
+constexpr int SCAN_OFF_KH = SCAN_OFF_KQ + 4 * 16384;   // K e^{G_C-G} transposed, hi and lo: [128 channels][128 B]
+constexpr int SCAN_OFF_IMG = SCAN_OFF_KH + 2 * 16384;  // the chunk's image (two find no room)
+constexpr int SCAN_OFF_V = SCAN_OFF_IMG + (IMG_BYTES + 1023) / 1024 * 1024;    // [64 tokens][V]
+template <typename T>
+constexpr int scan_off_st() { return SCAN_OFF_V + 64 * 128 * int(sizeof(T)); }         // k, q, g: [64 rows][K] each
 template <typename T>
 constexpr bool scan_staged(int K) { return sizeof(T) == 2 || K <= 64; }    // q and k too, not g alone
 template <typename T>
 constexpr int scan_off_g(int K) { return !scan_staged<T>(K) ? 0 : 32768; } // g, in the staging buffer
 template <typename T>
 constexpr int scan_stage(int K) { return scan_off_g<T>(K) + 64 * (K <= 64 ? 64 : 128) * 4; }
-template <typename T, bool PLO>
-constexpr int scan_bytes(int K) { return scan_off_st<T, PLO>() + scan_stage<T>(K) + 1024; }
+template <typename T>
+constexpr int scan_bytes(int K) { return scan_off_st<T>() + scan_stage<T>(K) + 1024; }
 static_assert(SCAN_OFF_TMEM + 4 <= SCAN_OFF_GAM, "header fits");
 static_assert(SCAN_OFF_GH + 64 * 4 <= SCAN_OFF_KQ, "small buffers fit");
-static_assert(scan_bytes<float, true>(64) <= 227 * 1024 && scan_bytes<float, true>(128) <= 227 * 1024 && scan_bytes<__half, true>(128) <= 227 * 1024 &&
-                  scan_bytes<__nv_bfloat16, false>(128) <= 227 * 1024, "fits the shared memory of one CTA");
+static_assert(scan_bytes<float>(64) <= 227 * 1024 && scan_bytes<float>(128) <= 227 * 1024 &&
+                  scan_bytes<__half>(128) <= 227 * 1024, "fits the shared memory of one CTA");
 // A chunk is taken token by token where its values are below 2^-16 of what the state can add to R
 // and no channel keeps more than 2^-12 of the state: what comes out is then
 // possibly below 2^-20 of what goes in.
@@ -127,19 +119,16 @@ __device__ __forceinline__ void put_operand(uint32_t ch, uint32_t cl, const floa
 }
 
 // D (+)= A B over `steps` steps of 16: A at TMEM columns ah, al; B at shared addresses bh, bl
-// (128-byte rows of 64 values; the second 64 values of a row at + bstep).  HI: hi hi only.
+// (128-byte rows of 64 values; the second 64 values of a row at + bstep).
 // Not unrolled: the issuing warp has few registers.
-template <bool HI>
 __device__ __forceinline__ void mma_split(int steps, uint32_t d, uint32_t ah, uint32_t al, uint32_t bh, uint32_t bl,
                                           uint32_t bstep, uint32_t idesc) {
     uint64_t dh = tc::sw128_desc(bh), dl = tc::sw128_desc(bl);
 #pragma unroll 1
     for (int ks = 0; ks < steps; ++ks) {
         tc::mma_f16_ts(d, ah, dh, idesc, ks > 0);
-        if (!HI) {
-            tc::mma_f16_ts(d, ah, dl, idesc, true);
-            tc::mma_f16_ts(d, al, dh, idesc, true);
-        }
+        tc::mma_f16_ts(d, ah, dl, idesc, true);
+        tc::mma_f16_ts(d, al, dh, idesc, true);
         ah += 8;
         al += 8;
         const uint32_t step = (ks == 3 ? bstep - 96 : 32) >> 4;    // the address field counts 16 bytes
@@ -238,14 +227,13 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
 // KW 128: K and V are 128, which makes every row pitch an immediate; 64: K is at most 64; 0: other
 // widths.  Staged rows are KP channels and 128 values long for all, zeros past K and V from the copy.  (One kernel for the last two, which reads FP32 both staged and not, took 592 us for 64 x 512
 // tokens, 32 heads of K = 64, V = 128; its own takes 434.)
-template <typename T, bool PLO, int KW, bool TRANS>
+template <typename T, int KW, bool TRANS>
 __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SCAN_OFF_TMEM);
     float *gam = reinterpret_cast<float *>(sm + SCAN_OFF_GAM);
-    constexpr int NI = scan_nimg<PLO>();
     constexpr bool W128 = KW == 128, STAGED = scan_staged<T>(KW == 64 ? 64 : 128);
     constexpr bool FOUR = W128 || (KW == 0 && STAGED);     // operands: four channels to a lane
     constexpr int KP = KW == 64 ? 64 : 128;
@@ -254,7 +242,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
     pdl_launch_dependents();
 
     if (tid == 0) {
-        const int count[SCAN_NBARS] = {16, 8, 1, 1, 4, 1, 1, 1, 1, 16, 1, 8, 1, 16, 1, 1, 1, 16, 1, 8, 4, 4, 1, 1};
+        const int count[SCAN_NBARS] = {16, 8, 1, 1, 4, 1, 1, 16, 1, 8, 1, 16, 1, 1, 1, 16, 1, 8, 4, 1, 1};
 #pragma unroll
         for (int b = 0; b < SCAN_NBARS; ++b) mbar_init(&bars[b], count[b]);
         fence_mbar_init();
@@ -325,9 +313,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         if (x.idle) x.nc = 0;
         return x;
     };
-    auto image_at = [&](const Walk1 &x) { return p.ws + (int64_t(x.before) * p.H + x.h) * img_bytes<PLO>(); };
+    auto image_at = [&](const Walk1 &x) { return p.ws + (int64_t(x.before) * p.H + x.h) * IMG_BYTES; };
     const int32_t w0 = blockIdx.x, wstep = gridDim.x;
-    const int64_t img_step = int64_t(p.H) * img_bytes<PLO>();
+    const int64_t img_step = int64_t(p.H) * IMG_BYTES;
     constexpr int nh = KW == 64 ? 1 : 2;                         // halves of 64 channels
     bool ok = true;
 
@@ -361,7 +349,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         float S[32];                                       // S[32 part + i][v]
         const bool held = 32 * part < K;                   // K is a multiple of 32
         const int t0 = 16 * part;                          // this thread's tokens of a chunk: t0 .. t0 + 15
-        T *sv = reinterpret_cast<T *>(sm + scan_off_v<PLO>()) + t0 * 128 + v;
+        T *sv = reinterpret_cast<T *>(sm + SCAN_OFF_V) + t0 * 128 + v;
         const uint32_t sop = tq + TM_SHI + 16 * part, rop = tq + TM_RHI + 8 * part;      // operand columns, hi parts
         auto put_state = [&](float s) {
 #pragma unroll
@@ -460,9 +448,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         for (int c = 0; c < x.nc; ++c, ++cc) {
             const uint32_t ph = cc & 1;
             const int left = x.rows - 64 * c;
-            prep_wait(ok, &bars[SB_IMG_FULL + cc % NI], (cc / NI) & 1, p.err);
-            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>() +
-                                                               img_hdr<PLO>());
+            prep_wait(ok, &bars[SB_IMG_FULL], ph, p.err);
+            const float *hdr = reinterpret_cast<const float *>(sm + SCAN_OFF_IMG + IMG_HDR);
             const float minv = hdr[HDR_MINV + (part >> 1)], msum = fmaxf(hdr[HDR_MSUM], hdr[HDR_MSUM + 1]);
             const float kmax = hdr[HDR_KMAX];
             float invk, invR, invU, invS1;
@@ -573,7 +560,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         // this thread's first row in the staging buffer or in memory; its channels are 64 x + 2 lane and
         // the next one.  Channels past K are zeros where staged, else another's values under a scale of zero.
         const int ks = STAGED ? KP : p.Hk * K;
-        unsigned char *st = sm + scan_off_st<T, PLO>();
+        unsigned char *st = sm + scan_off_st<T>();
         float *sg = reinterpret_cast<float *>(sm + SCAN_OFF_GH);
         uint32_t cc = 0;
         int4 next = entry(w0);
@@ -600,7 +587,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 __syncwarp();
                 gp = sg + 8 * rg;
             }
-            const float2 kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + img_hdr<PLO>() + 4 * HDR_KMAX);
+            const float2 kqmax = *reinterpret_cast<const float2 *>(img0 + c * img_step + IMG_HDR + 4 * HDR_KMAX);
             if (STAGED || p.gate == 0) {
                 prep_wait(ok, &bars[SB_ST_FULL], ph, p.err);
 #pragma unroll 1
@@ -688,15 +675,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                             split_f16(kv.x, kv.y, kh[j], kl[j]);
                             if (!TRANS) {
                                 const float2 qv = __fmul2_rn(W2::wide(rq[i].r[j]), __fmul2_rn(e, cq));
-                                if (PLO) split_f16(qv.x, qv.y, qh[j], ql[j]);
-                                else qh[j] = round_f16(qv.x, qv.y);
+                                split_f16(qv.x, qv.y, qh[j], ql[j]);
                             }
                         }
                         unsigned char *at = kq + (b + i) * 128 + 16 * (((lane & 15) >> 1) ^ (b + i));
                         *reinterpret_cast<uint2 *>(at) = make_uint2(kh[0], kh[1]);
                         *reinterpret_cast<uint2 *>(at + 16384) = make_uint2(kl[0], kl[1]);
                         if (!TRANS) *reinterpret_cast<uint2 *>(at + 32768) = make_uint2(qh[0], qh[1]);
-                        if (!TRANS && PLO) *reinterpret_cast<uint2 *>(at + 49152) = make_uint2(ql[0], ql[1]);
+                        if (!TRANS) *reinterpret_cast<uint2 *>(at + 49152) = make_uint2(ql[0], ql[1]);
                     }
                 }
                 if (rg == 7)                               // here G is the whole chunk's sum
@@ -730,14 +716,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         split_f16(kv.x, kv.y, kh, kl);
                         if (!TRANS) {
                             const float2 qv = __fmul2_rn(W2::wide(rq[i]), __fmul2_rn(e, cq));
-                            if (PLO) split_f16(qv.x, qv.y, qh, ql);
-                            else qh = round_f16(qv.x, qv.y);
+                            split_f16(qv.x, qv.y, qh, ql);
                         }
                         unsigned char *at = kq + (b + i) * 128 + 16 * ((lane >> 2) ^ (b + i));
                         *reinterpret_cast<uint32_t *>(at) = kh;
                         *reinterpret_cast<uint32_t *>(at + 16384) = kl;
                         if (!TRANS) *reinterpret_cast<uint32_t *>(at + 32768) = qh;
-                        if (!TRANS && PLO) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
+                        if (!TRANS) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
                     }
                 }
                 if (rg == 7)                               // here G is the whole chunk's sum
@@ -780,8 +765,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 split_f16(y[0].y, y[1].y, bh.x, bl.x); split_f16(y[2].y, y[3].y, bh.y, bl.y);
                 split_f16(y[4].y, y[5].y, bh.z, bl.z); split_f16(y[6].y, y[7].y, bh.w, bl.w);
                 const int d = 64 * x + 2 * lane;
-                unsigned char *a0 = sm + scan_off_kh<PLO>() + d * 128 + 16 * (rg ^ (d & 7));
-                unsigned char *a1 = sm + scan_off_kh<PLO>() + (d + 1) * 128 + 16 * (rg ^ ((d + 1) & 7));
+                unsigned char *a0 = sm + SCAN_OFF_KH + d * 128 + 16 * (rg ^ (d & 7));
+                unsigned char *a1 = sm + SCAN_OFF_KH + (d + 1) * 128 + 16 * (rg ^ ((d + 1) & 7));
                 *reinterpret_cast<uint4 *>(a0) = ah;
                 *reinterpret_cast<uint4 *>(a0 + 16384) = al;
                 *reinterpret_cast<uint4 *>(a1) = bh;
@@ -816,12 +801,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             // O = (scale Q e^G) S0 + P U
             prep_wait(ok, &bars[SB_U], ph, p.err);         // the chain's scales
             const float2 inv = sout[ph * 128 + v];
-            const float *hdr = reinterpret_cast<const float *>(sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>() +
-                                                               img_hdr<PLO>());
-            prep_wait(ok, &bars[SB_IMG_FULL + cc % NI], (cc / NI) & 1, p.err);
+            const float *hdr = reinterpret_cast<const float *>(sm + SCAN_OFF_IMG + IMG_HDR);
+            prep_wait(ok, &bars[SB_IMG_FULL], ph, p.err);
             const float p0 = hdr[HDR_PINV], p1 = hdr[HDR_PINV + 1], qmax = hdr[HDR_QMAX];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ + cc % NI]);
+            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ]);
             float invq;
             pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
             prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
@@ -863,7 +847,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         tc::fewer_registers<24>();
         if (warp == 28) {
             // --------------------------------------------------------- MMA issue
-            const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + scan_off_kh<PLO>());
+            const uint32_t kq = smem_u32(sm + SCAN_OFF_KQ), kh = smem_u32(sm + SCAN_OFF_KH);
             const int steps = 4 * nh;                      // of 16 channels
             const uint32_t id3 = nh == 2 ? SCAN_ID128 : SCAN_ID64;
             auto commit = [&](int b) { tc::commit(smem_u32(&bars[b])); };
@@ -875,13 +859,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             next = entry(w + wstep);
             for (; c < end; ++c) {
                 const uint32_t ph = c & 1;
-                const uint32_t img = smem_u32(sm + scan_off_img<PLO>() + (c % NI) * scan_img_pitch<PLO>());
+                const uint32_t img = smem_u32(sm + SCAN_OFF_IMG);
                 wait(SB_KQ_FULL, ph);
                 wait(SB_S, ph);
                 __syncwarp();
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_split<false>(steps, tmem + TM_D1, tmem + TM_SHI, tmem + TM_SLO, kq, kq + 16384, 8192, SCAN_ID64);
+                    mma_split(steps, tmem + TM_D1, tmem + TM_SHI, tmem + TM_SLO, kq, kq + 16384, 8192, SCAN_ID64);
                     commit(SB_D1);
                     if (TRANS) commit(SB_KQ_EMPTY);
                 }
@@ -889,16 +873,16 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 __syncwarp();
                 tc::fence_after_sync();
                 if (!TRANS && tc::elect_one()) {
-                    mma_split<!PLO>(steps, tmem + TM_O1, tmem + TM_SHI, tmem + TM_SLO, kq + 32768, kq + 49152, 8192,
+                    mma_split(steps, tmem + TM_O1, tmem + TM_SHI, tmem + TM_SLO, kq + 32768, kq + 49152, 8192,
                                     SCAN_ID64);
                     commit(SB_KQ_EMPTY);
                 }
-                wait(SB_IMG_FULL + c % NI, (c / NI) & 1);
+                wait(SB_IMG_FULL, ph);
                 wait(SB_R, ph);
                 __syncwarp();
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_split<false>(4, tmem + TM_D1, tmem + TM_RHI, tmem + TM_RLO, img + IMG_MHI, img + IMG_MLO, 0,
+                    mma_split(4, tmem + TM_D1, tmem + TM_RHI, tmem + TM_RLO, img + IMG_MHI, img + IMG_MLO, 0,
                                      SCAN_ID64);
                     commit(SB_D2);
                 }
@@ -907,15 +891,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 __syncwarp();
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_split<false>(4, tmem + TM_D3, tmem + TM_RHI, tmem + TM_RLO, kh, kh + 16384, 0, id3);
+                    mma_split(4, tmem + TM_D3, tmem + TM_RHI, tmem + TM_RLO, kh, kh + 16384, 0, id3);
                     commit(SB_D3);
                     commit(SB_KH_EMPTY);
                     if (!TRANS) {
-                        mma_split<!PLO>(4, tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0,
+                        mma_split(4, tmem + TM_O2, tmem + TM_RHI, tmem + TM_RLO, img + IMG_PHI, img + IMG_PLO, 0,
                                         SCAN_ID64);
                         commit(SB_O_FULL);
                     }
-                    commit(SB_IMG_EMPTY + c % NI);
+                    commit(SB_IMG_EMPTY);
                 }
                 __syncwarp();
             }
@@ -923,7 +907,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         } else if (warp == 29) {
             // ------------------------------------------------- loads of q, k and g
             if (STAGED || p.gate == 0) {
-                unsigned char *st = sm + scan_off_st<T, PLO>();
+                unsigned char *st = sm + scan_off_st<T>();
                 const uint32_t bytes = (STAGED ? (TRANS ? 1 : 2) * 64 * KP * sizeof(T) : 0) + (p.gate == 0 ? 64 * KP * 4 : 0);
                 uint32_t cc = 0;
                 Walk1 wk = walk_at(w0, entry(w0));
@@ -966,7 +950,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     __syncwarp();
                     if (tc::elect_one()) {
                         mbar_arrive_expect_tx(&bars[SB_V_FULL], 64 * 128 * sizeof(T));
-                        tma_load_3d(sm + scan_off_v<PLO>(), &maps.v, 0, wk.h, wk.row + 64 * c, &bars[SB_V_FULL]);
+                        tma_load_3d(sm + SCAN_OFF_V, &maps.v, 0, wk.h, wk.row + 64 * c, &bars[SB_V_FULL]);
                         if (c + 1 < wk.nc) tc::prefetch_3d(&maps.v, 0, wk.h, wk.row + 64 * c + 64);
                     }
                     __syncwarp();
@@ -982,27 +966,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 next = entry(w + wstep);
                 const unsigned char *src = image_at(wk);
                 for (int c = 0; c < wk.nc; ++c, ++cc, src += img_step) {
-                    prep_wait(ok, &bars[SB_IMG_EMPTY + cc % NI], ((cc / NI) & 1) ^ 1, p.err);
-                    if (!TRANS) prep_wait(ok, &bars[SB_IMG_READ + cc % NI], ((cc / NI) & 1) ^ 1, p.err);
+                    prep_wait(ok, &bars[SB_IMG_EMPTY], (cc & 1) ^ 1, p.err);
+                    if (!TRANS) prep_wait(ok, &bars[SB_IMG_READ], (cc & 1) ^ 1, p.err);
                     __syncwarp();
                     if (tc::elect_one()) {
-                        unsigned char *img = sm + scan_off_img<PLO>() + (cc % NI) * scan_img_pitch<PLO>();
-                        uint64_t *full = &bars[SB_IMG_FULL + cc % NI];
+                        unsigned char *img = sm + SCAN_OFF_IMG;
+                        uint64_t *full = &bars[SB_IMG_FULL];
                         if (TRANS) {                       // M and the header
                             mbar_arrive_expect_tx(full, IMG_PHI + IMG_HDR_BYTES);
                             bulk_load(img, src, IMG_PHI, full);
-                            bulk_load(img + img_hdr<PLO>(), src + img_hdr<PLO>(), IMG_HDR_BYTES, full);
+                            bulk_load(img + IMG_HDR, src + IMG_HDR, IMG_HDR_BYTES, full);
                         } else {
-                            mbar_arrive_expect_tx(full, img_bytes<PLO>());
-                            bulk_load(img, src, img_bytes<PLO>(), full);
+                            mbar_arrive_expect_tx(full, IMG_BYTES);
+                            bulk_load(img, src, IMG_BYTES, full);
                         }
-                        if (c + 1 < wk.nc) tc::prefetch_bulk(src + img_step, TRANS ? IMG_PHI : img_bytes<PLO>());
+                        if (c + 1 < wk.nc) tc::prefetch_bulk(src + img_step, TRANS ? IMG_PHI : IMG_BYTES);
                     }
                     __syncwarp();
                 }
             }
-            for (uint32_t i = cc > NI ? cc - NI : 0; i < cc; ++i)
-                prep_wait(ok, &bars[SB_IMG_FULL + i % NI], (i / NI) & 1, p.err);
+            if (cc > 0) prep_wait(ok, &bars[SB_IMG_FULL], (cc - 1) & 1, p.err);
         }
     }
     tc::fence_before_sync();
