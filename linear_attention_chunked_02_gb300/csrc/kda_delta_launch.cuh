@@ -33,7 +33,7 @@ cudaError_t chunked_ready(int device) {
         e = kernel_ready(kda_delta_scan_kernel<T, KW, false>, scan_bytes<T>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
     if (e == cudaSuccess)
         e = kernel_ready(kda_delta_scan_kernel<T, KW, true>, scan_bytes<T>(KW == 64 ? 64 : 128), SCAN_REGISTERS);
-    if (e == cudaSuccess) e = kernel_ready(kda_delta_join_kernel, JOIN_BYTES, 0);
+    if (e == cudaSuccess) e = kernel_ready(kda_delta_join_kernel<T>, JOIN_BYTES, 0);
     done[device] = e == cudaSuccess;
     return e;
 }
@@ -50,7 +50,7 @@ cudaError_t launch_widths(const DeltaParams &p, const DeltaMaps &prep, const Del
     if (e == cudaSuccess && p.seg > 0) {
         e = launch_pdl(true, kda_delta_scan_kernel<T, KW, true>, blocks(2 * walks), SCAN_THREADS, bytes, s, scan, p);
         if (e == cudaSuccess)
-            e = launch_pdl(true, kda_delta_join_kernel, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / JOIN_COLS),
+            e = launch_pdl(true, kda_delta_join_kernel<T>, unsigned(p.nseq) * unsigned(p.H) * unsigned(p.V / JOIN_COLS),
                            JOIN_THREADS, size_t(JOIN_BYTES), s, p);
     }
     if (e != cudaSuccess) return e;

@@ -26,7 +26,7 @@
 // relative to the state and values that go in; where a chunk's decay clears the state and its
 // values are next to nothing beside it, what comes out can be smaller than that:
 // the four lane quarters each look out for such a chunk and take it token by token in
-// FP32 (scan_tokens).
+// FP32 (scan_tokens).  A segment's map has the same limit: kda_delta_join_kernel looks out for that.
 //
 // Few heads and long sequences leave most of the GPU idle in that walk, so sequences can be split
 // into segments.  A segment maps the state by S -> M S + N, M [K, K], N [K, V]: a first run of
@@ -180,8 +180,8 @@ template <> struct Two<__half> {
 
 // A chunk token by token, for the four warps of one lane quarter: thread (part, v) has
 // S[32 part + i][v].  `row` is the chunk's first row, `n` its tokens; `sum` [4][128]
-// of shared memory takes the parts' sums.
-template <typename T>
+// of shared memory takes the parts' sums.  OUT: with the outputs.
+template <typename T, bool OUT>
 __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32], int64_t row, int n, int h, int part,
                                             int v, int quarter, float *sum) {
     const int hk = h / (p.H / p.Hk), d0 = 32 * part;
@@ -202,21 +202,26 @@ __device__ __forceinline__ void scan_tokens(const DeltaParams &p, float (&S)[32]
         if (d0 < p.K) {                                    // K is a multiple of 32
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float kd = widen1(kp[i]), qd = widen1(qp[i]);
+                const float kd = widen1(kp[i]);
                 S[i] *= expf(gp[p.gate == 0 ? i : 0]);
                 a = fmaf(kd, S[i], a);
-                b = fmaf(qd, S[i], b);
-                qk = fmaf(qd, kd, qk);
+                if (OUT) {
+                    const float qd = widen1(qp[i]);
+                    b = fmaf(qd, S[i], b);
+                    qk = fmaf(qd, kd, qk);
+                }
             }
         }
         a = total(a);
-        b = total(b);
-        qk = total(qk);
+        if (OUT) {
+            b = total(b);
+            qk = total(qk);
+        }
         const bool in = v < p.V;
         const int64_t at = (r * p.H + h) * p.V + v;
         const float val = in ? widen1(static_cast<const T *>(p.v)[at]) : 0.f;
         const float u = widen1(static_cast<const T *>(p.beta)[r * p.H + h]) * (val - a);
-        if (in && part == 0) put1(static_cast<T *>(p.o) + at, p.scale * fmaf(qk, u, b));
+        if (OUT && in && part == 0) put1(static_cast<T *>(p.o) + at, p.scale * fmaf(qk, u, b));
         if (d0 < p.K) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = fmaf(widen1(kp[i]), u, S[i]);
@@ -459,8 +464,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float bU = msum * bR;
             const float sU = pow2_scale(bU, VS_LO, VS_HI, invU);
             float sS = pow2_scale(bS + 64.f * kmax * bU, VS_LO, VS_HI, invS1);
-            // (M and N come without outputs, and are as good as the state that goes in)
-            bool weak = !TRANS && __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
+            // (M has no values: where its loss would count, the join takes the segment token by token)
+            bool weak = run == 0 && __any_sync(0xffffffffu, bR > SCAN_WEAK_V * bv);
             if (weak) {                                    // the same in the four warps of the quarter
                 prep_wait(ok, &bars[SB_GAM + ph], (cc >> 1) & 1, p.err);
                 float gmax = 0.f;
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < K; ++i) gmax = fmaxf(gmax, gam[ph * 128 + i]);
                 weak = __all_sync(0xffffffffu, gmax < SCAN_WEAK_G);
                 if (weak) {
-                    scan_tokens<T>(p, S, x.row + 64 * c, left < 64 ? left : 64, x.h, part, v, quarter,
+                    scan_tokens<T, !TRANS>(p, S, x.row + 64 * c, left < 64 ? left : 64, x.h, part, v, quarter,
                                    reinterpret_cast<float *>(sm + SCAN_OFF_SUM));
                     float m = state_max(), unused = 0.f;
                     lane_max(m, unused);
@@ -1001,12 +1006,102 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 // the sequence's first segment gave its state itself.  M comes through shared memory 64 columns
 // at a time, the next ones' copy under way during a product: at that size two blocks share an SM,
 // and the 256 blocks of 32 heads are one wave (8 segments: 45 us, 57 with all of M staged).
+//
+// M's columns are as good as 2^-34 or so of what went into each chunk, so where a chunk clears the state
+// M can have lost what little is left of it.  That counts where the state that comes in is so large
+// that the rest of it, M S, is not lost beside N.  A block which finds M S below JOIN_FALL of S in a column, but not
+// below 2^-20 of the sum, looks for such a chunk in the segment's decays, and if there is one walks the
+// segment token by token (join_tokens): about a microsecond a token.
 constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 68;
 constexpr int JOIN_BYTES = 2 * 128 * JOIN_PITCH * 4;
-static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const DeltaParams p) {
+constexpr float JOIN_FALL = 1.f / 256.f, JOIN_COUNTS = 1.f / 1048576.f;
+
+struct JoinShared {
+    float S[128][JOIN_COLS];
+    float k[2][128], d[2][128];                             // join_tokens: a token's key and decays
+    float part[2][8][JOIN_COLS];                            // the warps' sums or maxima
+    int32_t red[8];
+};
+
+// Whether one of the segment's chunks (rows a .. b of head h) keeps less than SCAN_WEAK_G of every channel.
+// The same for all threads.
+__device__ __forceinline__ bool join_cleared(const DeltaParams &p, int64_t a, int64_t b, int h) {
+    bool any = false;
+    for (; a < b; a += BT) {
+        const int n = b - a < BT ? int(b - a) : BT, d = int(threadIdx.x);
+        float sum = 0.f;
+        if (d < p.K)
+#pragma unroll 8
+            for (int t = 0; t < n; ++t) sum += p.g[p.gate == 0 ? ((a + t) * p.H + h) * p.K + d : (a + t) * p.H + h];
+        any |= __syncthreads_and(d >= p.K || expf(sum) < SCAN_WEAK_G) != 0;
+    }
+    return any;
+}
+
+// The state of rows r, r + 1 and columns c .. + 3 of the block's after rows a .. b, token by token in FP32.
+template <typename T>
+__device__ __forceinline__ void join_tokens(const DeltaParams &p, JoinShared &sh, float4 (&s)[2], int64_t a, int64_t b, int h,
+                                            int r, int c, int column) {
+    const int tid = threadIdx.x, hk = h / (p.H / p.Hk);
+    const bool in = r < p.K;
+    s[0] = in ? *reinterpret_cast<const float4 *>(&sh.S[r][c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    s[1] = in ? *reinterpret_cast<const float4 *>(&sh.S[r + 1][c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float nk = 0.f, ng = 0.f;                               // channel tid's key and log decay of the token that comes next
+    auto fetch = [&](int64_t t) {
+        if (t < b && tid < p.K) {
+            nk = widen1(static_cast<const T *>(p.k)[(t * p.Hk + hk) * p.K + tid]);
+            ng = p.g[p.gate == 0 ? (t * p.H + h) * p.K + tid : t * p.H + h];
+        }
+    };
+    auto put = [&](int at) {
+        if (tid < 128) {
+            sh.k[at][tid] = tid < p.K ? nk : 0.f;
+            sh.d[at][tid] = tid < p.K ? expf(ng) : 0.f;
+        }
+    };
+    fetch(a);
+    put(0);
+    fetch(a + 1);
+    __syncthreads();
+#pragma unroll 1
+    for (int64_t t = a; t < b; ++t) {
+        const int at = int(t - a) & 1;
+        const T *vp = static_cast<const T *>(p.v) + (t * p.H + h) * p.V + column + c;
+        const float beta = widen1(static_cast<const T *>(p.beta)[t * p.H + h]);
+        const float v[4] = {widen1(vp[0]), widen1(vp[1]), widen1(vp[2]), widen1(vp[3])};
+        const float k0 = sh.k[at][r], k1 = sh.k[at][r + 1], d0 = sh.d[at][r], d1 = sh.d[at][r + 1];
+        s[0].x *= d0; s[0].y *= d0; s[0].z *= d0; s[0].w *= d0;
+        s[1].x *= d1; s[1].y *= d1; s[1].z *= d1; s[1].w *= d1;
+        float x[4] = {fmaf(k1, s[1].x, k0 * s[0].x), fmaf(k1, s[1].y, k0 * s[0].y), fmaf(k1, s[1].z, k0 * s[0].z),
+                      fmaf(k1, s[1].w, k0 * s[0].w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
+        if ((tid & 31) < 4) *reinterpret_cast<float4 *>(&sh.part[at][tid >> 5][c]) = make_float4(x[0], x[1], x[2], x[3]);
+        put(at ^ 1);                                        // (read last before the barrier of the token before)
+        fetch(t + 2);
+        __syncthreads();
+        float u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) sum += sh.part[at][w][c + e];
+            u[e] = beta * (v[e] - sum);
+        }
+        s[0] = make_float4(fmaf(k0, u[0], s[0].x), fmaf(k0, u[1], s[0].y), fmaf(k0, u[2], s[0].z), fmaf(k0, u[3], s[0].w));
+        s[1] = make_float4(fmaf(k1, u[0], s[1].x), fmaf(k1, u[1], s[1].y), fmaf(k1, u[2], s[1].z), fmaf(k1, u[3], s[1].w));
+    }
+    __syncthreads();                                        // part is used again
+}
+
+template <typename T>
+__global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const DeltaParams p) {
     extern __shared__ __align__(16) float join_m[];
-    __shared__ int32_t red[8];
-    __shared__ __align__(16) float S[128][JOIN_COLS];
+    __shared__ __align__(16) JoinShared sh;
+    auto &S = sh.S;
+    auto &red = sh.red;
     const int tid = threadIdx.x, r = 2 * (tid >> 2), c = 4 * (tid & 3);
     const int slices = p.V / JOIN_COLS, slice = int(blockIdx.x) % slices, nh = int(blockIdx.x) / slices;
     const int n = nh / p.H, h = nh - n * p.H;
@@ -1052,11 +1147,36 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
         *reinterpret_cast<float4 *>(&S[r + 1][c]) = *row(0, 1);
     }
     fetch(halves);
+    // the largest values of column tid of 16 after the segment before (columns_max's)
+    auto columns_max = [&](const float4 (&x)[2], int to) {
+        float m[4] = {fmaxf(fabsf(x[0].x), fabsf(x[1].x)), fmaxf(fabsf(x[0].y), fabsf(x[1].y)),
+                      fmaxf(fabsf(x[0].z), fabsf(x[1].z)), fmaxf(fabsf(x[0].w), fabsf(x[1].w))};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
+        if ((tid & 31) < 4) *reinterpret_cast<float4 *>(&sh.part[to][tid >> 5][c]) = make_float4(m[0], m[1], m[2], m[3]);
+    };
+    auto column_max = [&](int from) {
+        float m = 0.f;
+#pragma unroll
+        for (int w = 0; w < JOIN_THREADS / 32; ++w) m = fmaxf(m, sh.part[from][w][tid & (JOIN_COLS - 1)]);
+        return m;
+    };
+    const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    float before = 0.f;
+    if (parts > 2) {
+        const float4 s[2] = {r < p.K ? *row(0, 0) : zero4, r < p.K ? *row(0, 1) : zero4};
+        columns_max(s, 0);
+        __syncthreads();
+        before = column_max(0);
+        __syncthreads();
+    }
     for (int i = 1; i < parts - 1; ++i) {
-        float4 a[2];
+        float4 a[2] = {zero4, zero4}, n4[2] = {zero4, zero4};
         if (r < p.K) {
-            a[0] = *row(i, 0);
-            a[1] = *row(i, 1);
+            n4[0] = *row(i, 0);
+            n4[1] = *row(i, 1);
         }
         for (int j = halves * i; j < halves * (i + 1); ++j) {
             fetch(j + 1);
@@ -1082,9 +1202,30 @@ static __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(con
             }
             __syncthreads();
         }
+        columns_max(a, 0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {                       // what goes out: N + M S
+            n4[e].x += a[e].x; n4[e].y += a[e].y; n4[e].z += a[e].z; n4[e].w += a[e].w;
+        }
+        columns_max(n4, 1);
+        __syncthreads();
+        const float rest = column_max(0), after = column_max(1);
+        if (__syncthreads_or(rest < JOIN_FALL * before && rest > JOIN_COUNTS * after)) {
+            int64_t r0, r1;
+            sequence_rows(p, n, r0, r1);
+            r0 += int64_t(BT) * p.seg * i;
+            if (r1 > r0 + int64_t(BT) * p.seg) r1 = r0 + int64_t(BT) * p.seg;
+            if (join_cleared(p, r0, r1, h)) join_tokens<T>(p, sh, n4, r0, r1, h, r, c, JOIN_COLS * slice);
+            columns_max(n4, 1);
+            __syncthreads();
+            before = column_max(1);
+            __syncthreads();
+        } else {
+            before = after;
+        }
         if (r < p.K) {
-            *row(i, 0) = *reinterpret_cast<float4 *>(&S[r][c]) = a[0];
-            *row(i, 1) = *reinterpret_cast<float4 *>(&S[r + 1][c]) = a[1];
+            *row(i, 0) = *reinterpret_cast<float4 *>(&S[r][c]) = n4[0];
+            *row(i, 1) = *reinterpret_cast<float4 *>(&S[r + 1][c]) = n4[1];
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

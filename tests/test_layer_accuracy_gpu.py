@@ -23,3 +23,36 @@ def test_prefill_output_is_rounded_once(kda, dtype, ulp, K, gate):  # noqa: F811
     rounded = f64(torch.from_numpy(want).to(dtype))
     off = np.linalg.norm(f64(o) - rounded) / np.linalg.norm(want)
     assert off <= 2 * np.sqrt(1e-6 * ulp), off
+
+
+CHUNK = 64
+
+
+def faded(x, big, clear, fall):
+    """One sequence whose values are of 1e8 in its first `big` chunks and of 1e-6 after them, and whose chunk
+    `clear` leaves next to nothing of the state: each row of it the same share, or the first ten rows all.  Rows
+    from the end of that chunk on see 1e8 e^-64 or 1e8 e^-28 of what was before."""
+    x.v[0, :CHUNK * big] *= 1e8
+    x.v[0, CHUNK * big:] *= 1e-6
+    if fall == "even":
+        x.g[0, CHUNK * clear:CHUNK * (clear + 1)] = -1.0
+    else:
+        x.g[0, CHUNK * clear:CHUNK * clear + 10] = -2.8
+    return CHUNK * (clear + 1)
+
+
+# 32 chunks of one head, which are walked in segments of four to eleven chunks: the chunk that clears the state
+# stands in all places of several segments, after the large values at once (a segment's own state) or later (the
+# state that comes into a segment).
+@pytest.mark.parametrize("big, clear", [(2, c) for c in range(3, 24, 2)] + [(c, c) for c in (3, 7, 8, 11, 14, 15, 17)])
+@pytest.mark.parametrize("fall", ["even", "first rows"])
+@pytest.mark.parametrize("K, V, dtype, gate", [(64, 32, F32, "channel"), (128, 128, F32, "head"), (96, 64, BF16, "channel")],
+                         ids=str)
+def test_split_sequence_forgets_what_a_chunk_clears(kda, big, clear, fall, K, V, dtype, gate):  # noqa: F811
+    x = Rule([32 * CHUNK], Hk=1, H=1, K=K, V=V, dtype=dtype, gate=gate, seed=big + clear, rate=0.002)
+    a = faded(x, big, clear, fall)
+    o, S = x.run(kda)
+    wo, wS = x.want()
+    close(o[a:], wo[0][a:], dtype, "outputs after the chunk")
+    close(S[0], wS[0], F32, "state")
+    close(o, wo[0], dtype, "all outputs")
