@@ -62,12 +62,11 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  *
  *   q, k, v, g, beta, o   as above with leading dimensions [B, T] (dense: every
  *               batch row is a sequence) or [1, T] with cu_seqlens (packed).
- *               16-byte aligned (beta: to its element size).  o must not overlap
- *               an input.
+ *               16-byte aligned (beta: to its element size).
  *   cu_seqlens, num_seqs, B, T   as for kda_solve_tril.  Sequences may be empty.
  *   state_in    states to start from, or NULL: all zero.
  *   state_out   states after the last token, or NULL: not wanted.  May be
- *               state_in itself; otherwise the two must not overlap.
+ *               state_in itself.
  *   slots       device int32 [sequences], or NULL.  Sequence n uses entry
  *               slots[n] of state_in and state_out, which then have num_slots
  *               entries; a slot outside [0, num_slots) means that the sequence
@@ -83,6 +82,9 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  *   workspace   device, 16-byte aligned, kda_delta_prefill_workspace_size()
  *               bytes; its contents are scratch (KDA_ERR_WORKSPACE if missing or
  *               too small).
+ *
+ * o, state_out and the workspace must not overlap each other or anything that is
+ * read (KDA_ERR_INVALID_ARGUMENT), but for state_out, which may be state_in.
  *
  * Sequences of no tokens copy their state (zeros without state_in).  With T == 0
  * or B == 0 there is nothing to read but the states.  Rows of T past the last
@@ -116,6 +118,7 @@ KDA_API kda_status_t kda_delta_prefill(const void *q, const void *k, const void 
  *               is at least N.  A slot outside [0, num_slots) (-1 for the padding
  *               rows of a captured batch) reads a state of zeros and stores
  *               nothing.  Two requests must not share a slot.
+ *               o and state must not overlap each other or another tensor.
  *   N           N == 0 is a no-op.  N * H < 2^31 - 1 over 4.
  */
 KDA_API kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta,

@@ -145,22 +145,41 @@ kda_status_t check_heads(int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dt
     return KDA_OK;
 }
 
-// Pointers of the token tensors: present, aligned, o clear of the inputs.
+// Pointers of the token tensors: present and aligned.
 kda_status_t check_tokens(const void *q, const void *k, const void *v, const float *g, const void *beta,
-                          const void *o, size_t rows, int32_t Hk, int32_t H, int32_t K, int32_t V, int32_t dtype,
-                          int32_t gate) {
+                          const void *o, int32_t dtype) {
     const size_t es = size_t(elt_size(dtype));
     if (q == nullptr || k == nullptr || v == nullptr || g == nullptr || beta == nullptr || o == nullptr)
         return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(o) ||
         reinterpret_cast<uintptr_t>(beta) % es != 0)
         return KDA_ERR_INVALID_ARGUMENT;
-    const size_t qb = rows * size_t(Hk) * size_t(K) * es, vb = rows * size_t(H) * size_t(V) * es;
-    const size_t gb = rows * size_t(H) * (gate == KDA_GATE_CHANNEL ? size_t(K) : 1) * 4, bb = rows * size_t(H) * es;
-    if (overlaps(o, vb, q, qb) || overlaps(o, vb, k, qb) || overlaps(o, vb, v, vb) || overlaps(o, vb, g, gb) ||
-        overlaps(o, vb, beta, bb))
-        return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
+}
+
+// A buffer of a call; no pointer or no bytes: not used.
+struct Span {
+    const void *at;
+    size_t bytes;
+};
+bool meet(const Span &a, const Span &b) {
+    return a.at != nullptr && b.at != nullptr && a.bytes > 0 && b.bytes > 0 && overlaps(a.at, a.bytes, b.at, b.bytes);
+}
+
+// Whether something that a call writes (o, states, workspace) lies on something else of its buffers; the
+// states may be updated in place.
+bool buffers_meet(const DeltaParams &p, size_t rows, int32_t dtype, size_t entries, size_t workspace_bytes) {
+    const size_t es = size_t(elt_size(dtype)), H = size_t(p.H);
+    const size_t qb = rows * size_t(p.Hk) * size_t(p.K) * es, vb = rows * H * size_t(p.V) * es;
+    const size_t gb = rows * H * (p.gate == KDA_GATE_CHANNEL ? size_t(p.K) : 1) * 4;
+    const size_t sb = entries * H * size_t(p.K) * size_t(p.V) * 4, nseq = size_t(p.nseq);
+    const Span in[] = {{p.q, qb}, {p.k, qb}, {p.v, vb}, {p.g, gb}, {p.beta, rows * H * es},
+                       {p.slots, nseq * 4}, {p.cu, (nseq + 1) * 4}};
+    const Span state_in{p.state_in, sb}, o{p.o, vb}, state_out{p.state_out, sb}, ws{p.ws, workspace_bytes};
+    for (const Span &x : in)
+        if (meet(o, x) || meet(state_out, x) || meet(ws, x)) return true;
+    return meet(o, state_in) || meet(o, state_out) || meet(o, ws) || meet(ws, state_in) || meet(ws, state_out) ||
+           (p.state_in != p.state_out && meet(state_in, state_out));
 }
 
 }  // namespace
@@ -196,29 +215,23 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     if (seqs == 0) return KDA_OK;
     const size_t rows = size_t(B) * size_t(T);
     if (rows > 0) {
-        st = check_tokens(q, k, v, g, beta, o, rows, Hk, H, K, V, dtype, gate);
+        st = check_tokens(q, k, v, g, beta, o, dtype);
         if (st != KDA_OK) return st;
     }
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_INVALID_ARGUMENT;
-    const size_t sb = size_t(slots != nullptr ? num_slots : seqs) * size_t(H) * size_t(K) * size_t(V) * 4;
-    if (state_in != nullptr && state_out != nullptr && state_in != state_out && overlaps(state_in, sb, state_out, sb))
-        return KDA_ERR_INVALID_ARGUMENT;
-    if (rows > 0 && overlaps(o, rows * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state_in, state_in != nullptr ? sb : 0))
-        return KDA_ERR_INVALID_ARGUMENT;
-    if (rows > 0 && overlaps(o, rows * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state_out, state_out != nullptr ? sb : 0))
-        return KDA_ERR_INVALID_ARGUMENT;
     const size_t need = kda_delta_prefill_workspace_size(B, T, H, num_seqs, K, V);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need) return KDA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return KDA_ERR_INVALID_ARGUMENT;
     }
-    if (rows == 0 && state_out == nullptr) return KDA_OK;
     DeltaParams p{q, k, v, g, beta, o, state_in, state_out, slots, num_slots, cu_seqlens, int32_t(seqs), T,
                   Hk, H, K, V, gate, scale, nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr};
+    p.ws = need > 0 ? static_cast<unsigned char *>(workspace) : nullptr;
+    if (buffers_meet(p, rows, dtype, size_t(slots != nullptr ? num_slots : seqs), need)) return KDA_ERR_INVALID_ARGUMENT;
+    if (rows == 0 && state_out == nullptr) return KDA_OK;
     if (!chunked_form(B, T, num_seqs)) return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
     p.cpr = int32_t((T + BT - 1) / BT);
     p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
-    p.ws = static_cast<unsigned char *>(workspace);
     int64_t units = 0;
     p.seg = segment_chunks(B, T, H, num_seqs, units);
     p.n_units = int32_t(units);
@@ -239,14 +252,12 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
     if (N < 0 || num_slots < 0 || (slots == nullptr && num_slots < N)) return KDA_ERR_INVALID_ARGUMENT;
     if (int64_t(N) * H >= (int64_t(1) << 28)) return KDA_ERR_UNSUPPORTED;
     if (N == 0) return KDA_OK;
-    st = check_tokens(q, k, v, g, beta, o, size_t(N), Hk, H, K, V, dtype, gate);
+    st = check_tokens(q, k, v, g, beta, o, dtype);
     if (st != KDA_OK) return st;
     if (state == nullptr || !aligned16(state)) return KDA_ERR_INVALID_ARGUMENT;
-    if (overlaps(o, size_t(N) * size_t(H) * size_t(V) * size_t(elt_size(dtype)), state,
-                 size_t(num_slots) * size_t(H) * size_t(K) * size_t(V) * 4))
-        return KDA_ERR_INVALID_ARGUMENT;
     const DeltaParams p{q, k, v, g, beta, o, state, state, slots, num_slots, nullptr, N, 1, Hk, H, K, V, gate, scale,
                         nullptr, 0, 0, nullptr, 0, 0, nullptr, nullptr};
+    if (buffers_meet(p, size_t(N), dtype, size_t(num_slots), 0)) return KDA_ERR_INVALID_ARGUMENT;
     return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
