@@ -49,10 +49,11 @@ typedef enum {
 /*
  * Workspace bytes kda_delta_prefill needs for this shape: 0 for an empty or
  * invalid one, and for sequences of fewer than 16 tokens on average, which run
- * token by token; else 32,896 for each chunk of 64 tokens and head, and where
- * sequences are split (few heads, many chunks) K (K + V) 4 for each segment and
- * head.  It grows with T and depends on nothing but the arguments.  Pure host
- * arithmetic.
+ * token by token; else 32,896 for each chunk of 64 tokens and head (packed: for
+ * the bound (T + 63 num_seqs) / 64 on the chunks, at most T); packed, 16 for each
+ * sequence; and where sequences are split (few heads, many chunks) K (K + V) 4 for
+ * each segment and head, the 16 bytes then for each segment.  It depends on nothing
+ * but the arguments.  Pure host arithmetic.
  */
 KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K,
                                                 int32_t V);
@@ -73,10 +74,10 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  *               starts from zero and its state is not stored.  Two sequences must
  *               not share a slot.  NULL: sequence n uses entry n (num_slots is
  *               ignored).
- *   Hk, H       key heads and heads; H is a multiple of Hk.  H * K and H * V are
- *               below 2^24, B*T < 2^31 and chunks * H < 2^30 with chunks of 64
- *               tokens, as for kda_solve_tril; larger sizes give
- *               KDA_ERR_UNSUPPORTED.
+ *   Hk, H       key heads and heads; H is a multiple of Hk.  H < 2^17 whatever K
+ *               and V, B*T <= 2^31 - 129, sequences * H < 2^28 and chunks * H < 2^30
+ *               with chunks of 64 tokens (bounded as for the workspace); larger
+ *               sizes give KDA_ERR_UNSUPPORTED.
  *   gate        kda_gate_t.
  *   scale       factor on the output, usually K^-0.5.
  *   workspace   device, 16-byte aligned, kda_delta_prefill_workspace_size()
@@ -119,7 +120,8 @@ KDA_API kda_status_t kda_delta_prefill(const void *q, const void *k, const void 
  *               rows of a captured batch) reads a state of zeros and stores
  *               nothing.  Two requests must not share a slot.
  *               o and state must not overlap each other or another tensor.
- *   N           N == 0 is a no-op.  N * H < 2^31 - 1 over 4.
+ *   N           N == 0 is a no-op.  N * H < 2^28 and H < 2^17, else
+ *               KDA_ERR_UNSUPPORTED.
  */
 KDA_API kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const void *beta,
                                     void *o, float *state, const int32_t *slots, int32_t num_slots, int32_t N,

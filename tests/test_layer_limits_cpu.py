@@ -1,10 +1,11 @@
-"""Refusals of the layer operators that need no GPU.
+"""Refusals of the layer operators that need no GPU, and their sizes at the limits.
 
-A call that passes the checks would launch on made-up addresses, so every call here is refused."""
+A call that passes the checks would launch on made-up addresses, so every call here is refused: where a
+size is just allowed, a missing pointer refuses it after the sizes were looked at."""
 import pytest
 
 import linear_attention_chunked_02_gb300 as kda
-from test_layer_abi_cpu import INVALID, L, P, prefill, step  # noqa: F401
+from test_layer_abi_cpu import INVALID, L, P, UNSUPPORTED, prefill, step  # noqa: F401
 
 WS = kda.delta_prefill_workspace_size
 
@@ -43,3 +44,51 @@ def test_step_refuses_overlapping_buffers(L, written, other):  # noqa: F811
     at = base[other]
     for start in (at, at - sizes[written] + 16, at + sizes[other] - 16):
         assert step(L, **dict(base, **{written: start})) == INVALID, (start, at)
+
+
+def test_prefill_limits(L):  # noqa: F811
+    """Each limit of the header from both sides."""
+    def sized(**kw):
+        return prefill(L, q=None, **kw)                    # INVALID where the sizes pass
+
+    top = 1 << 17
+    assert sized(Hk=1, H=top - 1) == INVALID and sized(Hk=1, H=top) == UNSUPPORTED
+    assert sized(Hk=1, H=top - 1, K=32, V=32) == INVALID and sized(Hk=1, H=top, K=32, V=32) == UNSUPPORTED
+    assert sized(T=(1 << 31) - 129, Hk=1, H=1) == INVALID and sized(T=(1 << 31) - 128, Hk=1, H=1) == UNSUPPORTED
+    # sequences x heads
+    assert sized(cu=P[8], nseq=(1 << 20) - 1, T=1, Hk=1, H=256) == INVALID
+    assert sized(cu=P[8], nseq=1 << 20, T=1, Hk=1, H=256) == UNSUPPORTED
+    # chunks x heads
+    assert sized(T=64 * ((1 << 20) - 1), Hk=1, H=1024) == INVALID
+    assert sized(T=64 * (1 << 20), Hk=1, H=1024) == UNSUPPORTED
+
+
+def test_step_limits(L):  # noqa: F811
+    assert step(L, q=None, N=(1 << 20) - 1, nslots=1 << 20, Hk=1, H=256) == INVALID
+    assert step(L, q=None, N=1 << 20, nslots=1 << 20, Hk=1, H=256) == UNSUPPORTED
+    assert step(L, q=None, Hk=1, H=(1 << 17) - 1) == INVALID and step(L, q=None, Hk=1, H=1 << 17) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("T, seqs", [(1000, 0), (1000, 7), (16384, 0), (16384, 1), (20000, 3), (40, 7)])
+@pytest.mark.parametrize("K, V, H", [(128, 128, 2), (32, 96, 1), (64, 128, 300)])
+def test_prefill_workspace_is_what_the_header_says(L, T, seqs, K, V, H):  # noqa: F811
+    got = WS(1, T, H, seqs, K, V)
+    if T < 16 * seqs:
+        assert got == 0
+        return
+    chunks = (T + 63) // 64 if seqs == 0 else (T + 63 * seqs) // 64
+    rest = got - 32896 * chunks * H
+    if H * max(1, seqs) >= 152:                            # never split
+        assert rest == 16 * seqs
+        return
+    unit = K * (K + V) * 4 * H + (16 if seqs else 0)
+    assert rest == 16 * seqs or (rest % unit == 0 and rest // unit > max(1, seqs))
+
+
+def test_prefill_workspace_of_split_sequences(L):  # noqa: F811
+    """One long sequence is split, packed or not: the segments' maps, and 16 bytes each where packed."""
+    dense, packed = WS(1, 16384, 2), WS(1, 16384, 2, 1)
+    images, unit = 32896 * 256 * 2, 128 * 256 * 4 * 2
+    parts = (dense - images) // unit
+    assert parts > 1 and dense == images + parts * unit
+    assert packed - images in [n * (unit + 16) for n in (parts, parts + 1)]
