@@ -53,7 +53,9 @@ typedef enum {
  * the bound (T + 63 num_seqs) / 64 on the chunks, at most T); packed, 16 for each
  * sequence; and where sequences are split (few heads, many chunks) K (K + V) 4 for
  * each segment and head, the 16 bytes then for each segment.  It depends on nothing
- * but the arguments.  Pure host arithmetic.
+ * but the arguments.  It can be less for a larger T, which may take fewer segments;
+ * what it gives for a T is enough for every smaller one all the same.  Pure host
+ * arithmetic.
  */
 KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K,
                                                 int32_t V);
@@ -81,8 +83,9 @@ KDA_API size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H,
  *   gate        kda_gate_t.
  *   scale       factor on the output, usually K^-0.5.
  *   workspace   device, 16-byte aligned, kda_delta_prefill_workspace_size()
- *               bytes; its contents are scratch (KDA_ERR_WORKSPACE if missing or
- *               too small).
+ *               bytes; its contents are scratch.  One that has no room for the
+ *               segments but for the rest leaves sequences whole (as accurate, and
+ *               slower); less, or none, gives KDA_ERR_WORKSPACE.
  *
  * o, state_out and the workspace must not overlap each other or anything that is
  * read (KDA_ERR_INVALID_ARGUMENT), but for state_out, which may be state_in.

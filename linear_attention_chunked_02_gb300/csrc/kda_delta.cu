@@ -61,6 +61,13 @@ size_t image_bytes(int64_t B, int64_t T, int32_t H, int32_t num_seqs) {
     return size_t(max_chunks(B, T, num_seqs, BT)) * size_t(H) * IMG_BYTES;
 }
 
+// The workspace of a call whose sequences are cut into segments of `seg` chunks (0: whole), `units` in all.
+size_t workspace_bytes_for(int64_t B, int64_t T, int32_t H, int32_t num_seqs, int32_t K, int32_t V, int32_t seg,
+                           int64_t units) {
+    return image_bytes(B, T, H, num_seqs) + (num_seqs > 0 ? size_t(units) * sizeof(int4) : 0) +
+           (seg > 0 ? size_t(units) * size_t(H) * size_t(K) * size_t(K + V) * sizeof(float) : 0);
+}
+
 bool width_ok(int32_t w) { return w == 32 || w == 64 || w == 96 || w == 128; }
 
 template <typename T>
@@ -192,8 +199,7 @@ size_t kda_delta_prefill_workspace_size(int64_t B, int64_t T, int32_t H, int32_t
     if (!chunked_form(B, T, num_seqs)) return 0;
     int64_t units = 0;
     const int32_t seg = segment_chunks(B, T, H, num_seqs, units);
-    return image_bytes(B, T, H, num_seqs) + (num_seqs > 0 ? size_t(units) * sizeof(int4) : 0) +
-           (seg > 0 ? size_t(units) * size_t(H) * size_t(K) * size_t(K + V) * sizeof(float) : 0);
+    return workspace_bytes_for(B, T, H, num_seqs, K, V, seg, units);
 }
 
 kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const void *beta, void *o,
@@ -219,8 +225,17 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
         if (st != KDA_OK) return st;
     }
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_INVALID_ARGUMENT;
-    const size_t need = kda_delta_prefill_workspace_size(B, T, H, num_seqs, K, V);
-    if (need > 0) {
+    int32_t seg = 0;
+    int64_t units = 0;
+    size_t need = 0;
+    if (chunked_form(B, T, num_seqs)) {
+        seg = segment_chunks(B, T, H, num_seqs, units);
+        need = workspace_bytes_for(B, T, H, num_seqs, K, V, seg, units);
+        if (workspace_bytes < need && seg > 0) {           // no room for the maps: sequences whole
+            seg = 0;
+            units = seqs;
+            need = workspace_bytes_for(B, T, H, num_seqs, K, V, seg, units);
+        }
         if (workspace == nullptr || workspace_bytes < need) return KDA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return KDA_ERR_INVALID_ARGUMENT;
     }
@@ -232,8 +247,7 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
     if (!chunked_form(B, T, num_seqs)) return run_rec(p, dtype, static_cast<cudaStream_t>(stream));
     p.cpr = int32_t((T + BT - 1) / BT);
     p.n_tasks = int32_t(max_chunks(B, T, num_seqs, BT) * H);
-    int64_t units = 0;
-    p.seg = segment_chunks(B, T, H, num_seqs, units);
+    p.seg = seg;
     p.n_units = int32_t(units);
     unsigned char *after = p.ws + image_bytes(B, T, H, num_seqs);
     if (num_seqs > 0) {

@@ -111,7 +111,7 @@ def _output(name: str, out: Optional[torch.Tensor], like: torch.Tensor) -> torch
 
 
 def delta_prefill_workspace_size(B: int, T: int, H: int, num_seqs: int = 0, K: int = 128, V: int = 128) -> int:
-    """Bytes of workspace delta_prefill needs for this shape."""
+    """Bytes of workspace delta_prefill needs for this shape; enough for every smaller T too."""
     return int(lib().kda_delta_prefill_workspace_size(B, T, H, num_seqs, K, V))
 
 

@@ -5,7 +5,7 @@ size is just allowed, a missing pointer refuses it after the sizes were looked a
 import pytest
 
 import linear_attention_chunked_02_gb300 as kda
-from test_layer_abi_cpu import INVALID, L, P, UNSUPPORTED, prefill, step  # noqa: F401
+from test_layer_abi_cpu import INVALID, L, P, UNSUPPORTED, WORKSPACE, prefill, step  # noqa: F401
 
 WS = kda.delta_prefill_workspace_size
 
@@ -92,3 +92,24 @@ def test_prefill_workspace_of_split_sequences(L):  # noqa: F811
     parts = (dense - images) // unit
     assert parts > 1 and dense == images + parts * unit
     assert packed - images in [n * (unit + 16) for n in (parts, parts + 1)]
+
+
+def test_prefill_workspace_serves_smaller_prompts(L):  # noqa: F811
+    """The size for one T is refused for no smaller one; what has no room for the images is, for every T."""
+    def given(T, ws, H, seqs):                             # a misplaced o refuses the call after the workspace's size
+        packed = {"cu": P[8], "nseq": seqs} if seqs else {}
+        return prefill(L, T=T, Hk=1, H=H, o=P[0], ws=P[11] * 64, wsb=ws, **packed)
+
+    for H, seqs in ((1, 0), (16, 0), (32, 0), (16, 4), (2, 3)):
+        largest, shrinks = 0, 0
+        for T in range(64, 20000, 320):
+            size = WS(1, T, H, seqs)
+            shrinks += size < largest
+            largest = max(largest, size)
+            chunks = (T + 63) // 64 if seqs == 0 else (T + 63 * seqs) // 64
+            least = 32896 * chunks * H + 16 * seqs
+            if size:
+                assert given(T, least, H, seqs) == INVALID and given(T, least - 1, H, seqs) == WORKSPACE
+                for longer in range(T, T + 3000, 320):
+                    assert WS(1, longer, H, seqs) >= least
+        assert shrinks > 0

@@ -83,3 +83,19 @@ def test_split_slots_of_none(kda):  # noqa: F811
         close(o[0, a:b], wo[n], F32, f"o {n}")
     close(pool[3], wS[0], F32, "state 0")
     assert all(torch.equal(pool[e], before[e]) for e in (0, 1, 2, 4))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_workspace_without_room_for_segments(kda, packed):  # noqa: F811
+    """A workspace that holds all but the segments' maps: the sequences are walked whole."""
+    x = Rule([2500, 2500], Hk=2, H=2, dtype=F32, packed=packed, seed=55, rate=0.02, initial=True)
+    size = kda.delta_prefill_workspace_size(*((1, 5000, 2, 2) if packed else (2, 2500, 2)))
+    chunks = (5000 + 126) // 64 if packed else 80
+    least = 32896 * chunks * 2 + (32 if packed else 0)
+    assert size > least
+    for given in (least, size - 1, size):
+        ws = torch.full((given + 256,), 255, dtype=torch.uint8, device=DEV)
+        x.check(kda, f"{given} bytes", workspace=ws[:given])
+        assert torch.all(ws[given:] == 255)
+    with pytest.raises(kda.KdaError, match="workspace"):
+        x.run(kda, workspace=ws[:least - 1])
