@@ -111,10 +111,11 @@ struct NormRow {
             for (int e = 0; e < VEC; ++e) {
                 a[e] = r[i][e] * inv * to_f32(w[i].v[e]);
                 if (KIND != NORM_ADD) {
-                    // the fast quotient and exponential: a few units in the last place, and 0 for a gate
-                    // far below zero, where the divisor passes 2^126
+                    // 16-bit types take the fast quotient and exponential, whose error grows with a gate below
+                    // zero: 6e-6 at -86, far below their rounding, and 0 further down, where the divisor
+                    // passes 2^126.  In FP32 that would be 64 units in the last place
                     const float g = to_f32(z[i].v[e]);
-                    const float sg = __fdividef(1.f, 1.f + __expf(-g));
+                    const float sg = sizeof(T) == 4 ? 1.f / (1.f + expf(-g)) : __fdividef(1.f, 1.f + __expf(-g));
                     a[e] *= KIND == NORM_GATED_SILU ? g * sg : sg;
                 }
             }

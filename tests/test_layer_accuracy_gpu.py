@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.layer as ref
+
 from test_layer_gpu import BF16, DEV, F16, F32, Rule, close, f64, kda  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +58,17 @@ def test_split_sequence_forgets_what_a_chunk_clears(kda, big, clear, fall, K, V,
     close(o[a:], wo[0][a:], dtype, "outputs after the chunk")
     close(S[0], wS[0], F32, "state")
     close(o, wo[0], dtype, "all outputs")
+
+
+# In FP32, units of 2^-24: the exponential 2, the sum with one 1, the quotient 1, four products 4, the root 4, the
+# mean of 128 squares (a chain of four and five steps between lanes, halved by the root) 5: 17, and 20 allowed.
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gated_norm_gates_far_out(kda, act):  # noqa: F811
+    rng = np.random.default_rng(71)
+    gate = torch.from_numpy(np.linspace(-86, 40, 128 * 512).reshape(512, 128)).float()
+    x = torch.from_numpy(rng.standard_normal((512, 128))).float()
+    w = torch.from_numpy(1 + 0.1 * rng.standard_normal(128)).float()
+    want = ref.gated_norm(f64(x), f64(gate), f64(w), 1e-6, act)
+    got = f64(kda.gated_norm(x.to(DEV), gate.to(DEV), w.to(DEV), activation=act))
+    worst = np.max(np.abs(got - want) / (np.abs(want) + 1e-38))
+    assert worst <= 20 * 2.0 ** -24, f"{worst * 2 ** 24:.1f} units of 2^-24"
