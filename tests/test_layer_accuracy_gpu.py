@@ -72,3 +72,15 @@ def test_gated_norm_gates_far_out(kda, act):  # noqa: F811
     got = f64(kda.gated_norm(x.to(DEV), gate.to(DEV), w.to(DEV), activation=act))
     worst = np.max(np.abs(got - want) / (np.abs(want) + 1e-38))
     assert worst <= 20 * 2.0 ** -24, f"{worst * 2 ** 24:.1f} units of 2^-24"
+
+
+# Both ways round at the same places to a type of unit roundoff u, and differ where a value falls on the other side:
+# some eight roundings a layer, each at most u / sqrt(3) sqrt(2) in the mean, two layers and a last norm: 17 of them
+# make 3.4 u in the mean square, 4 times that for the largest of 4000 outputs, which are up to 4 times their mean
+# themselves; four times the 3.4 u that this comes to allows for what the layers amplify.
+@pytest.mark.parametrize("dtype, u", [(F16, 2.0 ** -11), (BF16, 2.0 ** -8)], ids=str)
+def test_example_differs_by_roundings(dtype, u):
+    from test_layer_example_gpu import _example
+
+    _, off = _example().run(dtype, layers=2, dim=256, heads=4, width=64, lengths=(70, 1, 33), new_tokens=5)
+    assert off <= 14 * u, off / u
