@@ -5,7 +5,7 @@ before the block, ``delta_prefill`` over prompts or ``delta_step`` for one token
 each running request, ``gated_norm`` on the heads' outputs.  Inference only: no
 operator records gradients.
 
-With ``stream``, everything a call does (copies of tensors whose layout does not fit
+With ``stream`` (one of the tensors' device), everything a call does (copies of tensors whose layout does not fit
 and new outputs among it) happens on that stream; ordering it after the work that
 produced the inputs, and the outputs' use on other streams, is the caller's.
 """
@@ -24,6 +24,8 @@ ACT_CODE = {"sigmoid": 0, "silu": 1}
 def _elsewhere(device: int, stream: Optional[torch.cuda.Stream]):
     """None where the call can run as it is; else the context in which it can: `stream`, or `device` made current."""
     if stream is not None:
+        if stream.device_index != device:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
         return torch.cuda.stream(stream)
     return None if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
 

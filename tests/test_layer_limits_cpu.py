@@ -113,3 +113,13 @@ def test_prefill_workspace_serves_smaller_prompts(L):  # noqa: F811
                 for longer in range(T, T + 3000, 320):
                     assert WS(1, longer, H, seqs) >= least
         assert shrinks > 0
+
+
+def test_stream_of_another_device():
+    """Refused, not left for the tensors' device's current stream."""
+    class Stream:
+        device_index = 1
+
+    from linear_attention_chunked_02_gb300 import layer
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        layer._elsewhere(0, Stream())
