@@ -755,14 +755,18 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                     y[i] = W2::wide(two(kp, i, dc));
                     g[i] = decay(i, dc);
                 }
-                if (x == nh - 1) {                         // the staged chunk is read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[SB_ST_EMPTY]);
-                }
 #pragma unroll
                 for (int i = 7; i >= 0; --i) {
                     y[i] = __fmul2_rn(y[i], __fmul2_rn(make_float2(ex2(after.x), ex2(after.y)), sk));
                     after = __ffma2_rn(g[i], both(L2E), after);
+                }
+                // the staged chunk is read.  The loads must be done, not on their way, before a copy may follow:
+                // hence after what uses them, and with the fence.  (Without both, one run in fifteen with
+                // three walks to a CTA took some row's decays from the next chunk.)
+                if (x == nh - 1) {
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[SB_ST_EMPTY]);
                 }
                 uint4 ah, al, bh, bl;
                 split_f16(y[0].x, y[1].x, ah.x, al.x); split_f16(y[2].x, y[3].x, ah.y, al.y);
@@ -809,10 +813,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
             const float *hdr = reinterpret_cast<const float *>(sm + SCAN_OFF_IMG + IMG_HDR);
             prep_wait(ok, &bars[SB_IMG_FULL], ph, p.err);
             const float p0 = hdr[HDR_PINV], p1 = hdr[HDR_PINV + 1], qmax = hdr[HDR_QMAX];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ]);
             float invq;
             pow2_scale(qmax * fabsf(p.scale), KQ_LO, KQ_HI, invq);
+            fence_proxy_async();                           // read before the next image's copy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SB_IMG_READ]);
             prep_wait(ok, &bars[SB_O_FULL], ph, p.err);
             __syncwarp();
             tc::fence_after_sync();

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_layer_gpu import BF16, DEV, F32, Rule, close, kda  # noqa: F401
+from test_layer_gpu import BF16, DEV, F16, F32, Rule, close, kda  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,21 @@ def test_workspace_without_room_for_segments(kda, packed):  # noqa: F811
         assert torch.all(ws[given:] == 255)
     with pytest.raises(kda.KdaError, match="workspace"):
         x.run(kda, workspace=ws[:least - 1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("lens, H, reps", [([384, 640, 1024, 2048, 384], 10, 300), ([4160, 1, 16384, 4160], 16, 30),
+                                           ([320] * 40, 16, 60)], ids=str)
+def test_prefill_repeats_bit_for_bit_over_many_walks(kda, dtype, lens, H, reps):  # noqa: F811
+    """Several walks to a CTA, so that their buffers go from one to the next while other warps still read; one
+    chunk's row read too late shows in some runs only."""
+    x = Rule(lens, Hk=H, H=H, dtype=dtype, seed=57, rate=0.02, initial=True)
+    args, cu, S0 = x.args(), x.cu.to(DEV), x.state.to(DEV)
+    o, S = (t.clone() for t in kda.delta_prefill(*args, cu_seqlens=cu, initial_state=S0))
+    out, S1 = torch.empty_like(o), torch.empty_like(S)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(reps):
+        out.zero_()
+        kda.delta_prefill(*args, cu_seqlens=cu, initial_state=S0, final_state=S1, out=out)
+        differ += (out != o).any() | (S1 != S).any()
+    assert int(differ) == 0
