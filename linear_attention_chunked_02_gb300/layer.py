@@ -131,7 +131,7 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     initial_state, final_state: float32 [N, H, K, V] (N = B for the dense layout); zeros and
     a new tensor if not given.  With slots (int32 [N]) both are pools of which sequence n
     uses entry slots[n], final_state is written in place and defaults to initial_state.
-    workspace: optional CUDA buffer of delta_prefill_workspace_size() bytes.
+    workspace: optional contiguous CUDA buffer of delta_prefill_workspace_size() bytes.
     """
     device = _on_gpu("q k v g beta cu_seqlens initial_state final_state slots out workspace", q, k, v, g, beta,
                      cu_seqlens, initial_state, final_state, slots, out, workspace)
@@ -149,6 +149,8 @@ def delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     slots = _int32("slots", slots, N)
     if slots is not None and initial_state is None and final_state is None:
         raise ValueError("slots need a state pool")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")   # its elements are counted as consecutive bytes
     if final_state is None and slots is not None:
         final_state = initial_state
     entries = N if slots is None else final_state.shape[0]

@@ -117,3 +117,13 @@ def test_prefill_repeats_bit_for_bit_over_many_walks(kda, dtype, lens, H, reps):
         kda.delta_prefill(*args, cu_seqlens=cu, initial_state=S0, final_state=S1, out=out)
         differ += (out != o).any() | (S1 != S).any()
     assert int(differ) == 0
+
+
+def test_workspace_of_repeated_bytes(kda):  # noqa: F811
+    """A view with more elements than memory is refused before anything is launched."""
+    x = Rule([130, 64], dtype=BF16, seed=56)
+    need = kda.delta_prefill_workspace_size(1, 194, 2, 2)
+    one = torch.zeros(16, dtype=torch.uint8, device=DEV)
+    for ws in (one.repeat(2)[::2], one[:1].expand(need), torch.zeros(2 * need, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            x.run(kda, workspace=ws)
