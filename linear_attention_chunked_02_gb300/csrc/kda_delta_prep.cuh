@@ -53,8 +53,9 @@ namespace kda {
 constexpr int IMG_MHI = 0, IMG_MLO = 8192, IMG_PHI = 16384, IMG_PLO = 24576, IMG_HDR = 32768;
 constexpr int IMG_HDR_BYTES = 128, IMG_BYTES = IMG_HDR + IMG_HDR_BYTES;
 // header (floats): 1 / scale of M rows 0-31, 32-63; largest row sum of |M| in the halves;
-// 1 / scale of P in the halves; largest |k|, |q|
-constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7;
+// 1 / scale of P in the halves; largest |k|, |q|; and, from the walk that finds a segment's M, the largest
+// channel's decay over the chunk
+constexpr int HDR_MINV = 0, HDR_MSUM = 2, HDR_PINV = 4, HDR_KMAX = 6, HDR_QMAX = 7, HDR_GMAX = 8;
 
 constexpr int PREP_THREADS = 28 * 32, PREP_REGISTERS = 72;     // per thread at launch
 constexpr int PREP_TW = 8;                         // transform warps of a group

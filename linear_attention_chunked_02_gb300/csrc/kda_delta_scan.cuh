@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                 for (int i = 0; i < 8; ++i) sum = __ffma2_rn(decay(i, d), both(L2E), sum);   // in powers of two
                 *reinterpret_cast<float2 *>(tot + rg * 128 + 64 * x + 2 * lane) = sum;
             }
-            float inv, unused;
+            float inv, unused, gmax = 0.f;
             const float sk1 = pow2_scale(kqmax.x, KQ_LO, KQ_HI, inv);
             const float2 cq = both(p.scale * pow2_scale(kqmax.y * fabsf(p.scale), KQ_LO, KQ_HI, unused) * inv);
             named_sync<1, 256>();
@@ -690,9 +690,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         if (!TRANS) *reinterpret_cast<uint2 *>(at + 49152) = make_uint2(ql[0], ql[1]);
                     }
                 }
-                if (rg == 7)                               // here G is the whole chunk's sum
-                    *reinterpret_cast<float4 *>(gam + ph * 128 + 4 * lane) =
-                        make_float4(ex2(G[0].x), ex2(G[0].y), ex2(G[1].x), ex2(G[1].y));
+                if (rg == 7) {                             // here G is the whole chunk's sum
+                    const float4 e = make_float4(ex2(G[0].x), ex2(G[0].y), ex2(G[1].x), ex2(G[1].y));
+                    *reinterpret_cast<float4 *>(gam + ph * 128 + 4 * lane) = e;
+                    if (4 * lane < K) gmax = fmaxf(fmaxf(e.x, e.y), fmaxf(e.z, e.w));
+                }
             }
 #pragma unroll 1
             for (int x = 0; !FOUR && x < nh; ++x) {
@@ -730,8 +732,16 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
                         if (!TRANS) *reinterpret_cast<uint32_t *>(at + 49152) = ql;
                     }
                 }
-                if (rg == 7)                               // here G is the whole chunk's sum
-                    *reinterpret_cast<float2 *>(gam + ph * 128 + 64 * x + 2 * lane) = make_float2(ex2(G.x), ex2(G.y));
+                if (rg == 7) {                             // here G is the whole chunk's sum
+                    const float2 e = make_float2(ex2(G.x), ex2(G.y));
+                    *reinterpret_cast<float2 *>(gam + ph * 128 + 64 * x + 2 * lane) = e;
+                    if (64 * x + 2 * lane < K) gmax = fmaxf(gmax, fmaxf(e.x, e.y));
+                }
+            }
+            if (TRANS && rg == 7 && wk.run == 1) {         // for the join
+                gmax = warp_max(gmax);
+                if (lane == 0)
+                    *reinterpret_cast<float *>(const_cast<unsigned char *>(img0) + c * img_step + IMG_HDR + 4 * HDR_GMAX) = gmax;
             }
             fence_proxy_async();
             __syncwarp();
@@ -1015,7 +1025,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 // M's columns are as good as 2^-34 or so of what went into each chunk, so where a chunk clears the state
 // M can have lost what little is left of it.  That counts where the state that comes in is so large
 // that the rest of it, M S, is not lost beside N.  A block which finds M S below JOIN_FALL of S in a column, but not
-// below 2^-20 of the sum, looks for such a chunk in the segment's decays, and if there is one walks the
+// below 2^-20 of the sum, looks for such a chunk in the segment, and if there is one walks the
 // segment token by token (join_tokens): about a microsecond a token.
 constexpr int JOIN_THREADS = 256, JOIN_COLS = 16, JOIN_PITCH = 68;
 constexpr int JOIN_BYTES = 2 * 128 * JOIN_PITCH * 4;
@@ -1028,19 +1038,14 @@ struct JoinShared {
     int32_t red[8];
 };
 
-// Whether one of the segment's chunks (rows a .. b of head h) keeps less than SCAN_WEAK_G of every channel.
-// The same for all threads.
-__device__ __forceinline__ bool join_cleared(const DeltaParams &p, int64_t a, int64_t b, int h) {
+// Whether one of the `n` chunks from `chunk` on keeps less than SCAN_WEAK_G of every channel of head h, from what
+// M's walk left in their images (reading the decays themselves took 50 us at 1 x 2048 tokens x 32 heads).  The
+// same for all threads.
+__device__ __forceinline__ bool join_cleared(const DeltaParams &p, int64_t chunk, int n, int h) {
     bool any = false;
-    for (; a < b; a += BT) {
-        const int n = b - a < BT ? int(b - a) : BT, d = int(threadIdx.x);
-        float sum = 0.f;
-        if (d < p.K)
-#pragma unroll 8
-            for (int t = 0; t < n; ++t) sum += p.g[p.gate == 0 ? ((a + t) * p.H + h) * p.K + d : (a + t) * p.H + h];
-        any |= __syncthreads_and(d >= p.K || expf(sum) < SCAN_WEAK_G) != 0;
-    }
-    return any;
+    for (int i = int(threadIdx.x); i < n && (chunk + i + 1) * p.H <= p.n_tasks; i += JOIN_THREADS)
+        any |= *reinterpret_cast<const float *>(p.ws + ((chunk + i) * p.H + h) * IMG_BYTES + IMG_HDR + 4 * HDR_GMAX) < SCAN_WEAK_G;
+    return __syncthreads_or(any) != 0;
 }
 
 // The state of rows r, r + 1 and columns c .. + 3 of the block's after rows a .. b, token by token in FP32.
@@ -1220,7 +1225,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) kda_delta_join_kernel(const Delt
             sequence_rows(p, n, r0, r1);
             r0 += int64_t(BT) * p.seg * i;
             if (r1 > r0 + int64_t(BT) * p.seg) r1 = r0 + int64_t(BT) * p.seg;
-            if (join_cleared(p, r0, r1, h)) join_tokens<T>(p, sh, n4, r0, r1, h, r, c, JOIN_COLS * slice);
+            const int64_t chunk = p.cu == nullptr ? int64_t(n) * p.cpr : int64_t(p.units[u0].z);
+            if (join_cleared(p, max(int64_t(0), chunk) + int64_t(p.seg) * i, p.seg, h))
+                join_tokens<T>(p, sh, n4, r0, r1, h, r, c, JOIN_COLS * slice);
             columns_max(n4, 1);
             __syncthreads();
             before = column_max(1);
