@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
         if (w >= walks) return make_int4(0, 0, 0, 0);
         int run;
         const int32_t u = unit_at(w, run);
-        if (p.cu != nullptr) return __ldg(p.units + u);
+        if (p.cu != nullptr) return p.units[u];            // a plain load: the call's first kernel wrote it
         const int32_t n = u / parts;
         return make_int4(n, u - n * parts, n * p.cpr, parts);
     };
