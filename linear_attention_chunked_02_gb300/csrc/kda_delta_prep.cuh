@@ -33,8 +33,8 @@
 //     with beta and the mask into the solve's tile, P into its image;
 //   * warps 24-27: two pairs, each the 64-token solve of every second chunk-head,
 //     and M's image.
-// 16 x 512 tokens x 64 heads of BF16, K = 128: 203 us and 710 MB, 3.5 TB/s.  What bounds it is issue: 160
-// million warp instructions, 69 % of the slots; the transform groups and the solve pairs
+// 16 x 512 tokens x 64 heads of BF16, K = 128: 203 us and 770 MB, 3.8 TB/s.  What bounds it is issue: 162
+// million warp instructions, 70 % of the slots; the transform groups and the solve pairs
 // are both busy nearly all the time (7400 and 6500 cycles to a chunk-head).
 // Five kinds of code run at once on an SM whose instruction cache holds about 32 KB of
 // them: with everything unrolled (100 KB) half the cache's requests missed and

@@ -16,10 +16,10 @@
 // step, and lanes (value columns) never mix: a lane has scales of its own.
 //
 // FP32 accuracy from FP16: every operand is hi + lo (22 bits) and a product hi hi + hi lo +
-// lo hi, for all types: Q and P of BF16 calls with their high parts alone would save 2 to 4 %
-// (16 x 512 x 64 heads: 462 us, not 476) and take their outputs 1.1e-3 of the norm away from the rounded
-// 64-bit result, which they now meet to 1e-4.  FP16 has range for that only under scales.  They are powers of two from
-// rigorous bounds: the images carry the largest |k|, |q| and M's row sums; a lane
+// lo hi, for all types: Q and P of BF16 calls with their high parts alone saved 2 to 4 %
+// (16 x 512 x 64 heads: 462 us, 476 with both) and took their outputs 1.1e-3 of the norm away from
+// the rounded 64-bit result, which they now meet to 1e-4.  FP16 has range for that only under scales.  They are powers of
+// two from rigorous bounds: the images carry the largest |k|, |q| and M's row sums; a lane
 // measures |S| after each chunk and knows |v|; then |R| <= |v| + K |k| |S|,
 // |U| <= |M|_1 |R|, |S1| <= |S| + 64 |k| |U|.  The bounds overshoot by up to 2^13
 // and leave 2^-25 2^-15 2^13 of the largest value as the error of a product.  That is
@@ -49,13 +49,13 @@
 //   * warp 28: MMA issue; warps 29, 30 and 31: the loads (TMA) of q, k and g, of v, and of the
 //     images.  Plain loads stall here (what the CTA leaves of the L1 holds too
 //     little in flight), so g is staged in shared memory, and q and k where they find room: of 16
-//     bits, or of 32 bits and up to 64 channels (2 x 1000 tokens, 16 heads, K = 64: 73 us, not 77).
+//     bits, or of 32 bits and up to 64 channels (2 x 1000 tokens, 16 heads, K = 64: 5 % less time).
 //     32-bit ones of more channels are read directly (64 x 512 tokens, 32 heads of
 //     K = V = 128, the whole operator: 1250 us, 1397 with g read directly too).
-// 16 x 512 tokens x 64 heads of BF16, K = V = 128: 250 us and 1055 MB, 4.2 TB/s; 4.7 us a chunk and
-// CTA.  179 million warp instructions take 65 % of the issue slots, and the chain and the operand
-// warps each need about the whole of a chunk's 9000 cycles.  With segments (1 x 16384 x 32 heads):
-// N and M 333 us (2.9 us a chunk), the join 45, the walk 267.
+// 16 x 512 tokens x 64 heads of BF16, K = V = 128: 266 us and 1126 MB, 4.2 TB/s; 4.9 us a chunk and
+// CTA.  185 million warp instructions take 62 % of the issue slots, and the chain and the operand
+// warps each need about the whole of a chunk's 9500 cycles.  With segments (1 x 16384 x 32 heads):
+// N and M 360 us (3.1 us a chunk), the join 49, the walk 289.
 #pragma once
 
 #include "kda_delta_prep.cuh"
@@ -1020,7 +1020,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) kda_delta_scan_kernel(const _
 // segment i.  A block has 16 columns of one sequence-head, a thread four of them in two rows.  FP32;
 // the sequence's first segment gave its state itself.  M comes through shared memory 64 columns
 // at a time, the next ones' copy under way during a product: at that size two blocks share an SM,
-// and the 256 blocks of 32 heads are one wave (8 segments: 45 us, 57 with all of M staged).
+// and the 256 blocks of 32 heads are one wave (8 segments: 45 us, 57 with all of M staged; 49 with the
+// check that follows).
 //
 // M's columns are as good as 2^-34 or so of what went into each chunk, so where a chunk clears the state
 // M can have lost what little is left of it.  That counts where the state that comes in is so large
