@@ -1,5 +1,5 @@
 """The gated delta rule over sequences that are split into segments: states updated in place,
-packed batches whose walks take more than one round of the GPU's SMs.
+packed batches with more walks than the GPU has SMs.
 
 Tolerances are those of test_layer_gpu.py, fixed there.
 """
