@@ -6,7 +6,9 @@ the chunk's strictly lower-triangular matrix ``A`` (LightLLM PR #1703,
 tokens (the solver's shorter branches) are taken from A's last dimension.
 ``delta_prefill``,
 ``delta_step``, ``add_norm`` and ``gated_norm`` are the operators of the layer that
-holds the solve.  Every step runs in the
+holds the solve; ``gated_scan``, ``gated_step``, ``gated_scan_backward``, ``gated_norm_backward``,
+``checkpoint_save`` and ``checkpoint_load`` those of a gated recurrent layer, in training
+and serving.  Every step runs in the
 CUDA kernels of ``libkda_solve_tril.so``; this module only checks and
 marshals arguments (torch provides device memory and streams).
 """
@@ -20,6 +22,9 @@ import torch
 from ._lib import DTYPE_CODE, KdaError, LIB_PATH, check as _check, lib  # noqa: F401
 from .layer import (add_norm, delta_prefill, delta_prefill_workspace_size, delta_step,  # noqa: F401
                     gated_norm)
+from .recurrence import (SCAN_CHUNK, Checkpoint, checkpoint_load, checkpoint_save, gated_norm_backward,  # noqa: F401
+                         gated_norm_backward_workspace_size, gated_scan, gated_scan_backward, gated_scan_chunks,
+                         gated_step)
 
 BT = 64
 CHUNK_LENGTHS = (16, 32, 64)

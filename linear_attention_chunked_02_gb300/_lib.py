@@ -1,5 +1,5 @@
-"""ctypes loader for libkda_solve_tril.so (the C ABI in include/kda_solve_tril.h
-and include/kda_layer.h).
+"""ctypes loader for libkda_solve_tril.so (the C ABI in include/kda_solve_tril.h,
+include/kda_layer.h and include/kda_recurrent.h).
 
 There is no fallback: if the library is missing this raises, so nothing can
 silently run anywhere but the CUDA kernels.
@@ -47,6 +47,20 @@ SIGNATURES = [
                                                     _c.c_void_p]),
     ("kda_gated_norm", _c.c_int, [_c.c_void_p] * 4 + [_c.c_int64, _c.c_int32, _c.c_float, _c.c_int32, _c.c_int32,
                                                       _c.c_void_p]),
+    ("kda_gated_scan", _c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64] + [_c.c_void_p] * 4
+     + [_c.c_int32, _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int64] + [_c.c_int32] * 5 + [_c.c_void_p]),
+    ("kda_gated_scan_backward", _c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                           _c.c_void_p, _c.c_int64] + [_c.c_void_p] * 7
+     + [_c.c_int32, _c.c_int64, _c.c_int64] + [_c.c_int32] * 5 + [_c.c_void_p]),
+    ("kda_gated_step", _c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64] + [_c.c_void_p] * 3
+     + [_c.c_int32] * 7 + [_c.c_void_p]),
+    ("kda_checkpoint_save", _c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int32,
+                                       _c.c_int32, _c.c_void_p]),
+    ("kda_checkpoint_load", _c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int32, _c.c_int32,
+                                       _c.c_void_p]),
+    ("kda_gated_norm_backward_workspace_size", _c.c_size_t, [_c.c_int64, _c.c_int32]),
+    ("kda_gated_norm_backward", _c.c_int, [_c.c_void_p] * 9 + [_c.c_int64, _c.c_int32, _c.c_float, _c.c_int32, _c.c_int32,
+                                                               _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     ("kda_selftest_wait", _c.c_int, [_c.c_int32, _c.c_uint32, _c.c_void_p]),
     ("kda_status_string", _c.c_char_p, [_c.c_int32]),
     ("kda_device_error", _c.c_int, [_c.c_int32, _c.POINTER(_c.c_uint32)]),

@@ -1,0 +1,348 @@
+// kda_recur.cu -- C ABI of the gated linear recurrence (argument checks, launch shapes), the
+// decoding step, and 8-bit checkpoints of activations.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "kda_internal.h"
+#include "kda_launch.cuh"
+#include "kda_recur_launch.h"
+#include "kda_recurrent.h"
+#include "kda_spans.h"
+
+namespace {
+
+using namespace kda;
+
+// ------------------------------------------------------------- decoding step
+// h <- a h + c x for one token of every request: a thread takes VEC channels of one request.  Bound
+// by the state's traffic, or by the launch for few requests.
+struct StepParams {
+    const void *x, *g;
+    int64_t ldx, ldg;
+    void *y;
+    float *state;
+    const int32_t *slots;
+    int32_t num_slots, D, form, blocks;                     // blocks to a request
+};
+constexpr int STEP_THREADS = 128;
+
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(STEP_THREADS) kda_gated_step_kernel(const StepParams p) {
+    const int n = int(blockIdx.x / unsigned(p.blocks));
+    const int col = (int(blockIdx.x % unsigned(p.blocks)) * STEP_THREADS + int(threadIdx.x)) * VEC;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (col >= p.D) return;
+    int entry = n;
+    if (p.slots != nullptr) {
+        entry = p.slots[n];
+        if (entry >= p.num_slots) entry = -1;
+    }
+    float a[VEC], c[VEC], x[VEC], h[VEC] = {};
+    const raw_t<T, VEC> xr = load_once<T, VEC>(static_cast<const T *>(p.x) + n * p.ldx + col);
+    const raw_t<G, VEC> gr = load_once<G, VEC>(static_cast<const G *>(p.g) + n * p.ldg + col);
+    float *s = p.state + int64_t(entry) * p.D + col;
+    if (entry >= 0) widen<float, VEC>(*reinterpret_cast<const raw_t<float, VEC> *>(s), h);
+    widen<T, VEC>(xr, x);
+    widen<G, VEC>(gr, a);
+    decays<VEC>(p.form, a, c);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[v], h[v], p.form & RECUR_COMPLEMENT ? c[v] * x[v] : x[v]);
+    if (entry >= 0) store_raw<float, VEC>(s, narrow<float, VEC>(h));
+    store_raw<T, VEC>(static_cast<T *>(p.y) + int64_t(n) * p.D + col, narrow<T, VEC>(h));
+}
+
+template <typename T, typename G>
+cudaError_t launch_step(StepParams p, int32_t N, int vec, cudaStream_t s) {
+    p.blocks = (p.D + STEP_THREADS * vec - 1) / (STEP_THREADS * vec);
+    const unsigned grid = unsigned(N) * unsigned(p.blocks);
+    return vec == 2 ? launch_pdl(true, kda_gated_step_kernel<T, G, 2>, grid, STEP_THREADS, 0, s, p)
+                    : launch_pdl(true, kda_gated_step_kernel<T, G, 1>, grid, STEP_THREADS, 0, s, p);
+}
+
+// ------------------------------------------------------------- checkpoints
+struct CkptParams {
+    const void *x;              // save: [rows, dim] at pitch ldx
+    void *out;                  // load: [rows, dim]
+    int64_t ldx, units;         // units: blocks of 32 elements
+    int8_t *codes;
+    uint8_t *exponents;
+    int32_t dim, blocks;        // blocks of a row
+};
+constexpr int CKPT_THREADS = 256;
+
+// The exponent byte of a block whose largest magnitude has these bits: 127 2^e = 1.984375 2^(e + 6).
+__device__ __forceinline__ unsigned ckpt_exponent(unsigned top) {
+    const int e = int(top >> 23);
+    if (e == 255) return CKPT_BAD;
+    return unsigned(max(0, e - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0)));
+}
+
+// The code of x in a block of exponent byte e, whose inverse scale is given.  64 2^e is past the type's largest
+// finite value where e is the largest exponent that the type can have: 63 is taken in its place.
+template <typename T>
+__device__ __forceinline__ int8_t ckpt_code(float x, unsigned e, float inverse) {
+    constexpr unsigned TOP = (sizeof(T) == 2 && !std::is_same_v<T, __nv_bfloat16> ? 10 : 122) + 127;
+    if (e == CKPT_BAD) return 0;
+    const int k = __float2int_rn(x * inverse);
+    return int8_t(e == TOP ? max(-63, min(63, k)) : k);
+}
+
+// One warp to a block, one element to a lane.
+template <typename T>
+__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_save_kernel(const CkptParams p) {
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t u = int64_t(blockIdx.x) * (CKPT_THREADS / 32) + int(threadIdx.x >> 5); u < p.units;
+         u += int64_t(gridDim.x) * (CKPT_THREADS / 32)) {
+        const int64_t row = u / p.blocks;
+        const int col = int(u - row * p.blocks) * CKPT_BLOCK + lane;
+        const float x = col < p.dim ? widen_one(static_cast<const T *>(p.x)[row * p.ldx + col]) : 0.f;
+        const unsigned e = ckpt_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu));
+        const float inverse = __uint_as_float(e == CKPT_BAD ? 0u : (254u - e) << 23);
+        if (col < p.dim) p.codes[row * p.dim + col] = ckpt_code<T>(x, e, inverse);
+        if (lane == 0) p.exponents[u] = uint8_t(e);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_load_kernel(const CkptParams p) {
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t u = int64_t(blockIdx.x) * (CKPT_THREADS / 32) + int(threadIdx.x >> 5); u < p.units;
+         u += int64_t(gridDim.x) * (CKPT_THREADS / 32)) {
+        const int64_t row = u / p.blocks;
+        const int col = int(u - row * p.blocks) * CKPT_BLOCK + lane;
+        if (col < p.dim)
+            narrow_one(static_cast<T *>(p.out)[row * p.dim + col],
+                       float(p.codes[row * p.dim + col]) * ckpt_scale(p.exponents[u]));
+    }
+}
+
+template <typename T>
+cudaError_t launch_checkpoint(const CkptParams &p, cudaStream_t s) {
+    const int64_t need = (p.units + CKPT_THREADS / 32 - 1) / (CKPT_THREADS / 32), most = 152 * 8;
+    const unsigned grid = unsigned(need < most ? need : most);
+    return p.out == nullptr ? launch_pdl(true, kda_checkpoint_save_kernel<T>, grid, CKPT_THREADS, 0, s, p)
+                            : launch_pdl(true, kda_checkpoint_load_kernel<T>, grid, CKPT_THREADS, 0, s, p);
+}
+
+// ------------------------------------------------------------------- checks
+// Types, forms and widths that all entries of the recurrence share.
+kda_status_t check_form(int32_t D, int32_t dtype, int32_t g_dtype, int32_t decay, int32_t complement) {
+    if (!dtype_ok(dtype) || (g_dtype != dtype && g_dtype != KDA_F32)) return KDA_ERR_UNSUPPORTED;
+    if (decay != KDA_DECAY_LOG && decay != KDA_DECAY_SIGMOID) return KDA_ERR_INVALID_ARGUMENT;
+    if (complement != 0 && complement != 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (D < 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (D > KDA_RECUR_MAX_DIM) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status_t check_stream(const int32_t *cu, int32_t num_seqs, int64_t B, int64_t T) {
+    if (B < 0 || T < 0 || num_seqs < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if ((cu != nullptr) != (num_seqs > 0)) return KDA_ERR_INVALID_ARGUMENT;
+    if (cu != nullptr && (B != 1 || !aligned_to(cu, 4))) return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t limit = (int64_t(1) << 31) - (int64_t(1) << 16);
+    if (B >= (int64_t(1) << 30) || num_seqs >= (1 << 30) || T >= limit || (T > 0 && B > (limit - 1) / T))
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+int form_bits(int32_t decay, int32_t complement) {
+    return (decay == KDA_DECAY_SIGMOID ? RECUR_SIGMOID : 0) | (complement ? RECUR_COMPLEMENT : 0);
+}
+
+// Two channels to a lane where all vectors of two are aligned.
+bool pairs_fit(const Span *tensors, const size_t *es, const int64_t *ld, int n, int32_t D) {
+    if (D % 2 != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (tensors[i].at != nullptr && (!aligned_to(tensors[i].at, 2 * es[i]) || ld[i] % 2 != 0)) return false;
+    return true;
+}
+
+// The grid: 32 lanes' channels to a block, and as many parts of the stream as fill the GPU.
+void shape(RecurParams &p, RecurLaunch &l, int64_t B, int64_t T) {
+    l.slabs = unsigned((p.D + 32 * l.vec - 1) / (32 * l.vec));
+    const int64_t want = (152 * 4 + l.slabs - 1) / l.slabs;
+    int64_t parts = p.nseq < want ? p.nseq : want;
+    if (parts < 1) parts = 1;
+    int64_t part;
+    if (p.cu == nullptr) {
+        const int64_t each = (B + parts - 1) / parts;
+        parts = (B + each - 1) / each;
+        part = each * T;
+    } else {
+        part = (T + parts - 1) / parts;
+        if (part < 1) part = 1;
+        parts = T > 0 ? (T + part - 1) / part : 1;
+    }
+    l.parts = unsigned(parts);
+    p.part = int32_t(part);
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_gated_scan(const void *x, int64_t ldx, const void *g, int64_t ldg, void *y, const float *state_in,
+                            float *state_out, const int32_t *slots, int32_t num_slots, float *chunk_states,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t B, int64_t T, int32_t D, int32_t dtype,
+                            int32_t g_dtype, int32_t decay, int32_t complement, void *stream) {
+    kda_status_t st = check_form(D, dtype, g_dtype, decay, complement);
+    if (st == KDA_OK) st = check_stream(cu_seqlens, num_seqs, B, T);
+    if (st != KDA_OK) return st;
+    if (slots != nullptr && num_slots < 0) return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t seqs = cu_seqlens != nullptr ? num_seqs : B, rows = B * T;
+    if (seqs == 0) return KDA_OK;
+    const size_t es = size_t(elt_size(dtype)), gs = size_t(elt_size(g_dtype));
+    if (rows > 0 && (x == nullptr || g == nullptr || y == nullptr || ldx < D || ldg < D)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(x, es) || !aligned_to(g, gs) || !aligned_to(y, es) || !aligned_to(state_in, 4) ||
+        !aligned_to(state_out, 4) || !aligned_to(chunk_states, 4) || !aligned_to(slots, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t entries = slots != nullptr ? num_slots : seqs;
+    const Span xs = rows_span(x, rows, ldx, D, es), gsp = rows_span(g, rows, ldg, D, gs), ys = rows_span(y, rows, D, D, es);
+    const Span chunk = rows_span(chunk_states, (rows + RECUR_CHUNK - 1) / RECUR_CHUNK, D, D, 4);
+    const Span in_state = rows_span(state_in, entries, D, D, 4), out_state = rows_span(state_out, entries, D, D, 4);
+    const Span in[] = {xs, gsp, {slots, size_t(seqs) * 4}, {cu_seqlens, size_t(seqs + 1) * 4},
+                       state_in != state_out ? in_state : Span{nullptr, 0}};
+    const Span out[] = {ys, chunk, out_state};
+    if (any_meet(out, in) || meet(ys, in_state) || meet(chunk, in_state)) return KDA_ERR_INVALID_ARGUMENT;
+    if (rows == 0 && state_out == nullptr) return KDA_OK;
+    RecurParams p{};
+    p.x = x; p.g = g; p.ldx = ldx; p.ldg = ldg; p.cu = cu_seqlens; p.nseq = int32_t(seqs); p.T = int32_t(T);
+    p.rows = int32_t(rows); p.D = D; p.form = form_bits(decay, complement);
+    p.y = y; p.state_in = state_in; p.state_out = state_out; p.slots = slots; p.num_slots = num_slots;
+    p.chunk = chunk_states;
+    RecurLaunch l{};
+    l.wide_g = g_dtype == KDA_F32;
+    const Span all[] = {xs, gsp, ys, in_state, out_state, chunk};
+    const size_t sizes[] = {es, gs, es, 4, 4, 4};
+    const int64_t pitch[] = {ldx, ldg, D, D, D, D};
+    l.vec = pairs_fit(all, sizes, pitch, 6, D) ? 2 : 1;
+    shape(p, l, B, T);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == KDA_F32    ? launch_scan_f32(p, l, s)
+                          : dtype == KDA_BF16 ? launch_scan_bf16(p, l, s)
+                                              : launch_scan_f16(p, l, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const void *x, const uint8_t *x_exponents,
+                                     int64_t ldx, const void *g, const uint8_t *g_exponents, int64_t ldg,
+                                     const float *chunk_states, const float *state_in, const float *dstate_out,
+                                     void *dx, void *dg, float *dstate_in, const int32_t *cu_seqlens,
+                                     int32_t num_seqs, int64_t B, int64_t T, int32_t D, int32_t dtype, int32_t g_dtype,
+                                     int32_t decay, int32_t complement, void *stream) {
+    kda_status_t st = check_form(D, dtype, g_dtype, decay, complement);
+    if (st == KDA_OK) st = check_stream(cu_seqlens, num_seqs, B, T);
+    if (st != KDA_OK) return st;
+    const int64_t seqs = cu_seqlens != nullptr ? num_seqs : B, rows = B * T, blocks = (D + CKPT_BLOCK - 1) / CKPT_BLOCK;
+    if (seqs == 0) return KDA_OK;
+    const bool x8 = x_exponents != nullptr, g8 = g_exponents != nullptr;
+    const size_t es = size_t(elt_size(dtype)), gs = size_t(elt_size(g_dtype)), xin = x8 ? 1 : es, gin = g8 ? 1 : gs;
+    if (rows > 0 && (dy == nullptr || x == nullptr || g == nullptr || chunk_states == nullptr || dx == nullptr ||
+                     dg == nullptr || lddy < D || ldx < D || ldg < D))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && ((x8 && ldx != D) || (g8 && ldg != D))) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(dy, es) || !aligned_to(x, xin) || !aligned_to(g, gin) || !aligned_to(dx, es) || !aligned_to(dg, gs) ||
+        !aligned_to(chunk_states, 4) || !aligned_to(state_in, 4) || !aligned_to(dstate_out, 4) || !aligned_to(dstate_in, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const Span dys = rows_span(dy, rows, lddy, D, es), xs = rows_span(x, rows, ldx, D, xin);
+    const Span gsp = rows_span(g, rows, ldg, D, gin), dxs = rows_span(dx, rows, D, D, es), dgs = rows_span(dg, rows, D, D, gs);
+    const Span chunk = rows_span(chunk_states, (rows + RECUR_CHUNK - 1) / RECUR_CHUNK, D, D, 4);
+    const Span first = rows_span(state_in, seqs, D, D, 4), last = rows_span(dstate_out, seqs, D, D, 4);
+    const Span dfirst = rows_span(dstate_in, seqs, D, D, 4);
+    const Span in[] = {dys, xs, gsp, chunk, first, last, rows_span(x_exponents, rows, blocks, blocks, 1),
+                       rows_span(g_exponents, rows, blocks, blocks, 1), {cu_seqlens, size_t(seqs + 1) * 4}};
+    const Span out[] = {dxs, dgs, dfirst};
+    if (any_meet(out, in)) return KDA_ERR_INVALID_ARGUMENT;
+    if (rows == 0 && dstate_in == nullptr) return KDA_OK;
+    RecurParams p{};
+    p.x = x; p.g = g; p.xe = x_exponents; p.ge = g_exponents; p.ldx = ldx; p.ldg = ldg; p.cu = cu_seqlens;
+    p.nseq = int32_t(seqs); p.T = int32_t(T); p.rows = int32_t(rows); p.D = D; p.form = form_bits(decay, complement);
+    p.state_in = state_in; p.chunk = const_cast<float *>(chunk_states);
+    p.dy = dy; p.lddy = lddy; p.dfinal = dstate_out; p.dx = dx; p.dg = dg; p.dinitial = dstate_in;
+    RecurLaunch l{};
+    l.wide_g = g_dtype == KDA_F32; l.x8 = x8; l.g8 = g8;
+    const Span all[] = {dys, xs, gsp, dxs, dgs, chunk, first, last, dfirst};
+    const size_t sizes[] = {es, xin, gin, es, gs, 4, 4, 4, 4};
+    const int64_t pitch[] = {lddy, ldx, ldg, D, D, D, D, D, D};
+    l.vec = pairs_fit(all, sizes, pitch, 9, D) ? 2 : 1;
+    shape(p, l, B, T);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == KDA_F32    ? launch_scan_backward_f32(p, l, s)
+                          : dtype == KDA_BF16 ? launch_scan_backward_bf16(p, l, s)
+                                              : launch_scan_backward_f16(p, l, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, int64_t ldg, void *y, float *state,
+                            const int32_t *slots, int32_t num_slots, int32_t N, int32_t D, int32_t dtype,
+                            int32_t g_dtype, int32_t decay, int32_t complement, void *stream) {
+    const kda_status_t st = check_form(D, dtype, g_dtype, decay, complement);
+    if (st != KDA_OK) return st;
+    if (N < 0 || num_slots < 0 || (slots == nullptr && num_slots < N)) return KDA_ERR_INVALID_ARGUMENT;
+    if (int64_t(N) * ((D + 255) / 256) >= (int64_t(1) << 30)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    const size_t es = size_t(elt_size(dtype)), gs = size_t(elt_size(g_dtype));
+    if (x == nullptr || g == nullptr || y == nullptr || state == nullptr || ldx < D || ldg < D)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(x, es) || !aligned_to(g, gs) || !aligned_to(y, es) || !aligned_to(state, 4) || !aligned_to(slots, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const Span xs = rows_span(x, N, ldx, D, es), gsp = rows_span(g, N, ldg, D, gs), ys = rows_span(y, N, D, D, es);
+    const Span pool = rows_span(state, num_slots, D, D, 4);
+    const Span in[] = {xs, gsp, {slots, size_t(N) * 4}}, out[] = {ys, pool};
+    if (any_meet(out, in)) return KDA_ERR_INVALID_ARGUMENT;
+    const StepParams p{x, g, ldx, ldg, y, state, slots, num_slots, D, form_bits(decay, complement), 0};
+    const Span all[] = {xs, gsp, ys, pool};
+    const size_t sizes[] = {es, gs, es, 4};
+    const int64_t pitch[] = {ldx, ldg, D, D};
+    const int vec = pairs_fit(all, sizes, pitch, 4, D) ? 2 : 1;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == KDA_F32) e = launch_step<float, float>(p, N, vec, s);
+    else if (dtype == KDA_BF16)
+        e = g_dtype == KDA_F32 ? launch_step<__nv_bfloat16, float>(p, N, vec, s)
+                               : launch_step<__nv_bfloat16, __nv_bfloat16>(p, N, vec, s);
+    else e = g_dtype == KDA_F32 ? launch_step<__half, float>(p, N, vec, s) : launch_step<__half, __half>(p, N, vec, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// Checks and launch of both directions; x at pitch ldx is read (save) or written (load, ldx = dim).
+static kda_status_t run_checkpoint(bool save, void *x, int64_t ldx, int8_t *codes, uint8_t *exponents, int64_t rows,
+                                   int32_t dim, int32_t dtype, void *stream) {
+    if (!dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+    if (rows < 0 || dim < 1) return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t blocks = (dim + CKPT_BLOCK - 1) / CKPT_BLOCK;
+    if (dim > KDA_RECUR_MAX_DIM || rows >= (int64_t(1) << 36) / blocks) return KDA_ERR_UNSUPPORTED;
+    if (rows == 0) return KDA_OK;
+    const size_t es = size_t(elt_size(dtype));
+    if (x == nullptr || codes == nullptr || exponents == nullptr || ldx < dim || !aligned_to(x, es))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const Span xs = rows_span(x, rows, ldx, dim, es), cs{codes, size_t(rows) * size_t(dim)};
+    const Span ex{exponents, size_t(rows) * size_t(blocks)};
+    if (meet(xs, cs) || meet(xs, ex) || meet(cs, ex)) return KDA_ERR_INVALID_ARGUMENT;
+    const CkptParams p{x, save ? nullptr : x, ldx, rows * blocks, codes, exponents, dim, int32_t(blocks)};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == KDA_F32    ? launch_checkpoint<float>(p, s)
+                          : dtype == KDA_BF16 ? launch_checkpoint<__nv_bfloat16>(p, s)
+                                              : launch_checkpoint<__half>(p, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_checkpoint_save(const void *x, int64_t ldx, int8_t *codes, uint8_t *exponents, int64_t rows,
+                                 int32_t dim, int32_t dtype, void *stream) {
+    return run_checkpoint(true, const_cast<void *>(x), ldx, codes, exponents, rows, dim, dtype, stream);
+}
+
+kda_status_t kda_checkpoint_load(const int8_t *codes, const uint8_t *exponents, void *x, int64_t rows, int32_t dim,
+                                 int32_t dtype, void *stream) {
+    return run_checkpoint(false, x, dim, const_cast<int8_t *>(codes), const_cast<uint8_t *>(exponents), rows, dim, dtype,
+                          stream);
+}
+
+}  // extern "C"
