@@ -53,10 +53,10 @@ struct Piece {
 
 // act(z) and its slope.
 __device__ __forceinline__ void act_pair(int silu, float z, float &s, float &slope) {
-    float a, rest;
-    sigmoid_pair(z, a, rest);
-    s = silu ? z * a : a;
-    slope = silu ? a * fmaf(z, rest, 1.f) : a * rest;
+    float a[1] = {z}, rest[1];
+    sigmoid_pair<true, 1>(a, rest);
+    s = silu ? z * a[0] : a[0];
+    slope = silu ? a[0] * fmaf(z, rest[0], 1.f) : a[0] * rest[0];
 }
 
 // Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread.

@@ -47,9 +47,9 @@ __global__ void __launch_bounds__(STEP_THREADS) kda_gated_step_kernel(const Step
     if (entry >= 0) widen<float, VEC>(*reinterpret_cast<const raw_t<float, VEC> *>(s), h);
     widen<T, VEC>(xr, x);
     widen<G, VEC>(gr, a);
-    decays<VEC>(p.form, a, c);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[v], h[v], p.form & RECUR_COMPLEMENT ? c[v] * x[v] : x[v]);
+    decays<sizeof(G) == 4, VEC>(p.form, a, c);
+    if (p.form & RECUR_COMPLEMENT) mul_to<VEC>(x, x, c);
+    fma_to<VEC>(h, a, h, x);
     if (entry >= 0) store_raw<float, VEC>(s, narrow<float, VEC>(h));
     store_raw<T, VEC>(static_cast<T *>(p.y) + int64_t(n) * p.D + col, narrow<T, VEC>(h));
 }
@@ -156,18 +156,28 @@ int form_bits(int32_t decay, int32_t complement) {
     return (decay == KDA_DECAY_SIGMOID ? RECUR_SIGMOID : 0) | (complement ? RECUR_COMPLEMENT : 0);
 }
 
-// Two channels to a lane where all vectors of two are aligned.
-bool pairs_fit(const Span *tensors, const size_t *es, const int64_t *ld, int n, int32_t D) {
-    if (D % 2 != 0) return false;
-    for (int i = 0; i < n; ++i)
-        if (tensors[i].at != nullptr && (!aligned_to(tensors[i].at, 2 * es[i]) || ld[i] % 2 != 0)) return false;
+// A tensor of rows that the lanes read or write: its pitch and its elements' size.
+struct RowTensor {
+    const void *at;
+    int64_t ld;
+    size_t es;
+};
+// Whether all of them fit vectors of `bytes_of(es)` bytes.
+template <size_t N, typename F>
+bool vectors_fit(const RowTensor (&tensors)[N], int32_t D, F bytes_of) {
+    for (const RowTensor &t : tensors)
+        if (t.at != nullptr && (!aligned_to(t.at, bytes_of(t.es)) || size_t(t.ld) * t.es % bytes_of(t.es) != 0 ||
+                                size_t(D) * t.es % bytes_of(t.es) != 0))
+            return false;
     return true;
 }
 
-// The grid: 32 lanes' channels to a block, and as many parts of the stream as fill the GPU.
+// The grid: 32 lanes' channels to a cluster of blocks, and as many parts of the stream, then blocks to a
+// cluster, as fill the GPU.
 void shape(RecurParams &p, RecurLaunch &l, int64_t B, int64_t T) {
-    l.slabs = unsigned((p.D + 32 * l.vec - 1) / (32 * l.vec));
-    const int64_t want = (152 * 4 + l.slabs - 1) / l.slabs;
+    const int wide = l.staged ? 64 : 32;
+    l.slabs = unsigned((p.D + wide - 1) / wide);
+    const int64_t want = (152 * 3 + l.slabs - 1) / l.slabs;
     int64_t parts = p.nseq < want ? p.nseq : want;
     if (parts < 1) parts = 1;
     int64_t part;
@@ -182,6 +192,8 @@ void shape(RecurParams &p, RecurLaunch &l, int64_t B, int64_t T) {
     }
     l.parts = unsigned(parts);
     p.part = int32_t(part);
+    l.cluster = 1;
+    while (l.cluster < RECUR_CLUSTER && int64_t(l.cluster) * parts < want && part > int64_t(l.cluster) * RECUR_CHUNK) l.cluster *= 2;
 }
 
 }  // namespace
@@ -219,11 +231,13 @@ kda_status_t kda_gated_scan(const void *x, int64_t ldx, const void *g, int64_t l
     p.chunk = chunk_states;
     RecurLaunch l{};
     l.wide_g = g_dtype == KDA_F32;
-    const Span all[] = {xs, gsp, ys, in_state, out_state, chunk};
-    const size_t sizes[] = {es, gs, es, 4, 4, 4};
-    const int64_t pitch[] = {ldx, ldg, D, D, D, D};
-    l.vec = pairs_fit(all, sizes, pitch, 6, D) ? 2 : 1;
+    const RowTensor rowed[] = {{x, ldx, es}, {g, ldg, gs}, {y, D, es}, {state_in, D, 4}, {state_out, D, 4}, {chunk_states, D, 4}};
+    const RowTensor inputs[] = {rowed[0], rowed[1]};
+    l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
     shape(p, l, B, T);
+    DeviceInfo info;
+    if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
+    p.err = info.err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == KDA_F32    ? launch_scan_f32(p, l, s)
                           : dtype == KDA_BF16 ? launch_scan_bf16(p, l, s)
@@ -268,11 +282,14 @@ kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const void *x
     p.dy = dy; p.lddy = lddy; p.dfinal = dstate_out; p.dx = dx; p.dg = dg; p.dinitial = dstate_in;
     RecurLaunch l{};
     l.wide_g = g_dtype == KDA_F32; l.x8 = x8; l.g8 = g8;
-    const Span all[] = {dys, xs, gsp, dxs, dgs, chunk, first, last, dfirst};
-    const size_t sizes[] = {es, xin, gin, es, gs, 4, 4, 4, 4};
-    const int64_t pitch[] = {lddy, ldx, ldg, D, D, D, D, D, D};
-    l.vec = pairs_fit(all, sizes, pitch, 9, D) ? 2 : 1;
+    const RowTensor rowed[] = {{dy, lddy, es}, {x, ldx, xin}, {g, ldg, gin}, {dx, D, es}, {dg, D, gs}, {chunk_states, D, 4},
+                               {state_in, D, 4}, {dstate_out, D, 4}, {dstate_in, D, 4}};
+    const RowTensor inputs[] = {rowed[0], rowed[1], rowed[2]};
+    l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
     shape(p, l, B, T);
+    DeviceInfo info;
+    if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
+    p.err = info.err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == KDA_F32    ? launch_scan_backward_f32(p, l, s)
                           : dtype == KDA_BF16 ? launch_scan_backward_bf16(p, l, s)
@@ -298,10 +315,8 @@ kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, int64_t l
     const Span in[] = {xs, gsp, {slots, size_t(N) * 4}}, out[] = {ys, pool};
     if (any_meet(out, in)) return KDA_ERR_INVALID_ARGUMENT;
     const StepParams p{x, g, ldx, ldg, y, state, slots, num_slots, D, form_bits(decay, complement), 0};
-    const Span all[] = {xs, gsp, ys, pool};
-    const size_t sizes[] = {es, gs, es, 4};
-    const int64_t pitch[] = {ldx, ldg, D, D};
-    const int vec = pairs_fit(all, sizes, pitch, 4, D) ? 2 : 1;
+    const RowTensor rowed[] = {{x, ldx, es}, {g, ldg, gs}, {y, D, es}, {state, D, 4}};
+    const int vec = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) ? 2 : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == KDA_F32) e = launch_step<float, float>(p, N, vec, s);

@@ -5,11 +5,11 @@
 
 namespace kda {
 
-// vec: channels to a lane, 1 or 2; wide_g: g and dg in FP32; x8, g8: codes in place of x and g; slabs x parts blocks
 struct RecurLaunch {
-    int vec;
-    bool wide_g, x8, g8;
-    unsigned slabs, parts;
+    bool staged;                // the inputs' rows are whole, aligned 16-byte pieces: two channels to a lane, else one
+    bool wide_g, x8, g8;        // g and dg in FP32; codes in place of x and g
+    unsigned cluster, slabs, parts;
+    int device;
 };
 
 cudaError_t launch_scan_f32(const RecurParams &p, const RecurLaunch &l, cudaStream_t s);

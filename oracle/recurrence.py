@@ -7,13 +7,25 @@ one of its sum (2^-24 each): below 2^-21 a step, relative to the chain of absolu
 With E the recurrence of |x| and N the sum of E along the chain (N_t = a N_{t-1} + E_t), h_t is
 therefore within 2^-21 N_t; the gradients likewise.  Below 2^-126 the two units of a decay, or of
 1 - a, are 2^-148 whatever its size, and products that fall there are rounded to a multiple of 2^-149:
-TINY e stands for that beside the relative part, e being what the decay multiplies."""
+TINY e stands for that beside the relative part, e being what the decay multiplies.
+
+16-bit arguments of the sigmoid take a faster exponential (coarse, the largest |g|): the product |g| log2(e) is
+rounded (|g| 2^-24 of z = exp(-g)), the power of two is within 2^-22, and a = 1 / (1 + z) and z a are
+off by no more than z is and 2^-22: |g| 2^-24 + 2^-21 a step in all.  1 - a is then 0 below 2^-126, and a at
+least 2^-126."""
 from __future__ import annotations
 
 import numpy as np
 
 U = 2.0 ** -21
 TINY = 2.0 ** -147 / U
+
+
+def _scale(coarse):
+    """The bounds' factor and the least size of a decay, in units of U, for arguments up to `coarse`."""
+    return (1.0, TINY) if not coarse else (1 + coarse * 2.0 ** -24 / U, 2.0 ** -125 / U)
+
+
 CHUNK, BLOCK = 64, 32
 
 
@@ -25,9 +37,10 @@ def decays(g, gate):
         return 1 / (1 + np.exp(-g)), 1 / (1 + np.exp(g))
 
 
-def scan(x, g, spans, starts, gate, complement):
+def scan(x, g, spans, starts, gate, complement, coarse=0):
     """x, g [rows, D]; spans: (first, end) rows of the sequences; starts [N, D].  Returns (y, final, chunk states, bounds of
     the three); rows of no sequence are NaN, as are the chunk states of such rows."""
+    u, tiny = U * _scale(coarse)[0], _scale(coarse)[1]
     a, rest = decays(g, gate)
     b = rest * x if complement else x
     rows, D = x.shape
@@ -38,17 +51,18 @@ def scan(x, g, spans, starts, gate, complement):
         h, e, bound = np.array(starts[n], np.float64), np.abs(starts[n]).astype(np.float64), np.zeros(D)
         for t in range(first, end):
             if t % CHUNK == 0:
-                chunks[t // CHUNK], cb[t // CHUNK] = h, U * bound
+                chunks[t // CHUNK], cb[t // CHUNK] = h, u * bound
             h = a[t] * h + b[t]
-            bound = a[t] * (bound + e) + np.abs(b[t]) + TINY * (e + np.abs(x[t]) + 1)
+            bound = a[t] * (bound + e) + np.abs(b[t]) + tiny * (e + np.abs(x[t]) + 1)
             e = a[t] * e + np.abs(b[t])
-            y[t], yb[t] = h, U * bound
-        final[n], fb[n] = h, U * bound
+            y[t], yb[t] = h, u * bound
+        final[n], fb[n] = h, u * bound
     return y, final, chunks, yb, fb, cb
 
 
-def scan_backward(dy, x, g, chunks, spans, starts, dfinal, gate, complement):
+def scan_backward(dy, x, g, chunks, spans, starts, dfinal, gate, complement, coarse=0):
     """Returns (dx, dg, dstarts) and their bounds; h before a row comes from chunks (every 64 rows) and starts."""
+    u, tiny = U * _scale(coarse)[0], _scale(coarse)[1]
     a, rest = decays(g, gate)
     b, c = (rest * x, rest) if complement else (x, np.ones_like(x))
     out = [np.full(dy.shape, np.nan) for _ in range(4)]
@@ -62,7 +76,7 @@ def scan_backward(dy, x, g, chunks, spans, starts, dfinal, gate, complement):
                 e, bound = np.abs(h), np.zeros_like(h)
             before[t], size[t], off[t] = h, e, bound
             h = a[t] * h + b[t]
-            bound = a[t] * (bound + e) + np.abs(b[t]) + TINY * (e + np.abs(x[t]) + 1)
+            bound = a[t] * (bound + e) + np.abs(b[t]) + tiny * (e + np.abs(x[t]) + 1)
             e = a[t] * e + np.abs(b[t])
         d, e, bound = np.array(dfinal[n], np.float64), np.abs(dfinal[n]).astype(np.float64), np.zeros_like(h if end > first else ds[n])
         for t in range(end - 1, first - 1, -1):
@@ -70,11 +84,11 @@ def scan_backward(dy, x, g, chunks, spans, starts, dfinal, gate, complement):
             bound = bound + e
             m, ms, mo = before[t] - x[t] if complement else before[t], size[t] + (np.abs(x[t]) if complement else 0), off[t]
             k = a[t] * rest[t] if gate == "sigmoid" else a[t]
-            dx[t], dxb[t] = c[t] * d, U * (c[t] * (bound + 2 * e) + TINY * (e + 1))
+            dx[t], dxb[t] = c[t] * d, u * (c[t] * (bound + 2 * e) + tiny * (e + 1))
             # the product's factors are off by their own bounds, and it rounds five times
-            dg[t], dgb[t] = d * m * k, U * (k * (bound * ms + e * mo + 4 * e * ms) + TINY * (e + 1) * (ms + 1))
-            d, e, bound = a[t] * d, a[t] * e, a[t] * bound + a[t] * e + TINY * (e + 1)
-        ds[n], dsb[n] = d, U * bound
+            dg[t], dgb[t] = d * m * k, u * (k * (bound * ms + e * mo + 4 * e * ms) + tiny * (e + 1) * (ms + 1))
+            d, e, bound = a[t] * d, a[t] * e, a[t] * bound + a[t] * e + tiny * (e + 1)
+        ds[n], dsb[n] = d, u * bound
     return dx, dg, ds, dxb, dgb, dsb
 
 

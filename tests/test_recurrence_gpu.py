@@ -84,11 +84,18 @@ class Case:
         self.dfinal = torch.from_numpy(rng.standard_normal((len(lens), D))).to(F32)
         self.start = f64(self.state) if initial else np.zeros((len(lens), D))
 
+    def coarse(self, saved=False):
+        """The largest argument where the sigmoid's faster form is taken (the oracle says what it costs)."""
+        if self.form["gate"] != "sigmoid" or (self.gdtype == F32 and not saved):
+            return 0
+        g = np.abs(f64(self.g))
+        return float(np.max(g[np.isfinite(g)], initial=0))
+
     def flat(self, t):
         return f64(t).reshape(-1, self.D)
 
     def want(self):
-        return ref.scan(self.flat(self.x), self.flat(self.g), self.spans, self.start, **self.form)
+        return ref.scan(self.flat(self.x), self.flat(self.g), self.spans, self.start, **self.form, coarse=self.coarse())
 
     def gpu(self, t):
         return t.to(DEV) if t is not None else None
@@ -119,7 +126,7 @@ class Case:
         out = kda.gated_scan_backward(self.gpu(self.dy), x, g, self.gpu(chunks), self.gpu(self.cu),
                                       initial_state=self.gpu(self.state), dfinal_state=self.gpu(dfinal), dg=dg, **self.form)
         *want, bx, bg, bs = ref.scan_backward(self.flat(self.dy), wx, wg, f64(chunks), self.spans, self.start,
-                                              f64(self.dfinal) * with_final, **self.form)
+                                              f64(self.dfinal) * with_final, **self.form, coarse=self.coarse(save_g))
         assert out[0].dtype == self.dtype and out[1].dtype == (self.gdtype if not save_g or dg is not None else self.dtype)
         near(out[0], want[0], bx, f"{label} dx")
         near(out[1], want[1], bg, f"{label} dg")
@@ -241,6 +248,12 @@ def test_decays_at_the_ends_of_their_range(kda):
             with np.errstate(invalid="ignore"):
                 c.check(kda, f"{gate} {complement}")
                 c.check_backward(kda, label=f"{gate} {complement}")
+            if gate == "sigmoid":                           # the faster form of 16-bit arguments; rows of whole 16-byte pieces or not
+                for D in (64, 63):
+                    c = Case([90, 33], D, F16, F16, gate, complement, seed=8)
+                    c.g[0] = torch.tensor([values[i % len(values)] for i in range(123 * D)]).reshape(123, D)
+                    c.check(kda, f"{gate} {complement}")
+                    c.check_backward(kda, label=f"{gate} {complement}")
 
 
 def test_slots_and_states_in_place(kda):
