@@ -42,26 +42,33 @@ struct Piece {
         if constexpr (sizeof(S) == 1) e = exps[row * ((dim + CKPT_BLOCK - 1) / CKPT_BLOCK) + col / CKPT_BLOCK];
     }
     __device__ __forceinline__ void value(float (&v)[VEC]) const {
-        widen<S, VEC>(raw, v);
-        if constexpr (sizeof(S) == 1) {
-            const float s = ckpt_scale(e);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] *= s;
-        }
+        if constexpr (sizeof(S) == 1) code_values<VEC>(raw, ckpt_scale(e), v);
+        else widen<S, VEC>(raw, v);
     }
 };
 
-// act(z) and its slope.
-__device__ __forceinline__ void act_pair(int silu, float z, float &s, float &slope) {
-    float a[1] = {z}, rest[1];
-    sigmoid_pair<true, 1>(a, rest);
-    s = silu ? z * a[0] : a[0];
-    slope = silu ? a[0] * fmaf(z, rest[0], 1.f) : a[0] * rest[0];
+// act(z) and its slope; the sigmoid's faster form for 16-bit gates and codes, as in the recurrence.
+template <bool FULL, int VEC>
+__device__ __forceinline__ void act_pair(int silu, const float (&z)[VEC], float (&s)[VEC], float (&slope)[VEC]) {
+    float rest[VEC], one[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) s[v] = z[v], one[v] = 1.f;
+    sigmoid_pair<FULL, VEC>(s, rest);
+    if (silu) {
+        fma_to<VEC>(slope, z, rest, one);
+        mul_to<VEC>(slope, slope, s);
+        mul_to<VEC>(s, s, z);
+    } else {
+        mul_to<VEC>(slope, s, rest);
+    }
 }
 
-// Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread.
+// Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread, two rows on their way to a thread
+// while a third is worked on.
 template <typename T, typename X, typename Z, int VEC, int NV>
 __global__ void __launch_bounds__(NORM_GRAD_THREADS) kda_norm_grad_narrow_kernel(const NormGradParams p, const int lanes) {
+    constexpr int AHEAD = NV == 1 ? 2 : 1;
+    constexpr bool FULL = sizeof(Z) == 4;
     __shared__ float part[NORM_GRAD_THREADS * VEC];
     const int t = int(threadIdx.x) & (lanes - 1), groups = NORM_GRAD_THREADS / lanes, group = int(threadIdx.x) / lanes;
     const int nvec = p.dim / VEC;
@@ -75,64 +82,77 @@ __global__ void __launch_bounds__(NORM_GRAD_THREADS) kda_norm_grad_narrow_kernel
         for (int v = 0; v < VEC; ++v) w[i][v] = dw[i][v] = 0.f;
         if (j < nvec) widen<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(p.weight) + j * VEC), w[i]);
     }
-    // the same number of turns for all threads of a warp, whose shuffles go over all of them
-    const int64_t step = int64_t(gridDim.x) * groups;
-    for (int64_t base = int64_t(blockIdx.x) * groups; base < p.rows; base += step) {
-        const int64_t row = base + group;
-        const bool live = row < p.rows;
-        Piece<X, VEC> xs[NV];
-        Piece<Z, VEC> zs[NV];
-        Piece<T, VEC> ds[NV];
+    struct Row {
+        Piece<X, VEC> x[NV];
+        Piece<Z, VEC> z[NV];
+        Piece<T, VEC> d[NV];
+    } next[AHEAD];
+    auto fetch = [&](Row &r, int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = i * lanes + t;
-            if (!live || j >= nvec) continue;
-            xs[i].fetch(p.x, p.xe, row, p.dim, j * VEC);
-            zs[i].fetch(p.gate, p.ze, row, p.dim, j * VEC);
-            ds[i].fetch(p.dy, nullptr, row, p.dim, j * VEC);
+            if (row >= p.rows || j >= nvec) continue;
+            r.x[i].fetch(p.x, p.xe, row, p.dim, j * VEC);
+            r.z[i].fetch(p.gate, p.ze, row, p.dim, j * VEC);
+            r.d[i].fetch(p.dy, nullptr, row, p.dim, j * VEC);
         }
-        float x[NV][VEC], u[NV][VEC], ss = 0.f, ux = 0.f;   // u: dy w s
-        float q[NV][VEC], k[NV][VEC];                        // dy s, dy w slope
+    };
+    // the same number of turns for all threads of a block: shuffles go over whole warps
+    const int64_t step = int64_t(gridDim.x) * groups, first = int64_t(blockIdx.x) * groups;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool have = live && i * lanes + t < nvec;
-            float z[VEC], d[VEC];
-            if (have) {
-                xs[i].value(x[i]);
-                zs[i].value(z);
-                ds[i].value(d);
+    for (int k = 0; k < AHEAD; ++k) fetch(next[k], first + k * step + group);
+    for (int64_t base = first; base < p.rows; base += AHEAD * step) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int64_t row = base + k * step + group;
+            const bool live = row < p.rows;
+            float x[NV][VEC], u[NV][VEC], q[NV][VEC], g[NV][VEC], ss = 0.f, ux = 0.f;   // dy w s, dy s, dy w slope
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool have = live && i * lanes + t < nvec;
+                float z[VEC], d[VEC], s[VEC], sum[VEC];
+                if (have) {
+                    next[k].x[i].value(x[i]);
+                    next[k].z[i].value(z);
+                    next[k].d[i].value(d);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) x[i][v] = z[v] = d[v] = 0.f;
+                }
+                act_pair<FULL, VEC>(p.silu, z, s, g[i]);
+                mul_to<VEC>(q[i], d, s);
+                mul_to<VEC>(u[i], q[i], w[i]);
+                mul_to<VEC>(d, d, w[i]);
+                mul_to<VEC>(g[i], d, g[i]);
+                mul_to<VEC>(sum, x[i], x[i]);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) ss += sum[v];
+                mul_to<VEC>(sum, u[i], x[i]);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) ux += sum[v];
             }
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if (!have) x[i][v] = z[v] = d[v] = 0.f;
-                float s, slope;
-                act_pair(p.silu, z[v], s, slope);
-                q[i][v] = d[v] * s;
-                k[i][v] = d[v] * w[i][v] * slope;
-                u[i][v] = q[i][v] * w[i][v];
-                ss = fmaf(x[i][v], x[i][v], ss);
-                ux = fmaf(u[i][v], x[i][v], ux);
+            fetch(next[k], row + AHEAD * step);
+            for (int o = lanes >> 1; o > 0; o >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                ux += __shfl_xor_sync(0xffffffffu, ux, o);
             }
-        }
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            ux += __shfl_xor_sync(0xffffffffu, ux, o);
-        }
-        const float r = rsqrtf(ss * p.inv_dim + p.eps), m = ux * p.inv_dim * r * r;   // mean(u n) n = m x
+            const float r = rsqrtf(ss * p.inv_dim + p.eps), m = ux * p.inv_dim * r * r;   // mean(u n) n = m x
+            float rr[VEC], mm[VEC];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = i * lanes + t;
-            if (!live || j >= nvec) continue;
-            float ox[VEC], oz[VEC];
+            for (int v = 0; v < VEC; ++v) rr[v] = r, mm[v] = -m;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float n = x[i][v] * r;
-                ox[v] = r * fmaf(-m, x[i][v], u[i][v]);
-                oz[v] = k[i][v] * n;
-                dw[i][v] = fmaf(q[i][v], n, dw[i][v]);
+            for (int i = 0; i < NV; ++i) {
+                const int j = i * lanes + t;
+                if (!live || j >= nvec) continue;
+                float n[VEC];
+                mul_to<VEC>(n, x[i], rr);
+                fma_to<VEC>(dw[i], q[i], n, dw[i]);
+                mul_to<VEC>(g[i], g[i], n);
+                fma_to<VEC>(u[i], mm, x[i], u[i]);
+                mul_to<VEC>(u[i], u[i], rr);
+                store_raw<T, VEC>(static_cast<T *>(p.dx) + row * p.dim + j * VEC, narrow<T, VEC>(u[i]));
+                store_raw<T, VEC>(static_cast<T *>(p.dgate) + row * p.dim + j * VEC, narrow<T, VEC>(g[i]));
             }
-            store_raw<T, VEC>(static_cast<T *>(p.dx) + row * p.dim + j * VEC, narrow<T, VEC>(ox));
-            store_raw<T, VEC>(static_cast<T *>(p.dgate) + row * p.dim + j * VEC, narrow<T, VEC>(oz));
         }
     }
     // the groups' sums, one set of vectors after another
@@ -179,12 +199,12 @@ __global__ void __launch_bounds__(1024) kda_norm_grad_wide_kernel(const NormGrad
             zs.value(z);
             ds.value(d);
             widen<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(p.weight) + j * VEC), w);
+            float s[VEC], slope[VEC];
+            act_pair<sizeof(Z) == 4, VEC>(p.silu, z, s, slope);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                float s, slope;
-                act_pair(p.silu, z[v], s, slope);
                 ss = fmaf(x[v], x[v], ss);
-                ux = fmaf(d[v] * s * w[v], x[v], ux);
+                ux = fmaf(d[v] * s[v] * w[v], x[v], ux);
             }
         }
 #pragma unroll
@@ -214,13 +234,13 @@ __global__ void __launch_bounds__(1024) kda_norm_grad_wide_kernel(const NormGrad
             zs.value(z);
             ds.value(d);
             widen<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(p.weight) + j * VEC), w);
+            float s[VEC], slope[VEC];
+            act_pair<sizeof(Z) == 4, VEC>(p.silu, z, s, slope);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                float s, slope;
-                act_pair(p.silu, z[v], s, slope);
-                const float n = x[v] * r, q = d[v] * s;
+                const float n = x[v] * r, q = d[v] * s[v];
                 ox[v] = r * fmaf(-m, x[v], q * w[v]);
-                oz[v] = d[v] * w[v] * slope * n;
+                oz[v] = d[v] * w[v] * slope[v] * n;
                 dw[j * VEC + v] = fmaf(q, n, dw[j * VEC + v]);
             }
             store_raw<T, VEC>(static_cast<T *>(p.dx) + row * p.dim + j * VEC, narrow<T, VEC>(ox));

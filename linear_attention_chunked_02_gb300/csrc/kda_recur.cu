@@ -71,7 +71,7 @@ struct CkptParams {
     uint8_t *exponents;
     int32_t dim, blocks;        // blocks of a row
 };
-constexpr int CKPT_THREADS = 256;
+constexpr int CKPT_THREADS = 256, CKPT_WAVE = 1 << 20;
 
 // The exponent byte of a block whose largest magnitude has these bits: 127 2^e = 1.984375 2^(e + 6).
 __device__ __forceinline__ unsigned ckpt_exponent(unsigned top) {
@@ -90,9 +90,87 @@ __device__ __forceinline__ int8_t ckpt_code(float x, unsigned e, float inverse) 
     return int8_t(e == TOP ? max(-63, min(63, k)) : k);
 }
 
-// One warp to a block, one element to a lane.
+// Rows of whole blocks, in vectors of 16 bytes of the type (and as many codes): 4 or 8 threads to a block of 32, several vectors to
+// a thread at once.  Bound by HBM: 8192 x 8192 BF16, saved and read back, 407 MB.
+template <typename T>
+struct CkptVec {
+    static constexpr int N = 16 / int(sizeof(T)), LANES = CKPT_BLOCK / N, BATCH = 4;
+};
+
 template <typename T>
 __global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_save_kernel(const CkptParams p) {
+    using V = CkptVec<T>;
+    const int64_t vectors = p.units * V::LANES, step = int64_t(gridDim.x) * CKPT_THREADS;
+    const unsigned per_row = unsigned(p.blocks) * V::LANES;
+    pdl_launch_dependents();
+    pdl_wait();
+    // whole warps leave the loop together: vectors is a multiple of the lanes to a block, not of a warp
+    for (int64_t base = int64_t(blockIdx.x) * CKPT_THREADS; base < vectors; base += V::BATCH * step) {
+        raw_t<T, V::N> raw[V::BATCH];
+#pragma unroll
+        for (int i = 0; i < V::BATCH; ++i) {
+            const int64_t v = base + i * step + threadIdx.x;
+            if (v >= vectors) continue;
+            const int64_t at = p.ldx == p.dim ? v * V::N : v / per_row * p.ldx + v % per_row * V::N;
+            raw[i] = load_once<T, V::N>(static_cast<const T *>(p.x) + at);
+        }
+#pragma unroll
+        for (int i = 0; i < V::BATCH; ++i) {
+            const int64_t v = base + i * step + threadIdx.x;
+            if (base + i * step >= vectors) break;
+            float x[V::N];
+            unsigned top = 0;
+            if (v < vectors) {
+                widen<T, V::N>(raw[i], x);
+#pragma unroll
+                for (int k = 0; k < V::N; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+            }
+#pragma unroll
+            for (int o = V::LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (v >= vectors) continue;
+            const unsigned e = ckpt_exponent(top);
+            const float inverse = __uint_as_float(e == CKPT_BAD ? 0u : (254u - e) << 23);
+            int8_t k[V::N];
+#pragma unroll
+            for (int n = 0; n < V::N; ++n) k[n] = ckpt_code<T>(x[n], e, inverse);
+            raw_t<int8_t, V::N> out;
+            memcpy(&out, k, sizeof(out));
+            store_raw<int8_t, V::N>(p.codes + v * V::N, out);
+            if (threadIdx.x % V::LANES == 0) p.exponents[v / V::LANES] = uint8_t(e);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_load_kernel(const CkptParams p) {
+    using V = CkptVec<T>;
+    const int64_t vectors = p.units * V::LANES, step = int64_t(gridDim.x) * CKPT_THREADS;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t base = int64_t(blockIdx.x) * CKPT_THREADS + threadIdx.x; base < vectors; base += V::BATCH * step) {
+        raw_t<int8_t, V::N> raw[V::BATCH];
+        unsigned e[V::BATCH];
+#pragma unroll
+        for (int i = 0; i < V::BATCH; ++i) {
+            const int64_t v = base + i * step;
+            if (v >= vectors) continue;
+            raw[i] = load_once<int8_t, V::N>(p.codes + v * V::N);
+            e[i] = p.exponents[v / V::LANES];
+        }
+#pragma unroll
+        for (int i = 0; i < V::BATCH; ++i) {
+            const int64_t v = base + i * step;
+            if (v >= vectors) break;
+            float x[V::N];
+            code_values<V::N>(raw[i], ckpt_scale(e[i]), x);
+            store_raw<T, V::N>(static_cast<T *>(p.out) + v * V::N, narrow<T, V::N>(x));
+        }
+    }
+}
+
+// Any width and alignment: one warp to a block, one element to a lane.
+template <typename T>
+__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_save_any_kernel(const CkptParams p) {
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
@@ -109,7 +187,7 @@ __global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_save_kernel(const
 }
 
 template <typename T>
-__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_load_kernel(const CkptParams p) {
+__global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_load_any_kernel(const CkptParams p) {
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
@@ -125,10 +203,19 @@ __global__ void __launch_bounds__(CKPT_THREADS) kda_checkpoint_load_kernel(const
 
 template <typename T>
 cudaError_t launch_checkpoint(const CkptParams &p, cudaStream_t s) {
-    const int64_t need = (p.units + CKPT_THREADS / 32 - 1) / (CKPT_THREADS / 32), most = 152 * 8;
+    using V = CkptVec<T>;
+    const bool save = p.out == nullptr;
+    const void *x = save ? p.x : p.out;
+    const bool wide = p.dim % CKPT_BLOCK == 0 && p.ldx % V::N == 0 && aligned16(x) &&
+                      reinterpret_cast<uintptr_t>(p.codes) % V::N == 0;
+    const int64_t per = wide ? int64_t(CKPT_THREADS) * V::BATCH / V::LANES : CKPT_THREADS / 32;    // units to a block of threads
+    const int64_t need = (p.units + per - 1) / per, most = 152 * (wide ? CKPT_WAVE : 8);
     const unsigned grid = unsigned(need < most ? need : most);
-    return p.out == nullptr ? launch_pdl(true, kda_checkpoint_save_kernel<T>, grid, CKPT_THREADS, 0, s, p)
-                            : launch_pdl(true, kda_checkpoint_load_kernel<T>, grid, CKPT_THREADS, 0, s, p);
+    if (wide)
+        return save ? launch_pdl(true, kda_checkpoint_save_kernel<T>, grid, CKPT_THREADS, 0, s, p)
+                    : launch_pdl(true, kda_checkpoint_load_kernel<T>, grid, CKPT_THREADS, 0, s, p);
+    return save ? launch_pdl(true, kda_checkpoint_save_any_kernel<T>, grid, CKPT_THREADS, 0, s, p)
+                : launch_pdl(true, kda_checkpoint_load_any_kernel<T>, grid, CKPT_THREADS, 0, s, p);
 }
 
 // ------------------------------------------------------------------- checks
@@ -172,18 +259,30 @@ bool vectors_fit(const RowTensor (&tensors)[N], int32_t D, F bytes_of) {
     return true;
 }
 
-// The grid: 32 lanes' channels to a cluster of blocks, and as many parts of the stream, then blocks to a
-// cluster, as fill the GPU.
-void shape(RecurParams &p, RecurLaunch &l, int64_t B, int64_t T) {
-    const int wide = l.staged ? 64 : 32;
-    l.slabs = unsigned((p.D + wide - 1) / wide);
-    const int64_t want = (152 * 3 + l.slabs - 1) / l.slabs;
-    int64_t parts = p.nseq < want ? p.nseq : want;
-    if (parts < 1) parts = 1;
+// Packed sequences whose lengths every warp looks through, 32 at a time.
+constexpr int MOST_LOOKED_AT = 2048;
+
+// The grid: `vec` channels to each of 32 lanes, and the stream in as many parts, then blocks to a cluster, as `room` blocks
+// at once allow.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
+// blocks of a cluster share the rows.  Where the device sees that none is longer than three blocks' parts, they take parts
+// of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 153 us and
+// 212).  A tile of a block is `tile` rows.
+void shape(RecurParams &p, RecurLaunch &l, int vec, int tile, int64_t room, int64_t T) {
+    l.slabs = unsigned((p.D + 32 * vec - 1) / (32 * vec));
+    const int64_t want = room / l.slabs > 1 ? room / l.slabs : 1;
+    const int64_t rows = p.cu == nullptr ? T : p.rows;      // that a cluster may share
+    int64_t parts = 1;
+    l.cluster = 1;
+    if (p.cu == nullptr) parts = p.nseq < want ? p.nseq : want;
+    while (l.cluster < RECUR_CLUSTER && 2 * l.cluster * parts <= want && rows > int64_t(l.cluster) * tile) l.cluster *= 2;
+    if (p.cu != nullptr) {
+        parts = want / l.cluster < p.nseq ? want / l.cluster : p.nseq;
+        if (parts < 1) parts = 1;
+    }
     int64_t part;
     if (p.cu == nullptr) {
-        const int64_t each = (B + parts - 1) / parts;
-        parts = (B + each - 1) / each;
+        const int64_t each = (p.nseq + parts - 1) / parts;
+        parts = (p.nseq + each - 1) / each;
         part = each * T;
     } else {
         part = (T + parts - 1) / parts;
@@ -192,8 +291,38 @@ void shape(RecurParams &p, RecurLaunch &l, int64_t B, int64_t T) {
     }
     l.parts = unsigned(parts);
     p.part = int32_t(part);
-    l.cluster = 1;
-    while (l.cluster < RECUR_CLUSTER && int64_t(l.cluster) * parts < want && part > int64_t(l.cluster) * RECUR_CHUNK) l.cluster *= 2;
+    if (p.cu != nullptr && l.cluster > 1 && p.nseq > 1 && p.nseq <= MOST_LOOKED_AT) {
+        const int64_t alone = int64_t(l.parts) * l.cluster;
+        p.solo_part = int32_t((T + alone - 1) / alone);
+        p.solo_most = int32_t(3 * int64_t(p.solo_part) < INT32_MAX ? 3 * p.solo_part : INT32_MAX);
+    }
+}
+
+// Whether and how single warps walk the sequences: where there are enough of them for all SMs.  16 x 512 rows of 8192
+// channels in BF16 take 63 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
+// channels 70.  Packed sequences are walked where none is longer than three parts of the stream, which the device sees.
+void shape_walk(RecurParams &p, RecurLaunch &l, int wide, int64_t T) {
+    constexpr int64_t WARPS = 152 * 6;
+    if (p.rows == 0 || (p.cu != nullptr && p.nseq > MOST_LOOKED_AT)) return;
+    for (int vec = wide; vec >= wide / 2; vec -= wide / 2) {
+        const int64_t slabs = (p.D + 32 * vec - 1) / (32 * vec);
+        if (slabs * p.nseq < WARPS) continue;
+        int64_t parts = 2 * WARPS / slabs > 1 ? 2 * WARPS / slabs : 1;
+        if (parts > p.nseq) parts = p.nseq;
+        if (p.cu == nullptr) {
+            const int64_t each = (p.nseq + parts - 1) / parts;
+            parts = (p.nseq + each - 1) / each;
+            p.walk_part = int32_t(each * T);
+            l.cluster = 1, l.parts = 1, l.slabs = 152 * 2;  // all of its warps walk
+        } else {
+            p.walk_part = int32_t((T + parts - 1) / parts);
+            parts = (T + p.walk_part - 1) / p.walk_part;
+            p.walk_most = p.walk_part < INT32_MAX / 3 ? 3 * p.walk_part : INT32_MAX;
+        }
+        p.walk_parts = int32_t(parts);
+        p.walk_wide = vec == wide;
+        return;
+    }
 }
 
 }  // namespace
@@ -234,7 +363,8 @@ kda_status_t kda_gated_scan(const void *x, int64_t ldx, const void *g, int64_t l
     const RowTensor rowed[] = {{x, ldx, es}, {g, ldg, gs}, {y, D, es}, {state_in, D, 4}, {state_out, D, 4}, {chunk_states, D, 4}};
     const RowTensor inputs[] = {rowed[0], rowed[1]};
     l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
-    shape(p, l, B, T);
+    shape(p, l, l.staged ? 2 : 1, dtype == KDA_F32 ? 56 : 112, 152 * (dtype == KDA_F32 ? 3 : 2), T);
+    if (l.staged) shape_walk(p, l, 8 / int(es), T);
     DeviceInfo info;
     if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;
@@ -286,7 +416,8 @@ kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const void *x
                                {state_in, D, 4}, {dstate_out, D, 4}, {dstate_in, D, 4}};
     const RowTensor inputs[] = {rowed[0], rowed[1], rowed[2]};
     l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
-    shape(p, l, B, T);
+    const bool wide = dtype == KDA_F32 || (g_dtype == KDA_F32 && !g8);
+    shape(p, l, l.staged && !wide ? 2 : 1, RECUR_CHUNK, 152 * (l.staged && !wide ? 2 : 3), T);
     DeviceInfo info;
     if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;

@@ -24,6 +24,8 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 
+#include <type_traits>
+
 #include "kda_kernels.cuh"
 #include "kda_vec.cuh"
 
@@ -41,7 +43,13 @@ struct RecurParams {
     int32_t T;                  // dense: rows to a sequence; packed: all rows
     int32_t rows, D;
     int32_t form;
-    int32_t part;               // rows of the stream whose sequences a block takes (dense: a multiple of T)
+    int32_t part;               // rows of the stream whose sequences a cluster takes (dense: a multiple of T)
+    int32_t solo_part;          // packed: where no sequence is longer than solo_most, every block takes a part of this many
+    int32_t solo_most;          // rows by itself, cluster or not (0: never)
+    int32_t walk_parts;         // forward, sequences walked by single warps: their parts of the stream, or 0 for never,
+    int32_t walk_part;          // the parts' rows,
+    int32_t walk_most;          // the longest sequence for which that is done,
+    int32_t walk_wide;          // and whether a warp takes 8 bytes of x to a lane or 4
     // forward
     void *y;                    // [rows, D]
     const float *state_in;      // [entries, D] or nullptr; backward: [sequences, D]
@@ -71,9 +79,9 @@ __device__ __forceinline__ int count_until(const int32_t *cu, int n, int row, in
     return lo;
 }
 
-// The rows [begin, end) of this block's sequences: those that start in its part of the stream.
-__device__ __forceinline__ void part_rows(const RecurParams &p, int part, int parts, int lane, int &begin, int &end) {
-    const int64_t from = int64_t(part) * p.part, to = from + p.part;
+// The rows [begin, end) of a part's sequences: those that start in its `length` rows of the stream.
+__device__ __forceinline__ void part_rows(const RecurParams &p, int part, int parts, int length, int lane, int &begin, int &end) {
+    const int64_t from = int64_t(part) * length, to = from + length;
     if (p.cu == nullptr) {
         begin = int(from < p.rows ? from : p.rows);
         end = int(to < p.rows ? to : p.rows);
@@ -88,10 +96,31 @@ __device__ __forceinline__ void part_rows(const RecurParams &p, int part, int pa
     end = min(max(end, begin), p.rows);
 }
 
-// Boundaries of sequences near a warp's rows.  Between `low` and `high`, both exclusive, there is none.
+// Boundaries of sequences near a warp's rows: between `low` and `high`, both exclusive, there is none.
 struct Near {
     int low = INT_MAX, high = INT_MIN;
-    int first = 0, bound = INT_MAX;   // packed: boundary number `lane` from the last search is entry first + lane of cu
+};
+
+// The longest of the packed sequences, by the whole warp.
+__device__ __forceinline__ int longest_of(const RecurParams &p, int lane) {
+    int longest = 0;
+    for (int n = lane; n < p.nseq; n += 32) longest = max(longest, p.cu[n + 1] - p.cu[n]);
+    return __reduce_max_sync(0xffffffffu, longest);
+}
+
+// A block's place: the part of the stream whose rows it shares with the other blocks of a cluster, or takes alone.
+struct Place {
+    int part, parts, length, rank, size;
+
+    __device__ __forceinline__ Place(const RecurParams &p, int cluster_rank, int cluster_size, int longest)
+        : part(blockIdx.z), parts(gridDim.z), length(p.part), rank(cluster_rank), size(cluster_size) {
+        if (longest <= p.solo_most && p.solo_part > 0) {
+            part = part * size + rank;
+            parts *= size;
+            length = p.solo_part;
+            rank = 0, size = 1;
+        }
+    }
 };
 
 // What a warp knows of its R rows: which are its part's, which begin a sequence, which end one.
@@ -117,13 +146,12 @@ __device__ __forceinline__ Rows look_at(const RecurParams &p, Near &near, int ro
             near.low = int(before) - (before == unsigned(row0) ? 1 : 0);
             near.high = int(before == unsigned(row0) ? before : before + t);
         } else {
-            near.first = count_until(p.cu, p.nseq + 1, row0 - 1, lane);
-            int at = near.first + lane;
-            near.bound = at <= p.nseq ? p.cu[at] : INT_MAX;
-            near.low = near.first > 0 ? p.cu[near.first - 1] : -1;
-            near.high = __shfl_sync(0xffffffffu, near.bound, 0);
+            const int first = count_until(p.cu, p.nseq + 1, row0 - 1, lane);
+            int at = first + lane, v = at <= p.nseq ? p.cu[at] : INT_MAX;
+            near.low = first > 0 ? p.cu[first - 1] : -1;
+            near.high = __shfl_sync(0xffffffffu, v, 0);
             unsigned bits = 0;
-            for (int v = near.bound;;) {
+            for (;;) {
                 const int d = v - row0;
                 if (d >= 0 && d <= R) bits |= 1u << d;
                 if (__shfl_sync(0xffffffffu, v, 31) > row0 + R) break;
@@ -138,13 +166,6 @@ __device__ __forceinline__ Rows look_at(const RecurParams &p, Near &near, int ro
     if (end - 1 - row0 < R) r.lasts |= 1u << (end - 1 - row0);
     r.lasts &= r.live;
     return r;
-}
-
-// The sequence that `row` belongs to, for a live row that begins or ends one, after look_at; all lanes call it.
-__device__ __forceinline__ int sequence_of(const RecurParams &p, const Near &near, int row, int lane) {
-    if (p.cu == nullptr) return row / p.T;
-    const int k = __popc(__ballot_sync(0xffffffffu, near.bound <= row));
-    return (k < 32 ? near.first + k : count_until(p.cu, p.nseq + 1, row, lane)) - 1;
 }
 
 // State entry of sequence n, or -1 for none.
@@ -168,13 +189,22 @@ __device__ __forceinline__ void store_state(const float (&h)[VEC], float *base, 
     store_raw<float, VEC>(base + entry * D + col, narrow<float, VEC>(h));
 }
 
+// The state entry of the sequence that `row` belongs to; all lanes call it.  Out of line: it is for rows that begin or
+// end a sequence, and would fill the instruction cache in every unrolled row.
+inline __device__ __noinline__ int entry_of_row(const RecurParams &p, int row, int lane) {
+    return recur_entry(p, p.cu == nullptr ? row / p.T : count_until(p.cu, p.nseq + 1, row, lane) - 1);
+}
+
 // ---------------------------------------------------------------- arithmetic
 // VEC channels at once; two of them by the paired instructions, which halves what is issued.
 template <int VEC>
 __device__ __forceinline__ void mul_to(float (&r)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
-    if constexpr (VEC == 2) {
-        const float2 t = __fmul2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
-        r[0] = t.x, r[1] = t.y;
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 2) {
+            const float2 t = __fmul2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]));
+            r[v] = t.x, r[v + 1] = t.y;
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) r[v] = a[v] * b[v];
@@ -182,9 +212,12 @@ __device__ __forceinline__ void mul_to(float (&r)[VEC], const float (&a)[VEC], c
 }
 template <int VEC>
 __device__ __forceinline__ void add_to(float (&r)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
-    if constexpr (VEC == 2) {
-        const float2 t = __fadd2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
-        r[0] = t.x, r[1] = t.y;
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 2) {
+            const float2 t = __fadd2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]));
+            r[v] = t.x, r[v + 1] = t.y;
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) r[v] = a[v] + b[v];
@@ -192,9 +225,13 @@ __device__ __forceinline__ void add_to(float (&r)[VEC], const float (&a)[VEC], c
 }
 template <int VEC>
 __device__ __forceinline__ void fma_to(float (&r)[VEC], const float (&a)[VEC], const float (&b)[VEC], const float (&c)[VEC]) {
-    if constexpr (VEC == 2) {
-        const float2 t = __ffma2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]), make_float2(c[0], c[1]));
-        r[0] = t.x, r[1] = t.y;
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 2) {
+            const float2 t =
+                __ffma2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]), make_float2(c[v], c[v + 1]));
+            r[v] = t.x, r[v + 1] = t.y;
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) r[v] = fmaf(a[v], b[v], c[v]);
@@ -206,6 +243,24 @@ __device__ __forceinline__ void fma_to(float (&r)[VEC], const float (&a)[VEC], f
 #pragma unroll
     for (int v = 0; v < VEC; ++v) bb[v] = b, cc[v] = c;
     fma_to<VEC>(r, a, bb, cc);
+}
+
+// The values of VEC codes and their scale.  A code + 128 in the low byte of 2^23 is 2^23 + 128 + code: an addition makes it
+// a float, where conversions would take the slow pipe.
+template <int VEC>
+__device__ __forceinline__ void code_values(raw_t<int8_t, VEC> raw, float scale, float (&v)[VEC]) {
+    unsigned w[(VEC + 3) / 4] = {};
+    memcpy(w, &raw, sizeof(raw));
+    float off[VEC], s[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const unsigned u = w[i / 4] ^ 0x80808080u;
+        v[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650u | unsigned(i % 4)));
+        off[i] = -8388736.f;
+        s[i] = scale;
+    }
+    add_to<VEC>(v, v, off);
+    mul_to<VEC>(v, v, s);
 }
 
 // a and 1 - a from the sigmoid's arguments g, both without cancellation: with z = exp(-g), a = 1 / (1 + z) and 1 - a = z a.
@@ -282,78 +337,91 @@ __device__ __forceinline__ void copy_empty(const RecurParams &p, const float *fr
 }
 
 // ------------------------------------------------------------------- inputs
-// One row operand of a warp: R rows of the block's columns, of type S (int8_t: codes, with their exponents).
-//
-// Staged: every warp has a ring of its own in shared memory, filled by asynchronous copies of 16 bytes
-// whose place in the rows is not the lane that uses them, so a warp's barrier lies between.  It takes two channels to a
-// lane and rows of whole, aligned 16-byte pieces.  Direct: each lane loads its own elements into registers
-// one tile ahead; for any width and alignment.
-template <typename S, int VEC, int R, int STAGES>
+// One row operand of a warp: R rows of the block's columns, of type S (int8_t: codes, with their exponents), in a
+// ring in shared memory of the warp's own.  It is filled by asynchronous copies of PIECE bytes (16, or 4 for rows of
+// FP32 that 16 do not fit), or with PIECE 0 through registers, element by element, for any width and alignment (one
+// channel to a lane).
+template <typename S, int VEC, int R, int RING, int PIECE>
 struct Source {
-    static constexpr bool STAGED = STAGES > 0;
     static constexpr int ROW = 32 * VEC * int(sizeof(S)), BYTES = R * ROW;   // of a warp's rows
-    static constexpr int RING = BYTES * STAGES;
-    raw_t<S, VEC> raw[STAGED ? 1 : R];
-    unsigned scales = 0;        // codes: the exponent of row lane / VEC, block lane % VEC of the warp's columns
-    unsigned char *ring = nullptr;
+    static constexpr bool CODES = sizeof(S) == 1;
+    static constexpr int BYTES_RING = RING * (BYTES + (CODES ? 128 : 0));
+    static constexpr int PIECES = PIECE == 0 ? 32 : ROW / PIECE;             // of a row
+    static constexpr int ROWS = PIECES < 32 ? 32 / PIECES : 1;               // of one copy of the warp
+    static_assert(!CODES || R * VEC <= 32, "one scale to a lane");
+    unsigned char *ring;
+    const S *base;
+    int64_t ld;                 // pitch
+    int own_row, own_col;       // of the lane's pieces
+    raw_t<S, VEC> raw[PIECE == 0 ? R : 1];
+    unsigned exponent = 0;      // codes: of row lane / VEC, block lane % VEC of the warp's columns
 
-    // rows row0 .. row0 + R of [rows, D] at pitch ld, into place `stage`; rows without their bit in `live` read as zeros
-    __device__ __forceinline__ void fetch(const void *base, int64_t ld, int row0, unsigned live, int D, int slab, int lane,
-                                          int stage) {
-        const S *s = static_cast<const S *>(base);
-        if constexpr (STAGED) {
-            constexpr int PIECES = ROW / 16, ROWS = 32 / PIECES;             // rows of one copy of the warp
-            const int j0 = lane / PIECES, col = slab + lane % PIECES * (16 / int(sizeof(S)));
-            const S *from = s + int64_t(row0 + j0) * ld + col;
-            const uint32_t to = smem_u32(ring) + stage * BYTES + lane * 16;
-            const unsigned have = col < D ? live >> j0 : 0u;
-#pragma unroll
-            for (int i = 0; i < R / ROWS; ++i) {
-                const bool ok = have >> (i * ROWS) & 1u;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512),
-                             "l"(ok ? from + i * ROWS * ld : s), "r"(ok ? 16 : 0) : "memory");
-            }
-        } else {
-            const int col = slab + lane * VEC;
+    __device__ __forceinline__ void open(unsigned char *at, const void *from, int64_t pitch, int slab, int lane) {
+        ring = at;
+        base = static_cast<const S *>(from);
+        ld = pitch;
+        own_row = PIECE == 0 ? 0 : lane / PIECES;
+        own_col = slab + (PIECE == 0 ? lane * VEC : lane % PIECES * (PIECE / int(sizeof(S))));
+    }
+    // A tile's rows row0 .. row0 + R take two steps: load() when the tile before it is put(), and put() into its place of
+    // the ring.  Rows without their bit in `live` read as zeros.
+    __device__ __forceinline__ void load(const uint8_t *exps, int row0, unsigned live, int D, int slab, int lane) {
+        if constexpr (PIECE == 0) {
+            const S *s = base + int64_t(row0) * ld + own_col;
 #pragma unroll
             for (int j = 0; j < R; ++j)
-                raw[j] = col < D && (live >> j & 1u) ? load_once<S, VEC>(s + int64_t(row0 + j) * ld + col) : raw_t<S, VEC>{};
+                raw[j] = own_col < D && (live >> j & 1u) ? load_once<S, VEC>(s + j * ld) : raw_t<S, VEC>{};
         }
-    }
-    __device__ __forceinline__ unsigned fetch_scales(const uint8_t *exps, int row0, unsigned live, int D, int slab, int lane) {
-        if constexpr (sizeof(S) == 1) {
+        if constexpr (CODES) {
             // 32 VEC columns are VEC blocks of 32; the block's first column is a multiple of 32
             const int j = lane / VEC, block = slab / CKPT_BLOCK + lane % VEC, blocks = (D + CKPT_BLOCK - 1) / CKPT_BLOCK;
-            return j < R && block < blocks && (live >> j & 1u) ? exps[int64_t(row0 + j) * blocks + block] : 0u;
+            exponent = j < R && block < blocks && (live >> j & 1u) ? exps[int64_t(row0 + j) * blocks + block] : 0u;
         }
-        return 0u;
     }
-    __device__ __forceinline__ void set_scales(unsigned exponents) {
-        if constexpr (sizeof(S) == 1) scales = __float_as_uint(ckpt_scale(exponents));
-    }
-    __device__ __forceinline__ void value(int j, float (&v)[VEC], int lane, int stage) const {
-        if constexpr (STAGED)
-            widen<S, VEC>(*reinterpret_cast<const raw_t<S, VEC> *>(ring + stage * BYTES + j * ROW + lane * VEC * int(sizeof(S))), v);
+    __device__ __forceinline__ static void copy(uint32_t to, const S *from, int bytes) {
+        if constexpr (PIECE == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
         else
-            widen<S, VEC>(raw[j], v);
-        if constexpr (sizeof(S) == 1) {
-            const float s = __uint_as_float(__shfl_sync(0xffffffffu, scales, j * VEC + lane * VEC / CKPT_BLOCK));
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+    __device__ __forceinline__ void put(int row0, unsigned live, int D, int lane, int place) {
+        if constexpr (PIECE == 0) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] *= s;
+            for (int j = 0; j < R; ++j)
+                *reinterpret_cast<raw_t<S, VEC> *>(ring + place * BYTES + j * ROW + lane * VEC * int(sizeof(S))) = raw[j];
+        } else {
+            const S *from = base + int64_t(row0 + own_row) * ld + own_col;
+            const uint32_t to = smem_u32(ring) + place * BYTES + lane * PIECE;
+            if (R < ROWS && own_row >= R) {
+            } else if (live == (1u << R) - 1u && own_col < D) {
+#pragma unroll
+                for (int i = 0; i < (R + ROWS - 1) / ROWS; ++i, from += ROWS * ld) copy(to + i * ROWS * ROW, from, PIECE);
+            } else {
+#pragma unroll
+                for (int i = 0; i < (R + ROWS - 1) / ROWS; ++i, from += ROWS * ld) {
+                    const bool ok = own_col < D && (live >> (own_row + i * ROWS) & 1u);
+                    copy(to + i * ROWS * ROW, ok ? from : base, ok ? PIECE : 0);
+                }
+            }
         }
+        if constexpr (CODES) scales(place)[lane] = ckpt_scale(exponent);
+    }
+    __device__ __forceinline__ float *scales(int place) const {
+        return reinterpret_cast<float *>(ring + RING * BYTES) + place * 32;
+    }
+    __device__ __forceinline__ void value(int j, float (&v)[VEC], int lane, int place) const {
+        const raw_t<S, VEC> r =
+            *reinterpret_cast<const raw_t<S, VEC> *>(ring + place * BYTES + j * ROW + lane * VEC * int(sizeof(S)));
+        if constexpr (CODES) code_values<VEC>(r, scales(place)[j * VEC + lane * VEC / CKPT_BLOCK], v);
+        else widen<S, VEC>(r, v);
     }
 };
-template <int STAGES>
-__device__ __forceinline__ void tile_sent() {
-    if constexpr (STAGES > 0) asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// the oldest tile in the ring is there, for all lanes
-template <int STAGES>
+__device__ __forceinline__ void tile_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all tiles but the AHEAD ones sent last are there, for all lanes
+template <int AHEAD>
 __device__ __forceinline__ void tile_ready() {
-    if constexpr (STAGES > 0) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        __syncwarp();
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ clusters
@@ -370,15 +438,25 @@ __device__ __forceinline__ int cluster_size() {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Two floats to the same place in block `rank` of the cluster, counted there on its mbarrier `bar`.
-__device__ __forceinline__ void send_pair(const float2 *at, uint64_t *bar, int rank, float2 v) {
-    asm volatile(
-        "{\n\t.reg .b32 a, b;\n\t"
-        "mapa.shared::cluster.u32 a, %0, %2;\n\t"
-        "mapa.shared::cluster.u32 b, %1, %2;\n\t"
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [a], {%3, %4}, [b];\n\t}" ::"r"(smem_u32(at)),
-        "r"(smem_u32(bar)), "r"(rank), "f"(v.x), "f"(v.y)
-        : "memory");
+// N floats (2 or 4) to the same place in block `rank` of the cluster, counted there on its mbarrier `bar`.
+template <int N>
+__device__ __forceinline__ void send_floats(const float *at, uint64_t *bar, int rank, const float (&v)[N]) {
+    if constexpr (N == 4)
+        asm volatile(
+            "{\n\t.reg .b32 a, b;\n\t"
+            "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(smem_u32(at)),
+            "r"(smem_u32(bar)), "r"(rank), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .b32 a, b;\n\t"
+            "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [a], {%3, %4}, [b];\n\t}" ::"r"(smem_u32(at)),
+            "r"(smem_u32(bar)), "r"(rank), "f"(v[0]), "f"(v[1])
+            : "memory");
 }
 // Wait for phase `parity` of `bar`, whose bytes come from other blocks of the cluster; false after a second.
 __device__ __forceinline__ bool cluster_mbar_wait(uint64_t *bar, uint32_t parity) {
@@ -398,78 +476,98 @@ __device__ __forceinline__ bool cluster_mbar_wait(uint64_t *bar, uint32_t parity
     }
 }
 
-constexpr int RECUR_CLUSTER = 8;              // most blocks of a cluster
+constexpr int RECUR_CLUSTER = 16;             // most blocks of a cluster
 
-// The map of a run of rows for one channel: (A, H) for h -> A h + H, or with SET's bits in place of A for
-// h -> H, whatever came before.  Arithmetic never gives these bits: its NaNs are all 0x7fffffff.
+// The map of a run of rows for K neighbouring channels: a and h' of each, for h -> a h + h', or with SET's bits in place of a
+// for h -> h', whatever came before.  Arithmetic never gives these bits: its NaNs are all 0x7fffffff.
 constexpr unsigned MAP_SET = 0x7fc0a5e7u;
-__device__ __forceinline__ bool map_set(float2 m) { return __float_as_uint(m.x) == MAP_SET; }
-__device__ __forceinline__ float map_apply(float2 m, float h) { return map_set(m) ? m.y : fmaf(m.x, h, m.y); }
-
-// What the blocks exchange for one direction of the recurrence.
-template <int VEC, int W, bool BACK>
-struct Exchange {
-    static constexpr int C = 32 * VEC;
-    float2 maps[W][C];                        // of the block's warps
-    float in[W][C];                           // what each warp's rows start from
-    // the rest for clusters alone: the blocks' maps, two tiles' worth in turn
-    float2 blocks[2][RECUR_CLUSTER][C];
-    uint64_t bar[2];
-
-    static __host__ __device__ constexpr int bytes(bool cluster) {
-        return cluster ? int(sizeof(Exchange)) : W * C * int(sizeof(float2) + sizeof(float));
-    }
-    static __device__ __forceinline__ int of(int i) { return BACK ? W - 1 - i : i; }
-
-    __device__ __forceinline__ void put(int warp, int lane, const float (&a)[VEC], const float (&h)[VEC], bool set) {
+template <int VEC>
+struct Map {
+    float m[2 * VEC];                         // a, h' of each channel
+    __device__ __forceinline__ void read(const float *at) { widen<float, 2 * VEC>(*reinterpret_cast<const raw_t<float, 2 * VEC> *>(at), m); }
+    __device__ __forceinline__ void write(float *at) const { store_raw<float, 2 * VEC>(at, narrow<float, 2 * VEC>(m)); }
+    __device__ __forceinline__ bool set() const { return __float_as_uint(m[0]) == MAP_SET; }
+    __device__ __forceinline__ void apply(float (&h)[VEC]) const {
+        const bool s = set();
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) maps[warp][lane * VEC + v] = make_float2(set ? __uint_as_float(MAP_SET) : a[v], h[v]);
+        for (int v = 0; v < VEC; ++v) h[v] = s ? m[2 * v + 1] : fmaf(m[2 * v], h[v], m[2 * v + 1]);
+    }
+};
+
+// The maps that the W warps of a block hand to the warp that chains them, between two barriers of the block, and what
+// their rows start from, which comes back in the maps' place.
+template <int VEC, int W, bool BACK>
+struct Chain {
+    static constexpr int ROW = 64 * VEC, BYTES = W * ROW * int(sizeof(float));
+    float *maps;                              // [W][32 lanes]
+
+    static __device__ __forceinline__ int of(int i) { return BACK ? W - 1 - i : i; }
+    __device__ __forceinline__ float *at(int warp, int lane) const { return maps + warp * ROW + lane * 2 * VEC; }
+
+    __device__ __forceinline__ void put(int warp, int lane, const float (&a)[VEC], const float (&h)[VEC], bool set) const {
+        Map<VEC> m;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) m.m[2 * v] = set ? __uint_as_float(MAP_SET) : a[v], m.m[2 * v + 1] = h[v];
+        m.write(at(warp, lane));
     }
     __device__ __forceinline__ void get(int warp, int lane, float (&h)[VEC]) const {
-        widen<float, VEC>(*reinterpret_cast<const raw_t<float, VEC> *>(&in[warp][lane * VEC]), h);
-    }
-    // Channel c, by one thread of the block, between two barriers of the block: what every warp's rows
-    // start from, given the carry before the cluster's tiles; the carry becomes the one after them.
-    // `turn` counts the cluster's tiles.
-    __device__ __forceinline__ void chain(int c, float &carry, int rank, int size, int turn, bool &dead, unsigned *err) {
-        float h = carry;
-        if (size > 1) {
-            float A = 1.f, H = 0.f;
-            bool set = false;
+        Map<VEC> m;
+        m.read(at(warp, lane));
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float2 m = maps[of(i)][c];
-                H = map_apply(m, H);
-                A *= m.x;
-                set = set || map_set(m);
-            }
-            const int buf = turn & 1;
-            const float2 mine = make_float2(set ? __uint_as_float(MAP_SET) : A, H);
-            for (int to = 0; to < size; ++to) send_pair(&blocks[buf][rank][c], &bar[buf], to, mine);
-            if (c == 0) mbar_arrive_expect_tx(&bar[buf], uint32_t(size * C * int(sizeof(float2))));
-            // The next use of this place and of its phase is two tiles on: nobody sends there before it has
-            // this block's maps of the next tile, which go out behind the barrier that ends this tile.
-            if (!dead && !cluster_mbar_wait(&bar[buf], uint32_t(turn >> 1) & 1u)) {
-                dead = true;
-                atomicOr(err, ERR_WAIT_TIMEOUT);
-            }
-            float next = carry;
-            for (int i = 0; i < size; ++i) {
-                if (i == rank) h = next;
-                next = map_apply(blocks[buf][i][c], next);
-            }
-            carry = next;
-        }
-        float t = h;
+        for (int v = 0; v < VEC; ++v) h[v] = m.m[2 * v];
+    }
+    // K channels from number c on, by one thread: the map of all warps' rows in order; and what each warp's start
+    // from, given h, which becomes what follows them.  Four maps are read at a time.
+    template <int K>
+    __device__ __forceinline__ Map<K> all(int c) const {
+        float A[K], H[K];
+        bool set = false;
+#pragma unroll
+        for (int v = 0; v < K; ++v) A[v] = 1.f, H[v] = 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            in[of(i)][c] = t;
-            t = map_apply(maps[of(i)][c], t);
+            Map<K> m;
+            m.read(maps + of(i) * ROW + 2 * c);
+            m.apply(H);
+#pragma unroll
+            for (int v = 0; v < K; ++v) A[v] *= m.m[2 * v];
+            set = set || m.set();
         }
-        if (size == 1) carry = t;
+        Map<K> r;
+#pragma unroll
+        for (int v = 0; v < K; ++v) r.m[2 * v] = set ? __uint_as_float(MAP_SET) : A[v], r.m[2 * v + 1] = H[v];
+        return r;
     }
+    template <int K>
+    __device__ __forceinline__ void give(int c, float (&h)[K]) const {
+#pragma unroll
+        for (int base = 0; base < W; base += 4) {
+            Map<K> m[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (base + i < W) m[i].read(maps + of(base + i) * ROW + 2 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (base + i >= W) continue;
+#pragma unroll
+                for (int v = 0; v < K; ++v) maps[of(base + i) * ROW + 2 * (c + v)] = h[v];
+                m[i].apply(h);
+            }
+        }
+    }
+};
+
+// The same between the blocks of a cluster: every block's map of its tile to all of them, two tiles' worth in turn.
+template <int VEC>
+struct Blocks {
+    static constexpr int ROW = 64 * VEC;
+    float *maps;                              // [2][size][32 lanes]
+    uint64_t *bar;                            // [2]
+    bool dead = false;
+
+    static int bytes(int size) { return size > 1 ? 2 * size * ROW * int(sizeof(float)) + 16 : 0; }
     // all threads, before the first tile and behind the last one
-    __device__ __forceinline__ void open(int size) {
+    __device__ __forceinline__ void open(int size) const {
         if (size == 1) return;
         if (threadIdx.x == 0) {
             mbar_init(&bar[0], 1);
@@ -478,240 +576,405 @@ struct Exchange {
         }
         cluster_barrier();
     }
-    __device__ __forceinline__ void close(int size) {
+    __device__ __forceinline__ void close(int size) const {
         if (size > 1) cluster_barrier();       // no block leaves while another may still write to it
+    }
+    // K channels from number c on, by one thread; tile number `turn`
+    template <int K>
+    __device__ __forceinline__ void send(int c, int rank, int size, int turn, const Map<K> &mine) const {
+        const int buf = turn & 1;
+        for (int to = 0; to < size; ++to) send_floats<2 * K>(maps + (buf * size + rank) * ROW + 2 * c, &bar[buf], to, mine.m);
+        if (c == 0) mbar_arrive_expect_tx(&bar[buf], uint32_t(size * ROW * int(sizeof(float))));
+    }
+    // What this block's tile starts from; the carry is that of the cluster's tiles, and then of its next ones.  The place
+    // and its phase are used again two tiles on: nobody sends there before it has this block's map of the
+    // next tile, which goes out behind the barrier that ends this one.
+    template <int K>
+    __device__ __forceinline__ void receive(int c, int rank, int size, int turn, float (&carry)[K], float (&h)[K],
+                                            unsigned *err) {
+        const int buf = turn & 1;
+        if (!dead && !cluster_mbar_wait(&bar[buf], uint32_t(turn >> 1) & 1u)) {
+            dead = true;
+            atomicOr(err, ERR_WAIT_TIMEOUT);
+        }
+        for (int base = 0; base < size; base += 4) {                         // four loads at a time
+            Map<K> m[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (base + i < size) m[i].read(maps + (buf * size + base + i) * ROW + 2 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (base + i == rank) {
+#pragma unroll
+                    for (int v = 0; v < K; ++v) h[v] = carry[v];
+                }
+                if (base + i < size) m[i].apply(carry);
+            }
+        }
     }
 };
 
 // ------------------------------------------------------------------ forward
-// Bytes of shared memory: the warps' rings, then the exchange.
-template <typename T, typename G, int VEC, int R, int W, int STAGES>
-struct ScanShared {
-    static constexpr int RINGS = W * (Source<T, VEC, R, STAGES>::RING + Source<G, VEC, R, STAGES>::RING);
-    static int bytes(int cluster) { return RINGS + Exchange<VEC, W, false>::bytes(cluster > 1); }
+// Many sequences of like lengths: one warp walks the rows of a part alone, nothing is chained, and every row is looked at
+// once.  The warps of all blocks share the parts and columns.
+template <typename T, typename G, int VEC>
+struct WalkShape {
+    static constexpr int R = 8, TILE_BYTES = 32 * VEC * R * int(sizeof(T) + sizeof(G)), RING = TILE_BYTES > 4096 ? 2 : 3;
+    using X = Source<T, VEC, R, RING, 16>;
+    using S = Source<G, VEC, R, RING, 16>;
+    static constexpr int WARP = X::BYTES_RING + S::BYTES_RING;
 };
 
-// FORM: RECUR_ bits, or -1 for those of the parameters.
-template <typename T, typename G, int FORM, int VEC, int R, int W, int STAGES, int MIN>
-__global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_kernel(const RecurParams p) {
-    constexpr int TILE = R * W, AHEAD = STAGES > 0 ? STAGES - 1 : 1;
+template <typename T, typename G, int VEC, int R, int W, int RINGS, int PIECE>
+struct ScanShape {
+    static constexpr int RING = RINGS;        // tiles in a warp's ring
+    using X = Source<T, VEC, R, RING, PIECE>;
+    using S = Source<G, VEC, R, RING, PIECE>;
+    using Warps = Chain<VEC, W, false>;
+    using Cluster = Blocks<VEC>;
+    static constexpr int WARP = X::BYTES_RING + S::BYTES_RING, THREADS = (W + 1) * 32;
+    // of a walking warp of the block, with 8 bytes of x to a lane; 4 take less
+    static constexpr int WIDE = 8 / int(sizeof(T)), WALK = PIECE == 16 ? (W + 1) * WalkShape<T, G, WIDE>::WARP : 0;
+    static int bytes(int cluster) {
+        const int chained = W * WARP + Warps::BYTES + Cluster::bytes(cluster);
+        return chained > WALK ? chained : WALK;
+    }
+};
+
+template <typename T, typename G, int VEC>
+__device__ __forceinline__ void walk(const RecurParams &p, const int form, int part, int slab, unsigned char *ring, int lane) {
+    using Shape = WalkShape<T, G, VEC>;
+    constexpr int R = Shape::R, RING = Shape::RING;
+    constexpr bool FULL = sizeof(G) == 4;
+    const int col = slab + lane * VEC;
+    const bool in = col < p.D;
+    int begin, end;
+    part_rows(p, part, p.walk_parts, p.walk_part, lane, begin, end);
+    const int tile0 = begin / R, tiles = end > begin ? (end - 1) / R + 1 - tile0 : 0;
+    typename Shape::X xs;
+    typename Shape::S gs;
+    xs.open(ring, p.x, p.ldx, slab, lane);
+    gs.open(ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
+    auto put = [&](int tile, int place) {
+        if (tile < tiles) {
+            const int row0 = (tile0 + tile) * R;
+            const unsigned live = live_bits<R>(row0, begin, end);
+            xs.put(row0, live, p.D, lane, place);
+            gs.put(row0, live, p.D, lane, place);
+        }
+        tile_sent();
+    };
+    for (int i = 0; i < RING; ++i) put(i, i);
+    Near near;
+    float h[VEC] = {};
+    int place = 0;
+    T *y = static_cast<T *>(p.y) + int64_t(tile0) * R * p.D + col;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int row0 = (tile0 + tile) * R;
+        const Rows rows = look_at<R>(p, near, row0, begin, end, lane);
+        tile_ready<RING - 1>();
+        auto row = [&](int j) {
+            float a[VEC], b[VEC], c[VEC];
+            xs.value(j, b, lane, place);
+            gs.value(j, a, lane, place);
+            decays<FULL, VEC>(form, a, c);
+            if (form & RECUR_COMPLEMENT) mul_to<VEC>(b, b, c);
+            fma_to<VEC>(h, a, h, b);
+        };
+        if (row0 % RECUR_CHUNK == 0 && (rows.live & 1u) && !(rows.starts & 1u))
+            store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
+        if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                row(j);
+                if (in) store_raw<T, VEC>(y, narrow<T, VEC>(h));
+                y += p.D;
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < R; ++j, y += p.D) {
+                if (!(rows.live >> j & 1u)) continue;
+                if (rows.starts >> j & 1u) {
+                    load_state<VEC>(h, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                    if (j == 0 && row0 % RECUR_CHUNK == 0) store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
+                }
+                row(j);
+                if (in) store_raw<T, VEC>(y, narrow<T, VEC>(h));
+                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+            }
+        }
+        __syncwarp();
+        put(tile + RING, place);
+        place = place + 1 == RING ? 0 : place + 1;
+    }
+    copy_empty<VEC>(p, p.state_in, p.state_out, part, p.walk_parts, lane, col);
+    __syncwarp();                                           // the ring may go to the next part
+}
+
+template <typename T, typename G, int VEC>
+__device__ __forceinline__ void walk_all(const RecurParams &p, int form, unsigned char *shared, int warp, int warps, int lane) {
+    const int slabs = (p.D + 32 * VEC - 1) / (32 * VEC), units = slabs * p.walk_parts;
+    const int blocks = int(gridDim.x * gridDim.y * gridDim.z);
+    const int block = int(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
+    for (int u = warp * blocks + block; u < units; u += warps * blocks)
+        walk<T, G, VEC>(p, form, u / slabs, u % slabs * 32 * VEC, shared + warp * WalkShape<T, G, VEC>::WARP, lane);
+}
+
+// FORM: RECUR_ bits, or -1 for those of the parameters.  W warps take the rows, one more chains their maps: it would
+// not find the registers in theirs.
+template <typename T, typename G, int FORM, int VEC, int R, int W, int RING, int PIECE, int MIN>
+__global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const __grid_constant__ RecurParams p) {
+    constexpr int TILE = R * W;
     constexpr bool FULL = sizeof(G) == 4;
     static_assert(RECUR_CHUNK % R == 0 && R <= 16, "chunk states lie at warps' first rows");
-    using Ex = Exchange<VEC, W, false>;
+    using Shape = ScanShape<T, G, VEC, R, W, RING, PIECE>;
     extern __shared__ __align__(16) unsigned char shared[];
-    Ex &ex = *reinterpret_cast<Ex *>(shared + ScanShared<T, G, VEC, R, W, STAGES>::RINGS);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = cluster_rank(), size = cluster_size();
-    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC, part = blockIdx.z, parts = gridDim.z;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = cluster_size();
+    const typename Shape::Warps chain{reinterpret_cast<float *>(shared + W * Shape::WARP)};
+    typename Shape::Cluster cluster;
+    cluster.maps = reinterpret_cast<float *>(shared + W * Shape::WARP + Shape::Warps::BYTES);
+    cluster.bar = reinterpret_cast<uint64_t *>(cluster.maps + 2 * all * cluster.ROW);
+    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC;
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D;
     pdl_wait();
+    const int longest = p.cu != nullptr && (p.walk_parts > 0 || p.solo_part > 0) ? longest_of(p, lane) : 0;
+    if constexpr (PIECE == 16) {
+        if (p.walk_parts > 0 && longest <= p.walk_most) {   // the same for all blocks
+            if (p.walk_wide) walk_all<T, G, Shape::WIDE>(p, form, shared, warp, W + 1, lane);
+            else walk_all<T, G, Shape::WIDE / 2>(p, form, shared, warp, W + 1, lane);
+            pdl_launch_dependents();
+            return;
+        }
+    }
+    const Place at(p, cluster_rank(), all, longest);
+    const int rank = at.rank, size = at.size;
     int begin, end;
-    part_rows(p, part, parts, lane, begin, end);
+    part_rows(p, at.part, at.parts, at.length, lane, begin, end);
     const int tile0 = begin / TILE, tiles = end > begin ? (end - 1) / TILE + 1 - tile0 : 0;
     const int turns = (tiles + size - 1) / size;
-    Source<T, VEC, R, STAGES> xs;
-    Source<G, VEC, R, STAGES> gs;
-    xs.ring = shared + warp * (xs.RING + gs.RING);
-    gs.ring = xs.ring + xs.RING;
+    if (warp == W) {
+        float h[VEC] = {}, carry[VEC] = {};                 // what the block's and the cluster's tiles start from
+        const int c = lane * VEC;
+        cluster.open(size);
+        for (int turn = 0; turn < turns; ++turn) {
+            __syncthreads();
+            if (size > 1) {
+                cluster.template send<VEC>(c, rank, size, turn, chain.template all<VEC>(c));
+                cluster.template receive<VEC>(c, rank, size, turn, carry, h, p.err);
+            }
+            chain.template give<VEC>(c, h);
+            __syncthreads();
+        }
+        cluster.close(size);
+        return;
+    }
+    typename Shape::X xs;
+    typename Shape::S gs;
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
     auto first_row = [&](int turn) { return (tile0 + turn * size + rank) * TILE + warp * R; };
-    auto fetch = [&](int turn, int stage) {
+    auto live_of = [&](int turn) { return turn < turns ? live_bits<R>(first_row(turn), begin, end) : 0u; };
+    auto load = [&](int turn) {
+        if (PIECE != 0) return;
+        xs.load(nullptr, first_row(turn), live_of(turn), p.D, slab, lane);
+        gs.load(nullptr, first_row(turn), live_of(turn), p.D, slab, lane);
+    };
+    auto put = [&](int turn, int place) {
         if (turn < turns) {
             const int row0 = first_row(turn);
-            const unsigned live = live_bits<R>(row0, begin, end);
-            xs.fetch(p.x, p.ldx, row0, live, p.D, slab, lane, stage);
-            gs.fetch(p.g, p.ldg, row0, live, p.D, slab, lane, stage);
+            const unsigned live = live_of(turn);
+            xs.put(row0, live, p.D, lane, place);
+            gs.put(row0, live, p.D, lane, place);
         }
-        tile_sent<STAGES>();
+        tile_sent();
     };
+    // decay and input of row j
+    auto row_of = [&](int j, int place, float (&a)[VEC], float (&b)[VEC]) {
+        float c[VEC];
+        xs.value(j, b, lane, place);
+        gs.value(j, a, lane, place);
+        decays<FULL, VEC>(form, a, c);
+        if (form & RECUR_COMPLEMENT) mul_to<VEC>(b, b, c);
+    };
+    T *const y = static_cast<T *>(p.y) + col;
+    load(0);
+    for (int i = 0; i < RING; ++i) {
+        put(i, i);
+        load(i + 1);
+    }
+    cluster.open(size);
     Near near;
-    float carry = 0.f;                                      // of channel threadIdx.x
-    bool dead = false;
-    for (int i = 0; i < AHEAD; ++i) fetch(i, i);
-    ex.open(size);
-    int stage = 0, next = AHEAD % (STAGES > 0 ? STAGES : 1);
+    int place = 0;
     for (int turn = 0; turn < turns; ++turn) {
         const int row0 = first_row(turn);
-        float a[R][VEC], b[R][VEC];
-        if constexpr (STAGES > 0) {                        // the tile read in the last turn makes room
-            fetch(turn + AHEAD, next);
-            next = next + 1 == STAGES ? 0 : next + 1;
-        }
-        tile_ready<STAGES>();
+        float a[R][VEC], b[R][VEC], h[VEC], A[VEC], H[VEC];
+        tile_ready<RING - 1>();
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            float c[VEC];
-            xs.value(j, b[j], lane, stage);
-            gs.value(j, a[j], lane, stage);
-            decays<FULL, VEC>(form, a[j], c);
-            if (form & RECUR_COMPLEMENT) mul_to<VEC>(b[j], b[j], c);
-        }
-        if constexpr (STAGES > 0) {
-            __syncwarp();
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-        } else {
-            fetch(turn + 1, 0);
-        }
-        const Rows rows = look_at<R>(p, near, row0, begin, end, lane);
-        float start[VEC] = {};                              // the state before the first row, where that starts a sequence
-        float A[VEC], H[VEC];
+            row_of(j, place, a[j], b[j]);
+            if (j == 0) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = a[0][v], H[v] = b[0][v];
-        if (rows.starts != 0) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) H[v] = 0.f;
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-                const bool starts = rows.starts >> j & 1u;
-                if (starts) {
-                    load_state<VEC>(H, p.state_in, recur_entry(p, sequence_of(p, near, row0 + j, lane)), p.D, col);
-                    if (j == 0) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) start[v] = H[v];
-                    }
-                }
-                fma_to<VEC>(H, a[j], H, b[j]);
-                if (starts) {                              // what follows takes b as the row's state: state_in may be
-#pragma unroll                                                     // overwritten by then
-                    for (int v = 0; v < VEC; ++v) b[j][v] = H[v];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 1; j < R; ++j) {
+                for (int v = 0; v < VEC; ++v) A[v] = a[0][v], H[v] = b[0][v];
+            } else {
                 fma_to<VEC>(H, a[j], H, b[j]);
                 mul_to<VEC>(A, A, a[j]);
             }
         }
-        ex.put(warp, lane, A, H, rows.starts != 0);
+        const Rows rows = look_at<R>(p, near, row0, begin, end, lane);
+        if (rows.starts != 0) {
+            // from the first row that begins a sequence on, nothing depends on what came before: these rows
+            // are finished here, before state_in can be overwritten
+#pragma unroll 1
+            for (int j = __ffs(rows.starts) - 1; j < R; ++j) {
+                if (!(rows.live >> j & 1u)) break;
+                float aj[VEC], bj[VEC];
+                row_of(j, place, aj, bj);
+                if (rows.starts >> j & 1u) {
+                    load_state<VEC>(H, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                    if (j == 0 && row0 % RECUR_CHUNK == 0) store_state<VEC>(H, p.chunk, row0 / RECUR_CHUNK, p.D, col);
+                }
+                fma_to<VEC>(H, aj, H, bj);
+                if (in) store_raw<T, VEC>(y + int64_t(row0 + j) * p.D, narrow<T, VEC>(H));
+                if (rows.lasts >> j & 1u) store_state<VEC>(H, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+            }
+        }
+        chain.put(warp, lane, A, H, rows.starts != 0);
         __syncthreads();
-        if (threadIdx.x < Ex::C) ex.chain(threadIdx.x, carry, rank, size, turn, dead, p.err);
+        put(turn + RING, place);                            // all lanes are through with the tile's place
+        load(turn + RING + 1);
+        place = place + 1 == RING ? 0 : place + 1;
         __syncthreads();
         if (rows.live == 0) continue;
-        float h[VEC];
-        ex.get(warp, lane, h);
-        if (p.chunk != nullptr && row0 % RECUR_CHUNK == 0 && (rows.live & 1u))
-            store_state<VEC>(rows.starts & 1u ? start : h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
-        T *y = static_cast<T *>(p.y) + int64_t(row0) * p.D + col;
+        chain.get(warp, lane, h);
+        if (row0 % RECUR_CHUNK == 0 && (rows.live & 1u) && !(rows.starts & 1u))
+            store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
+        T *to = y + int64_t(row0) * p.D;
         if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 fma_to<VEC>(h, a[j], h, b[j]);
-                if (in) store_raw<T, VEC>(y, narrow<T, VEC>(h));
-                y += p.D;
+                if (in) store_raw<T, VEC>(to, narrow<T, VEC>(h));
+                to += p.D;
             }
-            continue;
-        }
+        } else {
+            const unsigned mine = rows.starts != 0 ? rows.live & ((rows.starts & (0u - rows.starts)) - 1u) : rows.live;
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const bool starts = rows.starts >> j & 1u;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = starts ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
-            if (in && (rows.live >> j & 1u)) store_raw<T, VEC>(y + int64_t(j) * p.D, narrow<T, VEC>(h));
-            if (rows.lasts >> j & 1u)
-                store_state<VEC>(h, p.state_out, recur_entry(p, sequence_of(p, near, row0 + j, lane)), p.D, col);
+            for (int j = 0; j < R; ++j) {
+                if (!(mine >> j & 1u)) continue;
+                fma_to<VEC>(h, a[j], h, b[j]);
+                if (in) store_raw<T, VEC>(to + int64_t(j) * p.D, narrow<T, VEC>(h));
+                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+            }
         }
     }
     pdl_launch_dependents();
-    copy_empty<VEC>(p, p.state_in, p.state_out, (part * size + rank) * W + warp, parts * size * W, lane, col);
-    ex.close(size);
+    copy_empty<VEC>(p, p.state_in, p.state_out, (at.part * size + rank) * W + warp, at.parts * size * W, lane, col);
+    cluster.close(size);
 }
 
 // ----------------------------------------------------------------- backward
-// Forwards the exchange stays in the block, since a tile is a chunk.
-template <typename T, typename X, typename S, int VEC, int R, int W, int STAGES>
-struct GradShared {
-    static constexpr int RINGS = W * (Source<X, VEC, R, STAGES>::RING + Source<S, VEC, R, STAGES>::RING +
-                                      Source<T, VEC, R, STAGES>::RING);
-    static constexpr int FORTH = Exchange<VEC, W, false>::bytes(false);
-    static int bytes(int cluster) { return RINGS + FORTH + Exchange<VEC, W, true>::bytes(cluster > 1); }
+template <typename T, typename X, typename S, int VEC, int R, int W, int RINGS, int PIECE>
+struct GradShape {
+    static constexpr int RING = RINGS;
+    using Xs = Source<X, VEC, R, RING, PIECE>;
+    using Gs = Source<S, VEC, R, RING, PIECE>;
+    using Ds = Source<T, VEC, R, RING, PIECE>;
+    using Forth = Chain<VEC, W, false>;       // of h within the tile, which is a chunk
+    using Back = Chain<VEC, W, true>;         // of a d
+    using Cluster = Blocks<VEC>;
+    static constexpr int WARP = Xs::BYTES_RING + Gs::BYTES_RING + Ds::BYTES_RING, THREADS = W * 32;
+    static int bytes(int cluster) { return W * WARP + Forth::BYTES + Back::BYTES + Cluster::bytes(cluster); }
 };
 
 // T: dy, dx; X, S: x and g, or int8_t for codes; G: dg.
-template <typename T, typename X, typename S, typename G, int FORM, int VEC, int R, int W, int STAGES, int MIN>
-__global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(const RecurParams p) {
-    constexpr int TILE = R * W, AHEAD = STAGES > 0 ? STAGES - 1 : 1;
+template <typename T, typename X, typename S, typename G, int FORM, int VEC, int R, int W, int RING, int PIECE, int MIN>
+__global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(const __grid_constant__ RecurParams p) {
+    constexpr int TILE = R * W;
     constexpr bool FULL = sizeof(S) == 4;
-    static_assert(TILE == RECUR_CHUNK && R * VEC <= 32, "a tile is a chunk");
-    using Shared = GradShared<T, X, S, VEC, R, W, STAGES>;
-    using Forth = Exchange<VEC, W, false>;
-    using Ex = Exchange<VEC, W, true>;
+    static_assert(TILE == RECUR_CHUNK, "a tile is a chunk");
+    using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;
     extern __shared__ __align__(16) unsigned char shared[];
-    Forth &forth = *reinterpret_cast<Forth *>(shared + Shared::RINGS);
-    Ex &ex = *reinterpret_cast<Ex *>(shared + Shared::RINGS + Shared::FORTH);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = cluster_rank(), size = cluster_size();
-    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC, part = blockIdx.z, parts = gridDim.z;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = cluster_size();
+    const typename Shape::Forth forth{reinterpret_cast<float *>(shared + W * Shape::WARP)};
+    const typename Shape::Back back{forth.maps + Shape::Forth::BYTES / int(sizeof(float))};
+    typename Shape::Cluster cluster;
+    cluster.maps = back.maps + Shape::Back::BYTES / int(sizeof(float));
+    cluster.bar = reinterpret_cast<uint64_t *>(cluster.maps + 2 * all * cluster.ROW);
+    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC;
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D, complement = form & RECUR_COMPLEMENT;
     pdl_wait();
+    const Place at(p, cluster_rank(), all, p.cu != nullptr && p.solo_part > 0 ? longest_of(p, lane) : 0);
+    const int rank = at.rank, size = at.size;
     int begin, end;
-    part_rows(p, part, parts, lane, begin, end);
+    part_rows(p, at.part, at.parts, at.length, lane, begin, end);
     const int tile0 = begin / TILE, tiles = end > begin ? (end - 1) / TILE + 1 - tile0 : 0;
     const int turns = (tiles + size - 1) / size;
-    Source<X, VEC, R, STAGES> xs;
-    Source<S, VEC, R, STAGES> gs;
-    Source<T, VEC, R, STAGES> ds;
-    xs.ring = shared + warp * (xs.RING + gs.RING + ds.RING);
-    gs.ring = xs.ring + xs.RING;
-    ds.ring = gs.ring + gs.RING;
+    typename Shape::Xs xs;
+    typename Shape::Gs gs;
+    typename Shape::Ds ds;
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
+    ds.open(gs.ring + gs.BYTES_RING, p.dy, p.lddy, slab, lane);
     // tiles from the last one back; those before the part's first have no live rows
     auto tile_of = [&](int turn) { return tile0 + tiles - 1 - (turn * size + rank); };
+    auto first_row = [&](int turn) { return tile_of(turn) * TILE + warp * R; };
     auto live_of = [&](int turn) {
-        return turn < turns && tile_of(turn) >= tile0 ? live_bits<R>(tile_of(turn) * TILE + warp * R, begin, end) : 0u;
+        return turn < turns && tile_of(turn) >= tile0 ? live_bits<R>(first_row(turn), begin, end) : 0u;
     };
-    auto fetch = [&](int turn, int stage) {
-        if (turn < turns) {
-            const int row0 = tile_of(turn) * TILE + warp * R;
-            const unsigned live = live_of(turn);
-            xs.fetch(p.x, p.ldx, row0, live, p.D, slab, lane, stage);
-            gs.fetch(p.g, p.ldg, row0, live, p.D, slab, lane, stage);
-            ds.fetch(p.dy, p.lddy, row0, live, p.D, slab, lane, stage);
-        }
-        tile_sent<STAGES>();
-    };
-    // one turn ahead: exponents, and the chunk's state for the tile's first warp
-    unsigned xscales = 0, gscales = 0;
-    float chunk[VEC];
-    auto fetch_small = [&](int turn) {
-        const int row0 = tile_of(turn) * TILE + warp * R;
+    auto load = [&](int turn) {
+        if (PIECE != 0 && !xs.CODES && !gs.CODES) return;
+        const int row0 = first_row(turn);
         const unsigned live = live_of(turn);
-        xscales = xs.fetch_scales(p.xe, row0, live, p.D, slab, lane);
-        gscales = gs.fetch_scales(p.ge, row0, live, p.D, slab, lane);
-        load_state<VEC>(chunk, p.chunk, warp == 0 && (live & 1u) ? tile_of(turn) : -1, p.D, col);
+        xs.load(p.xe, row0, live, p.D, slab, lane);
+        gs.load(p.ge, row0, live, p.D, slab, lane);
+        ds.load(nullptr, row0, live, p.D, slab, lane);
     };
-    Near near;
-    float carry = 0.f, none = 0.f;                          // of channel threadIdx.x
-    bool dead = false;
-    for (int i = 0; i < AHEAD; ++i) fetch(i, i);
-    fetch_small(0);
-    ex.open(size);
-    int stage = 0, next = AHEAD % (STAGES > 0 ? STAGES : 1);
-    for (int turn = 0; turn < turns; ++turn) {
-        const int row0 = tile_of(turn) * TILE + warp * R;
-        // x: in the end h before the row, less x where c = 1 - a
-        float a[R][VEC], rest[R][VEC], x[R][VEC], d[R][VEC], h[VEC];
-        if constexpr (STAGES > 0) {
-            fetch(turn + AHEAD, next);
-            next = next + 1 == STAGES ? 0 : next + 1;
+    auto put = [&](int turn, int place) {
+        if (turn < turns) {
+            const int row0 = first_row(turn);
+            const unsigned live = live_of(turn);
+            xs.put(row0, live, p.D, lane, place);
+            gs.put(row0, live, p.D, lane, place);
+            ds.put(row0, live, p.D, lane, place);
         }
-        tile_ready<STAGES>();
-        xs.set_scales(xscales);
-        gs.set_scales(gscales);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = chunk[v];
+        tile_sent();
+    };
+    // a thread to a channel chains the maps: the first C of them backwards, the next C forwards, from the state before the
+    // chunk; where the part begins inside the chunk, a row that begins a sequence makes that void
+    constexpr int C = 32 * VEC;
+    auto chunk_of = [&](int turn, float (&h)[1]) {
+        const int t = tile_of(turn), c = slab + int(threadIdx.x) - C;
+        const bool mine = threadIdx.x >= C && threadIdx.x < 2 * C && c < p.D;
+        h[0] = mine && turn < turns && t >= tile0 && t * TILE >= begin ? p.chunk[int64_t(t) * p.D + c] : 0.f;
+    };
+    load(0);
+    for (int i = 0; i < RING; ++i) {
+        put(i, i);
+        load(i + 1);
+    }
+    float chunk[1], carry[1] = {};
+    chunk_of(0, chunk);
+    cluster.open(size);
+    Near near;
+    int place = 0;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int row0 = first_row(turn);
+        // x: in the end h before the row, less x where c = 1 - a
+        float a[R][VEC], rest[R][VEC], x[R][VEC], d[R][VEC], h[VEC], e[VEC], A[VEC], H[VEC], E[VEC];
+        tile_ready<RING - 1>();
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            xs.value(j, x[j], lane, stage);
-            gs.value(j, a[j], lane, stage);
-            ds.value(j, d[j], lane, stage);
+            xs.value(j, x[j], lane, place);
+            gs.value(j, a[j], lane, place);
+            ds.value(j, d[j], lane, place);
             decays<FULL, VEC>(form, a[j], rest[j]);
         }
-        if constexpr (STAGES > 0) {
-            __syncwarp();
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-        } else {
-            fetch(turn + 1, 0);
-        }
-        fetch_small(turn + 1);
+        __syncwarp();
+        put(turn + RING, place);
+        load(turn + RING + 1);
+        place = place + 1 == RING ? 0 : place + 1;
         Rows rows{0, 0, 0};
         if (live_of(turn) != 0) rows = look_at<R>(p, near, row0, begin, end, lane);
         // h after row j, from h before it
@@ -724,69 +987,90 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                 fma_to<VEC>(s, a[j], s, x[j]);
             }
         };
-        // a sequence's state before its first row, or its state's gradient behind its last
-        auto edge = [&](float (&s)[VEC], const float *base, int j) {
-            load_state<VEC>(s, base, recur_entry(p, sequence_of(p, near, row0 + j, lane)), p.D, col);
+        // the rows' maps, forwards and backwards
+        auto sum_up = [&](auto edges) {
+            constexpr bool EDGES = decltype(edges)::value;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) A[v] = a[0][v], H[v] = E[v] = 0.f;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                if (EDGES && (rows.starts >> j & 1u)) load_state<VEC>(H, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                step(H, j);
+                if (j > 0) mul_to<VEC>(A, A, a[j]);
+            }
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                if (EDGES && (rows.lasts >> j & 1u)) load_state<VEC>(E, p.dfinal, entry_of_row(p, row0 + j, lane), p.D, col);
+                add_to<VEC>(E, E, d[j]);
+                mul_to<VEC>(E, E, a[j]);
+            }
         };
-        float A[VEC], H[VEC], E[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = a[0][v], H[v] = h[v], E[v] = 0.f;
-        // forwards; a first row's state is looked up here and once more below, where it is in the cache
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (rows.starts >> j & 1u) edge(H, p.state_in, j);
-            step(H, j);
-            if (j > 0) mul_to<VEC>(A, A, a[j]);
-        }
-        // backwards
-#pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
-            if (rows.lasts >> j & 1u) edge(E, p.dfinal, j);
-            add_to<VEC>(E, E, d[j]);
-            mul_to<VEC>(E, E, a[j]);
-        }
-        forth.put(warp, lane, A, H, warp == 0 || rows.starts != 0);
-        ex.put(warp, lane, A, E, rows.lasts != 0);
+        if ((rows.starts | rows.lasts) == 0) sum_up(std::false_type{});
+        else sum_up(std::true_type{});
+        forth.put(warp, lane, A, H, rows.starts != 0);
+        back.put(warp, lane, A, E, rows.lasts != 0);
         __syncthreads();
-        if (threadIdx.x < Ex::C) ex.chain(threadIdx.x, carry, rank, size, turn, dead, p.err);
-        else if (threadIdx.x < 2 * Ex::C) forth.chain(threadIdx.x - Ex::C, none, 0, 1, 0, dead, p.err);
+        if (threadIdx.x < C) {
+            const int c = threadIdx.x;
+            float t[1] = {carry[0]};
+            if (size > 1) {
+                cluster.template send<1>(c, rank, size, turn, back.template all<1>(c));
+                cluster.template receive<1>(c, rank, size, turn, carry, t, p.err);
+                back.template give<1>(c, t);
+            } else {
+                back.template give<1>(c, carry);
+            }
+        } else if (threadIdx.x < 2 * C) {
+            forth.template give<1>(int(threadIdx.x) - C, chunk);
+            chunk_of(turn + 1, chunk);
+        }
         __syncthreads();
         if (rows.live == 0) continue;
-        float e[VEC];
-        ex.get(warp, lane, e);
-        if (warp > 0) forth.get(warp, lane, h);
+        forth.get(warp, lane, h);
+        back.get(warp, lane, e);
+        auto finish = [&](auto edges) {
+            constexpr bool EDGES = decltype(edges)::value;
+            float minus[VEC];
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (rows.starts >> j & 1u) edge(h, p.state_in, j);
-            float was[VEC];
+            for (int v = 0; v < VEC; ++v) minus[v] = -1.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) was[v] = h[v];
-            if (j < R - 1) step(h, j);
+            for (int j = 0; j < R; ++j) {
+                if (EDGES && (rows.starts >> j & 1u)) load_state<VEC>(h, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                float was[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) x[j][v] = complement ? was[v] - x[j][v] : was[v];
-        }
-        T *dx = static_cast<T *>(p.dx) + int64_t(row0) * p.D + col;
-        G *dg = static_cast<G *>(p.dg) + int64_t(row0) * p.D + col;
+                for (int v = 0; v < VEC; ++v) was[v] = h[v];
+                if (j < R - 1) step(h, j);
+                if (complement) fma_to<VEC>(x[j], x[j], minus, was);
+                else {
 #pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
-            if (rows.lasts >> j & 1u) edge(e, p.dfinal, j);
-            float dh[VEC], og[VEC];
-            add_to<VEC>(dh, d[j], e);
-            mul_to<VEC>(e, a[j], dh);
-            mul_to<VEC>(og, e, x[j]);
-            if (form & RECUR_SIGMOID) mul_to<VEC>(og, og, rest[j]);
-            if (complement) mul_to<VEC>(dh, rest[j], dh);
-            if (in && (rows.live >> j & 1u)) {
-                store_raw<T, VEC>(dx + int64_t(j) * p.D, narrow<T, VEC>(dh));
-                store_raw<G, VEC>(dg + int64_t(j) * p.D, narrow<G, VEC>(og));
+                    for (int v = 0; v < VEC; ++v) x[j][v] = was[v];
+                }
             }
-            if (p.dinitial != nullptr && (rows.starts >> j & 1u))
-                store_state<VEC>(e, p.dinitial, recur_entry(p, sequence_of(p, near, row0 + j, lane)), p.D, col);
-        }
+            int64_t at = int64_t(row0 + R - 1) * p.D + col;
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                if (EDGES && (rows.lasts >> j & 1u)) load_state<VEC>(e, p.dfinal, entry_of_row(p, row0 + j, lane), p.D, col);
+                float dh[VEC], g[VEC];
+                add_to<VEC>(dh, d[j], e);
+                mul_to<VEC>(e, a[j], dh);
+                mul_to<VEC>(g, e, x[j]);
+                if (form & RECUR_SIGMOID) mul_to<VEC>(g, g, rest[j]);
+                if (complement) mul_to<VEC>(dh, rest[j], dh);
+                if (in && (!EDGES || (rows.live >> j & 1u))) {
+                    store_raw<T, VEC>(static_cast<T *>(p.dx) + at, narrow<T, VEC>(dh));
+                    store_raw<G, VEC>(static_cast<G *>(p.dg) + at, narrow<G, VEC>(g));
+                }
+                at -= p.D;
+                if (EDGES && p.dinitial != nullptr && (rows.starts >> j & 1u))
+                    store_state<VEC>(e, p.dinitial, entry_of_row(p, row0 + j, lane), p.D, col);
+            }
+        };
+        if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) finish(std::false_type{});
+        else finish(std::true_type{});
     }
     pdl_launch_dependents();
-    copy_empty<VEC>(p, p.dfinal, p.dinitial, (part * size + rank) * W + warp, parts * size * W, lane, col);
-    ex.close(size);
+    copy_empty<VEC>(p, p.dfinal, p.dinitial, (at.part * size + rank) * W + warp, at.parts * size * W, lane, col);
+    cluster.close(size);
 }
 
 }  // namespace kda

@@ -17,7 +17,8 @@ cudaError_t launch_recur(const RecurParams &p, const RecurLaunch &l, unsigned th
     static std::atomic<bool> set[64];
     if (l.device < 0 || l.device >= 64) return cudaErrorInvalidDevice;
     if (!set[l.device].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        cudaError_t e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(FN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         set[l.device].store(true, std::memory_order_relaxed);
     }
@@ -37,24 +38,21 @@ cudaError_t launch_recur(const RecurParams &p, const RecurLaunch &l, unsigned th
     return cudaLaunchKernelEx(&cfg, FN, p);
 }
 
-// Rows to a warp: 16, whose maps are half as often exchanged, or 8 where a ring of 16 rows (FP32 inputs) would leave room
-// for one block on an SM alone.
-template <typename T, typename G, int FORM, int VEC, int STAGES, int MIN>
-cudaError_t launch_scan_vec(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    constexpr int R = sizeof(T) == 4 || STAGES == 0 ? 8 : 16, W = 8;
-    using Shared = ScanShared<T, G, VEC, R, W, STAGES>;
-    return launch_recur<kda_gated_scan_kernel<T, G, FORM, VEC, R, W, STAGES, MIN>>(
-        p, l, W * 32, Shared::bytes(int(l.cluster)), Shared::bytes(RECUR_CLUSTER), s);
+template <typename T, typename G, int FORM, int VEC, int PIECE>
+cudaError_t launch_scan_form(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
+    constexpr int R = sizeof(T) == 4 ? 8 : 16, W = 7, RING = 2, MIN = sizeof(T) == 4 ? 3 : 2;
+    using Shape = ScanShape<T, G, VEC, R, W, RING, PIECE>;
+    return launch_recur<kda_gated_scan_kernel<T, G, FORM, VEC, R, W, RING, PIECE, MIN>>(
+        p, l, Shape::THREADS, Shape::bytes(int(l.cluster)), Shape::bytes(RECUR_CLUSTER), s);
 }
 template <typename T, typename G>
 cudaError_t launch_scan_g(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    constexpr int MIN = sizeof(T) == 4 ? 3 : 2;
-    if (!l.staged) return launch_scan_vec<T, G, -1, 1, 0, 2>(p, l, s);
+    if (!l.staged) return launch_scan_form<T, G, -1, 1, sizeof(T) == 4 ? 4 : 0>(p, l, s);
     switch (p.form) {
-        case 0: return launch_scan_vec<T, G, 0, 2, 2, MIN>(p, l, s);
-        case 1: return launch_scan_vec<T, G, 1, 2, 2, MIN>(p, l, s);
-        case 2: return launch_scan_vec<T, G, 2, 2, 2, MIN>(p, l, s);
-        default: return launch_scan_vec<T, G, 3, 2, 2, MIN>(p, l, s);
+        case 0: return launch_scan_form<T, G, 0, 2, 16>(p, l, s);
+        case 1: return launch_scan_form<T, G, 1, 2, 16>(p, l, s);
+        case 2: return launch_scan_form<T, G, 2, 2, 16>(p, l, s);
+        default: return launch_scan_form<T, G, 3, 2, 16>(p, l, s);
     }
 }
 template <typename T>
@@ -62,21 +60,23 @@ cudaError_t launch_scan(const RecurParams &p, const RecurLaunch &l, cudaStream_t
     return l.wide_g || std::is_same_v<T, float> ? launch_scan_g<T, float>(p, l, s) : launch_scan_g<T, T>(p, l, s);
 }
 
-template <typename T, typename X, typename S, typename G, int FORM, int VEC, int STAGES, int MIN>
-cudaError_t launch_backward_vec(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    constexpr int R = 8, W = 8;
-    using Shared = GradShared<T, X, S, VEC, R, W, STAGES>;
-    return launch_recur<kda_gated_scan_backward_kernel<T, X, S, G, FORM, VEC, R, W, STAGES, MIN>>(
-        p, l, W * 32, Shared::bytes(int(l.cluster)), Shared::bytes(RECUR_CLUSTER), s);
+template <typename T, typename X, typename S, typename G, int FORM, int VEC, int PIECE>
+cudaError_t launch_backward_form(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
+    constexpr int R = 8, W = 8, RING = 1;
+    using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;
+    return launch_recur<kda_gated_scan_backward_kernel<T, X, S, G, FORM, VEC, R, W, RING, PIECE, VEC == 1 ? 3 : 2>>(
+        p, l, Shape::THREADS, Shape::bytes(int(l.cluster)), Shape::bytes(RECUR_CLUSTER), s);
 }
 template <typename T, typename X, typename S, typename G>
 cudaError_t launch_backward_xs(const RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    if (!l.staged) return launch_backward_vec<T, X, S, G, -1, 1, 0, 2>(p, l, s);
+    // rows of FP32: four bytes at a time fit any of them
+    constexpr int ODD = sizeof(T) == 4 && sizeof(X) == 4 && sizeof(S) == 4 ? 4 : 0, VEC = backward_vec<T, X, S>();
+    if (!l.staged) return launch_backward_form<T, X, S, G, -1, 1, ODD>(p, l, s);
     switch (p.form) {
-        case 0: return launch_backward_vec<T, X, S, G, 0, 2, 2, 2>(p, l, s);
-        case 1: return launch_backward_vec<T, X, S, G, 1, 2, 2, 2>(p, l, s);
-        case 2: return launch_backward_vec<T, X, S, G, 2, 2, 2, 2>(p, l, s);
-        default: return launch_backward_vec<T, X, S, G, 3, 2, 2, 2>(p, l, s);
+        case 0: return launch_backward_form<T, X, S, G, 0, VEC, 16>(p, l, s);
+        case 1: return launch_backward_form<T, X, S, G, 1, VEC, 16>(p, l, s);
+        case 2: return launch_backward_form<T, X, S, G, 2, VEC, 16>(p, l, s);
+        default: return launch_backward_form<T, X, S, G, 3, VEC, 16>(p, l, s);
     }
 }
 template <typename T, typename G>

@@ -6,11 +6,18 @@
 namespace kda {
 
 struct RecurLaunch {
-    bool staged;                // the inputs' rows are whole, aligned 16-byte pieces: two channels to a lane, else one
+    bool staged;                // the inputs' rows are whole, aligned 16-byte pieces
     bool wide_g, x8, g8;        // g and dg in FP32; codes in place of x and g
     unsigned cluster, slabs, parts;
     int device;
 };
+
+// Channels to a lane of the gradients of staged rows: two, or one where an operand is FP32, whose rows of 64 channels
+// would leave room for one block on an SM alone.
+template <typename T, typename X, typename S>
+constexpr int backward_vec() {
+    return sizeof(T) == 4 || sizeof(X) == 4 || sizeof(S) == 4 ? 1 : 2;
+}
 
 cudaError_t launch_scan_f32(const RecurParams &p, const RecurLaunch &l, cudaStream_t s);
 cudaError_t launch_scan_bf16(const RecurParams &p, const RecurLaunch &l, cudaStream_t s);
