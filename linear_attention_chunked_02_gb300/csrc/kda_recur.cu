@@ -11,6 +11,79 @@
 #include "kda_recurrent.h"
 #include "kda_spans.h"
 
+namespace kda {
+
+// Packed sequences whose lengths every warp looks through, 32 at a time.
+constexpr int MOST_LOOKED_AT = 2048;
+
+// Whether and how single warps walk the sequences: where there are enough of them for all SMs.  16 x 512 rows of 8192
+// channels in BF16 take 63 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
+// channels 70.  Packed sequences are walked where none is longer than three parts of the stream, which the device sees.
+static bool walk_grid(RecurParams &p, int wide) {
+    constexpr int64_t WARPS = 152 * 6;
+    if (wide == 0 || p.rows == 0 || (p.cu != nullptr && p.nseq > MOST_LOOKED_AT)) return false;
+    for (int vec = wide; vec >= wide / 2; vec -= wide / 2) {
+        const int64_t slabs = (p.D + 32 * vec - 1) / (32 * vec);
+        if (slabs * p.nseq < WARPS) continue;
+        int64_t parts = 2 * WARPS / slabs > 1 ? 2 * WARPS / slabs : 1;
+        if (parts > p.nseq) parts = p.nseq;
+        if (p.cu == nullptr) {
+            const int64_t each = (p.nseq + parts - 1) / parts;
+            parts = (p.nseq + each - 1) / each;
+            p.walk_part = int32_t(each * p.T);
+        } else {
+            p.walk_part = int32_t((p.T + parts - 1) / parts);
+            parts = (p.T + p.walk_part - 1) / p.walk_part;
+            p.walk_most = p.walk_part < INT32_MAX / 3 ? 3 * p.walk_part : INT32_MAX;
+        }
+        p.walk_parts = int32_t(parts);
+        p.walk_wide = vec == wide;
+        return true;
+    }
+    return false;
+}
+
+// The grid: as many blocks as run at once, by clusters that share the rows and, for what they leave, by parts of the stream.  A
+// cluster's size is the one that takes the fewest rounds of tiles, a round counting a sixth more where blocks
+// exchange.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
+// blocks of a cluster share the rows.  Where the device sees that none is longer than three blocks' parts, they take parts
+// of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 153 us and
+// 212).
+RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide) {
+    const int64_t slabs = (p.D + columns - 1) / columns, T = p.T, seqs = p.cu == nullptr ? p.nseq : 1;
+    if (walk_grid(p, walk_wide) && p.cu == nullptr)         // all warps of the blocks walk
+        return {1, unsigned(room.blocks[1] < 65535 ? room.blocks[1] : 65535), 1};
+    int64_t parts = 1, each = 1;
+    int size = 1;
+    double best = 0;
+    for (int k = 1; k <= RECUR_CLUSTER; ++k) {
+        if (room.blocks[k] == 0) continue;
+        const int64_t fit = room.blocks[k] / (slabs * k), most = fit < 1 ? 1 : fit < seqs ? fit : seqs;
+        const int64_t per = seqs > 0 ? (seqs + most - 1) / most : 1, n = seqs > 0 ? (seqs + per - 1) / per : 1;
+        const int64_t waves = (slabs * k * n + room.blocks[k] - 1) / room.blocks[k], rounds = (per * T + tile * k - 1) / (tile * k);
+        const double cost = double(waves) * double(rounds) * (k > 1 ? 7. / 6. : 1.);
+        if (k == 1 || cost < best) best = cost, size = k, parts = n, each = per;
+    }
+    if (p.cu == nullptr) {
+        while (parts > 65535) each *= 2, parts = (seqs + each - 1) / each;
+        p.part = int32_t(each * T);
+        return {unsigned(size), unsigned(slabs), unsigned(parts)};
+    }
+    parts = room.blocks[size] / (slabs * size);
+    if (parts > p.nseq) parts = p.nseq;
+    if (parts < 1) parts = 1;
+    p.part = int32_t((T + parts - 1) / parts > 1 ? (T + parts - 1) / parts : 1);
+    parts = T > 0 ? (T + p.part - 1) / p.part : 1;
+    if (size > 1 && p.nseq > 1 && p.nseq <= MOST_LOOKED_AT) {
+        const int64_t alone = parts * size;
+        p.solo_part = int32_t((T + alone - 1) / alone > 1 ? (T + alone - 1) / alone : 1);
+        p.solo_most = int32_t(3 * int64_t(p.solo_part) < INT32_MAX ? 3 * int64_t(p.solo_part) : INT32_MAX);
+    }
+    return {unsigned(size), unsigned(slabs), unsigned(parts)};
+}
+
+}  // namespace kda
+
 namespace {
 
 using namespace kda;
@@ -259,72 +332,6 @@ bool vectors_fit(const RowTensor (&tensors)[N], int32_t D, F bytes_of) {
     return true;
 }
 
-// Packed sequences whose lengths every warp looks through, 32 at a time.
-constexpr int MOST_LOOKED_AT = 2048;
-
-// The grid: `vec` channels to each of 32 lanes, and the stream in as many parts, then blocks to a cluster, as `room` blocks
-// at once allow.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
-// blocks of a cluster share the rows.  Where the device sees that none is longer than three blocks' parts, they take parts
-// of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 153 us and
-// 212).  A tile of a block is `tile` rows.
-void shape(RecurParams &p, RecurLaunch &l, int vec, int tile, int64_t room, int64_t T) {
-    l.slabs = unsigned((p.D + 32 * vec - 1) / (32 * vec));
-    const int64_t want = room / l.slabs > 1 ? room / l.slabs : 1;
-    const int64_t rows = p.cu == nullptr ? T : p.rows;      // that a cluster may share
-    int64_t parts = 1;
-    l.cluster = 1;
-    if (p.cu == nullptr) parts = p.nseq < want ? p.nseq : want;
-    while (l.cluster < RECUR_CLUSTER && 2 * l.cluster * parts <= want && rows > int64_t(l.cluster) * tile) l.cluster *= 2;
-    if (p.cu != nullptr) {
-        parts = want / l.cluster < p.nseq ? want / l.cluster : p.nseq;
-        if (parts < 1) parts = 1;
-    }
-    int64_t part;
-    if (p.cu == nullptr) {
-        const int64_t each = (p.nseq + parts - 1) / parts;
-        parts = (p.nseq + each - 1) / each;
-        part = each * T;
-    } else {
-        part = (T + parts - 1) / parts;
-        if (part < 1) part = 1;
-        parts = T > 0 ? (T + part - 1) / part : 1;
-    }
-    l.parts = unsigned(parts);
-    p.part = int32_t(part);
-    if (p.cu != nullptr && l.cluster > 1 && p.nseq > 1 && p.nseq <= MOST_LOOKED_AT) {
-        const int64_t alone = int64_t(l.parts) * l.cluster;
-        p.solo_part = int32_t((T + alone - 1) / alone);
-        p.solo_most = int32_t(3 * int64_t(p.solo_part) < INT32_MAX ? 3 * p.solo_part : INT32_MAX);
-    }
-}
-
-// Whether and how single warps walk the sequences: where there are enough of them for all SMs.  16 x 512 rows of 8192
-// channels in BF16 take 63 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
-// channels 70.  Packed sequences are walked where none is longer than three parts of the stream, which the device sees.
-void shape_walk(RecurParams &p, RecurLaunch &l, int wide, int64_t T) {
-    constexpr int64_t WARPS = 152 * 6;
-    if (p.rows == 0 || (p.cu != nullptr && p.nseq > MOST_LOOKED_AT)) return;
-    for (int vec = wide; vec >= wide / 2; vec -= wide / 2) {
-        const int64_t slabs = (p.D + 32 * vec - 1) / (32 * vec);
-        if (slabs * p.nseq < WARPS) continue;
-        int64_t parts = 2 * WARPS / slabs > 1 ? 2 * WARPS / slabs : 1;
-        if (parts > p.nseq) parts = p.nseq;
-        if (p.cu == nullptr) {
-            const int64_t each = (p.nseq + parts - 1) / parts;
-            parts = (p.nseq + each - 1) / each;
-            p.walk_part = int32_t(each * T);
-            l.cluster = 1, l.parts = 1, l.slabs = 152 * 2;  // all of its warps walk
-        } else {
-            p.walk_part = int32_t((T + parts - 1) / parts);
-            parts = (T + p.walk_part - 1) / p.walk_part;
-            p.walk_most = p.walk_part < INT32_MAX / 3 ? 3 * p.walk_part : INT32_MAX;
-        }
-        p.walk_parts = int32_t(parts);
-        p.walk_wide = vec == wide;
-        return;
-    }
-}
-
 }  // namespace
 
 extern "C" {
@@ -363,8 +370,7 @@ kda_status_t kda_gated_scan(const void *x, int64_t ldx, const void *g, int64_t l
     const RowTensor rowed[] = {{x, ldx, es}, {g, ldg, gs}, {y, D, es}, {state_in, D, 4}, {state_out, D, 4}, {chunk_states, D, 4}};
     const RowTensor inputs[] = {rowed[0], rowed[1]};
     l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
-    shape(p, l, l.staged ? 2 : 1, dtype == KDA_F32 ? 56 : 112, 152 * (dtype == KDA_F32 ? 3 : 2), T);
-    if (l.staged) shape_walk(p, l, 8 / int(es), T);
+    l.walk_wide = l.staged ? 8 / int(es) : 0;
     DeviceInfo info;
     if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;
@@ -416,8 +422,6 @@ kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const void *x
                                {state_in, D, 4}, {dstate_out, D, 4}, {dstate_in, D, 4}};
     const RowTensor inputs[] = {rowed[0], rowed[1], rowed[2]};
     l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
-    const bool wide = dtype == KDA_F32 || (g_dtype == KDA_F32 && !g8);
-    shape(p, l, l.staged && !wide ? 2 : 1, RECUR_CHUNK, 152 * (l.staged && !wide ? 2 : 3), T);
     DeviceInfo info;
     if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;

@@ -130,6 +130,7 @@ struct Rows {
 
 template <int R>
 __device__ __forceinline__ unsigned live_bits(int row0, int begin, int end) {
+    if (row0 >= begin && row0 + R <= end) return (1u << R) - 1u;
     const int lo = max(begin - row0, 0), hi = min(end - row0, R);
     return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
@@ -350,18 +351,21 @@ struct Source {
     static constexpr int ROWS = PIECES < 32 ? 32 / PIECES : 1;               // of one copy of the warp
     static_assert(!CODES || R * VEC <= 32, "one scale to a lane");
     unsigned char *ring;
-    const S *base;
-    int64_t ld;                 // pitch
+    const S *base, *from;       // from: the lane's first piece of the next tile
+    int64_t ld, step;           // pitch; from one tile of the warp to its next
     int own_row, own_col;       // of the lane's pieces
     raw_t<S, VEC> raw[PIECE == 0 ? R : 1];
     unsigned exponent = 0;      // codes: of row lane / VEC, block lane % VEC of the warp's columns
 
-    __device__ __forceinline__ void open(unsigned char *at, const void *from, int64_t pitch, int slab, int lane) {
+    // the warp's tiles begin at row0 and are `rows` apart
+    __device__ __forceinline__ void open(unsigned char *at, const void *tensor, int64_t pitch, int row0, int rows, int slab, int lane) {
         ring = at;
-        base = static_cast<const S *>(from);
+        base = static_cast<const S *>(tensor);
         ld = pitch;
+        step = rows * ld;
         own_row = PIECE == 0 ? 0 : lane / PIECES;
         own_col = slab + (PIECE == 0 ? lane * VEC : lane % PIECES * (PIECE / int(sizeof(S))));
+        from = base + int64_t(row0 + own_row) * ld + own_col;
     }
     // A tile's rows row0 .. row0 + R take two steps: load() when the tile before it is put(), and put() into its place of
     // the ring.  Rows without their bit in `live` read as zeros.
@@ -384,25 +388,27 @@ struct Source {
         else
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
     }
-    __device__ __forceinline__ void put(int row0, unsigned live, int D, int lane, int place) {
+    __device__ __forceinline__ void put(unsigned live, int D, int lane, int place) {
         if constexpr (PIECE == 0) {
 #pragma unroll
             for (int j = 0; j < R; ++j)
                 *reinterpret_cast<raw_t<S, VEC> *>(ring + place * BYTES + j * ROW + lane * VEC * int(sizeof(S))) = raw[j];
         } else {
-            const S *from = base + int64_t(row0 + own_row) * ld + own_col;
             const uint32_t to = smem_u32(ring) + place * BYTES + lane * PIECE;
+            constexpr int COPIES = (R + ROWS - 1) / ROWS;
+            const S *s = from;
             if (R < ROWS && own_row >= R) {
             } else if (live == (1u << R) - 1u && own_col < D) {
 #pragma unroll
-                for (int i = 0; i < (R + ROWS - 1) / ROWS; ++i, from += ROWS * ld) copy(to + i * ROWS * ROW, from, PIECE);
+                for (int i = 0; i < COPIES; ++i, s += ROWS * ld) copy(to + i * ROWS * ROW, s, PIECE);
             } else {
 #pragma unroll
-                for (int i = 0; i < (R + ROWS - 1) / ROWS; ++i, from += ROWS * ld) {
+                for (int i = 0; i < COPIES; ++i, s += ROWS * ld) {
                     const bool ok = own_col < D && (live >> (own_row + i * ROWS) & 1u);
-                    copy(to + i * ROWS * ROW, ok ? from : base, ok ? PIECE : 0);
+                    copy(to + i * ROWS * ROW, ok ? s : base, ok ? PIECE : 0);
                 }
             }
+            from += step;
         }
         if constexpr (CODES) scales(place)[lane] = ckpt_scale(exponent);
     }
@@ -423,6 +429,9 @@ __device__ __forceinline__ void tile_ready() {
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
     __syncwarp();
 }
+
+// The warp's number in the block, the same register for all lanes as far as the compiler sees.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0); }
 
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ int cluster_rank() {
@@ -632,7 +641,7 @@ struct ScanShape {
     using S = Source<G, VEC, R, RING, PIECE>;
     using Warps = Chain<VEC, W, false>;
     using Cluster = Blocks<VEC>;
-    static constexpr int WARP = X::BYTES_RING + S::BYTES_RING, THREADS = (W + 1) * 32;
+    static constexpr int WARP = X::BYTES_RING + S::BYTES_RING, THREADS = (W + 1) * 32, COLUMNS = 32 * VEC, TILE = R * W;
     // of a walking warp of the block, with 8 bytes of x to a lane; 4 take less
     static constexpr int WIDE = 8 / int(sizeof(T)), WALK = PIECE == 16 ? (W + 1) * WalkShape<T, G, WIDE>::WARP : 0;
     static int bytes(int cluster) {
@@ -653,14 +662,13 @@ __device__ __forceinline__ void walk(const RecurParams &p, const int form, int p
     const int tile0 = begin / R, tiles = end > begin ? (end - 1) / R + 1 - tile0 : 0;
     typename Shape::X xs;
     typename Shape::S gs;
-    xs.open(ring, p.x, p.ldx, slab, lane);
-    gs.open(ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
+    xs.open(ring, p.x, p.ldx, tile0 * R, R, slab, lane);
+    gs.open(ring + xs.BYTES_RING, p.g, p.ldg, tile0 * R, R, slab, lane);
     auto put = [&](int tile, int place) {
         if (tile < tiles) {
-            const int row0 = (tile0 + tile) * R;
-            const unsigned live = live_bits<R>(row0, begin, end);
-            xs.put(row0, live, p.D, lane, place);
-            gs.put(row0, live, p.D, lane, place);
+            const unsigned live = live_bits<R>((tile0 + tile) * R, begin, end);
+            xs.put(live, p.D, lane, place);
+            gs.put(live, p.D, lane, place);
         }
         tile_sent();
     };
@@ -729,7 +737,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     static_assert(RECUR_CHUNK % R == 0 && R <= 16, "chunk states lie at warps' first rows");
     using Shape = ScanShape<T, G, VEC, R, W, RING, PIECE>;
     extern __shared__ __align__(16) unsigned char shared[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = cluster_size();
+    const int lane = threadIdx.x & 31, warp = warp_index(), all = cluster_size();
     const typename Shape::Warps chain{reinterpret_cast<float *>(shared + W * Shape::WARP)};
     typename Shape::Cluster cluster;
     cluster.maps = reinterpret_cast<float *>(shared + W * Shape::WARP + Shape::Warps::BYTES);
@@ -771,9 +779,9 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     }
     typename Shape::X xs;
     typename Shape::S gs;
-    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, slab, lane);
-    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
     auto first_row = [&](int turn) { return (tile0 + turn * size + rank) * TILE + warp * R; };
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), size * TILE, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), size * TILE, slab, lane);
     auto live_of = [&](int turn) { return turn < turns ? live_bits<R>(first_row(turn), begin, end) : 0u; };
     auto load = [&](int turn) {
         if (PIECE != 0) return;
@@ -782,10 +790,9 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     };
     auto put = [&](int turn, int place) {
         if (turn < turns) {
-            const int row0 = first_row(turn);
             const unsigned live = live_of(turn);
-            xs.put(row0, live, p.D, lane, place);
-            gs.put(row0, live, p.D, lane, place);
+            xs.put(live, p.D, lane, place);
+            gs.put(live, p.D, lane, place);
         }
         tile_sent();
     };
@@ -849,13 +856,12 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
         chain.get(warp, lane, h);
         if (row0 % RECUR_CHUNK == 0 && (rows.live & 1u) && !(rows.starts & 1u))
             store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
-        T *to = y + int64_t(row0) * p.D;
+        T *const to = static_cast<T *>(p.y) + int64_t(row0) * p.D + slab;
         if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 fma_to<VEC>(h, a[j], h, b[j]);
-                if (in) store_raw<T, VEC>(to, narrow<T, VEC>(h));
-                to += p.D;
+                if (in) store_raw<T, VEC>(to + unsigned(j * p.D + lane * VEC), narrow<T, VEC>(h));
             }
         } else {
             const unsigned mine = rows.starts != 0 ? rows.live & ((rows.starts & (0u - rows.starts)) - 1u) : rows.live;
@@ -863,7 +869,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
             for (int j = 0; j < R; ++j) {
                 if (!(mine >> j & 1u)) continue;
                 fma_to<VEC>(h, a[j], h, b[j]);
-                if (in) store_raw<T, VEC>(to + int64_t(j) * p.D, narrow<T, VEC>(h));
+                if (in) store_raw<T, VEC>(to + unsigned(j * p.D + lane * VEC), narrow<T, VEC>(h));
                 if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
             }
         }
@@ -884,6 +890,7 @@ struct GradShape {
     using Back = Chain<VEC, W, true>;         // of a d
     using Cluster = Blocks<VEC>;
     static constexpr int WARP = Xs::BYTES_RING + Gs::BYTES_RING + Ds::BYTES_RING, THREADS = W * 32;
+    static constexpr int COLUMNS = 32 * VEC, TILE = R * W;
     static int bytes(int cluster) { return W * WARP + Forth::BYTES + Back::BYTES + Cluster::bytes(cluster); }
 };
 
@@ -895,7 +902,7 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     static_assert(TILE == RECUR_CHUNK, "a tile is a chunk");
     using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;
     extern __shared__ __align__(16) unsigned char shared[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = cluster_size();
+    const int lane = threadIdx.x & 31, warp = warp_index(), all = cluster_size();
     const typename Shape::Forth forth{reinterpret_cast<float *>(shared + W * Shape::WARP)};
     const typename Shape::Back back{forth.maps + Shape::Forth::BYTES / int(sizeof(float))};
     typename Shape::Cluster cluster;
@@ -914,12 +921,12 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     typename Shape::Xs xs;
     typename Shape::Gs gs;
     typename Shape::Ds ds;
-    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, slab, lane);
-    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, slab, lane);
-    ds.open(gs.ring + gs.BYTES_RING, p.dy, p.lddy, slab, lane);
     // tiles from the last one back; those before the part's first have no live rows
     auto tile_of = [&](int turn) { return tile0 + tiles - 1 - (turn * size + rank); };
     auto first_row = [&](int turn) { return tile_of(turn) * TILE + warp * R; };
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), -size * TILE, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), -size * TILE, slab, lane);
+    ds.open(gs.ring + gs.BYTES_RING, p.dy, p.lddy, first_row(0), -size * TILE, slab, lane);
     auto live_of = [&](int turn) {
         return turn < turns && tile_of(turn) >= tile0 ? live_bits<R>(first_row(turn), begin, end) : 0u;
     };
@@ -933,11 +940,10 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     };
     auto put = [&](int turn, int place) {
         if (turn < turns) {
-            const int row0 = first_row(turn);
             const unsigned live = live_of(turn);
-            xs.put(row0, live, p.D, lane, place);
-            gs.put(row0, live, p.D, lane, place);
-            ds.put(row0, live, p.D, lane, place);
+            xs.put(live, p.D, lane, place);
+            gs.put(live, p.D, lane, place);
+            ds.put(live, p.D, lane, place);
         }
         tile_sent();
     };
@@ -1046,7 +1052,9 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                     for (int v = 0; v < VEC; ++v) x[j][v] = was[v];
                 }
             }
-            int64_t at = int64_t(row0 + R - 1) * p.D + col;
+            const int64_t first = int64_t(row0) * p.D + slab;
+            T *const dx = static_cast<T *>(p.dx) + first;
+            G *const dg = static_cast<G *>(p.dg) + first;
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 if (EDGES && (rows.lasts >> j & 1u)) load_state<VEC>(e, p.dfinal, entry_of_row(p, row0 + j, lane), p.D, col);
@@ -1057,10 +1065,10 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                 if (form & RECUR_SIGMOID) mul_to<VEC>(g, g, rest[j]);
                 if (complement) mul_to<VEC>(dh, rest[j], dh);
                 if (in && (!EDGES || (rows.live >> j & 1u))) {
-                    store_raw<T, VEC>(static_cast<T *>(p.dx) + at, narrow<T, VEC>(dh));
-                    store_raw<G, VEC>(static_cast<G *>(p.dg) + at, narrow<G, VEC>(g));
+                    const unsigned at = unsigned(j * p.D + lane * VEC);
+                    store_raw<T, VEC>(dx + at, narrow<T, VEC>(dh));
+                    store_raw<G, VEC>(dg + at, narrow<G, VEC>(g));
                 }
-                at -= p.D;
                 if (EDGES && p.dinitial != nullptr && (rows.starts >> j & 1u))
                     store_state<VEC>(e, p.dinitial, entry_of_row(p, row0 + j, lane), p.D, col);
             }
