@@ -45,7 +45,7 @@ static bool walk_grid(RecurParams &p, int wide) {
 
 // The grid: as many blocks as run at once, by clusters that share the rows and, for what they leave, by parts of the stream.  A
 // cluster's size is the one that takes the fewest rounds of tiles, a round counting a sixth more where blocks
-// exchange.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
+// exchange and a block half a round for its beginning.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
 // blocks of a cluster share the rows.  Where the device sees that none is longer than three blocks' parts, they take parts
 // of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 153 us and
 // 212).
@@ -58,11 +58,16 @@ RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int til
     double best = 0;
     for (int k = 1; k <= RECUR_CLUSTER; ++k) {
         if (room.blocks[k] == 0) continue;
-        const int64_t fit = room.blocks[k] / (slabs * k), most = fit < 1 ? 1 : fit < seqs ? fit : seqs;
-        const int64_t per = seqs > 0 ? (seqs + most - 1) / most : 1, n = seqs > 0 ? (seqs + per - 1) / per : 1;
-        const int64_t waves = (slabs * k * n + room.blocks[k] - 1) / room.blocks[k], rounds = (per * T + tile * k - 1) / (tile * k);
-        const double cost = double(waves) * double(rounds) * (k > 1 ? 7. / 6. : 1.);
-        if (k == 1 || cost < best) best = cost, size = k, parts = n, each = per;
+        const int64_t fit = room.blocks[k] / (slabs * k) > 1 ? room.blocks[k] / (slabs * k) : 1;
+        for (int64_t most = fit; most <= 8 * fit; most += fit) {             // also parts that run one after the other
+            const int64_t m = most < seqs ? most : seqs > 0 ? seqs : 1;
+            const int64_t per = seqs > 0 ? (seqs + m - 1) / m : 1, n = seqs > 0 ? (seqs + per - 1) / per : 1;
+            const int64_t waves = (slabs * k * n + room.blocks[k] - 1) / room.blocks[k];
+            const double rounds = double((per * T + tile * k - 1) / (tile * k));
+            const double cost = double(waves) * (rounds * (k > 1 ? 7. / 6. : 1.) + 0.5);
+            if (best == 0 || cost < best) best = cost, size = k, parts = n, each = per;
+            if (m < most) break;
+        }
     }
     if (p.cu == nullptr) {
         while (parts > 65535) each *= 2, parts = (seqs + each - 1) / each;

@@ -104,7 +104,7 @@ cudaError_t launch_scan(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
 
 template <typename T, typename X, typename S, typename G, int FORM, int VEC, int PIECE>
 cudaError_t launch_backward_form(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    constexpr int R = 8, W = 8, RING = 1, MIN = VEC == 1 && PIECE == 16 ? 3 : 2;
+    constexpr int R = 8, W = 8, RING = sizeof(X) == 1 || sizeof(S) == 1 ? 1 : 2, MIN = VEC == 1 && PIECE == 16 ? 3 : 2;
     using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;
     return launch_recur<kda_gated_scan_backward_kernel<T, X, S, G, FORM, VEC, R, W, RING, PIECE, MIN>, Shape>(p, l, s);
 }
