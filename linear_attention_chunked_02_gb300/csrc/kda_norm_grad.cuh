@@ -63,11 +63,12 @@ __device__ __forceinline__ void act_pair(int silu, const float (&z)[VEC], float 
     }
 }
 
-// Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread, two rows on their way to a thread
-// while a third is worked on.
+// Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread, three rows on their way to a
+// thread while a fourth is worked on.  8192 x 64 rows of 128, BF16, with one, two and three rows ahead: 132, 117 and 110 us
+// from tensors (floor 99), 123, 111 and 107 from codes (floor 80), which issue bounds.
 template <typename T, typename X, typename Z, int VEC, int NV>
-__global__ void __launch_bounds__(NORM_GRAD_THREADS) kda_norm_grad_narrow_kernel(const NormGradParams p, const int lanes) {
-    constexpr int AHEAD = NV == 1 ? 2 : 1;
+__global__ void __launch_bounds__(NORM_GRAD_THREADS, NV == 1 ? 2 : 1) kda_norm_grad_narrow_kernel(const NormGradParams p, const int lanes) {
+    constexpr int AHEAD = NV == 1 ? 3 : 1;
     constexpr bool FULL = sizeof(Z) == 4;
     __shared__ float part[NORM_GRAD_THREADS * VEC];
     const int t = int(threadIdx.x) & (lanes - 1), groups = NORM_GRAD_THREADS / lanes, group = int(threadIdx.x) / lanes;

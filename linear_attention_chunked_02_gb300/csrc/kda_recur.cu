@@ -74,7 +74,11 @@ RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int til
         p.part = int32_t(each * T);
         return {unsigned(size), unsigned(slabs), unsigned(parts)};
     }
-    parts = room.blocks[size] / (slabs * size);
+    const int64_t fit = room.blocks[size] / (slabs * size);
+    // parts that run one after the other even out the end, as long as they hold two sequences each; walking warps are
+    // all of the blocks' that run at once
+    parts = p.walk_parts > 0 ? fit : 4 * fit;
+    while (parts > fit && 2 * parts * size > p.nseq) --parts;
     if (parts > p.nseq) parts = p.nseq;
     if (parts < 1) parts = 1;
     p.part = int32_t((T + parts - 1) / parts > 1 ? (T + parts - 1) / parts : 1);

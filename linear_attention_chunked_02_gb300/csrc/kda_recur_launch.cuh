@@ -89,7 +89,18 @@ cudaError_t launch_scan_form(RecurParams &p, const RecurLaunch &l, cudaStream_t 
 }
 template <typename T, typename G>
 cudaError_t launch_scan_g(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    if (!l.staged) return launch_scan_form<T, G, -1, 1, sizeof(T) == 4 ? 4 : 0>(p, l, s);
+    if (!l.staged) {
+        if constexpr (sizeof(T) == 4) {                     // four bytes at a time fit any row of FP32
+            switch (p.form) {
+                case 0: return launch_scan_form<T, G, 0, 1, 4>(p, l, s);
+                case 1: return launch_scan_form<T, G, 1, 1, 4>(p, l, s);
+                case 2: return launch_scan_form<T, G, 2, 1, 4>(p, l, s);
+                default: return launch_scan_form<T, G, 3, 1, 4>(p, l, s);
+            }
+        } else {
+            return launch_scan_form<T, G, -1, 1, 0>(p, l, s);
+        }
+    }
     switch (p.form) {
         case 0: return launch_scan_form<T, G, 0, 2, 16>(p, l, s);
         case 1: return launch_scan_form<T, G, 1, 2, 16>(p, l, s);
@@ -104,15 +115,25 @@ cudaError_t launch_scan(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
 
 template <typename T, typename X, typename S, typename G, int FORM, int VEC, int PIECE>
 cudaError_t launch_backward_form(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    constexpr int R = 8, W = 8, RING = sizeof(X) == 1 || sizeof(S) == 1 ? 1 : 2, MIN = VEC == 1 && PIECE == 16 ? 3 : 2;
+    constexpr int R = 8, W = 8, RING = sizeof(X) == 1 || sizeof(S) == 1 ? 1 : 2, MIN = VEC == 1 && PIECE != 0 ? 3 : 2;
     using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;
     return launch_recur<kda_gated_scan_backward_kernel<T, X, S, G, FORM, VEC, R, W, RING, PIECE, MIN>, Shape>(p, l, s);
 }
 template <typename T, typename X, typename S, typename G>
 cudaError_t launch_backward_xs(RecurParams &p, const RecurLaunch &l, cudaStream_t s) {
-    // rows of FP32: four bytes at a time fit any of them
-    constexpr int ODD = sizeof(T) == 4 && sizeof(X) == 4 && sizeof(S) == 4 ? 4 : 0, VEC = backward_vec<T, X, S>();
-    if (!l.staged) return launch_backward_form<T, X, S, G, -1, 1, ODD>(p, l, s);
+    constexpr int VEC = backward_vec<T, X, S>();
+    if (!l.staged) {
+        if constexpr (sizeof(T) == 4 && sizeof(X) == 4 && sizeof(S) == 4) {
+            switch (p.form) {
+                case 0: return launch_backward_form<T, X, S, G, 0, 1, 4>(p, l, s);
+                case 1: return launch_backward_form<T, X, S, G, 1, 1, 4>(p, l, s);
+                case 2: return launch_backward_form<T, X, S, G, 2, 1, 4>(p, l, s);
+                default: return launch_backward_form<T, X, S, G, 3, 1, 4>(p, l, s);
+            }
+        } else {
+            return launch_backward_form<T, X, S, G, -1, 1, 0>(p, l, s);
+        }
+    }
     switch (p.form) {
         case 0: return launch_backward_form<T, X, S, G, 0, VEC, 16>(p, l, s);
         case 1: return launch_backward_form<T, X, S, G, 1, VEC, 16>(p, l, s);
