@@ -91,22 +91,24 @@ def _tensors(*saved):
 
 def _stream_rows(x: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):
     """(B, T, D, sequences given by cu_seqlens, sequences) of a [B, T, D] tensor."""
-    if x.dim() != 3 or x.shape[2] < 1:
-        raise ValueError(f"x must be [B, T, D], got {tuple(x.shape)}")
-    B, T, D = x.shape
-    if _int32("cu_seqlens", cu_seqlens) is not None and (B != 1 or cu_seqlens.numel() < 2):
+    shape = x.shape
+    if len(shape) != 3 or shape[2] < 1:
+        raise ValueError(f"x must be [B, T, D], got {tuple(shape)}")
+    B, T, D = shape
+    if cu_seqlens is None:
+        return B, T, D, 0, B
+    nseq = _int32("cu_seqlens", cu_seqlens).numel() - 1
+    if B != 1 or nseq < 1:
         raise ValueError("cu_seqlens needs B == 1 and at least one sequence")
-    nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    return B, T, D, nseq, nseq if cu_seqlens is not None else B
+    return B, T, D, nseq, nseq
 
 
-def _states(name: str, t: Optional[torch.Tensor], entries: Optional[int], D: int) -> None:
-    if t is None:
-        return
-    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != D or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 [entries, {D}], got {t.dtype} {tuple(t.shape)}")
-    if entries is not None and t.shape[0] != entries:
-        raise ValueError(f"{name} must have {entries} entries, got {t.shape[0]}")
+def _states(name: str, t: torch.Tensor, entries: Optional[int], D: int) -> None:
+    shape = t.shape
+    if t.dtype != torch.float32 or len(shape) != 2 or shape[1] != D or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [entries, {D}], got {t.dtype} {tuple(shape)}")
+    if entries is not None and shape[0] != entries:
+        raise ValueError(f"{name} must have {entries} entries, got {shape[0]}")
 
 
 def _out(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, device) -> torch.Tensor:
@@ -117,9 +119,18 @@ def _out(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, devi
     return out
 
 
-def _types(x: torch.Tensor, g: torch.Tensor) -> None:
-    if x.dtype not in DTYPE_CODE or g.dtype not in (x.dtype, torch.float32):
-        raise ValueError(f"unsupported dtypes x {x.dtype}, g {g.dtype}")
+def _types(x: torch.Tensor, g: torch.Tensor) -> Tuple[int, int]:
+    xt, gt = x.dtype, g.dtype
+    if xt not in DTYPE_CODE or (gt != xt and gt != torch.float32):
+        raise ValueError(f"unsupported dtypes x {xt}, g {gt}")
+    return DTYPE_CODE[xt], DTYPE_CODE[gt]
+
+
+def _like(name: str, out: Optional[torch.Tensor], t: torch.Tensor) -> torch.Tensor:
+    """_out for a tensor of t's shape and type."""
+    if out is None and t.is_contiguous():
+        return torch.empty_like(t)                         # the quickest way
+    return _out(name, out, t.shape, t.dtype, t.device)
 
 
 def gated_scan_chunks(B: int, T: int) -> int:
@@ -149,28 +160,33 @@ def gated_scan(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Optional[torch.Tens
             return gated_scan(x, g, cu_seqlens, gate, complement, initial_state, final_state, slots, chunk_states, out)
     decay, comp = _form(gate, complement)
     B, T, D, nseq, N = _stream_rows(x, cu_seqlens)
-    _types(x, g)
+    xt, gt = _types(x, g)
     if g.shape != x.shape:
         raise ValueError(f"g must be {tuple(x.shape)}, got {tuple(g.shape)}")
-    slots = _int32("slots", slots, N)
-    if slots is not None and initial_state is None and final_state is None:
-        raise ValueError("slots need a state pool")
-    if final_state is None and slots is not None:
-        final_state = initial_state
-    entries = N if slots is None else final_state.shape[0]
-    _states("initial_state", initial_state, entries, D)
-    _states("final_state", final_state, entries, D)
-    _states("chunk_states", chunk_states, gated_scan_chunks(B, T), D)
-    x, ldx = _pitched(x)
-    g, ldg = _pitched(g)
-    slots = slots.contiguous() if slots is not None else None
-    cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
-    out = _out("out", out, x.shape, x.dtype, x.device)
+    entries = N
+    if slots is not None:
+        slots = _int32("slots", slots, N).contiguous()
+        if initial_state is None and final_state is None:
+            raise ValueError("slots need a state pool")
+        if final_state is None:
+            final_state = initial_state
+        entries = final_state.shape[0]
+    if initial_state is not None:
+        _states("initial_state", initial_state, entries, D)
     if final_state is None:
         final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+    elif final_state is not initial_state:
+        _states("final_state", final_state, entries, D)
+    if chunk_states is not None:
+        _states("chunk_states", chunk_states, gated_scan_chunks(B, T), D)
+    if cu_seqlens is not None:
+        cu_seqlens = cu_seqlens.contiguous()
+    out = _like("out", out, x)
+    x, ldx = _pitched(x)
+    g, ldg = _pitched(g)
     st = lib().kda_gated_scan(x.data_ptr(), ldx, g.data_ptr(), ldg, out.data_ptr(), _ptr(initial_state),
                               final_state.data_ptr(), _ptr(slots), entries, _ptr(chunk_states), _ptr(cu_seqlens), nseq,
-                              B, T, D, DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], decay, comp, _current_stream(device))
+                              B, T, D, xt, gt, decay, comp, _current_stream(device))
     check(st, "kda_gated_scan")
     return out, final_state
 
@@ -198,30 +214,35 @@ def gated_scan_backward(dy: torch.Tensor, x: Saved, g: Saved, chunk_states: torc
                                        dx, dg, dinitial_state)
     decay, comp = _form(gate, complement)
     B, T, D, nseq, N = _stream_rows(dy, cu_seqlens)
-    if dy.dtype not in DTYPE_CODE:
-        raise ValueError(f"unsupported dtype dy {dy.dtype}")
-    x, xe = _saved("x", x, dy.shape, (dy.dtype,))
-    g_dtypes = (dy.dtype,) if dy.dtype == torch.float32 else (dy.dtype, torch.float32)
+    dt, f32 = dy.dtype, torch.float32
+    if dt not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype dy {dt}")
+    x, xe = _saved("x", x, dy.shape, (dt,))
+    g_dtypes = (dt,) if dt == f32 else (dt, f32)
     g, ge = _saved("g", g, dy.shape, g_dtypes)
-    g_dtype = dg.dtype if dg is not None else dy.dtype if ge is not None else g.dtype
+    g_dtype = dg.dtype if dg is not None else dt if ge is not None else g.dtype
     if g_dtype not in g_dtypes or (ge is None and g_dtype != g.dtype):
-        raise ValueError(f"unsupported dtypes dy {dy.dtype}, g {g.dtype}, dg {g_dtype}")
+        raise ValueError(f"unsupported dtypes dy {dt}, g {g.dtype}, dg {g_dtype}")
     _states("chunk_states", chunk_states, gated_scan_chunks(B, T), D)
-    _states("initial_state", initial_state, N, D)
-    _states("dfinal_state", dfinal_state, N, D)
-    _states("dinitial_state", dinitial_state, N, D)
+    if initial_state is not None:
+        _states("initial_state", initial_state, N, D)
+    if dfinal_state is not None:
+        _states("dfinal_state", dfinal_state, N, D)
+    if dinitial_state is not None:
+        _states("dinitial_state", dinitial_state, N, D)
+    elif initial_state is not None:
+        dinitial_state = torch.empty_like(initial_state)
+    if cu_seqlens is not None:
+        cu_seqlens = cu_seqlens.contiguous()
+    dx = _like("dx", dx, dy)
+    dg = _like("dg", dg, dy) if g_dtype == dt else _out("dg", dg, dy.shape, g_dtype, dy.device)
     dy, lddy = _pitched(dy)
     x, ldx = _pitched(x)
     g, ldg = _pitched(g)
-    cu_seqlens = cu_seqlens.contiguous() if cu_seqlens is not None else None
-    dx = _out("dx", dx, dy.shape, dy.dtype, dy.device)
-    dg = _out("dg", dg, dy.shape, g_dtype, dy.device)
-    if dinitial_state is None and initial_state is not None:
-        dinitial_state = torch.empty((N, D), dtype=torch.float32, device=dy.device)
     st = lib().kda_gated_scan_backward(dy.data_ptr(), lddy, x.data_ptr(), _ptr(xe), ldx, g.data_ptr(), _ptr(ge), ldg,
                                        chunk_states.data_ptr(), _ptr(initial_state), _ptr(dfinal_state), dx.data_ptr(),
                                        dg.data_ptr(), _ptr(dinitial_state), _ptr(cu_seqlens), nseq, B, T, D,
-                                       DTYPE_CODE[dy.dtype], DTYPE_CODE[g_dtype], decay, comp, _current_stream(device))
+                                       DTYPE_CODE[dt], DTYPE_CODE[g_dtype], decay, comp, _current_stream(device))
     check(st, "kda_gated_scan_backward")
     return dx, dg, dinitial_state
 
@@ -241,21 +262,22 @@ def gated_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, slots: Opt
         with other:
             return gated_step(x, g, state, slots, gate, complement, out)
     decay, comp = _form(gate, complement)
-    if x.dim() != 2 or x.shape[1] < 1 or g.shape != x.shape:
-        raise ValueError(f"x and g must be [N, D], got {tuple(x.shape)} and {tuple(g.shape)}")
-    _types(x, g)
-    N, D = x.shape
-    slots = _int32("slots", slots, N)
+    shape = x.shape
+    if len(shape) != 2 or shape[1] < 1 or g.shape != shape:
+        raise ValueError(f"x and g must be [N, D], got {tuple(shape)} and {tuple(g.shape)}")
+    xt, gt = _types(x, g)
+    N, D = shape
     _states("state", state, None, D)
-    if slots is None and state.shape[0] < N:
-        raise ValueError(f"{N} requests and a pool of {state.shape[0]} states")
+    entries = state.shape[0]
+    if slots is not None:
+        slots = _int32("slots", slots, N).contiguous()
+    elif entries < N:
+        raise ValueError(f"{N} requests and a pool of {entries} states")
+    out = _like("out", out, x)
     x, ldx = _pitched(x)
     g, ldg = _pitched(g)
-    slots = slots.contiguous() if slots is not None else None
-    out = _out("out", out, x.shape, x.dtype, x.device)
     st = lib().kda_gated_step(x.data_ptr(), ldx, g.data_ptr(), ldg, out.data_ptr(), state.data_ptr(), _ptr(slots),
-                              state.shape[0], N, D, DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], decay, comp,
-                              _current_stream(device))
+                              entries, N, D, xt, gt, decay, comp, _current_stream(device))
     check(st, "kda_gated_step")
     return out
 
@@ -336,8 +358,7 @@ def gated_norm_backward(dy: torch.Tensor, x: Saved, gate: Saved, weight: torch.T
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     dy, x, gate, weight = dy.contiguous(), x.contiguous(), gate.contiguous(), weight.contiguous()
-    dx = _out("dx", dx, dy.shape, dy.dtype, dy.device)
-    dgate = _out("dgate", dgate, dy.shape, dy.dtype, dy.device)
+    dx, dgate = _like("dx", dx, dy), _like("dgate", dgate, dy)
     dweight = _out("dweight", dweight, weight.shape, torch.float32, dy.device)
     need = gated_norm_backward_workspace_size(rows, dim)
     if workspace is None and need > 0:
