@@ -126,6 +126,7 @@ struct Place {
 // What a warp knows of its R rows: which are its part's, which begin a sequence, which end one.
 struct Rows {
     unsigned live, starts, lasts;
+    int entry;                  // lane j: the state entry of row j's sequence, where a row begins or ends one
 };
 
 template <int R>
@@ -135,46 +136,68 @@ __device__ __forceinline__ unsigned live_bits(int row0, int begin, int end) {
     return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
 
-template <int R>
-__device__ __forceinline__ Rows look_at(const RecurParams &p, Near &near, int row0, int begin, int end, int lane) {
-    Rows r{live_bits<R>(row0, begin, end), 0, 0};
-    if (r.live == 0) return r;
-    unsigned s = 0;                                        // bits 0 .. R: rows at which a sequence begins
-    if (!(near.low < row0 && row0 + R < near.high)) {
-        if (p.cu == nullptr) {
-            const unsigned t = unsigned(p.T), before = unsigned(row0) / t * t;
-            s = __ballot_sync(0xffffffffu, lane <= R && unsigned(row0 + lane) % t == 0);
-            near.low = int(before) - (before == unsigned(row0) ? 1 : 0);
-            near.high = int(before == unsigned(row0) ? before : before + t);
-        } else {
-            const int first = count_until(p.cu, p.nseq + 1, row0 - 1, lane);
-            int at = first + lane, v = at <= p.nseq ? p.cu[at] : INT_MAX;
-            near.low = first > 0 ? p.cu[first - 1] : -1;
-            near.high = __shfl_sync(0xffffffffu, v, 0);
-            unsigned bits = 0;
-            for (;;) {
-                const int d = v - row0;
-                if (d >= 0 && d <= R) bits |= 1u << d;
-                if (__shfl_sync(0xffffffffu, v, 31) > row0 + R) break;
-                at += 32;                                  // only where sequences are short or empty
-                v = at <= p.nseq ? p.cu[at] : INT_MAX;
-            }
-            s = __reduce_or_sync(0xffffffffu, bits);
-        }
-    }
-    r.starts = s & r.live;
-    r.lasts = s >> 1;
-    if (end - 1 - row0 < R) r.lasts |= 1u << (end - 1 - row0);
-    r.lasts &= r.live;
-    return r;
-}
-
 // State entry of sequence n, or -1 for none.
 __device__ __forceinline__ int recur_entry(const RecurParams &p, int n) {
     if (n < 0 || n >= p.nseq) return -1;                   // malformed cu_seqlens
     if (p.slots == nullptr) return n;
     const int s = p.slots[n];
     return s >= 0 && s < p.num_slots ? s : -1;
+}
+
+struct Looked {
+    Rows rows;
+    Near near;
+};
+template <int R>
+__device__ __noinline__ Looked look_closely(const RecurParams &p, int row0, unsigned live, int end, int lane) {
+    Near near;
+    int n = 0;                                             // of row row0 + lane
+    unsigned s;                                            // bits 0 .. R: rows at which a sequence begins
+    if (p.cu == nullptr) {
+        const unsigned t = unsigned(p.T), before = unsigned(row0) / t * t;
+        n = int(unsigned(row0 + lane) / t);
+        s = __ballot_sync(0xffffffffu, lane <= R && unsigned(n) * t == unsigned(row0 + lane));
+        near.low = int(before) - (before == unsigned(row0) ? 1 : 0);
+        near.high = int(before == unsigned(row0) ? before : before + t);
+    } else {
+        const int first = count_until(p.cu, p.nseq + 1, row0 - 1, lane);
+        int at = first + lane;
+        const int bound = at <= p.nseq ? p.cu[at] : INT_MAX;
+        near.low = first > 0 ? p.cu[first - 1] : -1;
+        near.high = __shfl_sync(0xffffffffu, bound, 0);
+        unsigned bits = 0;
+        for (int v = bound;;) {
+            const int d = v - row0;
+            if (d >= 0 && d <= R) bits |= 1u << d;
+            if (__shfl_sync(0xffffffffu, v, 31) > row0 + R) break;
+            at += 32;                                      // only where sequences are short or empty
+            v = at <= p.nseq ? p.cu[at] : INT_MAX;
+        }
+        s = __reduce_or_sync(0xffffffffu, bits);
+        if (s != 0 || end - row0 <= R) {
+#pragma unroll 1
+            for (int j = 0; j < R; ++j) {
+                int k = __popc(__ballot_sync(0xffffffffu, bound <= row0 + j));
+                if (k == 32) k = count_until(p.cu, p.nseq + 1, row0 + j, lane) - first;
+                if (lane == j) n = first + k - 1;
+            }
+        }
+    }
+    Rows r{live, s & live, s >> 1, -1};
+    if (end - 1 - row0 < R) r.lasts |= 1u << (end - 1 - row0);
+    r.lasts &= live;
+    if ((r.starts | r.lasts) >> (lane & 31) & 1u) r.entry = recur_entry(p, n);
+    return {r, near};
+}
+
+// What there is to know of the rows row0 .. row0 + R, those with their bit in `live`; most tiles are
+// inside a sequence that an earlier one has shown.
+template <int R>
+__device__ __forceinline__ Rows look_at(const RecurParams &p, Near &near, int row0, unsigned live, int end, int lane) {
+    if (live == 0 || (near.low < row0 && row0 + R < near.high && row0 + R < end)) return Rows{live, 0, 0, -1};
+    const Looked l = look_closely<R>(p, row0, live, end, lane);
+    near = l.near;
+    return l.rows;
 }
 
 template <int VEC>
@@ -188,12 +211,6 @@ template <int VEC>
 __device__ __forceinline__ void store_state(const float (&h)[VEC], float *base, int64_t entry, int D, int col) {
     if (base == nullptr || entry < 0 || col >= D) return;
     store_raw<float, VEC>(base + entry * D + col, narrow<float, VEC>(h));
-}
-
-// The state entry of the sequence that `row` belongs to; all lanes call it.  Out of line: it is for rows that begin or
-// end a sequence, and would fill the instruction cache in every unrolled row.
-inline __device__ __noinline__ int entry_of_row(const RecurParams &p, int row, int lane) {
-    return recur_entry(p, p.cu == nullptr ? row / p.T : count_until(p.cu, p.nseq + 1, row, lane) - 1);
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -679,7 +696,7 @@ __device__ __forceinline__ void walk(const RecurParams &p, const int form, int p
     T *y = static_cast<T *>(p.y) + int64_t(tile0) * R * p.D + col;
     for (int tile = 0; tile < tiles; ++tile) {
         const int row0 = (tile0 + tile) * R;
-        const Rows rows = look_at<R>(p, near, row0, begin, end, lane);
+        const Rows rows = look_at<R>(p, near, row0, live_bits<R>(row0, begin, end), end, lane);
         tile_ready<RING - 1>();
         auto row = [&](int j) {
             float a[VEC], b[VEC], c[VEC];
@@ -703,12 +720,12 @@ __device__ __forceinline__ void walk(const RecurParams &p, const int form, int p
             for (int j = 0; j < R; ++j, y += p.D) {
                 if (!(rows.live >> j & 1u)) continue;
                 if (rows.starts >> j & 1u) {
-                    load_state<VEC>(h, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                    load_state<VEC>(h, p.state_in, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
                     if (j == 0 && row0 % RECUR_CHUNK == 0) store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
                 }
                 row(j);
                 if (in) store_raw<T, VEC>(y, narrow<T, VEC>(h));
-                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
             }
         }
         __syncwarp();
@@ -828,7 +845,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
                 mul_to<VEC>(A, A, a[j]);
             }
         }
-        const Rows rows = look_at<R>(p, near, row0, begin, end, lane);
+        const Rows rows = look_at<R>(p, near, row0, live_bits<R>(row0, begin, end), end, lane);
         if (rows.starts != 0) {
             // from the first row that begins a sequence on, nothing depends on what came before: these rows
             // are finished here, before state_in can be overwritten
@@ -838,12 +855,12 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
                 float aj[VEC], bj[VEC];
                 row_of(j, place, aj, bj);
                 if (rows.starts >> j & 1u) {
-                    load_state<VEC>(H, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                    load_state<VEC>(H, p.state_in, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
                     if (j == 0 && row0 % RECUR_CHUNK == 0) store_state<VEC>(H, p.chunk, row0 / RECUR_CHUNK, p.D, col);
                 }
                 fma_to<VEC>(H, aj, H, bj);
                 if (in) store_raw<T, VEC>(y + int64_t(row0 + j) * p.D, narrow<T, VEC>(H));
-                if (rows.lasts >> j & 1u) store_state<VEC>(H, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (rows.lasts >> j & 1u) store_state<VEC>(H, p.state_out, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
             }
         }
         chain.put(warp, lane, A, H, rows.starts != 0);
@@ -857,7 +874,8 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
         if (row0 % RECUR_CHUNK == 0 && (rows.live & 1u) && !(rows.starts & 1u))
             store_state<VEC>(h, p.chunk, row0 / RECUR_CHUNK, p.D, col);
         T *const to = static_cast<T *>(p.y) + int64_t(row0) * p.D + slab;
-        if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) {
+        // rows that begin or end a sequence have code of their own: branches in the unrolled rows would keep them apart
+        if (__builtin_expect((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u, 1)) {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 fma_to<VEC>(h, a[j], h, b[j]);
@@ -870,7 +888,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
                 if (!(mine >> j & 1u)) continue;
                 fma_to<VEC>(h, a[j], h, b[j]);
                 if (in) store_raw<T, VEC>(to + unsigned(j * p.D + lane * VEC), narrow<T, VEC>(h));
-                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (rows.lasts >> j & 1u) store_state<VEC>(h, p.state_out, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
             }
         }
     }
@@ -989,8 +1007,7 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
             __syncwarp();
             refill(turn);
         }
-        Rows rows{0, 0, 0};
-        if (live_of(turn) != 0) rows = look_at<R>(p, near, row0, begin, end, lane);
+        const Rows rows = look_at<R>(p, near, row0, live_of(turn), end, lane);
         // h after row j, from h before it
         auto step = [&](float (&s)[VEC], int j) {
             if (complement) {
@@ -1001,25 +1018,30 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                 fma_to<VEC>(s, a[j], s, x[j]);
             }
         };
+        // a sequence's state before its first row, or its state's gradient behind its last
+        auto edge = [&](float (&s)[VEC], const float *states, int j) {
+            load_state<VEC>(s, states, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
+        };
         // the rows' maps, forwards and backwards
+        // rows that begin or end a sequence have code of their own: branches in the unrolled rows would keep them apart
         auto sum_up = [&](auto edges) {
             constexpr bool EDGES = decltype(edges)::value;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) A[v] = a[0][v], H[v] = E[v] = 0.f;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                if (EDGES && (rows.starts >> j & 1u)) load_state<VEC>(H, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (EDGES && (rows.starts >> j & 1u)) edge(H, p.state_in, j);
                 step(H, j);
                 if (j > 0) mul_to<VEC>(A, A, a[j]);
             }
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                if (EDGES && (rows.lasts >> j & 1u)) load_state<VEC>(E, p.dfinal, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (EDGES && (rows.lasts >> j & 1u)) edge(E, p.dfinal, j);
                 add_to<VEC>(E, E, d[j]);
                 mul_to<VEC>(E, E, a[j]);
             }
         };
-        if ((rows.starts | rows.lasts) == 0) sum_up(std::false_type{});
+        if (__builtin_expect((rows.starts | rows.lasts) == 0, 1)) sum_up(std::false_type{});
         else sum_up(std::true_type{});
         forth.put(warp, lane, A, H, rows.starts != 0);
         back.put(warp, lane, A, E, rows.lasts != 0);
@@ -1043,6 +1065,9 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
         if (rows.live == 0) continue;
         forth.get(warp, lane, h);
         back.get(warp, lane, e);
+        const int64_t first = int64_t(row0) * p.D + slab;
+        T *const dx = static_cast<T *>(p.dx) + first;
+        G *const dg = static_cast<G *>(p.dg) + first;
         auto finish = [&](auto edges) {
             constexpr bool EDGES = decltype(edges)::value;
             float minus[VEC];
@@ -1050,7 +1075,7 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
             for (int v = 0; v < VEC; ++v) minus[v] = -1.f;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                if (EDGES && (rows.starts >> j & 1u)) load_state<VEC>(h, p.state_in, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (EDGES && (rows.starts >> j & 1u)) edge(h, p.state_in, j);
                 float was[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) was[v] = h[v];
@@ -1061,12 +1086,9 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                     for (int v = 0; v < VEC; ++v) x[j][v] = was[v];
                 }
             }
-            const int64_t first = int64_t(row0) * p.D + slab;
-            T *const dx = static_cast<T *>(p.dx) + first;
-            G *const dg = static_cast<G *>(p.dg) + first;
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                if (EDGES && (rows.lasts >> j & 1u)) load_state<VEC>(e, p.dfinal, entry_of_row(p, row0 + j, lane), p.D, col);
+                if (EDGES && (rows.lasts >> j & 1u)) edge(e, p.dfinal, j);
                 float dh[VEC], g[VEC];
                 add_to<VEC>(dh, d[j], e);
                 mul_to<VEC>(e, a[j], dh);
@@ -1079,10 +1101,10 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
                     store_raw<G, VEC>(dg + at, narrow<G, VEC>(g));
                 }
                 if (EDGES && p.dinitial != nullptr && (rows.starts >> j & 1u))
-                    store_state<VEC>(e, p.dinitial, entry_of_row(p, row0 + j, lane), p.D, col);
+                    store_state<VEC>(e, p.dinitial, __shfl_sync(0xffffffffu, rows.entry, j), p.D, col);
             }
         };
-        if ((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u) finish(std::false_type{});
+        if (__builtin_expect((rows.starts | rows.lasts) == 0 && rows.live == (1u << R) - 1u, 1)) finish(std::false_type{});
         else finish(std::true_type{});
     }
     pdl_launch_dependents();
