@@ -51,8 +51,8 @@ static bool walk_grid(RecurParams &p, int wide) {
 // 212).
 RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide) {
     const int64_t slabs = (p.D + columns - 1) / columns, T = p.T, seqs = p.cu == nullptr ? p.nseq : 1;
-    if (walk_grid(p, walk_wide) && p.cu == nullptr)         // all warps of the blocks walk
-        return {1, unsigned(room.blocks[1] < 65535 ? room.blocks[1] : 65535), 1};
+    p.slabs = int32_t(slabs);
+    if (walk_grid(p, walk_wide) && p.cu == nullptr) return {1, unsigned(room.blocks[1])};   // all warps of the blocks walk
     int64_t parts = 1, each = 1;
     int size = 1;
     double best = 0;
@@ -70,14 +70,14 @@ RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int til
         }
     }
     if (p.cu == nullptr) {
-        while (parts > 65535) each *= 2, parts = (seqs + each - 1) / each;
         p.part = int32_t(each * T);
-        return {unsigned(size), unsigned(slabs), unsigned(parts)};
+        p.parts = int32_t(parts);
+        return {unsigned(size), unsigned(slabs * parts)};
     }
     const int64_t fit = room.blocks[size] / (slabs * size);
     // parts that run one after the other even out the end, as long as they hold two sequences each; walking warps are
     // all of the blocks' that run at once
-    parts = p.walk_parts > 0 ? fit : 4 * fit;
+    parts = p.walk_parts > 0 && fit > 0 ? fit : 4 * fit;
     while (parts > fit && 2 * parts * size > p.nseq) --parts;
     if (parts > p.nseq) parts = p.nseq;
     if (parts < 1) parts = 1;
@@ -88,7 +88,8 @@ RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int til
         p.solo_part = int32_t((T + alone - 1) / alone > 1 ? (T + alone - 1) / alone : 1);
         p.solo_most = int32_t(3 * int64_t(p.solo_part) < INT32_MAX ? 3 * int64_t(p.solo_part) : INT32_MAX);
     }
-    return {unsigned(size), unsigned(slabs), unsigned(parts)};
+    p.parts = int32_t(parts);
+    return {unsigned(size), unsigned(slabs * parts)};
 }
 
 }  // namespace kda

@@ -43,6 +43,7 @@ struct RecurParams {
     int32_t T;                  // dense: rows to a sequence; packed: all rows
     int32_t rows, D;
     int32_t form;
+    int32_t slabs, parts;       // clusters are numbered by columns, then by parts of the stream; those past them walk or idle
     int32_t part;               // rows of the stream whose sequences a cluster takes (dense: a multiple of T)
     int32_t solo_part;          // packed: where no sequence is longer than solo_most, every block takes a part of this many
     int32_t solo_most;          // rows by itself, cluster or not (0: never)
@@ -66,20 +67,27 @@ struct RecurParams {
     unsigned *err;              // device error word
 };
 
-// Entries of cu[0 .. n) that are at most `row`, found by the whole warp.  Any contents give a count in [0, n].
-__device__ __forceinline__ int count_until(const int32_t *cu, int n, int row, int lane) {
+// How many of the numbers 0 .. n - 1 `holds` is true for, if it is true up to some number and false from there on; found by
+// the whole warp.  Whatever holds() says, the answer is in [0, n].
+template <typename F>
+__device__ __forceinline__ int count_while(int n, int lane, F holds) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int step = (hi - lo + 31) >> 5, at = lo + step * (lane + 1) - 1;
-        const int k = __popc(__ballot_sync(0xffffffffu, at < hi && cu[at] <= row));
-        const int next = lo + step * (k + 1) - 1;          // the first probe past `row`, if it is one
+        const int k = __popc(__ballot_sync(0xffffffffu, at < hi && holds(at)));
+        const int next = lo + step * (k + 1) - 1;          // the first probe that is false, if there is one
         lo = min(lo + step * k, hi);
         hi = max(lo, min(hi, next));
     }
     return lo;
 }
+// Entries of cu[0 .. n) that are at most `row`.
+__device__ __forceinline__ int count_until(const int32_t *cu, int n, int row, int lane) {
+    return count_while(n, lane, [&](int i) { return cu[i] <= row; });
+}
 
-// The rows [begin, end) of a part's sequences: those that start in its `length` rows of the stream.
+// The rows [begin, end) of a part's sequences: those whose middle is in its `length` rows of the stream (their
+// first rows would put two of equal lengths into one part where the length is rounded up).
 __device__ __forceinline__ void part_rows(const RecurParams &p, int part, int parts, int length, int lane, int &begin, int &end) {
     const int64_t from = int64_t(part) * length, to = from + length;
     if (p.cu == nullptr) {
@@ -88,10 +96,9 @@ __device__ __forceinline__ void part_rows(const RecurParams &p, int part, int pa
         return;
     }
     auto first_from = [&](int64_t row) {
-        const int i = count_until(p.cu, p.nseq + 1, row > INT_MAX ? INT_MAX : int(row) - 1, lane);
-        return i <= p.nseq ? p.cu[i] : p.cu[p.nseq];
+        return p.cu[count_while(p.nseq, lane, [&](int n) { return int64_t(p.cu[n]) + p.cu[n + 1] < 2 * row; })];
     };
-    begin = min(max(first_from(from), 0), p.rows);
+    begin = min(max(part > 0 ? first_from(from) : p.cu[0], 0), p.rows);
     end = part + 1 < parts ? first_from(to) : p.cu[p.nseq];
     end = min(max(end, begin), p.rows);
 }
@@ -113,7 +120,7 @@ struct Place {
     int part, parts, length, rank, size;
 
     __device__ __forceinline__ Place(const RecurParams &p, int cluster_rank, int cluster_size, int longest)
-        : part(blockIdx.z), parts(gridDim.z), length(p.part), rank(cluster_rank), size(cluster_size) {
+        : part(int(blockIdx.x) / cluster_size / p.slabs), parts(p.parts), length(p.part), rank(cluster_rank), size(cluster_size) {
         if (longest <= p.solo_most && p.solo_part > 0) {
             part = part * size + rank;
             parts *= size;
@@ -326,12 +333,28 @@ template <bool FULL, int VEC>
 __device__ __forceinline__ void decays(int form, float (&a)[VEC], float (&rest)[VEC]) {
     if (form & RECUR_SIGMOID) {
         sigmoid_pair<FULL, VEC>(a, rest);
-    } else {
+        return;
+    }
+    float g[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            if (form & RECUR_COMPLEMENT) rest[v] = -expm1f(a[v]);
-            a[v] = expf(a[v]);
+    for (int v = 0; v < VEC; ++v) g[v] = a[v], a[v] = expf(a[v]);
+    if (form & RECUR_COMPLEMENT) {
+        // 1 - exp(g) = -g (1 + g/2! + g^2/3! + ...) near 0, where the difference would cancel: eight terms leave
+        // 0.35^8 / 9! = 6e-10 of it
+        float q[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) q[v] = 1.f / 40320.f;
+        const float inverse[7] = {1.f / 5040.f, 1.f / 720.f, 1.f / 120.f, 1.f / 24.f, 1.f / 6.f, 0.5f, 1.f};
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {
+            float c[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) c[v] = inverse[k];
+            fma_to<VEC>(q, q, g, c);
         }
+        mul_to<VEC>(q, q, g);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) rest[v] = g[v] > -0.35f ? -q[v] : 1.f - a[v];
     }
 }
 
@@ -368,30 +391,36 @@ struct Source {
     static constexpr int ROWS = PIECES < 32 ? 32 / PIECES : 1;               // of one copy of the warp
     static_assert(!CODES || R * VEC <= 32, "one scale to a lane");
     unsigned char *ring;
-    const S *base, *from;       // from: the lane's first piece of the next tile
-    int64_t ld, step;           // pitch; from one tile of the warp to its next
-    int own_row, own_col;       // of the lane's pieces
+    const S *base;
+    const char *from;           // the lane's first piece of the next tile
+    int64_t ld, step, down;     // pitch; bytes from one tile of the warp to its next, and between the rows of two copies
+    uint32_t to;                // the lane's place in the ring
+    int own_row;
+    bool own;                   // whether the lane has a piece: its row and column are there
     raw_t<S, VEC> raw[PIECE == 0 ? R : 1];
     unsigned exponent = 0;      // codes: of row lane / VEC, block lane % VEC of the warp's columns
 
     // the warp's tiles begin at row0 and are `rows` apart
-    __device__ __forceinline__ void open(unsigned char *at, const void *tensor, int64_t pitch, int row0, int rows, int slab, int lane) {
+    __device__ __forceinline__ void open(unsigned char *at, const void *tensor, int64_t pitch, int row0, int rows, int D, int slab,
+                                         int lane) {
         ring = at;
         base = static_cast<const S *>(tensor);
         ld = pitch;
-        step = rows * ld;
+        step = rows * ld * int(sizeof(S));
+        down = ROWS * ld * int(sizeof(S));
+        to = smem_u32(ring) + lane * PIECE;
         own_row = PIECE == 0 ? 0 : lane / PIECES;
-        own_col = slab + (PIECE == 0 ? lane * VEC : lane % PIECES * (PIECE / int(sizeof(S))));
-        from = base + int64_t(row0 + own_row) * ld + own_col;
+        const int col = slab + (PIECE == 0 ? lane * VEC : lane % PIECES * (PIECE / int(sizeof(S))));
+        own = col < D && own_row < R;
+        from = reinterpret_cast<const char *>(base + int64_t(row0 + own_row) * ld + col);
     }
     // A tile's rows row0 .. row0 + R take two steps: load() when the tile before it is put(), and put() into its place of
     // the ring.  Rows without their bit in `live` read as zeros.
     __device__ __forceinline__ void load(const uint8_t *exps, int row0, unsigned live, int D, int slab, int lane) {
         if constexpr (PIECE == 0) {
-            const S *s = base + int64_t(row0) * ld + own_col;
+            const S *s = base + int64_t(row0) * ld + slab + lane * VEC;
 #pragma unroll
-            for (int j = 0; j < R; ++j)
-                raw[j] = own_col < D && (live >> j & 1u) ? load_once<S, VEC>(s + j * ld) : raw_t<S, VEC>{};
+            for (int j = 0; j < R; ++j) raw[j] = own && (live >> j & 1u) ? load_once<S, VEC>(s + j * ld) : raw_t<S, VEC>{};
         }
         if constexpr (CODES) {
             // 32 VEC columns are VEC blocks of 32; the block's first column is a multiple of 32
@@ -399,30 +428,32 @@ struct Source {
             exponent = j < R && block < blocks && (live >> j & 1u) ? exps[int64_t(row0 + j) * blocks + block] : 0u;
         }
     }
-    __device__ __forceinline__ static void copy(uint32_t to, const S *from, int bytes) {
+    __device__ __forceinline__ static void copy(uint32_t at, const void *source, int bytes) {
         if constexpr (PIECE == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(source), "r"(bytes) : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(source), "r"(bytes) : "memory");
     }
-    __device__ __forceinline__ void put(unsigned live, int D, int lane, int place) {
+    // BRANCH: whole tiles apart, which is quicker where the copies are all that a warp has to do at the time.
+    template <bool BRANCH>
+    __device__ __forceinline__ void put(unsigned live, int lane, int place) {
         if constexpr (PIECE == 0) {
 #pragma unroll
             for (int j = 0; j < R; ++j)
                 *reinterpret_cast<raw_t<S, VEC> *>(ring + place * BYTES + j * ROW + lane * VEC * int(sizeof(S))) = raw[j];
         } else {
-            const uint32_t to = smem_u32(ring) + place * BYTES + lane * PIECE;
             constexpr int COPIES = (R + ROWS - 1) / ROWS;
-            const S *s = from;
-            if (R < ROWS && own_row >= R) {
-            } else if (live == (1u << R) - 1u && own_col < D) {
+            const uint32_t at = to + place * BYTES;
+            const char *s = from;
+            const unsigned have = own ? live >> own_row : 0u;
+            if (BRANCH && live == (1u << R) - 1u && own) {
 #pragma unroll
-                for (int i = 0; i < COPIES; ++i, s += ROWS * ld) copy(to + i * ROWS * ROW, s, PIECE);
+                for (int i = 0; i < COPIES; ++i, s += down) copy(at + i * ROWS * ROW, s, PIECE);
             } else {
 #pragma unroll
-                for (int i = 0; i < COPIES; ++i, s += ROWS * ld) {
-                    const bool ok = own_col < D && (live >> (own_row + i * ROWS) & 1u);
-                    copy(to + i * ROWS * ROW, ok ? s : base, ok ? PIECE : 0);
+                for (int i = 0; i < COPIES; ++i, s += down) {
+                    const bool ok = have >> (i * ROWS) & 1u;
+                    if (R >= ROWS || own_row < R) copy(at + i * ROWS * ROW, ok ? s : reinterpret_cast<const char *>(base), ok ? PIECE : 0);
                 }
             }
             from += step;
@@ -679,13 +710,13 @@ __device__ __forceinline__ void walk(const RecurParams &p, const int form, int p
     const int tile0 = begin / R, tiles = end > begin ? (end - 1) / R + 1 - tile0 : 0;
     typename Shape::X xs;
     typename Shape::S gs;
-    xs.open(ring, p.x, p.ldx, tile0 * R, R, slab, lane);
-    gs.open(ring + xs.BYTES_RING, p.g, p.ldg, tile0 * R, R, slab, lane);
+    xs.open(ring, p.x, p.ldx, tile0 * R, R, p.D, slab, lane);
+    gs.open(ring + xs.BYTES_RING, p.g, p.ldg, tile0 * R, R, p.D, slab, lane);
     auto put = [&](int tile, int place) {
         if (tile < tiles) {
             const unsigned live = live_bits<R>((tile0 + tile) * R, begin, end);
-            xs.put(live, p.D, lane, place);
-            gs.put(live, p.D, lane, place);
+            xs.template put<true>(live, lane, place);
+            gs.template put<true>(live, lane, place);
         }
         tile_sent();
     };
@@ -739,8 +770,7 @@ __device__ __forceinline__ void walk(const RecurParams &p, const int form, int p
 template <typename T, typename G, int VEC>
 __device__ __forceinline__ void walk_all(const RecurParams &p, int form, unsigned char *shared, int warp, int warps, int lane) {
     const int slabs = (p.D + 32 * VEC - 1) / (32 * VEC), units = slabs * p.walk_parts;
-    const int blocks = int(gridDim.x * gridDim.y * gridDim.z);
-    const int block = int(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
+    const int blocks = int(gridDim.x), block = int(blockIdx.x);
     for (int u = warp * blocks + block; u < units; u += warps * blocks)
         walk<T, G, VEC>(p, form, u / slabs, u % slabs * 32 * VEC, shared + warp * WalkShape<T, G, VEC>::WARP, lane);
 }
@@ -759,7 +789,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     typename Shape::Cluster cluster;
     cluster.maps = reinterpret_cast<float *>(shared + W * Shape::WARP + Shape::Warps::BYTES);
     cluster.bar = reinterpret_cast<uint64_t *>(cluster.maps + 2 * all * cluster.ROW);
-    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC;
+    const int slab = int(blockIdx.x) / all % p.slabs * 32 * VEC, col = slab + lane * VEC;
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D;
     pdl_wait();
@@ -773,6 +803,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
         }
     }
     const Place at(p, cluster_rank(), all, longest);
+    if (at.part >= at.parts) return;                        // the whole cluster
     const int rank = at.rank, size = at.size;
     int begin, end;
     part_rows(p, at.part, at.parts, at.length, lane, begin, end);
@@ -797,8 +828,8 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     typename Shape::X xs;
     typename Shape::S gs;
     auto first_row = [&](int turn) { return (tile0 + turn * size + rank) * TILE + warp * R; };
-    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), size * TILE, slab, lane);
-    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), size * TILE, slab, lane);
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), size * TILE, p.D, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), size * TILE, p.D, slab, lane);
     auto live_of = [&](int turn) { return turn < turns ? live_bits<R>(first_row(turn), begin, end) : 0u; };
     auto load = [&](int turn) {
         if (PIECE != 0) return;
@@ -808,8 +839,8 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     auto put = [&](int turn, int place) {
         if (turn < turns) {
             const unsigned live = live_of(turn);
-            xs.put(live, p.D, lane, place);
-            gs.put(live, p.D, lane, place);
+            xs.template put<true>(live, lane, place);
+            gs.template put<true>(live, lane, place);
         }
         tile_sent();
     };
@@ -929,7 +960,7 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     typename Shape::Cluster cluster;
     cluster.maps = back.maps + Shape::Back::BYTES / int(sizeof(float));
     cluster.bar = reinterpret_cast<uint64_t *>(cluster.maps + 2 * all * cluster.ROW);
-    const int slab = int(blockIdx.y) * 32 * VEC, col = slab + lane * VEC;
+    const int slab = int(blockIdx.x) / all % p.slabs * 32 * VEC, col = slab + lane * VEC;
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D, complement = form & RECUR_COMPLEMENT;
     pdl_wait();
@@ -945,9 +976,9 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     // tiles from the last one back; those before the part's first have no live rows
     auto tile_of = [&](int turn) { return tile0 + tiles - 1 - (turn * size + rank); };
     auto first_row = [&](int turn) { return tile_of(turn) * TILE + warp * R; };
-    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), -size * TILE, slab, lane);
-    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), -size * TILE, slab, lane);
-    ds.open(gs.ring + gs.BYTES_RING, p.dy, p.lddy, first_row(0), -size * TILE, slab, lane);
+    xs.open(shared + warp * Shape::WARP, p.x, p.ldx, first_row(0), -size * TILE, p.D, slab, lane);
+    gs.open(xs.ring + xs.BYTES_RING, p.g, p.ldg, first_row(0), -size * TILE, p.D, slab, lane);
+    ds.open(gs.ring + gs.BYTES_RING, p.dy, p.lddy, first_row(0), -size * TILE, p.D, slab, lane);
     auto live_of = [&](int turn) {
         return turn < turns && tile_of(turn) >= tile0 ? live_bits<R>(first_row(turn), begin, end) : 0u;
     };
@@ -962,9 +993,9 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     auto put = [&](int turn, int place) {
         if (turn < turns) {
             const unsigned live = live_of(turn);
-            xs.put(live, p.D, lane, place);
-            gs.put(live, p.D, lane, place);
-            ds.put(live, p.D, lane, place);
+            xs.template put<false>(live, lane, place);
+            gs.template put<false>(live, lane, place);
+            ds.template put<false>(live, lane, place);
         }
         tile_sent();
     };

@@ -77,7 +77,7 @@ cudaError_t launch_recur(RecurParams &p, const RecurLaunch &l, cudaStream_t stre
     const RecurGrid g = recur_grid(p, room, Shape::COLUMNS, Shape::TILE, l.walk_wide);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    recur_config(cfg, attr, g.cluster, dim3(g.cluster, g.slabs, g.parts), Shape::THREADS, Shape::bytes(int(g.cluster)), stream);
+    recur_config(cfg, attr, g.cluster, dim3(g.cluster * g.clusters), Shape::THREADS, Shape::bytes(int(g.cluster)), stream);
     return cudaLaunchKernelEx(&cfg, FN, p);
 }
 

@@ -17,7 +17,7 @@ struct RecurRoom {
     int blocks[RECUR_CLUSTER + 1] = {0};
 };
 struct RecurGrid {
-    unsigned cluster, slabs, parts;
+    unsigned cluster, clusters;
 };
 // How the stream is cut for a kernel whose blocks take `columns` channels and `tile` rows at a time (kda_recur.cu).
 RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide);
