@@ -46,9 +46,9 @@ static bool walk_grid(RecurParams &p, int wide) {
 // The grid: as many blocks as run at once, by clusters that share the rows and, for what they leave, by parts of the stream.  A
 // cluster's size is the one that takes the fewest rounds of tiles, a round counting a sixth more where blocks
 // exchange and a block half a round for its beginning.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
-// blocks of a cluster share the rows.  Where the device sees that none is longer than three blocks' parts, they take parts
-// of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 153 us and
-// 212).
+// blocks of a cluster share the rows.  Where the device sees that they are alike, or none longer than half a block's
+// part, the blocks take parts of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192
+// channels, BF16: 153 us and 212).
 RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide) {
     const int64_t slabs = (p.D + columns - 1) / columns, T = p.T, seqs = p.cu == nullptr ? p.nseq : 1;
     p.slabs = int32_t(slabs);
@@ -86,7 +86,8 @@ RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int til
     if (size > 1 && p.nseq > 1 && p.nseq <= MOST_LOOKED_AT) {
         const int64_t alone = parts * size;
         p.solo_part = int32_t((T + alone - 1) / alone > 1 ? (T + alone - 1) / alone : 1);
-        p.solo_most = int32_t(3 * int64_t(p.solo_part) < INT32_MAX ? 3 * int64_t(p.solo_part) : INT32_MAX);
+        const int64_t alike = p.nseq % alone == 0 || p.nseq >= 4 * alone ? T / p.nseq + T / p.nseq / 8 : 0;
+        p.solo_most = int32_t(alike > p.solo_part / 2 ? alike : p.solo_part / 2);
     }
     p.parts = int32_t(parts);
     return {unsigned(size), unsigned(slabs * parts)};
