@@ -178,9 +178,73 @@ def test_long_sequences(kda, lens):
     c.check_backward(kda, label="long")
 
 
+def _many(n, longest, seed, zeros=0.1):
+    rng = np.random.default_rng(seed)
+    return [0 if rng.uniform() < zeros else int(rng.integers(1, longest + 1)) for _ in range(n)]
+
+
+# Enough sequences that single warps walk them (8 bytes of x to a lane, or 4), alike or not; and one so long beside them that
+# they are chained after all.
+@pytest.mark.parametrize("dtype, gdtype", [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16)])
+@pytest.mark.parametrize("D, lens", [(512, _many(400, 12, 1)), (256, _many(300, 20, 2)), (136, [9] * 470), (512, [1] * 300 + [64] + [0] * 5),
+                                     (512, [2] * 200 + [1500] + [3] * 250), (1024, _many(240, 9, 3, 0.5))], ids=lambda v: str(v)[:12])
+def test_many_sequences(kda, dtype, gdtype, D, lens):
+    for gate, complement in (("sigmoid", True), ("log", False), ("log", True)):
+        c = Case(lens, D, dtype, gdtype, gate, complement, seed=D)
+        c.check(kda, f"{D}")
+    c.check_backward(kda, label=f"{D}")
+
+
+@pytest.mark.parametrize("B, T, D", [(230, 9, 512), (460, 3, 256), (920, 2, 64), (40, 65, 2000), (2, 700, 64), (3, 1, 4096)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dense_batches_of_whole_pieces(kda, B, T, D, dtype):
+    c = Case([T] * B, D, dtype, packed=False, gate="sigmoid", complement=True, seed=B)
+    c.check(kda, f"{B}x{T}x{D}")
+    c.check_backward(kda, label=f"{B}x{T}x{D}")
+
+
+# One sequence, or a few of any lengths, that the blocks of a cluster share tile by tile; parts of their own where they are alike.
+@pytest.mark.parametrize("lens", [[9000], [3000, 1, 0, 2500, 700], [512] * 16, [64] * 90, [40] * 300, [1] * 70 + [4000]], ids=lambda v: str(v)[:14])
+@pytest.mark.parametrize("dtype, gdtype", [(F32, F32), (BF16, BF16), (F16, F32)])
+def test_clusters(kda, lens, dtype, gdtype):
+    for D, gate, complement in ((64, "sigmoid", True), (72, "log", False)):
+        c = Case(lens, D, dtype, gdtype, gate, complement, seed=len(lens))
+        c.check(kda, f"{D}")
+        c.check_backward(kda, label=f"{D}")
+    c = Case(lens, 96, dtype, gdtype, "sigmoid", False, seed=5)
+    c.check_backward(kda, True, True, dg=torch.empty(c.dy.shape, dtype=gdtype, device=DEV), label="codes")
+
+
+def test_offsets_past_32_bits(kda):
+    """More than 2^31 elements: the last rows and channels are those of a narrower tensor."""
+    T, D, keep = 33000, 65600, 64
+    x = torch.empty(1, T, D, dtype=BF16, device=DEV)
+    g = torch.empty_like(x)
+    small = [torch.randn(1, T, keep, device=DEV).to(BF16), (torch.randn(1, T, keep, device=DEV) + 2).to(BF16)]
+    for big, part in zip((x, g), small):
+        big.zero_()
+        big[..., -keep:] = part
+    form = {"gate": "sigmoid", "complement": True}
+    chunks = torch.empty(kda.gated_scan_chunks(1, T), D, device=DEV)
+    few = torch.empty(kda.gated_scan_chunks(1, T), keep, device=DEV)
+    y, final = kda.gated_scan(x, g, chunk_states=chunks, **form)
+    want, end = kda.gated_scan(*small, chunk_states=few, **form)
+    # the same chains cut differently: both within the bound of the exact one, whose size is at most the values'
+    assert torch.allclose(chunks[:, -keep:], few, rtol=1e-4, atol=1e-5) and torch.allclose(final[:, -keep:], end, rtol=1e-4, atol=1e-5)
+    assert float((y[..., -keep:].float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max())
+    sx = kda.checkpoint_save(x)
+    assert torch.equal(sx.codes[..., -keep:], kda.checkpoint_save(small[0]).codes)
+    assert torch.equal(kda.checkpoint_load(sx, BF16)[..., -keep:], kda.checkpoint_load(kda.checkpoint_save(small[0]), BF16))
+    dx, dg, _ = kda.gated_scan_backward(y, sx, g, chunks, **form)
+    wx, wg, _ = kda.gated_scan_backward(want, kda.checkpoint_save(small[0]), small[1], few, **form)
+    for a, b in ((dx, wx), (dg, wg)):
+        # inputs that differ by roundings of y, results by theirs: a few of 2^-8
+        assert float((a[..., -keep:].float() - b.float()).abs().max()) <= 2.0 ** -6 * float(b.float().abs().max())
+
+
 @pytest.mark.parametrize("save_x, save_g", [(True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("dtype, gdtype", [(F32, F32), (BF16, BF16), (F16, F32)])
-@pytest.mark.parametrize("D", [31, 32, 33, 64, 98, 130])
+@pytest.mark.parametrize("D", [31, 32, 33, 64, 98, 130, 240])
 def test_gradients_from_checkpoints(kda, save_x, save_g, dtype, gdtype, D):
     c = Case([5, 0, 130, 64], D, dtype, gdtype, "sigmoid", True, seed=D)
     c.check_backward(kda, save_x, save_g, dg=torch.empty(c.dy.shape, dtype=gdtype, device=DEV))
