@@ -624,3 +624,82 @@ def test_a_training_block_against_autograd(kda):
     for name, a, b in (("out", got, out), ("dx", dx, want[0]), ("dg", dg, want[1]), ("dz", dz, want[2]), ("dw", dw, want[3])):
         a, b = f64(a).ravel(), b.detach().numpy().ravel()
         assert np.linalg.norm(a - b) <= 2.0 ** -15 * np.linalg.norm(b), name
+
+
+def test_python_refusals(kda):
+    def t(*shape, dtype=BF16):
+        return torch.zeros(*shape, dtype=dtype, device=DEV)
+
+    x, g, st, ch = t(2, 5, 8), t(2, 5, 8), t(2, 8, dtype=F32), t(1, 8, dtype=F32)
+    i32, w = torch.zeros(3, dtype=torch.int32, device=DEV), t(8)
+    bad = [
+        lambda: kda.gated_scan(x[0], g[0]), lambda: kda.gated_scan(x, g[:, :4]), lambda: kda.gated_scan(x, g.half()),
+        lambda: kda.gated_scan(x.double(), g.double()), lambda: kda.gated_scan(x, g, gate="tanh"),
+        lambda: kda.gated_scan(x, g, cu_seqlens=i32), lambda: kda.gated_scan(x[:1], g[:1], cu_seqlens=i32.long()),
+        lambda: kda.gated_scan(x[:1], g[:1], cu_seqlens=i32[:1]), lambda: kda.gated_scan(x, g, slots=i32[:2]),
+        lambda: kda.gated_scan(x, g, initial_state=st, slots=i32), lambda: kda.gated_scan(x, g, initial_state=st.half()),
+        lambda: kda.gated_scan(x, g, initial_state=st[:1]), lambda: kda.gated_scan(x, g, final_state=st[:, :4]),
+        lambda: kda.gated_scan(x, g, chunk_states=st), lambda: kda.gated_scan(x, g, out=x.float()),
+        lambda: kda.gated_scan(x, g, out=t(2, 5, 16)[..., ::2]), lambda: kda.gated_scan(x, g.cpu()),
+        lambda: kda.gated_scan(x.cpu(), g), lambda: kda.gated_scan(x, g, final_state=t(16, 2, dtype=F32).T[:2]),
+        lambda: kda.gated_scan_backward(x, x, g, st), lambda: kda.gated_scan_backward(x, x[:, :3], g, ch),
+        lambda: kda.gated_scan_backward(x, x.float(), g, ch), lambda: kda.gated_scan_backward(x, x, g.float(), ch, dg=g),
+        lambda: kda.gated_scan_backward(x, x, g, ch, dg=g.float()), lambda: kda.gated_scan_backward(x, x, g, ch, dx=g.half()),
+        lambda: kda.gated_scan_backward(x, kda.Checkpoint(t(2, 5, 8, dtype=torch.int8), t(2, 5, 2, dtype=torch.uint8)), g, ch),
+        lambda: kda.gated_scan_backward(x, kda.Checkpoint(t(2, 5, 8, dtype=torch.uint8), t(2, 5, 1, dtype=torch.uint8)), g, ch),
+        lambda: kda.gated_scan_backward(x, kda.Checkpoint(t(2, 5, 16, dtype=torch.int8)[..., :8], t(2, 5, 1, dtype=torch.uint8)), g, ch),
+        lambda: kda.gated_scan_backward(x, kda.Checkpoint(t(2, 5, 8, dtype=torch.int8).cpu(), t(2, 5, 1, dtype=torch.uint8)), g, ch),
+        lambda: kda.gated_scan_backward(x, x, g, ch, initial_state=st[:1]), lambda: kda.gated_scan_backward(x, x, g, ch, dfinal_state=st.half()),
+        lambda: kda.gated_step(x, g, st), lambda: kda.gated_step(x[0], g[0], st), lambda: kda.gated_step(x[0, :2], g[0, :2], st.half()),
+        lambda: kda.gated_step(x[0, :2], g[0, :2], st, slots=i32), lambda: kda.gated_step(x[0, :2], g[0, :3], st),
+        lambda: kda.checkpoint_save(x.double()), lambda: kda.checkpoint_save(t(0, 0)),
+        lambda: kda.checkpoint_save(x, out=kda.Checkpoint(t(2, 5, 8, dtype=torch.int8), t(2, 5, 2, dtype=torch.uint8))),
+        lambda: kda.checkpoint_load(kda.checkpoint_save(x), torch.float64),
+        lambda: kda.checkpoint_load(kda.checkpoint_save(x), BF16, out=x.float()),
+        lambda: kda.checkpoint_load(kda.Checkpoint(t(3, 8, dtype=torch.int8), t(2, 1, dtype=torch.uint8)), BF16),
+        lambda: kda.gated_norm_backward(x, x, g, w.float()), lambda: kda.gated_norm_backward(x, x, g, w[:4]),
+        lambda: kda.gated_norm_backward(x, x.float(), g, w), lambda: kda.gated_norm_backward(x, x, g[:1], w),
+        lambda: kda.gated_norm_backward(x, x, g, w, activation="tanh"), lambda: kda.gated_norm_backward(x, x, g, w, dweight=w),
+        lambda: kda.gated_norm_backward(x, x, g, w, workspace=t(9, 9, dtype=torch.uint8).T[:5]),
+        # a checkpoint of rows whose blocks are not those of the heads' rows
+        lambda: kda.gated_norm_backward(x, kda.checkpoint_save(x.view(2, 40)), g, w),
+    ]
+    for n, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {n} was not refused")
+    for call in (lambda: kda.gated_scan(x, g, out=x), lambda: kda.gated_scan(x, g, final_state=st, chunk_states=st[:1]),
+                 lambda: kda.gated_scan_backward(x, g, g, ch, dx=x), lambda: kda.gated_step(x[0, :2], g[0, :2], st, out=x[0, :2]),
+                 lambda: kda.gated_norm_backward(x, x, g, w, dx=x),
+                 lambda: kda.gated_norm_backward(x, x, g, w, workspace=t(4, dtype=torch.uint8))):
+        with pytest.raises(kda.KdaError):
+            call()
+    torch.cuda.synchronize()
+
+
+def test_two_streams_at_once(kda):
+    """Calls of every operator on two streams, with workspaces of their own, do not meet."""
+    cases = [Case([700, 33, 0, 250], 128, BF16, BF16, "sigmoid", True, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    data = [[c.gpu(t) for t in (c.x, c.g, c.dy, c.cu, c.state, c.dfinal)] for c in cases]
+    w = torch.ones(128, dtype=BF16, device=DEV)
+
+    def layer(d):
+        x, g, dy, cu, state, dfinal = d
+        chunks = torch.empty(kda.gated_scan_chunks(*x.shape[:2]), 128, device=DEV)
+        y, final = kda.gated_scan(x, g, cu, "sigmoid", True, initial_state=state, chunk_states=chunks)
+        sy, sx = kda.checkpoint_save(y), kda.checkpoint_save(x)
+        dh, dz, dw = kda.gated_norm_backward(dy, sy, g, w)
+        return [y, final, dz, dw, *kda.gated_scan_backward(dh, sx, g, chunks, cu, "sigmoid", True, initial_state=state,
+                                                           dfinal_state=dfinal)]
+
+    want = [layer(d) for d in data]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [None, None]
+        for n in (0, 1):
+            with torch.cuda.stream(streams[n]):
+                for _ in range(3):
+                    got[n] = layer(data[n])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for m in (0, 1) for a, b in zip(got[m], want[m]))
