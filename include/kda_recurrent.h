@@ -16,8 +16,8 @@
  * Sequences, packed or dense, are rows of one stream [rows, D]: row b T + t of the
  * dense layout is token t of batch row b.  Tensors are row-major with contiguous
  * rows; inputs may have a pitch (`ld..`, in elements, at least D) between rows,
- * outputs are contiguous.  Everything is aligned to its element size; channels go two to
- * a lane where D is even and all tensors allow vectors of two elements, which is faster.
+ * outputs are contiguous.  Everything is aligned to its element size.  Rows that are whole 16-byte
+ * pieces (addresses, pitches and D) take the quicker kernels.
  *
  *   x, y     [rows, D] of dtype
  *   g        [rows, D] of g_dtype: dtype or KDA_F32
@@ -26,11 +26,17 @@
  *            64 j of the stream, for a row that begins a sequence the state that the
  *            sequence starts from.
  *
- * Accuracy.  Decays, sums and states are FP32, decays within two units in the last
- * place; outputs are rounded to their type once.  Results do not depend on other
- * sequences, on other channels or on timing: repeated calls give the same bits.  A NaN or an
- * infinity reaches the later tokens of its channel and sequence (in the gradients also the
- * earlier ones), nothing else.
+ * Accuracy.  Decays, sums and states are FP32; outputs are rounded to their type once.  Decays are
+ * within two units in the last place, and 1 - a too, but for sigmoids of 16-bit arguments and of
+ * codes, where 1 - a (and a decay below 1/2) is within |g| 2^-24 + 2^-21 of itself, 0 below 2^-126, and a at least 2^-126:
+ * the argument's own rounding is 2^-12 |g| at best.  Results do not depend on the
+ * values of other sequences and channels, nor on timing: repeated calls give the same bits.  A
+ * NaN or an infinity reaches the later tokens of its channel and sequence (in the gradients also
+ * the earlier ones), nothing else.
+ *
+ * Capture.  A call can be captured into a graph after one of the same types, form (decay, complement) and alignment on
+ * the device, which sets the kernel's limits.  The blocks of a cluster wait on one another's messages for a second at
+ * most; a wait that runs out (it never should) is reported by kda_device_error().
  */
 #ifndef KDA_RECURRENT_H
 #define KDA_RECURRENT_H
@@ -162,7 +168,8 @@ KDA_API kda_status_t kda_checkpoint_load(const int8_t *codes, const uint8_t *exp
  *               their checkpoints.
  *   act         kda_act_t.
  *   dim, rows   as for kda_gated_norm.  With rows == 0, dweight is zeroed.
- *   workspace   device, 16-byte aligned, kda_gated_norm_backward_workspace_size() bytes; scratch.
+ *   workspace   device, 16-byte aligned, kda_gated_norm_backward_workspace_size() bytes; scratch.  Calls that may run at the
+ *               same time, replays of graphs among them, need workspaces of their own.
  * dx, dgate, dweight and the workspace must not overlap each other or anything that is read
  * (KDA_ERR_INVALID_ARGUMENT).
  *
