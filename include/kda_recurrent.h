@@ -123,7 +123,7 @@ KDA_API kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const
  *   slots       device int32 [N], or NULL: request n uses entry n, and num_slots is at
  *               least N.  A slot outside [0, num_slots) reads a state of zeros and stores
  *               nothing.  Two requests must not share a slot.
- *   N           N == 0 is a no-op.  N * ceil(D / 256) < 2^31, else KDA_ERR_UNSUPPORTED.
+ *   N           N == 0 is a no-op.  N * ceil(D / 256) < 2^30, else KDA_ERR_UNSUPPORTED.
  * y and state must not overlap each other or another tensor.
  */
 KDA_API kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, int64_t ldg, void *y, float *state,

@@ -17,7 +17,7 @@ namespace kda {
 constexpr int MOST_LOOKED_AT = 2048;
 
 // Whether and how single warps walk the sequences: where there are enough of them for all SMs.  16 x 512 rows of 8192
-// channels in BF16 take 63 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
+// channels in BF16 take 61 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
 // channels 70.  Packed sequences are walked where none is longer than three parts of the stream, which the device sees.
 static bool walk_grid(RecurParams &p, int wide) {
     constexpr int64_t WARPS = 152 * 6;
@@ -45,10 +45,10 @@ static bool walk_grid(RecurParams &p, int wide) {
 
 // The grid: as many blocks as run at once, by clusters that share the rows and, for what they leave, by parts of the stream.  A
 // cluster's size is the one that takes the fewest rounds of tiles, a round counting a sixth more where blocks
-// exchange and a block half a round for its beginning.  Clusters come first for packed sequences, whose lengths only the device knows: however they differ, the
-// blocks of a cluster share the rows.  Where the device sees that they are alike, or none longer than half a block's
-// part, the blocks take parts of their own all the same, which saves the exchange (gradients of 16 x 512 rows of 8192
-// channels, BF16: 153 us and 212).
+// exchange and a block half a round for its beginning.  Clusters come first for packed sequences, whose lengths only the
+// device knows: however they differ, the blocks of a cluster share the rows.  Where the device sees that they are
+// alike, or none longer than half a block's part, the blocks take parts of their own all the same, which saves the
+// exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 120 us, 158 by clusters of two).
 RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide) {
     const int64_t slabs = (p.D + columns - 1) / columns, T = p.T, seqs = p.cu == nullptr ? p.nseq : 1;
     p.slabs = int32_t(slabs);
@@ -100,8 +100,10 @@ namespace {
 using namespace kda;
 
 // ------------------------------------------------------------- decoding step
-// h <- a h + c x for one token of every request: a thread takes VEC channels of one request.  Bound
-// by the state's traffic, or by the launch for few requests.
+// h <- a h + c x for one token of every request: a thread takes two vectors of VEC channels of one request, all loaded before
+// the first is worked on.  Bound by the state's traffic.  In a graph, BF16, 256 and 1024 requests of 8192 channels: 6.2 and
+// 19.5 us (floors 4.3 and 17.3) with vectors of four, 6.5 and 20.4 by one vector to a thread, 9.1 and 34.0 by one of two
+// channels; 256 of 2305 in FP32 4.1 us, 5.3 by one channel to a thread.  One request takes the launch's 1.2 us.
 struct StepParams {
     const void *x, *g;
     int64_t ldx, ldg;
@@ -110,40 +112,59 @@ struct StepParams {
     const int32_t *slots;
     int32_t num_slots, D, form, blocks;                     // blocks to a request
 };
-constexpr int STEP_THREADS = 128;
+constexpr int STEP_THREADS = 128, STEP_TIMES = 2;
 
 template <typename T, typename G, int VEC>
 __global__ void __launch_bounds__(STEP_THREADS) kda_gated_step_kernel(const StepParams p) {
     const int n = int(blockIdx.x / unsigned(p.blocks));
-    const int col = (int(blockIdx.x % unsigned(p.blocks)) * STEP_THREADS + int(threadIdx.x)) * VEC;
+    const int col = (int(blockIdx.x % unsigned(p.blocks)) * STEP_TIMES * STEP_THREADS + int(threadIdx.x)) * VEC;
     pdl_launch_dependents();
     pdl_wait();
-    if (col >= p.D) return;
     int entry = n;
     if (p.slots != nullptr) {
         entry = p.slots[n];
         if (entry >= p.num_slots) entry = -1;
     }
-    float a[VEC], c[VEC], x[VEC], h[VEC] = {};
-    const raw_t<T, VEC> xr = load_once<T, VEC>(static_cast<const T *>(p.x) + n * p.ldx + col);
-    const raw_t<G, VEC> gr = load_once<G, VEC>(static_cast<const G *>(p.g) + n * p.ldg + col);
-    float *s = p.state + int64_t(entry) * p.D + col;
-    if (entry >= 0) widen<float, VEC>(*reinterpret_cast<const raw_t<float, VEC> *>(s), h);
-    widen<T, VEC>(xr, x);
-    widen<G, VEC>(gr, a);
-    decays<sizeof(G) == 4, VEC>(p.form, a, c);
-    if (p.form & RECUR_COMPLEMENT) mul_to<VEC>(x, x, c);
-    fma_to<VEC>(h, a, h, x);
-    if (entry >= 0) store_raw<float, VEC>(s, narrow<float, VEC>(h));
-    store_raw<T, VEC>(static_cast<T *>(p.y) + int64_t(n) * p.D + col, narrow<T, VEC>(h));
+    const T *const x = static_cast<const T *>(p.x) + n * p.ldx;
+    const G *const g = static_cast<const G *>(p.g) + n * p.ldg;
+    raw_t<T, VEC> xr[STEP_TIMES];
+    raw_t<G, VEC> gr[STEP_TIMES];
+    raw_t<float, VEC> hr[STEP_TIMES] = {};
+#pragma unroll
+    for (int i = 0; i < STEP_TIMES; ++i) {
+        const int c = col + i * STEP_THREADS * VEC;
+        if (c >= p.D) break;
+        xr[i] = load_once<T, VEC>(x + c);
+        gr[i] = load_once<G, VEC>(g + c);
+        if (entry >= 0) hr[i] = *reinterpret_cast<const raw_t<float, VEC> *>(p.state + int64_t(entry) * p.D + c);
+    }
+#pragma unroll
+    for (int i = 0; i < STEP_TIMES; ++i) {
+        const int c = col + i * STEP_THREADS * VEC;
+        if (c >= p.D) break;
+        float a[VEC], rest[VEC], b[VEC], h[VEC];
+        widen<float, VEC>(hr[i], h);
+        widen<T, VEC>(xr[i], b);
+        widen<G, VEC>(gr[i], a);
+        decays<sizeof(G) == 4, VEC>(p.form, a, rest);
+        if (p.form & RECUR_COMPLEMENT) mul_to<VEC>(b, b, rest);
+        fma_to<VEC>(h, a, h, b);
+        if (entry >= 0) store_raw<float, VEC>(p.state + int64_t(entry) * p.D + c, narrow<float, VEC>(h));
+        store_raw<T, VEC>(static_cast<T *>(p.y) + int64_t(n) * p.D + c, narrow<T, VEC>(h));
+    }
 }
 
+template <typename T, typename G, int VEC>
+cudaError_t launch_step_vec(StepParams p, int32_t N, cudaStream_t s) {
+    constexpr int COLUMNS = STEP_THREADS * STEP_TIMES * VEC;
+    p.blocks = (p.D + COLUMNS - 1) / COLUMNS;
+    return launch_pdl(true, kda_gated_step_kernel<T, G, VEC>, unsigned(N) * unsigned(p.blocks), STEP_THREADS, 0, s, p);
+}
 template <typename T, typename G>
-cudaError_t launch_step(StepParams p, int32_t N, int vec, cudaStream_t s) {
-    p.blocks = (p.D + STEP_THREADS * vec - 1) / (STEP_THREADS * vec);
-    const unsigned grid = unsigned(N) * unsigned(p.blocks);
-    return vec == 2 ? launch_pdl(true, kda_gated_step_kernel<T, G, 2>, grid, STEP_THREADS, 0, s, p)
-                    : launch_pdl(true, kda_gated_step_kernel<T, G, 1>, grid, STEP_THREADS, 0, s, p);
+cudaError_t launch_step(const StepParams &p, int32_t N, int vec, cudaStream_t s) {
+    return vec == 4   ? launch_step_vec<T, G, 4>(p, N, s)
+           : vec == 2 ? launch_step_vec<T, G, 2>(p, N, s)
+                      : launch_step_vec<T, G, 1>(p, N, s);
 }
 
 // ------------------------------------------------------------- checkpoints
@@ -514,7 +535,9 @@ kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, int64_t l
     if (any_meet(out, in)) return KDA_ERR_INVALID_ARGUMENT;
     const StepParams p{x, g, ldx, ldg, y, state, slots, num_slots, D, form_bits(decay, complement), 0};
     const RowTensor rowed[] = {{x, ldx, es}, {g, ldg, gs}, {y, D, es}, {state, D, 4}};
-    const int vec = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) ? 2 : 1;
+    const int vec = vectors_fit(rowed, D, [](size_t n) { return 4 * n; })   ? 4
+                    : vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) ? 2
+                                                                            : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == KDA_F32) e = launch_step<float, float>(p, N, vec, s);

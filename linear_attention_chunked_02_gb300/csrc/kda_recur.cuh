@@ -7,9 +7,9 @@
 // The sequences lie one after the other in a stream of rows.  A row maps the state before it to the
 // state after it, h -> A h + H, and so does any run of rows; a sequence's first row maps everything
 // to one state.  A cluster of blocks takes 32 lanes' channels of one part of the stream, tile after tile
-// in turn: each warp takes R consecutive rows of its block's tile into registers and works out their map; a
-// thread for each channel chains the maps of the block's warps, and those of the cluster's blocks, which
-// it sends and receives through their shared memory, to the state that every warp's rows start from; then
+// in turn: each warp takes R consecutive rows of its block's tile into registers and works out their map; the maps
+// of the block's warps, and of the cluster's blocks, which go from one's shared memory to the others', are chained (by
+// a warp of its own, in the gradients by a thread to a channel) to the state that every warp's rows start from; then
 // the warps walk their rows once more for the outputs.  So every input is read once, and one long
 // sequence of few channels still keeps many SMs busy.  The order of all sums is set by the shape alone.
 //
@@ -43,7 +43,7 @@ struct RecurParams {
     int32_t T;                  // dense: rows to a sequence; packed: all rows
     int32_t rows, D;
     int32_t form;
-    int32_t slabs, parts;       // clusters are numbered by columns, then by parts of the stream; those past them walk or idle
+    int32_t slabs, parts;       // clusters are numbered by columns, then by parts of the stream
     int32_t part;               // rows of the stream whose sequences a cluster takes (dense: a multiple of T)
     int32_t solo_part;          // packed: where no sequence is longer than solo_most, every block takes a part of this many
     int32_t solo_most;          // rows by itself, cluster or not (0: never)
@@ -673,7 +673,9 @@ struct Blocks {
 
 // ------------------------------------------------------------------ forward
 // Many sequences of like lengths: one warp walks the rows of a part alone, nothing is chained, and every row is looked at
-// once.  The warps of all blocks share the parts and columns.
+// once.  The warps of all blocks share the parts and columns.  Bound by HBM: 16 x 512 rows of 8192 channels, BF16, in 61 us,
+// 360 MB at 74 % of the DRAM's peak (floor 59).  The ring hides the latency of the loads, which 7 warps
+// to an SM would not.
 template <typename T, typename G, int VEC>
 struct WalkShape {
     static constexpr int R = 8, TILE_BYTES = 32 * VEC * R * int(sizeof(T) + sizeof(G)), RING = TILE_BYTES > 4096 ? 2 : 3;
@@ -777,6 +779,12 @@ __device__ __forceinline__ void walk_all(const RecurParams &p, int form, unsigne
 
 // FORM: RECUR_ bits, or -1 for those of the parameters.  W warps take the rows, one more chains their maps: it would
 // not find the registers in theirs.
+//
+// One sequence of 65536 rows of 2048 channels, BF16, chunk states kept: 175 us by 32 clusters of 8 (floor 120; 41 % of the issue
+// slots).  What bounds it is the exchange between the blocks of a cluster, one tile after the other: the same work
+// without it, by parts that are each a sequence, takes 145 us, and 131 by 9 parts, for which there is no room in
+// clusters.  Two tiles in the ring: 164 us for 16384 rows of 8192 channels, 170 with one.  16 rows to a warp are what the
+// registers of two blocks hold; half as many double the exchanges.
 template <typename T, typename G, int FORM, int VEC, int R, int W, int RING, int PIECE, int MIN>
 __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const __grid_constant__ RecurParams p) {
     constexpr int TILE = R * W;
@@ -944,12 +952,18 @@ struct GradShape {
 };
 
 // T: dy, dx; X, S: x and g, or int8_t for codes; G: dg.
+//
+// 16 x 512 rows of 8192 channels, BF16: 122 us (floor 100), 635 MB at 63 % of the DRAM's peak and 55 % of the issue slots, which
+// two blocks of 8 warps to an SM with a barrier twice to a tile do not use better.  One sequence of 16384 rows of 2048
+// channels from codes: 92 us (floor 40; 228 MB, 30 % and 48 %): a code takes more instructions than a BF16 value, and blocks
+// wait for one another as above; from tensors it takes 86.  Eight rows and two channels to a lane: with four channels and
+// four rows, one block to an SM, 16 x 512 takes 167 us (from codes 186, here 139).
 template <typename T, typename X, typename S, typename G, int FORM, int VEC, int R, int W, int RING, int PIECE, int MIN>
 __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(const __grid_constant__ RecurParams p) {
     constexpr int TILE = R * W;
     constexpr bool FULL = sizeof(S) == 4;
-    // Gradients of 16 x 512 x 8192 BF16: from tensors 141 us with one tile ahead, fetched at once, 133 with two, fetched
-    // behind the barrier; from codes 149 and 170.
+    // Gradients of 16 x 512 x 8192 BF16: from tensors 125 us with one tile ahead, fetched at once, 120 with two, fetched
+    // behind the barrier; from codes 139 and 155.
     constexpr bool LATE = RING > 1;
     static_assert(TILE == RECUR_CHUNK, "a tile is a chunk");
     using Shape = GradShape<T, X, S, VEC, R, W, RING, PIECE>;

@@ -444,6 +444,28 @@ def test_step(kda, dtype, gdtype, N, D):
         assert torch.equal(mine[others].cpu(), pool[others])
 
 
+@pytest.mark.parametrize("dtype, gdtype", [(F32, F32), (BF16, F32), (F16, F16)])
+@pytest.mark.parametrize("N, D", [(2, 127), (2, 254), (3, 258), (2, 512), (3, 516), (2, 1020), (5, 1028), (3, 2306), (2, 4100)])
+def test_step_widths(kda, dtype, gdtype, N, D):
+    """Widths at which a request's last block has one vector to a thread, part of one, or none for most; the same bits
+    from rows at other addresses, which go by smaller vectors."""
+    c = Case([1] * N, D, dtype, gdtype, "sigmoid" if D % 4 else "log", D % 4 == 2, seed=D)
+    wy, wf, _, by, bf, _ = c.want()
+    pool = torch.full((N + 1, D), 3.0, device=DEV)
+    pool[:N] = torch.from_numpy(c.start).to(F32)
+    x, g = c.gpu(c.x)[0], c.gpu(c.g)[0]
+    first = pool.clone()
+    y = kda.gated_step(x, g, first, **c.form)
+    near(y, wy, by, "step")
+    near(first[:N], wf, bf, "states")
+    assert (first[N] == 3.0).all()
+    for offset in (1, 2, 4):
+        wide = torch.zeros(N, D + 12, dtype=dtype, device=DEV)
+        wide[:, offset:offset + D] = x
+        again = pool.clone()
+        assert torch.equal(kda.gated_step(wide[:, offset:offset + D], g, again, **c.form), y) and torch.equal(again, first)
+
+
 def test_steps_go_on_from_a_scan(kda):
     """Prompts, then tokens one by one, as the same tokens in one scan."""
     lens, more, D = [70, 1, 33], 5, 66
