@@ -28,8 +28,8 @@ __global__ void __launch_bounds__(256) kda_norm_grad_sum_kernel(const float *par
     dweight[col] = sum;
 }
 
-// Blocks of the first kernel: two to an SM, all at once, or one to a row where there are fewer.  The grid, and with it the
-// order of dweight's sums, does not depend on alignment.
+// Blocks of the first kernel: two to an SM, or one to a row where there are fewer.  The workspace's size
+// follows from them, so that they do not depend on alignment.
 unsigned norm_grad_blocks(int64_t rows, int32_t dim) {
     const int64_t most = 152 * 2, each = dim <= 32 ? 8 : 1, need = (rows + each - 1) / each;
     return unsigned(need < most ? need : most);

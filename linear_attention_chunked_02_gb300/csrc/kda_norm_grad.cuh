@@ -4,10 +4,13 @@
 //
 //     dx = r (u - n mean(u n));   dgate = dy n w act'(gate);   dw = sum over rows of dy n s
 //
-// One pass: a row's x, gate and dy are loaded into registers, the sums of x^2 and of u x are
+// One pass: a row's x, gate and dy are loaded once, the next rows' on the way meanwhile, the sums of x^2 and of u x are
 // taken over its threads, and the row is finished from the registers.  dw is summed in
 // registers over the rows that a thread meets, then over a block, and the blocks' sums by a second kernel, all in
-// an order that the shape alone sets.
+// an order that the shape, the types and the alignment set.
+//
+// Bound by HBM for tensors (8192 x 64 rows of 128, BF16: 111 us, floor 99; 65536 x 512 FP32 110 and 99), for codes by
+// issue (107 us, floor 79; 65 % of the slots and 56 % of the DRAM's peak), for unaligned 16-bit rows by single-element loads.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -27,9 +30,6 @@ struct NormGradParams {
     int32_t dim, silu;
     float eps, inv_dim;
 };
-
-constexpr int NORM_GRAD_THREADS = 256;
-constexpr int NORM_GRAD_NARROW = 64;   // vectors of a row up to which its threads are a part of a warp
 
 // One vector of a row.
 template <typename S, int VEC>
@@ -63,119 +63,215 @@ __device__ __forceinline__ void act_pair(int silu, const float (&z)[VEC], float 
     }
 }
 
-// Narrow rows: `lanes` threads to a row (a power of two up to 32), NV vectors to a thread, three rows on their way to a
-// thread while a fourth is worked on.  8192 x 64 rows of 128, BF16, with one, two and three rows ahead: 132, 117 and 110 us
-// from tensors (floor 99), 123, 111 and 107 from codes (floor 80), which issue bounds.
-template <typename T, typename X, typename Z, int VEC, int NV>
-__global__ void __launch_bounds__(NORM_GRAD_THREADS, NV == 1 ? 2 : 1) kda_norm_grad_narrow_kernel(const NormGradParams p, const int lanes) {
-    constexpr int AHEAD = NV == 1 ? 3 : 1;
-    constexpr bool FULL = sizeof(Z) == 4;
-    __shared__ float part[NORM_GRAD_THREADS * VEC];
-    const int t = int(threadIdx.x) & (lanes - 1), groups = NORM_GRAD_THREADS / lanes, group = int(threadIdx.x) / lanes;
-    const int nvec = p.dim / VEC;
-    pdl_launch_dependents();
-    pdl_wait();
-    float w[NV][VEC], dw[NV][VEC];
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(uint32_t at, const void *source) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(source) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(source), "n"(BYTES) : "memory");
+}
+
+// One row operand of a thread: NV vectors a row, of type S, AHEAD rows on their way, to the thread's places in shared memory
+// with RING (a thread reads what it copied itself), else to registers.
+template <typename S, int VEC, int NV, int THREADS, int AHEAD, bool RING>
+struct NormSource {
+    static constexpr bool CODES = sizeof(S) == 1;
+    static constexpr int PIECE = VEC * int(sizeof(S)), ROW = THREADS * NV * PIECE, BYTES = RING ? AHEAD * ROW : 0;
+    unsigned char *ring;
+    const S *from;              // the thread's first vector of the next row to fetch
+    const uint8_t *exps;        // codes: the row's exponents
+    int64_t down, exps_down;    // elements from one row of the thread to its next
+    raw_t<S, VEC> raw[RING ? 1 : AHEAD][NV];
+    unsigned e[CODES ? AHEAD : 1][NV];
+
+    // the thread's rows begin at `row` and are `rows` apart; what it has no vector for reads as zeros
+    __device__ __forceinline__ void open(unsigned char *at, const void *base, const uint8_t *exponents, int64_t row, int64_t rows,
+                                         int dim, int first) {
+        ring = at + threadIdx.x * PIECE;
+        from = static_cast<const S *>(base) + row * dim + first * VEC;
+        down = rows * dim;
+        if constexpr (CODES) {
+            const int blocks = (dim + CKPT_BLOCK - 1) / CKPT_BLOCK;
+            exps = exponents + row * blocks;
+            exps_down = rows * blocks;
+        }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = i * lanes + t;
+        for (int k = 0; k < AHEAD; ++k) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) w[i][v] = dw[i][v] = 0.f;
-        if (j < nvec) widen<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(p.weight) + j * VEC), w[i]);
+            for (int i = 0; i < NV; ++i) {
+                if constexpr (RING) *reinterpret_cast<raw_t<S, VEC> *>(ring + k * ROW + i * (THREADS * PIECE)) = {};
+                else raw[k][i] = {};
+                if constexpr (CODES) e[k][i] = 0;
+            }
+        }
     }
-    struct Row {
-        Piece<X, VEC> x[NV];
-        Piece<Z, VEC> z[NV];
-        Piece<T, VEC> d[NV];
-    } next[AHEAD];
-    auto fetch = [&](Row &r, int64_t row) {
+    __device__ __forceinline__ void fetch(int k, bool live, int dim, int first, int lanes) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = i * lanes + t;
-            if (row >= p.rows || j >= nvec) continue;
-            r.x[i].fetch(p.x, p.xe, row, p.dim, j * VEC);
-            r.z[i].fetch(p.gate, p.ze, row, p.dim, j * VEC);
-            r.d[i].fetch(p.dy, nullptr, row, p.dim, j * VEC);
+            const int col = (first + i * lanes) * VEC;
+            if (!live || col >= dim) continue;
+            if constexpr (RING) copy_piece<PIECE>(smem_u32(ring) + k * ROW + i * (THREADS * PIECE), from + i * lanes * VEC);
+            else raw[k][i] = load_once<S, VEC>(from + i * lanes * VEC);
+            if constexpr (CODES) e[k][i] = exps[col / CKPT_BLOCK];
         }
-    };
+        from += down;
+        if constexpr (CODES) exps += exps_down;
+    }
+    __device__ __forceinline__ void value(int k, int i, float (&v)[VEC]) const {
+        raw_t<S, VEC> r;
+        if constexpr (RING) r = *reinterpret_cast<const raw_t<S, VEC> *>(ring + k * ROW + i * (THREADS * PIECE));
+        else r = raw[k][i];
+        if constexpr (CODES) code_values<VEC>(r, ckpt_scale(e[k][i]), v);
+        else widen<S, VEC>(r, v);
+    }
+};
+
+template <typename T, typename X, typename Z, int VEC, int NV, int THREADS, int REGS>
+struct NormShape {
+    static constexpr bool RING = REGS == 0;
+    static constexpr int ROW = THREADS * NV * VEC * int(sizeof(T) + sizeof(X) + sizeof(Z)), ROOM = THREADS * 400;
+    static constexpr int MOST = sizeof(X) == 1 || sizeof(Z) == 1 ? 2 : 4;   // exponents on their way are in registers
+    static constexpr int AHEAD = !RING ? REGS : ROOM / ROW > MOST ? MOST : ROOM / ROW > 2 ? ROOM / ROW : 2;
+    using Xs = NormSource<X, VEC, NV, THREADS, AHEAD, RING>;
+    using Zs = NormSource<Z, VEC, NV, THREADS, AHEAD, RING>;
+    using Ds = NormSource<T, VEC, NV, THREADS, AHEAD, RING>;
+    static constexpr int SUMS = THREADS * VEC * 4, BYTES = RING && AHEAD * ROW > SUMS ? AHEAD * ROW : SUMS;
+};
+
+// `lanes` threads to a row, a power of two up to 32 or whole warps, and NV vectors to a thread.  REGS: rows on their way in
+// registers, or 0 for a ring in shared memory.
+template <typename T, typename X, typename Z, int VEC, int NV, int THREADS, int REGS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) kda_norm_grad_kernel(const NormGradParams p, const int lanes) {
+    using Shape = NormShape<T, X, Z, VEC, NV, THREADS, REGS>;
+    constexpr int AHEAD = Shape::AHEAD;
+    constexpr bool FULL = sizeof(Z) == 4, RING = Shape::RING;
+    extern __shared__ __align__(16) unsigned char shared[];
+    __shared__ float2 part[2][THREADS / 32];
+    const int tid = int(threadIdx.x), groups = int(blockDim.x) / lanes, group = tid / lanes, t = tid - group * lanes;
+    const int lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
     // the same number of turns for all threads of a block: shuffles go over whole warps
     const int64_t step = int64_t(gridDim.x) * groups, first = int64_t(blockIdx.x) * groups;
+    typename Shape::Xs xs;
+    typename Shape::Zs zs;
+    typename Shape::Ds ds;
+    xs.open(shared, p.x, p.xe, first + group, step, p.dim, t);
+    zs.open(shared + xs.BYTES, p.gate, p.ze, first + group, step, p.dim, t);
+    ds.open(shared + xs.BYTES + zs.BYTES, p.dy, nullptr, first + group, step, p.dim, t);
+    auto fetch = [&](int64_t row, int k) {
+        const bool live = row < p.rows;
+        xs.fetch(k, live, p.dim, t, lanes);
+        zs.fetch(k, live, p.dim, t, lanes);
+        ds.fetch(k, live, p.dim, t, lanes);
+        if constexpr (RING) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) fetch(next[k], first + k * step + group);
+    for (int k = 0; k < AHEAD; ++k) fetch(first + k * step + group, k);
+    raw_t<T, VEC> w[NV];
+    float dw[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * lanes + t) * VEC;
+        w[i] = col < p.dim ? *reinterpret_cast<const raw_t<T, VEC> *>(static_cast<const T *>(p.weight) + col) : raw_t<T, VEC>{};
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) dw[i][v] = 0.f;
+    }
+    int buf = 0;
+    T *dx = static_cast<T *>(p.dx) + (first + group) * p.dim + t * VEC, *dgate = static_cast<T *>(p.dgate) + (first + group) * p.dim + t * VEC;
+    const int64_t down = step * p.dim;
+    auto work = [&](const int64_t row, const int k) {
+        // rows and columns that are not there read as zeros: their sums are none
+        float x[NV][VEC], q[NV][VEC], g[NV][VEC], ss = 0.f, ux = 0.f;   // q: dy s, g: dy w slope
+        if constexpr (RING) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float z[VEC], d[VEC], s[VEC], wv[VEC], sum[VEC];
+            xs.value(k, i, x[i]);
+            zs.value(k, i, z);
+            ds.value(k, i, d);
+            widen<T, VEC>(w[i], wv);
+            act_pair<FULL, VEC>(p.silu, z, s, g[i]);
+            mul_to<VEC>(q[i], d, s);
+            mul_to<VEC>(d, d, wv);
+            mul_to<VEC>(g[i], d, g[i]);
+            mul_to<VEC>(sum, x[i], x[i]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) ss += sum[v];
+            mul_to<VEC>(sum, q[i], wv);
+            mul_to<VEC>(sum, sum, x[i]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) ux += sum[v];
+        }
+        fetch(row + AHEAD * step, k);                       // this row's values are in registers
+        for (int o = (lanes < 32 ? lanes : 32) >> 1; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            ux += __shfl_xor_sync(0xffffffffu, ux, o);
+        }
+        if (lanes > 32) {
+            // two sets: the next row's sums go to the other
+            if (lane == 0) part[buf][warp] = make_float2(ss, ux);
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+            const int warps = lanes >> 5;
+            const float2 *of = &part[buf][group * warps];
+            ss = ux = 0.f;
+            buf ^= 1;
+            for (int i = 0; i < warps; ++i) ss += of[i].x, ux += of[i].y;
+        }
+        if (row >= p.rows) return;
+        const float r = rsqrtf(ss * p.inv_dim + p.eps), m = ux * p.inv_dim * r * r;   // mean(u n) n = m x
+        float rr[VEC], mm[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) rr[v] = r, mm[v] = -m;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * lanes + t) * VEC;
+            if (col >= p.dim) continue;
+            float n[VEC], u[VEC];
+            mul_to<VEC>(n, x[i], rr);
+            fma_to<VEC>(dw[i], q[i], n, dw[i]);
+            mul_to<VEC>(g[i], g[i], n);
+            widen<T, VEC>(w[i], u);
+            mul_to<VEC>(u, u, q[i]);
+            fma_to<VEC>(u, mm, x[i], u);
+            mul_to<VEC>(u, u, rr);
+            store_raw<T, VEC>(dx + i * lanes * VEC, narrow<T, VEC>(u));
+            store_raw<T, VEC>(dgate + i * lanes * VEC, narrow<T, VEC>(g[i]));
+        }
+    };
     for (int64_t base = first; base < p.rows; base += AHEAD * step) {
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int64_t row = base + k * step + group;
-            const bool live = row < p.rows;
-            float x[NV][VEC], u[NV][VEC], q[NV][VEC], g[NV][VEC], ss = 0.f, ux = 0.f;   // dy w s, dy s, dy w slope
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const bool have = live && i * lanes + t < nvec;
-                float z[VEC], d[VEC], s[VEC], sum[VEC];
-                if (have) {
-                    next[k].x[i].value(x[i]);
-                    next[k].z[i].value(z);
-                    next[k].d[i].value(d);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) x[i][v] = z[v] = d[v] = 0.f;
-                }
-                act_pair<FULL, VEC>(p.silu, z, s, g[i]);
-                mul_to<VEC>(q[i], d, s);
-                mul_to<VEC>(u[i], q[i], w[i]);
-                mul_to<VEC>(d, d, w[i]);
-                mul_to<VEC>(g[i], d, g[i]);
-                mul_to<VEC>(sum, x[i], x[i]);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) ss += sum[v];
-                mul_to<VEC>(sum, u[i], x[i]);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) ux += sum[v];
-            }
-            fetch(next[k], row + AHEAD * step);
-            for (int o = lanes >> 1; o > 0; o >>= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                ux += __shfl_xor_sync(0xffffffffu, ux, o);
-            }
-            const float r = rsqrtf(ss * p.inv_dim + p.eps), m = ux * p.inv_dim * r * r;   // mean(u n) n = m x
-            float rr[VEC], mm[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) rr[v] = r, mm[v] = -m;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = i * lanes + t;
-                if (!live || j >= nvec) continue;
-                float n[VEC];
-                mul_to<VEC>(n, x[i], rr);
-                fma_to<VEC>(dw[i], q[i], n, dw[i]);
-                mul_to<VEC>(g[i], g[i], n);
-                fma_to<VEC>(u[i], mm, x[i], u[i]);
-                mul_to<VEC>(u[i], u[i], rr);
-                store_raw<T, VEC>(static_cast<T *>(p.dx) + row * p.dim + j * VEC, narrow<T, VEC>(u[i]));
-                store_raw<T, VEC>(static_cast<T *>(p.dgate) + row * p.dim + j * VEC, narrow<T, VEC>(g[i]));
-            }
+            if (k > 0 && base + k * step >= p.rows) break;
+            work(base + k * step + group, k);
+            dx += down;
+            dgate += down;
         }
     }
+    if constexpr (RING) asm volatile("cp.async.wait_all;" ::: "memory");
     // the groups' sums, one set of vectors after another
+    float *const sums = reinterpret_cast<float *>(shared);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) part[threadIdx.x * VEC + v] = dw[i][v];
+        for (int v = 0; v < VEC; ++v) sums[tid * VEC + v] = dw[i][v];
         __syncthreads();
-        for (int c = threadIdx.x; c < lanes * VEC; c += NORM_GRAD_THREADS) {
+        for (int c = tid; c < lanes * VEC; c += int(blockDim.x)) {
             float sum = 0.f;
-            for (int gq = 0; gq < groups; ++gq) sum += part[gq * lanes * VEC + c];
+            for (int k = 0; k < groups; ++k) sum += sums[k * lanes * VEC + c];
             const int col = i * lanes * VEC + c;
             if (col < p.dim) p.partial[int64_t(blockIdx.x) * p.dim + col] = sum;
         }
     }
 }
 
-// Wide rows: one to a block, read once for the sums and once more (from the caches) for the results; dw in
-// shared memory, each thread adding to its own columns.
+// Rows that find no room in 512 threads' registers (over 8192 elements, unaligned over 4096): one to a block, read once for
+// the sums and once more (from the caches) for the results; dw in shared memory, each thread adding to its own columns.
+// 8192 x 16384 BF16: 384 us (floor 198).
+constexpr int NORM_GRAD_WIDE = 1024;
 template <typename T, typename X, typename Z, int VEC>
-__global__ void __launch_bounds__(1024) kda_norm_grad_wide_kernel(const NormGradParams p) {
+__global__ void __launch_bounds__(NORM_GRAD_WIDE) kda_norm_grad_wide_kernel(const NormGradParams p) {
     extern __shared__ float dw[];
     __shared__ float part[2][2][32];
     const int nvec = p.dim / VEC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;

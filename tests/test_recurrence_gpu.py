@@ -554,6 +554,31 @@ def test_norm_gradients(kda, dtype, rows, dim):
         near(got[2], dw, 2.0 ** -14 * sw, f"dweight {act} {save}")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows, dim", [(1300, 130), (1300, 264), (611, 257), (700, 768), (650, 1024), (620, 2048), (320, 2049),
+                                       (610, 2056), (500, 2304), (330, 4096), (306, 4097), (310, 4104), (305, 8192), (4, 8200)])
+def test_norm_gradients_of_rows_of_several_warps(kda, dtype, rows, dim):
+    """Teams of threads of every size, with more rows than teams; a NaN stays in its row, but for dweight."""
+    rng = np.random.default_rng(rows + dim)
+    x, z, dy = (torch.from_numpy(s * rng.standard_normal((rows, dim), np.float32)).to(dtype) for s in (0.3, 2.0, 1.0))
+    w = torch.from_numpy(1 + 0.1 * rng.standard_normal(dim)).to(dtype)
+    for act, saved in (("sigmoid", False), ("silu", True)):
+        gx, gz, wx, wz = x.to(DEV), z.to(DEV), f64(x), f64(z)
+        if saved:
+            gx, gz, wx, wz = kda.checkpoint_save(gx), kda.checkpoint_save(gz), ref.checkpoint(wx)[2], ref.checkpoint(wz)[2]
+        got = kda.gated_norm_backward(dy.to(DEV), gx, gz, w.to(DEV), eps=1e-5, activation=act)
+        dx, dz, dw, sx, sz, sw = ref.gated_norm_backward(f64(dy), wx, wz, f64(w), 1e-5, act)
+        near(got[0], dx, 2.0 ** -17 * sx, f"dx {act}")
+        near(got[1], dz, 2.0 ** -17 * sz, f"dgate {act}")
+        near(got[2], dw, 2.0 ** -14 * sw, f"dweight {act}")
+        bad = dy.to(DEV)
+        bad[rows // 2, dim - 1] = float("nan")
+        again = kda.gated_norm_backward(bad, gx, gz, w.to(DEV), eps=1e-5, activation=act)
+        others = [r for r in range(rows) if r != rows // 2]
+        assert all(torch.equal(a[others], b[others]) for a, b in zip(again[:2], got[:2]))
+        assert again[0][rows // 2].isnan().all() and again[2][dim - 1].isnan() and not again[2][:dim - 1].isnan().any()
+
+
 def test_norm_gradients_of_many_rows_and_heads(kda):
     """Heads' rows whose checkpoints were taken of whole tokens; layouts that need copies; no rows."""
     gen = torch.Generator(device=DEV).manual_seed(0)
