@@ -505,6 +505,27 @@ def test_checkpoints_are_exact(kda, dtype, rows, dim):
     assert torch.equal(again.codes, saved.codes) and torch.equal(again.exponents, saved.exponents)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows, dim", [(3, 255), (2, 256), (5, 257), (4, 289), (300, 515), (3, 1000), (2, 4100), (9000, 40)])
+def test_checkpoints_of_unaligned_rows(kda, dtype, rows, dim):
+    """Rows at odd addresses and of odd widths, into buffers whose neighbours stay as they are."""
+    rng = np.random.default_rng(dim)
+    x = torch.from_numpy(rng.standard_normal((rows, dim)) * 10.0 ** rng.uniform(-3, 3, (rows, dim))).to(dtype)
+    codes, exps, values = ref.checkpoint(f64(x))
+    wide = torch.zeros(rows, dim + 2, dtype=dtype, device=DEV)
+    wide[:, 1:dim + 1] = x.to(DEV)
+    blocks = -(-dim // 32)
+    cbox = torch.full((rows * dim + 2,), 99, dtype=torch.int8, device=DEV)
+    ebox = torch.full((rows * blocks + 2,), 99, dtype=torch.uint8, device=DEV)
+    saved = kda.Checkpoint(cbox[1:-1].view(rows, dim), ebox[1:-1].view(rows, blocks))
+    kda.checkpoint_save(wide[:, 1:dim + 1], out=saved)
+    assert (f64(saved.codes) == codes).all() and (f64(saved.exponents) == exps).all()
+    box = torch.full((rows * dim + 2,), 5.0, dtype=dtype, device=DEV)
+    kda.checkpoint_load(saved, dtype, out=box[1:-1].view(rows, dim))
+    assert (f64(box[1:-1]) == values.reshape(-1)).all()
+    assert all(b[0] == v and b[-1] == v for b, v in ((cbox, 99), (ebox, 99), (box, 5.0)))
+
+
 def test_checkpoints_of_special_values(kda):
     tiny = [2.0 ** -149, -(2.0 ** -140), 2.0 ** -127, 127 * 2.0 ** -127, 127.5 * 2.0 ** -127, 2.0 ** -126, 1e-38, 3e-36]
     large = [3.4e38, 2.0 ** 127, -3.4028235e38, 127 * 2.0 ** 120, 127.5 * 2.0 ** 120]
