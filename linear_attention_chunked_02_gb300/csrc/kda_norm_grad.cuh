@@ -10,7 +10,7 @@
 // an order that the shape, the types and the alignment set.
 //
 // Bound by HBM for tensors (8192 x 64 rows of 128, BF16: 111 us, floor 99; 65536 x 512 FP32 110 and 99), for codes by
-// issue (107 us, floor 79; 65 % of the slots and 56 % of the DRAM's peak), for unaligned 16-bit rows by single-element loads.
+// issue (107 us, floor 79; 64 % of the slots and 59 % of the DRAM's peak), for unaligned 16-bit rows by single-element loads.
 #pragma once
 
 #include <cuda_runtime.h>
