@@ -86,7 +86,7 @@ struct NormSource {
 
     // the thread's rows begin at `row` and are `rows` apart; what it has no vector for reads as zeros
     __device__ __forceinline__ void open(unsigned char *at, const void *base, const uint8_t *exponents, int64_t row, int64_t rows,
-                                         int dim, int first) {
+                                         int dim, int first, int lanes) {
         ring = at + threadIdx.x * PIECE;
         from = static_cast<const S *>(base) + row * dim + first * VEC;
         down = rows * dim;
@@ -99,8 +99,8 @@ struct NormSource {
         for (int k = 0; k < AHEAD; ++k) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if constexpr (RING) *reinterpret_cast<raw_t<S, VEC> *>(ring + k * ROW + i * (THREADS * PIECE)) = {};
-                else raw[k][i] = {};
+                if constexpr (!RING) raw[k][i] = {};
+                else if ((first + i * lanes) * VEC >= dim) *reinterpret_cast<raw_t<S, VEC> *>(ring + k * ROW + i * (THREADS * PIECE)) = {};
                 if constexpr (CODES) e[k][i] = 0;
             }
         }
@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kda_norm_grad_kernel(c
     typename Shape::Xs xs;
     typename Shape::Zs zs;
     typename Shape::Ds ds;
-    xs.open(shared, p.x, p.xe, first + group, step, p.dim, t);
-    zs.open(shared + xs.BYTES, p.gate, p.ze, first + group, step, p.dim, t);
-    ds.open(shared + xs.BYTES + zs.BYTES, p.dy, nullptr, first + group, step, p.dim, t);
+    xs.open(shared, p.x, p.xe, first + group, step, p.dim, t, lanes);
+    zs.open(shared + xs.BYTES, p.gate, p.ze, first + group, step, p.dim, t, lanes);
+    ds.open(shared + xs.BYTES + zs.BYTES, p.dy, nullptr, first + group, step, p.dim, t, lanes);
     auto fetch = [&](int64_t row, int k) {
         const bool live = row < p.rows;
         xs.fetch(k, live, p.dim, t, lanes);

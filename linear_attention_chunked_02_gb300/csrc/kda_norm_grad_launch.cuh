@@ -43,7 +43,8 @@ cudaError_t launch_norm_grad_vec(const NormGradParams &p, unsigned grid, cudaStr
             if (nvec <= 512) return launch_norm_grad_rows<T, X, Z, VEC, 1, 512, 3>(p, grid, s);
     }
     if constexpr (VEC > 1) {
-        if (nvec <= 256 * MORE) return launch_norm_grad_rows<T, X, Z, VEC, MORE, 256, 0>(p, grid, s);
+        if constexpr (!CODES || VEC < 8)
+            if (nvec <= 256 * MORE) return launch_norm_grad_rows<T, X, Z, VEC, MORE, 256, 0>(p, grid, s);
         if (nvec <= 512 * MORE) return launch_norm_grad_rows<T, X, Z, VEC, MORE, 512, 0>(p, grid, s);
     } else {
         if (nvec <= 256 * FEW) return launch_norm_grad_rows<T, X, Z, VEC, FEW, 256, 1>(p, grid, s);
