@@ -41,8 +41,6 @@ cudaError_t launch_norm_grad_vec(const NormGradParams &p, unsigned grid, cudaStr
         if (nvec <= 256) return launch_norm_grad_rows<T, X, Z, VEC, 1, 256, 3>(p, grid, s);
         if constexpr (CODES)
             if (nvec <= 512) return launch_norm_grad_rows<T, X, Z, VEC, 1, 512, 3>(p, grid, s);
-    }
-    if constexpr (VEC > 1) {
         if constexpr (!CODES || VEC < 8)
             if (nvec <= 256 * MORE) return launch_norm_grad_rows<T, X, Z, VEC, MORE, 256, 0>(p, grid, s);
         if (nvec <= 512 * MORE) return launch_norm_grad_rows<T, X, Z, VEC, MORE, 512, 0>(p, grid, s);
@@ -51,7 +49,7 @@ cudaError_t launch_norm_grad_vec(const NormGradParams &p, unsigned grid, cudaStr
         if (nvec <= 512 * FEW) return launch_norm_grad_rows<T, X, Z, VEC, FEW, 512, 1>(p, grid, s);
     }
     const size_t smem = size_t(p.dim) * 4;
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {                                 // beside what the kernel has of its own, 48 KB without asking
         const cudaError_t e = cudaFuncSetAttribute(kda_norm_grad_wide_kernel<T, X, Z, VEC>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;

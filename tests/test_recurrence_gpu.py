@@ -600,6 +600,20 @@ def test_norm_gradients_of_rows_of_several_warps(kda, dtype, rows, dim):
         assert again[0][rows // 2].isnan().all() and again[2][dim - 1].isnan() and not again[2][:dim - 1].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [10240, 12161, 12200, 12288, 12320])
+def test_norm_gradients_of_the_widest_rows(kda, dtype, dim):
+    """Widths whose sums of dweight fill what shared memory a kernel has without asking for more."""
+    rng = np.random.default_rng(dim)
+    x, z, dy = (torch.from_numpy(s * rng.standard_normal((3, dim), np.float32)).to(dtype) for s in (0.3, 2.0, 1.0))
+    w = torch.from_numpy(1 + 0.1 * rng.standard_normal(dim)).to(dtype)
+    got = kda.gated_norm_backward(dy.to(DEV), x.to(DEV), z.to(DEV), w.to(DEV), eps=1e-5)
+    dx, dz, dw, sx, sz, sw = ref.gated_norm_backward(f64(dy), f64(x), f64(z), f64(w), 1e-5, "sigmoid")
+    near(got[0], dx, 2.0 ** -17 * sx, "dx")
+    near(got[1], dz, 2.0 ** -17 * sz, "dgate")
+    near(got[2], dw, 2.0 ** -14 * sw, "dweight")
+
+
 def test_norm_gradients_of_many_rows_and_heads(kda):
     """Heads' rows whose checkpoints were taken of whole tokens; layouts that need copies; no rows."""
     gen = torch.Generator(device=DEV).manual_seed(0)
