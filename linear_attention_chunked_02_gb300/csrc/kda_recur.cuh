@@ -108,11 +108,17 @@ struct Near {
     int low = INT_MAX, high = INT_MIN;
 };
 
-// The longest of the packed sequences, by the whole warp.
-__device__ __forceinline__ int longest_of(const RecurParams &p, int lane) {
+// The longest of the packed sequences, by the whole block, whose threads all call this.
+__device__ __forceinline__ int longest_of(const RecurParams &p) {
+    __shared__ int most[32];
     int longest = 0;
-    for (int n = lane; n < p.nseq; n += 32) longest = max(longest, p.cu[n + 1] - p.cu[n]);
-    return __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll 4
+    for (int n = threadIdx.x; n < p.nseq; n += blockDim.x) longest = max(longest, p.cu[n + 1] - p.cu[n]);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = longest;
+    __syncthreads();
+    for (int w = 0; w < int(blockDim.x >> 5); ++w) longest = max(longest, most[w]);
+    return longest;
 }
 
 // A block's place: the part of the stream whose rows it shares with the other blocks of a cluster, or takes alone.
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__((W + 1) * 32, MIN) kda_gated_scan_kernel(const
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D;
     pdl_wait();
-    const int longest = p.cu != nullptr && (p.walk_parts > 0 || p.solo_part > 0) ? longest_of(p, lane) : 0;
+    const int longest = p.cu != nullptr && (p.walk_parts > 0 || p.solo_part > 0) ? longest_of(p) : 0;
     if constexpr (PIECE == 16) {
         if (p.walk_parts > 0 && longest <= p.walk_most) {   // the same for all blocks
             if (p.walk_wide) walk_all<T, G, Shape::WIDE>(p, form, shared, warp, W + 1, lane);
@@ -978,7 +984,7 @@ __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(co
     const int form = FORM < 0 ? p.form : FORM;
     const bool in = col < p.D, complement = form & RECUR_COMPLEMENT;
     pdl_wait();
-    const Place at(p, cluster_rank(), all, p.cu != nullptr && p.solo_part > 0 ? longest_of(p, lane) : 0);
+    const Place at(p, cluster_rank(), all, p.cu != nullptr && p.solo_part > 0 ? longest_of(p) : 0);
     const int rank = at.rank, size = at.size;
     int begin, end;
     part_rows(p, at.part, at.parts, at.length, lane, begin, end);

@@ -195,6 +195,16 @@ def test_many_sequences(kda, dtype, gdtype, D, lens):
     c.check_backward(kda, label=f"{D}")
 
 
+# So many sequences that a block looks through their lengths for long, or (past 65536) does not: walked, or chained for a long one
+# among them, by clusters or by parts alone.
+@pytest.mark.parametrize("D, lens", [(64, _many(2600, 3, 5)), (32, [1] * 33000), (16, _many(70000, 1, 6, 0.5)),
+                                     (64, [1] * 2500 + [1200] + [0] * 50 + [1] * 700), (40, [2] * 12000)], ids=lambda v: str(v)[:12])
+def test_very_many_sequences(kda, D, lens):
+    c = Case(lens, D, BF16, F32, "log", True, seed=D)
+    c.check(kda, f"{D}")
+    c.check_backward(kda, label=f"{D}")
+
+
 @pytest.mark.parametrize("B, T, D", [(230, 9, 512), (460, 3, 256), (920, 2, 64), (40, 65, 2000), (2, 700, 64), (3, 1, 4096)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_dense_batches_of_whole_pieces(kda, B, T, D, dtype):
