@@ -1,11 +1,16 @@
 """The argument checks of the gated linear recurrence, the checkpoints and the norm's gradients on a
-machine without a GPU: every refusal comes before any CUDA call, which would give KDA_ERR_CUDA here."""
+machine without a GPU: every refusal comes before any CUDA call, which would give KDA_ERR_CUDA here.
+
+The addresses are made up, and calls that nothing refuses go on to a launch.  Where there is a GPU that launch would
+read and write them, so none of these tests runs there."""
 import pytest
 import torch
 
 import linear_attention_chunked_02_gb300 as kda
 from linear_attention_chunked_02_gb300 import build as kbuild
 from linear_attention_chunked_02_gb300 import recurrence
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="a GPU is present: made-up addresses would be used")
 
 OK, INVALID, UNSUPPORTED, WORKSPACE, CUDA = 0, 1, 2, 3, 4
 P = [1 << (30 + i) for i in range(20)]                     # distinct, aligned, far apart
