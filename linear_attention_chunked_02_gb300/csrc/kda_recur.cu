@@ -21,10 +21,13 @@ constexpr int MOST_LOOKED_AT = 1 << 16, MOST_LOOKED_AT_OFTEN = 1 << 15;
 // Whether and how single warps walk the sequences: where there are enough of them for all SMs.  16 x 512 rows of 8192
 // channels in BF16 take 61 us by 1024 warps of 128 channels each, 97 chained; 8 sequences' 512 warps 83, 1024 of half the
 // channels 70.  Packed sequences are walked where none is longer than three parts of the stream, which the device sees.
-static bool walk_grid(RecurParams &p, int wide) {
+// A lane takes `wide` channels, or half as many where that makes too few warps or `fit` says that the outputs' and
+// states' addresses do not fit vectors of more.
+static bool walk_grid(RecurParams &p, int wide, int fit) {
     constexpr int64_t WARPS = 152 * 6;
     if (wide == 0 || p.rows == 0 || (p.cu != nullptr && p.nseq > MOST_LOOKED_AT)) return false;
     for (int vec = wide; vec >= wide / 2; vec -= wide / 2) {
+        if (vec > fit) continue;
         const int64_t slabs = (p.D + 32 * vec - 1) / (32 * vec);
         if (slabs * p.nseq < WARPS) continue;
         int64_t parts = 2 * WARPS / slabs > 1 ? 2 * WARPS / slabs : 1;
@@ -51,10 +54,10 @@ static bool walk_grid(RecurParams &p, int wide) {
 // device knows: however they differ, the blocks of a cluster share the rows.  Where the device sees that they are
 // alike, or none longer than half a block's part, the blocks take parts of their own all the same, which saves the
 // exchange (gradients of 16 x 512 rows of 8192 channels, BF16: 120 us, 158 by clusters of two).
-RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide) {
+RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide, int walk_fit) {
     const int64_t slabs = (p.D + columns - 1) / columns, T = p.T, seqs = p.cu == nullptr ? p.nseq : 1;
     p.slabs = int32_t(slabs);
-    if (walk_grid(p, walk_wide) && p.cu == nullptr) return {1, unsigned(room.blocks[1])};   // all warps of the blocks walk
+    if (walk_grid(p, walk_wide, walk_fit) && p.cu == nullptr) return {1, unsigned(room.blocks[1])};   // all warps of the blocks walk
     int64_t parts = 1, each = 1;
     int size = 1;
     double best = 0;
@@ -504,6 +507,7 @@ kda_status_t kda_gated_scan(const void *x, int64_t ldx, const void *g, int64_t l
     const RowTensor inputs[] = {rowed[0], rowed[1]};
     l.staged = vectors_fit(rowed, D, [](size_t n) { return 2 * n; }) && vectors_fit(inputs, D, [](size_t) { return size_t(16); });
     l.walk_wide = l.staged ? 8 / int(es) : 0;
+    l.walk_fit = vectors_fit(rowed, D, [](size_t n) { return 4 * n; }) ? 4 : 2;
     DeviceInfo info;
     if (cudaGetDevice(&l.device) != cudaSuccess || device_info(l.device, info) != cudaSuccess) return KDA_ERR_CUDA;
     p.err = info.err;

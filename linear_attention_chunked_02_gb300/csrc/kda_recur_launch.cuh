@@ -74,7 +74,7 @@ cudaError_t launch_recur(RecurParams &p, const RecurLaunch &l, cudaStream_t stre
     RecurRoom room;
     cudaError_t e = recur_room<FN, Shape>(l.device, room);
     if (e != cudaSuccess) return e;
-    const RecurGrid g = recur_grid(p, room, Shape::COLUMNS, Shape::TILE, l.walk_wide);
+    const RecurGrid g = recur_grid(p, room, Shape::COLUMNS, Shape::TILE, l.walk_wide, l.walk_fit);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     recur_config(cfg, attr, g.cluster, dim3(g.cluster * g.clusters), Shape::THREADS, Shape::bytes(int(g.cluster)), stream);

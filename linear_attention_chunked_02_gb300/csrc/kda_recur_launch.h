@@ -8,7 +8,8 @@ namespace kda {
 struct RecurLaunch {
     bool staged;                // the inputs' rows are whole, aligned 16-byte pieces
     bool wide_g, x8, g8;        // g and dg in FP32; codes in place of x and g
-    int walk_wide;              // forward, staged: channels to a lane of a walking warp at most; 0: no walks
+    int walk_wide;              // forward, staged: channels to a lane of a walking warp, or half as many; 0: no walks
+    int walk_fit;               // channels whose vectors fit the addresses of y, the states and the chunk states
     int device;
 };
 
@@ -20,7 +21,7 @@ struct RecurGrid {
     unsigned cluster, clusters;
 };
 // How the stream is cut for a kernel whose blocks take `columns` channels and `tile` rows at a time (kda_recur.cu).
-RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide);
+RecurGrid recur_grid(RecurParams &p, const RecurRoom &room, int columns, int tile, int walk_wide, int walk_fit);
 
 // Channels to a lane of the gradients of staged rows: two, or one where an operand is FP32, whose rows of 64 channels
 // would leave room for one block on an SM alone.
