@@ -55,6 +55,12 @@ __device__ __forceinline__ void act_pair(int silu, const float (&z)[VEC], float 
     for (int v = 0; v < VEC; ++v) s[v] = z[v], one[v] = 1.f;
     sigmoid_pair<FULL, VEC>(s, rest);
     if (silu) {
+        // the faster form goes no lower than 2^-126, at gates of -126 ln 2; the gate itself as a factor, as low as -3e38 for
+        // a mask, would bring that back to the size of 1
+        if constexpr (!FULL) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s[v] = z[v] < -87.33654f ? 0.f : s[v];
+        }
         fma_to<VEC>(slope, z, rest, one);
         mul_to<VEC>(slope, slope, s);
         mul_to<VEC>(s, s, z);
