@@ -119,7 +119,7 @@ KDA_API kda_status_t kda_gated_scan_backward(const void *dy, int64_t lddy, const
  * One token of each of N running requests; the states are updated in place.
  *
  *   x, g, y     as above with N rows.
- *   state       [num_slots, D].
+ *   state       [num_slots, D]; NULL where num_slots is 0.
  *   slots       device int32 [N], or NULL: request n uses entry n, and num_slots is at
  *               least N.  A slot outside [0, num_slots) reads a state of zeros and stores
  *               nothing.  Two requests must not share a slot.

@@ -579,7 +579,7 @@ kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, int64_t l
     if (int64_t(N) * ((D + 255) / 256) >= (int64_t(1) << 30)) return KDA_ERR_UNSUPPORTED;
     if (N == 0) return KDA_OK;
     const size_t es = size_t(elt_size(dtype)), gs = size_t(elt_size(g_dtype));
-    if (x == nullptr || g == nullptr || y == nullptr || state == nullptr || ldx < D || ldg < D)
+    if (x == nullptr || g == nullptr || y == nullptr || (state == nullptr && num_slots > 0) || ldx < D || ldg < D)
         return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned_to(x, es) || !aligned_to(g, gs) || !aligned_to(y, es) || !aligned_to(state, 4) || !aligned_to(slots, 4))
         return KDA_ERR_INVALID_ARGUMENT;
