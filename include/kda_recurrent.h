@@ -137,7 +137,7 @@ KDA_API kda_status_t kda_gated_step(const void *x, int64_t ldx, const void *g, i
  *
  *     code = x / 2^e rounded to the nearest integer (ties to even),   x ~ code * 2^e
  *
- * so that the error is at most 2^(e-1), 1 / 127 of the block's largest magnitude.  (A code whose value
+ * so that the error is at most 2^(e-1): 1 / 127 of the block's largest magnitude, or 2^-128 where e is -127.  (A code whose value
  * would pass the type's largest is rounded towards zero: 63 in place of 64 where x is within
  * 1 / 128 of it.)  The scale is a
  * power of two: codes are exact whatever arithmetic computes them, and the values that they stand

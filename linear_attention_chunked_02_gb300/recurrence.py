@@ -284,8 +284,9 @@ def gated_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, slots: Opt
 
 def checkpoint_save(x: torch.Tensor, out: Optional[Checkpoint] = None,
                     stream: Optional[torch.cuda.Stream] = None) -> Checkpoint:
-    """x [.., dim] in 8 bits, a power-of-two scale to 32 elements of a row; each value within 2 ** -7 of the
-    largest of its 32.  A block with a NaN or an infinity reads back as NaN."""
+    """x [.., dim] in 8 bits, a power-of-two scale to 32 elements of a row; each value within 1 / 127 of the
+    largest of its 32, or 2 ** -128 if that is more; 1 / 64 where the largest is so near its type's own that its
+    code is cut.  A block with a NaN or an infinity reads back as NaN."""
     device = _on_gpu("x codes exponents", x, *(out if out is not None else ()))
     other = _elsewhere(device, stream)
     if other is not None:
