@@ -8,7 +8,7 @@ LARGEST = float(np.finfo(np.float32).max)
 
 
 # just above 63.5 steps, which rounds by half a step; the type's largest value, 64 steps less 2^-18, whose code is cut to 63
-@pytest.mark.parametrize("largest, bound", [(63.5 + 2.0 ** -10, 127), (LARGEST, 64)])
+@pytest.mark.parametrize("largest, bound", [(63.5 + 2.0 ** -14, 127), (LARGEST, 64)])
 def test_the_bounds_are_met(largest, bound):
     x = np.zeros((1, 32))
     x[0, 0] = largest
