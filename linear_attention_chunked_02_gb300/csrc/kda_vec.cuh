@@ -32,11 +32,9 @@ __device__ __forceinline__ void store_raw(S *p, raw_t<S, N> v) {
 __device__ __forceinline__ float widen_one(float v) { return v; }
 __device__ __forceinline__ float widen_one(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float widen_one(__half v) { return __half2float(v); }
-__device__ __forceinline__ float widen_one(int8_t v) { return float(v); }
 __device__ __forceinline__ void narrow_one(float &to, float v) { to = v; }
 __device__ __forceinline__ void narrow_one(__nv_bfloat16 &to, float v) { to = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void narrow_one(__half &to, float v) { to = __float2half_rn(v); }
-__device__ __forceinline__ void narrow_one(int8_t &to, float v) { to = int8_t(__float2int_rn(v)); }
 
 template <typename S, int N>
 __device__ __forceinline__ void widen(raw_t<S, N> raw, float (&v)[N]) {
