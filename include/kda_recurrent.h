@@ -174,7 +174,7 @@ KDA_API kda_status_t kda_checkpoint_load(const int8_t *codes, const uint8_t *exp
  * (KDA_ERR_INVALID_ARGUMENT).
  *
  * Sums are FP32, dweight's in an order that depends on shapes, types and alignment alone.  act and act' of 16-bit gates and of
- * codes have the recurrence's accuracy for such sigmoids; SiLU's are 0 for gates below -126 ln 2.  Two launches.
+ * codes have the recurrence's accuracy for such sigmoids, but are 0 for gates below -126 ln 2.  Two launches.
  */
 KDA_API size_t kda_gated_norm_backward_workspace_size(int64_t rows, int32_t dim);
 KDA_API kda_status_t kda_gated_norm_backward(const void *dy, const void *x, const uint8_t *x_exponents,

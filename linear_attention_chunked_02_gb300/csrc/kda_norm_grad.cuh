@@ -47,20 +47,15 @@ struct Piece {
     }
 };
 
-// act(z) and its slope; the sigmoid's faster form for 16-bit gates and codes, as in the recurrence.
+// act(z) and its slope; the sigmoid's faster form for 16-bit gates and codes, as in the recurrence, but 0 below 2^-126, at gates
+// under -126 ln 2: SiLU's factor z, as low as -3e38 for a mask, would bring 2^-126 back to the size of 1.
 template <bool FULL, int VEC>
 __device__ __forceinline__ void act_pair(int silu, const float (&z)[VEC], float (&s)[VEC], float (&slope)[VEC]) {
     float rest[VEC], one[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) s[v] = z[v], one[v] = 1.f;
-    sigmoid_pair<FULL, VEC>(s, rest);
+    sigmoid_pair<FULL, VEC, true>(s, rest);
     if (silu) {
-        // the faster form goes no lower than 2^-126, at gates of -126 ln 2; the gate itself as a factor, as low as -3e38 for
-        // a mask, would bring that back to the size of 1
-        if constexpr (!FULL) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v] = z[v] < -87.33654f ? 0.f : s[v];
-        }
         fma_to<VEC>(slope, z, rest, one);
         mul_to<VEC>(slope, slope, s);
         mul_to<VEC>(s, s, z);

@@ -299,7 +299,8 @@ __device__ __forceinline__ void code_values(raw_t<int8_t, VEC> raw, float scale,
 // counts as often as the state remembers tokens.  FULL: the exponential of full accuracy, for FP32 arguments.
 // Else the fast one, whose error grows with |g| (2^-20 of 1 - a at 8, 2^-19 at 16; of a small a
 // likewise): 16-bit arguments carry 2^-12 |g| at best themselves.  Below 2^-126, 1 - a is then 0 and a is 2^-126.
-template <bool FULL, int VEC>
+// ZERO, the faster form: an a below 2^-126 is 0, and with it what is given for 1 - a, for use as a factor beside a alone.
+template <bool FULL, int VEC, bool ZERO = false>
 __device__ __forceinline__ void sigmoid_pair(float (&a)[VEC], float (&rest)[VEC]) {
     if constexpr (FULL) {
 #pragma unroll
@@ -319,7 +320,9 @@ __device__ __forceinline__ void sigmoid_pair(float (&a)[VEC], float (&rest)[VEC]
         mul_to<VEC>(z, a, k);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(z[v]));   // 126: 1 + z stays finite
+            // 126: 1 + z stays finite, and its reciprocal a normal number; 127: which is flushed to 0
+            if constexpr (ZERO) asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(z[v]));
+            else asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(z[v]));
             asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(z[v]));
         }
         fma_to<VEC>(m, z, -1.f, -1.f);                     // -(1 + z)
