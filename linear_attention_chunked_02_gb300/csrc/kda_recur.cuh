@@ -964,8 +964,8 @@ struct GradShape {
 //
 // 16 x 512 rows of 8192 channels, BF16: 122 us (floor 100), 635 MB at 63 % of the DRAM's peak and 55 % of the issue slots, which
 // two blocks of 8 warps to an SM with a barrier twice to a tile do not use better.  One sequence of 16384 rows of 2048
-// channels from codes: 92 us (floor 40; 228 MB, 30 % and 48 %): a code takes more instructions than a BF16 value, and blocks
-// wait for one another as above; from tensors it takes 86.  Eight rows and two channels to a lane: with four channels and
+// channels from codes: 92 us (floor 40; 228 MB, 30 % and 48 %): nothing is saturated, 16 warps to an SM wait for one another
+// twice a tile; from tensors it takes 86.  Eight rows and two channels to a lane: with four channels and
 // four rows, one block to an SM, 16 x 512 takes 167 us (from codes 186, here 139).
 template <typename T, typename X, typename S, typename G, int FORM, int VEC, int R, int W, int RING, int PIECE, int MIN>
 __global__ void __launch_bounds__(W * 32, MIN) kda_gated_scan_backward_kernel(const __grid_constant__ RecurParams p) {

@@ -1,14 +1,15 @@
 """The gated linear recurrence, its gradients and its step, 8-bit checkpoints and the gated norm's
 gradients against the 64-bit oracle on the same rounded inputs.
 
-Tolerances, fixed before the first run: the oracle's bounds on what FP32 arithmetic may lose
-(oracle/recurrence.py says where they come from), plus half a unit in the last place of a 16-bit output's
-type where there is one (2^-8 and 2^-11 of the value, half the least subnormal below the normal range).
+Tolerances: the oracle's bounds on what FP32 arithmetic may lose (oracle/recurrence.py says where they come from;
+that of sigmoids of 16-bit arguments was derived when they took the faster exponential, after the first
+run), plus half a unit in the last place of a 16-bit output's type where there is one (2^-8 and 2^-11 of the
+value, half the least subnormal below the normal range).
 Checkpoints are exact.  Norm gradients: sums over up to 16384 elements in a tree carry less than 32 * 2^-24
 relative to the sum of absolute values, and there are two of them in dx beside some ten roundings and
-functions of 2 units each: 2^-17 of the oracle's sums of absolute values.  dweight adds up to
-rows / 608 products in a row, 256 sums of those and 76 + 8 blocks': for the rows below less than
-2^-24 (rows / 608 + 400) + 2^-20, taken as 2^-14 of the sum of absolute values.
+functions of 2 units each: 2^-17 of the oracle's sums of absolute values.  dweight adds up
+rows / 304 + 1 products in a thread at most, 256 threads' sums, 38 blocks' in each of 8 warps and those 8: for the rows below
+less than 2^-24 (rows / 304 + 303) + 2^-19, taken as 2^-14 of the sum of absolute values.
 """
 from __future__ import annotations
 
